@@ -27,6 +27,8 @@ __all__ = ["validate_cu_seqlens", "count_nonfinite", "chunk_fwd", "chunk_fwd_sim
            "segmented_fwd", "decode_step", "chunk_bwd", "chunk_bwd_static_scratch",
            "bwd_timing_start", "bwd_timing_read", "chunk_fwd_variant", "gate_projection",
            "chunk_fwd_gated",
+           "gdr_chunk_fwd", "gdr_step", "residual_norm_fwd",
+           "residual_norm_bwd", "gated_norm_fwd", "gated_norm_bwd",
            "load_library",
            "kernel_launch_count", "read_device_flags", "selftest_bounded_wait",
            "library_path", "KDAError", "EXPORTED_SYMBOLS", "STATUS"]
@@ -45,7 +47,11 @@ EXPORTED_SYMBOLS = ("kda_version", "kda_status_string", "kda_last_error",
                     "kda_chunk_fwd_pipeline_plan", "kda_validate_cu_seqlens",
                     "kda_count_nonfinite", "kda_check_outputs",
                     "kda_chunk_fwd_gated_workspace_bytes", "kda_chunk_fwd_gated",
-                    "kda_gate_projection_out")
+                    "kda_gate_projection_out",
+                    "kda_gdr_chunk_fwd_workspace_bytes", "kda_gdr_chunk_fwd", "kda_gdr_step",
+                    "kda_residual_norm_fwd", "kda_residual_norm_bwd_workspace_bytes",
+                    "kda_residual_norm_bwd", "kda_gated_norm_fwd",
+                    "kda_gated_norm_bwd_workspace_bytes", "kda_gated_norm_bwd")
 
 _lock = threading.Lock()
 _lib = None
@@ -140,6 +146,19 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.kda_chunk_fwd_gated.restype = ctypes.c_int
         lib.kda_gate_projection_out.argtypes = [P, P, P, P, ctypes.c_int, I64, I32, I32, P]
         lib.kda_gate_projection_out.restype = ctypes.c_int
+        SZ, F, E = ctypes.c_size_t, ctypes.c_float, ctypes.c_int
+        for name, res, args in (
+                ("kda_gdr_chunk_fwd_workspace_bytes", SZ, [I64, I32, I32, E]),
+                ("kda_gdr_chunk_fwd", E, [P] * 3 + [I64] * 3 + [P] * 7 + [SZ, I64] + [I32] * 5 + [E, P]),
+                ("kda_gdr_step", E, [P] * 3 + [I64] * 3 + [P] * 5 + [I32] * 6 + [E, P]),
+                ("kda_residual_norm_fwd", E, [P, I64, P, I64] + [P] * 4 + [I64, I32, F, E, P]),
+                ("kda_residual_norm_bwd_workspace_bytes", SZ, [I64, I32, E]),
+                ("kda_residual_norm_bwd", E, [P, I64] * 4 + [P] * 7 + [SZ, I64, I32, F, E, P]),
+                ("kda_gated_norm_fwd", E, [P, I64] * 2 + [P, P, I64, I32, I32, F, I32, E, P]),
+                ("kda_gated_norm_bwd_workspace_bytes", SZ, [I64, I32, I32]),
+                ("kda_gated_norm_bwd", E, [P, I64] * 3 + [P] * 5 + [SZ, I64, I32, I32, F, I32, E, P])):
+            fn = getattr(lib, name)
+            fn.restype, fn.argtypes = res, args
         _lib = lib
         return lib
 
@@ -693,3 +712,7 @@ def segmented_fwd(q, k, v, gate_logits, beta, h0=None, cu_seqlens=None, *, segme
                           out=out[b1:])
     h_final = h_last[P - 2:P - 1].clone() if output_final_state else None
     return out, h_final
+
+
+from .block import (gated_norm_bwd, gated_norm_fwd, gdr_chunk_fwd, gdr_step,  # noqa: E402
+                    residual_norm_bwd, residual_norm_fwd)

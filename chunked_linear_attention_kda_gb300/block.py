@@ -1,0 +1,238 @@
+"""The operators of a block around the gated delta rule with one decay per head: the
+recurrence itself (chunked forward, one-token step over a pool of states), the residual
+norm before a block and the gated norm after the recurrence, with their backward passes.
+
+Like the rest of the package a thin binding of the C ABI in ``include/kda.h``: metadata
+checks, output and workspace allocation through torch, raw pointers and the current
+stream. Inputs are torch CUDA tensors; q, k, v and the norms' activations may be slices of
+a wider tensor (any stride between tokens, a token's row contiguous), everything else is
+contiguous. There is no CPU path.
+"""
+from __future__ import annotations
+
+import torch
+
+import chunked_linear_attention_kda_gb300 as _kda
+
+_CODE = {torch.float32: 0, torch.bfloat16: 1}
+ACTIVATIONS = {"sigmoid": 0, "silu": 1}
+
+
+def _start(t, what):
+    """The library and the stream of ``t``'s device for a call on ``t``."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} runs on CUDA tensors only (there is no CPU path)")
+    if t.dtype not in _CODE:
+        raise ValueError(f"{what}: activations must be bfloat16 or float32, got {t.dtype}")
+    return _kda._lib or _kda.load_library(), torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _rows(name, t, shape, like):
+    """The distance between tokens of ``t`` ([tokens, ...], a token's row contiguous)."""
+    if t.shape != shape or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must be {like.dtype} with shape {tuple(shape)} on {like.device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    width = 1
+    for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != width:
+            raise ValueError(f"{name}: a token's row must be contiguous")
+        width *= size
+    step = t.stride(0)
+    if shape[0] > 1 and step < width:
+        raise ValueError(f"{name}: tokens may not overlap or run backwards")
+    return step if step > width else width
+
+
+def _flat(name, t, shape, dtype, like):
+    if t.shape != shape or t.dtype != dtype or t.device != like.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} with shape {tuple(shape)} on "
+                         f"{like.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _p(t):
+    return None if t is None or t.numel() == 0 else t.data_ptr()
+
+
+def _done(lib, status):
+    if status != 0:
+        _kda._check(lib, status)
+
+
+def _gdr_inputs(q, k, v, g, beta):
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and k must be [N, H_k, d_k], v [N, H, d_v] (packed, token-major)")
+    n, hk, dk = q.shape
+    h, dv = v.shape[1:]
+    if hk == 0 or h % hk != 0:
+        raise ValueError(f"v's {h} heads must be a multiple of q's {hk}")
+    strides = (_rows("q", q, (n, hk, dk), q), _rows("k", k, (n, hk, dk), q),
+               _rows("v", v, (n, h, dv), q))
+    _flat("g", g, (n, h), torch.float32, q)
+    _flat("beta", beta, (n, h), torch.float32, q)
+    return n, hk, h, dk, dv, strides
+
+
+def _sequences(q, n, h, dk, dv, h0, cu_seqlens):
+    if cu_seqlens is None:
+        cu_seqlens = torch.tensor([0, n], dtype=torch.int32, device=q.device)
+    n_seq = cu_seqlens.numel() - 1
+    if n_seq < 0:
+        raise ValueError("cu_seqlens needs at least one entry")
+    _flat("cu_seqlens", cu_seqlens, (n_seq + 1,), torch.int32, q)
+    if h0 is not None:
+        _flat("h0", h0, (n_seq, h, dk, dv), torch.float32, q)
+    return n_seq, cu_seqlens
+
+
+def gdr_chunk_fwd(q, k, v, g, beta, h0=None, cu_seqlens=None, *, out=None, h_final=None,
+                  output_final_state=True, workspace=None):
+    """Chunked forward of the gated delta rule with one log-decay ``g`` per token and head
+    through ``kda_gdr_chunk_fwd``. ``q, k`` [N, H_k, d_k], ``v`` [N, H, d_v] (H a multiple of
+    H_k; bf16 or fp32), ``g, beta`` [N, H] fp32, ``h0`` [n_seq, H, d_k, d_v] fp32 or None,
+    ``cu_seqlens`` int32 [n_seq + 1] (None: one sequence). Returns ``(out, h_final)``, the
+    latter None when ``output_final_state`` is False."""
+    lib, stream = _start(q, "gdr_chunk_fwd")
+    n, hk, h, dk, dv, strides = _gdr_inputs(q, k, v, g, beta)
+    n_seq, cu_seqlens = _sequences(q, n, h, dk, dv, h0, cu_seqlens)
+    if out is None:
+        out = torch.empty((n, h, dv), dtype=q.dtype, device=q.device)
+    else:
+        _flat("out", out, (n, h, dv), q.dtype, q)
+    if h_final is not None:
+        _flat("h_final", h_final, (n_seq, h, dk, dv), torch.float32, q)
+    elif output_final_state:
+        h_final = torch.empty((n_seq, h, dk, dv), dtype=torch.float32, device=q.device)
+    code = _CODE[q.dtype]
+    if workspace is None:
+        need = lib.kda_gdr_chunk_fwd_workspace_bytes(n, n_seq, h, code)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _done(lib, lib.kda_gdr_chunk_fwd(
+        _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(h0), _p(cu_seqlens), _p(out),
+        _p(h_final), _p(workspace), workspace.numel() * workspace.element_size(), n, n_seq, hk,
+        h, dk, dv, code, stream))
+    return out, h_final
+
+
+def gdr_step(q, k, v, g, beta, state, slots=None, *, out=None):
+    """One token per row through ``kda_gdr_step``: row b updates ``state[slots[b]]`` in place
+    (``state`` [n_slots, H, d_k, d_v] fp32; ``slots`` int32 [B], None: row b has state b). A
+    slot outside the pool marks a padded row: its output is 0. The other tensors as for
+    ``gdr_chunk_fwd`` with B tokens. Returns ``out`` [B, H, d_v]."""
+    lib, stream = _start(q, "gdr_step")
+    n, hk, h, dk, dv, strides = _gdr_inputs(q, k, v, g, beta)
+    _flat("state", state, (state.shape[0], h, dk, dv), torch.float32, q)
+    if slots is not None:
+        _flat("slots", slots, (n,), torch.int32, q)
+    if out is None:
+        out = torch.empty((n, h, dv), dtype=q.dtype, device=q.device)
+    else:
+        _flat("out", out, (n, h, dv), q.dtype, q)
+    _done(lib, lib.kda_gdr_step(
+        _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(state), _p(slots), _p(out), n,
+        state.shape[0], hk, h, dk, dv, _CODE[q.dtype], stream))
+    return out
+
+
+def residual_norm_fwd(x, weight, residual=None, scale=None, *, eps=1e-6, out=None,
+                      residual_out=None):
+    """``r = residual + scale * x`` and ``y = weight * r / sqrt(mean(r^2) + eps)`` through
+    ``kda_residual_norm_fwd``: ``x, residual`` [N, d] bf16 or fp32, ``weight, scale`` [d] fp32.
+    Returns ``(y, r)``; with neither residual nor scale ``r`` is ``x`` itself."""
+    lib, stream = _start(x, "residual_norm_fwd")
+    if x.dim() != 2:
+        raise ValueError("x must be [N, d]")
+    n, d = x.shape
+    xs = _rows("x", x, (n, d), x)
+    _flat("weight", weight, (d,), torch.float32, x)
+    if scale is not None:
+        _flat("scale", scale, (d,), torch.float32, x)
+    rs = 0 if residual is None else _rows("residual", residual, (n, d), x)
+    same = residual is None and scale is None and residual_out is None
+    if residual_out is not None:
+        _flat("residual_out", residual_out, (n, d), x.dtype, x)
+    elif not same:
+        residual_out = torch.empty((n, d), dtype=x.dtype, device=x.device)
+    if out is None:
+        out = torch.empty((n, d), dtype=x.dtype, device=x.device)
+    else:
+        _flat("out", out, (n, d), x.dtype, x)
+    _done(lib, lib.kda_residual_norm_fwd(_p(x), xs, _p(residual), rs, _p(scale), _p(weight),
+                                         _p(residual_out), _p(out), n, d, eps, _CODE[x.dtype],
+                                         stream))
+    return out, (x if same else residual_out)
+
+
+def residual_norm_bwd(dy, r, weight, dr=None, x=None, scale=None, *, eps=1e-6, workspace=None):
+    """Gradients of ``residual_norm_fwd`` through ``kda_residual_norm_bwd`` from its ``r``:
+    ``dy`` the gradient of y, ``dr`` the one that reaches r from elsewhere (None: zero), ``x``
+    needed with a ``scale`` only. Returns ``(dx, dresidual, dweight, dscale)``; without a scale
+    ``dx`` is ``dresidual`` and ``dscale`` None."""
+    lib, stream = _start(r, "residual_norm_bwd")
+    if r.dim() != 2:
+        raise ValueError("r must be [N, d]")
+    n, d = r.shape
+    ss = [_rows("dy", dy, (n, d), r), 0 if dr is None else _rows("dr", dr, (n, d), r),
+          _rows("r", r, (n, d), r), 0]
+    _flat("weight", weight, (d,), torch.float32, r)
+    if scale is not None:
+        _flat("scale", scale, (d,), torch.float32, r)
+        if x is None:
+            raise ValueError("a scale's gradient needs x")
+        ss[3] = _rows("x", x, (n, d), r)
+    dres = torch.empty((n, d), dtype=r.dtype, device=r.device)
+    dw = torch.empty(d, dtype=torch.float32, device=r.device)
+    dx = None if scale is None else torch.empty_like(dres)
+    ds = None if scale is None else torch.empty_like(dw)
+    if workspace is None:
+        need = lib.kda_residual_norm_bwd_workspace_bytes(n, d, scale is not None)
+        workspace = torch.empty(need, dtype=torch.uint8, device=r.device)
+    _done(lib, lib.kda_residual_norm_bwd(
+        _p(dy), ss[0], _p(dr), ss[1], _p(r), ss[2], None if scale is None else _p(x), ss[3],
+        _p(scale), _p(weight), _p(dx), _p(dres), _p(ds), _p(dw), _p(workspace),
+        workspace.numel() * workspace.element_size(), n, d, eps, _CODE[r.dtype], stream))
+    return (dres if scale is None else dx), dres, dw, ds
+
+
+def _gated_inputs(x, gate, weight, activation):
+    if x.dim() != 3:
+        raise ValueError("x must be [N, H, d]")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    _flat("weight", weight, (x.shape[2],), torch.float32, x)
+    return _rows("x", x, x.shape, x), _rows("gate", gate, x.shape, x)
+
+
+def gated_norm_fwd(x, gate, weight, *, eps=1e-6, activation="sigmoid", out=None):
+    """``y = weight * x / sqrt(mean(x^2) + eps) * act(gate)`` per token and head through
+    ``kda_gated_norm_fwd``: ``x, gate`` [N, H, d] bf16 or fp32, ``weight`` [d] fp32,
+    ``activation`` "sigmoid" or "silu". Returns ``y`` [N, H, d]."""
+    lib, stream = _start(x, "gated_norm_fwd")
+    xs, gs = _gated_inputs(x, gate, weight, activation)
+    n, h, d = x.shape
+    if out is None:
+        out = torch.empty((n, h, d), dtype=x.dtype, device=x.device)
+    else:
+        _flat("out", out, (n, h, d), x.dtype, x)
+    _done(lib, lib.kda_gated_norm_fwd(_p(x), xs, _p(gate), gs, _p(weight), _p(out), n, h, d, eps,
+                                      ACTIVATIONS[activation], _CODE[x.dtype], stream))
+    return out
+
+
+def gated_norm_bwd(dy, x, gate, weight, *, eps=1e-6, activation="sigmoid", workspace=None):
+    """Gradients of ``gated_norm_fwd`` through ``kda_gated_norm_bwd``: ``(dx, dgate, dweight)``."""
+    lib, stream = _start(x, "gated_norm_bwd")
+    xs, gs = _gated_inputs(x, gate, weight, activation)
+    ys = _rows("dy", dy, x.shape, x)
+    n, h, d = x.shape
+    dx = torch.empty((n, h, d), dtype=x.dtype, device=x.device)
+    dgate = torch.empty_like(dx)
+    dw = torch.empty(d, dtype=torch.float32, device=x.device)
+    if workspace is None:
+        need = lib.kda_gated_norm_bwd_workspace_bytes(n, h, d)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _done(lib, lib.kda_gated_norm_bwd(
+        _p(dy), ys, _p(x), xs, _p(gate), gs, _p(weight), _p(dx), _p(dgate), _p(dw),
+        _p(workspace), workspace.numel() * workspace.element_size(), n, h, d, eps,
+        ACTIVATIONS[activation], _CODE[x.dtype], stream))
+    return dx, dgate, dw

@@ -11,7 +11,7 @@
 #include <string>
 #include <vector>
 
-#include "../../include/kda.h"
+#include "kda_api.h"
 #include "kda_internal.h"
 
 namespace {
@@ -236,6 +236,8 @@ size_t pipeline_workspace(int32_t n_seq, int32_t n_heads, int32_t d_k, int32_t d
 }  // namespace
 
 namespace kda {
+kda_status api_fail(kda_status status, const std::string &why) { return fail(status, why); }
+kda_status api_ok() { return ok(); }
 void count_launches(uint64_t n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 }  // namespace kda
 

@@ -1,0 +1,229 @@
+// Shared by the kernels of the gated delta rule with one decay per head (kda_gdr_fwd.cu,
+// kda_gdr_bwd.cu): sizes, workspace layout, operand tiles and warp-level products.
+// Internal; not part of the C ABI.
+//
+// Precision. Every product runs on bf16 mma.sync with fp32 accumulation; an operand that is
+// not a bf16 input is carried as a sum of bf16 planes (hi + lo, or hi + mid + lo), so that
+// the fp32 results (states, gate and beta gradients) keep about 2^-17 of relative error per
+// operand for bf16 inputs and 2^-24 for fp32 inputs. NI = planes of an input tile (1: bf16,
+// 3: fp32), NS = planes of an intermediate (2 or 3); a product of plane i with plane j is
+// formed only where i + j < NS (the rest is below the accumulator's rounding of the sum).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_internal.h"
+#include "kda_ptx.h"
+
+namespace kda {
+namespace gdr {
+
+constexpr int C = 64;           // tokens of a chunk
+constexpr int kTile = C * C;    // elements of a chunk's square tile
+constexpr float kGFloor = -200.f;
+
+// ---------------------------------------------------------------- workspace
+// Chunk c of sequence n lives in slot (cu[n] / 64) + n + c: distinct over all chunks and
+// below n_tok / 64 + n_seq, without a pass over the lengths on the host.
+__host__ __device__ __forceinline__ int64_t n_slots(int64_t n_tok, int64_t n_seq) {
+    return n_tok / C + n_seq;
+}
+__device__ __forceinline__ int64_t slot_base(const int32_t *cu, int n) {
+    return (int64_t)(cu[n] >> 6) + n;
+}
+
+struct Chunk {
+    int seq, len;      // len = 0: an unused slot
+    int64_t t0;
+};
+// the chunk in a slot
+__device__ __forceinline__ Chunk find_chunk(const int32_t *cu, int n_seq, int64_t slot) {
+    int lo = 0, hi = n_seq - 1;  // largest n with slot_base(n) <= slot
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (slot_base(cu, mid) <= slot) lo = mid; else hi = mid - 1;
+    }
+    const int64_t t0 = cu[lo] + (slot - slot_base(cu, lo)) * C;
+    const int64_t left = cu[lo + 1] - t0;
+    return {lo, left <= 0 ? 0 : left < C ? (int)left : C, t0};
+}
+
+// Per (slot, value head): X and P tile images (NS planes each, swizzled as the kernels read
+// them) and the gate vectors gamma, delta, beta, [Gamma].
+constexpr int kGateFloats = 4 * C;
+__host__ __device__ constexpr size_t terms_bytes(int ns) {
+    return (size_t)2 * ns * kTile * 2 + kGateFloats * 4;
+}
+
+// ---------------------------------------------------------------- tiles
+// A tile of bf16 rows of RB bytes, 16-byte groups XOR-swizzled so that ldmatrix reads eight
+// rows of one column group without bank conflicts.
+template <int RB>
+__device__ __forceinline__ uint32_t tile_off(int row, int col) {
+    constexpr int groups = RB / 16;
+    const int g = col >> 3;
+    int x;
+    if constexpr (RB >= 128) x = row & 7;
+    else x = (row / (128 / RB)) & (groups - 1);
+    return row * RB + ((g ^ x) << 4) + (col & 7) * 2;
+}
+
+// operand fragments of one 16 x 16 block of a tile whose stored rows are m (A), n (B) or the
+// contraction index (the _t forms)
+template <int RB>
+__device__ __forceinline__ void frag_a(uint32_t base, int m0, int k0, uint32_t *a) {
+    const int l = threadIdx.x & 31;
+    ptx::ldsm_x4(base + tile_off<RB>(m0 + (l & 15), k0 + (l >> 4) * 8), a[0], a[1], a[2], a[3]);
+}
+template <int RB>
+__device__ __forceinline__ void frag_a_t(uint32_t base, int k0, int m0, uint32_t *a) {
+    const int l = threadIdx.x & 31;
+    ptx::ldsm_x4_t(base + tile_off<RB>(k0 + (l >> 4) * 8 + (l & 7), m0 + ((l >> 3) & 1) * 8),
+                   a[0], a[1], a[2], a[3]);
+}
+// b[0..1]: columns n0..n0+7, b[2..3]: columns n0+8..n0+15
+template <int RB>
+__device__ __forceinline__ void frag_b(uint32_t base, int n0, int k0, uint32_t *b) {
+    const int l = threadIdx.x & 31;
+    ptx::ldsm_x4(base + tile_off<RB>(n0 + (l >> 4) * 8 + (l & 7), k0 + ((l >> 3) & 1) * 8),
+                 b[0], b[1], b[2], b[3]);
+}
+template <int RB>
+__device__ __forceinline__ void frag_b_t(uint32_t base, int k0, int n0, uint32_t *b) {
+    const int l = threadIdx.x & 31;
+    ptx::ldsm_x4_t(base + tile_off<RB>(k0 + (l & 15), n0 + (l >> 4) * 8), b[0], b[1], b[2], b[3]);
+}
+
+// two fp32 values as NP packed planes whose sum is the value
+template <int NP>
+__device__ __forceinline__ void split2(float x, float y, uint32_t *p) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const uint32_t w = ptx::pack_bf16(x, y);
+        p[i] = w;
+        if (i + 1 < NP) {
+            x -= __uint_as_float(w << 16);
+            y -= __uint_as_float(w & 0xffff0000u);
+        }
+    }
+}
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// acc tiles t0 = d[0], t1 = d[1] (columns 0..7 and 8..15 of a 16 x 16 block): as the A
+// operand whose contraction index is the block's column; plane p in a[p][0..3]
+template <int NP>
+__device__ __forceinline__ void acc_to_a(const float (*d)[4], uint32_t (*a)[4]) {
+    uint32_t w[NP];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float *t = d[i >> 1];
+        split2<NP>(t[(i & 1) * 2], t[(i & 1) * 2 + 1], w);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) a[p][i] = w[p];
+    }
+}
+
+// ---------------------------------------------------------------- loading inputs
+template <typename T> struct InputPlanes;
+template <> struct InputPlanes<__nv_bfloat16> { static constexpr int N = 1; };
+template <> struct InputPlanes<float> { static constexpr int N = 3; };
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void st_shared_16(uint32_t a, const uint32_t *w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]) : "memory");
+}
+
+// C rows of RB / 2 columns from src (rows `stride` elements apart) into the tile at `dst`
+// (planes `plane` bytes apart); rows >= rows and columns >= cols read as zero. vec: the rows
+// are 16-byte aligned and cols fills whole 16-byte groups (then bf16 goes by cp.async).
+template <typename T, int RB>
+__device__ __forceinline__ void load_tile(uint32_t dst, uint32_t plane, const T *src, int64_t stride,
+                                          int rows, int cols, bool vec, int tid, int nthreads) {
+    constexpr int groups = RB / 16;
+    for (int i = tid; i < C * groups; i += nthreads) {
+        const int r = i / groups, c = (i % groups) * 8;
+        const uint32_t at = dst + tile_off<RB>(r, c);
+        const bool in = r < rows && c < cols;
+        const T *p = src + (in ? r * stride + c : 0);
+        if constexpr (sizeof(T) == 2) {
+            if (vec) {
+                cp_async_16(at, p, in ? 16 : 0);
+                continue;
+            }
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (in) {
+                const uint16_t *e = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < cols) w[j >> 1] |= (uint32_t)e[j] << (16 * (j & 1));
+            }
+            st_shared_16(at, w);
+        } else {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = 0.f;
+            if (in) {
+                const float *e = reinterpret_cast<const float *>(p);
+                if (vec && c + 8 <= cols) {
+                    const float4 u = *reinterpret_cast<const float4 *>(e);
+                    const float4 v = *reinterpret_cast<const float4 *>(e + 4);
+                    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+                    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (c + j < cols) x[j] = e[j];
+                }
+            }
+            uint32_t w[3][4], s[3];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                split2<3>(x[2 * j], x[2 * j + 1], s);
+                w[0][j] = s[0]; w[1][j] = s[1]; w[2][j] = s[2];
+            }
+#pragma unroll
+            for (int q = 0; q < 3; ++q) st_shared_16(at + q * plane, w[q]);
+        }
+    }
+}
+// `bytes` (a multiple of 16) from the workspace, as they lie
+__device__ __forceinline__ void load_raw(uint32_t dst, const void *src, int bytes, int tid, int nthreads) {
+    const char *p = static_cast<const char *>(src);
+    for (int i = tid * 16; i < bytes; i += nthreads * 16) cp_async_16(dst + i, p + i, 16);
+}
+
+__device__ __forceinline__ void put(float *p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+// two neighbouring elements; wide: p is aligned to both
+__device__ __forceinline__ void put2(float *p, float x, float y, bool wide, bool second) {
+    if (wide) *reinterpret_cast<float2 *>(p) = make_float2(x, y);
+    else { p[0] = x; if (second) p[1] = y; }
+}
+__device__ __forceinline__ void put2(__nv_bfloat16 *p, float x, float y, bool wide, bool second) {
+    if (wide) *reinterpret_cast<uint32_t *>(p) = ptx::pack_bf16(x, y);
+    else { put(p, x); if (second) put(p + 1, y); }
+}
+
+// 16-byte loads of rows of `d` elements at this base and stride
+template <typename T>
+bool rows_vec(const void *p, int64_t stride, int d) {
+    return ((uintptr_t)p & 15u) == 0 && (stride * sizeof(T)) % 16 == 0 && (d * sizeof(T)) % 16 == 0;
+}
+
+}  // namespace gdr
+
+// Chunk terms (X, P, gates of every chunk and value head) into the workspace.
+cudaError_t launch_gdr_terms(const GdrArgs &args, cudaStream_t stream);
+
+}  // namespace kda

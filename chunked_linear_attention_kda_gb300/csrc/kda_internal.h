@@ -84,6 +84,74 @@ cudaError_t launch_bwd(const BwdArgs &args, cudaStream_t stream);
 constexpr size_t kStaticScratchBytes = (size_t)64 << 20;
 cudaError_t static_scratch(void **ptr);
 
+// Gated delta rule with one decay per head: q, k [n_tok, n_k_heads, d_k], v and out [n_tok,
+// n_heads, d_v] (tokens of q, k, v any stride apart, in elements), g and beta [n_tok,
+// n_heads], states [n_seq, n_heads, d_k, d_v]; value head h reads key head
+// h / (n_heads / n_k_heads). The backward pass adds dout and the gradients.
+struct GdrArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const float *g, *beta, *h0;
+    const int32_t *cu_seqlens;
+    void *out;
+    float *h_final;
+    const void *dout;
+    const float *dh_final;
+    void *dq, *dk, *dv;
+    float *dg, *dbeta, *dh0;
+    void *workspace;
+    int64_t n_tok;
+    int32_t n_seq, n_k_heads, n_heads, d_k, d_v;
+    bool bf16;
+};
+size_t gdr_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, bool bf16);
+cudaError_t launch_gdr_fwd(const GdrArgs &args, cudaStream_t stream);
+
+// One token per row: q, k, v, g, beta, out as one token of GdrArgs; row b's state is
+// state[slots[b]] (slots NULL: state[b]); a slot outside [0, n_slots) is a padded row.
+struct GdrStepArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const float *g, *beta;
+    float *state;
+    const int32_t *slots;
+    void *out;
+    int32_t n_rows, n_slots, n_k_heads, n_heads, d_k, d_v;
+    bool bf16;
+};
+cudaError_t launch_gdr_step(const GdrStepArgs &args, cudaStream_t stream);
+
+// The norms around a block (kda_norm.cu). Strides in elements between rows (tokens);
+// outputs contiguous. Forward: x, residual, scale, weight -> y, r. Backward: r, x, dy, dr,
+// scale, weight -> dx, dresidual, dw, dscale, with the partial sums in `partial`.
+struct ResidualNormArgs {
+    const void *x, *residual, *dy, *dr;
+    int64_t x_stride, residual_stride, dy_stride, dr_stride, r_stride;
+    const float *weight, *scale;
+    void *r;  // the forward's output, the backward's input
+    void *y, *dx, *dresidual;
+    float *dw, *dscale, *partial;
+    int64_t n_rows;
+    int32_t d;
+    float eps;
+    bool bf16;
+};
+struct GatedNormArgs {
+    const void *x, *gate, *dy;
+    int64_t x_stride, gate_stride, dy_stride;
+    const float *weight;
+    void *y, *dx, *dgate;
+    float *dw, *partial;
+    int64_t n_tok;
+    int32_t n_heads, d;
+    float eps;
+    bool silu, bf16;
+};
+size_t residual_norm_workspace_bytes(int64_t n_rows, int32_t d, bool scale);
+size_t gated_norm_workspace_bytes(int64_t n_tok, int32_t n_heads, int32_t d);
+cudaError_t launch_residual_norm(const ResidualNormArgs &args, bool bwd, cudaStream_t stream);
+cudaError_t launch_gated_norm(const GatedNormArgs &args, bool bwd, cudaStream_t stream);
+
 // Gate projection a[M, N] = x[M, K] W[N, K]^T (+ b[N]): bf16 x and W, fp32 a and b
 // (tcgen05 GEMM, kda_gemm.cu). K % 8 == 0, x, W and a 16-byte aligned.
 cudaError_t launch_gate_proj(const void *x, const void *w, const float *bias, float *out, int M,

@@ -1,0 +1,476 @@
+// kda_norm.cu -- the norms around a recurrence block, forward and backward.
+//
+// Residual norm, a row of d channels (before a block; x is the previous block's output):
+//   r = residual + scale x,   y = w r c,   c = (mean r^2 + eps)^-1/2
+//   backward, with n = r c, t = w dy:  dr' = dr + c (t - n mean(t n));  dresidual = dr',
+//   dx = scale dr', dscale = sum over rows of x dr', dw = sum over rows of dy n
+// Gated norm, a row of d channels of one (token, head) (after the recurrence):
+//   y = w n act(z),  n = x c;   backward with t = w act(z) dy:
+//   dx = c (t - n mean(t n)),  dz = dy w n act'(z),  dw = sum over rows of dy n act(z)
+// Sums and statistics are fp32. All are bound by HBM: every input is read once, kept in
+// registers across the row's reduction, every output written once. The sums over rows go to
+// one partial row per CTA (group), added up in a fixed order by a second kernel: the same
+// call gives the same bits.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "kda_internal.h"
+#include "kda_ptx.h"
+
+namespace kda {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+__device__ __forceinline__ float get(const float *p) { return *p; }
+__device__ __forceinline__ float get(const bf16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void put(float *p, float x) { *p = x; }
+__device__ __forceinline__ void put(bf16 *p, float x) { *p = __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ void load8(const float *p, float *x) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const bf16 *p, float *x) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void store8(float *p, const float *x) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(bf16 *p, const float *x) {
+    uint4 a;
+    a.x = ptx::pack_bf16(x[0], x[1]);
+    a.y = ptx::pack_bf16(x[2], x[3]);
+    a.z = ptx::pack_bf16(x[4], x[5]);
+    a.w = ptx::pack_bf16(x[6], x[7]);
+    *reinterpret_cast<uint4 *>(p) = a;
+}
+
+// A group of G threads holds a row of d channels, 8 NV of them per thread: with VEC thread
+// t the 8-channel runs 8 (t + G i), otherwise the channels t + G i one by one.
+template <int NV, bool VEC, typename T>
+__device__ __forceinline__ void load_row(const T *p, int d, int t, int G, float *x) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if constexpr (VEC) {
+            const int c = 8 * (t + G * i);
+            if (c < d) load8(p + c, x + 8 * i);
+            else
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[8 * i + j] = 0.f;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = t + G * (8 * i + j);
+                x[8 * i + j] = c < d ? get(p + c) : 0.f;
+            }
+        }
+    }
+}
+template <int NV, bool VEC, typename T>
+__device__ __forceinline__ void store_row(T *p, int d, int t, int G, const float *x) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if constexpr (VEC) {
+            const int c = 8 * (t + G * i);
+            if (c < d) store8(p + c, x + 8 * i);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int c = t + G * (8 * i + j);
+                if (c < d) put(p + c, x[8 * i + j]);
+            }
+        }
+    }
+}
+
+// Sum over the G threads (G = 32 WPR) of a group; every thread gets it. `buf` holds WPR
+// floats per group and alternates between two halves so that one barrier per sum suffices.
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+template <int WPR>
+__device__ __forceinline__ float group_sum(float x, float *buf, int group) {
+    x = warp_sum(x);
+    if constexpr (WPR > 1) {
+        const int w = (threadIdx.x >> 5) % WPR;
+        if ((threadIdx.x & 31) == 0) buf[group * WPR + w] = x;
+        __syncthreads();
+        x = 0.f;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) x += buf[group * WPR + i];
+    }
+    return x;
+}
+
+template <int WPR>
+struct Rows {
+    static constexpr int kWarps = WPR < 8 ? 8 : WPR;
+    static constexpr int kThreads = 32 * kWarps, kGroups = kWarps / WPR, G = 32 * WPR;
+};
+
+template <typename T, int WPR, int NV, bool VEC>
+__global__ void __launch_bounds__(Rows<WPR>::kThreads)
+    residual_norm_fwd_kernel(const ResidualNormArgs p) {
+    using L = Rows<WPR>;
+    __shared__ float buf[L::kWarps];
+    const int group = threadIdx.x / L::G, t = threadIdx.x % L::G;
+    const int64_t row = (int64_t)blockIdx.x * L::kGroups + group;
+    const bool live = row < p.n_rows;
+    float r[8 * NV];
+#pragma unroll
+    for (int i = 0; i < 8 * NV; ++i) r[i] = 0.f;
+    if (live) {
+        load_row<NV, VEC>(static_cast<const T *>(p.x) + row * p.x_stride, p.d, t, L::G, r);
+        float a[8 * NV];
+        if (p.scale) {
+            load_row<NV, VEC>(p.scale, p.d, t, L::G, a);
+#pragma unroll
+            for (int i = 0; i < 8 * NV; ++i) r[i] *= a[i];
+        }
+        if (p.residual) {
+            load_row<NV, VEC>(static_cast<const T *>(p.residual) + row * p.residual_stride, p.d, t, L::G, a);
+#pragma unroll
+            for (int i = 0; i < 8 * NV; ++i) r[i] += a[i];
+        }
+        if (p.r) store_row<NV, VEC>(static_cast<T *>(p.r) + row * p.d, p.d, t, L::G, r);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8 * NV; ++i) s = fmaf(r[i], r[i], s);
+    s = group_sum<WPR>(s, buf, group);
+    if (!live) return;
+    const float c = 1.f / sqrtf(s / p.d + p.eps);
+    float w[8 * NV];
+    load_row<NV, VEC>(p.weight, p.d, t, L::G, w);
+#pragma unroll
+    for (int i = 0; i < 8 * NV; ++i) w[i] *= r[i] * c;
+    store_row<NV, VEC>(static_cast<T *>(p.y) + row * p.d, p.d, t, L::G, w);
+}
+
+// Each group walks over rows first, first + step, ...; its sums of dw (and dscale) go to
+// row `blockIdx.x * kGroups + group` of the partials.
+template <typename T, int WPR, int NV, bool VEC>
+__global__ void __launch_bounds__(Rows<WPR>::kThreads)
+    residual_norm_bwd_kernel(const ResidualNormArgs p, int64_t rounds) {
+    using L = Rows<WPR>;
+    __shared__ float buf[2][2][L::kWarps];
+    const int group = threadIdx.x / L::G, t = threadIdx.x % L::G;
+    const int64_t part = (int64_t)blockIdx.x * L::kGroups + group, step = (int64_t)gridDim.x * L::kGroups;
+    float dw[8 * NV], ds[8 * NV], w[8 * NV], a[8 * NV];
+#pragma unroll
+    for (int i = 0; i < 8 * NV; ++i) dw[i] = ds[i] = 0.f;
+    load_row<NV, VEC>(p.weight, p.d, t, L::G, w);
+    for (int64_t i0 = 0; i0 < rounds; ++i0) {
+        const int64_t row = part + i0 * step;
+        const bool live = row < p.n_rows;
+        float r[8 * NV], dy[8 * NV];
+        float rr = 0.f, tr = 0.f;
+        if (live) {
+            load_row<NV, VEC>(static_cast<const T *>(p.r) + row * p.r_stride, p.d, t, L::G, r);
+            load_row<NV, VEC>(static_cast<const T *>(p.dy) + row * p.dy_stride, p.d, t, L::G, dy);
+#pragma unroll
+            for (int i = 0; i < 8 * NV; ++i) {
+                rr = fmaf(r[i], r[i], rr);
+                tr = fmaf(w[i] * dy[i], r[i], tr);
+            }
+        }
+        rr = group_sum<WPR>(rr, buf[i0 & 1][0], group);
+        tr = group_sum<WPR>(tr, buf[i0 & 1][1], group);
+        if (!live) continue;
+        const float c = 1.f / sqrtf(rr / p.d + p.eps), m = tr * c * c / p.d;
+        float g[8 * NV];
+        if (p.dr) load_row<NV, VEC>(static_cast<const T *>(p.dr) + row * p.dr_stride, p.d, t, L::G, g);
+        else
+#pragma unroll
+            for (int i = 0; i < 8 * NV; ++i) g[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8 * NV; ++i) {
+            g[i] += c * (w[i] * dy[i] - r[i] * m);
+            dw[i] = fmaf(dy[i] * c, r[i], dw[i]);
+        }
+        store_row<NV, VEC>(static_cast<T *>(p.dresidual) + row * p.d, p.d, t, L::G, g);
+        if (p.scale) {
+            load_row<NV, VEC>(static_cast<const T *>(p.x) + row * p.x_stride, p.d, t, L::G, a);
+#pragma unroll
+            for (int i = 0; i < 8 * NV; ++i) ds[i] = fmaf(a[i], g[i], ds[i]);
+            load_row<NV, VEC>(p.scale, p.d, t, L::G, a);
+#pragma unroll
+            for (int i = 0; i < 8 * NV; ++i) a[i] *= g[i];
+            store_row<NV, VEC>(static_cast<T *>(p.dx) + row * p.d, p.d, t, L::G, a);
+        }
+    }
+    store_row<NV, VEC>(p.partial + part * p.d, p.d, t, L::G, dw);
+    if (p.scale) store_row<NV, VEC>(p.partial + (step + part) * p.d, p.d, t, L::G, ds);
+}
+
+// out[c] = sum over the parts of partial[part][c], in a fixed order; blockIdx.y chooses the sum
+__global__ void __launch_bounds__(512)
+    sum_parts_kernel(const float *__restrict__ partial, int parts, int d, float *__restrict__ out0,
+                     float *__restrict__ out1) {
+    __shared__ float s[16][33];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), l = threadIdx.x >> 5;
+    const float *src = partial + (int64_t)blockIdx.y * parts * d;
+    float x = 0.f;
+    if (c < d)
+#pragma unroll 4
+        for (int i = l; i < parts; i += 16) x += src[(int64_t)i * d + c];
+    s[l][threadIdx.x & 31] = x;
+    __syncthreads();
+    if (l == 0 && c < d) {
+        x = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x += s[i][threadIdx.x & 31];
+        (blockIdx.y ? out1 : out0)[c] = x;
+    }
+}
+
+constexpr int kSMs = 152;
+
+struct RowPlan { int wpr, nv; };
+RowPlan row_plan(int d) {
+    if (d <= 256) return {1, 1};
+    if (d <= 512) return {1, 2};
+    int wpr = 2;
+    while (wpr < 32 && 512 * wpr < d) wpr *= 2;
+    return {wpr, 512 * wpr < d ? 4 : 2};
+}
+int plan_groups(const RowPlan &r) { return r.wpr < 8 ? 8 / r.wpr : 1; }
+int64_t residual_bwd_grid(int64_t n_rows, int d) {
+    const RowPlan r = row_plan(d);
+    const int per_sm = r.wpr <= 8 ? 3 : r.wpr == 16 ? 2 : 1;
+    return std::max<int64_t>(1, std::min<int64_t>((n_rows + plan_groups(r) - 1) / plan_groups(r), kSMs * per_sm));
+}
+
+template <typename T, int WPR, int NV, bool VEC>
+cudaError_t residual_run(const ResidualNormArgs &p, bool bwd, cudaStream_t stream) {
+    using L = Rows<WPR>;
+    if (!bwd) {
+        residual_norm_fwd_kernel<T, WPR, NV, VEC>
+            <<<(unsigned)((p.n_rows + L::kGroups - 1) / L::kGroups), L::kThreads, 0, stream>>>(p);
+        count_launches(1);
+        return cudaGetLastError();
+    }
+    const int64_t grid = residual_bwd_grid(p.n_rows, p.d), parts = grid * L::kGroups;
+    residual_norm_bwd_kernel<T, WPR, NV, VEC>
+        <<<(unsigned)grid, L::kThreads, 0, stream>>>(p, (p.n_rows + parts - 1) / parts);
+    sum_parts_kernel<<<dim3((p.d + 31) / 32, p.scale ? 2 : 1), 512, 0, stream>>>(p.partial, (int)parts, p.d, p.dw, p.dscale);
+    count_launches(2);
+    return cudaGetLastError();
+}
+
+template <typename T, bool VEC>
+cudaError_t residual_pick(const ResidualNormArgs &p, bool bwd, cudaStream_t s) {
+    const RowPlan r = row_plan(p.d);
+    if (r.nv == 1) return residual_run<T, 1, 1, VEC>(p, bwd, s);
+    if (r.nv == 4) return residual_run<T, 32, 4, VEC>(p, bwd, s);
+    switch (r.wpr) {
+        case 1: return residual_run<T, 1, 2, VEC>(p, bwd, s);
+        case 2: return residual_run<T, 2, 2, VEC>(p, bwd, s);
+        case 4: return residual_run<T, 4, 2, VEC>(p, bwd, s);
+        case 8: return residual_run<T, 8, 2, VEC>(p, bwd, s);
+        case 16: return residual_run<T, 16, 2, VEC>(p, bwd, s);
+        default: return residual_run<T, 32, 2, VEC>(p, bwd, s);
+    }
+}
+
+bool vec_ok(const void *p, int64_t stride, int es) {
+    return ((uintptr_t)p & 15u) == 0 && (stride * es) % 16 == 0;
+}
+
+// ---------------------------------------------------------------- gated norm
+
+// act(z) and act'(z); silu when SILU, else the sigmoid
+template <bool SILU>
+__device__ __forceinline__ void act(float z, float &a, float &da) {
+    const float s = 1.f / (1.f + expf(-z));
+    a = SILU ? z * s : s;
+    da = SILU ? s * fmaf(z, 1.f - s, 1.f) : s * (1.f - s);
+}
+
+constexpr int kGatedThreads = 256;
+
+// G threads (a power of two up to a warp) hold a row of d <= 8 G channels.
+template <typename T, int G, bool VEC, bool SILU>
+__global__ void __launch_bounds__(kGatedThreads)
+    gated_norm_fwd_kernel(const GatedNormArgs p) {
+    const int t = threadIdx.x % G;
+    const int64_t row = ((int64_t)blockIdx.x * kGatedThreads + threadIdx.x) / G;
+    const bool live = row < p.n_tok * p.n_heads;
+    const int64_t n = row / p.n_heads;
+    const int h = (int)(row - n * p.n_heads);
+    float x[8], z[8], w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    if (live) {
+        load_row<1, VEC>(static_cast<const T *>(p.x) + n * p.x_stride + (int64_t)h * p.d, p.d, t, G, x);
+        load_row<1, VEC>(static_cast<const T *>(p.gate) + n * p.gate_stride + (int64_t)h * p.d, p.d, t, G, z);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (!live) return;
+    const float c = 1.f / sqrtf(s / p.d + p.eps);
+    load_row<1, VEC>(p.weight, p.d, t, G, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float a, da;
+        act<SILU>(z[i], a, da);
+        x[i] = x[i] * c * w[i] * a;
+    }
+    store_row<1, VEC>(static_cast<T *>(p.y) + row * p.d, p.d, t, G, x);
+}
+
+template <typename T, int G, bool VEC, bool SILU>
+__global__ void __launch_bounds__(kGatedThreads)
+    gated_norm_bwd_kernel(const GatedNormArgs p, int64_t rounds) {
+    constexpr int kGroups = kGatedThreads / G;
+    __shared__ float sums[kGatedThreads / 32][8 * G];
+    const int t = threadIdx.x % G;
+    const int64_t rows = p.n_tok * p.n_heads, step = (int64_t)gridDim.x * kGroups;
+    float w[8], dw[8];
+    load_row<1, VEC>(p.weight, p.d, t, G, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[i] = 0.f;
+    for (int64_t i0 = 0; i0 < rounds; ++i0) {
+        const int64_t row = i0 * step + (int64_t)blockIdx.x * kGroups + threadIdx.x / G;
+        const bool live = row < rows;
+        float x[8], z[8], dy[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = z[i] = dy[i] = 0.f;
+        if (live) {
+            const int64_t n = row / p.n_heads;
+            const int64_t h = (row - n * p.n_heads) * p.d;
+            load_row<1, VEC>(static_cast<const T *>(p.x) + n * p.x_stride + h, p.d, t, G, x);
+            load_row<1, VEC>(static_cast<const T *>(p.gate) + n * p.gate_stride + h, p.d, t, G, z);
+            load_row<1, VEC>(static_cast<const T *>(p.dy) + n * p.dy_stride + h, p.d, t, G, dy);
+        }
+        float xx = 0.f, tx = 0.f, a[8], da[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            act<SILU>(z[i], a[i], da[i]);
+            xx = fmaf(x[i], x[i], xx);
+            tx = fmaf(w[i] * a[i] * dy[i], x[i], tx);
+        }
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) {
+            xx += __shfl_xor_sync(0xffffffffu, xx, o);
+            tx += __shfl_xor_sync(0xffffffffu, tx, o);
+        }
+        if (!live) continue;
+        const float c = 1.f / sqrtf(xx / p.d + p.eps), m = tx * c * c / p.d;
+        float dx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float n = x[i] * c, wd = w[i] * dy[i];
+            dx[i] = c * (wd * a[i] - x[i] * m);
+            z[i] = wd * n * da[i];
+            dw[i] = fmaf(dy[i] * a[i], n, dw[i]);
+        }
+        store_row<1, VEC>(static_cast<T *>(p.dx) + row * p.d, p.d, t, G, dx);
+        store_row<1, VEC>(static_cast<T *>(p.dgate) + row * p.d, p.d, t, G, z);
+    }
+    // the warp's groups, then the CTA's warps, in a fixed order
+#pragma unroll
+    for (int o = G; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
+    if ((threadIdx.x & 31) < G)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[threadIdx.x >> 5][VEC ? 8 * t + i : t + G * i] = dw[i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.d; c += kGatedThreads) {
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < kGatedThreads / 32; ++i) x += sums[i][c];
+        p.partial[(int64_t)blockIdx.x * p.d + c] = x;
+    }
+}
+
+int gated_group(int d) {
+    int g = 4;
+    while (8 * g < d) g *= 2;
+    return g;
+}
+int64_t gated_bwd_grid(int64_t n_tok, int n_heads, int d) {
+    const int per = kGatedThreads / gated_group(d);
+    return std::max<int64_t>(1, std::min<int64_t>((n_tok * n_heads + per - 1) / per, kSMs * 6));
+}
+
+template <typename T, int G, bool VEC, bool SILU>
+cudaError_t gated_run(const GatedNormArgs &p, bool bwd, cudaStream_t stream) {
+    constexpr int kGroups = kGatedThreads / G;
+    const int64_t rows = p.n_tok * p.n_heads;
+    if (!bwd) {
+        gated_norm_fwd_kernel<T, G, VEC, SILU><<<(unsigned)((rows + kGroups - 1) / kGroups), kGatedThreads, 0, stream>>>(p);
+        count_launches(1);
+        return cudaGetLastError();
+    }
+    const int64_t grid = gated_bwd_grid(p.n_tok, p.n_heads, p.d), step = grid * kGroups;
+    gated_norm_bwd_kernel<T, G, VEC, SILU><<<(unsigned)grid, kGatedThreads, 0, stream>>>(p, (rows + step - 1) / step);
+    sum_parts_kernel<<<dim3((p.d + 31) / 32, 1), 512, 0, stream>>>(p.partial, (int)grid, p.d, p.dw, nullptr);
+    count_launches(2);
+    return cudaGetLastError();
+}
+template <typename T, bool VEC, bool SILU>
+cudaError_t gated_pick(const GatedNormArgs &p, bool bwd, cudaStream_t s) {
+    switch (gated_group(p.d)) {
+        case 4: return gated_run<T, 4, VEC, SILU>(p, bwd, s);
+        case 8: return gated_run<T, 8, VEC, SILU>(p, bwd, s);
+        case 16: return gated_run<T, 16, VEC, SILU>(p, bwd, s);
+        default: return gated_run<T, 32, VEC, SILU>(p, bwd, s);
+    }
+}
+template <typename T>
+cudaError_t gated(const GatedNormArgs &p, bool bwd, cudaStream_t s) {
+    const int es = sizeof(T);
+    bool vec = p.d % 8 == 0 && vec_ok(p.x, p.x_stride, es) && vec_ok(p.gate, p.gate_stride, es) &&
+               vec_ok(p.weight, 0, 4);
+    if (bwd) vec = vec && vec_ok(p.dy, p.dy_stride, es) && vec_ok(p.dx, 0, es) && vec_ok(p.dgate, 0, es);
+    else vec = vec && vec_ok(p.y, 0, es);
+    if (vec) return p.silu ? gated_pick<T, true, true>(p, bwd, s) : gated_pick<T, true, false>(p, bwd, s);
+    return p.silu ? gated_pick<T, false, true>(p, bwd, s) : gated_pick<T, false, false>(p, bwd, s);
+}
+
+template <typename T>
+cudaError_t residual(const ResidualNormArgs &p, bool bwd, cudaStream_t s) {
+    const int es = sizeof(T);
+    bool vec = p.d % 8 == 0 && vec_ok(p.weight, 0, 4) && vec_ok(p.scale, 0, 4) && vec_ok(p.x, p.x_stride, es);
+    if (bwd)
+        vec = vec && vec_ok(p.r, p.r_stride, es) && vec_ok(p.dy, p.dy_stride, es) && vec_ok(p.dr, p.dr_stride, es) &&
+              vec_ok(p.dx, 0, es) && vec_ok(p.dresidual, 0, es);
+    else
+        vec = vec && vec_ok(p.residual, p.residual_stride, es) && vec_ok(p.r, 0, es) && vec_ok(p.y, 0, es);
+    return vec ? residual_pick<T, true>(p, bwd, s) : residual_pick<T, false>(p, bwd, s);
+}
+
+}  // namespace
+
+size_t residual_norm_workspace_bytes(int64_t n_rows, int32_t d, bool scale) {
+    const RowPlan r = row_plan(d);
+    return (size_t)residual_bwd_grid(n_rows, d) * plan_groups(r) * d * 4 * (scale ? 2 : 1);
+}
+size_t gated_norm_workspace_bytes(int64_t n_tok, int32_t n_heads, int32_t d) {
+    return (size_t)gated_bwd_grid(n_tok, n_heads, d) * d * 4;
+}
+cudaError_t launch_residual_norm(const ResidualNormArgs &p, bool bwd, cudaStream_t s) {
+    return p.bf16 ? residual<bf16>(p, bwd, s) : residual<float>(p, bwd, s);
+}
+cudaError_t launch_gated_norm(const GatedNormArgs &p, bool bwd, cudaStream_t s) {
+    return p.bf16 ? gated<bf16>(p, bwd, s) : gated<float>(p, bwd, s);
+}
+
+}  // namespace kda

@@ -491,6 +491,118 @@ int32_t kda_chunk_fwd_pipeline_plan(const int32_t *host_cu_seqlens, int32_t n_se
                                     int64_t n_tok, int32_t n_segments, int64_t *pieces,
                                     int32_t capacity);
 
+/*
+ * ---- the gated delta rule with one decay per head, and the norms around a block ----
+ *
+ * An addition of this library beside the bounded per-channel form above: the same state,
+ * forgotten through one unbounded factor per token and head,
+ *
+ *   S_t = exp(g_t) S_{t-1} + beta_t k_t (v_t - exp(g_t) S_{t-1}^T k_t)^T
+ *   o_t = d_k^-1/2 S_t^T q_t
+ *
+ * with the log-decay g_t itself as the input (any value up to 0; -inf forgets everything,
+ * as at the start of a new document; values below -200 act as -inf in the chunked calls)
+ * and grouped heads: value head h reads key head h / (n_heads / n_k_heads).
+ *   q, k     [n_tok, n_k_heads, d_k] dtype, tokens q_stride / k_stride elements apart
+ *   v        [n_tok, n_heads, d_v]   dtype, tokens v_stride elements apart
+ *            (a token's row is contiguous; q, k and v may be slices of one projection)
+ *   g, beta  [n_tok, n_heads]        float32, contiguous
+ *   h0, h_final, cu_seqlens, out     as for kda_chunk_fwd (n_heads heads), contiguous
+ * Inputs are aligned to their element size; 16-byte aligned rows are read faster.
+ * 1 <= d_k, d_v <= 128, n_heads a multiple of n_k_heads. State, sums and gradients of g and
+ * beta are fp32; with KDA_BF16 the products run on the tensor cores with every operand
+ * that is not itself a bf16 input carried in two bf16 parts (about 2^-17 of relative
+ * rounding), with KDA_F32 in three (about 2^-24). Results are deterministic. cu_seqlens
+ * is read on the device only, as above.
+ */
+
+/*
+ * kda_gdr_chunk_fwd -- the forward pass over packed sequences, in chunks of 64 tokens.
+ * workspace: device memory, 16-byte aligned, kda_gdr_chunk_fwd_workspace_bytes() bytes,
+ * caller-owned, contents ignored on entry (0 for invalid sizes). out and h_final (may be
+ * NULL) may not overlap an input, the workspace or each other. Asynchronous on `stream`;
+ * nothing is allocated. Returns KDA_ERR_INVALID_ARG (missing pointer, negative size, heads
+ * that do not divide, a stride below the row, misalignment, overlap, workspace),
+ * KDA_ERR_UNSUPPORTED (dtype, d_k or d_v above 128) or KDA_ERR_CUDA; no sequence or no
+ * token is valid (h_final = h0).
+ */
+size_t kda_gdr_chunk_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads,
+                                         kda_dtype dtype);
+kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const float *g,
+                             const float *beta, const float *h0, const int32_t *cu_seqlens,
+                             void *out, float *h_final, void *workspace,
+                             size_t workspace_bytes, int64_t n_tok, int32_t n_seq,
+                             int32_t n_k_heads, int32_t n_heads, int32_t d_k, int32_t d_v,
+                             kda_dtype dtype, void *stream);
+
+/*
+ * kda_gdr_step -- one token for each of n_rows sequences, in place on a pool of states:
+ * row b reads and rewrites state[slots[b]] ([n_slots, n_heads, d_k, d_v] fp32); slots NULL
+ * means row b owns state b (n_rows <= n_slots). A slot outside [0, n_slots) marks a padded
+ * row: its out is 0 and no state is touched. Two rows of a call may not share a slot.
+ * q, k, v, g, beta, out: n_rows tokens, as above. Errors as kda_gdr_chunk_fwd; state and
+ * out may not overlap each other or an input; n_rows = 0 is a valid no-op.
+ */
+kda_status kda_gdr_step(const void *q, const void *k, const void *v, int64_t q_stride,
+                        int64_t k_stride, int64_t v_stride, const float *g,
+                        const float *beta, float *state, const int32_t *slots, void *out,
+                        int32_t n_rows, int32_t n_slots, int32_t n_k_heads, int32_t n_heads,
+                        int32_t d_k, int32_t d_v, kda_dtype dtype, void *stream);
+
+/*
+ * kda_residual_norm_fwd -- the norm before a block, fused with the residual sum:
+ *   r = residual + scale x,   y = weight r / sqrt(mean(r^2) + eps)      per row of d channels
+ * x, residual [n_rows, d] dtype, rows x_stride / residual_stride elements apart; residual
+ * NULL: r = scale x; scale [d] float32 or NULL (1); weight [d] float32; r and y [n_rows, d]
+ * dtype, contiguous; r NULL: not written. The mean is taken over the fp32 r before its
+ * rounding to dtype. 1 <= d <= 32768, eps > 0.
+ *
+ * kda_residual_norm_bwd -- its gradients, from r as the forward pass wrote it, dy and dr
+ * (the gradient that reaches r from beyond the norm; NULL: none):
+ *   dresidual (the gradient of r), and with a scale dx = scale dresidual, dscale = the sum
+ *   over rows of x dresidual; dweight = the sum over rows of dy r / sqrt(mean(r^2) + eps).
+ * Without a scale dx and dscale are NULL and dx is dresidual. workspace: 16-byte aligned,
+ * kda_residual_norm_bwd_workspace_bytes() bytes. Sums over rows run in a fixed order.
+ * Both: asynchronous on `stream`, nothing allocated, no output over an input;
+ * KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED (dtype, d) or KDA_ERR_CUDA as above.
+ */
+kda_status kda_residual_norm_fwd(const void *x, int64_t x_stride, const void *residual,
+                                 int64_t residual_stride, const float *scale,
+                                 const float *weight, void *r, void *y, int64_t n_rows,
+                                 int32_t d, float eps, kda_dtype dtype, void *stream);
+size_t kda_residual_norm_bwd_workspace_bytes(int64_t n_rows, int32_t d, int with_scale);
+kda_status kda_residual_norm_bwd(const void *dy, int64_t dy_stride, const void *dr,
+                                 int64_t dr_stride, const void *r, int64_t r_stride,
+                                 const void *x, int64_t x_stride, const float *scale,
+                                 const float *weight, void *dx, void *dresidual,
+                                 float *dscale, float *dweight, void *workspace,
+                                 size_t workspace_bytes, int64_t n_rows, int32_t d, float eps,
+                                 kda_dtype dtype, void *stream);
+
+/*
+ * kda_gated_norm_fwd -- the norm after the recurrence, fused with its gate:
+ *   y = weight x / sqrt(mean(x^2) + eps) act(gate)                 per token and head of d channels
+ * x, gate [n_tok, n_heads, d] dtype, tokens x_stride / gate_stride elements apart; weight
+ * [d] float32, shared by the heads; y [n_tok, n_heads, d] contiguous; act(z) = sigmoid(z)
+ * or z sigmoid(z). 1 <= d <= 256, eps > 0.
+ *
+ * kda_gated_norm_bwd -- the gradients dx, dgate [n_tok, n_heads, d] and dweight [d] from
+ * dy; workspace and errors as kda_residual_norm_bwd.
+ */
+enum { KDA_ACT_SIGMOID = 0, KDA_ACT_SILU = 1 };
+kda_status kda_gated_norm_fwd(const void *x, int64_t x_stride, const void *gate,
+                              int64_t gate_stride, const float *weight, void *y,
+                              int64_t n_tok, int32_t n_heads, int32_t d, float eps,
+                              int32_t activation, kda_dtype dtype, void *stream);
+size_t kda_gated_norm_bwd_workspace_bytes(int64_t n_tok, int32_t n_heads, int32_t d);
+kda_status kda_gated_norm_bwd(const void *dy, int64_t dy_stride, const void *x,
+                              int64_t x_stride, const void *gate, int64_t gate_stride,
+                              const float *weight, void *dx, void *dgate, float *dweight,
+                              void *workspace, size_t workspace_bytes, int64_t n_tok,
+                              int32_t n_heads, int32_t d, float eps, int32_t activation,
+                              kda_dtype dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
