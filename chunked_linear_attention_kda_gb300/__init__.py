@@ -27,7 +27,7 @@ __all__ = ["validate_cu_seqlens", "count_nonfinite", "chunk_fwd", "chunk_fwd_sim
            "segmented_fwd", "decode_step", "chunk_bwd", "chunk_bwd_static_scratch",
            "bwd_timing_start", "bwd_timing_read", "chunk_fwd_variant", "gate_projection",
            "chunk_fwd_gated",
-           "gdr_chunk_fwd", "gdr_step", "residual_norm_fwd",
+           "gdr_chunk_fwd", "gdr_chunk_bwd", "gdr_step", "residual_norm_fwd",
            "residual_norm_bwd", "gated_norm_fwd", "gated_norm_bwd",
            "load_library",
            "kernel_launch_count", "read_device_flags", "selftest_bounded_wait",
@@ -48,7 +48,8 @@ EXPORTED_SYMBOLS = ("kda_version", "kda_status_string", "kda_last_error",
                     "kda_count_nonfinite", "kda_check_outputs",
                     "kda_chunk_fwd_gated_workspace_bytes", "kda_chunk_fwd_gated",
                     "kda_gate_projection_out",
-                    "kda_gdr_chunk_fwd_workspace_bytes", "kda_gdr_chunk_fwd", "kda_gdr_step",
+                    "kda_gdr_chunk_fwd_workspace_bytes", "kda_gdr_chunk_fwd",
+                    "kda_gdr_chunk_bwd_workspace_bytes", "kda_gdr_chunk_bwd", "kda_gdr_step",
                     "kda_residual_norm_fwd", "kda_residual_norm_bwd_workspace_bytes",
                     "kda_residual_norm_bwd", "kda_gated_norm_fwd",
                     "kda_gated_norm_bwd_workspace_bytes", "kda_gated_norm_bwd")
@@ -150,6 +151,8 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         for name, res, args in (
                 ("kda_gdr_chunk_fwd_workspace_bytes", SZ, [I64, I32, I32, E]),
                 ("kda_gdr_chunk_fwd", E, [P] * 3 + [I64] * 3 + [P] * 7 + [SZ, I64] + [I32] * 5 + [E, P]),
+                ("kda_gdr_chunk_bwd_workspace_bytes", SZ, [I64] + [I32] * 4 + [E]),
+                ("kda_gdr_chunk_bwd", E, [P] * 3 + [I64] * 3 + [P] * 13 + [SZ, I64] + [I32] * 5 + [E, P]),
                 ("kda_gdr_step", E, [P] * 3 + [I64] * 3 + [P] * 5 + [I32] * 6 + [E, P]),
                 ("kda_residual_norm_fwd", E, [P, I64, P, I64] + [P] * 4 + [I64, I32, F, E, P]),
                 ("kda_residual_norm_bwd_workspace_bytes", SZ, [I64, I32, E]),
@@ -714,5 +717,5 @@ def segmented_fwd(q, k, v, gate_logits, beta, h0=None, cu_seqlens=None, *, segme
     return out, h_final
 
 
-from .block import (gated_norm_bwd, gated_norm_fwd, gdr_chunk_fwd, gdr_step,  # noqa: E402
-                    residual_norm_bwd, residual_norm_fwd)
+from .block import (gated_norm_bwd, gated_norm_fwd, gdr_chunk_bwd, gdr_chunk_fwd,  # noqa: E402
+                    gdr_step, residual_norm_bwd, residual_norm_fwd)

@@ -114,6 +114,35 @@ def gdr_chunk_fwd(q, k, v, g, beta, h0=None, cu_seqlens=None, *, out=None, h_fin
     return out, h_final
 
 
+def gdr_chunk_bwd(q, k, v, g, beta, h0, cu_seqlens, dout, dh_final=None, *, want_dh0=True,
+                  workspace=None):
+    """Backward of ``gdr_chunk_fwd`` through ``kda_gdr_chunk_bwd``: the gradients of ``<dout,
+    out> + <dh_final, h_final>``. Returns ``(dq, dk, dv, dg, dbeta, dh0)`` (``dh0`` None unless
+    ``want_dh0``); ``dq`` and ``dk`` are summed over the value heads of a key head."""
+    lib, stream = _start(q, "gdr_chunk_bwd")
+    n, hk, h, dk, dv, strides = _gdr_inputs(q, k, v, g, beta)
+    n_seq, cu_seqlens = _sequences(q, n, h, dk, dv, h0, cu_seqlens)
+    _flat("dout", dout, (n, h, dv), q.dtype, q)
+    if dh_final is not None:
+        _flat("dh_final", dh_final, (n_seq, h, dk, dv), torch.float32, q)
+    grads = (torch.empty((n, hk, dk), dtype=q.dtype, device=q.device),
+             torch.empty((n, hk, dk), dtype=q.dtype, device=q.device),
+             torch.empty((n, h, dv), dtype=q.dtype, device=q.device),
+             torch.empty((n, h), dtype=torch.float32, device=q.device),
+             torch.empty((n, h), dtype=torch.float32, device=q.device),
+             torch.empty((n_seq, h, dk, dv), dtype=torch.float32, device=q.device)
+             if want_dh0 else None)
+    code = _CODE[q.dtype]
+    if workspace is None:
+        need = lib.kda_gdr_chunk_bwd_workspace_bytes(n, n_seq, h, dk, dv, code)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _done(lib, lib.kda_gdr_chunk_bwd(
+        _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(h0), _p(cu_seqlens), _p(dout),
+        _p(dh_final), *[_p(t) for t in grads], _p(workspace),
+        workspace.numel() * workspace.element_size(), n, n_seq, hk, h, dk, dv, code, stream))
+    return grads
+
+
 def gdr_step(q, k, v, g, beta, state, slots=None, *, out=None):
     """One token per row through ``kda_gdr_step``: row b updates ``state[slots[b]]`` in place
     (``state`` [n_slots, H, d_k, d_v] fp32; ``slots`` int32 [B], None: row b has state b). A

@@ -130,6 +130,43 @@ kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, int64_
     return launched(kda::launch_gdr_fwd(p, (cudaStream_t)stream), "gated delta rule forward launch");
 }
 
+size_t kda_gdr_chunk_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k,
+                                         int32_t d_v, kda_dtype dtype) {
+    if (n_tok < 0 || n_seq < 0 || n_heads <= 0 || d_k <= 0 || d_v <= 0 || d_k > 128 || d_v > 128) return 0;
+    return kda::gdr_bwd_workspace_bytes(n_tok, n_seq, n_heads, d_k, d_v, dtype == KDA_BF16);
+}
+
+kda_status kda_gdr_chunk_bwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, const float *g, const float *beta, const float *h0,
+                             const int32_t *cu_seqlens, const void *dout, const float *dh_final, void *dq,
+                             void *dk, void *dv, float *dg, float *dbeta, float *dh0, void *workspace,
+                             size_t workspace_bytes, int64_t n_tok, int32_t n_seq, int32_t n_k_heads,
+                             int32_t n_heads, int32_t d_k, int32_t d_v, kda_dtype dtype, void *stream) {
+    kda::GdrArgs p = gdr_args(q, k, v, q_stride, k_stride, v_stride, g, beta, h0, cu_seqlens, workspace, n_tok,
+                              n_seq, n_k_heads, n_heads, d_k, d_v, dtype);
+    p.dout = dout; p.dh_final = dh_final;
+    p.dq = dq; p.dk = dk; p.dv = dv; p.dg = dg; p.dbeta = dbeta; p.dh0 = dh0;
+    kda_status s = check_gdr(p, dtype);
+    if (s != KDA_OK) return s;
+    if (n_tok > 0 && (!dout || !dq || !dk || !dv || !dg || !dbeta))
+        return api_fail(KDA_ERR_INVALID_ARG, "dout, dq, dk, dv, dg and dbeta are required");
+    if (n_seq == 0) return api_ok();
+    const size_t need = n_tok ? kda::gdr_bwd_workspace_bytes(n_tok, n_seq, n_heads, d_k, d_v, p.bf16) : 0;
+    s = check_workspace(workspace, workspace_bytes, need);
+    if (s != KDA_OK) return s;
+    const size_t es = p.bf16 ? 2 : 4, st = (size_t)n_seq * n_heads * d_k * d_v * 4;
+    const int64_t wk = (int64_t)n_k_heads * d_k, wv = (int64_t)n_heads * d_v;
+    const Range ins[] = {rows(q, n_tok, q_stride, wk, es), rows(k, n_tok, k_stride, wk, es),
+                         rows(v, n_tok, v_stride, wv, es), rows(g, n_tok, n_heads, n_heads, 4),
+                         rows(beta, n_tok, n_heads, n_heads, 4), {h0, st}, {cu_seqlens, (size_t)(n_seq + 1) * 4},
+                         rows(dout, n_tok, wv, wv, es), {dh_final, st}};
+    const Range outs[] = {rows(dq, n_tok, wk, wk, es), rows(dk, n_tok, wk, wk, es), rows(dv, n_tok, wv, wv, es),
+                          rows(dg, n_tok, n_heads, n_heads, 4), rows(dbeta, n_tok, n_heads, n_heads, 4), {dh0, st},
+                          {workspace, need}};
+    if (clash(ins, outs)) return api_fail(KDA_ERR_INVALID_ARG, kOverlap);
+    return launched(kda::launch_gdr_bwd(p, (cudaStream_t)stream), "gated delta rule backward launch");
+}
+
 kda_status kda_gdr_step(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
                         int64_t v_stride, const float *g, const float *beta, float *state,
                         const int32_t *slots, void *out, int32_t n_rows, int32_t n_slots,

@@ -51,10 +51,27 @@ __device__ __forceinline__ Chunk find_chunk(const int32_t *cu, int n_seq, int64_
 }
 
 // Per (slot, value head): X and P tile images (NS planes each, swizzled as the kernels read
-// them) and the gate vectors gamma, delta, beta, [Gamma].
-constexpr int kGateFloats = 4 * C;
+// them) and the gate vectors gamma, delta, beta, Gamma (repeated) and the running sum of g as
+// two floats. The chains read the first four.
+constexpr int kGateFloats = 6 * C, kChainGates = 4 * C;
 __host__ __device__ constexpr size_t terms_bytes(int ns) {
     return (size_t)2 * ns * kTile * 2 + kGateFloats * 4;
+}
+
+// Per (slot, value head) of the backward pass, behind the terms: S0^T and dS1^T (value
+// channels x d_k padded to DKP), U^T and E^T (value channels x 64), NS planes each, swizzled.
+__host__ __device__ __forceinline__ int pad_v(int d_v) { return (d_v + 31) & ~31; }
+__host__ __device__ __forceinline__ size_t scan_state_bytes(int ns, int dkp, int d_v) {
+    return (size_t)ns * pad_v(d_v) * dkp * 2;
+}
+__host__ __device__ __forceinline__ size_t scan_value_bytes(int ns, int d_v) {
+    return (size_t)ns * pad_v(d_v) * C * 2;
+}
+__host__ __device__ __forceinline__ size_t scan_bytes(int ns, int dkp, int d_v) {
+    return 2 * (scan_state_bytes(ns, dkp, d_v) + scan_value_bytes(ns, d_v));
+}
+__host__ __device__ __forceinline__ size_t scan_offset(int64_t n_tok, int64_t n_seq, int64_t n_heads, int ns) {
+    return (size_t)n_slots(n_tok, n_seq) * n_heads * terms_bytes(ns);
 }
 
 // ---------------------------------------------------------------- tiles
@@ -124,6 +141,23 @@ __device__ __forceinline__ void acc_to_a(const float (*d)[4], uint32_t (*a)[4]) 
 #pragma unroll
         for (int p = 0; p < NP; ++p) a[p][i] = w[p];
     }
+}
+
+// 16 rows (row0 ..) of NT accumulator tiles as NS planes of a swizzled tile image in global
+// memory, planes `plane` bytes apart
+template <int NS, int NT, int RB>
+__device__ __forceinline__ void store_planes(char *dst, size_t plane, int row0, const float (*d)[4]) {
+    const int gr = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w[NS];
+            split2<NS>(d[n][2 * h], d[n][2 * h + 1], w);
+            char *at = dst + tile_off<RB>(row0 + gr + 8 * h, n * 8 + tq * 2);
+#pragma unroll
+            for (int p = 0; p < NS; ++p) *reinterpret_cast<uint32_t *>(at + p * plane) = w[p];
+        }
 }
 
 // ---------------------------------------------------------------- loading inputs

@@ -1,0 +1,736 @@
+// kda_gdr_bwd.cu -- backward pass of the chunked gated delta rule with one decay per head:
+// gradients of <dout, out> + <dh_final, h_final>. Notation and the forward's chunk form as
+// in kda_gdr_fwd.cu (X, P with the output scale folded in, gamma, delta, Gamma); s the scale.
+//
+// Per chunk, with the gradient dS1 of its end state:
+//   dU = P^T dO + (delta K) dS1,   E = X^T dU,   dV = beta E
+//   dS0 = Gamma dS1 + (s gamma Q)^T dO - (gamma beta K)^T E
+// and, from S0, dS1, U and E (local to the chunk, e = e^D, lower triangles):
+//   B = s e (dO U^T),  F = e (E U^T) below the diagonal
+//   dQ = s gamma (dO S0^T) + B K
+//   dK = -gamma beta (E S0^T) + delta (U dS1^T) + B^T Q - (beta F + (beta F)^T) K
+//   dbeta_r = E_r.V_r - gamma_r k_r.(E S0^T)_r - sum_j F_rj k_r.k_j
+//   dg_i = Gamma <S0, dS1> + sum_{r >= i} a_r + sum_{r < i} b_r + sum_{r >= i > j} M_rj
+//   a_r = gamma_r (s q_r.(dO S0^T)_r - beta_r k_r.(E S0^T)_r),  b_r = delta_r k_r.(U dS1^T)_r
+//   M_rj = B_rj q_r.k_j - beta_r F_rj k_r.k_j;  its double sum is a running sum of row sums
+//   minus column sums.
+//
+// Three launches: the chunk terms (shared with the forward); one launch with the forward
+// chain (S0, U of every chunk) and the reverse chain (dS1, E), which do not depend on each
+// other; and the local gradients, all chunks side by side, one CTA per (chunk, key head)
+// that walks over the value heads sharing the key head and adds their dQ and dK in
+// registers (no atomics: the same call gives the same bits).
+#include <cmath>
+
+#include "kda_gdr_chain.h"
+
+namespace kda {
+namespace gdr {
+namespace {
+
+// ---------------------------------------------------------------- reverse chain
+template <int NI, int DKP, int W>
+struct ReverseSmem {
+    static constexpr int NS = NI == 1 ? 2 : 3;
+    static constexpr int kStages = NI == 1 ? 2 : 1;
+    static constexpr int kPlane = C * DKP * 2, kVPlane = C * 16 * W * 2;
+    static constexpr int K = 0, Q = K + NI * kPlane, X = Q + NI * kPlane, P = X + NS * kTile * 2;
+    static constexpr int Gate = P + NS * kTile * 2, dO = Gate + kChainGates * 4;
+    static constexpr int kStage = dO + NI * kVPlane;
+    static constexpr int kBytes = kStages * kStage;
+};
+
+template <typename T, int DKP, int W>
+__device__ __forceinline__ void reverse_chain(const GdrArgs &p, int block, float scale, bool vec_qk, bool vec_do) {
+    constexpr int NI = InputPlanes<T>::N;
+    using L = ReverseSmem<NI, DKP, W>;
+    constexpr int NS = L::NS, RB = DKP * 2, VB = 32 * W, NT = DKP / 8;
+    extern __shared__ __align__(128) char smem[];
+    const uint32_t base = ptx::smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
+    const int n_blk = (p.d_v + 16 * W - 1) / (16 * W);
+    const int blk = block % n_blk, sh = block / n_blk;
+    const int head = sh % p.n_heads, seq = sh / p.n_heads, kh = head / (p.n_heads / p.n_k_heads);
+    const int64_t tok0 = p.cu_seqlens[seq];
+    const int len = (int)(p.cu_seqlens[seq + 1] - tok0);
+    const int n_chunks = (len + C - 1) / C;
+    const int64_t slot0 = slot_base(p.cu_seqlens, seq);
+    const int dv0 = blk * 16 * W, v0 = dv0 + warp * 16;
+    const char *ws = static_cast<const char *>(p.workspace);
+    const char *terms = ws + (slot0 * p.n_heads + head) * terms_bytes(NS);
+    const size_t terms_step = (size_t)p.n_heads * terms_bytes(NS);
+
+    float S[NT][4];  // dS^T, laid out as the forward chain's S^T
+    const size_t st_at = ((size_t)seq * p.n_heads + head) * p.d_k * p.d_v;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = n * 8 + tq * 2 + (i & 1), v = v0 + gr + (i >> 1) * 8;
+            S[n][i] = p.dh_final && c < p.d_k && v < p.d_v ? p.dh_final[st_at + (size_t)c * p.d_v + v] : 0.f;
+        }
+
+    auto load = [&](int c) {
+        const uint32_t s = base + (c % L::kStages) * L::kStage;
+        const int64_t t = tok0 + (int64_t)c * C;
+        const int rows = min(C, len - c * C);
+        load_tile<T, RB>(s + L::K, L::kPlane, static_cast<const T *>(p.k) + t * p.k_stride + (int64_t)kh * p.d_k,
+                         p.k_stride, rows, p.d_k, vec_qk, tid, 32 * W);
+        load_tile<T, RB>(s + L::Q, L::kPlane, static_cast<const T *>(p.q) + t * p.q_stride + (int64_t)kh * p.d_k,
+                         p.q_stride, rows, p.d_k, vec_qk, tid, 32 * W);
+        load_tile<T, VB>(s + L::dO, L::kVPlane,
+                         static_cast<const T *>(p.dout) + (t * p.n_heads + head) * p.d_v + dv0,
+                         (int64_t)p.n_heads * p.d_v, rows, p.d_v - dv0, vec_do, tid, 32 * W);
+        const char *src = terms + c * terms_step;
+        load_raw(s + L::X, src, 2 * NS * kTile * 2, tid, 32 * W);  // X and P
+        load_raw(s + L::Gate, src + 2 * NS * kTile * 2, kChainGates * 4, tid, 32 * W);
+    };
+
+    if (L::kStages == 2 && n_chunks > 0) load(n_chunks - 1);
+    ptx::cp_async_commit();
+    for (int c = n_chunks - 1; c >= 0; --c) {
+        if (L::kStages == 2) {
+            if (c > 0) load(c - 1);
+            ptx::cp_async_commit();
+            cp_async_wait<1>();
+        } else {
+            load(c);
+            ptx::cp_async_commit();
+            cp_async_wait<0>();
+        }
+        __syncthreads();
+        const uint32_t s = base + (c % L::kStages) * L::kStage;
+        const float *gate = reinterpret_cast<const float *>(smem + (c % L::kStages) * L::kStage + L::Gate);
+        char *rec = static_cast<char *>(p.workspace) + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
+                    ((slot0 + c) * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v);
+        const bool keep = v0 < pad_v(p.d_v);
+        if (keep)
+            store_planes<NS, NT, RB>(rec + scan_state_bytes(NS, DKP, p.d_v), (size_t)pad_v(p.d_v) * RB, v0, S);
+
+        // dU^T = delta (dS1^T K^T) + dO^T P
+        float y[8][4];
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[n][i] = 0.f;
+#pragma unroll
+        for (int kx = 0; kx < DKP / 16; ++kx) {
+            uint32_t a[NS][4];
+            acc_to_a<NS>(&S[2 * kx], a);
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int pb = 0; pb < NI; ++pb) {
+                    uint32_t b[4];
+                    frag_b<RB>(s + L::K + pb * L::kPlane, n * 16, kx * 16, b);
+#pragma unroll
+                    for (int pa = 0; pa + pb < NS; ++pa) {
+                        ptx::mma16816(y[2 * n], a[pa], b[0], b[1]);
+                        ptx::mma16816(y[2 * n + 1], a[pa], b[2], b[3]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const float2 de = *reinterpret_cast<const float2 *>(gate + C + n * 8 + tq * 2);
+            y[n][0] *= de.x; y[n][1] *= de.y; y[n][2] *= de.x; y[n][3] *= de.y;
+        }
+#pragma unroll
+        for (int kx = 0; kx < 4; ++kx) {
+            uint32_t a[NI][4];
+#pragma unroll
+            for (int pa = 0; pa < NI; ++pa) frag_a_t<VB>(s + L::dO + pa * L::kVPlane, kx * 16, warp * 16, a[pa]);
+#pragma unroll
+            for (int n = 0; n <= kx; ++n)
+#pragma unroll
+                for (int pb = 0; pb < NS; ++pb) {
+                    uint32_t b[4];
+                    frag_b_t<128>(s + L::P + pb * kTile * 2, kx * 16, n * 16, b);
+#pragma unroll
+                    for (int pa = 0; pa < NI && pa + pb < NS; ++pa) {
+                        ptx::mma16816(y[2 * n], a[pa], b[0], b[1]);
+                        ptx::mma16816(y[2 * n + 1], a[pa], b[2], b[3]);
+                    }
+                }
+        }
+        // E^T = dU^T X
+        float e[8][4];
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[n][i] = 0.f;
+#pragma unroll
+        for (int kx = 0; kx < 4; ++kx) {
+            uint32_t a[NS][4];
+            acc_to_a<NS>(&y[2 * kx], a);
+#pragma unroll
+            for (int n = 0; n <= kx; ++n)
+#pragma unroll
+                for (int pb = 0; pb < NS; ++pb) {
+                    uint32_t b[4];
+                    frag_b_t<128>(s + L::X + pb * kTile * 2, kx * 16, n * 16, b);
+#pragma unroll
+                    for (int pa = 0; pa + pb < NS; ++pa) {
+                        ptx::mma16816(e[2 * n], a[pa], b[0], b[1]);
+                        ptx::mma16816(e[2 * n + 1], a[pa], b[2], b[3]);
+                    }
+                }
+        }
+        if (keep)
+            store_planes<NS, 8, 128>(rec + 2 * scan_state_bytes(NS, DKP, p.d_v) + scan_value_bytes(NS, p.d_v),
+                                     (size_t)pad_v(p.d_v) * 128, v0, e);
+        // dS0^T = Gamma dS1^T - (gamma beta E)^T K + (s gamma dO)^T Q
+        const float whole = gate[3 * C];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[n][i] *= whole;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const float2 ga = *reinterpret_cast<const float2 *>(gate + n * 8 + tq * 2);
+            const float2 be = *reinterpret_cast<const float2 *>(gate + 2 * C + n * 8 + tq * 2);
+            const float x0 = -ga.x * be.x, x1 = -ga.y * be.y;
+            e[n][0] *= x0; e[n][1] *= x1; e[n][2] *= x0; e[n][3] *= x1;
+        }
+#pragma unroll
+        for (int kx = 0; kx < 4; ++kx) {
+            uint32_t a[NS][4], d[NS][4];
+            acc_to_a<NS>(&e[2 * kx], a);
+            {
+                uint32_t w[NI][4];
+#pragma unroll
+                for (int pa = 0; pa < NI; ++pa) frag_a_t<VB>(s + L::dO + pa * L::kVPlane, kx * 16, warp * 16, w[pa]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 ga = *reinterpret_cast<const float2 *>(gate + kx * 16 + (i >> 1) * 8 + tq * 2);
+                    float x = 0.f, z = 0.f;
+#pragma unroll
+                    for (int pa = 0; pa < NI; ++pa) {
+                        x += lo_f(w[pa][i]);
+                        z += hi_f(w[pa][i]);
+                    }
+                    uint32_t sp[NS];
+                    split2<NS>(x * (scale * ga.x), z * (scale * ga.y), sp);
+#pragma unroll
+                    for (int q = 0; q < NS; ++q) d[q][i] = sp[q];
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < DKP / 16; ++n)
+#pragma unroll
+                for (int pb = 0; pb < NI; ++pb) {
+                    uint32_t b[4], f[4];
+                    frag_b_t<RB>(s + L::K + pb * L::kPlane, kx * 16, n * 16, b);
+                    frag_b_t<RB>(s + L::Q + pb * L::kPlane, kx * 16, n * 16, f);
+#pragma unroll
+                    for (int pa = 0; pa + pb < NS; ++pa) {
+                        ptx::mma16816(S[2 * n], a[pa], b[0], b[1]);
+                        ptx::mma16816(S[2 * n + 1], a[pa], b[2], b[3]);
+                        ptx::mma16816(S[2 * n], d[pa], f[0], f[1]);
+                        ptx::mma16816(S[2 * n + 1], d[pa], f[2], f[3]);
+                    }
+                }
+        }
+        __syncthreads();
+    }
+    if (p.dh0) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = n * 8 + tq * 2 + (i & 1), v = v0 + gr + (i >> 1) * 8;
+                if (c < p.d_k && v < p.d_v) p.dh0[st_at + (size_t)c * p.d_v + v] = S[n][i];
+            }
+    }
+}
+
+// even blocks run the reverse chain (the longer one) of a channel block, odd ones the forward
+template <typename T, int DKP, int W>
+__global__ void __launch_bounds__(32 * W)
+    gdr_scan_kernel(const GdrArgs p, float scale, bool vec_qk, bool vec_v, bool vec_do) {
+    if (blockIdx.x & 1) chain<T, DKP, W, true>(p, blockIdx.x >> 1, scale, vec_qk, vec_v, false);
+    else reverse_chain<T, DKP, W>(p, blockIdx.x >> 1, scale, vec_qk, vec_do);
+}
+
+// ---------------------------------------------------------------- local gradients
+constexpr int kLocalThreads = 256;
+
+template <int NI, int DKP>
+struct LocalSmem {
+    static constexpr int NS = NI == 1 ? 2 : 3;
+    static constexpr int kStages = NI == 1 ? 2 : 1;
+    static constexpr int kPlane = C * DKP * 2;
+    static constexpr int kIn = C * 32 * 2, kVal = 32 * C * 2, kState = 32 * DKP * 2;  // one plane of a 32-channel slice
+    static constexpr int dO = 0, V = dO + NI * kIn, U = V + (NI == 1 ? kIn : 0),  // fp32 V is read in place
+                          E = U + NS * kVal, S = E + NS * kVal;
+    static constexpr int dS = S + NS * kState, kSlice = dS + NS * kState;
+    static constexpr int B = 0, F = NI * kTile * 2;  // over the first slice buffer, once the slices are done
+    static_assert(2 * NI * kTile * 2 <= kSlice, "B and F fit a slice buffer");
+    static constexpr int K = kStages * kSlice, Q = K + NI * kPlane, Pair = Q + NI * kPlane;
+    static constexpr int Gate = Pair + 2 * kTile * 4, Red = Gate + kGateFloats * 4;
+    // Red: [2][64] row sums of q.x, k.x, k.x, F k.k, M over the column halves; [64] E.V;
+    // [4][64] column sums of M over the row blocks; [8] the warps' parts of <S0, dS1>
+    static constexpr int kRed = 5 * 2 * C + C + 4 * C + 8;
+    static constexpr int kBytes = Red + kRed * 4;
+    static_assert(kBytes <= 227 * 1024, "fits an SM");
+};
+
+__device__ __forceinline__ float quad_sum(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+template <typename T, int DKP>
+__global__ void __launch_bounds__(kLocalThreads)
+    gdr_local_kernel(const GdrArgs p, float scale, bool vec_qk, bool vec_v, bool vec_do, bool wide_k, bool wide_v) {
+    constexpr int NI = InputPlanes<T>::N;
+    using L = LocalSmem<NI, DKP>;
+    constexpr int NS = L::NS, RB = DKP * 2, NH = DKP / 32;  // NH: 16-column steps of half the key channels
+    extern __shared__ __align__(128) char smem[];
+    const uint32_t base = ptx::smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
+    const int wr = warp & 3, wc = warp >> 2;  // token rows 16 wr .., half wc of the columns
+    const int64_t slot = blockIdx.x;
+    const Chunk ch = find_chunk(p.cu_seqlens, p.n_seq, slot);
+    if (ch.len == 0) return;
+    const int kh = blockIdx.y, group = p.n_heads / p.n_k_heads;
+    const int n_sl = pad_v(p.d_v) / 32;
+    const char *ws = static_cast<const char *>(p.workspace);
+    float *pair = reinterpret_cast<float *>(smem + L::Pair);
+    float *gate = reinterpret_cast<float *>(smem + L::Gate);
+    float *red = reinterpret_cast<float *>(smem + L::Red);
+    float *r_qx = red, *r_kx = red + 2 * C, *r_ku = red + 4 * C, *r_fk = red + 6 * C, *r_m = red + 8 * C;
+    float *r_ev = red + 10 * C, *c_m = red + 11 * C, *r_ss = red + 15 * C;
+
+    auto load = [&](int step) {  // slice `step % n_sl` of value head `step / n_sl`
+        const int head = kh * group + step / n_sl, sl = step % n_sl;
+        const uint32_t s = base + (step % L::kStages) * L::kSlice;
+        load_tile<T, 64>(s + L::dO, L::kIn, static_cast<const T *>(p.dout) + (ch.t0 * p.n_heads + head) * p.d_v + sl * 32,
+                         (int64_t)p.n_heads * p.d_v, ch.len, p.d_v - sl * 32, vec_do, tid, kLocalThreads);
+        if (NI == 1) load_tile<T, 64>(s + L::V, L::kIn, static_cast<const T *>(p.v) + ch.t0 * p.v_stride + (int64_t)head * p.d_v + sl * 32,
+                         p.v_stride, ch.len, p.d_v - sl * 32, vec_v, tid, kLocalThreads);
+        const char *rec = ws + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
+                          (slot * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v);
+        const size_t st = scan_state_bytes(NS, DKP, p.d_v), va = scan_value_bytes(NS, p.d_v);
+#pragma unroll
+        for (int q = 0; q < NS; ++q) {
+            load_raw(s + L::S + q * L::kState, rec + q * (st / NS) + sl * L::kState, L::kState, tid, kLocalThreads);
+            load_raw(s + L::dS + q * L::kState, rec + st + q * (st / NS) + sl * L::kState, L::kState, tid, kLocalThreads);
+            load_raw(s + L::U + q * L::kVal, rec + 2 * st + q * (va / NS) + sl * L::kVal, L::kVal, tid, kLocalThreads);
+            load_raw(s + L::E + q * L::kVal, rec + 2 * st + va + q * (va / NS) + sl * L::kVal, L::kVal, tid, kLocalThreads);
+        }
+    };
+
+    load_tile<T, RB>(base + L::K, L::kPlane, static_cast<const T *>(p.k) + ch.t0 * p.k_stride + (int64_t)kh * p.d_k,
+                     p.k_stride, ch.len, p.d_k, vec_qk, tid, kLocalThreads);
+    load_tile<T, RB>(base + L::Q, L::kPlane, static_cast<const T *>(p.q) + ch.t0 * p.q_stride + (int64_t)kh * p.d_k,
+                     p.q_stride, ch.len, p.d_k, vec_qk, tid, kLocalThreads);
+    ptx::cp_async_commit();
+    if (L::kStages == 2) load(0);
+    ptx::cp_async_commit();
+    cp_async_wait<1>();
+    __syncthreads();
+
+    // q_r.k_j and k_r.k_j of rows 16 wr .., columns 32 wc .., kept by each thread for itself
+    {
+        float kk[4][4], qk[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kk[n][i] = qk[n][i] = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < DKP; c += 16) {
+            uint32_t ak[NI][4], aq[NI][4];
+#pragma unroll
+            for (int q = 0; q < NI; ++q) {
+                frag_a<RB>(base + L::K + q * L::kPlane, wr * 16, c, ak[q]);
+                frag_a<RB>(base + L::Q + q * L::kPlane, wr * 16, c, aq[q]);
+            }
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+                if (2 * wc + n <= wr)
+#pragma unroll
+                    for (int pb = 0; pb < NI; ++pb) {
+                        uint32_t b[4];
+                        frag_b<RB>(base + L::K + pb * L::kPlane, wc * 32 + n * 16, c, b);
+#pragma unroll
+                        for (int pa = 0; pa + pb < NI; ++pa) {
+                            ptx::mma16816(kk[2 * n], ak[pa], b[0], b[1]);
+                            ptx::mma16816(kk[2 * n + 1], ak[pa], b[2], b[3]);
+                            ptx::mma16816(qk[2 * n], aq[pa], b[0], b[1]);
+                            ptx::mma16816(qk[2 * n + 1], aq[pa], b[2], b[3]);
+                        }
+                    }
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                pair[(n * 4 + i) * kLocalThreads + tid] = kk[n][i];
+                pair[(16 + n * 4 + i) * kLocalThreads + tid] = qk[n][i];
+            }
+    }
+
+    float dq[2 * NH][4], dk[2 * NH][4];  // this warp's rows, its half of the key channels
+#pragma unroll
+    for (int n = 0; n < 2 * NH; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dq[n][i] = dk[n][i] = 0.f;
+
+    for (int hh = 0; hh < group; ++hh) {
+        const int head = kh * group + hh;
+        float xq[2 * NH][4], xk[2 * NH][4], xu[2 * NH][4], ou[4][4], eu[4][4];
+#pragma unroll
+        for (int n = 0; n < 2 * NH; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xq[n][i] = xk[n][i] = xu[n][i] = 0.f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ou[n][i] = eu[n][i] = 0.f;
+        float ev[2] = {0.f, 0.f}, ss = 0.f;
+        for (int i = tid; i < kGateFloats; i += kLocalThreads)
+            gate[i] = reinterpret_cast<const float *>(ws + (slot * p.n_heads + head) * terms_bytes(NS) +
+                                                      (size_t)2 * NS * kTile * 2)[i];
+
+        for (int sl = 0; sl < n_sl; ++sl) {
+            const int step = hh * n_sl + sl;
+            if (L::kStages == 2) {
+                // the next head's first slice overwrites B and F of this one: it waits (below)
+                if (sl + 1 < n_sl) load(step + 1);
+                ptx::cp_async_commit();
+                cp_async_wait<1>();
+            } else {
+                load(step);
+                ptx::cp_async_commit();
+                cp_async_wait<0>();
+            }
+            __syncthreads();
+            const uint32_t s = base + (step % L::kStages) * L::kSlice;
+            const char *sp = smem + (step % L::kStages) * L::kSlice;
+            // <S0, dS1>
+            for (int i = tid; i < L::kState / 16; i += kLocalThreads) {
+                float x[8], z[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = z[j] = 0.f;
+#pragma unroll
+                for (int q = 0; q < NS; ++q) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(sp + L::S + q * L::kState + i * 16);
+                    const uint4 b = *reinterpret_cast<const uint4 *>(sp + L::dS + q * L::kState + i * 16);
+                    x[0] += lo_f(a.x); x[1] += hi_f(a.x); x[2] += lo_f(a.y); x[3] += hi_f(a.y);
+                    x[4] += lo_f(a.z); x[5] += hi_f(a.z); x[6] += lo_f(a.w); x[7] += hi_f(a.w);
+                    z[0] += lo_f(b.x); z[1] += hi_f(b.x); z[2] += lo_f(b.y); z[3] += hi_f(b.y);
+                    z[4] += lo_f(b.z); z[5] += hi_f(b.z); z[6] += lo_f(b.w); z[7] += hi_f(b.w);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss = fmaf(x[j], z[j], ss);
+            }
+#pragma unroll
+            for (int kx = 0; kx < 2; ++kx) {  // 16 value channels
+                uint32_t ao[NI][4], ae[NS][4], au[NS][4];
+#pragma unroll
+                for (int q = 0; q < NI; ++q) frag_a<64>(s + L::dO + q * L::kIn, wr * 16, kx * 16, ao[q]);
+#pragma unroll
+                for (int q = 0; q < NS; ++q) {
+                    frag_a_t<128>(s + L::E + q * L::kVal, kx * 16, wr * 16, ae[q]);
+                    frag_a_t<128>(s + L::U + q * L::kVal, kx * 16, wr * 16, au[q]);
+                }
+                if (wc == 0) {  // E_r.V_r
+                    uint32_t av[4];
+                    if constexpr (NI == 1) frag_a<64>(s + L::V, wr * 16, kx * 16, av);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x0 = 0.f, x1 = 0.f, z0 = 0.f, z1 = 0.f;
+#pragma unroll
+                        for (int q = 0; q < NS; ++q) { x0 += lo_f(ae[q][i]); x1 += hi_f(ae[q][i]); }
+                        if constexpr (NI == 1) {
+                            z0 = lo_f(av[i]);
+                            z1 = hi_f(av[i]);
+                        } else {
+                            const int r = wr * 16 + gr + (i & 1) * 8, v = sl * 32 + kx * 16 + (i >> 1) * 8 + tq * 2;
+                            const float *at = static_cast<const float *>(p.v) + (ch.t0 + r) * p.v_stride + (int64_t)head * p.d_v + v;
+                            if (r < ch.len && v < p.d_v) z0 = at[0];
+                            if (r < ch.len && v + 1 < p.d_v) z1 = at[1];
+                        }
+                        ev[i & 1] = fmaf(x0, z0, fmaf(x1, z1, ev[i & 1]));
+                    }
+                } else {  // dV = beta E
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+                        for (int q = 0; q < NS; ++q) { x0 += lo_f(ae[q][i]); x1 += hi_f(ae[q][i]); }
+                        const int r = wr * 16 + gr + (i & 1) * 8, v = sl * 32 + kx * 16 + (i >> 1) * 8 + tq * 2;
+                        if (r < ch.len && v < p.d_v) {
+                            const float be = gate[2 * C + r];
+                            put2(static_cast<T *>(p.dv) + ((ch.t0 + r) * p.n_heads + head) * p.d_v + v, be * x0, be * x1,
+                                 wide_v, v + 1 < p.d_v);
+                        }
+                    }
+                }
+                // dO S0^T, E S0^T, U dS1^T
+#pragma unroll
+                for (int n = 0; n < NH; ++n)
+#pragma unroll
+                    for (int pb = 0; pb < NS; ++pb) {
+                        uint32_t b[4], d[4];
+                        frag_b_t<RB>(s + L::S + pb * L::kState, kx * 16, wc * (DKP / 2) + n * 16, b);
+                        frag_b_t<RB>(s + L::dS + pb * L::kState, kx * 16, wc * (DKP / 2) + n * 16, d);
+#pragma unroll
+                        for (int pa = 0; pa + pb < NS; ++pa) {
+                            if (pa < NI) {
+                                ptx::mma16816(xq[2 * n], ao[pa], b[0], b[1]);
+                                ptx::mma16816(xq[2 * n + 1], ao[pa], b[2], b[3]);
+                            }
+                            ptx::mma16816(xk[2 * n], ae[pa], b[0], b[1]);
+                            ptx::mma16816(xk[2 * n + 1], ae[pa], b[2], b[3]);
+                            ptx::mma16816(xu[2 * n], au[pa], d[0], d[1]);
+                            ptx::mma16816(xu[2 * n + 1], au[pa], d[2], d[3]);
+                        }
+                    }
+                // dO U^T, E U^T
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    if (2 * wc + n <= wr)
+#pragma unroll
+                        for (int pb = 0; pb < NS; ++pb) {
+                            uint32_t b[4];
+                            frag_b_t<128>(s + L::U + pb * L::kVal, kx * 16, wc * 32 + n * 16, b);
+#pragma unroll
+                            for (int pa = 0; pa + pb < NS; ++pa) {
+                                if (pa < NI) {
+                                    ptx::mma16816(ou[2 * n], ao[pa], b[0], b[1]);
+                                    ptx::mma16816(ou[2 * n + 1], ao[pa], b[2], b[3]);
+                                }
+                                ptx::mma16816(eu[2 * n], ae[pa], b[0], b[1]);
+                                ptx::mma16816(eu[2 * n + 1], ae[pa], b[2], b[3]);
+                            }
+                        }
+            }
+            __syncthreads();
+        }
+
+        // row dots with q and k, and the products scaled into the head sums
+        const float *gam = gate, *del = gate + C, *bet = gate + 2 * C, *Gh = gate + 4 * C, *Gl = gate + 5 * C;
+        {
+            float qx[2] = {0.f, 0.f}, kx_[2] = {0.f, 0.f}, ku[2] = {0.f, 0.f};
+#pragma unroll
+            for (int n = 0; n < 2 * NH; ++n)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t at = tile_off<RB>(wr * 16 + gr + 8 * h, wc * (DKP / 2) + n * 8 + tq * 2);
+                    float k0 = 0.f, k1 = 0.f, q0 = 0.f, q1 = 0.f;
+#pragma unroll
+                    for (int q = 0; q < NI; ++q) {
+                        const uint32_t wk = *reinterpret_cast<const uint32_t *>(smem + L::K + q * L::kPlane + at);
+                        const uint32_t wq = *reinterpret_cast<const uint32_t *>(smem + L::Q + q * L::kPlane + at);
+                        k0 += lo_f(wk); k1 += hi_f(wk); q0 += lo_f(wq); q1 += hi_f(wq);
+                    }
+                    qx[h] = fmaf(q0, xq[n][2 * h], fmaf(q1, xq[n][2 * h + 1], qx[h]));
+                    kx_[h] = fmaf(k0, xk[n][2 * h], fmaf(k1, xk[n][2 * h + 1], kx_[h]));
+                    ku[h] = fmaf(k0, xu[n][2 * h], fmaf(k1, xu[n][2 * h + 1], ku[h]));
+                }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = wr * 16 + gr + 8 * h;
+                const float a = quad_sum(qx[h]), b = quad_sum(kx_[h]), d = quad_sum(ku[h]), e = quad_sum(ev[h]);
+                if (tq == 0) {
+                    r_qx[wc * C + r] = a;
+                    r_kx[wc * C + r] = b;
+                    r_ku[wc * C + r] = d;
+                    if (wc == 0) r_ev[r] = e;
+                }
+                const float sg = scale * gam[r], gb = -gam[r] * bet[r], de = del[r];
+#pragma unroll
+                for (int n = 0; n < 2 * NH; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        dq[n][2 * h + i] = fmaf(sg, xq[n][2 * h + i], dq[n][2 * h + i]);
+                        dk[n][2 * h + i] = fmaf(gb, xk[n][2 * h + i], fmaf(de, xu[n][2 * h + i], dk[n][2 * h + i]));
+                    }
+            }
+        }
+        // B (lower) and beta F + its transpose as operands; row and column sums
+        {
+            float fk[2] = {0.f, 0.f}, mr[2] = {0.f, 0.f};
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                float mc[2] = {0.f, 0.f};
+                const int j = wc * 32 + n * 8 + tq * 2;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = wr * 16 + gr + 8 * h;
+                    float bv[2], fv[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float kk = pair[(n * 4 + 2 * h + i) * kLocalThreads + tid];
+                        const float qk = pair[(16 + n * 4 + 2 * h + i) * kLocalThreads + tid];
+                        const float d = (Gh[r] - Gh[j + i]) + (Gl[r] - Gl[j + i]);
+                        const float e = j + i <= r ? expf(d) : 0.f;
+                        bv[i] = j + i <= r ? scale * e * ou[n][2 * h + i] : 0.f;
+                        const float f = j + i < r ? e * eu[n][2 * h + i] : 0.f;
+                        fv[i] = -bet[r] * f;
+                        fk[h] = fmaf(f, kk, fk[h]);
+                        const float m = j + i < r ? fmaf(bv[i], qk, fv[i] * kk) : 0.f;
+                        mr[h] += m;
+                        mc[i] += m;
+                    }
+                    uint32_t wb[NI], wf[NI];
+                    split2<NI>(bv[0], bv[1], wb);
+                    split2<NI>(fv[0], fv[1], wf);
+#pragma unroll
+                    for (int q = 0; q < NI; ++q) {
+                        *reinterpret_cast<uint32_t *>(smem + L::B + q * kTile * 2 + tile_off<128>(r, j)) = wb[q];
+                        char *ft = smem + L::F + q * kTile * 2;
+                        if (j < r) {  // (r, j) and, below the diagonal, (r, j + 1) with their mirror images
+                            *reinterpret_cast<uint16_t *>(ft + tile_off<128>(r, j)) = (uint16_t)wf[q];
+                            *reinterpret_cast<uint16_t *>(ft + tile_off<128>(j, r)) = (uint16_t)wf[q];
+                        }
+                        if (j + 1 < r) {
+                            *reinterpret_cast<uint16_t *>(ft + tile_off<128>(r, j + 1)) = (uint16_t)(wf[q] >> 16);
+                            *reinterpret_cast<uint16_t *>(ft + tile_off<128>(j + 1, r)) = (uint16_t)(wf[q] >> 16);
+                        }
+                        if (j == r || j + 1 == r) *reinterpret_cast<uint16_t *>(ft + tile_off<128>(r, r)) = 0;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) mc[i] += __shfl_xor_sync(0xffffffffu, mc[i], o);
+                    if (gr == 0) c_m[wr * C + j + i] = mc[i];
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float a = quad_sum(fk[h]), b = quad_sum(mr[h]);
+                if (tq == 0) {
+                    r_fk[wc * C + wr * 16 + gr + 8 * h] = a;
+                    r_m[wc * C + wr * 16 + gr + 8 * h] = b;
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (lane == 0) r_ss[warp] = ss;
+        }
+        __syncthreads();
+        if (warp == 0) {  // dbeta, dg: two tokens a lane, running sums over the chunk
+            double a[2], b[2];
+            float whole = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) whole += r_ss[i];
+            whole *= gate[3 * C];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 2 * lane + i;
+                const float kx = r_kx[r] + r_kx[C + r];
+                if (r < ch.len)
+                    p.dbeta[(ch.t0 + r) * p.n_heads + head] = r_ev[r] - gam[r] * kx - (r_fk[r] + r_fk[C + r]);
+                a[i] = (double)(gam[r] * (scale * (r_qx[r] + r_qx[C + r]) - bet[r] * kx)) + (double)(r_m[r] + r_m[C + r]) -
+                       (double)((c_m[r] + c_m[C + r]) + (c_m[2 * C + r] + c_m[3 * C + r]));
+                b[i] = del[r] * (r_ku[r] + r_ku[C + r]);
+            }
+            // inclusive sums over the tokens of a and b
+            double ra = a[0] + a[1], rb = b[0] + b[1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double x = __shfl_up_sync(0xffffffffu, ra, o), y = __shfl_up_sync(0xffffffffu, rb, o);
+                if (lane >= o) { ra += x; rb += y; }
+            }
+            const double total = __shfl_sync(0xffffffffu, ra, 31);
+            const double a0 = ra - (a[0] + a[1]), b0 = rb - (b[0] + b[1]);  // before token 2 lane
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 2 * lane + i;
+                const double sa = total - (i ? a0 + a[0] : a0), sb = i ? b0 + b[0] : b0;
+                if (r < ch.len) p.dg[(ch.t0 + r) * p.n_heads + head] = (float)((double)whole + sa + sb);
+            }
+        }
+        // dQ += B K, dK += B^T Q - (beta F + its transpose) K
+#pragma unroll
+        for (int kx = 0; kx < 4; ++kx) {
+            uint32_t ab[NI][4], at[NI][4], af[NI][4];
+#pragma unroll
+            for (int q = 0; q < NI; ++q) {
+                frag_a<128>(base + L::B + q * kTile * 2, wr * 16, kx * 16, ab[q]);
+                frag_a_t<128>(base + L::B + q * kTile * 2, kx * 16, wr * 16, at[q]);
+                frag_a<128>(base + L::F + q * kTile * 2, wr * 16, kx * 16, af[q]);
+            }
+#pragma unroll
+            for (int n = 0; n < NH; ++n)
+#pragma unroll
+                for (int pb = 0; pb < NI; ++pb) {
+                    uint32_t b[4], d[4];
+                    frag_b_t<RB>(base + L::K + pb * L::kPlane, kx * 16, wc * (DKP / 2) + n * 16, b);
+                    frag_b_t<RB>(base + L::Q + pb * L::kPlane, kx * 16, wc * (DKP / 2) + n * 16, d);
+#pragma unroll
+                    for (int pa = 0; pa + pb < NI; ++pa) {
+                        ptx::mma16816(dq[2 * n], ab[pa], b[0], b[1]);
+                        ptx::mma16816(dq[2 * n + 1], ab[pa], b[2], b[3]);
+                        ptx::mma16816(dk[2 * n], at[pa], d[0], d[1]);
+                        ptx::mma16816(dk[2 * n + 1], at[pa], d[2], d[3]);
+                        ptx::mma16816(dk[2 * n], af[pa], b[0], b[1]);
+                        ptx::mma16816(dk[2 * n + 1], af[pa], b[2], b[3]);
+                    }
+                }
+        }
+        __syncthreads();  // B, F, the gates and the sums are done with
+        if (L::kStages == 2 && hh + 1 < group) load((hh + 1) * n_sl);
+        ptx::cp_async_commit();
+    }
+    // write the key head's gradients
+#pragma unroll
+    for (int n = 0; n < 2 * NH; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = wr * 16 + gr + 8 * h, c = wc * (DKP / 2) + n * 8 + tq * 2;
+            if (r < ch.len && c < p.d_k) {
+                const size_t at = ((ch.t0 + r) * p.n_k_heads + kh) * p.d_k + c;
+                put2(static_cast<T *>(p.dq) + at, dq[n][2 * h], dq[n][2 * h + 1], wide_k, c + 1 < p.d_k);
+                put2(static_cast<T *>(p.dk) + at, dk[n][2 * h], dk[n][2 * h + 1], wide_k, c + 1 < p.d_k);
+            }
+        }
+}
+
+template <typename T, int DKP>
+cudaError_t backward(const GdrArgs &p, cudaStream_t stream) {
+    constexpr int NI = InputPlanes<T>::N, W = 2;
+    const float scale = 1.f / std::sqrt((float)p.d_k);
+    const bool vec_qk = rows_vec<T>(p.q, p.q_stride, p.d_k) && rows_vec<T>(p.k, p.k_stride, p.d_k);
+    const bool vec_v = rows_vec<T>(p.v, p.v_stride, p.d_v);
+    const bool vec_do = rows_vec<T>(p.dout, (int64_t)p.n_heads * p.d_v, p.d_v);
+    constexpr int fwd = ChainSmem<NI, DKP, W, true>::kBytes, rev = ReverseSmem<NI, DKP, W>::kBytes;
+    constexpr int scan = fwd > rev ? fwd : rev;
+    cudaError_t e = cudaFuncSetAttribute(gdr_scan_kernel<T, DKP, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, scan);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = 2u * ((p.d_v + 16 * W - 1) / (16 * W)) * p.n_heads * p.n_seq;
+    gdr_scan_kernel<T, DKP, W><<<grid, 32 * W, scan, stream>>>(p, scale, vec_qk, vec_v, vec_do);
+    count_launches(1);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.n_tok == 0) return e;
+    constexpr int local = LocalSmem<NI, DKP>::kBytes;
+    e = cudaFuncSetAttribute(gdr_local_kernel<T, DKP>, cudaFuncAttributeMaxDynamicSharedMemorySize, local);
+    if (e != cudaSuccess) return e;
+    auto wide = [](const void *x, int d) { return d % 2 == 0 && ((uintptr_t)x % (2 * sizeof(T))) == 0; };
+    gdr_local_kernel<T, DKP><<<dim3((unsigned)n_slots(p.n_tok, p.n_seq), p.n_k_heads), kLocalThreads, local, stream>>>(
+        p, scale, vec_qk, vec_v, vec_do, wide(p.dq, p.d_k) && wide(p.dk, p.d_k), wide(p.dv, p.d_v));
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace gdr
+
+size_t gdr_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k, int32_t d_v, bool bf16) {
+    const int ns = bf16 ? 2 : 3;
+    return gdr::scan_offset(n_tok, n_seq, n_heads, ns) +
+           (size_t)gdr::n_slots(n_tok, n_seq) * n_heads * gdr::scan_bytes(ns, d_k <= 64 ? 64 : 128, d_v);
+}
+
+cudaError_t launch_gdr_bwd(const GdrArgs &p, cudaStream_t stream) {
+    const cudaError_t e = launch_gdr_terms(p, stream);
+    if (e != cudaSuccess) return e;
+    if (p.bf16) return p.d_k <= 64 ? gdr::backward<__nv_bfloat16, 64>(p, stream) : gdr::backward<__nv_bfloat16, 128>(p, stream);
+    return p.d_k <= 64 ? gdr::backward<float, 64>(p, stream) : gdr::backward<float, 128>(p, stream);
+}
+
+}  // namespace kda

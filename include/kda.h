@@ -537,6 +537,26 @@ kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, int64_
                              kda_dtype dtype, void *stream);
 
 /*
+ * kda_gdr_chunk_bwd -- gradients of <dout, out> + <dh_final, h_final> of kda_gdr_chunk_fwd
+ * with respect to q, k, v, g, beta and h0. dout [n_tok, n_heads, d_v] dtype, dh_final like
+ * h_final or NULL (zero). dq, dk [n_tok, n_k_heads, d_k] (summed over the value heads that
+ * share a key head) and dv [n_tok, n_heads, d_v] in dtype, dg, dbeta [n_tok, n_heads]
+ * float32, dh0 like h0 or NULL, all contiguous and fully overwritten. Where g is -inf (or
+ * below -200) dg is 0. workspace as above, kda_gdr_chunk_bwd_workspace_bytes() bytes: it
+ * receives the state and the state gradient of every chunk. Errors as kda_gdr_chunk_fwd.
+ */
+size_t kda_gdr_chunk_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads,
+                                         int32_t d_k, int32_t d_v, kda_dtype dtype);
+kda_status kda_gdr_chunk_bwd(const void *q, const void *k, const void *v, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const float *g,
+                             const float *beta, const float *h0, const int32_t *cu_seqlens,
+                             const void *dout, const float *dh_final, void *dq, void *dk,
+                             void *dv, float *dg, float *dbeta, float *dh0, void *workspace,
+                             size_t workspace_bytes, int64_t n_tok, int32_t n_seq,
+                             int32_t n_k_heads, int32_t n_heads, int32_t d_k, int32_t d_v,
+                             kda_dtype dtype, void *stream);
+
+/*
  * kda_gdr_step -- one token for each of n_rows sequences, in place on a pool of states:
  * row b reads and rewrites state[slots[b]] ([n_slots, n_heads, d_k, d_v] fp32); slots NULL
  * means row b owns state b (n_rows <= n_slots). A slot outside [0, n_slots) marks a padded
