@@ -149,9 +149,9 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
         lib.kda_gate_projection_out.restype = ctypes.c_int
         SZ, F, E = ctypes.c_size_t, ctypes.c_float, ctypes.c_int
         for name, res, args in (
-                ("kda_gdr_chunk_fwd_workspace_bytes", SZ, [I64, I32, I32, E]),
+                ("kda_gdr_chunk_fwd_workspace_bytes", SZ, [I64] + [I32] * 5 + [E]),
                 ("kda_gdr_chunk_fwd", E, [P] * 3 + [I64] * 3 + [P] * 7 + [SZ, I64] + [I32] * 5 + [E, P]),
-                ("kda_gdr_chunk_bwd_workspace_bytes", SZ, [I64] + [I32] * 4 + [E]),
+                ("kda_gdr_chunk_bwd_workspace_bytes", SZ, [I64] + [I32] * 5 + [E]),
                 ("kda_gdr_chunk_bwd", E, [P] * 3 + [I64] * 3 + [P] * 13 + [SZ, I64] + [I32] * 5 + [E, P]),
                 ("kda_gdr_step", E, [P] * 3 + [I64] * 3 + [P] * 5 + [I32] * 6 + [E, P]),
                 ("kda_residual_norm_fwd", E, [P, I64, P, I64] + [P] * 4 + [I64, I32, F, E, P]),

@@ -105,7 +105,7 @@ def gdr_chunk_fwd(q, k, v, g, beta, h0=None, cu_seqlens=None, *, out=None, h_fin
         h_final = torch.empty((n_seq, h, dk, dv), dtype=torch.float32, device=q.device)
     code = _CODE[q.dtype]
     if workspace is None:
-        need = lib.kda_gdr_chunk_fwd_workspace_bytes(n, n_seq, h, code)
+        need = lib.kda_gdr_chunk_fwd_workspace_bytes(n, n_seq, hk, h, dk, dv, code)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _done(lib, lib.kda_gdr_chunk_fwd(
         _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(h0), _p(cu_seqlens), _p(out),
@@ -134,7 +134,7 @@ def gdr_chunk_bwd(q, k, v, g, beta, h0, cu_seqlens, dout, dh_final=None, *, want
              if want_dh0 else None)
     code = _CODE[q.dtype]
     if workspace is None:
-        need = lib.kda_gdr_chunk_bwd_workspace_bytes(n, n_seq, h, dk, dv, code)
+        need = lib.kda_gdr_chunk_bwd_workspace_bytes(n, n_seq, hk, h, dk, dv, code)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _done(lib, lib.kda_gdr_chunk_bwd(
         _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(h0), _p(cu_seqlens), _p(dout),

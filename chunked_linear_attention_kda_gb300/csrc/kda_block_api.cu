@@ -99,9 +99,14 @@ kda::GdrArgs gdr_args(const void *q, const void *k, const void *v, int64_t q_str
 
 extern "C" {
 
-size_t kda_gdr_chunk_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, kda_dtype dtype) {
-    if (n_tok < 0 || n_seq < 0 || n_heads <= 0) return 0;
-    return kda::gdr_fwd_workspace_bytes(n_tok, n_seq, n_heads, dtype == KDA_BF16);
+static bool gdr_sizes(int64_t n_tok, int32_t n_seq, int32_t n_k_heads, int32_t n_heads, int32_t d_k, int32_t d_v) {
+    return n_tok >= 0 && n_seq >= 0 && n_k_heads > 0 && n_heads > 0 && d_k > 0 && d_v > 0 && d_k <= 128 && d_v <= 128;
+}
+
+size_t kda_gdr_chunk_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_k_heads, int32_t n_heads,
+                                         int32_t d_k, int32_t d_v, kda_dtype dtype) {
+    if (!gdr_sizes(n_tok, n_seq, n_k_heads, n_heads, d_k, d_v)) return 0;
+    return kda::gdr_fwd_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v, dtype == KDA_BF16);
 }
 
 kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
@@ -117,7 +122,7 @@ kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, int64_
     if (s != KDA_OK) return s;
     if (n_tok > 0 && !out) return api_fail(KDA_ERR_INVALID_ARG, "out is required");
     if (n_seq == 0) return api_ok();
-    const size_t need = n_tok ? kda::gdr_fwd_workspace_bytes(n_tok, n_seq, n_heads, p.bf16) : 0;
+    const size_t need = n_tok ? kda::gdr_fwd_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v, p.bf16) : 0;
     s = check_workspace(workspace, workspace_bytes, need);
     if (s != KDA_OK) return s;
     const size_t es = p.bf16 ? 2 : 4, st = (size_t)n_seq * n_heads * d_k * d_v * 4;
@@ -130,10 +135,10 @@ kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, int64_
     return launched(kda::launch_gdr_fwd(p, (cudaStream_t)stream), "gated delta rule forward launch");
 }
 
-size_t kda_gdr_chunk_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k,
-                                         int32_t d_v, kda_dtype dtype) {
-    if (n_tok < 0 || n_seq < 0 || n_heads <= 0 || d_k <= 0 || d_v <= 0 || d_k > 128 || d_v > 128) return 0;
-    return kda::gdr_bwd_workspace_bytes(n_tok, n_seq, n_heads, d_k, d_v, dtype == KDA_BF16);
+size_t kda_gdr_chunk_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_k_heads, int32_t n_heads,
+                                         int32_t d_k, int32_t d_v, kda_dtype dtype) {
+    if (!gdr_sizes(n_tok, n_seq, n_k_heads, n_heads, d_k, d_v)) return 0;
+    return kda::gdr_bwd_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v, dtype == KDA_BF16);
 }
 
 kda_status kda_gdr_chunk_bwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
@@ -151,7 +156,7 @@ kda_status kda_gdr_chunk_bwd(const void *q, const void *k, const void *v, int64_
     if (n_tok > 0 && (!dout || !dq || !dk || !dv || !dg || !dbeta))
         return api_fail(KDA_ERR_INVALID_ARG, "dout, dq, dk, dv, dg and dbeta are required");
     if (n_seq == 0) return api_ok();
-    const size_t need = n_tok ? kda::gdr_bwd_workspace_bytes(n_tok, n_seq, n_heads, d_k, d_v, p.bf16) : 0;
+    const size_t need = n_tok ? kda::gdr_bwd_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v, p.bf16) : 0;
     s = check_workspace(workspace, workspace_bytes, need);
     if (s != KDA_OK) return s;
     const size_t es = p.bf16 ? 2 : 4, st = (size_t)n_seq * n_heads * d_k * d_v * 4;

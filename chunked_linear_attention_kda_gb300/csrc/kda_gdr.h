@@ -74,6 +74,21 @@ __host__ __device__ __forceinline__ size_t scan_offset(int64_t n_tok, int64_t n_
     return (size_t)n_slots(n_tok, n_seq) * n_heads * terms_bytes(ns);
 }
 
+// Tile images of q, k (per key head), v and, for the backward pass, dout (per value head) of
+// the chunks that a tensor copy cannot fetch: a sequence's last, partial chunk (rows past its
+// end must read as zero, not as the next sequence), and every chunk of inputs that are fp32
+// or not 16-byte aligned. Indexed by sequence when only partial chunks need one, else by slot.
+struct Images {
+    bool all;           // every chunk has an image
+    size_t offset;      // of the first, in the workspace
+    __host__ __device__ static size_t key_bytes(int ni, int dkp) { return (size_t)ni * C * dkp * 2; }
+    __host__ __device__ static size_t value_bytes(int ni, int d_v) { return (size_t)ni * pad_v(d_v) * C * 2; }
+    // one index: q and k of every key head, then v (and dout) of every value head
+    __host__ __device__ static size_t record(int ni, int dkp, int d_v, int hk, int hv, int values) {
+        return 2 * hk * key_bytes(ni, dkp) + (size_t)values * hv * value_bytes(ni, d_v);
+    }
+};
+
 // ---------------------------------------------------------------- tiles
 // A tile of bf16 rows of RB bytes, 16-byte groups XOR-swizzled so that ldmatrix reads eight
 // rows of one column group without bank conflicts.
@@ -111,6 +126,20 @@ template <int RB>
 __device__ __forceinline__ void frag_b_t(uint32_t base, int k0, int n0, uint32_t *b) {
     const int l = threadIdx.x & 31;
     ptx::ldsm_x4_t(base + tile_off<RB>(k0 + (l & 15), n0 + (l >> 4) * 8), b[0], b[1], b[2], b[3]);
+}
+
+// A tile of 64 tokens x DKP key channels: column halves of 64, each 64 rows of 128 bytes in
+// the tensor copy's 128-byte swizzle
+constexpr int kHalf = C * 128;
+__device__ __forceinline__ int key_off(int row, int col) { return (col >> 6) * kHalf + tile_off<128>(row, col & 63); }
+__device__ __forceinline__ void key_a(uint32_t base, int m0, int k0, uint32_t *a) {
+    frag_a<128>(base + (k0 >> 6) * kHalf, m0, k0 & 63, a);
+}
+__device__ __forceinline__ void key_b(uint32_t base, int n0, int k0, uint32_t *b) {
+    frag_b<128>(base + (k0 >> 6) * kHalf, n0, k0 & 63, b);
+}
+__device__ __forceinline__ void key_b_t(uint32_t base, int k0, int n0, uint32_t *b) {
+    frag_b_t<128>(base + (n0 >> 6) * kHalf, k0, n0 & 63, b);
 }
 
 // two fp32 values as NP packed planes whose sum is the value
@@ -231,6 +260,43 @@ __device__ __forceinline__ void load_tile(uint32_t dst, uint32_t plane, const T 
         }
     }
 }
+// the key tile of a chunk (planes C * DKP * 2 bytes apart)
+template <typename T, int DKP>
+__device__ __forceinline__ void load_key_tile(uint32_t dst, const T *src, int64_t stride, int rows, int cols,
+                                              bool vec, int tid, int nthreads) {
+#pragma unroll
+    for (int h = 0; h < DKP / 64; ++h)
+        load_tile<T, 128>(dst + h * kHalf, C * DKP * 2, src + h * 64, stride, rows, cols - h * 64, vec, tid, nthreads);
+}
+// The image of a chunk's value tile: slices of 32 channels, each NI planes of 64 rows of 64
+// bytes in the tensor copy's 64-byte swizzle.
+template <typename T>
+__device__ __forceinline__ void write_value_image(char *dst, const T *src, int64_t stride, int rows, int cols,
+                                                  int tid, int nthreads) {
+    constexpr int NI = InputPlanes<T>::N, plane = C * 64;
+    const int slices = pad_v(cols) / 32;
+    for (int i = tid; i < slices * C * 4; i += nthreads) {
+        const int sl = i / (C * 4), r = (i >> 2) % C, c = (i & 3) * 8;
+        uint32_t w[NI][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float x[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int col = sl * 32 + c + 2 * j + y;
+                x[y] = r < rows && col < cols ? (float)src[r * stride + col] : 0.f;
+            }
+            uint32_t s[NI];
+            split2<NI>(x[0], x[1], s);
+#pragma unroll
+            for (int q = 0; q < NI; ++q) w[q][j] = s[q];
+        }
+#pragma unroll
+        for (int q = 0; q < NI; ++q)
+            *reinterpret_cast<uint4 *>(dst + (sl * NI + q) * plane + tile_off<64>(r, c)) =
+                make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+    }
+}
 // `bytes` (a multiple of 16) from the workspace, as they lie
 __device__ __forceinline__ void load_raw(uint32_t dst, const void *src, int bytes, int tid, int nthreads) {
     const char *p = static_cast<const char *>(src);
@@ -257,7 +323,8 @@ bool rows_vec(const void *p, int64_t stride, int d) {
 
 }  // namespace gdr
 
-// Chunk terms (X, P, gates of every chunk and value head) into the workspace.
-cudaError_t launch_gdr_terms(const GdrArgs &args, cudaStream_t stream);
+// Chunk terms (X, P, gates of every chunk and value head) and the tile images into the
+// workspace; `values` = 2 when dout has images too.
+cudaError_t launch_gdr_terms(const GdrArgs &args, gdr::Images images, int values, cudaStream_t stream);
 
 }  // namespace kda

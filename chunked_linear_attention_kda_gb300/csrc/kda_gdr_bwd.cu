@@ -28,228 +28,14 @@ namespace kda {
 namespace gdr {
 namespace {
 
-// ---------------------------------------------------------------- reverse chain
-template <int NI, int DKP, int W>
-struct ReverseSmem {
-    static constexpr int NS = NI == 1 ? 2 : 3;
-    static constexpr int kStages = NI == 1 ? 2 : 1;
-    static constexpr int kPlane = C * DKP * 2, kVPlane = C * 16 * W * 2;
-    static constexpr int K = 0, Q = K + NI * kPlane, X = Q + NI * kPlane, P = X + NS * kTile * 2;
-    static constexpr int Gate = P + NS * kTile * 2, dO = Gate + kChainGates * 4;
-    static constexpr int kStage = dO + NI * kVPlane;
-    static constexpr int kBytes = kStages * kStage;
-};
-
-template <typename T, int DKP, int W>
-__device__ __forceinline__ void reverse_chain(const GdrArgs &p, int block, float scale, bool vec_qk, bool vec_do) {
-    constexpr int NI = InputPlanes<T>::N;
-    using L = ReverseSmem<NI, DKP, W>;
-    constexpr int NS = L::NS, RB = DKP * 2, VB = 32 * W, NT = DKP / 8;
-    extern __shared__ __align__(128) char smem[];
-    const uint32_t base = ptx::smem_u32(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
-    const int n_blk = (p.d_v + 16 * W - 1) / (16 * W);
-    const int blk = block % n_blk, sh = block / n_blk;
-    const int head = sh % p.n_heads, seq = sh / p.n_heads, kh = head / (p.n_heads / p.n_k_heads);
-    const int64_t tok0 = p.cu_seqlens[seq];
-    const int len = (int)(p.cu_seqlens[seq + 1] - tok0);
-    const int n_chunks = (len + C - 1) / C;
-    const int64_t slot0 = slot_base(p.cu_seqlens, seq);
-    const int dv0 = blk * 16 * W, v0 = dv0 + warp * 16;
-    const char *ws = static_cast<const char *>(p.workspace);
-    const char *terms = ws + (slot0 * p.n_heads + head) * terms_bytes(NS);
-    const size_t terms_step = (size_t)p.n_heads * terms_bytes(NS);
-
-    float S[NT][4];  // dS^T, laid out as the forward chain's S^T
-    const size_t st_at = ((size_t)seq * p.n_heads + head) * p.d_k * p.d_v;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = n * 8 + tq * 2 + (i & 1), v = v0 + gr + (i >> 1) * 8;
-            S[n][i] = p.dh_final && c < p.d_k && v < p.d_v ? p.dh_final[st_at + (size_t)c * p.d_v + v] : 0.f;
-        }
-
-    auto load = [&](int c) {
-        const uint32_t s = base + (c % L::kStages) * L::kStage;
-        const int64_t t = tok0 + (int64_t)c * C;
-        const int rows = min(C, len - c * C);
-        load_tile<T, RB>(s + L::K, L::kPlane, static_cast<const T *>(p.k) + t * p.k_stride + (int64_t)kh * p.d_k,
-                         p.k_stride, rows, p.d_k, vec_qk, tid, 32 * W);
-        load_tile<T, RB>(s + L::Q, L::kPlane, static_cast<const T *>(p.q) + t * p.q_stride + (int64_t)kh * p.d_k,
-                         p.q_stride, rows, p.d_k, vec_qk, tid, 32 * W);
-        load_tile<T, VB>(s + L::dO, L::kVPlane,
-                         static_cast<const T *>(p.dout) + (t * p.n_heads + head) * p.d_v + dv0,
-                         (int64_t)p.n_heads * p.d_v, rows, p.d_v - dv0, vec_do, tid, 32 * W);
-        const char *src = terms + c * terms_step;
-        load_raw(s + L::X, src, 2 * NS * kTile * 2, tid, 32 * W);  // X and P
-        load_raw(s + L::Gate, src + 2 * NS * kTile * 2, kChainGates * 4, tid, 32 * W);
-    };
-
-    if (L::kStages == 2 && n_chunks > 0) load(n_chunks - 1);
-    ptx::cp_async_commit();
-    for (int c = n_chunks - 1; c >= 0; --c) {
-        if (L::kStages == 2) {
-            if (c > 0) load(c - 1);
-            ptx::cp_async_commit();
-            cp_async_wait<1>();
-        } else {
-            load(c);
-            ptx::cp_async_commit();
-            cp_async_wait<0>();
-        }
-        __syncthreads();
-        const uint32_t s = base + (c % L::kStages) * L::kStage;
-        const float *gate = reinterpret_cast<const float *>(smem + (c % L::kStages) * L::kStage + L::Gate);
-        char *rec = static_cast<char *>(p.workspace) + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
-                    ((slot0 + c) * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v);
-        const bool keep = v0 < pad_v(p.d_v);
-        if (keep)
-            store_planes<NS, NT, RB>(rec + scan_state_bytes(NS, DKP, p.d_v), (size_t)pad_v(p.d_v) * RB, v0, S);
-
-        // dU^T = delta (dS1^T K^T) + dO^T P
-        float y[8][4];
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[n][i] = 0.f;
-#pragma unroll
-        for (int kx = 0; kx < DKP / 16; ++kx) {
-            uint32_t a[NS][4];
-            acc_to_a<NS>(&S[2 * kx], a);
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int pb = 0; pb < NI; ++pb) {
-                    uint32_t b[4];
-                    frag_b<RB>(s + L::K + pb * L::kPlane, n * 16, kx * 16, b);
-#pragma unroll
-                    for (int pa = 0; pa + pb < NS; ++pa) {
-                        ptx::mma16816(y[2 * n], a[pa], b[0], b[1]);
-                        ptx::mma16816(y[2 * n + 1], a[pa], b[2], b[3]);
-                    }
-                }
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const float2 de = *reinterpret_cast<const float2 *>(gate + C + n * 8 + tq * 2);
-            y[n][0] *= de.x; y[n][1] *= de.y; y[n][2] *= de.x; y[n][3] *= de.y;
-        }
-#pragma unroll
-        for (int kx = 0; kx < 4; ++kx) {
-            uint32_t a[NI][4];
-#pragma unroll
-            for (int pa = 0; pa < NI; ++pa) frag_a_t<VB>(s + L::dO + pa * L::kVPlane, kx * 16, warp * 16, a[pa]);
-#pragma unroll
-            for (int n = 0; n <= kx; ++n)
-#pragma unroll
-                for (int pb = 0; pb < NS; ++pb) {
-                    uint32_t b[4];
-                    frag_b_t<128>(s + L::P + pb * kTile * 2, kx * 16, n * 16, b);
-#pragma unroll
-                    for (int pa = 0; pa < NI && pa + pb < NS; ++pa) {
-                        ptx::mma16816(y[2 * n], a[pa], b[0], b[1]);
-                        ptx::mma16816(y[2 * n + 1], a[pa], b[2], b[3]);
-                    }
-                }
-        }
-        // E^T = dU^T X
-        float e[8][4];
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e[n][i] = 0.f;
-#pragma unroll
-        for (int kx = 0; kx < 4; ++kx) {
-            uint32_t a[NS][4];
-            acc_to_a<NS>(&y[2 * kx], a);
-#pragma unroll
-            for (int n = 0; n <= kx; ++n)
-#pragma unroll
-                for (int pb = 0; pb < NS; ++pb) {
-                    uint32_t b[4];
-                    frag_b_t<128>(s + L::X + pb * kTile * 2, kx * 16, n * 16, b);
-#pragma unroll
-                    for (int pa = 0; pa + pb < NS; ++pa) {
-                        ptx::mma16816(e[2 * n], a[pa], b[0], b[1]);
-                        ptx::mma16816(e[2 * n + 1], a[pa], b[2], b[3]);
-                    }
-                }
-        }
-        if (keep)
-            store_planes<NS, 8, 128>(rec + 2 * scan_state_bytes(NS, DKP, p.d_v) + scan_value_bytes(NS, p.d_v),
-                                     (size_t)pad_v(p.d_v) * 128, v0, e);
-        // dS0^T = Gamma dS1^T - (gamma beta E)^T K + (s gamma dO)^T Q
-        const float whole = gate[3 * C];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) S[n][i] *= whole;
-#pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const float2 ga = *reinterpret_cast<const float2 *>(gate + n * 8 + tq * 2);
-            const float2 be = *reinterpret_cast<const float2 *>(gate + 2 * C + n * 8 + tq * 2);
-            const float x0 = -ga.x * be.x, x1 = -ga.y * be.y;
-            e[n][0] *= x0; e[n][1] *= x1; e[n][2] *= x0; e[n][3] *= x1;
-        }
-#pragma unroll
-        for (int kx = 0; kx < 4; ++kx) {
-            uint32_t a[NS][4], d[NS][4];
-            acc_to_a<NS>(&e[2 * kx], a);
-            {
-                uint32_t w[NI][4];
-#pragma unroll
-                for (int pa = 0; pa < NI; ++pa) frag_a_t<VB>(s + L::dO + pa * L::kVPlane, kx * 16, warp * 16, w[pa]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 ga = *reinterpret_cast<const float2 *>(gate + kx * 16 + (i >> 1) * 8 + tq * 2);
-                    float x = 0.f, z = 0.f;
-#pragma unroll
-                    for (int pa = 0; pa < NI; ++pa) {
-                        x += lo_f(w[pa][i]);
-                        z += hi_f(w[pa][i]);
-                    }
-                    uint32_t sp[NS];
-                    split2<NS>(x * (scale * ga.x), z * (scale * ga.y), sp);
-#pragma unroll
-                    for (int q = 0; q < NS; ++q) d[q][i] = sp[q];
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < DKP / 16; ++n)
-#pragma unroll
-                for (int pb = 0; pb < NI; ++pb) {
-                    uint32_t b[4], f[4];
-                    frag_b_t<RB>(s + L::K + pb * L::kPlane, kx * 16, n * 16, b);
-                    frag_b_t<RB>(s + L::Q + pb * L::kPlane, kx * 16, n * 16, f);
-#pragma unroll
-                    for (int pa = 0; pa + pb < NS; ++pa) {
-                        ptx::mma16816(S[2 * n], a[pa], b[0], b[1]);
-                        ptx::mma16816(S[2 * n + 1], a[pa], b[2], b[3]);
-                        ptx::mma16816(S[2 * n], d[pa], f[0], f[1]);
-                        ptx::mma16816(S[2 * n + 1], d[pa], f[2], f[3]);
-                    }
-                }
-        }
-        __syncthreads();
-    }
-    if (p.dh0) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = n * 8 + tq * 2 + (i & 1), v = v0 + gr + (i >> 1) * 8;
-                if (c < p.d_k && v < p.d_v) p.dh0[st_at + (size_t)c * p.d_v + v] = S[n][i];
-            }
-    }
-}
-
 // even blocks run the reverse chain (the longer one) of a channel block, odd ones the forward
-template <typename T, int DKP, int W>
-__global__ void __launch_bounds__(32 * W)
-    gdr_scan_kernel(const GdrArgs p, float scale, bool vec_qk, bool vec_v, bool vec_do) {
-    if (blockIdx.x & 1) chain<T, DKP, W, true>(p, blockIdx.x >> 1, scale, vec_qk, vec_v, false);
-    else reverse_chain<T, DKP, W>(p, blockIdx.x >> 1, scale, vec_qk, vec_do);
+template <typename T, int DKP>
+__global__ void __launch_bounds__(kChainThreads)
+    gdr_scan_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                    const GdrArgs p, const Images im, float scale) {
+    if (blockIdx.x & 1) chain<T, DKP, Mode::kStates>(tm_q, tm_k, tm_v, p, im, 2, blockIdx.x >> 1, scale, false);
+    else chain<T, DKP, Mode::kReverse>(tm_q, tm_k, tm_do, p, im, 2, blockIdx.x >> 1, scale, false);
 }
 
 // ---------------------------------------------------------------- local gradients
@@ -321,10 +107,10 @@ __global__ void __launch_bounds__(kLocalThreads)
         }
     };
 
-    load_tile<T, RB>(base + L::K, L::kPlane, static_cast<const T *>(p.k) + ch.t0 * p.k_stride + (int64_t)kh * p.d_k,
-                     p.k_stride, ch.len, p.d_k, vec_qk, tid, kLocalThreads);
-    load_tile<T, RB>(base + L::Q, L::kPlane, static_cast<const T *>(p.q) + ch.t0 * p.q_stride + (int64_t)kh * p.d_k,
-                     p.q_stride, ch.len, p.d_k, vec_qk, tid, kLocalThreads);
+    load_key_tile<T, DKP>(base + L::K, static_cast<const T *>(p.k) + ch.t0 * p.k_stride + (int64_t)kh * p.d_k,
+                          p.k_stride, ch.len, p.d_k, vec_qk, tid, kLocalThreads);
+    load_key_tile<T, DKP>(base + L::Q, static_cast<const T *>(p.q) + ch.t0 * p.q_stride + (int64_t)kh * p.d_k,
+                          p.q_stride, ch.len, p.d_k, vec_qk, tid, kLocalThreads);
     ptx::cp_async_commit();
     if (L::kStages == 2) load(0);
     ptx::cp_async_commit();
@@ -343,8 +129,8 @@ __global__ void __launch_bounds__(kLocalThreads)
             uint32_t ak[NI][4], aq[NI][4];
 #pragma unroll
             for (int q = 0; q < NI; ++q) {
-                frag_a<RB>(base + L::K + q * L::kPlane, wr * 16, c, ak[q]);
-                frag_a<RB>(base + L::Q + q * L::kPlane, wr * 16, c, aq[q]);
+                key_a(base + L::K + q * L::kPlane, wr * 16, c, ak[q]);
+                key_a(base + L::Q + q * L::kPlane, wr * 16, c, aq[q]);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n)
@@ -352,7 +138,7 @@ __global__ void __launch_bounds__(kLocalThreads)
 #pragma unroll
                     for (int pb = 0; pb < NI; ++pb) {
                         uint32_t b[4];
-                        frag_b<RB>(base + L::K + pb * L::kPlane, wc * 32 + n * 16, c, b);
+                        key_b(base + L::K + pb * L::kPlane, wc * 32 + n * 16, c, b);
 #pragma unroll
                         for (int pa = 0; pa + pb < NI; ++pa) {
                             ptx::mma16816(kk[2 * n], ak[pa], b[0], b[1]);
@@ -518,7 +304,7 @@ __global__ void __launch_bounds__(kLocalThreads)
             for (int n = 0; n < 2 * NH; ++n)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t at = tile_off<RB>(wr * 16 + gr + 8 * h, wc * (DKP / 2) + n * 8 + tq * 2);
+                    const uint32_t at = key_off(wr * 16 + gr + 8 * h, wc * (DKP / 2) + n * 8 + tq * 2);
                     float k0 = 0.f, k1 = 0.f, q0 = 0.f, q1 = 0.f;
 #pragma unroll
                     for (int q = 0; q < NI; ++q) {
@@ -660,8 +446,8 @@ __global__ void __launch_bounds__(kLocalThreads)
 #pragma unroll
                 for (int pb = 0; pb < NI; ++pb) {
                     uint32_t b[4], d[4];
-                    frag_b_t<RB>(base + L::K + pb * L::kPlane, kx * 16, wc * (DKP / 2) + n * 16, b);
-                    frag_b_t<RB>(base + L::Q + pb * L::kPlane, kx * 16, wc * (DKP / 2) + n * 16, d);
+                    key_b_t(base + L::K + pb * L::kPlane, kx * 16, wc * (DKP / 2) + n * 16, b);
+                    key_b_t(base + L::Q + pb * L::kPlane, kx * 16, wc * (DKP / 2) + n * 16, d);
 #pragma unroll
                     for (int pa = 0; pa + pb < NI; ++pa) {
                         ptx::mma16816(dq[2 * n], ab[pa], b[0], b[1]);
@@ -693,17 +479,21 @@ __global__ void __launch_bounds__(kLocalThreads)
 
 template <typename T, int DKP>
 cudaError_t backward(const GdrArgs &p, cudaStream_t stream) {
-    constexpr int NI = InputPlanes<T>::N, W = 2;
+    constexpr int NI = InputPlanes<T>::N;
+    ChainMaps maps;
+    const Images im{!maps.make<T>(p, true), scan_offset(p.n_tok, p.n_seq, p.n_heads, NI == 1 ? 2 : 3) +
+                                                (size_t)n_slots(p.n_tok, p.n_seq) * p.n_heads * scan_bytes(NI == 1 ? 2 : 3, DKP, p.d_v)};
+    cudaError_t e = launch_gdr_terms(p, im, 2, stream);
+    if (e != cudaSuccess) return e;
     const float scale = 1.f / std::sqrt((float)p.d_k);
     const bool vec_qk = rows_vec<T>(p.q, p.q_stride, p.d_k) && rows_vec<T>(p.k, p.k_stride, p.d_k);
     const bool vec_v = rows_vec<T>(p.v, p.v_stride, p.d_v);
     const bool vec_do = rows_vec<T>(p.dout, (int64_t)p.n_heads * p.d_v, p.d_v);
-    constexpr int fwd = ChainSmem<NI, DKP, W, true>::kBytes, rev = ReverseSmem<NI, DKP, W>::kBytes;
+    constexpr int fwd = ChainSmem<NI, DKP, Mode::kStates>::kBytes, rev = ChainSmem<NI, DKP, Mode::kReverse>::kBytes;
     constexpr int scan = fwd > rev ? fwd : rev;
-    cudaError_t e = cudaFuncSetAttribute(gdr_scan_kernel<T, DKP, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, scan);
+    e = cudaFuncSetAttribute(gdr_scan_kernel<T, DKP>, cudaFuncAttributeMaxDynamicSharedMemorySize, scan);
     if (e != cudaSuccess) return e;
-    const unsigned grid = 2u * ((p.d_v + 16 * W - 1) / (16 * W)) * p.n_heads * p.n_seq;
-    gdr_scan_kernel<T, DKP, W><<<grid, 32 * W, scan, stream>>>(p, scale, vec_qk, vec_v, vec_do);
+    gdr_scan_kernel<T, DKP><<<2 * chain_blocks(p), kChainThreads, scan, stream>>>(maps.q, maps.k, maps.v, maps.dout, p, im, scale);
     count_launches(1);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.n_tok == 0) return e;
@@ -720,17 +510,21 @@ cudaError_t backward(const GdrArgs &p, cudaStream_t stream) {
 }  // namespace
 }  // namespace gdr
 
-size_t gdr_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k, int32_t d_v, bool bf16) {
-    const int ns = bf16 ? 2 : 3;
+size_t gdr_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k,
+                               int32_t d_v, bool bf16) {
+    const int ns = bf16 ? 2 : 3, dkp = d_k <= 64 ? 64 : 128;
     return gdr::scan_offset(n_tok, n_seq, n_heads, ns) +
-           (size_t)gdr::n_slots(n_tok, n_seq) * n_heads * gdr::scan_bytes(ns, d_k <= 64 ? 64 : 128, d_v);
+           (size_t)gdr::n_slots(n_tok, n_seq) * (n_heads * gdr::scan_bytes(ns, dkp, d_v) +
+                                                 gdr::Images::record(bf16 ? 1 : 3, dkp, d_v, n_k_heads, n_heads, 2));
 }
 
 cudaError_t launch_gdr_bwd(const GdrArgs &p, cudaStream_t stream) {
-    const cudaError_t e = launch_gdr_terms(p, stream);
-    if (e != cudaSuccess) return e;
     if (p.bf16) return p.d_k <= 64 ? gdr::backward<__nv_bfloat16, 64>(p, stream) : gdr::backward<__nv_bfloat16, 128>(p, stream);
     return p.d_k <= 64 ? gdr::backward<float, 64>(p, stream) : gdr::backward<float, 128>(p, stream);
+}
+
+cudaError_t read_gdr_bwd_flags(unsigned int *flags, bool reset, cudaStream_t stream) {
+    return gdr::read_flags(flags, reset, stream);
 }
 
 }  // namespace kda

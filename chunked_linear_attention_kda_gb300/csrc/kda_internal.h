@@ -104,11 +104,15 @@ struct GdrArgs {
     int32_t n_seq, n_k_heads, n_heads, d_k, d_v;
     bool bf16;
 };
-size_t gdr_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, bool bf16);
+size_t gdr_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k,
+                               int32_t d_v, bool bf16);
 cudaError_t launch_gdr_fwd(const GdrArgs &args, cudaStream_t stream);
-size_t gdr_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k, int32_t d_v,
-                               bool bf16);
+size_t gdr_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k,
+                               int32_t d_v, bool bf16);
 cudaError_t launch_gdr_bwd(const GdrArgs &args, cudaStream_t stream);
+// The status words of the two passes' chains (bit 4: a pipeline wait gave up).
+cudaError_t read_gdr_fwd_flags(unsigned int *flags, bool reset, cudaStream_t stream);
+cudaError_t read_gdr_bwd_flags(unsigned int *flags, bool reset, cudaStream_t stream);
 
 // One token per row: q, k, v, g, beta, out as one token of GdrArgs; row b's state is
 // state[slots[b]] (slots NULL: state[b]); a slot outside [0, n_slots) is a padded row.

@@ -92,7 +92,7 @@ uint64_t kda_kernel_launch_count(void);
  * two seconds); that kernel then stopped early and its outputs are unspecified:
  * bit 0 the 16-token-step tensor-core forward (and the self-test below), bit 1 the
  * gate-projection GEMM, bit 2 the backward's serial passes, bit 3 the 64-token-step
- * tensor-core forward. A healthy run leaves the word 0. Returns KDA_ERR_INVALID_ARG
+ * tensor-core forward, bit 4 the chains of the gated delta rule. A healthy run leaves the word 0. Returns KDA_ERR_INVALID_ARG
  * for a NULL `flags`, KDA_ERR_CUDA if the copy or the synchronisation fails.
  */
 kda_status kda_read_device_flags(uint32_t *flags, int reset, void *stream);
@@ -526,7 +526,8 @@ int32_t kda_chunk_fwd_pipeline_plan(const int32_t *host_cu_seqlens, int32_t n_se
  * KDA_ERR_UNSUPPORTED (dtype, d_k or d_v above 128) or KDA_ERR_CUDA; no sequence or no
  * token is valid (h_final = h0).
  */
-size_t kda_gdr_chunk_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads,
+size_t kda_gdr_chunk_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_k_heads,
+                                         int32_t n_heads, int32_t d_k, int32_t d_v,
                                          kda_dtype dtype);
 kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, int64_t q_stride,
                              int64_t k_stride, int64_t v_stride, const float *g,
@@ -545,8 +546,9 @@ kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, int64_
  * below -200) dg is 0. workspace as above, kda_gdr_chunk_bwd_workspace_bytes() bytes: it
  * receives the state and the state gradient of every chunk. Errors as kda_gdr_chunk_fwd.
  */
-size_t kda_gdr_chunk_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads,
-                                         int32_t d_k, int32_t d_v, kda_dtype dtype);
+size_t kda_gdr_chunk_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_k_heads,
+                                         int32_t n_heads, int32_t d_k, int32_t d_v,
+                                         kda_dtype dtype);
 kda_status kda_gdr_chunk_bwd(const void *q, const void *k, const void *v, int64_t q_stride,
                              int64_t k_stride, int64_t v_stride, const float *g,
                              const float *beta, const float *h0, const int32_t *cu_seqlens,
