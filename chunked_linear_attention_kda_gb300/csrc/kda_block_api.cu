@@ -292,7 +292,7 @@ static kda_status check_gated(int64_t n_tok, int32_t n_heads, int32_t d, float e
     if (n_tok < 0 || n_heads <= 0 || d <= 0)
         return api_fail(KDA_ERR_INVALID_ARG, "n_tok must be >= 0, n_heads and d positive");
     if (d > 256) return api_fail(KDA_ERR_UNSUPPORTED, "d above 256 is not built");
-    if (n_tok * n_heads > 0x7fffffffLL * 8) return api_fail(KDA_ERR_UNSUPPORTED, "n_tok * n_heads above 2^34");
+    if (n_tok > 0x7fffffffLL / n_heads) return api_fail(KDA_ERR_UNSUPPORTED, "n_tok * n_heads above 2^31 - 1");
     if (!(eps > 0.f)) return api_fail(KDA_ERR_INVALID_ARG, "eps must be positive");
     return KDA_OK;
 }

@@ -51,8 +51,8 @@ __device__ __forceinline__ Chunk find_chunk(const int32_t *cu, int n_seq, int64_
 }
 
 // Per (slot, value head): X and P tile images (NS planes each, swizzled as the kernels read
-// them) and the gate vectors gamma, delta, beta, Gamma (repeated) and the running sum of g as
-// two floats. The chains read the first four.
+// them) and the gate vectors gamma, delta, beta, Gamma (repeated) and the running sum of
+// g log2(e) as pairs of floats. The chains read the first four.
 constexpr int kGateFloats = 6 * C, kChainGates = 4 * C;
 __host__ __device__ constexpr size_t terms_bytes(int ns) {
     return (size_t)2 * ns * kTile * 2 + kGateFloats * 4;
@@ -142,6 +142,13 @@ __device__ __forceinline__ void key_b_t(uint32_t base, int k0, int n0, uint32_t 
     frag_b_t<128>(base + (n0 >> 6) * kHalf, k0, n0 & 63, b);
 }
 
+// 2^x (0 below the normal range)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // two fp32 values as NP packed planes whose sum is the value
 template <int NP>
 __device__ __forceinline__ void split2(float x, float y, uint32_t *p) {
@@ -170,23 +177,6 @@ __device__ __forceinline__ void acc_to_a(const float (*d)[4], uint32_t (*a)[4]) 
 #pragma unroll
         for (int p = 0; p < NP; ++p) a[p][i] = w[p];
     }
-}
-
-// 16 rows (row0 ..) of NT accumulator tiles as NS planes of a swizzled tile image in global
-// memory, planes `plane` bytes apart
-template <int NS, int NT, int RB>
-__device__ __forceinline__ void store_planes(char *dst, size_t plane, int row0, const float (*d)[4]) {
-    const int gr = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t w[NS];
-            split2<NS>(d[n][2 * h], d[n][2 * h + 1], w);
-            char *at = dst + tile_off<RB>(row0 + gr + 8 * h, n * 8 + tq * 2);
-#pragma unroll
-            for (int p = 0; p < NS; ++p) *reinterpret_cast<uint32_t *>(at + p * plane) = w[p];
-        }
 }
 
 // ---------------------------------------------------------------- loading inputs
@@ -275,8 +265,16 @@ __device__ __forceinline__ void write_value_image(char *dst, const T *src, int64
                                                   int tid, int nthreads) {
     constexpr int NI = InputPlanes<T>::N, plane = C * 64;
     const int slices = pad_v(cols) / 32;
+    const bool vec = sizeof(T) == 2 && cols % 8 == 0 && ((uintptr_t)src & 15) == 0 && (stride & 7) == 0;
+#pragma unroll 4
     for (int i = tid; i < slices * C * 4; i += nthreads) {
         const int sl = i / (C * 4), r = (i >> 2) % C, c = (i & 3) * 8;
+        if (vec) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (r < rows && sl * 32 + c < cols) x = *reinterpret_cast<const uint4 *>(src + r * stride + sl * 32 + c);
+            *reinterpret_cast<uint4 *>(dst + sl * plane + tile_off<64>(r, c)) = x;
+            continue;
+        }
         uint32_t w[NI][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -324,7 +322,7 @@ bool rows_vec(const void *p, int64_t stride, int d) {
 }  // namespace gdr
 
 // Chunk terms (X, P, gates of every chunk and value head) and the tile images into the
-// workspace; `values` = 2 when dout has images too.
-cudaError_t launch_gdr_terms(const GdrArgs &args, gdr::Images images, int values, cudaStream_t stream);
+// workspace; `values` = 2 when dout has images too, `ns` planes.
+cudaError_t launch_gdr_terms(const GdrArgs &args, gdr::Images images, int values, int ns, cudaStream_t stream);
 
 }  // namespace kda

@@ -28,23 +28,23 @@ namespace kda {
 namespace gdr {
 namespace {
 
-// even blocks run the reverse chain (the longer one) of a channel block, odd ones the forward
-template <typename T, int DKP>
+// the first half of the blocks runs the reverse chains (the longer ones), the second the forward
+template <typename T, int DKP, int NS>
 __global__ void __launch_bounds__(kChainThreads)
     gdr_scan_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                     const GdrArgs p, const Images im, float scale) {
-    if (blockIdx.x & 1) chain<T, DKP, Mode::kStates>(tm_q, tm_k, tm_v, p, im, 2, blockIdx.x >> 1, scale, false);
-    else chain<T, DKP, Mode::kReverse>(tm_q, tm_k, tm_do, p, im, 2, blockIdx.x >> 1, scale, false);
+    const unsigned n = gridDim.x / 2;
+    if (blockIdx.x >= n) chain<T, DKP, NS, Mode::kStates>(tm_q, tm_k, tm_v, p, im, 2, blockIdx.x - n, scale, false);
+    else chain<T, DKP, NS, Mode::kReverse>(tm_q, tm_k, tm_do, p, im, 2, blockIdx.x, scale, false);
 }
 
 // ---------------------------------------------------------------- local gradients
 constexpr int kLocalThreads = 256;
 
-template <int NI, int DKP>
+template <int NI, int DKP, int NS>
 struct LocalSmem {
-    static constexpr int NS = NI == 1 ? 2 : 3;
-    static constexpr int kStages = NI == 1 ? 2 : 1;
+    static constexpr int kStages = NS == 2 ? 2 : 1;
     static constexpr int kPlane = C * DKP * 2;
     static constexpr int kIn = C * 32 * 2, kVal = 32 * C * 2, kState = 32 * DKP * 2;  // one plane of a 32-channel slice
     static constexpr int dO = 0, V = dO + NI * kIn, U = V + (NI == 1 ? kIn : 0),  // fp32 V is read in place
@@ -66,12 +66,12 @@ __device__ __forceinline__ float quad_sum(float x) {
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
-template <typename T, int DKP>
+template <typename T, int DKP, int NS>
 __global__ void __launch_bounds__(kLocalThreads)
     gdr_local_kernel(const GdrArgs p, float scale, bool vec_qk, bool vec_v, bool vec_do, bool wide_k, bool wide_v) {
     constexpr int NI = InputPlanes<T>::N;
-    using L = LocalSmem<NI, DKP>;
-    constexpr int NS = L::NS, RB = DKP * 2, NH = DKP / 32;  // NH: 16-column steps of half the key channels
+    using L = LocalSmem<NI, DKP, NS>;
+    constexpr int RB = DKP * 2, NH = DKP / 32;  // NH: 16-column steps of half the key channels
     extern __shared__ __align__(128) char smem[];
     const uint32_t base = ptx::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(kLocalThreads)
         }
 
         // row dots with q and k, and the products scaled into the head sums
-        const float *gam = gate, *del = gate + C, *bet = gate + 2 * C, *Gh = gate + 4 * C, *Gl = gate + 5 * C;
+        const float *gam = gate, *del = gate + C, *bet = gate + 2 * C;
+        const float2 *G2 = reinterpret_cast<const float2 *>(gate + 4 * C);
         {
             float qx[2] = {0.f, 0.f}, kx_[2] = {0.f, 0.f}, ku[2] = {0.f, 0.f};
 #pragma unroll
@@ -351,8 +352,8 @@ __global__ void __launch_bounds__(kLocalThreads)
                     for (int i = 0; i < 2; ++i) {
                         const float kk = pair[(n * 4 + 2 * h + i) * kLocalThreads + tid];
                         const float qk = pair[(16 + n * 4 + 2 * h + i) * kLocalThreads + tid];
-                        const float d = (Gh[r] - Gh[j + i]) + (Gl[r] - Gl[j + i]);
-                        const float e = j + i <= r ? expf(d) : 0.f;
+                        const float d = (G2[r].x - G2[j + i].x) + (G2[r].y - G2[j + i].y);
+                        const float e = j + i <= r ? ex2(d) : 0.f;
                         bv[i] = j + i <= r ? scale * e * ou[n][2 * h + i] : 0.f;
                         const float f = j + i < r ? e * eu[n][2 * h + i] : 0.f;
                         fv[i] = -bet[r] * f;
@@ -477,34 +478,43 @@ __global__ void __launch_bounds__(kLocalThreads)
         }
 }
 
-template <typename T, int DKP>
+template <typename T, int DKP, int NS>
 cudaError_t backward(const GdrArgs &p, cudaStream_t stream) {
     constexpr int NI = InputPlanes<T>::N;
-    ChainMaps maps;
-    const Images im{!maps.make<T>(p, true), scan_offset(p.n_tok, p.n_seq, p.n_heads, NI == 1 ? 2 : 3) +
-                                                (size_t)n_slots(p.n_tok, p.n_seq) * p.n_heads * scan_bytes(NI == 1 ? 2 : 3, DKP, p.d_v)};
-    cudaError_t e = launch_gdr_terms(p, im, 2, stream);
-    if (e != cudaSuccess) return e;
     const float scale = 1.f / std::sqrt((float)p.d_k);
+    ChainMaps maps;
+    const Images im{!maps.make<T>(p, true), scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
+                                                (size_t)n_slots(p.n_tok, p.n_seq) * p.n_heads * scan_bytes(NS, DKP, p.d_v)};
+    cudaError_t e = launch_gdr_terms(p, im, 2, NS, stream);
+    if (e != cudaSuccess) return e;
     const bool vec_qk = rows_vec<T>(p.q, p.q_stride, p.d_k) && rows_vec<T>(p.k, p.k_stride, p.d_k);
     const bool vec_v = rows_vec<T>(p.v, p.v_stride, p.d_v);
     const bool vec_do = rows_vec<T>(p.dout, (int64_t)p.n_heads * p.d_v, p.d_v);
-    constexpr int fwd = ChainSmem<NI, DKP, Mode::kStates>::kBytes, rev = ChainSmem<NI, DKP, Mode::kReverse>::kBytes;
+    constexpr int fwd = ChainSmem<NI, DKP, NS, Mode::kStates>::kBytes, rev = ChainSmem<NI, DKP, NS, Mode::kReverse>::kBytes;
     constexpr int scan = fwd > rev ? fwd : rev;
-    e = cudaFuncSetAttribute(gdr_scan_kernel<T, DKP>, cudaFuncAttributeMaxDynamicSharedMemorySize, scan);
+    e = cudaFuncSetAttribute(gdr_scan_kernel<T, DKP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, scan);
     if (e != cudaSuccess) return e;
-    gdr_scan_kernel<T, DKP><<<2 * chain_blocks(p), kChainThreads, scan, stream>>>(maps.q, maps.k, maps.v, maps.dout, p, im, scale);
+    gdr_scan_kernel<T, DKP, NS><<<2 * chain_blocks(p), kChainThreads, scan, stream>>>(maps.q, maps.k, maps.v, maps.dout, p, im, scale);
     count_launches(1);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.n_tok == 0) return e;
-    constexpr int local = LocalSmem<NI, DKP>::kBytes;
-    e = cudaFuncSetAttribute(gdr_local_kernel<T, DKP>, cudaFuncAttributeMaxDynamicSharedMemorySize, local);
+    constexpr int local = LocalSmem<NI, DKP, NS>::kBytes;
+    e = cudaFuncSetAttribute(gdr_local_kernel<T, DKP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, local);
     if (e != cudaSuccess) return e;
     auto wide = [](const void *x, int d) { return d % 2 == 0 && ((uintptr_t)x % (2 * sizeof(T))) == 0; };
-    gdr_local_kernel<T, DKP><<<dim3((unsigned)n_slots(p.n_tok, p.n_seq), p.n_k_heads), kLocalThreads, local, stream>>>(
+    gdr_local_kernel<T, DKP, NS><<<dim3((unsigned)n_slots(p.n_tok, p.n_seq), p.n_k_heads), kLocalThreads, local, stream>>>(
         p, scale, vec_qk, vec_v, vec_do, wide(p.dq, p.d_k) && wide(p.dk, p.d_k), wide(p.dv, p.d_v));
     count_launches(1);
     return cudaGetLastError();
+}
+
+// Planes of the intermediates. dg sums inner products of states with state gradients, which
+// cancel: with two planes its error is 3e-6 to 6e-6 of its norm over many heads and chunks, but
+// where few independent sums make up the norm it was seen at 2e-5. Problems below 1024 (chunk,
+// head) pairs, whose time is latency and not products, take three planes (3e-7); 16K tokens
+// of 32 heads take 2.3 ms with two planes.
+int planes(int64_t n_tok, int32_t n_seq, int32_t n_heads, bool bf16) {
+    return bf16 && n_slots(n_tok, n_seq) * n_heads >= 1024 ? 2 : 3;
 }
 
 }  // namespace
@@ -512,15 +522,18 @@ cudaError_t backward(const GdrArgs &p, cudaStream_t stream) {
 
 size_t gdr_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k,
                                int32_t d_v, bool bf16) {
-    const int ns = bf16 ? 2 : 3, dkp = d_k <= 64 ? 64 : 128;
+    const int ns = gdr::planes(n_tok, n_seq, n_heads, bf16), dkp = d_k <= 64 ? 64 : 128;
     return gdr::scan_offset(n_tok, n_seq, n_heads, ns) +
            (size_t)gdr::n_slots(n_tok, n_seq) * (n_heads * gdr::scan_bytes(ns, dkp, d_v) +
                                                  gdr::Images::record(bf16 ? 1 : 3, dkp, d_v, n_k_heads, n_heads, 2));
 }
 
 cudaError_t launch_gdr_bwd(const GdrArgs &p, cudaStream_t stream) {
-    if (p.bf16) return p.d_k <= 64 ? gdr::backward<__nv_bfloat16, 64>(p, stream) : gdr::backward<__nv_bfloat16, 128>(p, stream);
-    return p.d_k <= 64 ? gdr::backward<float, 64>(p, stream) : gdr::backward<float, 128>(p, stream);
+    using bf16 = __nv_bfloat16;
+    if (!p.bf16) return p.d_k <= 64 ? gdr::backward<float, 64, 3>(p, stream) : gdr::backward<float, 128, 3>(p, stream);
+    if (gdr::planes(p.n_tok, p.n_seq, p.n_heads, true) == 3)
+        return p.d_k <= 64 ? gdr::backward<bf16, 64, 3>(p, stream) : gdr::backward<bf16, 128, 3>(p, stream);
+    return p.d_k <= 64 ? gdr::backward<bf16, 64, 2>(p, stream) : gdr::backward<bf16, 128, 2>(p, stream);
 }
 
 cudaError_t read_gdr_bwd_flags(unsigned int *flags, bool reset, cudaStream_t stream) {

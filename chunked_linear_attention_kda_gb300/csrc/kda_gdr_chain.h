@@ -3,19 +3,21 @@
 // mathematics is in kda_gdr_fwd.cu and kda_gdr_bwd.cu. Internal; not part of the C ABI.
 //
 // A CTA advances 32 value channels of one (sequence, head) through the sequence:
-//   warps 0, 1  the state: 16 value channels each, S^T (16 x d_k, fp32) in registers for the
-//               whole sequence. An fp32 accumulator tile of mma.sync lies in registers as the
-//               A operand (and as the B operand of the transposed product) of the next one,
-//               so S^T -> Y^T -> Z^T -> U^T -> S^T never leaves the warp: the serial path
-//               has no barrier and no shared-memory round trip.
-//   warps 2, 3  what the serial path need not wait for: the output O (from copies of S^T and
-//               U^T handed over in shared memory) or, in reverse, dO^T P and (gamma dO)^T Q,
-//               which they hand to the state warps ahead of their use.
-//   warp 4      one thread loads: tensor copies of whole chunks, bulk copies of the chunk
-//               terms and of tile images, into rings of stages (one ring for what the state
-//               warps read, one for the others').
-// Per chunk and state warp (bf16, d_k = 128) 316 mma.sync m16n8k16 at 8 cycles each bound a
-// step from below: 1.3 us.
+//   warps 0..3  the state, a pair of warps to 16 value channels. S^T (16 x d_k) is held as bf16
+//               planes by both warps and in fp32 by halves of d_k. An accumulator tile of
+//               mma.sync lies in registers as the A operand of the next product, so a warp goes
+//               S^T -> Y^T -> Z^T -> U^T without leaving its registers; each warp of a pair
+//               takes one half of the chunk's tokens, then one half of d_k in the update of S,
+//               and the pair exchanges its halves of U^T and S^T through shared memory at three
+//               barriers of 64 threads.
+//   warps 4..7  what the serial path need not wait for, a pair to 16 value channels: the output
+//               O (from copies of S^T and U^T left in shared memory) or, in reverse, dO^T P and
+//               (gamma dO)^T Q, handed to the state warps ahead of their use.
+//   warp 8      one thread loads: tensor copies of whole chunks, bulk copies of the chunk terms
+//               and of tile images, into rings of stages (one ring for what the state warps
+//               read, one for the others').
+// Per chunk a state warp issues about 170 mma.sync m16n8k16 (bf16, d_k = 128) of 8 cycles each:
+// 0.7 us bound a step from below; the rest is the latency of the hand-offs.
 #pragma once
 
 #include <cuda.h>
@@ -27,7 +29,7 @@ namespace kda {
 namespace gdr {
 
 enum class Mode { kForward, kStates, kReverse };
-constexpr int kChainThreads = 160;
+constexpr int kChainThreads = 288;
 constexpr int kBlockV = 32;  // value channels of a CTA
 constexpr long long kWaitLimit = 4000000000LL;  // SM cycles, about two seconds
 
@@ -64,15 +66,21 @@ __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t byt
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
                  : "memory");
 }
+// one 16 x 16 block of an A-operand fragment to a swizzled tile, `a` the address of lane's row
+__device__ __forceinline__ void store_block(uint32_t a, const uint32_t *f) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(f[0]), "r"(f[1]),
+                 "r"(f[2]), "r"(f[3]) : "memory");
+}
 __device__ __forceinline__ void bulk_wait0() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Shared memory (offsets from a 1024-byte boundary). Ring 1 (state warps): K, X, gates and,
-// forward, V. Ring 2 (the others): Q, P, gates and, reverse, dO. Hand: from the state warps
-// to the others (forward: S^T and U^T fragments) or back (reverse: two accumulators). Keep:
-// the state warps' staging of the records that go to the workspace.
-template <int NI, int DKP, Mode M>
+// forward, V. Ring 2 (the others): Q, P, gates and, reverse, dO. Per pair: Sx the planes of
+// S^T and Uo those of U^T (both read by the output warps), Ux the scaled planes of U^T that
+// the pair exchanges, Zx those of the first half's Z^T; Hand the accumulators handed over in
+// reverse; Keep the staging of the records that go to the workspace (bf16; fp32 inputs, whose
+// tiles leave no room for it, store them from registers).
+template <int NI, int DKP, int NS, Mode M>
 struct ChainSmem {
-    static constexpr int NS = NI == 1 ? 2 : 3;
     static constexpr bool kOut = M == Mode::kForward, kRev = M == Mode::kReverse;
     static constexpr int kKey = NI * C * DKP * 2, kVal = NI * C * kBlockV * 2;
     static constexpr int kX = NS * kTile * 2;
@@ -81,24 +89,24 @@ struct ChainSmem {
     // ring 1
     static constexpr int K = 0, V = K + kKey, X = V + (kRev ? 0 : kVal), Gate1 = X + kX;
     static constexpr int kStage1 = Gate1 + kGate;
-    static constexpr int kBytes1 = kStage1;
-    static constexpr int N1 = NI == 1 ? (kRev ? 2 : 3) : 1;
+    static constexpr int N1 = NS == 2 ? (kRev ? 2 : 3) : 1;
     // ring 2
     static constexpr int Q = 0, dO = Q + kKey, P = dO + (kRev ? kVal : 0), Gate2 = P + kP;
     static constexpr int kStage2 = Gate2 + kGate;
-    static constexpr int N2 = M == Mode::kStates ? 0 : NI == 1 ? 2 : 1;
-    // per warp
-    static constexpr int NH = NI == 1 ? 2 : 1;                    // hand-over buffers
-    static constexpr int kHandS = kOut ? NI * DKP * 32 : DKP * 64;       // S^T fragments, or G^T accumulators
-    static constexpr int kHandU = kOut ? NS * C * 32 : C * 64;           // U^T fragments, or (dO^T P) accumulators
-    static constexpr int kHand = M == Mode::kStates ? 0 : kHandS + kHandU;
+    static constexpr int N2 = M == Mode::kStates ? 0 : NS == 2 ? 2 : 1;
+    // per pair
+    static constexpr int NH = kOut && NS == 2 ? 2 : 1;            // buffers of Sx and Uo
+    static constexpr int kSx = NS * (DKP / 16) * 512, kUx = NS * 4 * 512, kZx = NS * 2 * 512;
+    static constexpr int kUo = kOut ? kUx : 0;
+    static constexpr int kHandG = DKP * 64, kHand = kRev ? kHandG + C * 64 : 0;
     static constexpr int kKeepS = NS * 16 * DKP * 2, kKeepU = NS * 16 * C * 2;
-    static constexpr int kKeep = kOut ? 0 : kKeepS + kKeepU;
-    static constexpr int Ring2 = N1 * kStage1, Hand = Ring2 + N2 * kStage2, Keep = Hand + 2 * NH * kHand;
-    static constexpr int Bars = Keep + 2 * kKeep;
+    static constexpr int kKeep = kOut || NI == 3 ? 0 : kKeepS + kKeepU;
+    static constexpr int Sx = 0, Uo = Sx + NH * kSx, Ux = Uo + NH * kUo, Zx = Ux + kUx, Hand = Zx + kZx, Keep = Hand + kHand;
+    static constexpr int kPair = Keep + kKeep;
+    static constexpr int Ring2 = N1 * kStage1, Pairs = Ring2 + N2 * kStage2, Bars = Pairs + 2 * kPair;
     static constexpr int kBars = 2 * N1 + 2 * N2 + 4 * NH;
     static constexpr int kBytes = Bars + 8 * kBars + 1024;        // the base is rounded up to 1024
-    static_assert(kBytes <= 227 * 1024, "fits an SM");
+    static_assert(kBytes <= 226 * 1024, "fits an SM");
     static_assert(kStage1 % 1024 == 0 && kStage2 % 1024 == 0, "tensor copies land on swizzle boundaries");
 };
 
@@ -163,48 +171,77 @@ __device__ __forceinline__ int ranked_sequence(const int32_t *cu, int n_seq, int
     return *shared;
 }
 
-// ---- products of the state warps: S is NT tiles of S^T (rows: 16 value channels)
+// ---- products of the state warps
 
-// y (16 x 64) += S^T K^T
+// y (16 x 16, tokens n0 ..) = S^T K^T from the planes of S^T; the products of lower planes run
+// on accumulators of their own, so that no product waits for the one before it
 template <int NI, int NS, int DKP>
-__device__ __forceinline__ void state_times_keys(const float (*S)[4], uint32_t k, float (*y)[4]) {
+__device__ __forceinline__ void state_times_keys(const uint32_t (*a)[DKP / 16][4], uint32_t k, int n0, float (*y)[4]) {
+    float lo[2][4];
 #pragma unroll
-    for (int kx = 0; kx < DKP / 16; ++kx) {
-        uint32_t a[NS][4];
-        acc_to_a<NS>(&S[2 * kx], a);
+    for (int i = 0; i < 4; ++i) y[0][i] = y[1][i] = lo[0][i] = lo[1][i] = 0.f;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+    for (int kx = 0; kx < DKP / 16; ++kx)
 #pragma unroll
-            for (int pb = 0; pb < NI; ++pb) {
-                uint32_t b[4];
-                key_b(k + pb * C * DKP * 2, n * 16, kx * 16, b);
+        for (int pb = 0; pb < NI; ++pb) {
+            uint32_t b[4];
+            key_b(k + pb * C * DKP * 2, n0, kx * 16, b);
 #pragma unroll
-                for (int pa = 0; pa + pb < NS; ++pa) {
-                    ptx::mma16816(y[2 * n], a[pa], b[0], b[1]);
-                    ptx::mma16816(y[2 * n + 1], a[pa], b[2], b[3]);
-                }
+            for (int pa = 0; pa + pb < NS; ++pa) {
+                ptx::mma16816(pa + pb ? lo[0] : y[0], a[pa][kx], b[0], b[1]);
+                ptx::mma16816(pa + pb ? lo[1] : y[1], a[pa][kx], b[2], b[3]);
             }
+        }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        y[0][i] += lo[0][i];
+        y[1][i] += lo[1][i];
     }
 }
-// S += u^T K, u^T (16 x 64) an accumulator
+// S (16 x DKP / 2, key channels c0 ..) += u^T K over tokens k0 .. k0 + 15, u^T as planes
 template <int NI, int NS, int DKP>
-__device__ __forceinline__ void add_values_keys(const float (*u)[4], uint32_t k, float (*S)[4]) {
+__device__ __forceinline__ void add_values_keys(const uint32_t (*a)[4], uint32_t k, int k0, int c0, float (*S)[4]) {
 #pragma unroll
-    for (int kx = 0; kx < 4; ++kx) {
-        uint32_t a[NS][4];
-        acc_to_a<NS>(&u[2 * kx], a);
+    for (int n = 0; n < DKP / 32; ++n)
 #pragma unroll
-        for (int n = 0; n < DKP / 16; ++n)
+        for (int pb = 0; pb < NI; ++pb) {
+            uint32_t b[4];
+            key_b_t(k + pb * C * DKP * 2, k0, c0 + n * 16, b);
 #pragma unroll
-            for (int pb = 0; pb < NI; ++pb) {
-                uint32_t b[4];
-                key_b_t(k + pb * C * DKP * 2, kx * 16, n * 16, b);
-#pragma unroll
-                for (int pa = 0; pa + pb < NS; ++pa) {
-                    ptx::mma16816(S[2 * n], a[pa], b[0], b[1]);
-                    ptx::mma16816(S[2 * n + 1], a[pa], b[2], b[3]);
-                }
+            for (int pa = 0; pa + pb < NS; ++pa) {
+                ptx::mma16816(S[2 * n], a[pa], b[0], b[1]);
+                ptx::mma16816(S[2 * n + 1], a[pa], b[2], b[3]);
             }
+        }
+}
+// u (16 x 16, rows or columns n0 of X) += a X over one 16-token block k0 of the contraction
+template <int NS, bool REV>
+__device__ __forceinline__ void add_times_x(const uint32_t (*a)[4], uint32_t x, int k0, int n0, float (*u)[4]) {
+#pragma unroll
+    for (int pb = 0; pb < NS; ++pb) {
+        uint32_t b[4];
+        if (REV) frag_b_t<128>(x + pb * kTile * 2, k0, n0, b);
+        else frag_b<128>(x + pb * kTile * 2, n0, k0, b);
+#pragma unroll
+        for (int pa = 0; pa + pb < NS; ++pa) {
+            ptx::mma16816(u[0], a[pa], b[0], b[1]);
+            ptx::mma16816(u[1], a[pa], b[2], b[3]);
+        }
+    }
+}
+// planes of a 16 x 16 block to and from shared memory, 16 bytes a lane, planes `plane` apart
+template <int NS>
+__device__ __forceinline__ void put_block(char *p, int plane, const uint32_t (*a)[4]) {
+#pragma unroll
+    for (int q = 0; q < NS; ++q)
+        *reinterpret_cast<uint4 *>(p + q * plane + (threadIdx.x & 31) * 16) = make_uint4(a[q][0], a[q][1], a[q][2], a[q][3]);
+}
+template <int NS>
+__device__ __forceinline__ void get_block(const char *p, int plane, uint32_t (*a)[4]) {
+#pragma unroll
+    for (int q = 0; q < NS; ++q) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p + q * plane + (threadIdx.x & 31) * 16);
+        a[q][0] = x.x; a[q][1] = x.y; a[q][2] = x.z; a[q][3] = x.w;
     }
 }
 template <int N>
@@ -214,47 +251,38 @@ __device__ __forceinline__ void zero(float (*x)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
 }
-// x (16 x 64, columns = tokens) *= the tokens' factors
-__device__ __forceinline__ void scale_tokens(float (*x)[4], const float *f) {
-    const int tq = threadIdx.x & 3;
-#pragma unroll
-    for (int n = 0; n < 8; ++n) {
-        const float2 v = *reinterpret_cast<const float2 *>(f + n * 8 + tq * 2);
-        x[n][0] *= v.x; x[n][1] *= v.y; x[n][2] *= v.x; x[n][3] *= v.y;
-    }
-}
 template <int NT>
-__device__ __forceinline__ void load_state(float (*S)[4], const float *src, int v0, int d_k, int d_v) {
+__device__ __forceinline__ void load_state(float (*S)[4], const float *src, int c0, int v0, int d_k, int d_v) {
     const int gr = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c = n * 8 + tq * 2 + (i & 1), v = v0 + gr + (i >> 1) * 8;
+            const int c = c0 + n * 8 + tq * 2 + (i & 1), v = v0 + gr + (i >> 1) * 8;
             S[n][i] = src && c < d_k && v < d_v ? src[(size_t)c * d_v + v] : 0.f;
         }
 }
 template <int NT>
-__device__ __forceinline__ void store_state(const float (*S)[4], float *dst, int v0, int d_k, int d_v) {
+__device__ __forceinline__ void store_state(const float (*S)[4], float *dst, int c0, int v0, int d_k, int d_v) {
     const int gr = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int c = n * 8 + tq * 2 + (i & 1), v = v0 + gr + (i >> 1) * 8;
+            const int c = c0 + n * 8 + tq * 2 + (i & 1), v = v0 + gr + (i >> 1) * 8;
             if (c < d_k && v < d_v) dst[(size_t)c * d_v + v] = S[n][i];
         }
 }
 
 // One CTA's chain; `block` counts channel blocks, then heads, then sequences (longest first).
 // tm_v is dout's map in reverse; `values` and `im` as given to the chunk terms.
-template <typename T, int DKP, Mode M>
+template <typename T, int DKP, int NS, Mode M>
 __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                       const GdrArgs &p, const Images &im, int values, int block, float scale,
                                       bool wide_out) {
     constexpr int NI = InputPlanes<T>::N;
-    using L = ChainSmem<NI, DKP, M>;
-    constexpr int NS = L::NS, NT = DKP / 8, N1 = L::N1, N2 = L::N2, NH = L::NH;
+    using L = ChainSmem<NI, DKP, NS, M>;
+    constexpr int NT = DKP / 16, KX = DKP / 16, N1 = L::N1, N2 = L::N2, NH = L::NH;
     constexpr bool kOut = L::kOut, kRev = L::kRev;
     extern __shared__ __align__(1024) char smem_raw[];
     char *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -269,9 +297,11 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
     const int len = (int)(p.cu_seqlens[seq + 1] - tok0);
     const int n_chunks = (len + C - 1) / C;
     const int64_t slot0 = slot_base(p.cu_seqlens, seq);
-    const int w = warp & 1, v0 = blk * kBlockV + w * 16;
+    // pair w of the CTA's 16-channel halves; half h of its tokens and of d_k
+    const int w = (warp >> 1) & 1, h = warp & 1, v0 = blk * kBlockV + w * 16;
     const size_t st_at = ((size_t)seq * p.n_heads + head) * p.d_k * p.d_v;
     char *ws = static_cast<char *>(p.workspace);
+    char *pair = smem + L::Pairs + w * L::kPair;
 
     auto bar = [&](int i) { return base + L::Bars + 8 * i; };
     auto full1 = [&](int s) { return bar(s); };
@@ -281,16 +311,16 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
     auto hfull = [&](int b) { return bar(2 * N1 + 2 * N2 + b * 2 + w); };
     auto hempty = [&](int b) { return bar(2 * N1 + 2 * N2 + 2 * NH + b * 2 + w); };
     if (tid == 0) {
-        for (int s = 0; s < N1; ++s) { ptx::mbar_init(full1(s), 1); ptx::mbar_init(empty1(s), 2); }
-        for (int s = 0; s < N2; ++s) { ptx::mbar_init(full2(s), 1); ptx::mbar_init(empty2(s), 2); }
-        for (int b = 0; b < 4 * NH; ++b) ptx::mbar_init(bar(2 * N1 + 2 * N2 + b), 1);
+        for (int s = 0; s < N1; ++s) { ptx::mbar_init(full1(s), 1); ptx::mbar_init(empty1(s), 4); }
+        for (int s = 0; s < N2; ++s) { ptx::mbar_init(full2(s), 1); ptx::mbar_init(empty2(s), 4); }
+        for (int b = 0; b < 4 * NH; ++b) ptx::mbar_init(bar(2 * N1 + 2 * N2 + b), 2);
         ptx::mbar_init_fence();
     }
     __syncthreads();
     // step i works on chunk at(i)
     auto at = [&](int i) { return kRev ? n_chunks - 1 - i : i; };
 
-    if (warp == 4) {
+    if (warp == 8) {
         // ------------------------------------------------ loads
         if (lane == 0) {
             const size_t rec = Images::record(NI, DKP, p.d_v, p.n_k_heads, p.n_heads, values);
@@ -344,56 +374,72 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                     for (int i = max(0, done2 - N2); i < done2; ++i) wait_bar(full2(i % N2), (i / N2) & 1);
             }
         }
-    } else if (warp < 2) {
+    } else if (warp < 4) {
         // ------------------------------------------------ state
-        float S[NT][4];
-        load_state<NT>(S, kRev ? (p.dh_final ? p.dh_final + st_at : nullptr) : (p.h0 ? p.h0 + st_at : nullptr), v0,
+        // A failed wait ends no warp of a pair before the other (their barriers would hang): the
+        // step goes on with what is there, and with the flag set no later wait waits.
+        constexpr int kBlk = 512;                      // a plane of a 16 x 16 block
+        constexpr int kSP = KX * kBlk, kUP = 4 * kBlk;  // plane strides of Sx and of Ux, Uo
+        // In the triangular product the first warp's tokens feed both halves: tokens 0..31
+        // forward, 32..63 in reverse.
+        const bool first = h == (kRev ? 1 : 0);
+        const int t0 = 2 * h, o0 = 2 - t0;             // this half's, the other half's first 16-token block
+        auto meet = [&]() { ptx::named_sync(1 + w, 64); };
+        float S[NT][4];                                // key channels h DKP / 2 ..
+        uint32_t sp[NS][KX][4];                        // all key channels, as planes
+        const int c0 = h * (DKP / 2);
+        load_state<NT>(S, kRev ? (p.dh_final ? p.dh_final + st_at : nullptr) : (p.h0 ? p.h0 + st_at : nullptr), c0, v0,
                        p.d_k, p.d_v);
-        char *keep = smem + L::Keep + w * L::kKeep;
+        const size_t rec_s = scan_state_bytes(NS, DKP, p.d_v), rec_u = scan_value_bytes(NS, p.d_v), vp = pad_v(p.d_v);
+        char *keep = pair + L::Keep;
+        // this half's planes of S^T to the pair's buffer, the other half's from it
+        auto share_state = [&](int hb) {
+            char *sx = pair + L::Sx + hb * L::kSx;
+#pragma unroll
+            for (int i = 0; i < KX / 2; ++i) {
+                uint32_t a[NS][4];
+                acc_to_a<NS>(&S[2 * i], a);
+                put_block<NS>(sx + (h * (KX / 2) + i) * kBlk, kSP, a);
+#pragma unroll
+                for (int q = 0; q < NS; ++q)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {  // static register indexes for either half
+                        if (h == 0) sp[q][i][x] = a[q][x];
+                        else sp[q][KX / 2 + i][x] = a[q][x];
+                    }
+            }
+            meet();
+#pragma unroll
+            for (int i = 0; i < KX / 2; ++i) {
+                uint32_t a[NS][4];
+                get_block<NS>(sx + ((1 - h) * (KX / 2) + i) * kBlk, kSP, a);
+#pragma unroll
+                for (int q = 0; q < NS; ++q)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        if (h == 0) sp[q][KX / 2 + i][x] = a[q][x];
+                        else sp[q][i][x] = a[q][x];
+                    }
+            }
+        };
+        if (n_chunks > 0) share_state(0);
         for (int i = 0; i < n_chunks; ++i) {
             const int c = at(i), s1 = i % N1, hb = i % NH;
             const uint32_t s = base + s1 * L::kStage1;
             const float *gate = reinterpret_cast<const float *>(smem + s1 * L::kStage1 + L::Gate1);
-            char *hand = smem + L::Hand + (hb * 2 + w) * L::kHand;
-            [[maybe_unused]] char *rec = ws + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
-                                         ((slot0 + c) * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v);
-            const size_t rec_s = scan_state_bytes(NS, DKP, p.d_v), rec_u = scan_value_bytes(NS, p.d_v);
-            const size_t plane_s = (size_t)pad_v(p.d_v) * DKP * 2, plane_u = (size_t)pad_v(p.d_v) * C * 2;
-            if (kOut) {  // the others are done with the hand-over of NH steps ago
-                if (!warp_wait(hempty(hb), ((i / NH) & 1) ^ 1)) break;
-#pragma unroll
-                for (int kx = 0; kx < DKP / 16; ++kx) {
-                    uint32_t a[NI][4];
-                    acc_to_a<NI>(&S[2 * kx], a);
-#pragma unroll
-                    for (int q = 0; q < NI; ++q)
-                        *reinterpret_cast<uint4 *>(hand + ((q * (DKP / 16) + kx) * 32 + lane) * 16) =
-                            make_uint4(a[q][0], a[q][1], a[q][2], a[q][3]);
-                }
-            } else {     // record the chunk's S0 (or dS1); the staging of the last step has been read
-                if (lane == 0) ptx::bulk_wait_read0();
-                __syncwarp();
-                store_planes<NS, NT, DKP * 2>(keep, 16 * DKP * 2, 0, S);
-                ptx::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) {
-#pragma unroll
-                    for (int q = 0; q < NS; ++q)
-                        bulk_store(rec + (kRev ? rec_s : 0) + q * plane_s + (size_t)v0 * DKP * 2,
-                                   ptx::smem_u32(keep) + q * 16 * DKP * 2, 16 * DKP * 2);
-                    ptx::bulk_commit();
-                }
-            }
-            if (!warp_wait(full1(s1), (i / N1) & 1)) break;
+            char *rec = ws + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
+                        ((slot0 + c) * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v);
+            warp_wait(full1(s1), (i / N1) & 1);
+            if (kRev) warp_wait(hfull(hb), (i / NH) & 1);
 
-            float y[8][4], u[8][4];
-            zero<8>(y);
-            zero<8>(u);
-            state_times_keys<NI, NS, DKP>(S, s + L::K, y);
-            if (!kRev) {
-                // beta Z^T = beta (V^T - gamma Y^T), then U^T = (beta Z)^T X^T, X lower triangular
+            // this half's tokens: forward Y^T, then beta Z^T; in reverse dU^T
+            uint32_t z[2][NS][4];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
+            for (int b = 0; b < 2; ++b) {
+                const int tb = t0 + b;
+                float y[2][4];
+                state_times_keys<NI, NS, DKP>(sp, s + L::K, tb * 16, y);
+                if (!kRev) {  // beta Z^T = beta (V^T - gamma Y^T)
                     float v[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] = 0.f;
@@ -401,7 +447,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                     for (int q = 0; q < NI; ++q) {
                         uint32_t x[4];
                         ptx::ldsm_x4_t(s + L::V + q * C * kBlockV * 2 +
-                                           tile_off<64>(n * 16 + (lane >> 4) * 8 + (lane & 7), w * 16 + ((lane >> 3) & 1) * 8),
+                                           tile_off<64>(tb * 16 + (lane >> 4) * 8 + (lane & 7), w * 16 + ((lane >> 3) & 1) * 8),
                                        x[0], x[1], x[2], x[3]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -410,153 +456,202 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                         }
                     }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int t = n * 16 + h * 8 + tq * 2;
+                    for (int n = 0; n < 2; ++n) {
+                        const int t = tb * 16 + n * 8 + tq * 2;
                         const float2 ga = *reinterpret_cast<const float2 *>(gate + t);
                         const float2 be = *reinterpret_cast<const float2 *>(gate + 2 * C + t);
-                        float *z = y[2 * n + h];
-                        z[0] = be.x * fmaf(-ga.x, z[0], v[4 * h]);
-                        z[1] = be.y * fmaf(-ga.y, z[1], v[4 * h + 1]);
-                        z[2] = be.x * fmaf(-ga.x, z[2], v[4 * h + 2]);
-                        z[3] = be.y * fmaf(-ga.y, z[3], v[4 * h + 3]);
+                        y[n][0] = be.x * fmaf(-ga.x, y[n][0], v[4 * n]);
+                        y[n][1] = be.y * fmaf(-ga.y, y[n][1], v[4 * n + 1]);
+                        y[n][2] = be.x * fmaf(-ga.x, y[n][2], v[4 * n + 2]);
+                        y[n][3] = be.y * fmaf(-ga.y, y[n][3], v[4 * n + 3]);
+                    }
+                } else {      // dU^T = delta (dS1^T K^T) + dO^T P
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int t = 2 * tb + n;
+                        const float2 de = *reinterpret_cast<const float2 *>(gate + C + t * 8 + tq * 2);
+                        const float4 x = *reinterpret_cast<const float4 *>(pair + L::Hand + L::kHandG + (t * 32 + lane) * 16);
+                        y[n][0] = fmaf(de.x, y[n][0], x.x);
+                        y[n][1] = fmaf(de.y, y[n][1], x.y);
+                        y[n][2] = fmaf(de.x, y[n][2], x.z);
+                        y[n][3] = fmaf(de.y, y[n][3], x.w);
                     }
                 }
+                acc_to_a<NS>(y, z[b]);
+            }
+            if constexpr (!kOut && L::kKeep > 0) {  // this half of S0 (or dS1) to the staging, once the
+                if (h == 0 && lane == 0) ptx::bulk_wait_read0();  // last step's record has been read
+                meet();
 #pragma unroll
-                for (int kx = 0; kx < 4; ++kx) {
+                for (int q = 0; q < NS; ++q)
+#pragma unroll
+                    for (int x = 0; x < KX / 2; ++x) {
+                        uint32_t f[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) f[y] = h == 0 ? sp[q][x][y] : sp[q][KX / 2 + x][y];
+                        store_block(ptx::smem_u32(keep) + q * 16 * DKP * 2 +
+                                        tile_off<DKP * 2>(lane & 15, c0 + x * 16 + (lane >> 4) * 8), f);
+                    }
+            }
+            // U^T = (beta Z)^T X^T (X lower triangular), in reverse E^T = dU^T X: each half's diagonal
+            // block by its own warp; the block between the halves by the second warp, which gets
+            // the first one's planes (it would otherwise wait for that product and its own finish)
+            if (first)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) put_block<NS>(pair + L::Zx + b * kBlk, 2 * kBlk, z[b]);
+            float u[4][4];
+            zero<4>(u);
+            if (first) meet();
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+                    if (kRev ? n <= b : n >= b)
+                        add_times_x<NS, kRev>(z[b], s + L::X, (t0 + b) * 16, (t0 + n) * 16, &u[2 * n]);
+            if (!first) {
+                meet();
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
                     uint32_t a[NS][4];
-                    acc_to_a<NS>(&y[2 * kx], a);
+                    get_block<NS>(pair + L::Zx + b * kBlk, 2 * kBlk, a);
 #pragma unroll
-                    for (int n = kx; n < 4; ++n)
-#pragma unroll
-                        for (int pb = 0; pb < NS; ++pb) {
-                            uint32_t b[4];
-                            frag_b<128>(s + L::X + pb * kTile * 2, n * 16, kx * 16, b);
-#pragma unroll
-                            for (int pa = 0; pa + pb < NS; ++pa) {
-                                ptx::mma16816(u[2 * n], a[pa], b[0], b[1]);
-                                ptx::mma16816(u[2 * n + 1], a[pa], b[2], b[3]);
-                            }
-                        }
-                }
-            } else {
-                // dU^T = delta (dS1^T K^T) + dO^T P, then E^T = dU^T X
-                scale_tokens(y, gate + C);
-                if (!warp_wait(hfull(hb), (i / NH) & 1)) break;
-#pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const float4 x = *reinterpret_cast<const float4 *>(hand + L::kHandS + (n * 32 + lane) * 16);
-                    y[n][0] += x.x; y[n][1] += x.y; y[n][2] += x.z; y[n][3] += x.w;
-                }
-#pragma unroll
-                for (int kx = 0; kx < 4; ++kx) {
-                    uint32_t a[NS][4];
-                    acc_to_a<NS>(&y[2 * kx], a);
-#pragma unroll
-                    for (int n = 0; n <= kx; ++n)
-#pragma unroll
-                        for (int pb = 0; pb < NS; ++pb) {
-                            uint32_t b[4];
-                            frag_b_t<128>(s + L::X + pb * kTile * 2, kx * 16, n * 16, b);
-#pragma unroll
-                            for (int pa = 0; pa + pb < NS; ++pa) {
-                                ptx::mma16816(u[2 * n], a[pa], b[0], b[1]);
-                                ptx::mma16816(u[2 * n + 1], a[pa], b[2], b[3]);
-                            }
-                        }
+                    for (int n = 0; n < 2; ++n)
+                        add_times_x<NS, kRev>(a, s + L::X, (o0 + b) * 16, (t0 + n) * 16, &u[2 * n]);
                 }
             }
-            // hand U^T over, or record it (E^T)
-            if (kOut) {
+            auto finish = [&]() {  // u complete: to the output or the record; scaled, to the pair
 #pragma unroll
-                for (int kx = 0; kx < 4; ++kx) {
+                for (int b = 0; b < 2; ++b) {
                     uint32_t a[NS][4];
-                    acc_to_a<NS>(&u[2 * kx], a);
+                    acc_to_a<NS>(&u[2 * b], a);
+                    if constexpr (kOut) put_block<NS>(pair + L::Uo + hb * L::kUo + (t0 + b) * kBlk, kUP, a);
+                    else if constexpr (L::kKeep > 0) {
 #pragma unroll
-                    for (int q = 0; q < NS; ++q)
-                        *reinterpret_cast<uint4 *>(hand + L::kHandS + ((q * 4 + kx) * 32 + lane) * 16) =
-                            make_uint4(a[q][0], a[q][1], a[q][2], a[q][3]);
-                }
-                warp_arrive(hfull(hb));
-            } else {
-                char *ku = keep + L::kKeepS;
-                store_planes<NS, 8, 128>(ku, 16 * C * 2, 0, u);
-                ptx::fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) {
+                        for (int q = 0; q < NS; ++q)
+                            store_block(ptx::smem_u32(keep) + L::kKeepS + q * 16 * C * 2 +
+                                            tile_off<128>(lane & 15, (t0 + b) * 16 + (lane >> 4) * 8), a[q]);
+                    } else {  // straight to the record
 #pragma unroll
-                    for (int q = 0; q < NS; ++q)
-                        bulk_store(rec + 2 * rec_s + (kRev ? rec_u : 0) + q * plane_u + (size_t)v0 * C * 2,
-                                   ptx::smem_u32(ku) + q * 16 * C * 2, 16 * C * 2);
-                    ptx::bulk_commit();
+                        for (int q = 0; q < NS; ++q)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                *reinterpret_cast<uint32_t *>(rec + 2 * rec_s + (kRev ? rec_u : 0) + q * vp * C * 2 +
+                                                              tile_off<128>(v0 + gr + (y & 1) * 8, (t0 + b) * 16 + (y >> 1) * 8 + tq * 2)) = a[q][y];
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {  // delta U, in reverse -gamma beta E
+                        const int t = (t0 + b) * 16 + n * 8 + tq * 2;
+                        float2 f = *reinterpret_cast<const float2 *>(gate + (kRev ? 0 : C) + t);
+                        if (kRev) {
+                            const float2 be = *reinterpret_cast<const float2 *>(gate + 2 * C + t);
+                            f.x *= -be.x;
+                            f.y *= -be.y;
+                        }
+                        float *x = u[2 * b + n];
+                        x[0] *= f.x; x[1] *= f.y; x[2] *= f.x; x[3] *= f.y;
+                    }
+                    acc_to_a<NS>(&u[2 * b], z[b]);
+                    put_block<NS>(pair + L::Ux + (t0 + b) * kBlk, kUP, z[b]);
                 }
-            }
+                if (kOut) warp_arrive(hfull(hb));
+            };
+            // S = Gamma S (+ G, in reverse) while the other warp finishes its half
             const float whole = gate[3 * C];
-            if (!kRev) {
-                // S1^T = Gamma S0^T + (delta U)^T K
-                scale_tokens(u, gate + C);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) S[n][j] *= whole;
-            } else {
-                // dS0^T = Gamma dS1^T + (s gamma dO)^T Q - (gamma beta E)^T K
-#pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const float2 ga = *reinterpret_cast<const float2 *>(gate + n * 8 + tq * 2);
-                    const float2 be = *reinterpret_cast<const float2 *>(gate + 2 * C + n * 8 + tq * 2);
-                    const float x0 = -ga.x * be.x, x1 = -ga.y * be.y;
-                    u[n][0] *= x0; u[n][1] *= x1; u[n][2] *= x0; u[n][3] *= x1;
-                }
+            auto decay = [&]() {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float4 x = *reinterpret_cast<const float4 *>(hand + (n * 32 + lane) * 16);
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (kRev) x = *reinterpret_cast<const float4 *>(pair + L::Hand + ((h * NT + n) * 32 + lane) * 16);
                     S[n][0] = fmaf(whole, S[n][0], x.x);
                     S[n][1] = fmaf(whole, S[n][1], x.y);
                     S[n][2] = fmaf(whole, S[n][2], x.z);
                     S[n][3] = fmaf(whole, S[n][3], x.w);
                 }
-                warp_arrive(hempty(hb));
+                if (kRev) warp_arrive(hempty(hb));
+            };
+            finish();
+            decay();
+            if (first) {  // its own tokens' share of S while the second warp is not done
+#pragma unroll
+                for (int b = 0; b < 2; ++b) add_values_keys<NI, NS, DKP>(z[b], s + L::K, (t0 + b) * 16, c0, S);
+                meet();
+            } else {
+                meet();
+#pragma unroll
+                for (int b = 0; b < 2; ++b) add_values_keys<NI, NS, DKP>(z[b], s + L::K, (t0 + b) * 16, c0, S);
             }
-            add_values_keys<NI, NS, DKP>(u, s + L::K, S);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {  // the other half's tokens
+                uint32_t a[NS][4];
+                get_block<NS>(pair + L::Ux + (o0 + b) * kBlk, kUP, a);
+                add_values_keys<NI, NS, DKP>(a, s + L::K, (o0 + b) * 16, c0, S);
+            }
             warp_arrive(empty1(s1));
+            if constexpr (!kOut && L::kKeep == 0) {  // this half of S0 (or dS1), straight to the record
+#pragma unroll
+                for (int q = 0; q < NS; ++q)
+#pragma unroll
+                    for (int x = 0; x < KX / 2; ++x)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            *reinterpret_cast<uint32_t *>(rec + (kRev ? rec_s : 0) + q * vp * DKP * 2 +
+                                                          tile_off<DKP * 2>(v0 + gr + (y & 1) * 8, c0 + x * 16 + (y >> 1) * 8 + tq * 2)) =
+                                h == 0 ? sp[q][x][y] : sp[q][KX / 2 + x][y];
+            }
+            if constexpr (L::kKeep > 0) ptx::fence_proxy_async();
+            if (kOut && i + 1 >= NH)  // the output that read the next step's buffers is done
+                warp_wait(hempty((i + 1) % NH), ((i + 1 - NH) / NH) & 1);
+            share_state((i + 1) % NH);
+            if constexpr (L::kKeep > 0) {
+                // both halves are staged (the barrier in share_state): one lane sends the record
+                if (h == 0 && lane == 0) {
+#pragma unroll
+                    for (int q = 0; q < NS; ++q) {
+                        bulk_store(rec + (kRev ? rec_s : 0) + (q * vp + v0) * DKP * 2, ptx::smem_u32(keep) + q * 16 * DKP * 2,
+                                   16 * DKP * 2);
+                        bulk_store(rec + 2 * rec_s + (kRev ? rec_u : 0) + (q * vp + v0) * C * 2,
+                                   ptx::smem_u32(keep) + L::kKeepS + q * 16 * C * 2, 16 * C * 2);
+                    }
+                    ptx::bulk_commit();
+                }
+            }
         }
-        if (!kOut && lane == 0) bulk_wait0();
+        if (L::kKeep > 0 && h == 0 && lane == 0) bulk_wait0();
         float *end = kRev ? p.dh0 : kOut ? p.h_final : nullptr;
-        if (end) store_state<NT>(S, end + st_at, v0, p.d_k, p.d_v);
+        if (end) store_state<NT>(S, end + st_at, c0, v0, p.d_k, p.d_v);
     } else if constexpr (kOut) {
-        // ------------------------------------------------ output: O = s gamma Q S0 + (s P) U
+        // ------------------------------------------------ output: O = s gamma Q S0 + (s P) U, half h
         T *out = static_cast<T *>(p.out);
         for (int i = 0; i < n_chunks; ++i) {
             const int s2 = i % N2, hb = i % NH;
             const uint32_t s = base + L::Ring2 + s2 * L::kStage2;
             const float *gate = reinterpret_cast<const float *>(smem + L::Ring2 + s2 * L::kStage2 + L::Gate2);
-            const char *hand = smem + L::Hand + (hb * 2 + w) * L::kHand;
+            const char *sx = pair + L::Sx + hb * L::kSx, *uo = pair + L::Uo + hb * L::kUo;
             if (!warp_wait(full2(s2), (i / N2) & 1)) break;
             if (!warp_wait(hfull(hb), (i / NH) & 1)) break;
-            float o[4][2][4];
-            zero<8>(&o[0][0]);
+            float o[2][2][4];
+            zero<4>(&o[0][0]);
 #pragma unroll
-            for (int kx = 0; kx < DKP / 16; ++kx) {
-                uint4 a[NI];
+            for (int kx = 0; kx < KX; ++kx) {
+                uint32_t a[NI][4];
+                get_block<NI>(sx + kx * 512, KX * 512, a);
 #pragma unroll
-                for (int q = 0; q < NI; ++q)
-                    a[q] = *reinterpret_cast<const uint4 *>(hand + ((q * (DKP / 16) + kx) * 32 + lane) * 16);
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int pq = 0; pq < NI; ++pq) {
                         uint32_t f[4];
-                        key_a(s + L::Q + pq * C * DKP * 2, m * 16, kx * 16, f);
+                        key_a(s + L::Q + pq * C * DKP * 2, (2 * h + m) * 16, kx * 16, f);
 #pragma unroll
                         for (int pa = 0; pa + pq < NI; ++pa) {
-                            ptx::mma16816(o[m][0], f, a[pa].x, a[pa].z);
-                            ptx::mma16816(o[m][1], f, a[pa].y, a[pa].w);
+                            ptx::mma16816(o[m][0], f, a[pa][0], a[pa][2]);
+                            ptx::mma16816(o[m][1], f, a[pa][1], a[pa][3]);
                         }
                     }
             }
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float g0 = scale * gate[m * 16 + gr], g1 = scale * gate[m * 16 + gr + 8];
+            for (int m = 0; m < 2; ++m) {
+                const int r = (2 * h + m) * 16 + gr;
+                const float g0 = scale * gate[r], g1 = scale * gate[r + 8];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     o[m][n][0] *= g0; o[m][n][1] *= g0; o[m][n][2] *= g1; o[m][n][3] *= g1;
@@ -564,49 +659,50 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
             }
 #pragma unroll
             for (int kx = 0; kx < 4; ++kx) {
-                uint4 a[NS];
+                if (kx > 2 * h + 1) break;
+                uint32_t a[NS][4];
+                get_block<NS>(uo + kx * 512, 4 * 512, a);
 #pragma unroll
-                for (int q = 0; q < NS; ++q)
-                    a[q] = *reinterpret_cast<const uint4 *>(hand + L::kHandS + ((q * 4 + kx) * 32 + lane) * 16);
-#pragma unroll
-                for (int m = kx; m < 4; ++m)
+                for (int m = 0; m < 2; ++m) {
+                    if (kx > 2 * h + m) continue;
 #pragma unroll
                     for (int pq = 0; pq < NI; ++pq) {
                         uint32_t f[4];
-                        frag_a<128>(s + L::P + pq * kTile * 2, m * 16, kx * 16, f);
+                        frag_a<128>(s + L::P + pq * kTile * 2, (2 * h + m) * 16, kx * 16, f);
 #pragma unroll
                         for (int pa = 0; pa + pq < NS; ++pa) {
-                            ptx::mma16816(o[m][0], f, a[pa].x, a[pa].z);
-                            ptx::mma16816(o[m][1], f, a[pa].y, a[pa].w);
+                            ptx::mma16816(o[m][0], f, a[pa][0], a[pa][2]);
+                            ptx::mma16816(o[m][1], f, a[pa][1], a[pa][3]);
                         }
                     }
+                }
             }
             warp_arrive(hempty(hb));
             warp_arrive(empty2(s2));
 #pragma unroll
-            for (int m = 0; m < 4; ++m)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = i * C + m * 16 + gr + h * 8;
+                for (int x = 0; x < 2; ++x) {
+                    const int r = i * C + (2 * h + m) * 16 + gr + x * 8;
                     if (r >= len) continue;
                     T *row = out + ((tok0 + r) * p.n_heads + head) * p.d_v;
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
                         const int v = v0 + n * 8 + tq * 2;
-                        if (v < p.d_v) put2(row + v, o[m][n][h * 2], o[m][n][h * 2 + 1], wide_out, v + 1 < p.d_v);
+                        if (v < p.d_v) put2(row + v, o[m][n][x * 2], o[m][n][x * 2 + 1], wide_out, v + 1 < p.d_v);
                     }
                 }
         }
     } else if constexpr (kRev) {
-        // ------------------------------------------------ G^T = (s gamma dO)^T Q and dO^T P
+        // ------------------------------------------------ G^T = (s gamma dO)^T Q, key channels of half
+        // h, and dO^T P, tokens of half h
         for (int i = 0; i < n_chunks; ++i) {
             const int s2 = i % N2, hb = i % NH;
             const uint32_t s = base + L::Ring2 + s2 * L::kStage2;
             const float *gate = reinterpret_cast<const float *>(smem + L::Ring2 + s2 * L::kStage2 + L::Gate2);
-            char *hand = smem + L::Hand + (hb * 2 + w) * L::kHand;
             if (!warp_wait(full2(s2), (i / N2) & 1)) break;
-            float y[8][4], G[NT][4];
-            zero<8>(y);
+            float y[4][4], G[NT][4];
+            zero<4>(y);
             zero<NT>(G);
 #pragma unroll
             for (int kx = 0; kx < 4; ++kx) {
@@ -614,17 +710,18 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                 for (int q = 0; q < NI; ++q) frag_a_t<64>(s + L::dO + q * C * kBlockV * 2, kx * 16, w * 16, a[q]);
 #pragma unroll
-                for (int n = 0; n <= kx; ++n)
+                for (int n = 0; n < 2; ++n)
+                    if (2 * h + n <= kx)
 #pragma unroll
-                    for (int pb = 0; pb < NS; ++pb) {
-                        uint32_t b[4];
-                        frag_b_t<128>(s + L::P + pb * kTile * 2, kx * 16, n * 16, b);
+                        for (int pb = 0; pb < NS; ++pb) {
+                            uint32_t b[4];
+                            frag_b_t<128>(s + L::P + pb * kTile * 2, kx * 16, (2 * h + n) * 16, b);
 #pragma unroll
-                        for (int pa = 0; pa < NI && pa + pb < NS; ++pa) {
-                            ptx::mma16816(y[2 * n], a[pa], b[0], b[1]);
-                            ptx::mma16816(y[2 * n + 1], a[pa], b[2], b[3]);
+                            for (int pa = 0; pa < NI && pa + pb < NS; ++pa) {
+                                ptx::mma16816(y[2 * n], a[pa], b[0], b[1]);
+                                ptx::mma16816(y[2 * n + 1], a[pa], b[2], b[3]);
+                            }
                         }
-                    }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 ga = *reinterpret_cast<const float2 *>(gate + kx * 16 + (j >> 1) * 8 + tq * 2);
@@ -639,27 +736,16 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                     for (int q = 0; q < NS; ++q) d[q][j] = sp[q];
                 }
-#pragma unroll
-                for (int n = 0; n < DKP / 16; ++n)
-#pragma unroll
-                    for (int pb = 0; pb < NI; ++pb) {
-                        uint32_t b[4];
-                        key_b_t(s + L::Q + pb * C * DKP * 2, kx * 16, n * 16, b);
-#pragma unroll
-                        for (int pa = 0; pa + pb < NS; ++pa) {
-                            ptx::mma16816(G[2 * n], d[pa], b[0], b[1]);
-                            ptx::mma16816(G[2 * n + 1], d[pa], b[2], b[3]);
-                        }
-                    }
+                add_values_keys<NI, NS, DKP>(d, s + L::Q, kx * 16, h * (DKP / 2), G);
             }
             warp_arrive(empty2(s2));
             if (!warp_wait(hempty(hb), ((i / NH) & 1) ^ 1)) break;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                *reinterpret_cast<float4 *>(hand + (n * 32 + lane) * 16) = make_float4(G[n][0], G[n][1], G[n][2], G[n][3]);
+                *reinterpret_cast<float4 *>(pair + L::Hand + ((h * NT + n) * 32 + lane) * 16) = make_float4(G[n][0], G[n][1], G[n][2], G[n][3]);
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
-                *reinterpret_cast<float4 *>(hand + L::kHandS + (n * 32 + lane) * 16) =
+            for (int n = 0; n < 4; ++n)
+                *reinterpret_cast<float4 *>(pair + L::Hand + L::kHandG + ((4 * h + n) * 32 + lane) * 16) =
                     make_float4(y[n][0], y[n][1], y[n][2], y[n][3]);
             warp_arrive(hfull(hb));
         }

@@ -26,20 +26,34 @@ namespace kda {
 namespace gdr {
 namespace {
 
-constexpr int kTermThreads = 128;
+constexpr int kTermThreads = 256;
 constexpr int kARow = 68;  // floats of a row of A in shared memory
 
-template <int NI, int DKP>
+template <int NI, int DKP, int NS>
 struct TermsSmem {
-    static constexpr int NS = NI == 1 ? 2 : 3;
     static constexpr int kPlane = C * DKP * 2;
     static constexpr int K = 0, Q = K + NI * kPlane;
     static constexpr int kTileP = NS * kTile * 2;               // P of one head, over K or Q once they are used
     static constexpr int kHead = kTileP > NI * kPlane ? kTileP : NI * kPlane;
     static constexpr int A = 2 * kHead;
-    static constexpr int Vec = A + 2 * C * kARow * 4;           // per head: Ghi, Glo, beta
+    static constexpr int Vec = A + 2 * C * kARow * 4;           // per head: G as float2, beta
     static constexpr int kBytes = Vec + 2 * 3 * C * 4;
 };
+
+// A sum carried as two floats.
+struct Two { float hi, lo; };
+__device__ __forceinline__ Two add(Two x, Two y) {
+    const float s = x.hi + y.hi, t = s - x.hi;
+    const float e = (x.hi - (s - t)) + (y.hi - t) + (x.lo + y.lo);
+    const float hi = s + e;
+    return {hi, e - (hi - s)};
+}
+constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596299e-8f;  // log2(e) in two floats
+// 2^(hi + lo), lo far below hi
+__device__ __forceinline__ float exp2_of(float hi, float lo) {
+    const float e = ex2(hi);
+    return fmaf(e * 0.693147181f, lo, e);
+}
 
 // ---- the inverse of I + A, a head at a time by two warps, in place over A (fp32, rows kARow
 // apart; strictly lower entries valid). 16 x 16 diagonal blocks by forward substitution, a
@@ -152,11 +166,11 @@ __device__ __forceinline__ void join_blocks(float *A, int r0, int c0, int n0, bo
     __syncthreads();
 }
 
-template <typename T, int DKP>
-__global__ void __launch_bounds__(kTermThreads)
+template <typename T, int DKP, int NS>
+__global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
     gdr_terms_kernel(const GdrArgs p, const Images im, int values, float scale, bool vec) {
-    constexpr int NI = InputPlanes<T>::N, NS = NI == 1 ? 2 : 3;
-    using L = TermsSmem<NI, DKP>;
+    constexpr int NI = InputPlanes<T>::N;
+    using L = TermsSmem<NI, DKP, NS>;
     extern __shared__ __align__(1024) char smem[];
     const uint32_t base = ptx::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -171,6 +185,20 @@ __global__ void __launch_bounds__(kTermThreads)
     load_key_tile<T, DKP>(base + L::Q, static_cast<const T *>(p.q) + ch.t0 * p.q_stride + (int64_t)kh * p.d_k,
                           p.q_stride, ch.len, p.d_k, vec, tid, kTermThreads);
     ptx::cp_async_commit();
+    // g and beta of the first two heads, ahead of their use: warp w < 2 takes one head of a pair
+    float gx[2], bx[2];
+    auto fetch_gates = [&](int h0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = lane * 2 + i;
+            gx[i] = bx[i] = 0.f;
+            if (warp < min(2, group - h0) && r < ch.len) {
+                gx[i] = p.g[(ch.t0 + r) * hv + kh * group + h0 + warp];
+                bx[i] = p.beta[(ch.t0 + r) * hv + kh * group + h0 + warp];
+            }
+        }
+    };
+    fetch_gates(0);
     cp_async_wait<0>();
     __syncthreads();
 
@@ -193,33 +221,30 @@ __global__ void __launch_bounds__(kTermThreads)
         }
     }
 
-    // K K^T and Q K^T: warp w the rows 16 w .., columns up to its own
-    float kk[8][4], qk[8][4];
+    // K K^T (warps 0..3) and Q K^T (warps 4..7): rows 16 (warp % 4) .., columns up to their own
+    const int wr = warp & 3;
+    const bool keys = warp < 4;
+    float kk[8][4];
 #pragma unroll
     for (int n = 0; n < 8; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) kk[n][i] = qk[n][i] = 0.f;
+        for (int i = 0; i < 4; ++i) kk[n][i] = 0.f;
 #pragma unroll 2
     for (int c = 0; c < DKP; c += 16) {
-        uint32_t ak[NI][4], aq[NI][4];
+        uint32_t a[NI][4];
 #pragma unroll
-        for (int q = 0; q < NI; ++q) {
-            key_a(base + L::K + q * L::kPlane, warp * 16, c, ak[q]);
-            key_a(base + L::Q + q * L::kPlane, warp * 16, c, aq[q]);
-        }
+        for (int q = 0; q < NI; ++q) key_a(base + (keys ? L::K : L::Q) + q * L::kPlane, wr * 16, c, a[q]);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            if (n > warp) break;
+            if (n > wr) break;
 #pragma unroll
             for (int pb = 0; pb < NI; ++pb) {
                 uint32_t b[4];
                 key_b(base + L::K + pb * L::kPlane, n * 16, c, b);
 #pragma unroll
                 for (int pa = 0; pa + pb < NI; ++pa) {
-                    ptx::mma16816(kk[2 * n], ak[pa], b[0], b[1]);
-                    ptx::mma16816(kk[2 * n + 1], ak[pa], b[2], b[3]);
-                    ptx::mma16816(qk[2 * n], aq[pa], b[0], b[1]);
-                    ptx::mma16816(qk[2 * n + 1], aq[pa], b[2], b[3]);
+                    ptx::mma16816(kk[2 * n], a[pa], b[0], b[1]);
+                    ptx::mma16816(kk[2 * n + 1], a[pa], b[2], b[3]);
                 }
             }
         }
@@ -229,76 +254,85 @@ __global__ void __launch_bounds__(kTermThreads)
     float *vec_s = reinterpret_cast<float *>(smem + L::Vec);
     for (int h0 = 0; h0 < group; h0 += 2) {
         const int nh = min(2, group - h0);
-        // gates: warp w < nh takes head h0 + w; running sums in double, held as two floats
+        // gates: warp w < nh takes head h0 + w; running sums of g log2(e) in two floats (the
+        // fp64 pipe of this part is narrow), so that differences of neighbours stay exact
         if (warp < nh) {
             const int head = kh * group + h0 + warp;
-            double s[2];
-            float b[2];
+            Two s[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int r = lane * 2 + i;
-                float x = 0.f;
-                b[i] = 0.f;
-                if (r < ch.len) {
-                    x = p.g[(ch.t0 + r) * hv + head];
-                    // below -200 (and at -inf) the decay is 0 in fp32 all the same; a finite
-                    // floor keeps differences of the sums free of inf - inf
-                    x = x < kGFloor ? kGFloor : x;
-                    b[i] = p.beta[(ch.t0 + r) * hv + head];
-                }
-                s[i] = x;
+                // below -200 (and at -inf) the decay is 0 in fp32 all the same; a finite floor
+                // keeps differences of the sums free of inf - inf
+                const float x = gx[i] < kGFloor ? kGFloor : gx[i];
+                s[i].hi = x * kLog2e;
+                s[i].lo = fmaf(x, kLog2e, -s[i].hi) + x * kLog2eLo;
             }
-            s[1] += s[0];
-            double run = s[1];
+            s[1] = add(s[0], s[1]);
+            Two run = s[1];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += y;
+                const Two y = {__shfl_up_sync(0xffffffffu, run.hi, o), __shfl_up_sync(0xffffffffu, run.lo, o)};
+                if (lane >= o) run = add(y, run);
             }
-            const double before = run - s[1], total = __shfl_sync(0xffffffffu, run, 31);
+            Two before = {__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
+            if (lane == 0) before = {0.f, 0.f};
+            const Two total = {__shfl_sync(0xffffffffu, run.hi, 31), __shfl_sync(0xffffffffu, run.lo, 31)};
             float *out = reinterpret_cast<float *>(ws + (slot * hv + head) * terms_bytes(NS) + (size_t)2 * NS * kTile * 2);
+            float2 *G2 = reinterpret_cast<float2 *>(vec_s + warp * 3 * C);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = lane * 2 + i;
-                const double G = before + s[i];
-                const float hi = (float)G, lo = (float)(G - (double)hi);
-                vec_s[warp * 3 * C + r] = hi;
-                vec_s[warp * 3 * C + C + r] = lo;
-                vec_s[warp * 3 * C + 2 * C + r] = b[i];
-                out[r] = expf(hi);
-                out[C + r] = expf((float)(total - G));
-                out[2 * C + r] = b[i];
-                out[3 * C + r] = expf((float)total);
-                out[4 * C + r] = hi;
-                out[5 * C + r] = lo;
+                const Two G = i ? run : add(before, s[0]);
+                G2[r] = make_float2(G.hi, G.lo);
+                vec_s[warp * 3 * C + 2 * C + r] = bx[i];
+                out[r] = exp2_of(G.hi, G.lo);
+                out[C + r] = ex2((total.hi - G.hi) + (total.lo - G.lo));
+                out[2 * C + r] = bx[i];
+                out[3 * C + r] = exp2_of(total.hi, total.lo);
+                reinterpret_cast<float2 *>(out + 4 * C)[r] = make_float2(G.hi, G.lo);
             }
         }
+        fetch_gates(h0 + 2);
         __syncthreads();  // the gates are in; K and Q (or the previous pair's P) are done with
-        // A (fp32, zero above the diagonal) and P (bf16 planes) of both heads
+        // A (fp32; warps 0..3) and P (bf16 planes; warps 4..7) of both heads, zero above the diagonal
         for (int hh = 0; hh < nh; ++hh) {
-            const float *Gh = vec_s + hh * 3 * C, *Gl = Gh + C, *B = Gl + C;
+            const float2 *G2 = reinterpret_cast<const float2 *>(vec_s + hh * 3 * C);
+            const float *B = vec_s + hh * 3 * C + 2 * C;
             char *tile = smem + hh * L::kHead;
-            const int r0 = warp * 16 + (lane >> 2);
+            float *Ah = A + hh * C * kARow;
+            const int r0 = wr * 16 + (lane >> 2);
+            const float2 g0 = G2[r0], g1 = G2[r0 + 8];
+            const float f0 = keys ? B[r0] : scale, f1 = keys ? B[r0 + 8] : scale;
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
                 const int j = n * 8 + (lane & 3) * 2;
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    const int r = r0 + hf * 8;
-                    float a[2], pv[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float d = (Gh[r] - Gh[j + i]) + (Gl[r] - Gl[j + i]);
-                        const float e = j + i <= r ? expf(d) : 0.f;
-                        pv[i] = j + i <= r ? scale * e * qk[n][hf * 2 + i] : 0.f;
-                        a[i] = j + i < r ? B[r] * e * kk[n][hf * 2 + i] : 0.f;
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                if (n <= 2 * wr + 1) {
+                    const float4 gj = *reinterpret_cast<const float4 *>(&G2[j]);
+                    x[0] = f0 * kk[n][0] * ex2((g0.x - gj.x) + (g0.y - gj.y));
+                    x[1] = f0 * kk[n][1] * ex2((g0.x - gj.z) + (g0.y - gj.w));
+                    x[2] = f1 * kk[n][2] * ex2((g1.x - gj.x) + (g1.y - gj.y));
+                    x[3] = f1 * kk[n][3] * ex2((g1.x - gj.z) + (g1.y - gj.w));
+                    if (n >= 2 * wr) {  // the diagonal block; A is strictly lower
+                        const int e = keys ? 0 : 1;
+                        if (j >= r0 + e) x[0] = 0.f;
+                        if (j + 1 >= r0 + e) x[1] = 0.f;
+                        if (j >= r0 + 8 + e) x[2] = 0.f;
+                        if (j + 1 >= r0 + 8 + e) x[3] = 0.f;
                     }
-                    *reinterpret_cast<float2 *>(A + hh * C * kARow + r * kARow + j) = make_float2(a[0], a[1]);
-                    uint32_t w[NS];
-                    split2<NS>(pv[0], pv[1], w);
+                }
+                if (keys) {
+                    *reinterpret_cast<float2 *>(Ah + r0 * kARow + j) = make_float2(x[0], x[1]);
+                    *reinterpret_cast<float2 *>(Ah + (r0 + 8) * kARow + j) = make_float2(x[2], x[3]);
+                } else {
 #pragma unroll
-                    for (int pl = 0; pl < NS; ++pl)
-                        *reinterpret_cast<uint32_t *>(tile + pl * kTile * 2 + tile_off<128>(r, j)) = w[pl];
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t w[NS];
+                        split2<NS>(x[2 * h], x[2 * h + 1], w);
+                        char *at = tile + tile_off<128>(r0 + 8 * h, j);
+#pragma unroll
+                        for (int pl = 0; pl < NS; ++pl) *reinterpret_cast<uint32_t *>(at + pl * kTile * 2) = w[pl];
+                    }
                 }
             }
         }
@@ -307,16 +341,18 @@ __global__ void __launch_bounds__(kTermThreads)
             const int head = kh * group + h0 + hh;
             uint4 *dst = reinterpret_cast<uint4 *>(ws + (slot * hv + head) * terms_bytes(NS) + (size_t)NS * kTile * 2);
             const uint4 *src = reinterpret_cast<const uint4 *>(smem + hh * L::kHead);
-            for (int i = tid; i < NS * kTile / 8; i += kTermThreads) dst[i] = src[i];
+            const int planes = values == 2 ? NS : NI;  // the forward pass alone reads P at the inputs' precision
+            for (int i = tid; i < planes * kTile / 8; i += kTermThreads) dst[i] = src[i];
         }
-        // X in place: warps 2 h, 2 h + 1 for head h
+        // X in place: warps 2 h, 2 h + 1 for head h (the other warps only keep the barriers)
         {
             const int hh = warp >> 1, w = warp & 1, t = tid & 63;
-            float *X = A + hh * C * kARow;
-            diagonal_column(X, t >> 4, t & 15, hh < nh);
+            const bool on = hh < nh;
+            float *X = A + (on ? hh : 0) * C * kARow;
+            diagonal_column(X, t >> 4, t & 15, on);
             __syncthreads();
-            join_blocks<16>(X, 32 * w + 16, 32 * w, 0, hh < nh);
-            join_blocks<32>(X, 32, 0, 16 * w, hh < nh);
+            join_blocks<16>(X, 32 * w + 16, 32 * w, 0, on);
+            join_blocks<32>(X, 32, 0, 16 * w, on);
         }
         for (int hh = 0; hh < nh; ++hh) {  // X out, split into planes on the way
             const int head = kh * group + h0 + hh;
@@ -343,37 +379,38 @@ __global__ void __launch_bounds__(kTermThreads)
     }
 }
 
-template <typename T, int DKP>
+template <typename T, int DKP, int NS>
 __global__ void __launch_bounds__(kChainThreads)
     gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const GdrArgs p, const Images im, float scale,
                      bool wide_out) {
-    chain<T, DKP, Mode::kForward>(tm_q, tm_k, tm_v, p, im, 1, blockIdx.x, scale, wide_out);
+    chain<T, DKP, NS, Mode::kForward>(tm_q, tm_k, tm_v, p, im, 1, blockIdx.x, scale, wide_out);
 }
 
-template <typename T, int DKP>
+template <typename T, int DKP, int NS>
 cudaError_t terms(const GdrArgs &p, const Images &im, int values, cudaStream_t stream) {
-    constexpr int bytes = TermsSmem<InputPlanes<T>::N, DKP>::kBytes;
-    const cudaError_t e = cudaFuncSetAttribute(gdr_terms_kernel<T, DKP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    constexpr int bytes = TermsSmem<InputPlanes<T>::N, DKP, NS>::kBytes;
+    const cudaError_t e = cudaFuncSetAttribute(gdr_terms_kernel<T, DKP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     const bool vec = rows_vec<T>(p.q, p.q_stride, p.d_k) && rows_vec<T>(p.k, p.k_stride, p.d_k);
     const dim3 grid((unsigned)n_slots(p.n_tok, p.n_seq), p.n_k_heads);
-    gdr_terms_kernel<T, DKP><<<grid, kTermThreads, bytes, stream>>>(p, im, values, 1.f / std::sqrt((float)p.d_k), vec);
+    gdr_terms_kernel<T, DKP, NS><<<grid, kTermThreads, bytes, stream>>>(p, im, values, 1.f / std::sqrt((float)p.d_k), vec);
     count_launches(1);
     return cudaGetLastError();
 }
 
 template <typename T, int DKP>
 cudaError_t forward(const GdrArgs &p, cudaStream_t stream) {
+    constexpr int NI = InputPlanes<T>::N, NS = NI == 1 ? 2 : 3;
     ChainMaps maps;
-    Images im{!maps.make<T>(p, false), scan_offset(p.n_tok, p.n_seq, p.n_heads, InputPlanes<T>::N == 1 ? 2 : 3)};
-    cudaError_t e = launch_gdr_terms(p, im, 1, stream);
+    const Images im{!maps.make<T>(p, false), scan_offset(p.n_tok, p.n_seq, p.n_heads, NS)};
+    cudaError_t e = launch_gdr_terms(p, im, 1, NS, stream);
     if (e != cudaSuccess) return e;
-    constexpr int bytes = ChainSmem<InputPlanes<T>::N, DKP, Mode::kForward>::kBytes;
-    e = cudaFuncSetAttribute(gdr_chain_kernel<T, DKP>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    constexpr int bytes = ChainSmem<NI, DKP, NS, Mode::kForward>::kBytes;
+    e = cudaFuncSetAttribute(gdr_chain_kernel<T, DKP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     const bool wide = p.d_v % 2 == 0 && ((uintptr_t)p.out % (2 * sizeof(T))) == 0;
-    gdr_chain_kernel<T, DKP><<<chain_blocks(p), kChainThreads, bytes, stream>>>(
+    gdr_chain_kernel<T, DKP, NS><<<chain_blocks(p), kChainThreads, bytes, stream>>>(
         maps.q, maps.k, maps.v, p, im, 1.f / std::sqrt((float)p.d_k), wide);
     count_launches(1);
     return cudaGetLastError();
@@ -389,10 +426,12 @@ size_t gdr_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, in
                gdr::Images::record(bf16 ? 1 : 3, d_k <= 64 ? 64 : 128, d_v, n_k_heads, n_heads, 1);
 }
 
-cudaError_t launch_gdr_terms(const GdrArgs &p, gdr::Images im, int values, cudaStream_t stream) {
+cudaError_t launch_gdr_terms(const GdrArgs &p, gdr::Images im, int values, int ns, cudaStream_t stream) {
+    using bf16 = __nv_bfloat16;
     if (p.n_tok == 0) return cudaSuccess;
-    if (p.bf16) return p.d_k <= 64 ? gdr::terms<__nv_bfloat16, 64>(p, im, values, stream) : gdr::terms<__nv_bfloat16, 128>(p, im, values, stream);
-    return p.d_k <= 64 ? gdr::terms<float, 64>(p, im, values, stream) : gdr::terms<float, 128>(p, im, values, stream);
+    if (!p.bf16) return p.d_k <= 64 ? gdr::terms<float, 64, 3>(p, im, values, stream) : gdr::terms<float, 128, 3>(p, im, values, stream);
+    if (ns == 3) return p.d_k <= 64 ? gdr::terms<bf16, 64, 3>(p, im, values, stream) : gdr::terms<bf16, 128, 3>(p, im, values, stream);
+    return p.d_k <= 64 ? gdr::terms<bf16, 64, 2>(p, im, values, stream) : gdr::terms<bf16, 128, 2>(p, im, values, stream);
 }
 
 cudaError_t launch_gdr_fwd(const GdrArgs &p, cudaStream_t stream) {

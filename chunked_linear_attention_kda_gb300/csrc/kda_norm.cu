@@ -93,6 +93,39 @@ __device__ __forceinline__ void store_row(T *p, int d, int t, int G, const float
     }
 }
 
+// A thread's 8 NV channels of a row as they were loaded: unpacked to floats only at use, so
+// that several rows' worth of loads can be in flight without their fp32 copies' registers.
+template <typename T, int NV, bool VEC>
+struct Held {
+    float x[8 * NV];
+    __device__ __forceinline__ void load(const T *p, int d, int t, int G) { load_row<NV, VEC>(p, d, t, G, x); }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8 * NV; ++i) x[i] = 0.f;
+    }
+    __device__ __forceinline__ float get(int i) const { return x[i]; }
+};
+template <int NV>
+struct Held<bf16, NV, true> {
+    uint32_t w[4 * NV];
+    __device__ __forceinline__ void load(const bf16 *p, int d, int t, int G) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = 8 * (t + G * i);
+            uint4 a = make_uint4(0, 0, 0, 0);
+            if (c < d) a = *reinterpret_cast<const uint4 *>(p + c);
+            w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 4 * NV; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+};
+
 // Sum over the G threads (G = 32 WPR) of a group; every thread gets it. `buf` holds WPR
 // floats per group and alternates between two halves so that one barrier per sum suffices.
 __device__ __forceinline__ float warp_sum(float x) {
@@ -114,6 +147,28 @@ __device__ __forceinline__ float group_sum(float x, float *buf, int group) {
     return x;
 }
 
+// two sums at once, one barrier; `buf` (WPR pairs per group) alternates between two halves
+template <int WPR>
+__device__ __forceinline__ float2 group_sum2(float2 x, float2 *buf, int group) {
+    x.x = warp_sum(x.x);
+    x.y = warp_sum(x.y);
+    if constexpr (WPR > 1) {
+        const int w = (threadIdx.x >> 5) % WPR;
+        if ((threadIdx.x & 31) == 0) buf[group * WPR + w] = x;
+        __syncthreads();
+        const int l = threadIdx.x & 31;
+        x = l < WPR ? buf[group * WPR + l] : make_float2(0.f, 0.f);
+#pragma unroll
+        for (int o = WPR / 2; o > 0; o >>= 1) {
+            x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+            x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+        }
+        x.x = __shfl_sync(0xffffffffu, x.x, 0);
+        x.y = __shfl_sync(0xffffffffu, x.y, 0);
+    }
+    return x;
+}
+
 template <int WPR>
 struct Rows {
     static constexpr int kWarps = WPR < 8 ? 8 : WPR;
@@ -128,21 +183,22 @@ __global__ void __launch_bounds__(Rows<WPR>::kThreads)
     const int group = threadIdx.x / L::G, t = threadIdx.x % L::G;
     const int64_t row = (int64_t)blockIdx.x * L::kGroups + group;
     const bool live = row < p.n_rows;
-    float r[8 * NV];
+    float r[8 * NV], w[8 * NV];
 #pragma unroll
     for (int i = 0; i < 8 * NV; ++i) r[i] = 0.f;
     if (live) {
-        load_row<NV, VEC>(static_cast<const T *>(p.x) + row * p.x_stride, p.d, t, L::G, r);
-        float a[8 * NV];
+        Held<T, NV, VEC> x, res;
+        x.load(static_cast<const T *>(p.x) + row * p.x_stride, p.d, t, L::G);
+        if (p.residual) res.load(static_cast<const T *>(p.residual) + row * p.residual_stride, p.d, t, L::G);
+        else res.clear();
+        load_row<NV, VEC>(p.weight, p.d, t, L::G, w);
         if (p.scale) {
-            load_row<NV, VEC>(p.scale, p.d, t, L::G, a);
+            load_row<NV, VEC>(p.scale, p.d, t, L::G, r);
 #pragma unroll
-            for (int i = 0; i < 8 * NV; ++i) r[i] *= a[i];
-        }
-        if (p.residual) {
-            load_row<NV, VEC>(static_cast<const T *>(p.residual) + row * p.residual_stride, p.d, t, L::G, a);
+            for (int i = 0; i < 8 * NV; ++i) r[i] = fmaf(r[i], x.get(i), res.get(i));
+        } else {
 #pragma unroll
-            for (int i = 0; i < 8 * NV; ++i) r[i] += a[i];
+            for (int i = 0; i < 8 * NV; ++i) r[i] = x.get(i) + res.get(i);
         }
         if (p.r) store_row<NV, VEC>(static_cast<T *>(p.r) + row * p.d, p.d, t, L::G, r);
     }
@@ -152,104 +208,120 @@ __global__ void __launch_bounds__(Rows<WPR>::kThreads)
     s = group_sum<WPR>(s, buf, group);
     if (!live) return;
     const float c = 1.f / sqrtf(s / p.d + p.eps);
-    float w[8 * NV];
-    load_row<NV, VEC>(p.weight, p.d, t, L::G, w);
 #pragma unroll
     for (int i = 0; i < 8 * NV; ++i) w[i] *= r[i] * c;
     store_row<NV, VEC>(static_cast<T *>(p.y) + row * p.d, p.d, t, L::G, w);
 }
 
 // Each group walks over rows first, first + step, ...; its sums of dw (and dscale) go to
-// row `blockIdx.x * kGroups + group` of the partials.
-template <typename T, int WPR, int NV, bool VEC>
-__global__ void __launch_bounds__(Rows<WPR>::kThreads)
+// row `blockIdx.x * kGroups + group` of the partials. All of a row's loads are issued before
+// its reduction: 64 bytes a thread in flight at 2048 threads an SM.
+template <typename T, int WPR, int NV, bool VEC, bool SCALE>
+__global__ void __launch_bounds__(Rows<WPR>::kThreads, NV == 1 ? 1024 / Rows<WPR>::kThreads : 1)
     residual_norm_bwd_kernel(const ResidualNormArgs p, int64_t rounds) {
     using L = Rows<WPR>;
-    __shared__ float buf[2][2][L::kWarps];
+    __shared__ float2 buf[2][L::kWarps];
     const int group = threadIdx.x / L::G, t = threadIdx.x % L::G;
     const int64_t part = (int64_t)blockIdx.x * L::kGroups + group, step = (int64_t)gridDim.x * L::kGroups;
-    float dw[8 * NV], ds[8 * NV], w[8 * NV], a[8 * NV];
+    const float inv_d = 1.f / p.d;
+    // weight and scale wait in shared memory (up to 8192 channels, else they are reloaded
+    // through the cache): 16 registers fewer, which two CTAs of 512 threads need
+    extern __shared__ __align__(16) float params[];
+    const float *weight = p.weight, *scale = p.scale;
+    if constexpr (NV == 1) {
+        for (int i = threadIdx.x; i < p.d; i += L::kThreads) {
+            params[i] = p.weight[i];
+            if constexpr (SCALE) params[p.d + i] = p.scale[i];
+        }
+        weight = params;
+        scale = params + p.d;
+        __syncthreads();
+    }
+    float dw[8 * NV], ds[SCALE ? 8 * NV : 1];
 #pragma unroll
-    for (int i = 0; i < 8 * NV; ++i) dw[i] = ds[i] = 0.f;
-    load_row<NV, VEC>(p.weight, p.d, t, L::G, w);
+    for (int i = 0; i < 8 * NV; ++i) dw[i] = 0.f;
+    if constexpr (SCALE)
+#pragma unroll
+        for (int i = 0; i < 8 * NV; ++i) ds[i] = 0.f;
     for (int64_t i0 = 0; i0 < rounds; ++i0) {
         const int64_t row = part + i0 * step;
         const bool live = row < p.n_rows;
-        float r[8 * NV], dy[8 * NV];
-        float rr = 0.f, tr = 0.f;
+        Held<T, NV, VEC> r, dy, dr;
+        [[maybe_unused]] Held<T, NV, VEC> x;
+        r.clear();
+        dy.clear();
+        dr.clear();
         if (live) {
-            load_row<NV, VEC>(static_cast<const T *>(p.r) + row * p.r_stride, p.d, t, L::G, r);
-            load_row<NV, VEC>(static_cast<const T *>(p.dy) + row * p.dy_stride, p.d, t, L::G, dy);
-#pragma unroll
-            for (int i = 0; i < 8 * NV; ++i) {
-                rr = fmaf(r[i], r[i], rr);
-                tr = fmaf(w[i] * dy[i], r[i], tr);
-            }
+            r.load(static_cast<const T *>(p.r) + row * p.r_stride, p.d, t, L::G);
+            dy.load(static_cast<const T *>(p.dy) + row * p.dy_stride, p.d, t, L::G);
+            if (p.dr) dr.load(static_cast<const T *>(p.dr) + row * p.dr_stride, p.d, t, L::G);
+            if constexpr (SCALE) x.load(static_cast<const T *>(p.x) + row * p.x_stride, p.d, t, L::G);
         }
-        rr = group_sum<WPR>(rr, buf[i0 & 1][0], group);
-        tr = group_sum<WPR>(tr, buf[i0 & 1][1], group);
-        if (!live) continue;
-        const float c = 1.f / sqrtf(rr / p.d + p.eps), m = tr * c * c / p.d;
-        float g[8 * NV];
-        if (p.dr) load_row<NV, VEC>(static_cast<const T *>(p.dr) + row * p.dr_stride, p.d, t, L::G, g);
-        else
-#pragma unroll
-            for (int i = 0; i < 8 * NV; ++i) g[i] = 0.f;
+        float2 sum = make_float2(0.f, 0.f);  // r^2 and w dy r
+        float w[8 * NV];
+        load_row<NV, VEC>(weight, p.d, t, L::G, w);
 #pragma unroll
         for (int i = 0; i < 8 * NV; ++i) {
-            g[i] += c * (w[i] * dy[i] - r[i] * m);
-            dw[i] = fmaf(dy[i] * c, r[i], dw[i]);
+            sum.x = fmaf(r.get(i), r.get(i), sum.x);
+            sum.y = fmaf(w[i] * dy.get(i), r.get(i), sum.y);
+        }
+        sum = group_sum2<WPR>(sum, buf[i0 & 1], group);
+        if (!live) continue;
+        const float c = 1.f / sqrtf(fmaf(sum.x, inv_d, p.eps)), m = sum.y * c * c * inv_d;
+        float g[8 * NV];
+        load_row<NV, VEC>(weight, p.d, t, L::G, w);
+#pragma unroll
+        for (int i = 0; i < 8 * NV; ++i) {
+            g[i] = fmaf(c, fmaf(w[i], dy.get(i), -r.get(i) * m), dr.get(i));
+            dw[i] = fmaf(dy.get(i) * c, r.get(i), dw[i]);
         }
         store_row<NV, VEC>(static_cast<T *>(p.dresidual) + row * p.d, p.d, t, L::G, g);
-        if (p.scale) {
-            load_row<NV, VEC>(static_cast<const T *>(p.x) + row * p.x_stride, p.d, t, L::G, a);
+        if constexpr (SCALE) {
+            load_row<NV, VEC>(scale, p.d, t, L::G, w);
 #pragma unroll
-            for (int i = 0; i < 8 * NV; ++i) ds[i] = fmaf(a[i], g[i], ds[i]);
-            load_row<NV, VEC>(p.scale, p.d, t, L::G, a);
-#pragma unroll
-            for (int i = 0; i < 8 * NV; ++i) a[i] *= g[i];
-            store_row<NV, VEC>(static_cast<T *>(p.dx) + row * p.d, p.d, t, L::G, a);
+            for (int i = 0; i < 8 * NV; ++i) {
+                ds[i] = fmaf(x.get(i), g[i], ds[i]);
+                g[i] *= w[i];
+            }
+            store_row<NV, VEC>(static_cast<T *>(p.dx) + row * p.d, p.d, t, L::G, g);
         }
     }
     store_row<NV, VEC>(p.partial + part * p.d, p.d, t, L::G, dw);
-    if (p.scale) store_row<NV, VEC>(p.partial + (step + part) * p.d, p.d, t, L::G, ds);
+    if constexpr (SCALE) store_row<NV, VEC>(p.partial + (step + part) * p.d, p.d, t, L::G, ds);
 }
 
 // out[c] = sum over the parts of partial[part][c], in a fixed order; blockIdx.y chooses the sum
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(1024)
     sum_parts_kernel(const float *__restrict__ partial, int parts, int d, float *__restrict__ out0,
                      float *__restrict__ out1) {
-    __shared__ float s[16][33];
+    __shared__ float s[32][33];
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), l = threadIdx.x >> 5;
     const float *src = partial + (int64_t)blockIdx.y * parts * d;
     float x = 0.f;
     if (c < d)
-#pragma unroll 4
-        for (int i = l; i < parts; i += 16) x += src[(int64_t)i * d + c];
+#pragma unroll 8
+        for (int i = l; i < parts; i += 32) x += src[(int64_t)i * d + c];
     s[l][threadIdx.x & 31] = x;
     __syncthreads();
-    if (l == 0 && c < d) {
-        x = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x += s[i][threadIdx.x & 31];
-        (blockIdx.y ? out1 : out0)[c] = x;
+    if (blockIdx.x * 32 + l < d) {  // warp l adds up column l
+        x = warp_sum(s[threadIdx.x & 31][l]);
+        if ((threadIdx.x & 31) == 0) (blockIdx.y ? out1 : out0)[blockIdx.x * 32 + l] = x;
     }
 }
 
 constexpr int kSMs = 152;
 
+// warps to a row (a power of two) and 8-channel runs to a thread: one run up to 8192 channels
 struct RowPlan { int wpr, nv; };
 RowPlan row_plan(int d) {
-    if (d <= 256) return {1, 1};
-    if (d <= 512) return {1, 2};
-    int wpr = 2;
-    while (wpr < 32 && 512 * wpr < d) wpr *= 2;
-    return {wpr, 512 * wpr < d ? 4 : 2};
+    int wpr = 1;
+    while (wpr < 32 && 256 * wpr < d) wpr *= 2;
+    return {wpr, 256 * wpr >= d ? 1 : 512 * wpr >= d ? 2 : 4};
 }
 int plan_groups(const RowPlan &r) { return r.wpr < 8 ? 8 / r.wpr : 1; }
 int64_t residual_bwd_grid(int64_t n_rows, int d) {
     const RowPlan r = row_plan(d);
-    const int per_sm = r.wpr <= 8 ? 3 : r.wpr == 16 ? 2 : 1;
+    const int per_sm = r.nv > 1 ? 1 : r.wpr <= 8 ? 4 : 32 / r.wpr;
     return std::max<int64_t>(1, std::min<int64_t>((n_rows + plan_groups(r) - 1) / plan_groups(r), kSMs * per_sm));
 }
 
@@ -263,9 +335,15 @@ cudaError_t residual_run(const ResidualNormArgs &p, bool bwd, cudaStream_t strea
         return cudaGetLastError();
     }
     const int64_t grid = residual_bwd_grid(p.n_rows, p.d), parts = grid * L::kGroups;
-    residual_norm_bwd_kernel<T, WPR, NV, VEC>
-        <<<(unsigned)grid, L::kThreads, 0, stream>>>(p, (p.n_rows + parts - 1) / parts);
-    sum_parts_kernel<<<dim3((p.d + 31) / 32, p.scale ? 2 : 1), 512, 0, stream>>>(p.partial, (int)parts, p.d, p.dw, p.dscale);
+    const int64_t rounds = (p.n_rows + parts - 1) / parts;
+    const int smem = NV == 1 ? p.d * 4 * (p.scale ? 2 : 1) : 0;
+    auto kernel = p.scale ? residual_norm_bwd_kernel<T, WPR, NV, VEC, true> : residual_norm_bwd_kernel<T, WPR, NV, VEC, false>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<(unsigned)grid, L::kThreads, smem, stream>>>(p, rounds);
+    sum_parts_kernel<<<dim3((p.d + 31) / 32, p.scale ? 2 : 1), 1024, 0, stream>>>(p.partial, (int)parts, p.d, p.dw, p.dscale);
     count_launches(2);
     return cudaGetLastError();
 }
@@ -273,15 +351,15 @@ cudaError_t residual_run(const ResidualNormArgs &p, bool bwd, cudaStream_t strea
 template <typename T, bool VEC>
 cudaError_t residual_pick(const ResidualNormArgs &p, bool bwd, cudaStream_t s) {
     const RowPlan r = row_plan(p.d);
-    if (r.nv == 1) return residual_run<T, 1, 1, VEC>(p, bwd, s);
     if (r.nv == 4) return residual_run<T, 32, 4, VEC>(p, bwd, s);
+    if (r.nv == 2) return residual_run<T, 32, 2, VEC>(p, bwd, s);
     switch (r.wpr) {
-        case 1: return residual_run<T, 1, 2, VEC>(p, bwd, s);
-        case 2: return residual_run<T, 2, 2, VEC>(p, bwd, s);
-        case 4: return residual_run<T, 4, 2, VEC>(p, bwd, s);
-        case 8: return residual_run<T, 8, 2, VEC>(p, bwd, s);
-        case 16: return residual_run<T, 16, 2, VEC>(p, bwd, s);
-        default: return residual_run<T, 32, 2, VEC>(p, bwd, s);
+        case 1: return residual_run<T, 1, 1, VEC>(p, bwd, s);
+        case 2: return residual_run<T, 2, 1, VEC>(p, bwd, s);
+        case 4: return residual_run<T, 4, 1, VEC>(p, bwd, s);
+        case 8: return residual_run<T, 8, 1, VEC>(p, bwd, s);
+        case 16: return residual_run<T, 16, 1, VEC>(p, bwd, s);
+        default: return residual_run<T, 32, 1, VEC>(p, bwd, s);
     }
 }
 
@@ -291,28 +369,40 @@ bool vec_ok(const void *p, int64_t stride, int es) {
 
 // ---------------------------------------------------------------- gated norm
 
-// act(z) and act'(z); silu when SILU, else the sigmoid
-template <bool SILU>
+// act(z) and act'(z); silu when SILU, else the sigmoid. FAST (bf16 tensors): the hardware's
+// exponential and quotient, within a few units in 2^-22 of the sigmoid, far below the
+// result's rounding to bf16; with the accurate forms the bf16 kernels are bound by
+// instruction issue instead of HBM.
+template <bool SILU, bool FAST>
 __device__ __forceinline__ void act(float z, float &a, float &da) {
-    const float s = 1.f / (1.f + expf(-z));
+    const float s = FAST ? __fdividef(1.f, 1.f + __expf(-z)) : 1.f / (1.f + expf(-z));
     a = SILU ? z * s : s;
     da = SILU ? s * fmaf(z, 1.f - s, 1.f) : s * (1.f - s);
 }
+
+// row / n_heads for row < 2^31 as a multiplication: (umulhi(row, m) + row) >> s
+struct HeadDiv { uint32_t m, s; };
+HeadDiv head_div(uint32_t d) {
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    return {(uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1), s};
+}
+__device__ __forceinline__ uint32_t divide(uint32_t row, HeadDiv h) { return (__umulhi(row, h.m) + row) >> h.s; }
 
 constexpr int kGatedThreads = 256;
 
 // G threads (a power of two up to a warp) hold a row of d <= 8 G channels.
 template <typename T, int G, bool VEC, bool SILU>
 __global__ void __launch_bounds__(kGatedThreads)
-    gated_norm_fwd_kernel(const GatedNormArgs p) {
+    gated_norm_fwd_kernel(const GatedNormArgs p, const HeadDiv by) {
     const int t = threadIdx.x % G;
     const int64_t row = ((int64_t)blockIdx.x * kGatedThreads + threadIdx.x) / G;
     const bool live = row < p.n_tok * p.n_heads;
-    const int64_t n = row / p.n_heads;
-    const int h = (int)(row - n * p.n_heads);
+    const uint32_t n = divide((uint32_t)row, by), h = (uint32_t)row - n * p.n_heads;
     float x[8], z[8], w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    load_row<1, VEC>(p.weight, p.d, t, G, w);
     if (live) {
         load_row<1, VEC>(static_cast<const T *>(p.x) + n * p.x_stride + (int64_t)h * p.d, p.d, t, G, x);
         load_row<1, VEC>(static_cast<const T *>(p.gate) + n * p.gate_stride + (int64_t)h * p.d, p.d, t, G, z);
@@ -324,23 +414,23 @@ __global__ void __launch_bounds__(kGatedThreads)
     for (int o = G / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (!live) return;
     const float c = 1.f / sqrtf(s / p.d + p.eps);
-    load_row<1, VEC>(p.weight, p.d, t, G, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float a, da;
-        act<SILU>(z[i], a, da);
+        act<SILU, sizeof(T) == 2>(z[i], a, da);
         x[i] = x[i] * c * w[i] * a;
     }
     store_row<1, VEC>(static_cast<T *>(p.y) + row * p.d, p.d, t, G, x);
 }
 
 template <typename T, int G, bool VEC, bool SILU>
-__global__ void __launch_bounds__(kGatedThreads)
-    gated_norm_bwd_kernel(const GatedNormArgs p, int64_t rounds) {
+__global__ void __launch_bounds__(kGatedThreads, 4)
+    gated_norm_bwd_kernel(const GatedNormArgs p, const HeadDiv by, int64_t rounds) {
     constexpr int kGroups = kGatedThreads / G;
     __shared__ float sums[kGatedThreads / 32][8 * G];
     const int t = threadIdx.x % G;
     const int64_t rows = p.n_tok * p.n_heads, step = (int64_t)gridDim.x * kGroups;
+    const float inv_d = 1.f / p.d;
     float w[8], dw[8];
     load_row<1, VEC>(p.weight, p.d, t, G, w);
 #pragma unroll
@@ -352,8 +442,8 @@ __global__ void __launch_bounds__(kGatedThreads)
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = z[i] = dy[i] = 0.f;
         if (live) {
-            const int64_t n = row / p.n_heads;
-            const int64_t h = (row - n * p.n_heads) * p.d;
+            const uint32_t n = divide((uint32_t)row, by);
+            const int64_t h = (int64_t)((uint32_t)row - n * p.n_heads) * p.d;
             load_row<1, VEC>(static_cast<const T *>(p.x) + n * p.x_stride + h, p.d, t, G, x);
             load_row<1, VEC>(static_cast<const T *>(p.gate) + n * p.gate_stride + h, p.d, t, G, z);
             load_row<1, VEC>(static_cast<const T *>(p.dy) + n * p.dy_stride + h, p.d, t, G, dy);
@@ -361,7 +451,7 @@ __global__ void __launch_bounds__(kGatedThreads)
         float xx = 0.f, tx = 0.f, a[8], da[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            act<SILU>(z[i], a[i], da[i]);
+            act<SILU, sizeof(T) == 2>(z[i], a[i], da[i]);
             xx = fmaf(x[i], x[i], xx);
             tx = fmaf(w[i] * a[i] * dy[i], x[i], tx);
         }
@@ -371,7 +461,7 @@ __global__ void __launch_bounds__(kGatedThreads)
             tx += __shfl_xor_sync(0xffffffffu, tx, o);
         }
         if (!live) continue;
-        const float c = 1.f / sqrtf(xx / p.d + p.eps), m = tx * c * c / p.d;
+        const float c = 1.f / sqrtf(fmaf(xx, inv_d, p.eps)), m = tx * c * c * inv_d;
         float dx[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -407,7 +497,7 @@ int gated_group(int d) {
 }
 int64_t gated_bwd_grid(int64_t n_tok, int n_heads, int d) {
     const int per = kGatedThreads / gated_group(d);
-    return std::max<int64_t>(1, std::min<int64_t>((n_tok * n_heads + per - 1) / per, kSMs * 6));
+    return std::max<int64_t>(1, std::min<int64_t>((n_tok * n_heads + per - 1) / per, kSMs * 4));
 }
 
 template <typename T, int G, bool VEC, bool SILU>
@@ -415,13 +505,13 @@ cudaError_t gated_run(const GatedNormArgs &p, bool bwd, cudaStream_t stream) {
     constexpr int kGroups = kGatedThreads / G;
     const int64_t rows = p.n_tok * p.n_heads;
     if (!bwd) {
-        gated_norm_fwd_kernel<T, G, VEC, SILU><<<(unsigned)((rows + kGroups - 1) / kGroups), kGatedThreads, 0, stream>>>(p);
+        gated_norm_fwd_kernel<T, G, VEC, SILU><<<(unsigned)((rows + kGroups - 1) / kGroups), kGatedThreads, 0, stream>>>(p, head_div(p.n_heads));
         count_launches(1);
         return cudaGetLastError();
     }
     const int64_t grid = gated_bwd_grid(p.n_tok, p.n_heads, p.d), step = grid * kGroups;
-    gated_norm_bwd_kernel<T, G, VEC, SILU><<<(unsigned)grid, kGatedThreads, 0, stream>>>(p, (rows + step - 1) / step);
-    sum_parts_kernel<<<dim3((p.d + 31) / 32, 1), 512, 0, stream>>>(p.partial, (int)grid, p.d, p.dw, nullptr);
+    gated_norm_bwd_kernel<T, G, VEC, SILU><<<(unsigned)grid, kGatedThreads, 0, stream>>>(p, head_div(p.n_heads), (rows + step - 1) / step);
+    sum_parts_kernel<<<dim3((p.d + 31) / 32, 1), 1024, 0, stream>>>(p.partial, (int)grid, p.d, p.dw, nullptr);
     count_launches(2);
     return cudaGetLastError();
 }
