@@ -429,7 +429,10 @@ __global__ void __launch_bounds__(kLocalThreads)
             for (int i = 0; i < 2; ++i) {
                 const int r = 2 * lane + i;
                 const double sa = total - (i ? a0 + a[0] : a0), sb = i ? b0 + b[0] : b0;
-                if (r < ch.len) p.dg[(ch.t0 + r) * p.n_heads + head] = (float)((double)whole + sa + sb);
+                if (r < ch.len) {  // nothing passes a decay of 0: what the sums leave there is rounding
+                    const int64_t t = (ch.t0 + r) * p.n_heads + head;
+                    p.dg[t] = p.g[t] < kGFloor ? 0.f : (float)((double)whole + sa + sb);
+                }
             }
         }
         // dQ += B K, dK += B^T Q - (beta F + its transpose) K

@@ -18,6 +18,9 @@ Contents
 
 ``projection``  the gate projection a = x W^T + b (one fp64 matrix product).
 
+``block``       the gated delta rule with one decay per head and the norms around a block,
+                with their gradients.
+
 ``recurrence.decode_step`` is the recurrence on one-token sequences (a decode step).
 """
 from .recurrence import build, kda_forward, oracle_library_path  # noqa: F401
