@@ -15,7 +15,12 @@ import torch
 import chunked_linear_attention_kda_gb300 as _kda
 
 _CODE = {torch.float32: 0, torch.bfloat16: 1}
+_F32, _I32 = torch.float32, torch.int32
 ACTIVATIONS = {"sigmoid": 0, "silu": 1}
+
+# The checks below run on every call, in front of kernels of a few microseconds: they read a
+# tensor's attributes once, compare device indexes, and take the raw stream handle.
+_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _start(t, what):
@@ -24,34 +29,42 @@ def _start(t, what):
         raise ValueError(f"{what} runs on CUDA tensors only (there is no CPU path)")
     if t.dtype not in _CODE:
         raise ValueError(f"{what}: activations must be bfloat16 or float32, got {t.dtype}")
-    return _kda._lib or _kda.load_library(), torch.cuda.current_stream(t.device).cuda_stream
+    dev = t.get_device()
+    return _kda._lib or _kda.load_library(), _stream(dev), dev
 
 
-def _rows(name, t, shape, like):
+def _refuse(name, t, shape, dtype, dev):
+    raise ValueError(f"{name} must be {dtype} with shape {tuple(shape)} on cuda:{dev}, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}")
+
+
+def _rows(name, t, shape, dtype, dev):
     """The distance between tokens of ``t`` ([tokens, ...], a token's row contiguous)."""
-    if t.shape != shape or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} must be {like.dtype} with shape {tuple(shape)} on {like.device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    width = 1
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(name, t, shape, dtype, dev)
+    width = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+    if t.is_contiguous():
+        return width
+    want = 1
     for size, stride in zip(reversed(shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != width:
+        if size != 1 and stride != want:
             raise ValueError(f"{name}: a token's row must be contiguous")
-        width *= size
+        want *= size
     step = t.stride(0)
     if shape[0] > 1 and step < width:
         raise ValueError(f"{name}: tokens may not overlap or run backwards")
     return step if step > width else width
 
 
-def _flat(name, t, shape, dtype, like):
-    if t.shape != shape or t.dtype != dtype or t.device != like.device or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype} with shape {tuple(shape)} on "
-                         f"{like.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t
+def _flat(name, t, shape, dtype, dev):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(name, t, shape, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _p(t):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    return None if t is None else t.data_ptr()  # an empty tensor's is 0
 
 
 def _done(lib, status):
@@ -59,29 +72,36 @@ def _done(lib, status):
         _kda._check(lib, status)
 
 
-def _gdr_inputs(q, k, v, g, beta):
+def _bytes(need, like):
+    """A workspace; None where none is needed."""
+    return torch.empty(need, dtype=torch.uint8, device=like.device)
+
+
+def _gdr_inputs(q, k, v, g, beta, dev):
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q and k must be [N, H_k, d_k], v [N, H, d_v] (packed, token-major)")
-    n, hk, dk = q.shape
-    h, dv = v.shape[1:]
+    shape = q.shape
+    n, hk, dk = shape
+    _, h, dv = v.shape
     if hk == 0 or h % hk != 0:
         raise ValueError(f"v's {h} heads must be a multiple of q's {hk}")
-    strides = (_rows("q", q, (n, hk, dk), q), _rows("k", k, (n, hk, dk), q),
-               _rows("v", v, (n, h, dv), q))
-    _flat("g", g, (n, h), torch.float32, q)
-    _flat("beta", beta, (n, h), torch.float32, q)
+    dtype = q.dtype
+    strides = (_rows("q", q, shape, dtype, dev), _rows("k", k, shape, dtype, dev),
+               _rows("v", v, (n, h, dv), dtype, dev))
+    _flat("g", g, (n, h), _F32, dev)
+    _flat("beta", beta, (n, h), _F32, dev)
     return n, hk, h, dk, dv, strides
 
 
-def _sequences(q, n, h, dk, dv, h0, cu_seqlens):
+def _sequences(q, dev, n, h, dk, dv, h0, cu_seqlens):
     if cu_seqlens is None:
         cu_seqlens = torch.tensor([0, n], dtype=torch.int32, device=q.device)
     n_seq = cu_seqlens.numel() - 1
     if n_seq < 0:
         raise ValueError("cu_seqlens needs at least one entry")
-    _flat("cu_seqlens", cu_seqlens, (n_seq + 1,), torch.int32, q)
+    _flat("cu_seqlens", cu_seqlens, (n_seq + 1,), _I32, dev)
     if h0 is not None:
-        _flat("h0", h0, (n_seq, h, dk, dv), torch.float32, q)
+        _flat("h0", h0, (n_seq, h, dk, dv), _F32, dev)
     return n_seq, cu_seqlens
 
 
@@ -92,21 +112,21 @@ def gdr_chunk_fwd(q, k, v, g, beta, h0=None, cu_seqlens=None, *, out=None, h_fin
     H_k; bf16 or fp32), ``g, beta`` [N, H] fp32, ``h0`` [n_seq, H, d_k, d_v] fp32 or None,
     ``cu_seqlens`` int32 [n_seq + 1] (None: one sequence). Returns ``(out, h_final)``, the
     latter None when ``output_final_state`` is False."""
-    lib, stream = _start(q, "gdr_chunk_fwd")
-    n, hk, h, dk, dv, strides = _gdr_inputs(q, k, v, g, beta)
-    n_seq, cu_seqlens = _sequences(q, n, h, dk, dv, h0, cu_seqlens)
+    lib, stream, dev = _start(q, "gdr_chunk_fwd")
+    n, hk, h, dk, dv, strides = _gdr_inputs(q, k, v, g, beta, dev)
+    n_seq, cu_seqlens = _sequences(q, dev, n, h, dk, dv, h0, cu_seqlens)
     if out is None:
         out = torch.empty((n, h, dv), dtype=q.dtype, device=q.device)
     else:
-        _flat("out", out, (n, h, dv), q.dtype, q)
+        _flat("out", out, (n, h, dv), q.dtype, dev)
     if h_final is not None:
-        _flat("h_final", h_final, (n_seq, h, dk, dv), torch.float32, q)
+        _flat("h_final", h_final, (n_seq, h, dk, dv), _F32, dev)
     elif output_final_state:
         h_final = torch.empty((n_seq, h, dk, dv), dtype=torch.float32, device=q.device)
     code = _CODE[q.dtype]
     if workspace is None:
         need = lib.kda_gdr_chunk_fwd_workspace_bytes(n, n_seq, hk, h, dk, dv, code)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _bytes(need, q)
     _done(lib, lib.kda_gdr_chunk_fwd(
         _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(h0), _p(cu_seqlens), _p(out),
         _p(h_final), _p(workspace), workspace.numel() * workspace.element_size(), n, n_seq, hk,
@@ -119,12 +139,12 @@ def gdr_chunk_bwd(q, k, v, g, beta, h0, cu_seqlens, dout, dh_final=None, *, want
     """Backward of ``gdr_chunk_fwd`` through ``kda_gdr_chunk_bwd``: the gradients of ``<dout,
     out> + <dh_final, h_final>``. Returns ``(dq, dk, dv, dg, dbeta, dh0)`` (``dh0`` None unless
     ``want_dh0``); ``dq`` and ``dk`` are summed over the value heads of a key head."""
-    lib, stream = _start(q, "gdr_chunk_bwd")
-    n, hk, h, dk, dv, strides = _gdr_inputs(q, k, v, g, beta)
-    n_seq, cu_seqlens = _sequences(q, n, h, dk, dv, h0, cu_seqlens)
-    _flat("dout", dout, (n, h, dv), q.dtype, q)
+    lib, stream, dev = _start(q, "gdr_chunk_bwd")
+    n, hk, h, dk, dv, strides = _gdr_inputs(q, k, v, g, beta, dev)
+    n_seq, cu_seqlens = _sequences(q, dev, n, h, dk, dv, h0, cu_seqlens)
+    _flat("dout", dout, (n, h, dv), q.dtype, dev)
     if dh_final is not None:
-        _flat("dh_final", dh_final, (n_seq, h, dk, dv), torch.float32, q)
+        _flat("dh_final", dh_final, (n_seq, h, dk, dv), _F32, dev)
     grads = (torch.empty((n, hk, dk), dtype=q.dtype, device=q.device),
              torch.empty((n, hk, dk), dtype=q.dtype, device=q.device),
              torch.empty((n, h, dv), dtype=q.dtype, device=q.device),
@@ -135,7 +155,7 @@ def gdr_chunk_bwd(q, k, v, g, beta, h0, cu_seqlens, dout, dh_final=None, *, want
     code = _CODE[q.dtype]
     if workspace is None:
         need = lib.kda_gdr_chunk_bwd_workspace_bytes(n, n_seq, hk, h, dk, dv, code)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _bytes(need, q)
     _done(lib, lib.kda_gdr_chunk_bwd(
         _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(h0), _p(cu_seqlens), _p(dout),
         _p(dh_final), *[_p(t) for t in grads], _p(workspace),
@@ -148,15 +168,15 @@ def gdr_step(q, k, v, g, beta, state, slots=None, *, out=None):
     (``state`` [n_slots, H, d_k, d_v] fp32; ``slots`` int32 [B], None: row b has state b). A
     slot outside the pool marks a padded row: its output is 0. The other tensors as for
     ``gdr_chunk_fwd`` with B tokens. Returns ``out`` [B, H, d_v]."""
-    lib, stream = _start(q, "gdr_step")
-    n, hk, h, dk, dv, strides = _gdr_inputs(q, k, v, g, beta)
-    _flat("state", state, (state.shape[0], h, dk, dv), torch.float32, q)
+    lib, stream, dev = _start(q, "gdr_step")
+    n, hk, h, dk, dv, strides = _gdr_inputs(q, k, v, g, beta, dev)
+    _flat("state", state, (state.shape[0], h, dk, dv), _F32, dev)
     if slots is not None:
-        _flat("slots", slots, (n,), torch.int32, q)
+        _flat("slots", slots, (n,), _I32, dev)
     if out is None:
         out = torch.empty((n, h, dv), dtype=q.dtype, device=q.device)
     else:
-        _flat("out", out, (n, h, dv), q.dtype, q)
+        _flat("out", out, (n, h, dv), q.dtype, dev)
     _done(lib, lib.kda_gdr_step(
         _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(state), _p(slots), _p(out), n,
         state.shape[0], hk, h, dk, dv, _CODE[q.dtype], stream))
@@ -168,24 +188,24 @@ def residual_norm_fwd(x, weight, residual=None, scale=None, *, eps=1e-6, out=Non
     """``r = residual + scale * x`` and ``y = weight * r / sqrt(mean(r^2) + eps)`` through
     ``kda_residual_norm_fwd``: ``x, residual`` [N, d] bf16 or fp32, ``weight, scale`` [d] fp32.
     Returns ``(y, r)``; with neither residual nor scale ``r`` is ``x`` itself."""
-    lib, stream = _start(x, "residual_norm_fwd")
+    lib, stream, dev = _start(x, "residual_norm_fwd")
     if x.dim() != 2:
         raise ValueError("x must be [N, d]")
     n, d = x.shape
-    xs = _rows("x", x, (n, d), x)
-    _flat("weight", weight, (d,), torch.float32, x)
+    xs = _rows("x", x, (n, d), x.dtype, dev)
+    _flat("weight", weight, (d,), _F32, dev)
     if scale is not None:
-        _flat("scale", scale, (d,), torch.float32, x)
-    rs = 0 if residual is None else _rows("residual", residual, (n, d), x)
+        _flat("scale", scale, (d,), _F32, dev)
+    rs = 0 if residual is None else _rows("residual", residual, (n, d), x.dtype, dev)
     same = residual is None and scale is None and residual_out is None
     if residual_out is not None:
-        _flat("residual_out", residual_out, (n, d), x.dtype, x)
+        _flat("residual_out", residual_out, (n, d), x.dtype, dev)
     elif not same:
         residual_out = torch.empty((n, d), dtype=x.dtype, device=x.device)
     if out is None:
         out = torch.empty((n, d), dtype=x.dtype, device=x.device)
     else:
-        _flat("out", out, (n, d), x.dtype, x)
+        _flat("out", out, (n, d), x.dtype, dev)
     _done(lib, lib.kda_residual_norm_fwd(_p(x), xs, _p(residual), rs, _p(scale), _p(weight),
                                          _p(residual_out), _p(out), n, d, eps, _CODE[x.dtype],
                                          stream))
@@ -197,25 +217,25 @@ def residual_norm_bwd(dy, r, weight, dr=None, x=None, scale=None, *, eps=1e-6, w
     ``dy`` the gradient of y, ``dr`` the one that reaches r from elsewhere (None: zero), ``x``
     needed with a ``scale`` only. Returns ``(dx, dresidual, dweight, dscale)``; without a scale
     ``dx`` is ``dresidual`` and ``dscale`` None."""
-    lib, stream = _start(r, "residual_norm_bwd")
+    lib, stream, dev = _start(r, "residual_norm_bwd")
     if r.dim() != 2:
         raise ValueError("r must be [N, d]")
     n, d = r.shape
-    ss = [_rows("dy", dy, (n, d), r), 0 if dr is None else _rows("dr", dr, (n, d), r),
-          _rows("r", r, (n, d), r), 0]
-    _flat("weight", weight, (d,), torch.float32, r)
+    ss = [_rows("dy", dy, (n, d), r.dtype, dev), 0 if dr is None else _rows("dr", dr, (n, d), r.dtype, dev),
+          _rows("r", r, (n, d), r.dtype, dev), 0]
+    _flat("weight", weight, (d,), _F32, dev)
     if scale is not None:
-        _flat("scale", scale, (d,), torch.float32, r)
+        _flat("scale", scale, (d,), _F32, dev)
         if x is None:
             raise ValueError("a scale's gradient needs x")
-        ss[3] = _rows("x", x, (n, d), r)
+        ss[3] = _rows("x", x, (n, d), r.dtype, dev)
     dres = torch.empty((n, d), dtype=r.dtype, device=r.device)
     dw = torch.empty(d, dtype=torch.float32, device=r.device)
     dx = None if scale is None else torch.empty_like(dres)
     ds = None if scale is None else torch.empty_like(dw)
     if workspace is None:
         need = lib.kda_residual_norm_bwd_workspace_bytes(n, d, scale is not None)
-        workspace = torch.empty(need, dtype=torch.uint8, device=r.device)
+        workspace = _bytes(need, r)
     _done(lib, lib.kda_residual_norm_bwd(
         _p(dy), ss[0], _p(dr), ss[1], _p(r), ss[2], None if scale is None else _p(x), ss[3],
         _p(scale), _p(weight), _p(dx), _p(dres), _p(ds), _p(dw), _p(workspace),
@@ -223,26 +243,26 @@ def residual_norm_bwd(dy, r, weight, dr=None, x=None, scale=None, *, eps=1e-6, w
     return (dres if scale is None else dx), dres, dw, ds
 
 
-def _gated_inputs(x, gate, weight, activation):
+def _gated_inputs(x, gate, weight, activation, dev):
     if x.dim() != 3:
         raise ValueError("x must be [N, H, d]")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
-    _flat("weight", weight, (x.shape[2],), torch.float32, x)
-    return _rows("x", x, x.shape, x), _rows("gate", gate, x.shape, x)
+    _flat("weight", weight, (x.shape[2],), _F32, dev)
+    return _rows("x", x, x.shape, x.dtype, dev), _rows("gate", gate, x.shape, x.dtype, dev)
 
 
 def gated_norm_fwd(x, gate, weight, *, eps=1e-6, activation="sigmoid", out=None):
     """``y = weight * x / sqrt(mean(x^2) + eps) * act(gate)`` per token and head through
     ``kda_gated_norm_fwd``: ``x, gate`` [N, H, d] bf16 or fp32, ``weight`` [d] fp32,
     ``activation`` "sigmoid" or "silu". Returns ``y`` [N, H, d]."""
-    lib, stream = _start(x, "gated_norm_fwd")
-    xs, gs = _gated_inputs(x, gate, weight, activation)
+    lib, stream, dev = _start(x, "gated_norm_fwd")
+    xs, gs = _gated_inputs(x, gate, weight, activation, dev)
     n, h, d = x.shape
     if out is None:
         out = torch.empty((n, h, d), dtype=x.dtype, device=x.device)
     else:
-        _flat("out", out, (n, h, d), x.dtype, x)
+        _flat("out", out, (n, h, d), x.dtype, dev)
     _done(lib, lib.kda_gated_norm_fwd(_p(x), xs, _p(gate), gs, _p(weight), _p(out), n, h, d, eps,
                                       ACTIVATIONS[activation], _CODE[x.dtype], stream))
     return out
@@ -250,16 +270,16 @@ def gated_norm_fwd(x, gate, weight, *, eps=1e-6, activation="sigmoid", out=None)
 
 def gated_norm_bwd(dy, x, gate, weight, *, eps=1e-6, activation="sigmoid", workspace=None):
     """Gradients of ``gated_norm_fwd`` through ``kda_gated_norm_bwd``: ``(dx, dgate, dweight)``."""
-    lib, stream = _start(x, "gated_norm_bwd")
-    xs, gs = _gated_inputs(x, gate, weight, activation)
-    ys = _rows("dy", dy, x.shape, x)
+    lib, stream, dev = _start(x, "gated_norm_bwd")
+    xs, gs = _gated_inputs(x, gate, weight, activation, dev)
+    ys = _rows("dy", dy, x.shape, x.dtype, dev)
     n, h, d = x.shape
     dx = torch.empty((n, h, d), dtype=x.dtype, device=x.device)
     dgate = torch.empty_like(dx)
     dw = torch.empty(d, dtype=torch.float32, device=x.device)
     if workspace is None:
         need = lib.kda_gated_norm_bwd_workspace_bytes(n, h, d)
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _bytes(need, x)
     _done(lib, lib.kda_gated_norm_bwd(
         _p(dy), ys, _p(x), xs, _p(gate), gs, _p(weight), _p(dx), _p(dgate), _p(dw),
         _p(workspace), workspace.numel() * workspace.element_size(), n, h, d, eps,
