@@ -21,7 +21,10 @@ namespace kda {
 namespace gdr {
 
 constexpr int C = 64;           // tokens of a chunk
-constexpr int kTile = C * C;    // elements of a chunk's square tile
+// A chunk's 64 x 64 lower triangular tile as its ten 16 x 16 blocks on and below the diagonal,
+// row after row of blocks, a block's rows of 32 bytes swizzled
+constexpr int kTri = 10 * 512;  // bytes of one bf16 plane
+__host__ __device__ constexpr int tri_block(int I, int J) { return (I * (I + 1) / 2 + J) * 512; }
 constexpr float kGFloor = -200.f;
 
 // ---------------------------------------------------------------- workspace
@@ -50,12 +53,11 @@ __device__ __forceinline__ Chunk find_chunk(const int32_t *cu, int n_seq, int64_
     return {lo, left <= 0 ? 0 : left < C ? (int)left : C, t0};
 }
 
-// Per (slot, value head): X and P tile images (NS planes each, swizzled as the kernels read
-// them) and the gate vectors gamma, delta, beta, Gamma (repeated) and the running sum of
+// Per (slot, value head): X and P (NS triangular planes each) and the gate vectors gamma, delta, beta, Gamma (repeated) and the running sum of
 // g log2(e) as pairs of floats. The chains read the first four.
 constexpr int kGateFloats = 6 * C, kChainGates = 4 * C;
 __host__ __device__ constexpr size_t terms_bytes(int ns) {
-    return (size_t)2 * ns * kTile * 2 + kGateFloats * 4;
+    return (size_t)2 * ns * kTri + kGateFloats * 4;
 }
 
 // Per (slot, value head) of the backward pass, behind the terms: S0^T and dS1^T (value
@@ -258,41 +260,41 @@ __device__ __forceinline__ void load_key_tile(uint32_t dst, const T *src, int64_
     for (int h = 0; h < DKP / 64; ++h)
         load_tile<T, 128>(dst + h * kHalf, C * DKP * 2, src + h * 64, stride, rows, cols - h * 64, vec, tid, nthreads);
 }
-// The image of a chunk's value tile: slices of 32 channels, each NI planes of 64 rows of 64
-// bytes in the tensor copy's 64-byte swizzle.
+// The images of `heads` neighbouring value tiles of a chunk (vb bytes apart): slices of 32
+// channels, each NI planes of 64 rows of 64 bytes in the tensor copy's 64-byte swizzle.
 template <typename T>
-__device__ __forceinline__ void write_value_image(char *dst, const T *src, int64_t stride, int rows, int cols,
-                                                  int tid, int nthreads) {
+__device__ __forceinline__ void write_value_images(char *dst, size_t vb, const T *src, int64_t stride, int heads,
+                                                   int rows, int cols, int tid, int nthreads) {
     constexpr int NI = InputPlanes<T>::N, plane = C * 64;
-    const int slices = pad_v(cols) / 32;
+    const int per = pad_v(cols) / 32 * C * 4;
     const bool vec = sizeof(T) == 2 && cols % 8 == 0 && ((uintptr_t)src & 15) == 0 && (stride & 7) == 0;
 #pragma unroll 4
-    for (int i = tid; i < slices * C * 4; i += nthreads) {
-        const int sl = i / (C * 4), r = (i >> 2) % C, c = (i & 3) * 8;
+    for (int i = tid; i < heads * per; i += nthreads) {
+        const int head = i / per, k = i - head * per;
+        const int sl = k / (C * 4), r = (k >> 2) % C, c = (k & 3) * 8, col = sl * 32 + c;
+        const T *p = src + r * stride + head * cols + col;
+        char *at = dst + head * vb + sl * NI * plane + tile_off<64>(r, c);
+        const bool in = r < rows && col < cols;
         if (vec) {
             uint4 x = make_uint4(0, 0, 0, 0);
-            if (r < rows && sl * 32 + c < cols) x = *reinterpret_cast<const uint4 *>(src + r * stride + sl * 32 + c);
-            *reinterpret_cast<uint4 *>(dst + sl * plane + tile_off<64>(r, c)) = x;
+            if (in) x = *reinterpret_cast<const uint4 *>(p);
+            *reinterpret_cast<uint4 *>(at) = x;
             continue;
         }
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = in && col + j < cols ? (float)p[j] : 0.f;
         uint32_t w[NI][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float x[2];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const int col = sl * 32 + c + 2 * j + y;
-                x[y] = r < rows && col < cols ? (float)src[r * stride + col] : 0.f;
-            }
             uint32_t s[NI];
-            split2<NI>(x[0], x[1], s);
+            split2<NI>(x[2 * j], x[2 * j + 1], s);
 #pragma unroll
             for (int q = 0; q < NI; ++q) w[q][j] = s[q];
         }
 #pragma unroll
         for (int q = 0; q < NI; ++q)
-            *reinterpret_cast<uint4 *>(dst + (sl * NI + q) * plane + tile_off<64>(r, c)) =
-                make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+            *reinterpret_cast<uint4 *>(at + q * plane) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
     }
 }
 // `bytes` (a multiple of 16) from the workspace, as they lie

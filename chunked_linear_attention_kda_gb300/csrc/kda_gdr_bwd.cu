@@ -40,7 +40,8 @@ __global__ void __launch_bounds__(kChainThreads)
 }
 
 // ---------------------------------------------------------------- local gradients
-constexpr int kLocalThreads = 256;
+constexpr int kLocalThreads = 512;
+constexpr int kCols = kLocalThreads / 128;  // column parts: a warp has 16 tokens x 1 / kCols of the columns
 
 template <int NI, int DKP, int NS>
 struct LocalSmem {
@@ -50,17 +51,25 @@ struct LocalSmem {
     static constexpr int dO = 0, V = dO + NI * kIn, U = V + (NI == 1 ? kIn : 0),  // fp32 V is read in place
                           E = U + NS * kVal, S = E + NS * kVal;
     static constexpr int dS = S + NS * kState, kSlice = dS + NS * kState;
-    static constexpr int B = 0, F = NI * kTile * 2;  // over the first slice buffer, once the slices are done
-    static_assert(2 * NI * kTile * 2 <= kSlice, "B and F fit a slice buffer");
+    static constexpr int kTile = C * C * 2;  // bytes of a plane of B and F
+    static constexpr int B = 0, F = NI * kTile;  // over the first slice buffer, once the slices are done
+    static_assert(2 * NI * kTile <= kSlice, "B and F fit a slice buffer");
     static constexpr int K = kStages * kSlice, Q = K + NI * kPlane, Pair = Q + NI * kPlane;
-    static constexpr int Gate = Pair + 2 * kTile * 4, Red = Gate + kGateFloats * 4;
-    // Red: [2][64] row sums of q.x, k.x, k.x, F k.k, M over the column halves; [64] E.V;
-    // [4][64] column sums of M over the row blocks; [8] the warps' parts of <S0, dS1>
-    static constexpr int kRed = 5 * 2 * C + C + 4 * C + 8;
+    static constexpr int Gate = Pair + 2 * C * C * 4, Red = Gate + kGateFloats * 4;
+    // Red: [kCols][64] row sums of q.x, k.x, k.x, F k.k, M over the column parts; [64] E.V;
+    // [4][64] column sums of M over the row blocks; the warps' parts of <S0, dS1>
+    static constexpr int kRed = 5 * kCols * C + C + 4 * C + kLocalThreads / 32;
     static constexpr int kBytes = Red + kRed * 4;
     static_assert(kBytes <= 227 * 1024, "fits an SM");
 };
 
+// a row's sum over the column parts
+__device__ __forceinline__ float parts(const float *x, int r) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) s += x[i * C + r];
+    return s;
+}
 __device__ __forceinline__ float quad_sum(float x) {
     x += __shfl_xor_sync(0xffffffffu, x, 1);
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
@@ -71,11 +80,12 @@ __global__ void __launch_bounds__(kLocalThreads)
     gdr_local_kernel(const GdrArgs p, float scale, bool vec_qk, bool vec_v, bool vec_do, bool wide_k, bool wide_v) {
     constexpr int NI = InputPlanes<T>::N;
     using L = LocalSmem<NI, DKP, NS>;
-    constexpr int RB = DKP * 2, NH = DKP / 32;  // NH: 16-column steps of half the key channels
+    constexpr int RB = DKP * 2, KC = DKP / kCols, NH = KC / 16;  // a warp's key channels, in steps of 16
+    constexpr int PC = C / kCols, NP = PC / 16;              // its columns of the 64 x 64 products
     extern __shared__ __align__(128) char smem[];
     const uint32_t base = ptx::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
-    const int wr = warp & 3, wc = warp >> 2;  // token rows 16 wr .., half wc of the columns
+    const int wr = warp & 3, wc = warp >> 2;  // token rows 16 wr .., column part wc
     const int64_t slot = blockIdx.x;
     const Chunk ch = find_chunk(p.cu_seqlens, p.n_seq, slot);
     if (ch.len == 0) return;
@@ -85,8 +95,8 @@ __global__ void __launch_bounds__(kLocalThreads)
     float *pair = reinterpret_cast<float *>(smem + L::Pair);
     float *gate = reinterpret_cast<float *>(smem + L::Gate);
     float *red = reinterpret_cast<float *>(smem + L::Red);
-    float *r_qx = red, *r_kx = red + 2 * C, *r_ku = red + 4 * C, *r_fk = red + 6 * C, *r_m = red + 8 * C;
-    float *r_ev = red + 10 * C, *c_m = red + 11 * C, *r_ss = red + 15 * C;
+    float *r_qx = red, *r_kx = r_qx + kCols * C, *r_ku = r_kx + kCols * C, *r_fk = r_ku + kCols * C;
+    float *r_m = r_fk + kCols * C, *r_ev = r_m + kCols * C, *c_m = r_ev + C, *r_ss = c_m + 4 * C;
 
     auto load = [&](int step) {  // slice `step % n_sl` of value head `step / n_sl`
         const int head = kh * group + step / n_sl, sl = step % n_sl;
@@ -117,11 +127,11 @@ __global__ void __launch_bounds__(kLocalThreads)
     cp_async_wait<1>();
     __syncthreads();
 
-    // q_r.k_j and k_r.k_j of rows 16 wr .., columns 32 wc .., kept by each thread for itself
+    // q_r.k_j and k_r.k_j of rows 16 wr .., columns PC wc .., kept by each thread for itself
     {
-        float kk[4][4], qk[4][4];
+        float kk[2 * NP][4], qk[2 * NP][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < 2 * NP; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) kk[n][i] = qk[n][i] = 0.f;
 #pragma unroll 1
@@ -133,12 +143,12 @@ __global__ void __launch_bounds__(kLocalThreads)
                 key_a(base + L::Q + q * L::kPlane, wr * 16, c, aq[q]);
             }
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-                if (2 * wc + n <= wr)
+            for (int n = 0; n < NP; ++n)
+                if (NP * wc + n <= wr)
 #pragma unroll
                     for (int pb = 0; pb < NI; ++pb) {
                         uint32_t b[4];
-                        key_b(base + L::K + pb * L::kPlane, wc * 32 + n * 16, c, b);
+                        key_b(base + L::K + pb * L::kPlane, wc * PC + n * 16, c, b);
 #pragma unroll
                         for (int pa = 0; pa + pb < NI; ++pa) {
                             ptx::mma16816(kk[2 * n], ak[pa], b[0], b[1]);
@@ -149,15 +159,15 @@ __global__ void __launch_bounds__(kLocalThreads)
                     }
         }
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < 2 * NP; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 pair[(n * 4 + i) * kLocalThreads + tid] = kk[n][i];
-                pair[(16 + n * 4 + i) * kLocalThreads + tid] = qk[n][i];
+                pair[(8 * NP + n * 4 + i) * kLocalThreads + tid] = qk[n][i];
             }
     }
 
-    float dq[2 * NH][4], dk[2 * NH][4];  // this warp's rows, its half of the key channels
+    float dq[2 * NH][4], dk[2 * NH][4];  // this warp's rows and key channels
 #pragma unroll
     for (int n = 0; n < 2 * NH; ++n)
 #pragma unroll
@@ -165,19 +175,19 @@ __global__ void __launch_bounds__(kLocalThreads)
 
     for (int hh = 0; hh < group; ++hh) {
         const int head = kh * group + hh;
-        float xq[2 * NH][4], xk[2 * NH][4], xu[2 * NH][4], ou[4][4], eu[4][4];
+        float xq[2 * NH][4], xk[2 * NH][4], xu[2 * NH][4], ou[2 * NP][4], eu[2 * NP][4];
 #pragma unroll
         for (int n = 0; n < 2 * NH; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) xq[n][i] = xk[n][i] = xu[n][i] = 0.f;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < 2 * NP; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) ou[n][i] = eu[n][i] = 0.f;
         float ev[2] = {0.f, 0.f}, ss = 0.f;
         for (int i = tid; i < kGateFloats; i += kLocalThreads)
             gate[i] = reinterpret_cast<const float *>(ws + (slot * p.n_heads + head) * terms_bytes(NS) +
-                                                      (size_t)2 * NS * kTile * 2)[i];
+                                                      2 * NS * kTri)[i];
 
         for (int sl = 0; sl < n_sl; ++sl) {
             const int step = hh * n_sl + sl;
@@ -240,7 +250,7 @@ __global__ void __launch_bounds__(kLocalThreads)
                         }
                         ev[i & 1] = fmaf(x0, z0, fmaf(x1, z1, ev[i & 1]));
                     }
-                } else {  // dV = beta E
+                } else if (wc == 1) {  // dV = beta E
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float x0 = 0.f, x1 = 0.f;
@@ -260,8 +270,8 @@ __global__ void __launch_bounds__(kLocalThreads)
 #pragma unroll
                     for (int pb = 0; pb < NS; ++pb) {
                         uint32_t b[4], d[4];
-                        frag_b_t<RB>(s + L::S + pb * L::kState, kx * 16, wc * (DKP / 2) + n * 16, b);
-                        frag_b_t<RB>(s + L::dS + pb * L::kState, kx * 16, wc * (DKP / 2) + n * 16, d);
+                        frag_b_t<RB>(s + L::S + pb * L::kState, kx * 16, wc * KC + n * 16, b);
+                        frag_b_t<RB>(s + L::dS + pb * L::kState, kx * 16, wc * KC + n * 16, d);
 #pragma unroll
                         for (int pa = 0; pa + pb < NS; ++pa) {
                             if (pa < NI) {
@@ -276,12 +286,12 @@ __global__ void __launch_bounds__(kLocalThreads)
                     }
                 // dO U^T, E U^T
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    if (2 * wc + n <= wr)
+                for (int n = 0; n < NP; ++n)
+                    if (NP * wc + n <= wr)
 #pragma unroll
                         for (int pb = 0; pb < NS; ++pb) {
                             uint32_t b[4];
-                            frag_b_t<128>(s + L::U + pb * L::kVal, kx * 16, wc * 32 + n * 16, b);
+                            frag_b_t<128>(s + L::U + pb * L::kVal, kx * 16, wc * PC + n * 16, b);
 #pragma unroll
                             for (int pa = 0; pa + pb < NS; ++pa) {
                                 if (pa < NI) {
@@ -305,7 +315,7 @@ __global__ void __launch_bounds__(kLocalThreads)
             for (int n = 0; n < 2 * NH; ++n)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t at = key_off(wr * 16 + gr + 8 * h, wc * (DKP / 2) + n * 8 + tq * 2);
+                    const uint32_t at = key_off(wr * 16 + gr + 8 * h, wc * KC + n * 8 + tq * 2);
                     float k0 = 0.f, k1 = 0.f, q0 = 0.f, q1 = 0.f;
 #pragma unroll
                     for (int q = 0; q < NI; ++q) {
@@ -341,9 +351,9 @@ __global__ void __launch_bounds__(kLocalThreads)
         {
             float fk[2] = {0.f, 0.f}, mr[2] = {0.f, 0.f};
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
+            for (int n = 0; n < 2 * NP; ++n) {
                 float mc[2] = {0.f, 0.f};
-                const int j = wc * 32 + n * 8 + tq * 2;
+                const int j = wc * PC + n * 8 + tq * 2;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int r = wr * 16 + gr + 8 * h;
@@ -351,7 +361,7 @@ __global__ void __launch_bounds__(kLocalThreads)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float kk = pair[(n * 4 + 2 * h + i) * kLocalThreads + tid];
-                        const float qk = pair[(16 + n * 4 + 2 * h + i) * kLocalThreads + tid];
+                        const float qk = pair[(8 * NP + n * 4 + 2 * h + i) * kLocalThreads + tid];
                         const float d = (G2[r].x - G2[j + i].x) + (G2[r].y - G2[j + i].y);
                         const float e = j + i <= r ? ex2(d) : 0.f;
                         bv[i] = j + i <= r ? scale * e * ou[n][2 * h + i] : 0.f;
@@ -367,8 +377,8 @@ __global__ void __launch_bounds__(kLocalThreads)
                     split2<NI>(fv[0], fv[1], wf);
 #pragma unroll
                     for (int q = 0; q < NI; ++q) {
-                        *reinterpret_cast<uint32_t *>(smem + L::B + q * kTile * 2 + tile_off<128>(r, j)) = wb[q];
-                        char *ft = smem + L::F + q * kTile * 2;
+                        *reinterpret_cast<uint32_t *>(smem + L::B + q * L::kTile + tile_off<128>(r, j)) = wb[q];
+                        char *ft = smem + L::F + q * L::kTile;
                         if (j < r) {  // (r, j) and, below the diagonal, (r, j + 1) with their mirror images
                             *reinterpret_cast<uint16_t *>(ft + tile_off<128>(r, j)) = (uint16_t)wf[q];
                             *reinterpret_cast<uint16_t *>(ft + tile_off<128>(j, r)) = (uint16_t)wf[q];
@@ -404,17 +414,17 @@ __global__ void __launch_bounds__(kLocalThreads)
             double a[2], b[2];
             float whole = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) whole += r_ss[i];
+            for (int i = 0; i < kLocalThreads / 32; ++i) whole += r_ss[i];
             whole *= gate[3 * C];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = 2 * lane + i;
-                const float kx = r_kx[r] + r_kx[C + r];
+                const float kx = parts(r_kx, r);
                 if (r < ch.len)
-                    p.dbeta[(ch.t0 + r) * p.n_heads + head] = r_ev[r] - gam[r] * kx - (r_fk[r] + r_fk[C + r]);
-                a[i] = (double)(gam[r] * (scale * (r_qx[r] + r_qx[C + r]) - bet[r] * kx)) + (double)(r_m[r] + r_m[C + r]) -
+                    p.dbeta[(ch.t0 + r) * p.n_heads + head] = r_ev[r] - gam[r] * kx - parts(r_fk, r);
+                a[i] = (double)(gam[r] * (scale * parts(r_qx, r) - bet[r] * kx)) + (double)parts(r_m, r) -
                        (double)((c_m[r] + c_m[C + r]) + (c_m[2 * C + r] + c_m[3 * C + r]));
-                b[i] = del[r] * (r_ku[r] + r_ku[C + r]);
+                b[i] = del[r] * parts(r_ku, r);
             }
             // inclusive sums over the tokens of a and b
             double ra = a[0] + a[1], rb = b[0] + b[1];
@@ -441,17 +451,17 @@ __global__ void __launch_bounds__(kLocalThreads)
             uint32_t ab[NI][4], at[NI][4], af[NI][4];
 #pragma unroll
             for (int q = 0; q < NI; ++q) {
-                frag_a<128>(base + L::B + q * kTile * 2, wr * 16, kx * 16, ab[q]);
-                frag_a_t<128>(base + L::B + q * kTile * 2, kx * 16, wr * 16, at[q]);
-                frag_a<128>(base + L::F + q * kTile * 2, wr * 16, kx * 16, af[q]);
+                frag_a<128>(base + L::B + q * L::kTile, wr * 16, kx * 16, ab[q]);
+                frag_a_t<128>(base + L::B + q * L::kTile, kx * 16, wr * 16, at[q]);
+                frag_a<128>(base + L::F + q * L::kTile, wr * 16, kx * 16, af[q]);
             }
 #pragma unroll
             for (int n = 0; n < NH; ++n)
 #pragma unroll
                 for (int pb = 0; pb < NI; ++pb) {
                     uint32_t b[4], d[4];
-                    key_b_t(base + L::K + pb * L::kPlane, kx * 16, wc * (DKP / 2) + n * 16, b);
-                    key_b_t(base + L::Q + pb * L::kPlane, kx * 16, wc * (DKP / 2) + n * 16, d);
+                    key_b_t(base + L::K + pb * L::kPlane, kx * 16, wc * KC + n * 16, b);
+                    key_b_t(base + L::Q + pb * L::kPlane, kx * 16, wc * KC + n * 16, d);
 #pragma unroll
                     for (int pa = 0; pa + pb < NI; ++pa) {
                         ptx::mma16816(dq[2 * n], ab[pa], b[0], b[1]);
@@ -472,7 +482,7 @@ __global__ void __launch_bounds__(kLocalThreads)
     for (int n = 0; n < 2 * NH; ++n)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int r = wr * 16 + gr + 8 * h, c = wc * (DKP / 2) + n * 8 + tq * 2;
+            const int r = wr * 16 + gr + 8 * h, c = wc * KC + n * 8 + tq * 2;
             if (r < ch.len && c < p.d_k) {
                 const size_t at = ((ch.t0 + r) * p.n_k_heads + kh) * p.d_k + c;
                 put2(static_cast<T *>(p.dq) + at, dq[n][2 * h], dq[n][2 * h + 1], wide_k, c + 1 < p.d_k);

@@ -50,6 +50,13 @@ __device__ __forceinline__ bool wait_bar(uint32_t a, uint32_t parity) {
         }
     }
 }
+// whether the phase is complete, without waiting
+__device__ __forceinline__ bool test_bar(uint32_t a, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok) : "r"(a), "r"(parity) : "memory");
+    return ok != 0;
+}
 // every lane of a warp waits; all leave with the same answer
 __device__ __forceinline__ bool warp_wait(uint32_t a, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_bar(a, parity));
@@ -83,16 +90,16 @@ template <int NI, int DKP, int NS, Mode M>
 struct ChainSmem {
     static constexpr bool kOut = M == Mode::kForward, kRev = M == Mode::kReverse;
     static constexpr int kKey = NI * C * DKP * 2, kVal = NI * C * kBlockV * 2;
-    static constexpr int kX = NS * kTile * 2;
-    static constexpr int kP = (kOut ? NI : NS) * kTile * 2;       // the output takes P in bf16 for bf16
+    static constexpr int kX = NS * kTri;
+    static constexpr int kP = (kOut ? NI : NS) * kTri;       // the output takes P in bf16 for bf16
     static constexpr int kGate = kChainGates * 4;
     // ring 1
     static constexpr int K = 0, V = K + kKey, X = V + (kRev ? 0 : kVal), Gate1 = X + kX;
-    static constexpr int kStage1 = Gate1 + kGate;
+    static constexpr int kStage1 = (Gate1 + kGate + 1023) / 1024 * 1024;
     static constexpr int N1 = NS == 2 ? (kRev ? 2 : 3) : 1;
     // ring 2
     static constexpr int Q = 0, dO = Q + kKey, P = dO + (kRev ? kVal : 0), Gate2 = P + kP;
-    static constexpr int kStage2 = Gate2 + kGate;
+    static constexpr int kStage2 = (Gate2 + kGate + 1023) / 1024 * 1024;
     static constexpr int N2 = M == Mode::kStates ? 0 : NS == 2 ? 2 : 1;
     // per pair
     static constexpr int NH = kOut && NS == 2 ? 2 : 1;            // buffers of Sx and Uo
@@ -107,7 +114,7 @@ struct ChainSmem {
     static constexpr int kBars = 2 * N1 + 2 * N2 + 4 * NH;
     static constexpr int kBytes = Bars + 8 * kBars + 1024;        // the base is rounded up to 1024
     static_assert(kBytes <= 226 * 1024, "fits an SM");
-    static_assert(kStage1 % 1024 == 0 && kStage2 % 1024 == 0, "tensor copies land on swizzle boundaries");
+    static_assert(kKey % 1024 == 0 && kVal % 1024 == 0, "tensor copies land on swizzle boundaries");
 };
 
 // The tensor maps of q, k and v (and dout); make() is false when the inputs need images.
@@ -214,14 +221,14 @@ __device__ __forceinline__ void add_values_keys(const uint32_t (*a)[4], uint32_t
             }
         }
 }
-// u (16 x 16, rows or columns n0 of X) += a X over one 16-token block k0 of the contraction
+// u (16 x 16, block n of the result's tokens) += a X over block k of the contraction
 template <int NS, bool REV>
-__device__ __forceinline__ void add_times_x(const uint32_t (*a)[4], uint32_t x, int k0, int n0, float (*u)[4]) {
+__device__ __forceinline__ void add_times_x(const uint32_t (*a)[4], uint32_t x, int k, int n, float (*u)[4]) {
 #pragma unroll
     for (int pb = 0; pb < NS; ++pb) {
         uint32_t b[4];
-        if (REV) frag_b_t<128>(x + pb * kTile * 2, k0, n0, b);
-        else frag_b<128>(x + pb * kTile * 2, n0, k0, b);
+        if (REV) frag_b_t<32>(x + pb * kTri + tri_block(k, n), 0, 0, b);
+        else frag_b<32>(x + pb * kTri + tri_block(n, k), 0, 0, b);
 #pragma unroll
         for (int pa = 0; pa + pb < NS; ++pa) {
             ptx::mma16816(u[0], a[pa], b[0], b[1]);
@@ -347,7 +354,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                         if (!kRev) ptx::tma_load_3d(d + L::V, &tm_v, blk * kBlockV, head, t, m);
                     }
                     bulk_load(d + L::X, terms, L::kX, m);
-                    bulk_load(d + L::Gate1, terms + 2 * NS * kTile * 2, L::kGate, m);
+                    bulk_load(d + L::Gate1, terms + 2 * NS * kTri, L::kGate, m);
                     ++done1;
                 }
                 if constexpr (N2 > 0) {
@@ -363,8 +370,8 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                         for (int h = 0; h < DKP / 64; ++h) ptx::tma_load_3d(d + L::Q + h * kHalf, &tm_q, h * 64, kh, t, m);
                         if (kRev) ptx::tma_load_3d(d + L::dO, &tm_v, blk * kBlockV, head, t, m);
                     }
-                    bulk_load(d + L::P, terms + NS * kTile * 2, L::kP, m);
-                    bulk_load(d + L::Gate2, terms + 2 * NS * kTile * 2, L::kGate, m);
+                    bulk_load(d + L::P, terms + NS * kTri, L::kP, m);
+                    bulk_load(d + L::Gate2, terms + 2 * NS * kTri, L::kGate, m);
                     ++done2;
                 }
             }
@@ -423,14 +430,16 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
             }
         };
         if (n_chunks > 0) share_state(0);
+        bool ready = false;  // asked ahead of time: the answer's latency hides behind the update of S
         for (int i = 0; i < n_chunks; ++i) {
             const int c = at(i), s1 = i % N1, hb = i % NH;
             const uint32_t s = base + s1 * L::kStage1;
             const float *gate = reinterpret_cast<const float *>(smem + s1 * L::kStage1 + L::Gate1);
             char *rec = ws + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
                         ((slot0 + c) * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v);
-            warp_wait(full1(s1), (i / N1) & 1);
-            if (kRev) warp_wait(hfull(hb), (i / NH) & 1);
+            if (!ready) wait_bar(full1(s1), (i / N1) & 1);
+            if (kRev) wait_bar(hfull(hb), (i / NH) & 1);
+            __syncwarp();
 
             // this half's tokens: forward Y^T, then beta Z^T; in reverse dU^T
             uint32_t z[2][NS][4];
@@ -507,7 +516,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
                     if (kRev ? n <= b : n >= b)
-                        add_times_x<NS, kRev>(z[b], s + L::X, (t0 + b) * 16, (t0 + n) * 16, &u[2 * n]);
+                        add_times_x<NS, kRev>(z[b], s + L::X, t0 + b, t0 + n, &u[2 * n]);
             if (!first) {
                 meet();
 #pragma unroll
@@ -516,7 +525,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                     get_block<NS>(pair + L::Zx + b * kBlk, 2 * kBlk, a);
 #pragma unroll
                     for (int n = 0; n < 2; ++n)
-                        add_times_x<NS, kRev>(a, s + L::X, (o0 + b) * 16, (t0 + n) * 16, &u[2 * n]);
+                        add_times_x<NS, kRev>(a, s + L::X, o0 + b, t0 + n, &u[2 * n]);
                 }
             }
             auto finish = [&]() {  // u complete: to the output or the record; scaled, to the pair
@@ -580,6 +589,9 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                 for (int b = 0; b < 2; ++b) add_values_keys<NI, NS, DKP>(z[b], s + L::K, (t0 + b) * 16, c0, S);
             }
+            bool drained = true;
+            if (kOut && i + 1 >= NH) drained = test_bar(hempty((i + 1) % NH), ((i + 1 - NH) / NH) & 1);
+            ready = N1 > 1 && test_bar(full1((i + 1) % N1), ((i + 1) / N1) & 1);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {  // the other half's tokens
                 uint32_t a[NS][4];
@@ -599,8 +611,9 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                                 h == 0 ? sp[q][x][y] : sp[q][KX / 2 + x][y];
             }
             if constexpr (L::kKeep > 0) ptx::fence_proxy_async();
-            if (kOut && i + 1 >= NH)  // the output that read the next step's buffers is done
-                warp_wait(hempty((i + 1) % NH), ((i + 1 - NH) / NH) & 1);
+            if (!drained)  // the output that read the next step's buffers is done
+                wait_bar(hempty((i + 1) % NH), ((i + 1 - NH) / NH) & 1);
+            __syncwarp();
             share_state((i + 1) % NH);
             if constexpr (L::kKeep > 0) {
                 // both halves are staged (the barrier in share_state): one lane sends the record
@@ -668,7 +681,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                     for (int pq = 0; pq < NI; ++pq) {
                         uint32_t f[4];
-                        frag_a<128>(s + L::P + pq * kTile * 2, (2 * h + m) * 16, kx * 16, f);
+                        frag_a<32>(s + L::P + pq * kTri + tri_block(2 * h + m, kx), 0, 0, f);
 #pragma unroll
                         for (int pa = 0; pa + pq < NS; ++pa) {
                             ptx::mma16816(o[m][0], f, a[pa][0], a[pa][2]);
@@ -715,7 +728,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                         for (int pb = 0; pb < NS; ++pb) {
                             uint32_t b[4];
-                            frag_b_t<128>(s + L::P + pb * kTile * 2, kx * 16, (2 * h + n) * 16, b);
+                            frag_b_t<32>(s + L::P + pb * kTri + tri_block(kx, 2 * h + n), 0, 0, b);
 #pragma unroll
                             for (int pa = 0; pa < NI && pa + pb < NS; ++pa) {
                                 ptx::mma16816(y[2 * n], a[pa], b[0], b[1]);

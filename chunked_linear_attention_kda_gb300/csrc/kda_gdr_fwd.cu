@@ -29,13 +29,10 @@ namespace {
 constexpr int kTermThreads = 256;
 constexpr int kARow = 68;  // floats of a row of A in shared memory
 
-template <int NI, int DKP, int NS>
+template <int NI, int DKP>
 struct TermsSmem {
     static constexpr int kPlane = C * DKP * 2;
-    static constexpr int K = 0, Q = K + NI * kPlane;
-    static constexpr int kTileP = NS * kTile * 2;               // P of one head, over K or Q once they are used
-    static constexpr int kHead = kTileP > NI * kPlane ? kTileP : NI * kPlane;
-    static constexpr int A = 2 * kHead;
+    static constexpr int K = 0, Q = K + NI * kPlane, A = Q + NI * kPlane;
     static constexpr int Vec = A + 2 * C * kARow * 4;           // per head: G as float2, beta
     static constexpr int kBytes = Vec + 2 * 3 * C * 4;
 };
@@ -166,39 +163,84 @@ __device__ __forceinline__ void join_blocks(float *A, int r0, int c0, int n0, bo
     __syncthreads();
 }
 
+// The ten 16 x 16 blocks on and below the diagonal, shared out over four warps: at most three
+// each. w 0: (3,0) (3,1) (0,0)   1: (3,2) (1,0) (1,1)   2: (3,3) (2,0)   3: (2,1) (2,2)
+__device__ __forceinline__ void block_of(int w, int s, int &I, int &J) {
+    const uint32_t t = (w & 2 ? (w & 1 ? 0x2221u : 0x2033u) : (w & 1 ? 0x111032u : 0x003130u)) >> (8 * s);
+    I = (t >> 4) & 15;
+    J = t & 15;
+}
+
 template <typename T, int DKP, int NS>
 __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
     gdr_terms_kernel(const GdrArgs p, const Images im, int values, float scale, bool vec) {
     constexpr int NI = InputPlanes<T>::N;
-    using L = TermsSmem<NI, DKP, NS>;
+    using L = TermsSmem<NI, DKP>;
     extern __shared__ __align__(1024) char smem[];
     const uint32_t base = ptx::smem_u32(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
     const int64_t slot = blockIdx.x;
     const Chunk ch = find_chunk(p.cu_seqlens, p.n_seq, slot);
     if (ch.len == 0) return;
     const int hk = p.n_k_heads, hv = p.n_heads, kh = blockIdx.y, group = hv / hk;
     char *ws = static_cast<char *>(p.workspace);
+    float *A = reinterpret_cast<float *>(smem + L::A);
+    float *vec_s = reinterpret_cast<float *>(smem + L::Vec);
 
     load_key_tile<T, DKP>(base + L::K, static_cast<const T *>(p.k) + ch.t0 * p.k_stride + (int64_t)kh * p.d_k,
                           p.k_stride, ch.len, p.d_k, vec, tid, kTermThreads);
     load_key_tile<T, DKP>(base + L::Q, static_cast<const T *>(p.q) + ch.t0 * p.q_stride + (int64_t)kh * p.d_k,
                           p.q_stride, ch.len, p.d_k, vec, tid, kTermThreads);
     ptx::cp_async_commit();
-    // g and beta of the first two heads, ahead of their use: warp w < 2 takes one head of a pair
-    float gx[2], bx[2];
-    auto fetch_gates = [&](int h0) {
+
+    // The gates of the heads h0 and h0 + 1, a warp each: running sums of g log2(e) in two floats
+    // (the fp64 pipe of this part is narrow), so that differences of neighbours stay exact.
+    auto gates = [&](int h0) {
+        if (warp >= min(2, group - h0)) return;
+        const int head = kh * group + h0 + warp;
+        Two s[2];
+        float b[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = lane * 2 + i;
-            gx[i] = bx[i] = 0.f;
-            if (warp < min(2, group - h0) && r < ch.len) {
-                gx[i] = p.g[(ch.t0 + r) * hv + kh * group + h0 + warp];
-                bx[i] = p.beta[(ch.t0 + r) * hv + kh * group + h0 + warp];
+            float x = 0.f;
+            b[i] = 0.f;
+            if (r < ch.len) {
+                x = p.g[(ch.t0 + r) * hv + head];
+                // below -200 (and at -inf) the decay is 0 in fp32 all the same; a finite floor
+                // keeps differences of the sums free of inf - inf
+                x = x < kGFloor ? kGFloor : x;
+                b[i] = p.beta[(ch.t0 + r) * hv + head];
             }
+            s[i].hi = x * kLog2e;
+            s[i].lo = fmaf(x, kLog2e, -s[i].hi) + x * kLog2eLo;
+        }
+        s[1] = add(s[0], s[1]);
+        Two run = s[1];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Two y = {__shfl_up_sync(0xffffffffu, run.hi, o), __shfl_up_sync(0xffffffffu, run.lo, o)};
+            if (lane >= o) run = add(y, run);
+        }
+        Two before = {__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
+        if (lane == 0) before = {0.f, 0.f};
+        const Two total = {__shfl_sync(0xffffffffu, run.hi, 31), __shfl_sync(0xffffffffu, run.lo, 31)};
+        float *out = reinterpret_cast<float *>(ws + (slot * hv + head) * terms_bytes(NS) + 2 * NS * kTri);
+        float2 *G2 = reinterpret_cast<float2 *>(vec_s + warp * 3 * C);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = lane * 2 + i;
+            const Two G = i ? run : add(before, s[0]);
+            G2[r] = make_float2(G.hi, G.lo);
+            vec_s[warp * 3 * C + 2 * C + r] = b[i];
+            out[r] = exp2_of(G.hi, G.lo);
+            out[C + r] = ex2((total.hi - G.hi) + (total.lo - G.lo));
+            out[2 * C + r] = b[i];
+            out[3 * C + r] = exp2_of(total.hi, total.lo);
+            reinterpret_cast<float2 *>(out + 4 * C)[r] = make_float2(G.hi, G.lo);
         }
     };
-    fetch_gates(0);
+    gates(0);  // while the tiles arrive
     cp_async_wait<0>();
     __syncthreads();
 
@@ -210,140 +252,104 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
             reinterpret_cast<uint4 *>(img + kh * kb)[i] = reinterpret_cast<const uint4 *>(smem + L::Q)[i];
             reinterpret_cast<uint4 *>(img + (hk + kh) * kb)[i] = reinterpret_cast<const uint4 *>(smem + L::K)[i];
         }
-        for (int head = kh * group; head < (kh + 1) * group; ++head) {
-            write_value_image<T>(img + 2 * hk * kb + head * vb,
-                                 static_cast<const T *>(p.v) + ch.t0 * p.v_stride + (int64_t)head * p.d_v,
-                                 p.v_stride, ch.len, p.d_v, tid, kTermThreads);
-            if (values == 2)
-                write_value_image<T>(img + 2 * hk * kb + (hv + head) * vb,
-                                     static_cast<const T *>(p.dout) + (ch.t0 * hv + head) * p.d_v,
-                                     (int64_t)hv * p.d_v, ch.len, p.d_v, tid, kTermThreads);
-        }
+        write_value_images<T>(img + 2 * hk * kb + kh * group * vb, vb,
+                              static_cast<const T *>(p.v) + ch.t0 * p.v_stride + (int64_t)kh * group * p.d_v,
+                              p.v_stride, group, ch.len, p.d_v, tid, kTermThreads);
+        if (values == 2)
+            write_value_images<T>(img + 2 * hk * kb + (hv + kh * group) * vb, vb,
+                                  static_cast<const T *>(p.dout) + (ch.t0 * hv + kh * group) * p.d_v,
+                                  (int64_t)hv * p.d_v, group, ch.len, p.d_v, tid, kTermThreads);
     }
 
-    // K K^T (warps 0..3) and Q K^T (warps 4..7): rows 16 (warp % 4) .., columns up to their own
-    const int wr = warp & 3;
+    // K K^T (warps 0..3) and Q K^T (warps 4..7), the blocks of block_of()
+    const int wr = warp & 3, nb = wr < 2 ? 3 : 2;
     const bool keys = warp < 4;
-    float kk[8][4];
+    int I[3], J[3];
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+    for (int s = 0; s < 3; ++s) block_of(wr, s < nb ? s : 0, I[s], J[s]);
+    float kk[3][2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) kk[n][i] = 0.f;
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kk[s][0][i] = kk[s][1][i] = 0.f;
 #pragma unroll 2
-    for (int c = 0; c < DKP; c += 16) {
-        uint32_t a[NI][4];
+    for (int c = 0; c < DKP; c += 16)
 #pragma unroll
-        for (int q = 0; q < NI; ++q) key_a(base + (keys ? L::K : L::Q) + q * L::kPlane, wr * 16, c, a[q]);
+        for (int s = 0; s < 3; ++s) {
+            if (s >= nb) break;
+            uint32_t a[NI][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            if (n > wr) break;
+            for (int q = 0; q < NI; ++q) key_a(base + (keys ? L::K : L::Q) + q * L::kPlane, I[s] * 16, c, a[q]);
 #pragma unroll
             for (int pb = 0; pb < NI; ++pb) {
                 uint32_t b[4];
-                key_b(base + L::K + pb * L::kPlane, n * 16, c, b);
+                key_b(base + L::K + pb * L::kPlane, J[s] * 16, c, b);
 #pragma unroll
                 for (int pa = 0; pa + pb < NI; ++pa) {
-                    ptx::mma16816(kk[2 * n], a[pa], b[0], b[1]);
-                    ptx::mma16816(kk[2 * n + 1], a[pa], b[2], b[3]);
+                    ptx::mma16816(kk[s][0], a[pa], b[0], b[1]);
+                    ptx::mma16816(kk[s][1], a[pa], b[2], b[3]);
                 }
             }
         }
-    }
 
-    float *A = reinterpret_cast<float *>(smem + L::A);
-    float *vec_s = reinterpret_cast<float *>(smem + L::Vec);
     for (int h0 = 0; h0 < group; h0 += 2) {
         const int nh = min(2, group - h0);
-        // gates: warp w < nh takes head h0 + w; running sums of g log2(e) in two floats (the
-        // fp64 pipe of this part is narrow), so that differences of neighbours stay exact
-        if (warp < nh) {
-            const int head = kh * group + h0 + warp;
-            Two s[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                // below -200 (and at -inf) the decay is 0 in fp32 all the same; a finite floor
-                // keeps differences of the sums free of inf - inf
-                const float x = gx[i] < kGFloor ? kGFloor : gx[i];
-                s[i].hi = x * kLog2e;
-                s[i].lo = fmaf(x, kLog2e, -s[i].hi) + x * kLog2eLo;
-            }
-            s[1] = add(s[0], s[1]);
-            Two run = s[1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const Two y = {__shfl_up_sync(0xffffffffu, run.hi, o), __shfl_up_sync(0xffffffffu, run.lo, o)};
-                if (lane >= o) run = add(y, run);
-            }
-            Two before = {__shfl_up_sync(0xffffffffu, run.hi, 1), __shfl_up_sync(0xffffffffu, run.lo, 1)};
-            if (lane == 0) before = {0.f, 0.f};
-            const Two total = {__shfl_sync(0xffffffffu, run.hi, 31), __shfl_sync(0xffffffffu, run.lo, 31)};
-            float *out = reinterpret_cast<float *>(ws + (slot * hv + head) * terms_bytes(NS) + (size_t)2 * NS * kTile * 2);
-            float2 *G2 = reinterpret_cast<float2 *>(vec_s + warp * 3 * C);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = lane * 2 + i;
-                const Two G = i ? run : add(before, s[0]);
-                G2[r] = make_float2(G.hi, G.lo);
-                vec_s[warp * 3 * C + 2 * C + r] = bx[i];
-                out[r] = exp2_of(G.hi, G.lo);
-                out[C + r] = ex2((total.hi - G.hi) + (total.lo - G.lo));
-                out[2 * C + r] = bx[i];
-                out[3 * C + r] = exp2_of(total.hi, total.lo);
-                reinterpret_cast<float2 *>(out + 4 * C)[r] = make_float2(G.hi, G.lo);
-            }
+        if (h0) {
+            __syncthreads();  // A and the gates of the pair before are done with
+            gates(h0);
+            __syncthreads();
         }
-        fetch_gates(h0 + 2);
-        __syncthreads();  // the gates are in; K and Q (or the previous pair's P) are done with
-        // A (fp32; warps 0..3) and P (bf16 planes; warps 4..7) of both heads, zero above the diagonal
+        // A (fp32, to shared memory; warps 0..3) and P (bf16 planes, to the workspace; warps 4..7)
         for (int hh = 0; hh < nh; ++hh) {
             const float2 *G2 = reinterpret_cast<const float2 *>(vec_s + hh * 3 * C);
             const float *B = vec_s + hh * 3 * C + 2 * C;
-            char *tile = smem + hh * L::kHead;
             float *Ah = A + hh * C * kARow;
-            const int r0 = wr * 16 + (lane >> 2);
-            const float2 g0 = G2[r0], g1 = G2[r0 + 8];
-            const float f0 = keys ? B[r0] : scale, f1 = keys ? B[r0 + 8] : scale;
+            char *P = ws + (slot * hv + kh * group + h0 + hh) * terms_bytes(NS) + NS * kTri;
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                const int j = n * 8 + (lane & 3) * 2;
-                float x[4] = {0.f, 0.f, 0.f, 0.f};
-                if (n <= 2 * wr + 1) {
+            for (int s = 0; s < 3; ++s) {
+                if (s >= nb) break;
+                const int r0 = I[s] * 16 + gr;
+                const float2 g0 = G2[r0], g1 = G2[r0 + 8];
+                const float f0 = keys ? B[r0] : scale, f1 = keys ? B[r0 + 8] : scale;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const int j = J[s] * 16 + n * 8 + tq * 2;
                     const float4 gj = *reinterpret_cast<const float4 *>(&G2[j]);
-                    x[0] = f0 * kk[n][0] * ex2((g0.x - gj.x) + (g0.y - gj.y));
-                    x[1] = f0 * kk[n][1] * ex2((g0.x - gj.z) + (g0.y - gj.w));
-                    x[2] = f1 * kk[n][2] * ex2((g1.x - gj.x) + (g1.y - gj.y));
-                    x[3] = f1 * kk[n][3] * ex2((g1.x - gj.z) + (g1.y - gj.w));
-                    if (n >= 2 * wr) {  // the diagonal block; A is strictly lower
+                    const float *k4 = kk[s][n];
+                    float x[4];
+                    x[0] = f0 * k4[0] * ex2((g0.x - gj.x) + (g0.y - gj.y));
+                    x[1] = f0 * k4[1] * ex2((g0.x - gj.z) + (g0.y - gj.w));
+                    x[2] = f1 * k4[2] * ex2((g1.x - gj.x) + (g1.y - gj.y));
+                    x[3] = f1 * k4[3] * ex2((g1.x - gj.z) + (g1.y - gj.w));
+                    if (I[s] == J[s]) {  // A is strictly lower triangular, P lower
                         const int e = keys ? 0 : 1;
                         if (j >= r0 + e) x[0] = 0.f;
                         if (j + 1 >= r0 + e) x[1] = 0.f;
                         if (j >= r0 + 8 + e) x[2] = 0.f;
                         if (j + 1 >= r0 + 8 + e) x[3] = 0.f;
                     }
-                }
-                if (keys) {
-                    *reinterpret_cast<float2 *>(Ah + r0 * kARow + j) = make_float2(x[0], x[1]);
-                    *reinterpret_cast<float2 *>(Ah + (r0 + 8) * kARow + j) = make_float2(x[2], x[3]);
-                } else {
+                    if (keys) {
+                        *reinterpret_cast<float2 *>(Ah + r0 * kARow + j) = make_float2(x[0], x[1]);
+                        *reinterpret_cast<float2 *>(Ah + (r0 + 8) * kARow + j) = make_float2(x[2], x[3]);
+                    } else {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t w[NS];
-                        split2<NS>(x[2 * h], x[2 * h + 1], w);
-                        char *at = tile + tile_off<128>(r0 + 8 * h, j);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t w[NS];
+                            split2<NS>(x[2 * h], x[2 * h + 1], w);
+                            char *at = P + tri_block(I[s], J[s]) + tile_off<32>(gr + 8 * h, n * 8 + tq * 2);
 #pragma unroll
-                        for (int pl = 0; pl < NS; ++pl) *reinterpret_cast<uint32_t *>(at + pl * kTile * 2) = w[pl];
+                            for (int pl = 0; pl < NS; ++pl)  // the forward pass alone reads NI planes of P
+                                if (pl < NI || values == 2) *reinterpret_cast<uint32_t *>(at + pl * kTri) = w[pl];
+                        }
                     }
                 }
             }
+            if (wr == 3 && !keys) {  // the block above the diagonal that join_blocks<32> reads
+#pragma unroll
+                for (int i = 0; i < 8; ++i) Ah[(lane >> 1) * kARow + 16 + (lane & 1) * 8 + i] = 0.f;
+            }
         }
         __syncthreads();
-        for (int hh = 0; hh < nh; ++hh) {  // P out
-            const int head = kh * group + h0 + hh;
-            uint4 *dst = reinterpret_cast<uint4 *>(ws + (slot * hv + head) * terms_bytes(NS) + (size_t)NS * kTile * 2);
-            const uint4 *src = reinterpret_cast<const uint4 *>(smem + hh * L::kHead);
-            const int planes = values == 2 ? NS : NI;  // the forward pass alone reads P at the inputs' precision
-            for (int i = tid; i < planes * kTile / 8; i += kTermThreads) dst[i] = src[i];
-        }
         // X in place: warps 2 h, 2 h + 1 for head h (the other warps only keep the barriers)
         {
             const int hh = warp >> 1, w = warp & 1, t = tid & 63;
@@ -354,28 +360,21 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
             join_blocks<16>(X, 32 * w + 16, 32 * w, 0, on);
             join_blocks<32>(X, 32, 0, 16 * w, on);
         }
-        for (int hh = 0; hh < nh; ++hh) {  // X out, split into planes on the way
-            const int head = kh * group + h0 + hh;
-            char *dst = ws + (slot * hv + head) * terms_bytes(NS);
-            for (int i = tid; i < C * 8; i += kTermThreads) {
-                const int r = i >> 3, c = (i & 7) * 8;
-                const float *src = A + hh * C * kARow + r * kARow + c;
-                uint32_t w[NS][4];
+        for (int i = tid; i < nh * 320; i += kTermThreads) {  // X out, split into planes on the way
+            const int hh = i / 320, k = i % 320, b = k >> 5, r = (k >> 1) & 15, c = (k & 1) * 8;
+            const int bi = b >= 6 ? 3 : b >= 3 ? 2 : b >= 1 ? 1 : 0, bj = b - bi * (bi + 1) / 2;
+            const float *src = A + hh * C * kARow + (bi * 16 + r) * kARow + bj * 16 + c;
+            char *dst = ws + (slot * hv + kh * group + h0 + hh) * terms_bytes(NS) + b * 512 + tile_off<32>(r, c);
+            const float4 u = *reinterpret_cast<const float4 *>(src), v = *reinterpret_cast<const float4 *>(src + 4);
+            uint32_t w[4][NS];
+            split2<NS>(u.x, u.y, w[0]);
+            split2<NS>(u.z, u.w, w[1]);
+            split2<NS>(v.x, v.y, w[2]);
+            split2<NS>(v.z, v.w, w[3]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t s[NS];
-                    const float2 v = *reinterpret_cast<const float2 *>(src + 2 * j);
-                    split2<NS>(v.x, v.y, s);
-#pragma unroll
-                    for (int q = 0; q < NS; ++q) w[q][j] = s[q];
-                }
-#pragma unroll
-                for (int q = 0; q < NS; ++q)
-                    *reinterpret_cast<uint4 *>(dst + q * kTile * 2 + tile_off<128>(r, c)) =
-                        make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
-            }
+            for (int q = 0; q < NS; ++q)
+                *reinterpret_cast<uint4 *>(dst + q * kTri) = make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
         }
-        __syncthreads();  // A and the gates are free for the next pair
     }
 }
 
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(kChainThreads)
 
 template <typename T, int DKP, int NS>
 cudaError_t terms(const GdrArgs &p, const Images &im, int values, cudaStream_t stream) {
-    constexpr int bytes = TermsSmem<InputPlanes<T>::N, DKP, NS>::kBytes;
+    constexpr int bytes = TermsSmem<InputPlanes<T>::N, DKP>::kBytes;
     const cudaError_t e = cudaFuncSetAttribute(gdr_terms_kernel<T, DKP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     const bool vec = rows_vec<T>(p.q, p.q_stride, p.d_k) && rows_vec<T>(p.k, p.k_stride, p.d_k);
