@@ -37,6 +37,29 @@ __device__ __forceinline__ int64_t slot_base(const int32_t *cu, int n) {
     return (int64_t)(cu[n] >> 6) + n;
 }
 
+// Dependent launches: the kernel starts while the one before it on the stream drains, and
+// waits here for that one's results.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, const A &...args) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
 struct Chunk {
     int seq, len;      // len = 0: an unused slot
     int64_t t0;
@@ -77,11 +100,13 @@ __host__ __device__ __forceinline__ size_t scan_offset(int64_t n_tok, int64_t n_
 }
 
 // Tile images of q, k (per key head), v and, for the backward pass, dout (per value head) of
-// the chunks that a tensor copy cannot fetch: a sequence's last, partial chunk (rows past its
-// end must read as zero, not as the next sequence), and every chunk of inputs that are fp32
-// or not 16-byte aligned. Indexed by sequence when only partial chunks need one, else by slot.
+// the chunks that a tensor copy cannot fetch: the last, partial chunk of a sequence that
+// another one follows (rows past its end must read as zero, not as the next sequence; past
+// the last token the copy itself fills in zeros), and every chunk of inputs that are fp32 or
+// not 16-byte aligned. Indexed by sequence when only partial chunks need one, else by slot.
 struct Images {
     bool all;           // every chunk has an image
+    __device__ bool has(int64_t t0, int len, int64_t n_tok) const { return all || (len < C && t0 + len < n_tok); }
     size_t offset;      // of the first, in the workspace
     __host__ __device__ static size_t key_bytes(int ni, int dkp) { return (size_t)ni * C * dkp * 2; }
     __host__ __device__ static size_t value_bytes(int ni, int d_v) { return (size_t)ni * pad_v(d_v) * C * 2; }
@@ -297,12 +322,6 @@ __device__ __forceinline__ void write_value_images(char *dst, size_t vb, const T
             *reinterpret_cast<uint4 *>(at + q * plane) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
     }
 }
-// `bytes` (a multiple of 16) from the workspace, as they lie
-__device__ __forceinline__ void load_raw(uint32_t dst, const void *src, int bytes, int tid, int nthreads) {
-    const char *p = static_cast<const char *>(src);
-    for (int i = tid * 16; i < bytes; i += nthreads * 16) cp_async_16(dst + i, p + i, 16);
-}
-
 __device__ __forceinline__ void put(float *p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 // two neighbouring elements; wide: p is aligned to both

@@ -34,13 +34,14 @@ __global__ void __launch_bounds__(kChainThreads)
     gdr_scan_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                     const GdrArgs p, const Images im, float scale) {
+    let_next_kernel_start();
     const unsigned n = gridDim.x / 2;
     if (blockIdx.x >= n) chain<T, DKP, NS, Mode::kStates>(tm_q, tm_k, tm_v, p, im, 2, blockIdx.x - n, scale, false);
     else chain<T, DKP, NS, Mode::kReverse>(tm_q, tm_k, tm_do, p, im, 2, blockIdx.x, scale, false);
 }
 
 // ---------------------------------------------------------------- local gradients
-constexpr int kLocalThreads = 512;
+constexpr int kLocalThreads = 256;
 constexpr int kCols = kLocalThreads / 128;  // column parts: a warp has 16 tokens x 1 / kCols of the columns
 
 template <int NI, int DKP, int NS>
@@ -49,7 +50,7 @@ struct LocalSmem {
     static constexpr int kPlane = C * DKP * 2;
     static constexpr int kIn = C * 32 * 2, kVal = 32 * C * 2, kState = 32 * DKP * 2;  // one plane of a 32-channel slice
     static constexpr int dO = 0, V = dO + NI * kIn, U = V + (NI == 1 ? kIn : 0),  // fp32 V is read in place
-                          E = U + NS * kVal, S = E + NS * kVal;
+                         E = U + NS * kVal, S = E + NS * kVal;
     static constexpr int dS = S + NS * kState, kSlice = dS + NS * kState;
     static constexpr int kTile = C * C * 2;  // bytes of a plane of B and F
     static constexpr int B = 0, F = NI * kTile;  // over the first slice buffer, once the slices are done
@@ -59,8 +60,10 @@ struct LocalSmem {
     // Red: [kCols][64] row sums of q.x, k.x, k.x, F k.k, M over the column parts; [64] E.V;
     // [4][64] column sums of M over the row blocks; the warps' parts of <S0, dS1>
     static constexpr int kRed = 5 * kCols * C + C + 4 * C + kLocalThreads / 32;
-    static constexpr int kBytes = Red + kRed * 4;
+    static constexpr int Bars = (Red + kRed * 4 + 7) / 8 * 8;
+    static constexpr int kBytes = Bars + 8 * (kStages + 1) + 1024;  // the base is rounded up to 1024
     static_assert(kBytes <= 227 * 1024, "fits an SM");
+    static_assert(kSlice % 1024 == 0, "tensor copies land on swizzle boundaries");
 };
 
 // a row's sum over the column parts
@@ -77,13 +80,17 @@ __device__ __forceinline__ float quad_sum(float x) {
 
 template <typename T, int DKP, int NS>
 __global__ void __launch_bounds__(kLocalThreads)
-    gdr_local_kernel(const GdrArgs p, float scale, bool vec_qk, bool vec_v, bool vec_do, bool wide_k, bool wide_v) {
+    gdr_local_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                     const GdrArgs p, const Images im, float scale, bool wide_k, bool wide_v) {
     constexpr int NI = InputPlanes<T>::N;
     using L = LocalSmem<NI, DKP, NS>;
     constexpr int RB = DKP * 2, KC = DKP / kCols, NH = KC / 16;  // a warp's key channels, in steps of 16
     constexpr int PC = C / kCols, NP = PC / 16;              // its columns of the 64 x 64 products
-    extern __shared__ __align__(128) char smem[];
+    extern __shared__ __align__(1024) char smem_raw[];
+    char *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_u32(smem);
+    wait_for_previous_kernel();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
     const int wr = warp & 3, wc = warp >> 2;  // token rows 16 wr .., column part wc
     const int64_t slot = blockIdx.x;
@@ -98,34 +105,60 @@ __global__ void __launch_bounds__(kLocalThreads)
     float *r_qx = red, *r_kx = r_qx + kCols * C, *r_ku = r_kx + kCols * C, *r_fk = r_ku + kCols * C;
     float *r_m = r_fk + kCols * C, *r_ev = r_m + kCols * C, *c_m = r_ev + C, *r_ss = c_m + 4 * C;
 
+    // one thread loads: K and Q, then the 32-channel slices of the value heads, head after head
+    auto bar = [&](int i) { return base + L::Bars + 8 * i; };  // a slice buffer's; kStages: K and Q
+    const bool image = im.has(ch.t0, ch.len, p.n_tok);
+    const size_t img_rec = Images::record(NI, DKP, p.d_v, p.n_k_heads, p.n_heads, 2);
+    const size_t kb = Images::key_bytes(NI, DKP), vb = Images::value_bytes(NI, p.d_v);
+    const char *img = ws + im.offset + (im.all ? slot : (int64_t)ch.seq) * img_rec;
+    bool ok = true;
+    int issued = 0;
     auto load = [&](int step) {  // slice `step % n_sl` of value head `step / n_sl`
+        if (!ok) return;
+        ++issued;
         const int head = kh * group + step / n_sl, sl = step % n_sl;
-        const uint32_t s = base + (step % L::kStages) * L::kSlice;
-        load_tile<T, 64>(s + L::dO, L::kIn, static_cast<const T *>(p.dout) + (ch.t0 * p.n_heads + head) * p.d_v + sl * 32,
-                         (int64_t)p.n_heads * p.d_v, ch.len, p.d_v - sl * 32, vec_do, tid, kLocalThreads);
-        if (NI == 1) load_tile<T, 64>(s + L::V, L::kIn, static_cast<const T *>(p.v) + ch.t0 * p.v_stride + (int64_t)head * p.d_v + sl * 32,
-                         p.v_stride, ch.len, p.d_v - sl * 32, vec_v, tid, kLocalThreads);
+        const uint32_t s = base + (step % L::kStages) * L::kSlice, m = bar(step % L::kStages);
         const char *rec = ws + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
                           (slot * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v);
         const size_t st = scan_state_bytes(NS, DKP, p.d_v), va = scan_value_bytes(NS, p.d_v);
+        ptx::mbar_arrive_tx(m, L::kSlice);
+        if (image) {
+            const char *v = img + 2 * p.n_k_heads * kb + (size_t)sl * NI * L::kIn;
+            bulk_load(s + L::dO, v + (p.n_heads + head) * vb, NI * L::kIn, m);
+            if (NI == 1) bulk_load(s + L::V, v + head * vb, L::kIn, m);
+        } else {
+            ptx::tma_load_3d(s + L::dO, &tm_do, sl * 32, head, (int)ch.t0, m);
+            if (NI == 1) ptx::tma_load_3d(s + L::V, &tm_v, sl * 32, head, (int)ch.t0, m);
+        }
 #pragma unroll
         for (int q = 0; q < NS; ++q) {
-            load_raw(s + L::S + q * L::kState, rec + q * (st / NS) + sl * L::kState, L::kState, tid, kLocalThreads);
-            load_raw(s + L::dS + q * L::kState, rec + st + q * (st / NS) + sl * L::kState, L::kState, tid, kLocalThreads);
-            load_raw(s + L::U + q * L::kVal, rec + 2 * st + q * (va / NS) + sl * L::kVal, L::kVal, tid, kLocalThreads);
-            load_raw(s + L::E + q * L::kVal, rec + 2 * st + va + q * (va / NS) + sl * L::kVal, L::kVal, tid, kLocalThreads);
+            bulk_load(s + L::S + q * L::kState, rec + q * (st / NS) + sl * L::kState, L::kState, m);
+            bulk_load(s + L::dS + q * L::kState, rec + st + q * (st / NS) + sl * L::kState, L::kState, m);
+            bulk_load(s + L::U + q * L::kVal, rec + 2 * st + q * (va / NS) + sl * L::kVal, L::kVal, m);
+            bulk_load(s + L::E + q * L::kVal, rec + 2 * st + va + q * (va / NS) + sl * L::kVal, L::kVal, m);
         }
     };
-
-    load_key_tile<T, DKP>(base + L::K, static_cast<const T *>(p.k) + ch.t0 * p.k_stride + (int64_t)kh * p.d_k,
-                          p.k_stride, ch.len, p.d_k, vec_qk, tid, kLocalThreads);
-    load_key_tile<T, DKP>(base + L::Q, static_cast<const T *>(p.q) + ch.t0 * p.q_stride + (int64_t)kh * p.d_k,
-                          p.q_stride, ch.len, p.d_k, vec_qk, tid, kLocalThreads);
-    ptx::cp_async_commit();
-    if (L::kStages == 2) load(0);
-    ptx::cp_async_commit();
-    cp_async_wait<1>();
+    if (tid == 0) {
+        for (int i = 0; i <= L::kStages; ++i) ptx::mbar_init(bar(i), 1);
+        ptx::mbar_init_fence();
+        const uint32_t m = bar(L::kStages);
+        ptx::mbar_arrive_tx(m, 2 * NI * L::kPlane);
+        if (image) {
+            bulk_load(base + L::Q, img + kh * kb, NI * L::kPlane, m);
+            bulk_load(base + L::K, img + (p.n_k_heads + kh) * kb, NI * L::kPlane, m);
+        } else {
+#pragma unroll
+            for (int h = 0; h < DKP / 64; ++h) {
+                ptx::tma_load_3d(base + L::Q + h * kHalf, &tm_q, h * 64, kh, (int)ch.t0, m);
+                ptx::tma_load_3d(base + L::K + h * kHalf, &tm_k, h * 64, kh, (int)ch.t0, m);
+            }
+        }
+        load(0);
+    }
     __syncthreads();
+    // A failed wait sets the flag and the block goes on with what is there: nothing more is
+    // loaded, and every later wait returns at once.
+    ok = wait_bar(bar(L::kStages), 0);
 
     // q_r.k_j and k_r.k_j of rows 16 wr .., columns PC wc .., kept by each thread for itself
     {
@@ -184,42 +217,38 @@ __global__ void __launch_bounds__(kLocalThreads)
         for (int n = 0; n < 2 * NP; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) ou[n][i] = eu[n][i] = 0.f;
-        float ev[2] = {0.f, 0.f}, ss = 0.f;
+        float ev[2] = {0.f, 0.f}, ss[2][4];
+        zero<2>(ss);
         for (int i = tid; i < kGateFloats; i += kLocalThreads)
             gate[i] = reinterpret_cast<const float *>(ws + (slot * p.n_heads + head) * terms_bytes(NS) +
                                                       2 * NS * kTri)[i];
 
         for (int sl = 0; sl < n_sl; ++sl) {
             const int step = hh * n_sl + sl;
-            if (L::kStages == 2) {
-                // the next head's first slice overwrites B and F of this one: it waits (below)
-                if (sl + 1 < n_sl) load(step + 1);
-                ptx::cp_async_commit();
-                cp_async_wait<1>();
-            } else {
-                load(step);
-                ptx::cp_async_commit();
-                cp_async_wait<0>();
-            }
-            __syncthreads();
+            // the next slice; the next head's first one overwrites B and F of this head: it comes
+            // after them (below)
+            if (L::kStages == 2 && tid == 0 && sl + 1 < n_sl) load(step + 1);
+            if (L::kStages == 1 && tid == 0 && step > 0) load(step);
+            ok &= wait_bar(bar(step % L::kStages), (step / L::kStages) & 1);
+            if (sl == 0) __syncthreads();  // the gates
             const uint32_t s = base + (step % L::kStages) * L::kSlice;
-            const char *sp = smem + (step % L::kStages) * L::kSlice;
-            // <S0, dS1>
-            for (int i = tid; i < L::kState / 16; i += kLocalThreads) {
-                float x[8], z[8];
+            // <S0, dS1>: the diagonals of S0^T dS1 of 16 x 16 blocks, shared out over the warps
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = z[j] = 0.f;
+            for (int i = 0; i < DKP / 8 / (kLocalThreads / 32); ++i) {
+                const int b = i * (kLocalThreads / 32) + warp, v = (b & 1) * 16, c = (b >> 1) * 16;
+                uint32_t x[NS][4], y[NS][4];
 #pragma unroll
                 for (int q = 0; q < NS; ++q) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(sp + L::S + q * L::kState + i * 16);
-                    const uint4 b = *reinterpret_cast<const uint4 *>(sp + L::dS + q * L::kState + i * 16);
-                    x[0] += lo_f(a.x); x[1] += hi_f(a.x); x[2] += lo_f(a.y); x[3] += hi_f(a.y);
-                    x[4] += lo_f(a.z); x[5] += hi_f(a.z); x[6] += lo_f(a.w); x[7] += hi_f(a.w);
-                    z[0] += lo_f(b.x); z[1] += hi_f(b.x); z[2] += lo_f(b.y); z[3] += hi_f(b.y);
-                    z[4] += lo_f(b.z); z[5] += hi_f(b.z); z[6] += lo_f(b.w); z[7] += hi_f(b.w);
+                    frag_a<RB>(s + L::S + q * L::kState, v, c, x[q]);
+                    frag_b<RB>(s + L::dS + q * L::kState, v, c, y[q]);
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) ss = fmaf(x[j], z[j], ss);
+                for (int pa = 0; pa < NS; ++pa)
+#pragma unroll
+                    for (int pb = 0; pa + pb < NS; ++pb) {
+                        ptx::mma16816(ss[0], x[pa], y[pb][0], y[pb][1]);
+                        ptx::mma16816(ss[1], x[pa], y[pb][2], y[pb][3]);
+                    }
             }
 #pragma unroll
             for (int kx = 0; kx < 2; ++kx) {  // 16 value channels
@@ -405,9 +434,11 @@ __global__ void __launch_bounds__(kLocalThreads)
                     r_m[wc * C + wr * 16 + gr + 8 * h] = b;
                 }
             }
+            // rows gr of the first tile's columns 0..7, rows gr + 8 of the second's 8..15
+            float d = gr == 2 * tq ? ss[0][0] + ss[1][2] : gr == 2 * tq + 1 ? ss[0][1] + ss[1][3] : 0.f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (lane == 0) r_ss[warp] = ss;
+            for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+            if (lane == 0) r_ss[warp] = d;
         }
         __syncthreads();
         if (warp == 0) {  // dbeta, dg: two tokens a lane, running sums over the chunk
@@ -473,9 +504,13 @@ __global__ void __launch_bounds__(kLocalThreads)
                     }
                 }
         }
-        __syncthreads();  // B, F, the gates and the sums are done with
-        if (L::kStages == 2 && hh + 1 < group) load((hh + 1) * n_sl);
-        ptx::cp_async_commit();
+        ptx::fence_proxy_async();  // B and F were written by plain stores; the next copies overwrite them
+        __syncthreads();           // B, F, the gates and the sums are done with
+        if (L::kStages == 2 && tid == 0 && hh + 1 < group) load((hh + 1) * n_sl);
+    }
+    if (!ok && tid == 0) {  // nothing may land in shared memory after the block has gone
+        drain_bar(bar(L::kStages), 0);
+        for (int i = max(0, issued - L::kStages); i < issued; ++i) drain_bar(bar(i % L::kStages), (i / L::kStages) & 1);
     }
     // write the key head's gradients
 #pragma unroll
@@ -500,25 +535,15 @@ cudaError_t backward(const GdrArgs &p, cudaStream_t stream) {
                                                 (size_t)n_slots(p.n_tok, p.n_seq) * p.n_heads * scan_bytes(NS, DKP, p.d_v)};
     cudaError_t e = launch_gdr_terms(p, im, 2, NS, stream);
     if (e != cudaSuccess) return e;
-    const bool vec_qk = rows_vec<T>(p.q, p.q_stride, p.d_k) && rows_vec<T>(p.k, p.k_stride, p.d_k);
-    const bool vec_v = rows_vec<T>(p.v, p.v_stride, p.d_v);
-    const bool vec_do = rows_vec<T>(p.dout, (int64_t)p.n_heads * p.d_v, p.d_v);
     constexpr int fwd = ChainSmem<NI, DKP, NS, Mode::kStates>::kBytes, rev = ChainSmem<NI, DKP, NS, Mode::kReverse>::kBytes;
     constexpr int scan = fwd > rev ? fwd : rev;
-    e = cudaFuncSetAttribute(gdr_scan_kernel<T, DKP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, scan);
-    if (e != cudaSuccess) return e;
-    gdr_scan_kernel<T, DKP, NS><<<2 * chain_blocks(p), kChainThreads, scan, stream>>>(maps.q, maps.k, maps.v, maps.dout, p, im, scale);
-    count_launches(1);
-    e = cudaGetLastError();
+    e = launch_dependent(gdr_scan_kernel<T, DKP, NS>, 2 * chain_blocks(p), kChainThreads, scan, stream, maps.q, maps.k,
+                         maps.v, maps.dout, p, im, scale);
     if (e != cudaSuccess || p.n_tok == 0) return e;
-    constexpr int local = LocalSmem<NI, DKP, NS>::kBytes;
-    e = cudaFuncSetAttribute(gdr_local_kernel<T, DKP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, local);
-    if (e != cudaSuccess) return e;
     auto wide = [](const void *x, int d) { return d % 2 == 0 && ((uintptr_t)x % (2 * sizeof(T))) == 0; };
-    gdr_local_kernel<T, DKP, NS><<<dim3((unsigned)n_slots(p.n_tok, p.n_seq), p.n_k_heads), kLocalThreads, local, stream>>>(
-        p, scale, vec_qk, vec_v, vec_do, wide(p.dq, p.d_k) && wide(p.dk, p.d_k), wide(p.dv, p.d_v));
-    count_launches(1);
-    return cudaGetLastError();
+    return launch_dependent(gdr_local_kernel<T, DKP, NS>, dim3((unsigned)n_slots(p.n_tok, p.n_seq), p.n_k_heads),
+                            kLocalThreads, LocalSmem<NI, DKP, NS>::kBytes, stream, maps.q, maps.k, maps.v, maps.dout, p, im,
+                            scale, wide(p.dq, p.d_k) && wide(p.dk, p.d_k), wide(p.dv, p.d_v));
 }
 
 // Planes of the intermediates. dg sums inner products of states with state gradients, which

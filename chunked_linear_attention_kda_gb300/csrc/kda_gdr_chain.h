@@ -50,6 +50,11 @@ __device__ __forceinline__ bool wait_bar(uint32_t a, uint32_t parity) {
         }
     }
 }
+// for copies in flight after a failed wait: waits for them whatever the flag says, as long again
+static __device__ __noinline__ void drain_bar(uint32_t a, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!ptx::mbar_try(a, parity) && clock64() - t0 < kWaitLimit) {}
+}
 // whether the phase is complete, without waiting
 __device__ __forceinline__ bool test_bar(uint32_t a, uint32_t parity) {
     uint32_t ok;
@@ -144,7 +149,7 @@ struct ChainMaps {
     }
     template <typename T>
     bool make(const GdrArgs &p, bool with_dout) {
-        if (sizeof(T) != 2 || p.n_tok < C) return false;
+        if (sizeof(T) != 2 || p.n_tok == 0) return false;
         if (!rows_vec<T>(p.q, p.q_stride, p.d_k) || !rows_vec<T>(p.k, p.k_stride, p.d_k) ||
             !rows_vec<T>(p.v, p.v_stride, p.d_v))
             return false;
@@ -295,6 +300,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
     char *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_u32(smem);
     __shared__ int ranked;
+    wait_for_previous_kernel();  // the chunk terms
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
     const int n_blk = (p.d_v + kBlockV - 1) / kBlockV;
     const int blk = block % n_blk, sh = block / n_blk;
@@ -336,7 +342,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
             bool ok = true;
             for (int i = 0; i < n_chunks && ok; ++i) {
                 const int c = at(i), t = (int)tok0 + c * C;
-                const bool image = im.all || len - c * C < C;
+                const bool image = im.has(t, min(C, len - c * C), p.n_tok);
                 const char *img = ws + im.offset + (im.all ? slot0 + c : (int64_t)seq) * rec;
                 const char *vimg = img + 2 * p.n_k_heads * kb + (kRev ? p.n_heads + head : head) * vb + (size_t)blk * L::kVal;
                 const char *terms = ws + ((slot0 + c) * p.n_heads + head) * terms_bytes(NS);
@@ -376,9 +382,9 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                 }
             }
             if (!ok) {  // nothing may land in shared memory after the CTA has gone
-                for (int i = max(0, done1 - N1); i < done1; ++i) wait_bar(full1(i % N1), (i / N1) & 1);
+                for (int i = max(0, done1 - N1); i < done1; ++i) drain_bar(full1(i % N1), (i / N1) & 1);
                 if constexpr (N2 > 0)
-                    for (int i = max(0, done2 - N2); i < done2; ++i) wait_bar(full2(i % N2), (i / N2) & 1);
+                    for (int i = max(0, done2 - N2); i < done2; ++i) drain_bar(full2(i % N2), (i / N2) & 1);
             }
         }
     } else if (warp < 4) {

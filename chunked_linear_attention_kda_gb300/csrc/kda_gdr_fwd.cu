@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
     extern __shared__ __align__(1024) char smem[];
     const uint32_t base = ptx::smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
+    let_next_kernel_start();
     const int64_t slot = blockIdx.x;
     const Chunk ch = find_chunk(p.cu_seqlens, p.n_seq, slot);
     if (ch.len == 0) return;
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
     cp_async_wait<0>();
     __syncthreads();
 
-    if (im.all || ch.len < C) {
+    if (im.has(ch.t0, ch.len, p.n_tok)) {
         const size_t rec = Images::record(NI, DKP, p.d_v, hk, hv, values), kb = Images::key_bytes(NI, DKP);
         const size_t vb = Images::value_bytes(NI, p.d_v);
         char *img = ws + im.offset + (im.all ? slot : (int64_t)ch.seq) * rec;
@@ -406,13 +407,9 @@ cudaError_t forward(const GdrArgs &p, cudaStream_t stream) {
     cudaError_t e = launch_gdr_terms(p, im, 1, NS, stream);
     if (e != cudaSuccess) return e;
     constexpr int bytes = ChainSmem<NI, DKP, NS, Mode::kForward>::kBytes;
-    e = cudaFuncSetAttribute(gdr_chain_kernel<T, DKP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
     const bool wide = p.d_v % 2 == 0 && ((uintptr_t)p.out % (2 * sizeof(T))) == 0;
-    gdr_chain_kernel<T, DKP, NS><<<chain_blocks(p), kChainThreads, bytes, stream>>>(
-        maps.q, maps.k, maps.v, p, im, 1.f / std::sqrt((float)p.d_k), wide);
-    count_launches(1);
-    return cudaGetLastError();
+    return launch_dependent(gdr_chain_kernel<T, DKP, NS>, chain_blocks(p), kChainThreads, bytes, stream, maps.q, maps.k,
+                            maps.v, p, im, 1.f / std::sqrt((float)p.d_k), wide);
 }
 
 }  // namespace
