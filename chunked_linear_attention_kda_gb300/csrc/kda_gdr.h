@@ -14,6 +14,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <vector>
+
 #include "kda_internal.h"
 #include "kda_ptx.h"
 
@@ -41,9 +43,23 @@ __device__ __forceinline__ int64_t slot_base(const int32_t *cu, int n) {
 // waits here for that one's results.
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Lets a kernel have `smem` bytes of dynamic shared memory on the current device; asked of the
+// runtime once per kernel and device (a call of 1 us in front of kernels of 10).
+inline cudaError_t allow_smem(const void *kernel, int smem) {
+    struct Seen { const void *kernel; int device; };
+    thread_local std::vector<Seen> seen;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    for (const Seen &s : seen)
+        if (s.kernel == kernel && s.device == device) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) seen.push_back({kernel, device});
+    return e;
+}
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, const A &...args) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -169,6 +185,14 @@ __device__ __forceinline__ void key_b_t(uint32_t base, int k0, int n0, uint32_t 
     frag_b_t<128>(base + (n0 >> 6) * kHalf, k0, n0 & 63, b);
 }
 
+// A sum carried as two floats (the fp64 pipe of this part is narrow).
+struct Two { float hi, lo; };
+__device__ __forceinline__ Two add(Two x, Two y) {
+    const float s = x.hi + y.hi, t = s - x.hi;
+    const float e = (x.hi - (s - t)) + (y.hi - t) + (x.lo + y.lo);
+    const float hi = s + e;
+    return {hi, e - (hi - s)};
+}
 // 2^x (0 below the normal range)
 __device__ __forceinline__ float ex2(float x) {
     float y;

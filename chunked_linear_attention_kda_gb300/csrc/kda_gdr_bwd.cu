@@ -442,37 +442,44 @@ __global__ void __launch_bounds__(kLocalThreads)
         }
         __syncthreads();
         if (warp == 0) {  // dbeta, dg: two tokens a lane, running sums over the chunk
-            double a[2], b[2];
             float whole = 0.f;
 #pragma unroll
             for (int i = 0; i < kLocalThreads / 32; ++i) whole += r_ss[i];
             whole *= gate[3 * C];
+            Two a[2], b[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = 2 * lane + i;
                 const float kx = parts(r_kx, r);
                 if (r < ch.len)
                     p.dbeta[(ch.t0 + r) * p.n_heads + head] = r_ev[r] - gam[r] * kx - parts(r_fk, r);
-                a[i] = (double)(gam[r] * (scale * parts(r_qx, r) - bet[r] * kx)) + (double)parts(r_m, r) -
-                       (double)((c_m[r] + c_m[C + r]) + (c_m[2 * C + r] + c_m[3 * C + r]));
-                b[i] = del[r] * parts(r_ku, r);
+                const float cols = (c_m[r] + c_m[C + r]) + (c_m[2 * C + r] + c_m[3 * C + r]);
+                a[i] = add({gam[r] * (scale * parts(r_qx, r) - bet[r] * kx), 0.f}, add({parts(r_m, r), 0.f}, {-cols, 0.f}));
+                b[i] = {del[r] * parts(r_ku, r), 0.f};
             }
-            // inclusive sums over the tokens of a and b
-            double ra = a[0] + a[1], rb = b[0] + b[1];
+            // inclusive sums over the tokens of a and b; a0, b0 before token 2 lane
+            Two ra = add(a[0], a[1]), rb = add(b[0], b[1]);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const double x = __shfl_up_sync(0xffffffffu, ra, o), y = __shfl_up_sync(0xffffffffu, rb, o);
-                if (lane >= o) { ra += x; rb += y; }
+                const Two x = {__shfl_up_sync(0xffffffffu, ra.hi, o), __shfl_up_sync(0xffffffffu, ra.lo, o)};
+                const Two y = {__shfl_up_sync(0xffffffffu, rb.hi, o), __shfl_up_sync(0xffffffffu, rb.lo, o)};
+                if (lane >= o) {
+                    ra = add(x, ra);
+                    rb = add(y, rb);
+                }
             }
-            const double total = __shfl_sync(0xffffffffu, ra, 31);
-            const double a0 = ra - (a[0] + a[1]), b0 = rb - (b[0] + b[1]);  // before token 2 lane
+            const Two total = {__shfl_sync(0xffffffffu, ra.hi, 31), __shfl_sync(0xffffffffu, ra.lo, 31)};
+            Two a0 = {__shfl_up_sync(0xffffffffu, ra.hi, 1), __shfl_up_sync(0xffffffffu, ra.lo, 1)};
+            Two b0 = {__shfl_up_sync(0xffffffffu, rb.hi, 1), __shfl_up_sync(0xffffffffu, rb.lo, 1)};
+            if (lane == 0) a0 = b0 = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = 2 * lane + i;
-                const double sa = total - (i ? a0 + a[0] : a0), sb = i ? b0 + b[0] : b0;
+                const Two before = i ? add(a0, a[0]) : a0, sb = i ? add(b0, b[0]) : b0;
+                const Two sum = add(add(total, {-before.hi, -before.lo}), add({whole, 0.f}, sb));
                 if (r < ch.len) {  // nothing passes a decay of 0: what the sums leave there is rounding
                     const int64_t t = (ch.t0 + r) * p.n_heads + head;
-                    p.dg[t] = p.g[t] < kGFloor ? 0.f : (float)((double)whole + sa + sb);
+                    p.dg[t] = p.g[t] < kGFloor ? 0.f : sum.hi + sum.lo;
                 }
             }
         }

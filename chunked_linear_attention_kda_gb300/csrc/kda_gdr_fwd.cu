@@ -37,14 +37,6 @@ struct TermsSmem {
     static constexpr int kBytes = Vec + 2 * 3 * C * 4;
 };
 
-// A sum carried as two floats.
-struct Two { float hi, lo; };
-__device__ __forceinline__ Two add(Two x, Two y) {
-    const float s = x.hi + y.hi, t = s - x.hi;
-    const float e = (x.hi - (s - t)) + (y.hi - t) + (x.lo + y.lo);
-    const float hi = s + e;
-    return {hi, e - (hi - s)};
-}
 constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596299e-8f;  // log2(e) in two floats
 // 2^(hi + lo), lo far below hi
 __device__ __forceinline__ float exp2_of(float hi, float lo) {
@@ -194,8 +186,8 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
                           p.q_stride, ch.len, p.d_k, vec, tid, kTermThreads);
     ptx::cp_async_commit();
 
-    // The gates of the heads h0 and h0 + 1, a warp each: running sums of g log2(e) in two floats
-    // (the fp64 pipe of this part is narrow), so that differences of neighbours stay exact.
+    // The gates of the heads h0 and h0 + 1, a warp each: running sums of g log2(e) in two floats,
+    // so that differences of neighbours stay exact.
     auto gates = [&](int h0) {
         if (warp >= min(2, group - h0)) return;
         const int head = kh * group + h0 + warp;
@@ -390,7 +382,7 @@ __global__ void __launch_bounds__(kChainThreads)
 template <typename T, int DKP, int NS>
 cudaError_t terms(const GdrArgs &p, const Images &im, int values, cudaStream_t stream) {
     constexpr int bytes = TermsSmem<InputPlanes<T>::N, DKP>::kBytes;
-    const cudaError_t e = cudaFuncSetAttribute(gdr_terms_kernel<T, DKP, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(gdr_terms_kernel<T, DKP, NS>), bytes);
     if (e != cudaSuccess) return e;
     const bool vec = rows_vec<T>(p.q, p.q_stride, p.d_k) && rows_vec<T>(p.k, p.k_stride, p.d_k);
     const dim3 grid((unsigned)n_slots(p.n_tok, p.n_seq), p.n_k_heads);
