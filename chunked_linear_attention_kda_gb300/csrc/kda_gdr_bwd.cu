@@ -29,15 +29,15 @@ namespace gdr {
 namespace {
 
 // the first half of the blocks runs the reverse chains (the longer ones), the second the forward
-template <typename T, int DKP, int NS>
+template <typename T, int DKP, int NS, int PAIRS>
 __global__ void __launch_bounds__(kChainThreads)
     gdr_scan_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                     const GdrArgs p, const Images im, float scale) {
     let_next_kernel_start();
     const unsigned n = gridDim.x / 2;
-    if (blockIdx.x >= n) chain<T, DKP, NS, Mode::kStates>(tm_q, tm_k, tm_v, p, im, 2, blockIdx.x - n, scale, false);
-    else chain<T, DKP, NS, Mode::kReverse>(tm_q, tm_k, tm_do, p, im, 2, blockIdx.x, scale, false);
+    if (blockIdx.x >= n) chain<T, DKP, NS, Mode::kStates, PAIRS>(tm_q, tm_k, tm_v, p, im, 2, blockIdx.x - n, scale, false);
+    else chain<T, DKP, NS, Mode::kReverse, PAIRS>(tm_q, tm_k, tm_do, p, im, 2, blockIdx.x, scale, false);
 }
 
 // ---------------------------------------------------------------- local gradients
@@ -542,10 +542,19 @@ cudaError_t backward(const GdrArgs &p, cudaStream_t stream) {
                                                 (size_t)n_slots(p.n_tok, p.n_seq) * p.n_heads * scan_bytes(NS, DKP, p.d_v)};
     cudaError_t e = launch_gdr_terms(p, im, 2, NS, stream);
     if (e != cudaSuccess) return e;
-    constexpr int fwd = ChainSmem<NI, DKP, NS, Mode::kStates>::kBytes, rev = ChainSmem<NI, DKP, NS, Mode::kReverse>::kBytes;
-    constexpr int scan = fwd > rev ? fwd : rev;
-    e = launch_dependent(gdr_scan_kernel<T, DKP, NS>, 2 * chain_blocks(p), kChainThreads, scan, stream, maps.q, maps.k,
-                         maps.v, maps.dout, p, im, scale);
+    auto scan = [&](auto kernel, int pairs, int fwd, int rev) {
+        return launch_dependent(kernel, 2 * chain_blocks(p, pairs), kChainThreads, fwd > rev ? fwd : rev, stream, maps.q,
+                                maps.k, maps.v, maps.dout, p, im, scale);
+    };
+    bool wide_scan = false;
+    if constexpr (NS == 2) wide_scan = scan_pairs(p) == 4;
+    if constexpr (NS == 2)
+        if (wide_scan)
+            e = scan(gdr_scan_kernel<T, DKP, NS, 4>, 4, ChainSmem<NI, DKP, NS, Mode::kStates, 4>::kBytes,
+                     ChainSmem<NI, DKP, NS, Mode::kReverse, 4>::kBytes);
+    if (!wide_scan)
+        e = scan(gdr_scan_kernel<T, DKP, NS, 2>, 2, ChainSmem<NI, DKP, NS, Mode::kStates, 2>::kBytes,
+                 ChainSmem<NI, DKP, NS, Mode::kReverse, 2>::kBytes);
     if (e != cudaSuccess || p.n_tok == 0) return e;
     auto wide = [](const void *x, int d) { return d % 2 == 0 && ((uintptr_t)x % (2 * sizeof(T))) == 0; };
     return launch_dependent(gdr_local_kernel<T, DKP, NS>, dim3((unsigned)n_slots(p.n_tok, p.n_seq), p.n_k_heads),

@@ -2,20 +2,20 @@
 // backward pass with a record of every chunk's state) and the backward's reverse one. The
 // mathematics is in kda_gdr_fwd.cu and kda_gdr_bwd.cu. Internal; not part of the C ABI.
 //
-// A CTA advances 32 value channels of one (sequence, head) through the sequence:
-//   warps 0..3  the state, a pair of warps to 16 value channels. S^T (16 x d_k) is held as bf16
-//               planes by both warps and in fp32 by halves of d_k. An accumulator tile of
-//               mma.sync lies in registers as the A operand of the next product, so a warp goes
-//               S^T -> Y^T -> Z^T -> U^T without leaving its registers; each warp of a pair
-//               takes one half of the chunk's tokens, then one half of d_k in the update of S,
-//               and the pair exchanges its halves of U^T and S^T through shared memory at three
-//               barriers of 64 threads.
-//   warps 4..7  what the serial path need not wait for, a pair to 16 value channels: the output
-//               O (from copies of S^T and U^T left in shared memory) or, in reverse, dO^T P and
-//               (gamma dO)^T Q, handed to the state warps ahead of their use.
-//   warp 8      one thread loads: tensor copies of whole chunks, bulk copies of the chunk terms
-//               and of tile images, into rings of stages (one ring for what the state warps
-//               read, one for the others').
+// A CTA of nine warps advances 16 value channels per pair of state warps through a sequence:
+//   state warps   S^T (16 x d_k) is held as bf16 planes by both warps of a pair and in fp32 by
+//                 halves of d_k. An accumulator tile of mma.sync lies in registers as the A
+//                 operand of the next product, so a warp goes S^T -> Y^T -> Z^T -> U^T without
+//                 leaving its registers; each warp of a pair takes one half of the chunk's
+//                 tokens, then one half of d_k in the update of S, and the pair exchanges its
+//                 halves of Z^T, U^T and S^T through shared memory at barriers of 64 threads.
+//   the last warp one thread loads: tensor copies of whole chunks, bulk copies of the chunk
+//                 terms and of tile images, into rings of stages.
+// With two pairs the other four warps take what the serial path need not wait for: the output
+// O (from copies of S^T and U^T left in shared memory) or, in reverse, dO^T P and (gamma dO)^T
+// Q, handed to the state warps ahead of their use. With four pairs (the backward pass, when
+// there are more chains than SMs) the state warps do that themselves: a step is longer but
+// covers twice the channels, and each scheduler has two state warps to choose from.
 // Per chunk a state warp issues about 170 mma.sync m16n8k16 (bf16, d_k = 128) of 8 cycles each:
 // 0.7 us bound a step from below; the rest is the latency of the hand-offs.
 #pragma once
@@ -30,7 +30,6 @@ namespace gdr {
 
 enum class Mode { kForward, kStates, kReverse };
 constexpr int kChainThreads = 288;
-constexpr int kBlockV = 32;  // value channels of a CTA
 constexpr long long kWaitLimit = 4000000000LL;  // SM cycles, about two seconds
 
 static __device__ unsigned int g_gdr_flags;  // bit 4: a pipeline wait exceeded its limit
@@ -87,14 +86,15 @@ __device__ __forceinline__ void bulk_wait0() { asm volatile("cp.async.bulk.wait_
 
 // Shared memory (offsets from a 1024-byte boundary). Ring 1 (state warps): K, X, gates and,
 // forward, V. Ring 2 (the others): Q, P, gates and, reverse, dO. Per pair: Sx the planes of
-// S^T and Uo those of U^T (both read by the output warps), Ux the scaled planes of U^T that
+// S^T and Uo U^T itself (both read by the output warps), Ux the scaled planes of U^T that
 // the pair exchanges, Zx those of the first half's Z^T; Hand the accumulators handed over in
 // reverse; Keep the staging of the records that go to the workspace (bf16; fp32 inputs, whose
 // tiles leave no room for it, store them from registers).
-template <int NI, int DKP, int NS, Mode M>
+template <int NI, int DKP, int NS, Mode M, int PAIRS>
 struct ChainSmem {
+    static constexpr bool kHelp = PAIRS == 2;
     static constexpr bool kOut = M == Mode::kForward, kRev = M == Mode::kReverse;
-    static constexpr int kKey = NI * C * DKP * 2, kVal = NI * C * kBlockV * 2;
+    static constexpr int kKey = NI * C * DKP * 2, kSlice = NI * C * 64, kVal = PAIRS / 2 * kSlice;
     static constexpr int kX = NS * kTri;
     static constexpr int kP = (kOut ? NI : NS) * kTri;       // the output takes P in bf16 for bf16
     static constexpr int kGate = kChainGates * 4;
@@ -105,21 +105,21 @@ struct ChainSmem {
     // ring 2
     static constexpr int Q = 0, dO = Q + kKey, P = dO + (kRev ? kVal : 0), Gate2 = P + kP;
     static constexpr int kStage2 = (Gate2 + kGate + 1023) / 1024 * 1024;
-    static constexpr int N2 = M == Mode::kStates ? 0 : NS == 2 ? 2 : 1;
+    static constexpr int N2 = M == Mode::kStates ? 0 : NS == 2 && kHelp ? 2 : 1;
     // per pair
     static constexpr int NH = kOut && NS == 2 ? 2 : 1;            // buffers of Sx and Uo
     static constexpr int kSx = NS * (DKP / 16) * 512, kUx = NS * 4 * 512, kZx = NS * 2 * 512;
-    static constexpr int kUo = kOut ? kUx : 0;
-    static constexpr int kHandG = DKP * 64, kHand = kRev ? kHandG + C * 64 : 0;
+    static constexpr int kUo = kOut ? C * 64 : 0;
+    static constexpr int kHandG = DKP * 64, kHand = kRev && kHelp ? kHandG + C * 64 : 0;
     static constexpr int kKeepS = NS * 16 * DKP * 2, kKeepU = NS * 16 * C * 2;
     static constexpr int kKeep = kOut || NI == 3 ? 0 : kKeepS + kKeepU;
     static constexpr int Sx = 0, Uo = Sx + NH * kSx, Ux = Uo + NH * kUo, Zx = Ux + kUx, Hand = Zx + kZx, Keep = Hand + kHand;
     static constexpr int kPair = Keep + kKeep;
-    static constexpr int Ring2 = N1 * kStage1, Pairs = Ring2 + N2 * kStage2, Bars = Pairs + 2 * kPair;
-    static constexpr int kBars = 2 * N1 + 2 * N2 + 4 * NH;
+    static constexpr int Ring2 = N1 * kStage1, Pairs = Ring2 + N2 * kStage2, Bars = Pairs + PAIRS * kPair;
+    static constexpr int kBars = 2 * N1 + 2 * N2 + (kHelp ? 4 * NH : 0);
     static constexpr int kBytes = Bars + 8 * kBars + 1024;        // the base is rounded up to 1024
     static_assert(kBytes <= 226 * 1024, "fits an SM");
-    static_assert(kKey % 1024 == 0 && kVal % 1024 == 0, "tensor copies land on swizzle boundaries");
+    static_assert(kKey % 1024 == 0 && kSlice % 1024 == 0, "tensor copies land on swizzle boundaries");
 };
 
 // The tensor maps of q, k and v (and dout); make() is false when the inputs need images.
@@ -157,13 +157,21 @@ struct ChainMaps {
         if (with_dout && !rows_vec<T>(p.dout, vs, p.d_v)) return false;
         return encode(&q, p.q, p.n_tok, p.q_stride, p.n_k_heads, p.d_k, 64) &&
                encode(&k, p.k, p.n_tok, p.k_stride, p.n_k_heads, p.d_k, 64) &&
-               encode(&v, p.v, p.n_tok, p.v_stride, p.n_heads, p.d_v, kBlockV) &&
-               (!with_dout || encode(&dout, p.dout, p.n_tok, vs, p.n_heads, p.d_v, kBlockV));
+               encode(&v, p.v, p.n_tok, p.v_stride, p.n_heads, p.d_v, 32) &&
+               (!with_dout || encode(&dout, p.dout, p.n_tok, vs, p.n_heads, p.d_v, 32));
     }
 };
 
-inline unsigned chain_blocks(const GdrArgs &p) {
-    return (unsigned)((p.d_v + kBlockV - 1) / kBlockV) * p.n_heads * p.n_seq;
+inline unsigned chain_blocks(const GdrArgs &p, int pairs) {
+    return (unsigned)((p.d_v + 16 * pairs - 1) / (16 * pairs)) * p.n_heads * p.n_seq;
+}
+// Pairs of the backward pass's chains. At 512 CTAs of two pairs (two sequences of 8K tokens, 32
+// heads, forward and reverse) a step takes 3500 (forward) and 4600 cycles (reverse), 1.12 ms in
+// all; as 256 CTAs of four pairs 4450 and 7800 cycles, 0.87 ms. The forward pass itself gains
+// nothing from four (the output would lengthen its step to over 6500 cycles).
+inline int scan_pairs(const GdrArgs &p) {
+    constexpr unsigned kSMs = 152;
+    return p.d_v > 32 && 2 * chain_blocks(p, 2) > kSMs ? 4 : 2;
 }
 
 // The sequence of the given rank, longest first (ties by index): the longest chains start
@@ -187,8 +195,9 @@ __device__ __forceinline__ int ranked_sequence(const int32_t *cu, int n_seq, int
 
 // y (16 x 16, tokens n0 ..) = S^T K^T from the planes of S^T; the products of lower planes run
 // on accumulators of their own, so that no product waits for the one before it
+// (the planes of half h of the key channels come first)
 template <int NI, int NS, int DKP>
-__device__ __forceinline__ void state_times_keys(const uint32_t (*a)[DKP / 16][4], uint32_t k, int n0, float (*y)[4]) {
+__device__ __forceinline__ void state_times_keys(const uint32_t (*a)[DKP / 16][4], uint32_t k, int h, int n0, float (*y)[4]) {
     float lo[2][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[0][i] = y[1][i] = lo[0][i] = lo[1][i] = 0.f;
@@ -197,7 +206,8 @@ __device__ __forceinline__ void state_times_keys(const uint32_t (*a)[DKP / 16][4
 #pragma unroll
         for (int pb = 0; pb < NI; ++pb) {
             uint32_t b[4];
-            key_b(k + pb * C * DKP * 2, n0, kx * 16, b);
+            const int half = kx < DKP / 32 ? h : 1 - h;
+            key_b(k + pb * C * DKP * 2, n0, half * (DKP / 2) + (kx % (DKP / 32)) * 16, b);
 #pragma unroll
             for (int pa = 0; pa + pb < NS; ++pa) {
                 ptx::mma16816(pa + pb ? lo[0] : y[0], a[pa][kx], b[0], b[1]);
@@ -256,6 +266,126 @@ __device__ __forceinline__ void get_block(const char *p, int plane, uint32_t (*a
         a[q][0] = x.x; a[q][1] = x.y; a[q][2] = x.z; a[q][3] = x.w;
     }
 }
+// ---- the output, 32 tokens x 16 value channels: o[m][n], token blocks m0 + m
+
+// o += Q S0, key channels of block kx; a the planes of S^T
+template <int NI, int DKP>
+__device__ __forceinline__ void add_queries(const uint32_t (*a)[4], uint32_t q, int m0, int kx, float (*o)[2][4]) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int pq = 0; pq < NI; ++pq) {
+            uint32_t f[4];
+            key_a(q + pq * C * DKP * 2, (m0 + m) * 16, kx * 16, f);
+#pragma unroll
+            for (int pa = 0; pa + pq < NI; ++pa) {
+                ptx::mma16816(o[m][0], f, a[pa][0], a[pa][2]);
+                ptx::mma16816(o[m][1], f, a[pa][1], a[pa][3]);
+            }
+        }
+}
+__device__ __forceinline__ void scale_output(float (*o)[2][4], const float *gate, float scale, int m0) {
+    const int gr = (threadIdx.x & 31) >> 2;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const int r = (m0 + m) * 16 + gr;
+        const float g0 = scale * gate[r], g1 = scale * gate[r + 8];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            o[m][n][0] *= g0; o[m][n][1] *= g0; o[m][n][2] *= g1; o[m][n][3] *= g1;
+        }
+    }
+}
+// o += P U for the tokens of half h; uo the pair's U^T (fp32 accumulators)
+template <int NI, int NS>
+__device__ __forceinline__ void add_p_values(const char *uo, uint32_t pt, int h, float (*o)[2][4]) {
+#pragma unroll
+    for (int kx = 0; kx < 4; ++kx) {
+        if (kx > 2 * h + 1) break;
+        uint32_t a[NS][4];
+        float u[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const float4 x = *reinterpret_cast<const float4 *>(uo + ((2 * kx + n) * 32 + (threadIdx.x & 31)) * 16);
+            u[n][0] = x.x; u[n][1] = x.y; u[n][2] = x.z; u[n][3] = x.w;
+        }
+        acc_to_a<NS>(u, a);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            if (kx > 2 * h + m) continue;
+#pragma unroll
+            for (int pq = 0; pq < NI; ++pq) {
+                uint32_t f[4];
+                frag_a<32>(pt + pq * kTri + tri_block(2 * h + m, kx), 0, 0, f);
+#pragma unroll
+                for (int pa = 0; pa + pq < NS; ++pa) {
+                    ptx::mma16816(o[m][0], f, a[pa][0], a[pa][2]);
+                    ptx::mma16816(o[m][1], f, a[pa][1], a[pa][3]);
+                }
+            }
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_output(T *out, const float (*o)[2][4], int row0, int m0, int v0, int64_t tok0,
+                                             int len, int head, const GdrArgs &p, bool wide) {
+    const int gr = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int r = row0 + (m0 + m) * 16 + gr + x * 8;
+            if (r >= len) continue;
+            T *row = out + ((tok0 + r) * p.n_heads + head) * p.d_v;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int v = v0 + n * 8 + tq * 2;
+                if (v < p.d_v) put2(row + v, o[m][n][x * 2], o[m][n][x * 2 + 1], wide, v + 1 < p.d_v);
+            }
+        }
+}
+
+// ---- the reverse chain's products with dO (a slice of 32 channels; channel half w of it)
+
+template <int NI>
+__device__ __forceinline__ void frag_dout(uint32_t dout, int kx, int w, uint32_t (*a)[4]) {
+#pragma unroll
+    for (int q = 0; q < NI; ++q) frag_a_t<64>(dout + q * C * 64, kx * 16, w * 16, a[q]);
+}
+// y (16 x 16) += dO^T P, P's block at `pt`
+template <int NI, int NS>
+__device__ __forceinline__ void add_dout_p(const uint32_t (*a)[4], uint32_t pt, float (*y)[4]) {
+#pragma unroll
+    for (int pb = 0; pb < NS; ++pb) {
+        uint32_t b[4];
+        frag_b_t<32>(pt + pb * kTri, 0, 0, b);
+#pragma unroll
+        for (int pa = 0; pa < NI && pa + pb < NS; ++pa) {
+            ptx::mma16816(y[0], a[pa], b[0], b[1]);
+            ptx::mma16816(y[1], a[pa], b[2], b[3]);
+        }
+    }
+}
+// planes of (s gamma dO)^T
+template <int NI, int NS>
+__device__ __forceinline__ void scale_dout(const uint32_t (*a)[4], const float *gate, float scale, int kx, uint32_t (*d)[4]) {
+    const int tq = threadIdx.x & 3;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 ga = *reinterpret_cast<const float2 *>(gate + kx * 16 + (j >> 1) * 8 + tq * 2);
+        float x = 0.f, z = 0.f;
+#pragma unroll
+        for (int q = 0; q < NI; ++q) {
+            x += lo_f(a[q][j]);
+            z += hi_f(a[q][j]);
+        }
+        uint32_t sp[NS];
+        split2<NS>(x * (scale * ga.x), z * (scale * ga.y), sp);
+#pragma unroll
+        for (int q = 0; q < NS; ++q) d[q][j] = sp[q];
+    }
+}
+
 template <int N>
 __device__ __forceinline__ void zero(float (*x)[4]) {
 #pragma unroll
@@ -288,21 +418,21 @@ __device__ __forceinline__ void store_state(const float (*S)[4], float *dst, int
 
 // One CTA's chain; `block` counts channel blocks, then heads, then sequences (longest first).
 // tm_v is dout's map in reverse; `values` and `im` as given to the chunk terms.
-template <typename T, int DKP, int NS, Mode M>
+template <typename T, int DKP, int NS, Mode M, int PAIRS>
 __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                                       const GdrArgs &p, const Images &im, int values, int block, float scale,
                                       bool wide_out) {
     constexpr int NI = InputPlanes<T>::N;
-    using L = ChainSmem<NI, DKP, NS, M>;
+    using L = ChainSmem<NI, DKP, NS, M, PAIRS>;
     constexpr int NT = DKP / 16, KX = DKP / 16, N1 = L::N1, N2 = L::N2, NH = L::NH;
-    constexpr bool kOut = L::kOut, kRev = L::kRev;
+    constexpr bool kOut = L::kOut, kRev = L::kRev, kHelp = L::kHelp;
     extern __shared__ __align__(1024) char smem_raw[];
     char *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_u32(smem);
     __shared__ int ranked;
     wait_for_previous_kernel();  // the chunk terms
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
-    const int n_blk = (p.d_v + kBlockV - 1) / kBlockV;
+    const int n_blk = (p.d_v + 16 * PAIRS - 1) / (16 * PAIRS);
     const int blk = block % n_blk, sh = block / n_blk;
     const int head = sh % p.n_heads, kh = head / (p.n_heads / p.n_k_heads);
     const int seq = ranked_sequence(p.cu_seqlens, p.n_seq, sh / p.n_heads, &ranked);
@@ -311,7 +441,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
     const int n_chunks = (len + C - 1) / C;
     const int64_t slot0 = slot_base(p.cu_seqlens, seq);
     // pair w of the CTA's 16-channel halves; half h of its tokens and of d_k
-    const int w = (warp >> 1) & 1, h = warp & 1, v0 = blk * kBlockV + w * 16;
+    const int w = (warp >> 1) & (PAIRS - 1), h = warp & 1, v0 = (blk * PAIRS + w) * 16;
     const size_t st_at = ((size_t)seq * p.n_heads + head) * p.d_k * p.d_v;
     char *ws = static_cast<char *>(p.workspace);
     char *pair = smem + L::Pairs + w * L::kPair;
@@ -324,9 +454,10 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
     auto hfull = [&](int b) { return bar(2 * N1 + 2 * N2 + b * 2 + w); };
     auto hempty = [&](int b) { return bar(2 * N1 + 2 * N2 + 2 * NH + b * 2 + w); };
     if (tid == 0) {
-        for (int s = 0; s < N1; ++s) { ptx::mbar_init(full1(s), 1); ptx::mbar_init(empty1(s), 4); }
-        for (int s = 0; s < N2; ++s) { ptx::mbar_init(full2(s), 1); ptx::mbar_init(empty2(s), 4); }
-        for (int b = 0; b < 4 * NH; ++b) ptx::mbar_init(bar(2 * N1 + 2 * N2 + b), 2);
+        for (int s = 0; s < N1; ++s) { ptx::mbar_init(full1(s), 1); ptx::mbar_init(empty1(s), 2 * PAIRS); }
+        for (int s = 0; s < N2; ++s) { ptx::mbar_init(full2(s), 1); ptx::mbar_init(empty2(s), kHelp ? 4 : 8); }
+        if (kHelp)
+            for (int b = 0; b < 4 * NH; ++b) ptx::mbar_init(bar(2 * N1 + 2 * N2 + b), 2);
         ptx::mbar_init_fence();
     }
     __syncthreads();
@@ -338,6 +469,14 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
         if (lane == 0) {
             const size_t rec = Images::record(NI, DKP, p.d_v, p.n_k_heads, p.n_heads, values);
             const size_t kb = Images::key_bytes(NI, DKP), vb = Images::value_bytes(NI, p.d_v);
+            // 32-channel slices of v (dout) that this CTA has; a pair past them works on what lies there
+            const int slices = min(PAIRS / 2, pad_v(p.d_v) / 32 - blk * (PAIRS / 2));
+            const int c32 = blk * (PAIRS / 2) * 32;
+            auto load_values = [&](uint32_t d, bool image, const char *vimg, int t, uint32_t m) {
+                if (image) bulk_load(d, vimg, slices * L::kSlice, m);
+                else
+                    for (int x = 0; x < slices; ++x) ptx::tma_load_3d(d + x * L::kSlice, &tm_v, c32 + x * 32, head, t, m);
+            };
             int done1 = 0, done2 = 0;
             bool ok = true;
             for (int i = 0; i < n_chunks && ok; ++i) {
@@ -350,15 +489,14 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                     const int s = i % N1;
                     const uint32_t d = base + s * L::kStage1, m = full1(s);
                     if (!(ok = wait_bar(empty1(s), ((i / N1) & 1) ^ 1))) break;
-                    ptx::mbar_arrive_tx(m, L::kKey + (kRev ? 0 : L::kVal) + L::kX + L::kGate);
+                    ptx::mbar_arrive_tx(m, L::kKey + (kRev ? 0 : slices * L::kSlice) + L::kX + L::kGate);
                     if (image) {
                         bulk_load(d + L::K, img + (p.n_k_heads + kh) * kb, L::kKey, m);
-                        if (!kRev) bulk_load(d + L::V, vimg, L::kVal, m);
                     } else {
 #pragma unroll
                         for (int h = 0; h < DKP / 64; ++h) ptx::tma_load_3d(d + L::K + h * kHalf, &tm_k, h * 64, kh, t, m);
-                        if (!kRev) ptx::tma_load_3d(d + L::V, &tm_v, blk * kBlockV, head, t, m);
                     }
+                    if (!kRev) load_values(d + L::V, image, vimg, t, m);
                     bulk_load(d + L::X, terms, L::kX, m);
                     bulk_load(d + L::Gate1, terms + 2 * NS * kTri, L::kGate, m);
                     ++done1;
@@ -367,15 +505,14 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                     const int s = i % N2;
                     const uint32_t d = base + L::Ring2 + s * L::kStage2, m = full2(s);
                     if (!(ok = wait_bar(empty2(s), ((i / N2) & 1) ^ 1))) break;
-                    ptx::mbar_arrive_tx(m, L::kKey + (kRev ? L::kVal : 0) + L::kP + L::kGate);
+                    ptx::mbar_arrive_tx(m, L::kKey + (kRev ? slices * L::kSlice : 0) + L::kP + L::kGate);
                     if (image) {
                         bulk_load(d + L::Q, img + kh * kb, L::kKey, m);
-                        if (kRev) bulk_load(d + L::dO, vimg, L::kVal, m);
                     } else {
 #pragma unroll
                         for (int h = 0; h < DKP / 64; ++h) ptx::tma_load_3d(d + L::Q + h * kHalf, &tm_q, h * 64, kh, t, m);
-                        if (kRev) ptx::tma_load_3d(d + L::dO, &tm_v, blk * kBlockV, head, t, m);
                     }
+                    if (kRev) load_values(d + L::dO, image, vimg, t, m);
                     bulk_load(d + L::P, terms + NS * kTri, L::kP, m);
                     bulk_load(d + L::Gate2, terms + 2 * NS * kTri, L::kGate, m);
                     ++done2;
@@ -387,7 +524,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                     for (int i = max(0, done2 - N2); i < done2; ++i) drain_bar(full2(i % N2), (i / N2) & 1);
             }
         }
-    } else if (warp < 4) {
+    } else if (warp < 2 * PAIRS) {
         // ------------------------------------------------ state
         // A failed wait ends no warp of a pair before the other (their barriers would hang): the
         // step goes on with what is there, and with the flag set no later wait waits.
@@ -399,12 +536,12 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
         const int t0 = 2 * h, o0 = 2 - t0;             // this half's, the other half's first 16-token block
         auto meet = [&]() { ptx::named_sync(1 + w, 64); };
         float S[NT][4];                                // key channels h DKP / 2 ..
-        uint32_t sp[NS][KX][4];                        // all key channels, as planes
+        uint32_t sp[NS][KX][4];                        // all key channels as planes, this half's first
         const int c0 = h * (DKP / 2);
         load_state<NT>(S, kRev ? (p.dh_final ? p.dh_final + st_at : nullptr) : (p.h0 ? p.h0 + st_at : nullptr), c0, v0,
                        p.d_k, p.d_v);
         const size_t rec_s = scan_state_bytes(NS, DKP, p.d_v), rec_u = scan_value_bytes(NS, p.d_v), vp = pad_v(p.d_v);
-        char *keep = pair + L::Keep;
+        [[maybe_unused]] char *keep = pair + L::Keep;
         // this half's planes of S^T to the pair's buffer, the other half's from it
         auto share_state = [&](int hb) {
             char *sx = pair + L::Sx + hb * L::kSx;
@@ -416,10 +553,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                 for (int q = 0; q < NS; ++q)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {  // static register indexes for either half
-                        if (h == 0) sp[q][i][x] = a[q][x];
-                        else sp[q][KX / 2 + i][x] = a[q][x];
-                    }
+                    for (int x = 0; x < 4; ++x) sp[q][i][x] = a[q][x];
             }
             meet();
 #pragma unroll
@@ -429,10 +563,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                 for (int q = 0; q < NS; ++q)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        if (h == 0) sp[q][KX / 2 + i][x] = a[q][x];
-                        else sp[q][i][x] = a[q][x];
-                    }
+                    for (int x = 0; x < 4; ++x) sp[q][KX / 2 + i][x] = a[q][x];
             }
         };
         if (n_chunks > 0) share_state(0);
@@ -444,7 +575,10 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
             char *rec = ws + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
                         ((slot0 + c) * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v);
             if (!ready) wait_bar(full1(s1), (i / N1) & 1);
-            if (kRev) wait_bar(hfull(hb), (i / NH) & 1);
+            if (kRev && kHelp) wait_bar(hfull(hb), (i / NH) & 1);
+            [[maybe_unused]] const int s2 = N2 > 0 ? i % (N2 > 0 ? N2 : 1) : 0;
+            [[maybe_unused]] const uint32_t r2 = base + L::Ring2 + s2 * L::kStage2;
+            if (!kHelp && N2 > 0 && kRev) wait_bar(full2(s2), (i / (N2 > 0 ? N2 : 1)) & 1);
             __syncwarp();
 
             // this half's tokens: forward Y^T, then beta Z^T; in reverse dU^T
@@ -453,7 +587,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
             for (int b = 0; b < 2; ++b) {
                 const int tb = t0 + b;
                 float y[2][4];
-                state_times_keys<NI, NS, DKP>(sp, s + L::K, tb * 16, y);
+                state_times_keys<NI, NS, DKP>(sp, s + L::K, h, tb * 16, y);
                 if (!kRev) {  // beta Z^T = beta (V^T - gamma Y^T)
                     float v[8];
 #pragma unroll
@@ -461,8 +595,8 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                     for (int q = 0; q < NI; ++q) {
                         uint32_t x[4];
-                        ptx::ldsm_x4_t(s + L::V + q * C * kBlockV * 2 +
-                                           tile_off<64>(tb * 16 + (lane >> 4) * 8 + (lane & 7), w * 16 + ((lane >> 3) & 1) * 8),
+                        ptx::ldsm_x4_t(s + L::V + (w >> 1) * L::kSlice + q * C * 64 +
+                                           tile_off<64>(tb * 16 + (lane >> 4) * 8 + (lane & 7), (w & 1) * 16 + ((lane >> 3) & 1) * 8),
                                        x[0], x[1], x[2], x[3]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -485,12 +619,21 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                     for (int n = 0; n < 2; ++n) {
                         const int t = 2 * tb + n;
                         const float2 de = *reinterpret_cast<const float2 *>(gate + C + t * 8 + tq * 2);
-                        const float4 x = *reinterpret_cast<const float4 *>(pair + L::Hand + L::kHandG + (t * 32 + lane) * 16);
+                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (kHelp) x = *reinterpret_cast<const float4 *>(pair + L::Hand + L::kHandG + (t * 32 + lane) * 16);
                         y[n][0] = fmaf(de.x, y[n][0], x.x);
                         y[n][1] = fmaf(de.y, y[n][1], x.y);
                         y[n][2] = fmaf(de.x, y[n][2], x.z);
                         y[n][3] = fmaf(de.y, y[n][3], x.w);
                     }
+                    if constexpr (kRev && !kHelp)
+#pragma unroll
+                        for (int kx = 0; kx < 4; ++kx)
+                            if (kx >= tb) {
+                                uint32_t f[NI][4];
+                                frag_dout<NI>(r2 + L::dO + (w >> 1) * L::kSlice, kx, w & 1, f);
+                                add_dout_p<NI, NS>(f, r2 + L::P + tri_block(kx, tb), y);
+                            }
                 }
                 acc_to_a<NS>(y, z[b]);
             }
@@ -500,13 +643,9 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                 for (int q = 0; q < NS; ++q)
 #pragma unroll
-                    for (int x = 0; x < KX / 2; ++x) {
-                        uint32_t f[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) f[y] = h == 0 ? sp[q][x][y] : sp[q][KX / 2 + x][y];
+                    for (int x = 0; x < KX / 2; ++x)
                         store_block(ptx::smem_u32(keep) + q * 16 * DKP * 2 +
-                                        tile_off<DKP * 2>(lane & 15, c0 + x * 16 + (lane >> 4) * 8), f);
-                    }
+                                        tile_off<DKP * 2>(lane & 15, c0 + x * 16 + (lane >> 4) * 8), sp[q][x]);
             }
             // U^T = (beta Z)^T X^T (X lower triangular), in reverse E^T = dU^T X: each half's diagonal
             // block by its own warp; the block between the halves by the second warp, which gets
@@ -538,9 +677,13 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     uint32_t a[NS][4];
-                    acc_to_a<NS>(&u[2 * b], a);
-                    if constexpr (kOut) put_block<NS>(pair + L::Uo + hb * L::kUo + (t0 + b) * kBlk, kUP, a);
-                    else if constexpr (L::kKeep > 0) {
+                    if constexpr (!kOut) acc_to_a<NS>(&u[2 * b], a);
+                    if constexpr (kOut) {  // in fp32: the output warps, which have the time, split it
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+                            *reinterpret_cast<float4 *>(pair + L::Uo + hb * L::kUo + ((2 * (t0 + b) + n) * 32 + lane) * 16) =
+                                make_float4(u[2 * b + n][0], u[2 * b + n][1], u[2 * b + n][2], u[2 * b + n][3]);
+                    } else if constexpr (L::kKeep > 0) {
 #pragma unroll
                         for (int q = 0; q < NS; ++q)
                             store_block(ptx::smem_u32(keep) + L::kKeepS + q * 16 * C * 2 +
@@ -570,19 +713,29 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                 }
                 if (kOut) warp_arrive(hfull(hb));
             };
-            // S = Gamma S (+ G, in reverse) while the other warp finishes its half
+            // S = Gamma S (+ G = (s gamma dO)^T Q, in reverse) while the other warp finishes its half
             const float whole = gate[3 * C];
             auto decay = [&]() {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (kRev) x = *reinterpret_cast<const float4 *>(pair + L::Hand + ((h * NT + n) * 32 + lane) * 16);
+                    if (kRev && kHelp) x = *reinterpret_cast<const float4 *>(pair + L::Hand + ((h * NT + n) * 32 + lane) * 16);
                     S[n][0] = fmaf(whole, S[n][0], x.x);
                     S[n][1] = fmaf(whole, S[n][1], x.y);
                     S[n][2] = fmaf(whole, S[n][2], x.z);
                     S[n][3] = fmaf(whole, S[n][3], x.w);
                 }
-                if (kRev) warp_arrive(hempty(hb));
+                if (kRev && kHelp) warp_arrive(hempty(hb));
+                if constexpr (kRev && !kHelp) {
+#pragma unroll
+                    for (int kx = 0; kx < 4; ++kx) {
+                        uint32_t f[NI][4], d[NS][4];
+                        frag_dout<NI>(r2 + L::dO + (w >> 1) * L::kSlice, kx, w & 1, f);
+                        scale_dout<NI, NS>(f, gate, scale, kx, d);
+                        add_values_keys<NI, NS, DKP>(d, r2 + L::Q, kx * 16, c0, S);
+                    }
+                    warp_arrive(empty2(s2));
+                }
             };
             finish();
             decay();
@@ -613,8 +766,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             *reinterpret_cast<uint32_t *>(rec + (kRev ? rec_s : 0) + q * vp * DKP * 2 +
-                                                          tile_off<DKP * 2>(v0 + gr + (y & 1) * 8, c0 + x * 16 + (y >> 1) * 8 + tq * 2)) =
-                                h == 0 ? sp[q][x][y] : sp[q][KX / 2 + x][y];
+                                                          tile_off<DKP * 2>(v0 + gr + (y & 1) * 8, c0 + x * 16 + (y >> 1) * 8 + tq * 2)) = sp[q][x][y];
             }
             if constexpr (L::kKeep > 0) ptx::fence_proxy_async();
             if (!drained)  // the output that read the next step's buffers is done
@@ -623,7 +775,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
             share_state((i + 1) % NH);
             if constexpr (L::kKeep > 0) {
                 // both halves are staged (the barrier in share_state): one lane sends the record
-                if (h == 0 && lane == 0) {
+                if (h == 0 && lane == 0 && v0 < vp) {
 #pragma unroll
                     for (int q = 0; q < NS; ++q) {
                         bulk_store(rec + (kRev ? rec_s : 0) + (q * vp + v0) * DKP * 2, ptx::smem_u32(keep) + q * 16 * DKP * 2,
@@ -640,12 +792,10 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
         if (end) store_state<NT>(S, end + st_at, c0, v0, p.d_k, p.d_v);
     } else if constexpr (kOut) {
         // ------------------------------------------------ output: O = s gamma Q S0 + (s P) U, half h
-        T *out = static_cast<T *>(p.out);
         for (int i = 0; i < n_chunks; ++i) {
             const int s2 = i % N2, hb = i % NH;
             const uint32_t s = base + L::Ring2 + s2 * L::kStage2;
             const float *gate = reinterpret_cast<const float *>(smem + L::Ring2 + s2 * L::kStage2 + L::Gate2);
-            const char *sx = pair + L::Sx + hb * L::kSx, *uo = pair + L::Uo + hb * L::kUo;
             if (!warp_wait(full2(s2), (i / N2) & 1)) break;
             if (!warp_wait(hfull(hb), (i / NH) & 1)) break;
             float o[2][2][4];
@@ -653,66 +803,16 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
             for (int kx = 0; kx < KX; ++kx) {
                 uint32_t a[NI][4];
-                get_block<NI>(sx + kx * 512, KX * 512, a);
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int pq = 0; pq < NI; ++pq) {
-                        uint32_t f[4];
-                        key_a(s + L::Q + pq * C * DKP * 2, (2 * h + m) * 16, kx * 16, f);
-#pragma unroll
-                        for (int pa = 0; pa + pq < NI; ++pa) {
-                            ptx::mma16816(o[m][0], f, a[pa][0], a[pa][2]);
-                            ptx::mma16816(o[m][1], f, a[pa][1], a[pa][3]);
-                        }
-                    }
+                get_block<NI>(pair + L::Sx + hb * L::kSx + kx * 512, KX * 512, a);
+                add_queries<NI, DKP>(a, s + L::Q, 2 * h, kx, o);
             }
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int r = (2 * h + m) * 16 + gr;
-                const float g0 = scale * gate[r], g1 = scale * gate[r + 8];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    o[m][n][0] *= g0; o[m][n][1] *= g0; o[m][n][2] *= g1; o[m][n][3] *= g1;
-                }
-            }
-#pragma unroll
-            for (int kx = 0; kx < 4; ++kx) {
-                if (kx > 2 * h + 1) break;
-                uint32_t a[NS][4];
-                get_block<NS>(uo + kx * 512, 4 * 512, a);
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    if (kx > 2 * h + m) continue;
-#pragma unroll
-                    for (int pq = 0; pq < NI; ++pq) {
-                        uint32_t f[4];
-                        frag_a<32>(s + L::P + pq * kTri + tri_block(2 * h + m, kx), 0, 0, f);
-#pragma unroll
-                        for (int pa = 0; pa + pq < NS; ++pa) {
-                            ptx::mma16816(o[m][0], f, a[pa][0], a[pa][2]);
-                            ptx::mma16816(o[m][1], f, a[pa][1], a[pa][3]);
-                        }
-                    }
-                }
-            }
+            scale_output(o, gate, scale, 2 * h);
+            add_p_values<NI, NS>(pair + L::Uo + hb * L::kUo, s + L::P, h, o);
             warp_arrive(hempty(hb));
             warp_arrive(empty2(s2));
-#pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int r = i * C + (2 * h + m) * 16 + gr + x * 8;
-                    if (r >= len) continue;
-                    T *row = out + ((tok0 + r) * p.n_heads + head) * p.d_v;
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        const int v = v0 + n * 8 + tq * 2;
-                        if (v < p.d_v) put2(row + v, o[m][n][x * 2], o[m][n][x * 2 + 1], wide_out, v + 1 < p.d_v);
-                    }
-                }
+            store_output(static_cast<T *>(p.out), o, i * C, 2 * h, v0, tok0, len, head, p, wide_out);
         }
-    } else if constexpr (kRev) {
+    } else if constexpr (kRev && kHelp) {
         // ------------------------------------------------ G^T = (s gamma dO)^T Q, key channels of half
         // h, and dO^T P, tokens of half h
         for (int i = 0; i < n_chunks; ++i) {
@@ -726,35 +826,11 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
             for (int kx = 0; kx < 4; ++kx) {
                 uint32_t a[NI][4], d[NS][4];
-#pragma unroll
-                for (int q = 0; q < NI; ++q) frag_a_t<64>(s + L::dO + q * C * kBlockV * 2, kx * 16, w * 16, a[q]);
+                frag_dout<NI>(s + L::dO, kx, w, a);
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
-                    if (2 * h + n <= kx)
-#pragma unroll
-                        for (int pb = 0; pb < NS; ++pb) {
-                            uint32_t b[4];
-                            frag_b_t<32>(s + L::P + pb * kTri + tri_block(kx, 2 * h + n), 0, 0, b);
-#pragma unroll
-                            for (int pa = 0; pa < NI && pa + pb < NS; ++pa) {
-                                ptx::mma16816(y[2 * n], a[pa], b[0], b[1]);
-                                ptx::mma16816(y[2 * n + 1], a[pa], b[2], b[3]);
-                            }
-                        }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 ga = *reinterpret_cast<const float2 *>(gate + kx * 16 + (j >> 1) * 8 + tq * 2);
-                    float x = 0.f, z = 0.f;
-#pragma unroll
-                    for (int q = 0; q < NI; ++q) {
-                        x += lo_f(a[q][j]);
-                        z += hi_f(a[q][j]);
-                    }
-                    uint32_t sp[NS];
-                    split2<NS>(x * (scale * ga.x), z * (scale * ga.y), sp);
-#pragma unroll
-                    for (int q = 0; q < NS; ++q) d[q][j] = sp[q];
-                }
+                    if (2 * h + n <= kx) add_dout_p<NI, NS>(a, s + L::P + tri_block(kx, 2 * h + n), &y[2 * n]);
+                scale_dout<NI, NS>(a, gate, scale, kx, d);
                 add_values_keys<NI, NS, DKP>(d, s + L::Q, kx * 16, h * (DKP / 2), G);
             }
             warp_arrive(empty2(s2));

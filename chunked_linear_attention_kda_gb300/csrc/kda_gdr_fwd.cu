@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kChainThreads)
     gdr_chain_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const GdrArgs p, const Images im, float scale,
                      bool wide_out) {
-    chain<T, DKP, NS, Mode::kForward>(tm_q, tm_k, tm_v, p, im, 1, blockIdx.x, scale, wide_out);
+    chain<T, DKP, NS, Mode::kForward, 2>(tm_q, tm_k, tm_v, p, im, 1, blockIdx.x, scale, wide_out);
 }
 
 template <typename T, int DKP, int NS>
@@ -398,10 +398,10 @@ cudaError_t forward(const GdrArgs &p, cudaStream_t stream) {
     const Images im{!maps.make<T>(p, false), scan_offset(p.n_tok, p.n_seq, p.n_heads, NS)};
     cudaError_t e = launch_gdr_terms(p, im, 1, NS, stream);
     if (e != cudaSuccess) return e;
-    constexpr int bytes = ChainSmem<NI, DKP, NS, Mode::kForward>::kBytes;
     const bool wide = p.d_v % 2 == 0 && ((uintptr_t)p.out % (2 * sizeof(T))) == 0;
-    return launch_dependent(gdr_chain_kernel<T, DKP, NS>, chain_blocks(p), kChainThreads, bytes, stream, maps.q, maps.k,
-                            maps.v, p, im, 1.f / std::sqrt((float)p.d_k), wide);
+    return launch_dependent(gdr_chain_kernel<T, DKP, NS>, chain_blocks(p, 2), kChainThreads,
+                            ChainSmem<NI, DKP, NS, Mode::kForward, 2>::kBytes, stream, maps.q, maps.k, maps.v, p, im,
+                            1.f / std::sqrt((float)p.d_k), wide);
 }
 
 }  // namespace
