@@ -174,12 +174,15 @@ def gdr_step(q, k, v, g, beta, state, slots=None, *, out=None):
     if slots is not None:
         _flat("slots", slots, (n,), _I32, dev)
     if out is None:
-        out = torch.empty((n, h, dv), dtype=q.dtype, device=q.device)
+        out = torch.empty(v.shape, dtype=q.dtype, device=q.device)
     else:
-        _flat("out", out, (n, h, dv), q.dtype, dev)
-    _done(lib, lib.kda_gdr_step(
-        _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(state), _p(slots), _p(out), n,
-        state.shape[0], hk, h, dk, dv, _CODE[q.dtype], stream))
+        _flat("out", out, v.shape, q.dtype, dev)
+    status = lib.kda_gdr_step(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, g.data_ptr(), beta.data_ptr(),
+        state.data_ptr(), None if slots is None else slots.data_ptr(), out.data_ptr(), n,
+        state.shape[0], hk, h, dk, dv, _CODE[q.dtype], stream)
+    if status:
+        _kda._check(lib, status)
     return out
 
 
@@ -191,24 +194,29 @@ def residual_norm_fwd(x, weight, residual=None, scale=None, *, eps=1e-6, out=Non
     lib, stream, dev = _start(x, "residual_norm_fwd")
     if x.dim() != 2:
         raise ValueError("x must be [N, d]")
-    n, d = x.shape
-    xs = _rows("x", x, (n, d), x.dtype, dev)
+    shape, dtype = x.shape, x.dtype
+    n, d = shape
+    xs = _rows("x", x, shape, dtype, dev)
     _flat("weight", weight, (d,), _F32, dev)
     if scale is not None:
         _flat("scale", scale, (d,), _F32, dev)
-    rs = 0 if residual is None else _rows("residual", residual, (n, d), x.dtype, dev)
+    rs = 0 if residual is None else _rows("residual", residual, shape, dtype, dev)
     same = residual is None and scale is None and residual_out is None
     if residual_out is not None:
-        _flat("residual_out", residual_out, (n, d), x.dtype, dev)
+        _flat("residual_out", residual_out, shape, dtype, dev)
     elif not same:
-        residual_out = torch.empty((n, d), dtype=x.dtype, device=x.device)
+        residual_out = torch.empty(shape, dtype=dtype, device=x.device)
     if out is None:
-        out = torch.empty((n, d), dtype=x.dtype, device=x.device)
+        out = torch.empty(shape, dtype=dtype, device=x.device)
     else:
-        _flat("out", out, (n, d), x.dtype, dev)
-    _done(lib, lib.kda_residual_norm_fwd(_p(x), xs, _p(residual), rs, _p(scale), _p(weight),
-                                         _p(residual_out), _p(out), n, d, eps, _CODE[x.dtype],
-                                         stream))
+        _flat("out", out, shape, dtype, dev)
+    status = lib.kda_residual_norm_fwd(
+        x.data_ptr(), xs, None if residual is None else residual.data_ptr(), rs,
+        None if scale is None else scale.data_ptr(), weight.data_ptr(),
+        None if residual_out is None else residual_out.data_ptr(), out.data_ptr(), n, d, eps,
+        _CODE[dtype], stream)
+    if status:
+        _kda._check(lib, status)
     return out, (x if same else residual_out)
 
 

@@ -32,7 +32,9 @@ constexpr int kARow = 68;  // floats of a row of A in shared memory
 template <int NI, int DKP>
 struct TermsSmem {
     static constexpr int kPlane = C * DKP * 2;
-    static constexpr int K = 0, Q = K + NI * kPlane, A = Q + NI * kPlane;
+    static constexpr int K = 0, Q = K + NI * kPlane;
+    static constexpr int kKept = 24 * kTermThreads * 4;  // the products K K^T and Q K^T, over K and Q
+    static constexpr int A = 2 * NI * kPlane > kKept ? 2 * NI * kPlane : kKept;
     static constexpr int Vec = A + 2 * C * kARow * 4;           // per head: G as float2, beta
     static constexpr int kBytes = Vec + 2 * 3 * C * 4;
 };
@@ -164,7 +166,7 @@ __device__ __forceinline__ void block_of(int w, int s, int &I, int &J) {
 }
 
 template <typename T, int DKP, int NS>
-__global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 3 : 1)
     gdr_terms_kernel(const GdrArgs p, const Images im, int values, float scale, bool vec) {
     constexpr int NI = InputPlanes<T>::N;
     using L = TermsSmem<NI, DKP>;
@@ -180,6 +182,21 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
     float *A = reinterpret_cast<float *>(smem + L::A);
     float *vec_s = reinterpret_cast<float *>(smem + L::Vec);
 
+    // The gates' inputs of the heads h0 and h0 + 1, a warp each, ahead of their use.
+    float gx[2], bx[2];
+    auto fetch_gates = [&](int h0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = lane * 2 + i;
+            gx[i] = bx[i] = 0.f;
+            if (warp < min(2, group - h0) && r < ch.len) {
+                const int64_t at = (ch.t0 + r) * hv + kh * group + h0 + warp;
+                gx[i] = p.g[at];
+                bx[i] = p.beta[at];
+            }
+        }
+    };
+    fetch_gates(0);
     load_key_tile<T, DKP>(base + L::K, static_cast<const T *>(p.k) + ch.t0 * p.k_stride + (int64_t)kh * p.d_k,
                           p.k_stride, ch.len, p.d_k, vec, tid, kTermThreads);
     load_key_tile<T, DKP>(base + L::Q, static_cast<const T *>(p.q) + ch.t0 * p.q_stride + (int64_t)kh * p.d_k,
@@ -192,19 +209,11 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
         if (warp >= min(2, group - h0)) return;
         const int head = kh * group + h0 + warp;
         Two s[2];
-        float b[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int r = lane * 2 + i;
-            float x = 0.f;
-            b[i] = 0.f;
-            if (r < ch.len) {
-                x = p.g[(ch.t0 + r) * hv + head];
-                // below -200 (and at -inf) the decay is 0 in fp32 all the same; a finite floor
-                // keeps differences of the sums free of inf - inf
-                x = x < kGFloor ? kGFloor : x;
-                b[i] = p.beta[(ch.t0 + r) * hv + head];
-            }
+            // below -200 (and at -inf) the decay is 0 in fp32 all the same; a finite floor keeps
+            // differences of the sums free of inf - inf
+            const float x = gx[i] < kGFloor ? kGFloor : gx[i];
             s[i].hi = x * kLog2e;
             s[i].lo = fmaf(x, kLog2e, -s[i].hi) + x * kLog2eLo;
         }
@@ -225,10 +234,10 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
             const int r = lane * 2 + i;
             const Two G = i ? run : add(before, s[0]);
             G2[r] = make_float2(G.hi, G.lo);
-            vec_s[warp * 3 * C + 2 * C + r] = b[i];
+            vec_s[warp * 3 * C + 2 * C + r] = bx[i];
             out[r] = exp2_of(G.hi, G.lo);
             out[C + r] = ex2((total.hi - G.hi) + (total.lo - G.lo));
-            out[2 * C + r] = b[i];
+            out[2 * C + r] = bx[i];
             out[3 * C + r] = exp2_of(total.hi, total.lo);
             reinterpret_cast<float2 *>(out + 4 * C)[r] = make_float2(G.hi, G.lo);
         }
@@ -285,6 +294,14 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
             }
         }
 
+    // kept by each thread for itself over K and Q: 24 registers fewer, which three CTAs an SM need
+    __syncthreads();
+    float *kept = reinterpret_cast<float *>(smem + L::K) + tid;
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) kept[(s * 8 + i) * kTermThreads] = kk[s][i >> 2][i & 3];
+
     for (int h0 = 0; h0 < group; h0 += 2) {
         const int nh = min(2, group - h0);
         if (h0) {
@@ -292,6 +309,7 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
             gates(h0);
             __syncthreads();
         }
+        fetch_gates(h0 + 2);
         // A (fp32, to shared memory; warps 0..3) and P (bf16 planes, to the workspace; warps 4..7)
         for (int hh = 0; hh < nh; ++hh) {
             const float2 *G2 = reinterpret_cast<const float2 *>(vec_s + hh * 3 * C);
@@ -308,12 +326,12 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 2 : 1)
                 for (int n = 0; n < 2; ++n) {
                     const int j = J[s] * 16 + n * 8 + tq * 2;
                     const float4 gj = *reinterpret_cast<const float4 *>(&G2[j]);
-                    const float *k4 = kk[s][n];
+                    const float *k4 = kept + (s * 8 + n * 4) * kTermThreads;
                     float x[4];
                     x[0] = f0 * k4[0] * ex2((g0.x - gj.x) + (g0.y - gj.y));
-                    x[1] = f0 * k4[1] * ex2((g0.x - gj.z) + (g0.y - gj.w));
-                    x[2] = f1 * k4[2] * ex2((g1.x - gj.x) + (g1.y - gj.y));
-                    x[3] = f1 * k4[3] * ex2((g1.x - gj.z) + (g1.y - gj.w));
+                    x[1] = f0 * k4[kTermThreads] * ex2((g0.x - gj.z) + (g0.y - gj.w));
+                    x[2] = f1 * k4[2 * kTermThreads] * ex2((g1.x - gj.x) + (g1.y - gj.y));
+                    x[3] = f1 * k4[3 * kTermThreads] * ex2((g1.x - gj.z) + (g1.y - gj.w));
                     if (I[s] == J[s]) {  // A is strictly lower triangular, P lower
                         const int e = keys ? 0 : 1;
                         if (j >= r0 + e) x[0] = 0.f;
