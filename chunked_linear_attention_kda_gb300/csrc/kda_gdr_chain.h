@@ -107,7 +107,7 @@ struct ChainSmem {
     static constexpr int kStage2 = (Gate2 + kGate + 1023) / 1024 * 1024;
     static constexpr int N2 = M == Mode::kStates ? 0 : NS == 2 && kHelp ? 2 : 1;
     // per pair
-    static constexpr int NH = kOut && NS == 2 ? 2 : 1;            // buffers of Sx and Uo
+    static constexpr int NH = kOut ? 2 : 1;            // buffers of Sx and Uo
     static constexpr int kSx = NS * (DKP / 16) * 512, kUx = NS * 4 * 512, kZx = NS * 2 * 512;
     static constexpr int kUo = kOut ? C * 64 : 0;
     static constexpr int kHandG = DKP * 64, kHand = kRev && kHelp ? kHandG + C * 64 : 0;
