@@ -193,6 +193,41 @@ __device__ __forceinline__ Two add(Two x, Two y) {
     const float hi = s + e;
     return {hi, e - (hi - s)};
 }
+// acc (two neighbouring 16 x 8 tiles) += A B from planes a, b: the products of planes i + j < LIM.
+// With three planes the tensor cores' own sums show: they drop bits of every addend below the
+// running sum's last place. The smallest products are then summed first, in accumulators that
+// start at zero, and only their sum meets acc, rounded to nearest.
+template <int NA, int NB, int LIM>
+__device__ __forceinline__ void product(float (*acc)[4], const uint32_t (*a)[4], const uint32_t (*b)[4]) {
+    if constexpr (LIM == 3) {
+        float t[2][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[0][i] = t[1][i] = 0.f;
+#pragma unroll
+        for (int level = LIM - 1; level >= 0; --level)
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                if (i > level || level - i >= NB) continue;
+                ptx::mma16816(t[0], a[i], b[level - i][0], b[level - i][1]);
+                ptx::mma16816(t[1], a[i], b[level - i][2], b[level - i][3]);
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            acc[0][i] += t[0][i];
+            acc[1][i] += t[1][i];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                if (i + j >= LIM) continue;
+                ptx::mma16816(acc[0], a[i], b[j][0], b[j][1]);
+                ptx::mma16816(acc[1], a[i], b[j][2], b[j][3]);
+            }
+    }
+}
+
 // 2^x (0 below the normal range)
 __device__ __forceinline__ float ex2(float x) {
     float y;

@@ -177,19 +177,13 @@ __global__ void __launch_bounds__(kLocalThreads)
             }
 #pragma unroll
             for (int n = 0; n < NP; ++n)
-                if (NP * wc + n <= wr)
+                if (NP * wc + n <= wr) {
+                    uint32_t b[NI][4];
 #pragma unroll
-                    for (int pb = 0; pb < NI; ++pb) {
-                        uint32_t b[4];
-                        key_b(base + L::K + pb * L::kPlane, wc * PC + n * 16, c, b);
-#pragma unroll
-                        for (int pa = 0; pa + pb < NI; ++pa) {
-                            ptx::mma16816(kk[2 * n], ak[pa], b[0], b[1]);
-                            ptx::mma16816(kk[2 * n + 1], ak[pa], b[2], b[3]);
-                            ptx::mma16816(qk[2 * n], aq[pa], b[0], b[1]);
-                            ptx::mma16816(qk[2 * n + 1], aq[pa], b[2], b[3]);
-                        }
-                    }
+                    for (int q = 0; q < NI; ++q) key_b(base + L::K + q * L::kPlane, wc * PC + n * 16, c, b[q]);
+                    product<NI, NI, NI>(&kk[2 * n], ak, b);
+                    product<NI, NI, NI>(&qk[2 * n], aq, b);
+                }
         }
 #pragma unroll
         for (int n = 0; n < 2 * NP; ++n)
@@ -242,13 +236,7 @@ __global__ void __launch_bounds__(kLocalThreads)
                     frag_a<RB>(s + L::S + q * L::kState, v, c, x[q]);
                     frag_b<RB>(s + L::dS + q * L::kState, v, c, y[q]);
                 }
-#pragma unroll
-                for (int pa = 0; pa < NS; ++pa)
-#pragma unroll
-                    for (int pb = 0; pa + pb < NS; ++pb) {
-                        ptx::mma16816(ss[0], x[pa], y[pb][0], y[pb][1]);
-                        ptx::mma16816(ss[1], x[pa], y[pb][2], y[pb][3]);
-                    }
+                product<NS, NS, NS>(ss, x, y);
             }
 #pragma unroll
             for (int kx = 0; kx < 2; ++kx) {  // 16 value channels
@@ -295,42 +283,26 @@ __global__ void __launch_bounds__(kLocalThreads)
                 }
                 // dO S0^T, E S0^T, U dS1^T
 #pragma unroll
-                for (int n = 0; n < NH; ++n)
+                for (int n = 0; n < NH; ++n) {
+                    uint32_t b[NS][4];
 #pragma unroll
-                    for (int pb = 0; pb < NS; ++pb) {
-                        uint32_t b[4], d[4];
-                        frag_b_t<RB>(s + L::S + pb * L::kState, kx * 16, wc * KC + n * 16, b);
-                        frag_b_t<RB>(s + L::dS + pb * L::kState, kx * 16, wc * KC + n * 16, d);
+                    for (int q = 0; q < NS; ++q) frag_b_t<RB>(s + L::S + q * L::kState, kx * 16, wc * KC + n * 16, b[q]);
+                    product<NI, NS, NS>(&xq[2 * n], ao, b);
+                    product<NS, NS, NS>(&xk[2 * n], ae, b);
 #pragma unroll
-                        for (int pa = 0; pa + pb < NS; ++pa) {
-                            if (pa < NI) {
-                                ptx::mma16816(xq[2 * n], ao[pa], b[0], b[1]);
-                                ptx::mma16816(xq[2 * n + 1], ao[pa], b[2], b[3]);
-                            }
-                            ptx::mma16816(xk[2 * n], ae[pa], b[0], b[1]);
-                            ptx::mma16816(xk[2 * n + 1], ae[pa], b[2], b[3]);
-                            ptx::mma16816(xu[2 * n], au[pa], d[0], d[1]);
-                            ptx::mma16816(xu[2 * n + 1], au[pa], d[2], d[3]);
-                        }
-                    }
+                    for (int q = 0; q < NS; ++q) frag_b_t<RB>(s + L::dS + q * L::kState, kx * 16, wc * KC + n * 16, b[q]);
+                    product<NS, NS, NS>(&xu[2 * n], au, b);
+                }
                 // dO U^T, E U^T
 #pragma unroll
                 for (int n = 0; n < NP; ++n)
-                    if (NP * wc + n <= wr)
+                    if (NP * wc + n <= wr) {
+                        uint32_t b[NS][4];
 #pragma unroll
-                        for (int pb = 0; pb < NS; ++pb) {
-                            uint32_t b[4];
-                            frag_b_t<128>(s + L::U + pb * L::kVal, kx * 16, wc * PC + n * 16, b);
-#pragma unroll
-                            for (int pa = 0; pa + pb < NS; ++pa) {
-                                if (pa < NI) {
-                                    ptx::mma16816(ou[2 * n], ao[pa], b[0], b[1]);
-                                    ptx::mma16816(ou[2 * n + 1], ao[pa], b[2], b[3]);
-                                }
-                                ptx::mma16816(eu[2 * n], ae[pa], b[0], b[1]);
-                                ptx::mma16816(eu[2 * n + 1], ae[pa], b[2], b[3]);
-                            }
-                        }
+                        for (int q = 0; q < NS; ++q) frag_b_t<128>(s + L::U + q * L::kVal, kx * 16, wc * PC + n * 16, b[q]);
+                        product<NI, NS, NS>(&ou[2 * n], ao, b);
+                        product<NS, NS, NS>(&eu[2 * n], ae, b);
+                    }
             }
             __syncthreads();
         }
@@ -494,22 +466,16 @@ __global__ void __launch_bounds__(kLocalThreads)
                 frag_a<128>(base + L::F + q * L::kTile, wr * 16, kx * 16, af[q]);
             }
 #pragma unroll
-            for (int n = 0; n < NH; ++n)
+            for (int n = 0; n < NH; ++n) {
+                uint32_t b[NI][4];
 #pragma unroll
-                for (int pb = 0; pb < NI; ++pb) {
-                    uint32_t b[4], d[4];
-                    key_b_t(base + L::K + pb * L::kPlane, kx * 16, wc * KC + n * 16, b);
-                    key_b_t(base + L::Q + pb * L::kPlane, kx * 16, wc * KC + n * 16, d);
+                for (int q = 0; q < NI; ++q) key_b_t(base + L::K + q * L::kPlane, kx * 16, wc * KC + n * 16, b[q]);
+                product<NI, NI, NI>(&dq[2 * n], ab, b);
+                product<NI, NI, NI>(&dk[2 * n], af, b);
 #pragma unroll
-                    for (int pa = 0; pa + pb < NI; ++pa) {
-                        ptx::mma16816(dq[2 * n], ab[pa], b[0], b[1]);
-                        ptx::mma16816(dq[2 * n + 1], ab[pa], b[2], b[3]);
-                        ptx::mma16816(dk[2 * n], at[pa], d[0], d[1]);
-                        ptx::mma16816(dk[2 * n + 1], at[pa], d[2], d[3]);
-                        ptx::mma16816(dk[2 * n], af[pa], b[0], b[1]);
-                        ptx::mma16816(dk[2 * n + 1], af[pa], b[2], b[3]);
-                    }
-                }
+                for (int q = 0; q < NI; ++q) key_b_t(base + L::Q + q * L::kPlane, kx * 16, wc * KC + n * 16, b[q]);
+                product<NI, NI, NI>(&dk[2 * n], at, b);
+            }
         }
         ptx::fence_proxy_async();  // B and F were written by plain stores; the next copies overwrite them
         __syncthreads();           // B, F, the gates and the sums are done with

@@ -193,27 +193,34 @@ __device__ __forceinline__ int ranked_sequence(const int32_t *cu, int n_seq, int
 
 // ---- products of the state warps
 
-// y (16 x 16, tokens n0 ..) = S^T K^T from the planes of S^T; the products of lower planes run
-// on accumulators of their own, so that no product waits for the one before it
-// (the planes of half h of the key channels come first)
+// y (16 x 16, tokens n0 ..) = S^T K^T from the planes of S^T, those of half h of the key channels
+// first; with two planes the lower one's products run on accumulators of their own, so that no
+// product waits for the one before it
 template <int NI, int NS, int DKP>
 __device__ __forceinline__ void state_times_keys(const uint32_t (*a)[DKP / 16][4], uint32_t k, int h, int n0, float (*y)[4]) {
     float lo[2][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[0][i] = y[1][i] = lo[0][i] = lo[1][i] = 0.f;
 #pragma unroll
-    for (int kx = 0; kx < DKP / 16; ++kx)
+    for (int kx = 0; kx < DKP / 16; ++kx) {
+        const int half = kx < DKP / 32 ? h : 1 - h;
+        uint32_t b[NI][4];
 #pragma unroll
-        for (int pb = 0; pb < NI; ++pb) {
-            uint32_t b[4];
-            const int half = kx < DKP / 32 ? h : 1 - h;
-            key_b(k + pb * C * DKP * 2, n0, half * (DKP / 2) + (kx % (DKP / 32)) * 16, b);
+        for (int q = 0; q < NI; ++q) key_b(k + q * C * DKP * 2, n0, half * (DKP / 2) + (kx % (DKP / 32)) * 16, b[q]);
+        if constexpr (NS == 3) {
+            uint32_t x[NS][4];
 #pragma unroll
-            for (int pa = 0; pa + pb < NS; ++pa) {
-                ptx::mma16816(pa + pb ? lo[0] : y[0], a[pa][kx], b[0], b[1]);
-                ptx::mma16816(pa + pb ? lo[1] : y[1], a[pa][kx], b[2], b[3]);
-            }
+            for (int q = 0; q < NS; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[q][i] = a[q][kx][i];
+            product<NS, NI, 3>(y, x, b);
+        } else {
+            ptx::mma16816(y[0], a[0][kx], b[0][0], b[0][1]);
+            ptx::mma16816(y[1], a[0][kx], b[0][2], b[0][3]);
+            ptx::mma16816(lo[0], a[1][kx], b[0][0], b[0][1]);
+            ptx::mma16816(lo[1], a[1][kx], b[0][2], b[0][3]);
         }
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         y[0][i] += lo[0][i];
@@ -224,32 +231,23 @@ __device__ __forceinline__ void state_times_keys(const uint32_t (*a)[DKP / 16][4
 template <int NI, int NS, int DKP>
 __device__ __forceinline__ void add_values_keys(const uint32_t (*a)[4], uint32_t k, int k0, int c0, float (*S)[4]) {
 #pragma unroll
-    for (int n = 0; n < DKP / 32; ++n)
+    for (int n = 0; n < DKP / 32; ++n) {
+        uint32_t b[NI][4];
 #pragma unroll
-        for (int pb = 0; pb < NI; ++pb) {
-            uint32_t b[4];
-            key_b_t(k + pb * C * DKP * 2, k0, c0 + n * 16, b);
-#pragma unroll
-            for (int pa = 0; pa + pb < NS; ++pa) {
-                ptx::mma16816(S[2 * n], a[pa], b[0], b[1]);
-                ptx::mma16816(S[2 * n + 1], a[pa], b[2], b[3]);
-            }
-        }
+        for (int q = 0; q < NI; ++q) key_b_t(k + q * C * DKP * 2, k0, c0 + n * 16, b[q]);
+        product<NS, NI, NS>(&S[2 * n], a, b);
+    }
 }
 // u (16 x 16, block n of the result's tokens) += a X over block k of the contraction
 template <int NS, bool REV>
 __device__ __forceinline__ void add_times_x(const uint32_t (*a)[4], uint32_t x, int k, int n, float (*u)[4]) {
+    uint32_t b[NS][4];
 #pragma unroll
-    for (int pb = 0; pb < NS; ++pb) {
-        uint32_t b[4];
-        if (REV) frag_b_t<32>(x + pb * kTri + tri_block(k, n), 0, 0, b);
-        else frag_b<32>(x + pb * kTri + tri_block(n, k), 0, 0, b);
-#pragma unroll
-        for (int pa = 0; pa + pb < NS; ++pa) {
-            ptx::mma16816(u[0], a[pa], b[0], b[1]);
-            ptx::mma16816(u[1], a[pa], b[2], b[3]);
-        }
+    for (int q = 0; q < NS; ++q) {
+        if (REV) frag_b_t<32>(x + q * kTri + tri_block(k, n), 0, 0, b[q]);
+        else frag_b<32>(x + q * kTri + tri_block(n, k), 0, 0, b[q]);
     }
+    product<NS, NS, NS>(u, a, b);
 }
 // planes of a 16 x 16 block to and from shared memory, 16 bytes a lane, planes `plane` apart
 template <int NS>
@@ -268,21 +266,26 @@ __device__ __forceinline__ void get_block(const char *p, int plane, uint32_t (*a
 }
 // ---- the output, 32 tokens x 16 value channels: o[m][n], token blocks m0 + m
 
+// the A-operand planes of a 16 x 16 block as the B operand of the transposed product
+template <int NP>
+__device__ __forceinline__ void as_b(const uint32_t (*a)[4], uint32_t (*b)[4]) {
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+        b[q][0] = a[q][0]; b[q][1] = a[q][2]; b[q][2] = a[q][1]; b[q][3] = a[q][3];
+    }
+}
 // o += Q S0, key channels of block kx; a the planes of S^T
 template <int NI, int DKP>
 __device__ __forceinline__ void add_queries(const uint32_t (*a)[4], uint32_t q, int m0, int kx, float (*o)[2][4]) {
+    uint32_t b[NI][4];
+    as_b<NI>(a, b);
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 2; ++m) {
+        uint32_t f[NI][4];
 #pragma unroll
-        for (int pq = 0; pq < NI; ++pq) {
-            uint32_t f[4];
-            key_a(q + pq * C * DKP * 2, (m0 + m) * 16, kx * 16, f);
-#pragma unroll
-            for (int pa = 0; pa + pq < NI; ++pa) {
-                ptx::mma16816(o[m][0], f, a[pa][0], a[pa][2]);
-                ptx::mma16816(o[m][1], f, a[pa][1], a[pa][3]);
-            }
-        }
+        for (int x = 0; x < NI; ++x) key_a(q + x * C * DKP * 2, (m0 + m) * 16, kx * 16, f[x]);
+        product<NI, NI, NI>(o[m], f, b);
+    }
 }
 __device__ __forceinline__ void scale_output(float (*o)[2][4], const float *gate, float scale, int m0) {
     const int gr = (threadIdx.x & 31) >> 2;
@@ -310,19 +313,15 @@ __device__ __forceinline__ void add_p_values(const char *uo, uint32_t pt, int h,
             u[n][0] = x.x; u[n][1] = x.y; u[n][2] = x.z; u[n][3] = x.w;
         }
         acc_to_a<NS>(u, a);
+        uint32_t b[NS][4];
+        as_b<NS>(a, b);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
             if (kx > 2 * h + m) continue;
+            uint32_t f[NI][4];
 #pragma unroll
-            for (int pq = 0; pq < NI; ++pq) {
-                uint32_t f[4];
-                frag_a<32>(pt + pq * kTri + tri_block(2 * h + m, kx), 0, 0, f);
-#pragma unroll
-                for (int pa = 0; pa + pq < NS; ++pa) {
-                    ptx::mma16816(o[m][0], f, a[pa][0], a[pa][2]);
-                    ptx::mma16816(o[m][1], f, a[pa][1], a[pa][3]);
-                }
-            }
+            for (int q = 0; q < NI; ++q) frag_a<32>(pt + q * kTri + tri_block(2 * h + m, kx), 0, 0, f[q]);
+            product<NI, NS, NS>(o[m], f, b);
         }
     }
 }
@@ -355,16 +354,10 @@ __device__ __forceinline__ void frag_dout(uint32_t dout, int kx, int w, uint32_t
 // y (16 x 16) += dO^T P, P's block at `pt`
 template <int NI, int NS>
 __device__ __forceinline__ void add_dout_p(const uint32_t (*a)[4], uint32_t pt, float (*y)[4]) {
+    uint32_t b[NS][4];
 #pragma unroll
-    for (int pb = 0; pb < NS; ++pb) {
-        uint32_t b[4];
-        frag_b_t<32>(pt + pb * kTri, 0, 0, b);
-#pragma unroll
-        for (int pa = 0; pa < NI && pa + pb < NS; ++pa) {
-            ptx::mma16816(y[0], a[pa], b[0], b[1]);
-            ptx::mma16816(y[1], a[pa], b[2], b[3]);
-        }
-    }
+    for (int q = 0; q < NS; ++q) frag_b_t<32>(pt + q * kTri, 0, 0, b[q]);
+    product<NI, NS, NS>(y, a, b);
 }
 // planes of (s gamma dO)^T
 template <int NI, int NS>

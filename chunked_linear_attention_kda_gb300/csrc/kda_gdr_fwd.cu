@@ -282,16 +282,10 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 3 : 1)
             uint32_t a[NI][4];
 #pragma unroll
             for (int q = 0; q < NI; ++q) key_a(base + (keys ? L::K : L::Q) + q * L::kPlane, I[s] * 16, c, a[q]);
+            uint32_t b[NI][4];
 #pragma unroll
-            for (int pb = 0; pb < NI; ++pb) {
-                uint32_t b[4];
-                key_b(base + L::K + pb * L::kPlane, J[s] * 16, c, b);
-#pragma unroll
-                for (int pa = 0; pa + pb < NI; ++pa) {
-                    ptx::mma16816(kk[s][0], a[pa], b[0], b[1]);
-                    ptx::mma16816(kk[s][1], a[pa], b[2], b[3]);
-                }
-            }
+            for (int q = 0; q < NI; ++q) key_b(base + L::K + q * L::kPlane, J[s] * 16, c, b[q]);
+            product<NI, NI, NI>(kk[s], a, b);
         }
 
     // kept by each thread for itself over K and Q: 24 registers fewer, which three CTAs an SM need
