@@ -100,7 +100,8 @@ __host__ __device__ constexpr size_t terms_bytes(int ns) {
 }
 
 // Per (slot, value head) of the backward pass, behind the terms: S0^T and dS1^T (value
-// channels x d_k padded to DKP), U^T and E^T (value channels x 64), NS planes each, swizzled.
+// channels x d_k padded to DKP, see state_block), U^T and E^T (value channels x 64), NS planes each,
+// in rows of 128 bytes with the 128-byte swizzle: what tcgen05 reads as MN-major operands.
 __host__ __device__ __forceinline__ int pad_v(int d_v) { return (d_v + 31) & ~31; }
 __host__ __device__ __forceinline__ size_t scan_state_bytes(int ns, int dkp, int d_v) {
     return (size_t)ns * pad_v(d_v) * dkp * 2;
@@ -184,6 +185,13 @@ __device__ __forceinline__ void key_b(uint32_t base, int n0, int k0, uint32_t *b
 __device__ __forceinline__ void key_b_t(uint32_t base, int k0, int n0, uint32_t *b) {
     frag_b_t<128>(base + (n0 >> 6) * kHalf, k0, n0 & 63, b);
 }
+
+// A plane of S0^T or dS1^T: blocks of 16 value channels, a block's halves of 64 key channels one
+// after the other, each 16 rows of 128 bytes. Byte offset of the 16 x 16 block at value channel v
+// (a multiple of 16) and key channel c within its half; the rest of the offset is
+// tile_off<128>(v % 16, c % 64).
+template <int DKP>
+__device__ __forceinline__ uint32_t state_block(int v, int c) { return (v >> 4) * (16 * DKP * 2) + (c >> 6) * 2048; }
 
 // A sum carried as two floats (the fp64 pipe of this part is narrow).
 struct Two { float hi, lo; };

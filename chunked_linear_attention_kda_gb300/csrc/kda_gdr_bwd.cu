@@ -41,11 +41,18 @@ __global__ void __launch_bounds__(kChainThreads)
 }
 
 // ---------------------------------------------------------------- local gradients
-constexpr int kLocalThreads = 256;
+constexpr int kLocalThreads = 256;          // that compute
 constexpr int kCols = kLocalThreads / 128;  // column parts: a warp has 16 tokens x 1 / kCols of the columns
+// The products with S0, dS1 and U run on tcgen05 where operands have one and two planes; three
+// planes want sums from the smallest product up, which mma.sync's registers give.
+template <typename T, int NS>
+constexpr bool kTensor = InputPlanes<T>::N == 1 && NS == 2;
 
-template <int NI, int DKP, int NS>
+template <typename T, int DKP, int NS>
 struct LocalSmem {
+    static constexpr bool TC = kTensor<T, NS>;
+    static constexpr int NI = InputPlanes<T>::N;
+    static constexpr int kThreads = kLocalThreads + (TC ? 32 : 0);  // a ninth warp loads and issues
     static constexpr int kStages = NS == 2 ? 2 : 1;
     static constexpr int kPlane = C * DKP * 2;
     static constexpr int kIn = C * 32 * 2, kVal = 32 * C * 2, kState = 32 * DKP * 2;  // one plane of a 32-channel slice
@@ -53,15 +60,22 @@ struct LocalSmem {
                          E = U + NS * kVal, S = E + NS * kVal;
     static constexpr int dS = S + NS * kState, kSlice = dS + NS * kState;
     static constexpr int kTile = C * C * 2;  // bytes of a plane of B and F
-    static constexpr int B = 0, F = NI * kTile;  // over the first slice buffer, once the slices are done
-    static_assert(2 * NI * kTile <= kSlice, "B and F fit a slice buffer");
     static constexpr int K = kStages * kSlice, Q = K + NI * kPlane, Pair = Q + NI * kPlane;
-    static constexpr int Gate = Pair + 2 * C * C * 4, Red = Gate + kGateFloats * 4;
+    // B and F: without tcgen05 over the first slice buffer, once the slices are done
+    static constexpr int B = TC ? Pair + 2 * C * C * 4 : 0, F = B + NI * kTile;
+    static_assert(2 * NI * kTile <= kSlice, "B and F fit a slice buffer");
+    // a head's gates are loaded with its first slice, two slices ahead: with one slice a head
+    // while the head two before is still being finished
+    static constexpr int kGates = TC ? 3 : 1;
+    static constexpr int Gate = Pair + 2 * C * C * 4 + (TC ? 2 * NI * kTile : 0), Red = Gate + kGates * kGateFloats * 4;
     // Red: [kCols][64] row sums of q.x, k.x, k.x, F k.k, M over the column parts; [64] E.V;
     // [4][64] column sums of M over the row blocks; the warps' parts of <S0, dS1>
     static constexpr int kRed = 5 * kCols * C + C + 4 * C + kLocalThreads / 32;
     static constexpr int Bars = (Red + kRed * 4 + 7) / 8 * 8;
-    static constexpr int kBytes = Bars + 8 * (kStages + 1) + 1024;  // the base is rounded up to 1024
+    // a slice buffer full [kStages], K and Q full; with tcgen05 also a slice buffer read
+    // [kStages], a head's sums complete, read, and one to drain by; then the tensor memory's address
+    static constexpr int kBars = kStages + 1 + (TC ? kStages + 3 : 0);
+    static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;  // the base is rounded up to 1024
     static_assert(kBytes <= 227 * 1024, "fits an SM");
     static_assert(kSlice % 1024 == 0, "tensor copies land on swizzle boundaries");
 };
@@ -79,18 +93,21 @@ __device__ __forceinline__ float quad_sum(float x) {
 }
 
 template <typename T, int DKP, int NS>
-__global__ void __launch_bounds__(kLocalThreads)
+__global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
     gdr_local_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                      const GdrArgs p, const Images im, float scale, bool wide_k, bool wide_v) {
     constexpr int NI = InputPlanes<T>::N;
-    using L = LocalSmem<NI, DKP, NS>;
-    constexpr int RB = DKP * 2, KC = DKP / kCols, NH = KC / 16;  // a warp's key channels, in steps of 16
+    using L = LocalSmem<T, DKP, NS>;
+    constexpr bool TC = L::TC;
+    // columns of tensor memory: dO S0^T from 0, E S0^T, U dS1^T, then dO U^T and E U^T (64 tokens
+    // use 16 lanes of each warp's 32)
+    [[maybe_unused]] constexpr int kXk = DKP, kXu = 2 * DKP, kOu = 3 * DKP, kEu = 3 * DKP + C;
+    constexpr int KC = DKP / kCols, NH = KC / 16;  // a warp's key channels, in steps of 16
     constexpr int PC = C / kCols, NP = PC / 16;              // its columns of the 64 x 64 products
     extern __shared__ __align__(1024) char smem_raw[];
     char *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_u32(smem);
-    wait_for_previous_kernel();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
     const int wr = warp & 3, wc = warp >> 2;  // token rows 16 wr .., column part wc
     const int64_t slot = blockIdx.x;
@@ -100,13 +117,19 @@ __global__ void __launch_bounds__(kLocalThreads)
     const int n_sl = pad_v(p.d_v) / 32;
     const char *ws = static_cast<const char *>(p.workspace);
     float *pair = reinterpret_cast<float *>(smem + L::Pair);
-    float *gate = reinterpret_cast<float *>(smem + L::Gate);
+    float *gate = reinterpret_cast<float *>(smem + L::Gate);  // TC: head hh's at hh % 3
     float *red = reinterpret_cast<float *>(smem + L::Red);
     float *r_qx = red, *r_kx = r_qx + kCols * C, *r_ku = r_kx + kCols * C, *r_fk = r_ku + kCols * C;
     float *r_m = r_fk + kCols * C, *r_ev = r_m + kCols * C, *c_m = r_ev + C, *r_ss = c_m + 4 * C;
 
+    auto meet = [&]() {  // of the threads that compute
+        if constexpr (TC) ptx::named_sync(1, kLocalThreads);
+        else __syncthreads();
+    };
     // one thread loads: K and Q, then the 32-channel slices of the value heads, head after head
     auto bar = [&](int i) { return base + L::Bars + 8 * i; };  // a slice buffer's; kStages: K and Q
+    auto used = [&](int i) { return bar(L::kStages + 1 + i); };
+    [[maybe_unused]] const uint32_t sums_done = bar(2 * L::kStages + 1), sums_read = sums_done + 8, drain = sums_done + 16;
     const bool image = im.has(ch.t0, ch.len, p.n_tok);
     const size_t img_rec = Images::record(NI, DKP, p.d_v, p.n_k_heads, p.n_heads, 2);
     const size_t kb = Images::key_bytes(NI, DKP), vb = Images::value_bytes(NI, p.d_v);
@@ -121,7 +144,13 @@ __global__ void __launch_bounds__(kLocalThreads)
         const char *rec = ws + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
                           (slot * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v);
         const size_t st = scan_state_bytes(NS, DKP, p.d_v), va = scan_value_bytes(NS, p.d_v);
-        ptx::mbar_arrive_tx(m, L::kSlice);
+        if (TC && sl == 0) {
+            ptx::mbar_arrive_tx(m, L::kSlice + kGateFloats * 4);
+            bulk_load(base + L::Gate + (step / n_sl % 3) * kGateFloats * 4,
+                      ws + (slot * p.n_heads + head) * terms_bytes(NS) + 2 * NS * kTri, kGateFloats * 4, m);
+        } else {
+            ptx::mbar_arrive_tx(m, L::kSlice);
+        }
         if (image) {
             const char *v = img + 2 * p.n_k_heads * kb + (size_t)sl * NI * L::kIn;
             bulk_load(s + L::dO, v + (p.n_heads + head) * vb, NI * L::kIn, m);
@@ -138,9 +167,21 @@ __global__ void __launch_bounds__(kLocalThreads)
             bulk_load(s + L::E + q * L::kVal, rec + 2 * st + va + q * (va / NS) + sl * L::kVal, L::kVal, m);
         }
     };
-    if (tid == 0) {
+    const int loader = TC ? kLocalThreads : 0;
+    if (tid == loader) {
         for (int i = 0; i <= L::kStages; ++i) ptx::mbar_init(bar(i), 1);
+        if constexpr (TC) {
+            for (int i = 0; i < L::kStages; ++i) ptx::mbar_init(used(i), kLocalThreads / 32 + 1);
+            ptx::mbar_init(sums_done, 1);
+            ptx::mbar_init(sums_read, kLocalThreads / 32);
+            ptx::mbar_init(drain, 1);
+        }
         ptx::mbar_init_fence();
+    }
+    if constexpr (TC)
+        if (warp == kLocalThreads / 32) ptx::tmem_alloc(bar(L::kBars), 512);
+    wait_for_previous_kernel();
+    if (tid == loader) {
         const uint32_t m = bar(L::kStages);
         ptx::mbar_arrive_tx(m, 2 * NI * L::kPlane);
         if (image) {
@@ -155,7 +196,78 @@ __global__ void __launch_bounds__(kLocalThreads)
         }
         load(0);
     }
+    if constexpr (TC) ptx::tc_fence_before();
     __syncthreads();
+    [[maybe_unused]] uint32_t tmem = 0;
+    if constexpr (TC) {
+        ptx::tc_fence_after();
+        tmem = *reinterpret_cast<const uint32_t *>(smem + L::Bars + 8 * L::kBars);
+    }
+    if (TC && warp == kLocalThreads / 32) {
+        // The ninth warp: a thread loads the slices and issues their products, two slices ahead of
+        // the others at most and into the next head's sums while those finish the last head's.
+        if constexpr (TC)
+            if (lane == 0) {
+                constexpr uint32_t id_o = ptx::idesc_bf16(64, DKP, 0, 1), id_e = ptx::idesc_bf16(64, DKP, 1, 1);
+                constexpr uint32_t id_ou = ptx::idesc_bf16(64, C, 0, 1), id_eu = ptx::idesc_bf16(64, C, 1, 1);
+                const int steps = group * n_sl;
+                if (steps > 1) load(1);
+                for (int step = 0, hh = 0, sl = 0; step < steps; ++step) {
+                    const int b = step & 1;
+                    ok = wait_bar(bar(b), (step >> 1) & 1);
+                    if (ok && sl == 0 && hh > 0) ok = wait_bar(sums_read, (hh - 1) & 1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t s = base + b * L::kSlice;
+#pragma unroll
+                    for (int kx = 0; kx < 2; ++kx) {  // 16 value channels
+                        const uint32_t more = sl + kx > 0;
+                        const uint64_t dO = ptx::sdesc_sw64(s + L::dO + kx * 32, 512);
+                        uint64_t E[NS], U[NS], S[NS], dS[NS];
+#pragma unroll
+                        for (int q = 0; q < NS; ++q) {
+                            E[q] = ptx::sdesc_sw128(s + L::E + q * L::kVal + kx * 2048, 1024, 1024);
+                            U[q] = ptx::sdesc_sw128(s + L::U + q * L::kVal + kx * 2048, 1024, 1024);
+                            S[q] = ptx::sdesc_sw128(s + L::S + q * L::kState + kx * (32 * DKP), 2048, 1024);
+                            dS[q] = ptx::sdesc_sw128(s + L::dS + q * L::kState + kx * (32 * DKP), 2048, 1024);
+                        }
+#pragma unroll
+                        for (int i = 0; i < NS; ++i) {
+                            ptx::umma_ss(tmem, dO, S[i], id_o, more | (i > 0));
+                            ptx::umma_ss(tmem + kOu, dO, U[i], id_ou, more | (i > 0));
+#pragma unroll
+                            for (int j = 0; i + j < NS; ++j) {
+                                const uint32_t acc = more | (i + j > 0);
+                                ptx::umma_ss(tmem + kXk, E[i], S[j], id_e, acc);
+                                ptx::umma_ss(tmem + kXu, U[i], dS[j], id_e, acc);
+                                ptx::umma_ss(tmem + kEu, E[i], U[j], id_eu, acc);
+                            }
+                        }
+                    }
+                    ptx::umma_commit(used(b));
+                    if (sl == n_sl - 1) ptx::umma_commit(sums_done);
+                    if (step > 0 && step + 1 < steps) {
+                        ok = wait_bar(used(b ^ 1), ((step - 1) >> 1) & 1);
+                        if (!ok) break;
+                        load(step + 1);
+                    }
+                    if (++sl == n_sl) {
+                        sl = 0;
+                        ++hh;
+                    }
+                }
+                if (!ok) {  // nothing may land in shared or tensor memory after the block has gone
+                    ptx::umma_commit(drain);
+                    drain_bar(drain, 0);
+                    drain_bar(bar(L::kStages), 0);
+                    for (int i = max(0, issued - L::kStages); i < issued; ++i) drain_bar(bar(i % L::kStages), (i / L::kStages) & 1);
+                }
+            }
+        __syncwarp();
+        __syncthreads();  // the others have read the last sums
+        if constexpr (TC) ptx::tmem_dealloc(tmem, 512);
+        return;
+    }
     // A failed wait sets the flag and the block goes on with what is there: nothing more is
     // loaded, and every later wait returns at once.
     ok = wait_bar(bar(L::kStages), 0);
@@ -202,29 +314,32 @@ __global__ void __launch_bounds__(kLocalThreads)
 
     for (int hh = 0; hh < group; ++hh) {
         const int head = kh * group + hh;
-        float xq[2 * NH][4], xk[2 * NH][4], xu[2 * NH][4], ou[2 * NP][4], eu[2 * NP][4];
-#pragma unroll
-        for (int n = 0; n < 2 * NH; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) xq[n][i] = xk[n][i] = xu[n][i] = 0.f;
-#pragma unroll
-        for (int n = 0; n < 2 * NP; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ou[n][i] = eu[n][i] = 0.f;
+        constexpr int XT = TC ? 4 : 2 * NH;  // tiles of 8 key channels in registers at a time
+        float xq[XT][4], xk[XT][4], xu[XT][4], ou[2 * NP][4], eu[2 * NP][4];
+        if constexpr (!TC) {
+            zero<XT>(xq);
+            zero<XT>(xk);
+            zero<XT>(xu);
+            zero<2 * NP>(ou);
+            zero<2 * NP>(eu);
+        }
         float ev[2] = {0.f, 0.f}, ss[2][4];
         zero<2>(ss);
-        for (int i = tid; i < kGateFloats; i += kLocalThreads)
-            gate[i] = reinterpret_cast<const float *>(ws + (slot * p.n_heads + head) * terms_bytes(NS) +
-                                                      2 * NS * kTri)[i];
+        if constexpr (TC) {
+            gate = reinterpret_cast<float *>(smem + L::Gate) + (hh % 3) * kGateFloats;
+        } else {
+            for (int i = tid; i < kGateFloats; i += kLocalThreads)
+                gate[i] = reinterpret_cast<const float *>(ws + (slot * p.n_heads + head) * terms_bytes(NS) + 2 * NS * kTri)[i];
+        }
 
         for (int sl = 0; sl < n_sl; ++sl) {
             const int step = hh * n_sl + sl;
             // the next slice; the next head's first one overwrites B and F of this head: it comes
             // after them (below)
-            if (L::kStages == 2 && tid == 0 && sl + 1 < n_sl) load(step + 1);
-            if (L::kStages == 1 && tid == 0 && step > 0) load(step);
+            if (!TC && L::kStages == 2 && tid == 0 && sl + 1 < n_sl) load(step + 1);
+            if (!TC && L::kStages == 1 && tid == 0 && step > 0) load(step);
             ok &= wait_bar(bar(step % L::kStages), (step / L::kStages) & 1);
-            if (sl == 0) __syncthreads();  // the gates
+            if (!TC && sl == 0) __syncthreads();  // the gates
             const uint32_t s = base + (step % L::kStages) * L::kSlice;
             // <S0, dS1>: the diagonals of S0^T dS1 of 16 x 16 blocks, shared out over the warps
 #pragma unroll
@@ -233,21 +348,16 @@ __global__ void __launch_bounds__(kLocalThreads)
                 uint32_t x[NS][4], y[NS][4];
 #pragma unroll
                 for (int q = 0; q < NS; ++q) {
-                    frag_a<RB>(s + L::S + q * L::kState, v, c, x[q]);
-                    frag_b<RB>(s + L::dS + q * L::kState, v, c, y[q]);
+                    frag_a<128>(s + L::S + q * L::kState + state_block<DKP>(v, c), 0, c & 63, x[q]);
+                    frag_b<128>(s + L::dS + q * L::kState + state_block<DKP>(v, c), 0, c & 63, y[q]);
                 }
                 product<NS, NS, NS>(ss, x, y);
             }
 #pragma unroll
             for (int kx = 0; kx < 2; ++kx) {  // 16 value channels
-                uint32_t ao[NI][4], ae[NS][4], au[NS][4];
+                uint32_t ae[NS][4];
 #pragma unroll
-                for (int q = 0; q < NI; ++q) frag_a<64>(s + L::dO + q * L::kIn, wr * 16, kx * 16, ao[q]);
-#pragma unroll
-                for (int q = 0; q < NS; ++q) {
-                    frag_a_t<128>(s + L::E + q * L::kVal, kx * 16, wr * 16, ae[q]);
-                    frag_a_t<128>(s + L::U + q * L::kVal, kx * 16, wr * 16, au[q]);
-                }
+                for (int q = 0; q < NS; ++q) frag_a_t<128>(s + L::E + q * L::kVal, kx * 16, wr * 16, ae[q]);
                 if (wc == 0) {  // E_r.V_r
                     uint32_t av[4];
                     if constexpr (NI == 1) frag_a<64>(s + L::V, wr * 16, kx * 16, av);
@@ -281,30 +391,46 @@ __global__ void __launch_bounds__(kLocalThreads)
                         }
                     }
                 }
-                // dO S0^T, E S0^T, U dS1^T
+                if constexpr (!TC) {
+                    uint32_t ao[NI][4], au[NS][4];
 #pragma unroll
-                for (int n = 0; n < NH; ++n) {
-                    uint32_t b[NS][4];
+                    for (int q = 0; q < NI; ++q) frag_a<64>(s + L::dO + q * L::kIn, wr * 16, kx * 16, ao[q]);
 #pragma unroll
-                    for (int q = 0; q < NS; ++q) frag_b_t<RB>(s + L::S + q * L::kState, kx * 16, wc * KC + n * 16, b[q]);
-                    product<NI, NS, NS>(&xq[2 * n], ao, b);
-                    product<NS, NS, NS>(&xk[2 * n], ae, b);
+                    for (int q = 0; q < NS; ++q) frag_a_t<128>(s + L::U + q * L::kVal, kx * 16, wr * 16, au[q]);
+                    // dO S0^T, E S0^T, U dS1^T
 #pragma unroll
-                    for (int q = 0; q < NS; ++q) frag_b_t<RB>(s + L::dS + q * L::kState, kx * 16, wc * KC + n * 16, b[q]);
-                    product<NS, NS, NS>(&xu[2 * n], au, b);
-                }
-                // dO U^T, E U^T
-#pragma unroll
-                for (int n = 0; n < NP; ++n)
-                    if (NP * wc + n <= wr) {
+                    for (int n = 0; n < NH; ++n) {
+                        const int c = wc * KC + n * 16;
+                        const uint32_t at = s + state_block<DKP>(kx * 16, c);
                         uint32_t b[NS][4];
 #pragma unroll
-                        for (int q = 0; q < NS; ++q) frag_b_t<128>(s + L::U + q * L::kVal, kx * 16, wc * PC + n * 16, b[q]);
-                        product<NI, NS, NS>(&ou[2 * n], ao, b);
-                        product<NS, NS, NS>(&eu[2 * n], ae, b);
+                        for (int q = 0; q < NS; ++q) frag_b_t<128>(at + L::S + q * L::kState, 0, c & 63, b[q]);
+                        product<NI, NS, NS>(&xq[2 * n], ao, b);
+                        product<NS, NS, NS>(&xk[2 * n], ae, b);
+#pragma unroll
+                        for (int q = 0; q < NS; ++q) frag_b_t<128>(at + L::dS + q * L::kState, 0, c & 63, b[q]);
+                        product<NS, NS, NS>(&xu[2 * n], au, b);
                     }
+                    // dO U^T, E U^T
+#pragma unroll
+                    for (int n = 0; n < NP; ++n)
+                        if (NP * wc + n <= wr) {
+                            uint32_t b[NS][4];
+#pragma unroll
+                            for (int q = 0; q < NS; ++q) frag_b_t<128>(s + L::U + q * L::kVal, kx * 16, wc * PC + n * 16, b[q]);
+                            product<NI, NS, NS>(&ou[2 * n], ao, b);
+                            product<NS, NS, NS>(&eu[2 * n], ae, b);
+                        }
+                }
             }
-            __syncthreads();
+            if constexpr (TC) warp_arrive(used(step & 1));
+            else __syncthreads();
+        }
+        [[maybe_unused]] const uint32_t lanes = tmem + ((uint32_t)(wr * 32) << 16);
+        if constexpr (TC) {
+            ok &= wait_bar(sums_done, hh & 1);
+            ptx::tc_fence_after();
+            if (hh > 0) meet();  // B, F and the sums of the head before are done with
         }
 
         // row dots with q and k, and the products scaled into the head sums
@@ -313,21 +439,38 @@ __global__ void __launch_bounds__(kLocalThreads)
         {
             float qx[2] = {0.f, 0.f}, kx_[2] = {0.f, 0.f}, ku[2] = {0.f, 0.f};
 #pragma unroll
-            for (int n = 0; n < 2 * NH; ++n)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t at = key_off(wr * 16 + gr + 8 * h, wc * KC + n * 8 + tq * 2);
-                    float k0 = 0.f, k1 = 0.f, q0 = 0.f, q1 = 0.f;
-#pragma unroll
-                    for (int q = 0; q < NI; ++q) {
-                        const uint32_t wk = *reinterpret_cast<const uint32_t *>(smem + L::K + q * L::kPlane + at);
-                        const uint32_t wq = *reinterpret_cast<const uint32_t *>(smem + L::Q + q * L::kPlane + at);
-                        k0 += lo_f(wk); k1 += hi_f(wk); q0 += lo_f(wq); q1 += hi_f(wq);
-                    }
-                    qx[h] = fmaf(q0, xq[n][2 * h], fmaf(q1, xq[n][2 * h + 1], qx[h]));
-                    kx_[h] = fmaf(k0, xk[n][2 * h], fmaf(k1, xk[n][2 * h + 1], kx_[h]));
-                    ku[h] = fmaf(k0, xu[n][2 * h], fmaf(k1, xu[n][2 * h + 1], ku[h]));
+            for (int part = 0; part < 2 * NH / XT; ++part) {
+                if constexpr (TC) {
+                    const uint32_t at = lanes + wc * KC + part * 32;
+                    ptx::tmem_ld_frag4(at, reinterpret_cast<uint32_t *>(xq[0]));
+                    ptx::tmem_ld_frag4(at + kXk, reinterpret_cast<uint32_t *>(xk[0]));
+                    ptx::tmem_ld_frag4(at + kXu, reinterpret_cast<uint32_t *>(xu[0]));
+                    ptx::tmem_ld_wait();
                 }
+#pragma unroll
+                for (int n = 0; n < XT; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = wr * 16 + gr + 8 * h, t = part * XT + n;
+                        const uint32_t at = key_off(r, wc * KC + t * 8 + tq * 2);
+                        float k0 = 0.f, k1 = 0.f, q0 = 0.f, q1 = 0.f;
+#pragma unroll
+                        for (int q = 0; q < NI; ++q) {
+                            const uint32_t wk = *reinterpret_cast<const uint32_t *>(smem + L::K + q * L::kPlane + at);
+                            const uint32_t wq = *reinterpret_cast<const uint32_t *>(smem + L::Q + q * L::kPlane + at);
+                            k0 += lo_f(wk); k1 += hi_f(wk); q0 += lo_f(wq); q1 += hi_f(wq);
+                        }
+                        qx[h] = fmaf(q0, xq[n][2 * h], fmaf(q1, xq[n][2 * h + 1], qx[h]));
+                        kx_[h] = fmaf(k0, xk[n][2 * h], fmaf(k1, xk[n][2 * h + 1], kx_[h]));
+                        ku[h] = fmaf(k0, xu[n][2 * h], fmaf(k1, xu[n][2 * h + 1], ku[h]));
+                        const float sg = scale * gam[r], gb = -gam[r] * bet[r], de = del[r];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            dq[t][2 * h + i] = fmaf(sg, xq[n][2 * h + i], dq[t][2 * h + i]);
+                            dk[t][2 * h + i] = fmaf(gb, xk[n][2 * h + i], fmaf(de, xu[n][2 * h + i], dk[t][2 * h + i]));
+                        }
+                    }
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = wr * 16 + gr + 8 * h;
@@ -338,17 +481,16 @@ __global__ void __launch_bounds__(kLocalThreads)
                     r_ku[wc * C + r] = d;
                     if (wc == 0) r_ev[r] = e;
                 }
-                const float sg = scale * gam[r], gb = -gam[r] * bet[r], de = del[r];
-#pragma unroll
-                for (int n = 0; n < 2 * NH; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        dq[n][2 * h + i] = fmaf(sg, xq[n][2 * h + i], dq[n][2 * h + i]);
-                        dk[n][2 * h + i] = fmaf(gb, xk[n][2 * h + i], fmaf(de, xu[n][2 * h + i], dk[n][2 * h + i]));
-                    }
             }
         }
         // B (lower) and beta F + its transpose as operands; row and column sums
+        if constexpr (TC) {
+            ptx::tmem_ld_frag4(lanes + kOu + wc * PC, reinterpret_cast<uint32_t *>(ou[0]));
+            ptx::tmem_ld_frag4(lanes + kEu + wc * PC, reinterpret_cast<uint32_t *>(eu[0]));
+            ptx::tmem_ld_wait();
+            ptx::tc_fence_before();
+            warp_arrive(sums_read);
+        }
         {
             float fk[2] = {0.f, 0.f}, mr[2] = {0.f, 0.f};
 #pragma unroll
@@ -412,7 +554,7 @@ __global__ void __launch_bounds__(kLocalThreads)
             for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
             if (lane == 0) r_ss[warp] = d;
         }
-        __syncthreads();
+        meet();
         if (warp == 0) {  // dbeta, dg: two tokens a lane, running sums over the chunk
             float whole = 0.f;
 #pragma unroll
@@ -477,13 +619,19 @@ __global__ void __launch_bounds__(kLocalThreads)
                 product<NI, NI, NI>(&dk[2 * n], at, b);
             }
         }
-        ptx::fence_proxy_async();  // B and F were written by plain stores; the next copies overwrite them
-        __syncthreads();           // B, F, the gates and the sums are done with
-        if (L::kStages == 2 && tid == 0 && hh + 1 < group) load((hh + 1) * n_sl);
+        if constexpr (!TC) {
+            ptx::fence_proxy_async();  // B and F were written by plain stores; the next copies overwrite them
+            __syncthreads();           // B, F, the gates and the sums are done with
+            if (L::kStages == 2 && tid == 0 && hh + 1 < group) load((hh + 1) * n_sl);
+        }
     }
-    if (!ok && tid == 0) {  // nothing may land in shared memory after the block has gone
+    if (!TC && !ok && tid == 0) {  // nothing may land in shared memory after the block has gone
         drain_bar(bar(L::kStages), 0);
         for (int i = max(0, issued - L::kStages); i < issued; ++i) drain_bar(bar(i % L::kStages), (i / L::kStages) & 1);
+    }
+    if constexpr (TC) {
+        ptx::tc_fence_before();
+        __syncthreads();  // the ninth warp may free the tensor memory
     }
     // write the key head's gradients
 #pragma unroll
@@ -524,7 +672,7 @@ cudaError_t backward(const GdrArgs &p, cudaStream_t stream) {
     if (e != cudaSuccess || p.n_tok == 0) return e;
     auto wide = [](const void *x, int d) { return d % 2 == 0 && ((uintptr_t)x % (2 * sizeof(T))) == 0; };
     return launch_dependent(gdr_local_kernel<T, DKP, NS>, dim3((unsigned)n_slots(p.n_tok, p.n_seq), p.n_k_heads),
-                            kLocalThreads, LocalSmem<NI, DKP, NS>::kBytes, stream, maps.q, maps.k, maps.v, maps.dout, p, im,
+                            LocalSmem<T, DKP, NS>::kThreads, LocalSmem<T, DKP, NS>::kBytes, stream, maps.q, maps.k, maps.v, maps.dout, p, im,
                             scale, wide(p.dq, p.d_k) && wide(p.dk, p.d_k), wide(p.dv, p.d_v));
 }
 

@@ -638,7 +638,8 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                     for (int x = 0; x < KX / 2; ++x)
                         store_block(ptx::smem_u32(keep) + q * 16 * DKP * 2 +
-                                        tile_off<DKP * 2>(lane & 15, c0 + x * 16 + (lane >> 4) * 8), sp[q][x]);
+                                        state_block<DKP>(0, c0 + x * 16) +
+                                            tile_off<128>(lane & 15, ((c0 + x * 16) & 63) + (lane >> 4) * 8), sp[q][x]);
             }
             // U^T = (beta Z)^T X^T (X lower triangular), in reverse E^T = dU^T X: each half's diagonal
             // block by its own warp; the block between the halves by the second warp, which gets
@@ -759,7 +760,8 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             *reinterpret_cast<uint32_t *>(rec + (kRev ? rec_s : 0) + q * vp * DKP * 2 +
-                                                          tile_off<DKP * 2>(v0 + gr + (y & 1) * 8, c0 + x * 16 + (y >> 1) * 8 + tq * 2)) = sp[q][x][y];
+                                                          state_block<DKP>(v0, c0 + x * 16) +
+                                                          tile_off<128>(gr + (y & 1) * 8, ((c0 + x * 16) & 63) + (y >> 1) * 8 + tq * 2)) = sp[q][x][y];
             }
             if constexpr (L::kKeep > 0) ptx::fence_proxy_async();
             if (!drained)  // the output that read the next step's buffers is done

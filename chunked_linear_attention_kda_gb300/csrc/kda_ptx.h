@@ -164,6 +164,11 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t addr, uint32_t lbo, uin
     return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16) |
            ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
+// The same with the 64-byte swizzle: K-major rows of 64 bytes, groups of eight rows sbo apart
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t addr, uint32_t sbo) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)((sbo >> 4) & 0x3FFF) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)4 << 61);
+}
 // Instruction descriptor of kind::f16: fp32 accumulator, bf16 A and B; a_mn / b_mn set
 // the operand to MN-major (else K-major).
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
@@ -233,6 +238,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t ta, const uint32_t *r) {
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
         "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
         ::"r"(ta), KDA_W8(0), KDA_W8(8), KDA_W8(16), KDA_W8(24));
+}
+// 16 lanes x 32 columns (warp-collective): r[4 n ..] is the m16n8 accumulator fragment of
+// columns 8 n .. 8 n + 7, the layout of mma16816's d
+__device__ __forceinline__ void tmem_ld_frag4(uint32_t ta, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : KDA_R8(0), KDA_R8(8) : "r"(ta));
 }
 #undef KDA_R8
 #undef KDA_W8
