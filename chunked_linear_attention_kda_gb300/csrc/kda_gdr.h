@@ -99,18 +99,15 @@ __host__ __device__ constexpr size_t terms_bytes(int ns) {
     return (size_t)2 * ns * kTri + kGateFloats * 4;
 }
 
-// Per (slot, value head) of the backward pass, behind the terms: S0^T and dS1^T (value
-// channels x d_k padded to DKP, see state_block), U^T and E^T (value channels x 64), NS planes each,
-// in rows of 128 bytes with the 128-byte swizzle: what tcgen05 reads as MN-major operands.
-__host__ __device__ __forceinline__ int pad_v(int d_v) { return (d_v + 31) & ~31; }
-__host__ __device__ __forceinline__ size_t scan_state_bytes(int ns, int dkp, int d_v) {
-    return (size_t)ns * pad_v(d_v) * dkp * 2;
-}
-__host__ __device__ __forceinline__ size_t scan_value_bytes(int ns, int d_v) {
-    return (size_t)ns * pad_v(d_v) * C * 2;
-}
+// Per (slot, value head) of the backward pass, behind the terms: for each 16 value channels (of
+// d_v padded to a multiple of 32) the forward chain's part, S0^T (16 x d_k padded to DKP) and U^T
+// (16 x 64), then the reverse chain's, dS1^T and E^T; NS planes each, in rows of 128 bytes with the
+// 128-byte swizzle, key channels in halves of 64: what tcgen05 reads as MN-major operands. A
+// chain writes a part in one copy and the local gradients read a block in one.
+__host__ __device__ __forceinline__ constexpr int pad_v(int d_v) { return (d_v + 31) & ~31; }
+__host__ __device__ constexpr int scan_part(int ns, int dkp) { return ns * 16 * (dkp + C) * 2; }
 __host__ __device__ __forceinline__ size_t scan_bytes(int ns, int dkp, int d_v) {
-    return 2 * (scan_state_bytes(ns, dkp, d_v) + scan_value_bytes(ns, d_v));
+    return (size_t)(pad_v(d_v) / 16) * 2 * scan_part(ns, dkp);
 }
 __host__ __device__ __forceinline__ size_t scan_offset(int64_t n_tok, int64_t n_seq, int64_t n_heads, int ns) {
     return (size_t)n_slots(n_tok, n_seq) * n_heads * terms_bytes(ns);
@@ -186,12 +183,9 @@ __device__ __forceinline__ void key_b_t(uint32_t base, int k0, int n0, uint32_t 
     frag_b_t<128>(base + (n0 >> 6) * kHalf, k0, n0 & 63, b);
 }
 
-// A plane of S0^T or dS1^T: blocks of 16 value channels, a block's halves of 64 key channels one
-// after the other, each 16 rows of 128 bytes. Byte offset of the 16 x 16 block at value channel v
-// (a multiple of 16) and key channel c within its half; the rest of the offset is
-// tile_off<128>(v % 16, c % 64).
-template <int DKP>
-__device__ __forceinline__ uint32_t state_block(int v, int c) { return (v >> 4) * (16 * DKP * 2) + (c >> 6) * 2048; }
+// In 16 rows of value channels, halves of 64 key channels one after the other: byte offset of the
+// half of key channel c; the rest is tile_off<128>(value channel, c % 64).
+__device__ __forceinline__ int state_half(int c) { return (c >> 6) * 2048; }
 
 // A sum carried as two floats (the fp64 pipe of this part is narrow).
 struct Two { float hi, lo; };

@@ -53,18 +53,25 @@ struct LocalSmem {
     static constexpr bool TC = kTensor<T, NS>;
     static constexpr int NI = InputPlanes<T>::N;
     static constexpr int kThreads = kLocalThreads + (TC ? 32 : 0);  // a ninth warp loads and issues
-    static constexpr int kStages = NS == 2 ? 2 : 1;
+    // Slices of the value channels: 16 and four buffers with tcgen05 (with 32 and two the copies
+    // waited for each other: 767 us against 16K tokens of 32 heads' KEEP), else 32 and one or two.
+    static constexpr int kSl = TC ? 16 : 32, kStages = TC ? 4 : 1;
     static constexpr int kPlane = C * DKP * 2;
-    static constexpr int kIn = C * 32 * 2, kVal = 32 * C * 2, kState = 32 * DKP * 2;  // one plane of a 32-channel slice
-    static constexpr int dO = 0, V = dO + NI * kIn, U = V + (NI == 1 ? kIn : 0),  // fp32 V is read in place
-                         E = U + NS * kVal, S = E + NS * kVal;
-    static constexpr int dS = S + NS * kState, kSlice = dS + NS * kState;
+    static constexpr int kIn = C * 32 * 2;  // a plane of 32 channels of dO or V
+    // a block of 16 value channels as the chains left it: S, U, dS, E, one plane after the other
+    static constexpr int kVal = 16 * C * 2, kState = 16 * DKP * 2, kBlock = 2 * scan_part(NS, DKP);
+    static constexpr int S = 0, U = NS * kState, dS = kBlock / 2, E = dS + U, kBlocks = kSl / 16 * kBlock;
+    // With tcgen05, dO and V have buffers of their own, three of 32 channels, copied with every
+    // other slice; else they lie behind the slice's blocks (fp32 V is read in place).
+    static constexpr int dO = TC ? 0 : kBlocks, V = dO + NI * kIn;
+    static constexpr int kSlice = TC ? kBlocks : V + (NI == 1 ? kIn : 0);
+    static constexpr int Vals = kStages * kSlice, kVals = TC ? 2 * kIn : 0;
     static constexpr int kTile = C * C * 2;  // bytes of a plane of B and F
-    static constexpr int K = kStages * kSlice, Q = K + NI * kPlane, Pair = Q + NI * kPlane;
+    static constexpr int K = Vals + 3 * kVals, Q = K + NI * kPlane, Pair = Q + NI * kPlane;
     // B and F: without tcgen05 over the first slice buffer, once the slices are done
     static constexpr int B = TC ? Pair + 2 * C * C * 4 : 0, F = B + NI * kTile;
-    static_assert(2 * NI * kTile <= kSlice, "B and F fit a slice buffer");
-    // a head's gates are loaded with its first slice, two slices ahead: with one slice a head
+    static_assert(TC || 2 * NI * kTile <= kSlice, "B and F fit a slice buffer");
+    // a head's gates are loaded with its first slice, four slices ahead: with two slices a head
     // while the head two before is still being finished
     static constexpr int kGates = TC ? 3 : 1;
     static constexpr int Gate = Pair + 2 * C * C * 4 + (TC ? 2 * NI * kTile : 0), Red = Gate + kGates * kGateFloats * 4;
@@ -114,7 +121,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
     const Chunk ch = find_chunk(p.cu_seqlens, p.n_seq, slot);
     if (ch.len == 0) return;
     const int kh = blockIdx.y, group = p.n_heads / p.n_k_heads;
-    const int n_sl = pad_v(p.d_v) / 32;
+    const int n_sl = pad_v(p.d_v) / L::kSl;
     const char *ws = static_cast<const char *>(p.workspace);
     float *pair = reinterpret_cast<float *>(smem + L::Pair);
     float *gate = reinterpret_cast<float *>(smem + L::Gate);  // TC: head hh's at hh % 3
@@ -143,29 +150,24 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
         const uint32_t s = base + (step % L::kStages) * L::kSlice, m = bar(step % L::kStages);
         const char *rec = ws + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
                           (slot * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v);
-        const size_t st = scan_state_bytes(NS, DKP, p.d_v), va = scan_value_bytes(NS, p.d_v);
-        if (TC && sl == 0) {
-            ptx::mbar_arrive_tx(m, L::kSlice + kGateFloats * 4);
+        const bool values = !TC || (sl & 1) == 0, gates = TC && sl == 0;  // n_sl is even with tcgen05
+        ptx::mbar_arrive_tx(m, L::kSlice + (values ? L::kVals : 0) + (gates ? kGateFloats * 4 : 0));
+        if (gates)
             bulk_load(base + L::Gate + (step / n_sl % 3) * kGateFloats * 4,
                       ws + (slot * p.n_heads + head) * terms_bytes(NS) + 2 * NS * kTri, kGateFloats * 4, m);
-        } else {
-            ptx::mbar_arrive_tx(m, L::kSlice);
+        if (values) {
+            const uint32_t to = TC ? base + L::Vals + ((step >> 1) % 3) * L::kVals : s;
+            const int part = TC ? sl >> 1 : sl;
+            if (image) {
+                const char *v = img + 2 * p.n_k_heads * kb + (size_t)part * NI * L::kIn;
+                bulk_load(to + L::dO, v + (p.n_heads + head) * vb, NI * L::kIn, m);
+                if (NI == 1) bulk_load(to + L::V, v + head * vb, L::kIn, m);
+            } else {
+                ptx::tma_load_3d(to + L::dO, &tm_do, part * 32, head, (int)ch.t0, m);
+                if (NI == 1) ptx::tma_load_3d(to + L::V, &tm_v, part * 32, head, (int)ch.t0, m);
+            }
         }
-        if (image) {
-            const char *v = img + 2 * p.n_k_heads * kb + (size_t)sl * NI * L::kIn;
-            bulk_load(s + L::dO, v + (p.n_heads + head) * vb, NI * L::kIn, m);
-            if (NI == 1) bulk_load(s + L::V, v + head * vb, L::kIn, m);
-        } else {
-            ptx::tma_load_3d(s + L::dO, &tm_do, sl * 32, head, (int)ch.t0, m);
-            if (NI == 1) ptx::tma_load_3d(s + L::V, &tm_v, sl * 32, head, (int)ch.t0, m);
-        }
-#pragma unroll
-        for (int q = 0; q < NS; ++q) {
-            bulk_load(s + L::S + q * L::kState, rec + q * (st / NS) + sl * L::kState, L::kState, m);
-            bulk_load(s + L::dS + q * L::kState, rec + st + q * (st / NS) + sl * L::kState, L::kState, m);
-            bulk_load(s + L::U + q * L::kVal, rec + 2 * st + q * (va / NS) + sl * L::kVal, L::kVal, m);
-            bulk_load(s + L::E + q * L::kVal, rec + 2 * st + va + q * (va / NS) + sl * L::kVal, L::kVal, m);
-        }
+        bulk_load(s, rec + (size_t)sl * L::kBlocks, L::kBlocks, m);
     };
     const int loader = TC ? kLocalThreads : 0;
     if (tid == loader) {
@@ -204,52 +206,61 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
         tmem = *reinterpret_cast<const uint32_t *>(smem + L::Bars + 8 * L::kBars);
     }
     if (TC && warp == kLocalThreads / 32) {
-        // The ninth warp: a thread loads the slices and issues their products, two slices ahead of
+        // The ninth warp: a thread loads the slices and issues their products, four slices ahead of
         // the others at most and into the next head's sums while those finish the last head's.
         if constexpr (TC)
             if (lane == 0) {
                 constexpr uint32_t id_o = ptx::idesc_bf16(64, DKP, 0, 1), id_e = ptx::idesc_bf16(64, DKP, 1, 1);
                 constexpr uint32_t id_ou = ptx::idesc_bf16(64, C, 0, 1), id_eu = ptx::idesc_bf16(64, C, 1, 1);
+                constexpr uint32_t id_p = ptx::idesc_bf16(64, C, 0, 0);
                 const int steps = group * n_sl;
-                if (steps > 1) load(1);
-                for (int step = 0, hh = 0, sl = 0; step < steps; ++step) {
-                    const int b = step & 1;
-                    ok = wait_bar(bar(b), (step >> 1) & 1);
-                    if (ok && sl == 0 && hh > 0) ok = wait_bar(sums_read, (hh - 1) & 1);
+                for (int i = 1; i < L::kStages && i < steps; ++i) load(i);
+                // q_r.k_j and k_r.k_j, in the columns of dO U^T and E U^T
+                ok = wait_bar(bar(L::kStages), 0);
+                if (ok) {
+#pragma unroll
+                    for (int kx = 0; kx < DKP / 16; ++kx) {
+                        const uint32_t at = base + (kx >> 2) * kHalf + (kx & 3) * 32;
+                        const uint64_t k = ptx::sdesc_sw128(at + L::K, 16, 1024), q = ptx::sdesc_sw128(at + L::Q, 16, 1024);
+                        ptx::umma_ss(tmem + kOu, q, k, id_p, kx > 0);
+                        ptx::umma_ss(tmem + kEu, k, k, id_p, kx > 0);
+                    }
+                    ptx::umma_commit(sums_done);
+                }
+                for (int step = 0, hh = 0, sl = 0; ok && step < steps; ++step) {
+                    const int b = step % L::kStages;
+                    ok = wait_bar(bar(b), (step / L::kStages) & 1);
+                    if (ok && sl == 0) ok = wait_bar(sums_read, hh & 1);
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    const uint32_t s = base + b * L::kSlice;
+                    const uint32_t s = base + b * L::kSlice, more = sl > 0;
+                    const uint64_t dO = ptx::sdesc_sw64(base + L::Vals + ((step >> 1) % 3) * L::kVals + (sl & 1) * 32, 512);
+                    uint64_t E[NS], U[NS], S[NS], dS[NS];
 #pragma unroll
-                    for (int kx = 0; kx < 2; ++kx) {  // 16 value channels
-                        const uint32_t more = sl + kx > 0;
-                        const uint64_t dO = ptx::sdesc_sw64(s + L::dO + kx * 32, 512);
-                        uint64_t E[NS], U[NS], S[NS], dS[NS];
+                    for (int q = 0; q < NS; ++q) {
+                        E[q] = ptx::sdesc_sw128(s + L::E + q * L::kVal, 1024, 1024);
+                        U[q] = ptx::sdesc_sw128(s + L::U + q * L::kVal, 1024, 1024);
+                        S[q] = ptx::sdesc_sw128(s + L::S + q * L::kState, 2048, 1024);
+                        dS[q] = ptx::sdesc_sw128(s + L::dS + q * L::kState, 2048, 1024);
+                    }
 #pragma unroll
-                        for (int q = 0; q < NS; ++q) {
-                            E[q] = ptx::sdesc_sw128(s + L::E + q * L::kVal + kx * 2048, 1024, 1024);
-                            U[q] = ptx::sdesc_sw128(s + L::U + q * L::kVal + kx * 2048, 1024, 1024);
-                            S[q] = ptx::sdesc_sw128(s + L::S + q * L::kState + kx * (32 * DKP), 2048, 1024);
-                            dS[q] = ptx::sdesc_sw128(s + L::dS + q * L::kState + kx * (32 * DKP), 2048, 1024);
-                        }
+                    for (int i = 0; i < NS; ++i) {
+                        ptx::umma_ss(tmem, dO, S[i], id_o, more | (i > 0));
+                        ptx::umma_ss(tmem + kOu, dO, U[i], id_ou, more | (i > 0));
 #pragma unroll
-                        for (int i = 0; i < NS; ++i) {
-                            ptx::umma_ss(tmem, dO, S[i], id_o, more | (i > 0));
-                            ptx::umma_ss(tmem + kOu, dO, U[i], id_ou, more | (i > 0));
-#pragma unroll
-                            for (int j = 0; i + j < NS; ++j) {
-                                const uint32_t acc = more | (i + j > 0);
-                                ptx::umma_ss(tmem + kXk, E[i], S[j], id_e, acc);
-                                ptx::umma_ss(tmem + kXu, U[i], dS[j], id_e, acc);
-                                ptx::umma_ss(tmem + kEu, E[i], U[j], id_eu, acc);
-                            }
+                        for (int j = 0; i + j < NS; ++j) {
+                            const uint32_t acc = more | (i + j > 0);
+                            ptx::umma_ss(tmem + kXk, E[i], S[j], id_e, acc);
+                            ptx::umma_ss(tmem + kXu, U[i], dS[j], id_e, acc);
+                            ptx::umma_ss(tmem + kEu, E[i], U[j], id_eu, acc);
                         }
                     }
                     ptx::umma_commit(used(b));
                     if (sl == n_sl - 1) ptx::umma_commit(sums_done);
-                    if (step > 0 && step + 1 < steps) {
-                        ok = wait_bar(used(b ^ 1), ((step - 1) >> 1) & 1);
+                    if (step > 0 && step - 1 + L::kStages < steps) {
+                        ok = wait_bar(used((step - 1) % L::kStages), ((step - 1) / L::kStages) & 1);
                         if (!ok) break;
-                        load(step + 1);
+                        load(step - 1 + L::kStages);
                     }
                     if (++sl == n_sl) {
                         sl = 0;
@@ -268,6 +279,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
         if constexpr (TC) ptx::tmem_dealloc(tmem, 512);
         return;
     }
+    [[maybe_unused]] const uint32_t lanes = tmem + ((uint32_t)(wr * 32) << 16);
     // A failed wait sets the flag and the block goes on with what is there: nothing more is
     // loaded, and every later wait returns at once.
     ok = wait_bar(bar(L::kStages), 0);
@@ -275,27 +287,37 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
     // q_r.k_j and k_r.k_j of rows 16 wr .., columns PC wc .., kept by each thread for itself
     {
         float kk[2 * NP][4], qk[2 * NP][4];
+        if constexpr (TC) {
+            ok &= wait_bar(sums_done, 0);
+            ptx::tc_fence_after();
+            ptx::tmem_ld_frag4(lanes + kOu + wc * PC, reinterpret_cast<uint32_t *>(qk[0]));
+            ptx::tmem_ld_frag4(lanes + kEu + wc * PC, reinterpret_cast<uint32_t *>(kk[0]));
+            ptx::tmem_ld_wait();
+            ptx::tc_fence_before();
+            warp_arrive(sums_read);
+        } else {
 #pragma unroll
-        for (int n = 0; n < 2 * NP; ++n)
+            for (int n = 0; n < 2 * NP; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) kk[n][i] = qk[n][i] = 0.f;
+                for (int i = 0; i < 4; ++i) kk[n][i] = qk[n][i] = 0.f;
 #pragma unroll 1
-        for (int c = 0; c < DKP; c += 16) {
-            uint32_t ak[NI][4], aq[NI][4];
+            for (int c = 0; c < DKP; c += 16) {
+                uint32_t ak[NI][4], aq[NI][4];
 #pragma unroll
-            for (int q = 0; q < NI; ++q) {
-                key_a(base + L::K + q * L::kPlane, wr * 16, c, ak[q]);
-                key_a(base + L::Q + q * L::kPlane, wr * 16, c, aq[q]);
-            }
-#pragma unroll
-            for (int n = 0; n < NP; ++n)
-                if (NP * wc + n <= wr) {
-                    uint32_t b[NI][4];
-#pragma unroll
-                    for (int q = 0; q < NI; ++q) key_b(base + L::K + q * L::kPlane, wc * PC + n * 16, c, b[q]);
-                    product<NI, NI, NI>(&kk[2 * n], ak, b);
-                    product<NI, NI, NI>(&qk[2 * n], aq, b);
+                for (int q = 0; q < NI; ++q) {
+                    key_a(base + L::K + q * L::kPlane, wr * 16, c, ak[q]);
+                    key_a(base + L::Q + q * L::kPlane, wr * 16, c, aq[q]);
                 }
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+                    if (NP * wc + n <= wr) {
+                        uint32_t b[NI][4];
+#pragma unroll
+                        for (int q = 0; q < NI; ++q) key_b(base + L::K + q * L::kPlane, wc * PC + n * 16, c, b[q]);
+                        product<NI, NI, NI>(&kk[2 * n], ak, b);
+                        product<NI, NI, NI>(&qk[2 * n], aq, b);
+                    }
+            }
         }
 #pragma unroll
         for (int n = 0; n < 2 * NP; ++n)
@@ -334,33 +356,32 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
 
         for (int sl = 0; sl < n_sl; ++sl) {
             const int step = hh * n_sl + sl;
-            // the next slice; the next head's first one overwrites B and F of this head: it comes
-            // after them (below)
-            if (!TC && L::kStages == 2 && tid == 0 && sl + 1 < n_sl) load(step + 1);
-            if (!TC && L::kStages == 1 && tid == 0 && step > 0) load(step);
+            if (!TC && tid == 0 && step > 0) load(step);
             ok &= wait_bar(bar(step % L::kStages), (step / L::kStages) & 1);
             if (!TC && sl == 0) __syncthreads();  // the gates
             const uint32_t s = base + (step % L::kStages) * L::kSlice;
             // <S0, dS1>: the diagonals of S0^T dS1 of 16 x 16 blocks, shared out over the warps
 #pragma unroll
-            for (int i = 0; i < DKP / 8 / (kLocalThreads / 32); ++i) {
-                const int b = i * (kLocalThreads / 32) + warp, v = (b & 1) * 16, c = (b >> 1) * 16;
+            for (int b = warp; b < L::kSl / 16 * (DKP / 16); b += kLocalThreads / 32) {
+                const int c = b / (L::kSl / 16) * 16;
+                const uint32_t at = s + b % (L::kSl / 16) * L::kBlock + state_half(c);
                 uint32_t x[NS][4], y[NS][4];
 #pragma unroll
                 for (int q = 0; q < NS; ++q) {
-                    frag_a<128>(s + L::S + q * L::kState + state_block<DKP>(v, c), 0, c & 63, x[q]);
-                    frag_b<128>(s + L::dS + q * L::kState + state_block<DKP>(v, c), 0, c & 63, y[q]);
+                    frag_a<128>(at + L::S + q * L::kState, 0, c & 63, x[q]);
+                    frag_b<128>(at + L::dS + q * L::kState, 0, c & 63, y[q]);
                 }
                 product<NS, NS, NS>(ss, x, y);
             }
 #pragma unroll
-            for (int kx = 0; kx < 2; ++kx) {  // 16 value channels
+            for (int kx = 0; kx < L::kSl / 16; ++kx) {  // 16 value channels
+                const int vx = TC ? sl & 1 : kx;         // of the 32 that dO and V are copied by
                 uint32_t ae[NS][4];
 #pragma unroll
-                for (int q = 0; q < NS; ++q) frag_a_t<128>(s + L::E + q * L::kVal, kx * 16, wr * 16, ae[q]);
+                for (int q = 0; q < NS; ++q) frag_a_t<128>(s + kx * L::kBlock + L::E + q * L::kVal, 0, wr * 16, ae[q]);
                 if (wc == 0) {  // E_r.V_r
                     uint32_t av[4];
-                    if constexpr (NI == 1) frag_a<64>(s + L::V, wr * 16, kx * 16, av);
+                    if constexpr (NI == 1) frag_a<64>((TC ? base + L::Vals + ((step >> 1) % 3) * L::kVals : s) + L::V, wr * 16, vx * 16, av);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float x0 = 0.f, x1 = 0.f, z0 = 0.f, z1 = 0.f;
@@ -370,7 +391,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                             z0 = lo_f(av[i]);
                             z1 = hi_f(av[i]);
                         } else {
-                            const int r = wr * 16 + gr + (i & 1) * 8, v = sl * 32 + kx * 16 + (i >> 1) * 8 + tq * 2;
+                            const int r = wr * 16 + gr + (i & 1) * 8, v = sl * L::kSl + kx * 16 + (i >> 1) * 8 + tq * 2;
                             const float *at = static_cast<const float *>(p.v) + (ch.t0 + r) * p.v_stride + (int64_t)head * p.d_v + v;
                             if (r < ch.len && v < p.d_v) z0 = at[0];
                             if (r < ch.len && v + 1 < p.d_v) z1 = at[1];
@@ -383,7 +404,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                         float x0 = 0.f, x1 = 0.f;
 #pragma unroll
                         for (int q = 0; q < NS; ++q) { x0 += lo_f(ae[q][i]); x1 += hi_f(ae[q][i]); }
-                        const int r = wr * 16 + gr + (i & 1) * 8, v = sl * 32 + kx * 16 + (i >> 1) * 8 + tq * 2;
+                        const int r = wr * 16 + gr + (i & 1) * 8, v = sl * L::kSl + kx * 16 + (i >> 1) * 8 + tq * 2;
                         if (r < ch.len && v < p.d_v) {
                             const float be = gate[2 * C + r];
                             put2(static_cast<T *>(p.dv) + ((ch.t0 + r) * p.n_heads + head) * p.d_v + v, be * x0, be * x1,
@@ -396,12 +417,12 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
 #pragma unroll
                     for (int q = 0; q < NI; ++q) frag_a<64>(s + L::dO + q * L::kIn, wr * 16, kx * 16, ao[q]);
 #pragma unroll
-                    for (int q = 0; q < NS; ++q) frag_a_t<128>(s + L::U + q * L::kVal, kx * 16, wr * 16, au[q]);
+                    for (int q = 0; q < NS; ++q) frag_a_t<128>(s + kx * L::kBlock + L::U + q * L::kVal, 0, wr * 16, au[q]);
                     // dO S0^T, E S0^T, U dS1^T
 #pragma unroll
                     for (int n = 0; n < NH; ++n) {
                         const int c = wc * KC + n * 16;
-                        const uint32_t at = s + state_block<DKP>(kx * 16, c);
+                        const uint32_t at = s + kx * L::kBlock + state_half(c);
                         uint32_t b[NS][4];
 #pragma unroll
                         for (int q = 0; q < NS; ++q) frag_b_t<128>(at + L::S + q * L::kState, 0, c & 63, b[q]);
@@ -417,18 +438,17 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                         if (NP * wc + n <= wr) {
                             uint32_t b[NS][4];
 #pragma unroll
-                            for (int q = 0; q < NS; ++q) frag_b_t<128>(s + L::U + q * L::kVal, kx * 16, wc * PC + n * 16, b[q]);
+                            for (int q = 0; q < NS; ++q) frag_b_t<128>(s + kx * L::kBlock + L::U + q * L::kVal, 0, wc * PC + n * 16, b[q]);
                             product<NI, NS, NS>(&ou[2 * n], ao, b);
                             product<NS, NS, NS>(&eu[2 * n], ae, b);
                         }
                 }
             }
-            if constexpr (TC) warp_arrive(used(step & 1));
+            if constexpr (TC) warp_arrive(used(step % L::kStages));
             else __syncthreads();
         }
-        [[maybe_unused]] const uint32_t lanes = tmem + ((uint32_t)(wr * 32) << 16);
         if constexpr (TC) {
-            ok &= wait_bar(sums_done, hh & 1);
+            ok &= wait_bar(sums_done, (hh + 1) & 1);
             ptx::tc_fence_after();
             if (hh > 0) meet();  // B, F and the sums of the head before are done with
         }
@@ -622,7 +642,6 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
         if constexpr (!TC) {
             ptx::fence_proxy_async();  // B and F were written by plain stores; the next copies overwrite them
             __syncthreads();           // B, F, the gates and the sums are done with
-            if (L::kStages == 2 && tid == 0 && hh + 1 < group) load((hh + 1) * n_sl);
         }
     }
     if (!TC && !ok && tid == 0) {  // nothing may land in shared memory after the block has gone

@@ -111,8 +111,8 @@ struct ChainSmem {
     static constexpr int kSx = NS * (DKP / 16) * 512, kUx = NS * 4 * 512, kZx = NS * 2 * 512;
     static constexpr int kUo = kOut ? C * 64 : 0;
     static constexpr int kHandG = DKP * 64, kHand = kRev && kHelp ? kHandG + C * 64 : 0;
-    static constexpr int kKeepS = NS * 16 * DKP * 2, kKeepU = NS * 16 * C * 2;
-    static constexpr int kKeep = kOut || NI == 3 ? 0 : kKeepS + kKeepU;
+    static constexpr int kKeepS = NS * 16 * DKP * 2;
+    static constexpr int kKeep = kOut || NI == 3 ? 0 : scan_part(NS, DKP);
     static constexpr int Sx = 0, Uo = Sx + NH * kSx, Ux = Uo + NH * kUo, Zx = Ux + kUx, Hand = Zx + kZx, Keep = Hand + kHand;
     static constexpr int kPair = Keep + kKeep;
     static constexpr int Ring2 = N1 * kStage1, Pairs = Ring2 + N2 * kStage2, Bars = Pairs + PAIRS * kPair;
@@ -533,7 +533,6 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
         const int c0 = h * (DKP / 2);
         load_state<NT>(S, kRev ? (p.dh_final ? p.dh_final + st_at : nullptr) : (p.h0 ? p.h0 + st_at : nullptr), c0, v0,
                        p.d_k, p.d_v);
-        const size_t rec_s = scan_state_bytes(NS, DKP, p.d_v), rec_u = scan_value_bytes(NS, p.d_v), vp = pad_v(p.d_v);
         [[maybe_unused]] char *keep = pair + L::Keep;
         // this half's planes of S^T to the pair's buffer, the other half's from it
         auto share_state = [&](int hb) {
@@ -566,7 +565,8 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
             const uint32_t s = base + s1 * L::kStage1;
             const float *gate = reinterpret_cast<const float *>(smem + s1 * L::kStage1 + L::Gate1);
             char *rec = ws + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
-                        ((slot0 + c) * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v);
+                        ((slot0 + c) * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v) +
+                        ((v0 >> 4) * 2 + kRev) * scan_part(NS, DKP);
             if (!ready) wait_bar(full1(s1), (i / N1) & 1);
             if (kRev && kHelp) wait_bar(hfull(hb), (i / NH) & 1);
             [[maybe_unused]] const int s2 = N2 > 0 ? i % (N2 > 0 ? N2 : 1) : 0;
@@ -638,8 +638,8 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
 #pragma unroll
                     for (int x = 0; x < KX / 2; ++x)
                         store_block(ptx::smem_u32(keep) + q * 16 * DKP * 2 +
-                                        state_block<DKP>(0, c0 + x * 16) +
-                                            tile_off<128>(lane & 15, ((c0 + x * 16) & 63) + (lane >> 4) * 8), sp[q][x]);
+                                        state_half(c0 + x * 16) +
+                                        tile_off<128>(lane & 15, ((c0 + x * 16) & 63) + (lane >> 4) * 8), sp[q][x]);
             }
             // U^T = (beta Z)^T X^T (X lower triangular), in reverse E^T = dU^T X: each half's diagonal
             // block by its own warp; the block between the halves by the second warp, which gets
@@ -687,8 +687,8 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                         for (int q = 0; q < NS; ++q)
 #pragma unroll
                             for (int y = 0; y < 4; ++y)
-                                *reinterpret_cast<uint32_t *>(rec + 2 * rec_s + (kRev ? rec_u : 0) + q * vp * C * 2 +
-                                                              tile_off<128>(v0 + gr + (y & 1) * 8, (t0 + b) * 16 + (y >> 1) * 8 + tq * 2)) = a[q][y];
+                                *reinterpret_cast<uint32_t *>(rec + L::kKeepS + q * 16 * C * 2 +
+                                                              tile_off<128>(gr + (y & 1) * 8, (t0 + b) * 16 + (y >> 1) * 8 + tq * 2)) = a[q][y];
                     }
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {  // delta U, in reverse -gamma beta E
@@ -759,8 +759,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                     for (int x = 0; x < KX / 2; ++x)
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
-                            *reinterpret_cast<uint32_t *>(rec + (kRev ? rec_s : 0) + q * vp * DKP * 2 +
-                                                          state_block<DKP>(v0, c0 + x * 16) +
+                            *reinterpret_cast<uint32_t *>(rec + q * 16 * DKP * 2 + state_half(c0 + x * 16) +
                                                           tile_off<128>(gr + (y & 1) * 8, ((c0 + x * 16) & 63) + (y >> 1) * 8 + tq * 2)) = sp[q][x][y];
             }
             if constexpr (L::kKeep > 0) ptx::fence_proxy_async();
@@ -770,14 +769,8 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
             share_state((i + 1) % NH);
             if constexpr (L::kKeep > 0) {
                 // both halves are staged (the barrier in share_state): one lane sends the record
-                if (h == 0 && lane == 0 && v0 < vp) {
-#pragma unroll
-                    for (int q = 0; q < NS; ++q) {
-                        bulk_store(rec + (kRev ? rec_s : 0) + (q * vp + v0) * DKP * 2, ptx::smem_u32(keep) + q * 16 * DKP * 2,
-                                   16 * DKP * 2);
-                        bulk_store(rec + 2 * rec_s + (kRev ? rec_u : 0) + (q * vp + v0) * C * 2,
-                                   ptx::smem_u32(keep) + L::kKeepS + q * 16 * C * 2, 16 * C * 2);
-                    }
+                if (h == 0 && lane == 0 && v0 < pad_v(p.d_v)) {
+                    bulk_store(rec, ptx::smem_u32(keep), L::kKeep);
                     ptx::bulk_commit();
                 }
             }
