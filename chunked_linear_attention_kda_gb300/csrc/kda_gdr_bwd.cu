@@ -52,7 +52,7 @@ template <typename T, int DKP, int NS>
 struct LocalSmem {
     static constexpr bool TC = kTensor<T, NS>;
     static constexpr int NI = InputPlanes<T>::N;
-    static constexpr int kThreads = kLocalThreads + (TC ? 32 : 0);  // a ninth warp loads and issues
+    static constexpr int kThreads = kLocalThreads + (TC ? 64 : 0);  // a warp issues products, one loads
     // Slices of the value channels: 16 and four buffers with tcgen05 (with 32 and two the copies
     // waited for each other: 767 us against 16K tokens of 32 heads' KEEP), else 32 and one or two.
     static constexpr int kSl = TC ? 16 : 32, kStages = TC ? 4 : 1;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
         }
         bulk_load(s, rec + (size_t)sl * L::kBlocks, L::kBlocks, m);
     };
-    const int loader = TC ? kLocalThreads : 0;
+    const int loader = TC ? kLocalThreads + 32 : 0;
     if (tid == loader) {
         for (int i = 0; i <= L::kStages; ++i) ptx::mbar_init(bar(i), 1);
         if constexpr (TC) {
@@ -205,16 +205,31 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
         ptx::tc_fence_after();
         tmem = *reinterpret_cast<const uint32_t *>(smem + L::Bars + 8 * L::kBars);
     }
-    if (TC && warp == kLocalThreads / 32) {
-        // The ninth warp: a thread loads the slices and issues their products, four slices ahead of
-        // the others at most and into the next head's sums while those finish the last head's.
-        if constexpr (TC)
+    if constexpr (TC)
+        if (warp > kLocalThreads / 32) {  // a thread loads the slices, as buffers become free
+            if (tid == loader) {
+                const int steps = group * n_sl;
+                for (int step = 1; step < steps; ++step) {
+                    if (step >= L::kStages) ok = wait_bar(used(step % L::kStages), (step / L::kStages - 1) & 1);
+                    if (!ok) break;
+                    load(step);
+                }
+                if (!ok) {  // nothing may land in shared memory after the block has gone
+                    drain_bar(bar(L::kStages), 0);
+                    for (int i = max(0, issued - L::kStages); i < issued; ++i) drain_bar(bar(i % L::kStages), (i / L::kStages) & 1);
+                }
+            }
+            __syncwarp();
+            __syncthreads();  // the end of the others
+            return;
+        } else if (warp == kLocalThreads / 32) {
+            // a thread issues the products, up to four slices ahead of the warps that read the sums,
+            // and those of the next head while they finish the last one's
             if (lane == 0) {
                 constexpr uint32_t id_o = ptx::idesc_bf16(64, DKP, 0, 1), id_e = ptx::idesc_bf16(64, DKP, 1, 1);
                 constexpr uint32_t id_ou = ptx::idesc_bf16(64, C, 0, 1), id_eu = ptx::idesc_bf16(64, C, 1, 1);
                 constexpr uint32_t id_p = ptx::idesc_bf16(64, C, 0, 0);
                 const int steps = group * n_sl;
-                for (int i = 1; i < L::kStages && i < steps; ++i) load(i);
                 // q_r.k_j and k_r.k_j, in the columns of dO U^T and E U^T
                 ok = wait_bar(bar(L::kStages), 0);
                 if (ok) {
@@ -256,29 +271,22 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                         }
                     }
                     ptx::umma_commit(used(b));
-                    if (sl == n_sl - 1) ptx::umma_commit(sums_done);
-                    if (step > 0 && step - 1 + L::kStages < steps) {
-                        ok = wait_bar(used((step - 1) % L::kStages), ((step - 1) / L::kStages) & 1);
-                        if (!ok) break;
-                        load(step - 1 + L::kStages);
-                    }
                     if (++sl == n_sl) {
+                        ptx::umma_commit(sums_done);
                         sl = 0;
                         ++hh;
                     }
                 }
-                if (!ok) {  // nothing may land in shared or tensor memory after the block has gone
+                if (!ok) {  // nor may a product run on
                     ptx::umma_commit(drain);
                     drain_bar(drain, 0);
-                    drain_bar(bar(L::kStages), 0);
-                    for (int i = max(0, issued - L::kStages); i < issued; ++i) drain_bar(bar(i % L::kStages), (i / L::kStages) & 1);
                 }
             }
-        __syncwarp();
-        __syncthreads();  // the others have read the last sums
-        if constexpr (TC) ptx::tmem_dealloc(tmem, 512);
-        return;
-    }
+            __syncwarp();
+            __syncthreads();  // the others have read the last sums
+            ptx::tmem_dealloc(tmem, 512);
+            return;
+        }
     [[maybe_unused]] const uint32_t lanes = tmem + ((uint32_t)(wr * 32) << 16);
     // A failed wait sets the flag and the block goes on with what is there: nothing more is
     // loaded, and every later wait returns at once.
@@ -650,7 +658,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
     }
     if constexpr (TC) {
         ptx::tc_fence_before();
-        __syncthreads();  // the ninth warp may free the tensor memory
+        __syncthreads();  // the tensor memory may be freed
     }
     // write the key head's gradients
 #pragma unroll
