@@ -100,10 +100,10 @@ __host__ __device__ constexpr size_t terms_bytes(int ns) {
 }
 
 // Per (slot, value head) of the backward pass, behind the terms: for each 16 value channels (of
-// d_v padded to a multiple of 32) the forward chain's part, S0^T (16 x d_k padded to DKP) and U^T
-// (16 x 64), then the reverse chain's, dS1^T and E^T; NS planes each, in rows of 128 bytes with the
-// 128-byte swizzle, key channels in halves of 64: what tcgen05 reads as MN-major operands. A
-// chain writes a part in one copy and the local gradients read a block in one.
+// d_v padded to a multiple of 32) the forward chain's part, then the reverse chain's. A part is
+// NS planes of S0^T (16 x d_k padded to DKP) and U^T (16 x 64), or of dS1^T and E^T: DKP / 64 + 1
+// tiles of 16 rows of 128 bytes in the 128-byte swizzle, which tcgen05 reads as one MN-major
+// operand. A chain writes a part in one copy and the local gradients read a block in one.
 __host__ __device__ __forceinline__ constexpr int pad_v(int d_v) { return (d_v + 31) & ~31; }
 __host__ __device__ constexpr int scan_part(int ns, int dkp) { return ns * 16 * (dkp + C) * 2; }
 __host__ __device__ __forceinline__ size_t scan_bytes(int ns, int dkp, int d_v) {
@@ -183,8 +183,8 @@ __device__ __forceinline__ void key_b_t(uint32_t base, int k0, int n0, uint32_t 
     frag_b_t<128>(base + (n0 >> 6) * kHalf, k0, n0 & 63, b);
 }
 
-// In 16 rows of value channels, halves of 64 key channels one after the other: byte offset of the
-// half of key channel c; the rest is tile_off<128>(value channel, c % 64).
+// Byte offset of the tile of key channel c in a plane of a part; U^T or E^T is the tile after the
+// last. The rest of the offset is tile_off<128>(value channel, c % 64).
 __device__ __forceinline__ int state_half(int c) { return (c >> 6) * 2048; }
 
 // A sum carried as two floats (the fp64 pipe of this part is narrow).

@@ -52,15 +52,15 @@ template <typename T, int DKP, int NS>
 struct LocalSmem {
     static constexpr bool TC = kTensor<T, NS>;
     static constexpr int NI = InputPlanes<T>::N;
-    static constexpr int kThreads = kLocalThreads + (TC ? 64 : 0);  // a warp issues products, one loads
+    static constexpr int kThreads = kLocalThreads + (TC ? 96 : 0);  // a warp issues products, one loads, one sums dg
     // Slices of the value channels: 16 and four buffers with tcgen05 (with 32 and two the copies
     // waited for each other: 767 us against 16K tokens of 32 heads' KEEP), else 32 and one or two.
     static constexpr int kSl = TC ? 16 : 32, kStages = TC ? 4 : 1;
     static constexpr int kPlane = C * DKP * 2;
     static constexpr int kIn = C * 32 * 2;  // a plane of 32 channels of dO or V
-    // a block of 16 value channels as the chains left it: S, U, dS, E, one plane after the other
-    static constexpr int kVal = 16 * C * 2, kState = 16 * DKP * 2, kBlock = 2 * scan_part(NS, DKP);
-    static constexpr int S = 0, U = NS * kState, dS = kBlock / 2, E = dS + U, kBlocks = kSl / 16 * kBlock;
+    // a block of 16 value channels as the chains left it: planes of S and U, planes of dS and E
+    static constexpr int kState = 16 * DKP * 2, kPl = 16 * (DKP + C) * 2, kBlock = 2 * NS * kPl;  // kPl: a plane
+    static constexpr int S = 0, U = kState, dS = kBlock / 2, E = dS + U, kBlocks = kSl / 16 * kBlock;
     // With tcgen05, dO and V have buffers of their own, three of 32 channels, copied with every
     // other slice; else they lie behind the slice's blocks (fp32 V is read in place).
     static constexpr int dO = TC ? 0 : kBlocks, V = dO + NI * kIn;
@@ -72,8 +72,8 @@ struct LocalSmem {
     static constexpr int B = TC ? Pair + 2 * C * C * 4 : 0, F = B + NI * kTile;
     static_assert(TC || 2 * NI * kTile <= kSlice, "B and F fit a slice buffer");
     // a head's gates are loaded with its first slice, four slices ahead: with two slices a head
-    // while the head two before is still being finished
-    static constexpr int kGates = TC ? 3 : 1;
+    // while the head three before is still being finished
+    static constexpr int kGates = TC ? 4 : 1;
     static constexpr int Gate = Pair + 2 * C * C * 4 + (TC ? 2 * NI * kTile : 0), Red = Gate + kGates * kGateFloats * 4;
     // Red: [kCols][64] row sums of q.x, k.x, k.x, F k.k, M over the column parts; [64] E.V;
     // [4][64] column sums of M over the row blocks; the warps' parts of <S0, dS1>
@@ -99,6 +99,23 @@ __device__ __forceinline__ float quad_sum(float x) {
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
+// eight values from NS planes of bf16
+template <int NS>
+__device__ __forceinline__ void sum_planes(const char *at, int plane, float *x) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+#pragma unroll
+    for (int q = NS - 1; q >= 0; --q) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(at + q * plane);
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] += lo_f(v[e]);
+            x[2 * e + 1] += hi_f(v[e]);
+        }
+    }
+}
+
 template <typename T, int DKP, int NS>
 __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
     gdr_local_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -107,9 +124,9 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
     constexpr int NI = InputPlanes<T>::N;
     using L = LocalSmem<T, DKP, NS>;
     constexpr bool TC = L::TC;
-    // columns of tensor memory: dO S0^T from 0, E S0^T, U dS1^T, then dO U^T and E U^T (64 tokens
-    // use 16 lanes of each warp's 32)
-    [[maybe_unused]] constexpr int kXk = DKP, kXu = 2 * DKP, kOu = 3 * DKP, kEu = 3 * DKP + C;
+    // columns of tensor memory: dO [S0 U]^T from 0, E [S0 U]^T, U dS1^T (64 tokens use 16 lanes of
+    // each warp's 32)
+    [[maybe_unused]] constexpr int kOu = DKP, kXk = DKP + C, kEu = kXk + DKP, kXu = 2 * kXk;
     constexpr int KC = DKP / kCols, NH = KC / 16;  // a warp's key channels, in steps of 16
     constexpr int PC = C / kCols, NP = PC / 16;              // its columns of the 64 x 64 products
     extern __shared__ __align__(1024) char smem_raw[];
@@ -124,14 +141,58 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
     const int n_sl = pad_v(p.d_v) / L::kSl;
     const char *ws = static_cast<const char *>(p.workspace);
     float *pair = reinterpret_cast<float *>(smem + L::Pair);
-    float *gate = reinterpret_cast<float *>(smem + L::Gate);  // TC: head hh's at hh % 3
+    float *gate = reinterpret_cast<float *>(smem + L::Gate);  // TC: head hh's at hh % kGates
     float *red = reinterpret_cast<float *>(smem + L::Red);
     float *r_qx = red, *r_kx = r_qx + kCols * C, *r_ku = r_kx + kCols * C, *r_fk = r_ku + kCols * C;
     float *r_m = r_fk + kCols * C, *r_ev = r_m + kCols * C, *c_m = r_ev + C, *r_ss = c_m + 4 * C;
 
-    auto meet = [&]() {  // of the threads that compute
-        if constexpr (TC) ptx::named_sync(1, kLocalThreads);
+    auto meet = [&](int id) {  // of the warps that compute and the one that sums dg
+        if constexpr (TC) ptx::named_sync(id, kLocalThreads + 32);
         else __syncthreads();
+    };
+    // dbeta and dg of a head, by a warp: two tokens a lane, running sums over the chunk
+    auto decay_gradients = [&](int head, const float *gate) {
+        const float *gam = gate, *del = gate + C, *bet = gate + 2 * C;
+        float whole = 0.f;
+#pragma unroll
+        for (int i = 0; i < kLocalThreads / 32; ++i) whole += r_ss[i];
+        whole *= gate[3 * C];
+        Two a[2], b[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * lane + i;
+            const float kx = parts(r_kx, r);
+            if (r < ch.len)
+                p.dbeta[(ch.t0 + r) * p.n_heads + head] = r_ev[r] - gam[r] * kx - parts(r_fk, r);
+            const float cols = (c_m[r] + c_m[C + r]) + (c_m[2 * C + r] + c_m[3 * C + r]);
+            a[i] = add({gam[r] * (scale * parts(r_qx, r) - bet[r] * kx), 0.f}, add({parts(r_m, r), 0.f}, {-cols, 0.f}));
+            b[i] = {del[r] * parts(r_ku, r), 0.f};
+        }
+        // inclusive sums over the tokens of a and b; a0, b0 before token 2 lane
+        Two ra = add(a[0], a[1]), rb = add(b[0], b[1]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Two x = {__shfl_up_sync(0xffffffffu, ra.hi, o), __shfl_up_sync(0xffffffffu, ra.lo, o)};
+            const Two y = {__shfl_up_sync(0xffffffffu, rb.hi, o), __shfl_up_sync(0xffffffffu, rb.lo, o)};
+            if (lane >= o) {
+                ra = add(x, ra);
+                rb = add(y, rb);
+            }
+        }
+        const Two total = {__shfl_sync(0xffffffffu, ra.hi, 31), __shfl_sync(0xffffffffu, ra.lo, 31)};
+        Two a0 = {__shfl_up_sync(0xffffffffu, ra.hi, 1), __shfl_up_sync(0xffffffffu, ra.lo, 1)};
+        Two b0 = {__shfl_up_sync(0xffffffffu, rb.hi, 1), __shfl_up_sync(0xffffffffu, rb.lo, 1)};
+        if (lane == 0) a0 = b0 = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * lane + i;
+            const Two before = i ? add(a0, a[0]) : a0, sb = i ? add(b0, b[0]) : b0;
+            const Two sum = add(add(total, {-before.hi, -before.lo}), add({whole, 0.f}, sb));
+            if (r < ch.len) {  // nothing passes a decay of 0: what the sums leave there is rounding
+                const int64_t t = (ch.t0 + r) * p.n_heads + head;
+                p.dg[t] = p.g[t] < kGFloor ? 0.f : sum.hi + sum.lo;
+            }
+        }
     };
     // one thread loads: K and Q, then the 32-channel slices of the value heads, head after head
     auto bar = [&](int i) { return base + L::Bars + 8 * i; };  // a slice buffer's; kStages: K and Q
@@ -153,7 +214,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
         const bool values = !TC || (sl & 1) == 0, gates = TC && sl == 0;  // n_sl is even with tcgen05
         ptx::mbar_arrive_tx(m, L::kSlice + (values ? L::kVals : 0) + (gates ? kGateFloats * 4 : 0));
         if (gates)
-            bulk_load(base + L::Gate + (step / n_sl % 3) * kGateFloats * 4,
+            bulk_load(base + L::Gate + (step / n_sl % L::kGates) * kGateFloats * 4,
                       ws + (slot * p.n_heads + head) * terms_bytes(NS) + 2 * NS * kTri, kGateFloats * 4, m);
         if (values) {
             const uint32_t to = TC ? base + L::Vals + ((step >> 1) % 3) * L::kVals : s;
@@ -206,7 +267,15 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
         tmem = *reinterpret_cast<const uint32_t *>(smem + L::Bars + 8 * L::kBars);
     }
     if constexpr (TC)
-        if (warp > kLocalThreads / 32) {  // a thread loads the slices, as buffers become free
+        if (warp == kLocalThreads / 32 + 2) {  // dbeta and dg
+            for (int hh = 0; hh < group; ++hh) {
+                meet(2);
+                decay_gradients(kh * group + hh, reinterpret_cast<float *>(smem + L::Gate) + (hh % L::kGates) * kGateFloats);
+                if (hh + 1 < group) ptx::named_arrive(1, kLocalThreads + 32);
+            }
+            __syncthreads();  // the end of the others
+            return;
+        } else if (warp == kLocalThreads / 32 + 1) {  // a thread loads the slices, as buffers become free
             if (tid == loader) {
                 const int steps = group * n_sl;
                 for (int step = 1; step < steps; ++step) {
@@ -226,9 +295,8 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
             // a thread issues the products, up to four slices ahead of the warps that read the sums,
             // and those of the next head while they finish the last one's
             if (lane == 0) {
-                constexpr uint32_t id_o = ptx::idesc_bf16(64, DKP, 0, 1), id_e = ptx::idesc_bf16(64, DKP, 1, 1);
-                constexpr uint32_t id_ou = ptx::idesc_bf16(64, C, 0, 1), id_eu = ptx::idesc_bf16(64, C, 1, 1);
-                constexpr uint32_t id_p = ptx::idesc_bf16(64, C, 0, 0);
+                constexpr uint32_t id_o = ptx::idesc_bf16(64, DKP + C, 0, 1), id_e = ptx::idesc_bf16(64, DKP + C, 1, 1);
+                constexpr uint32_t id_u = ptx::idesc_bf16(64, DKP, 1, 1), id_p = ptx::idesc_bf16(64, C, 0, 0);
                 const int steps = group * n_sl;
                 // q_r.k_j and k_r.k_j, in the columns of dO U^T and E U^T
                 ok = wait_bar(bar(L::kStages), 0);
@@ -253,21 +321,19 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                     uint64_t E[NS], U[NS], S[NS], dS[NS];
 #pragma unroll
                     for (int q = 0; q < NS; ++q) {
-                        E[q] = ptx::sdesc_sw128(s + L::E + q * L::kVal, 1024, 1024);
-                        U[q] = ptx::sdesc_sw128(s + L::U + q * L::kVal, 1024, 1024);
-                        S[q] = ptx::sdesc_sw128(s + L::S + q * L::kState, 2048, 1024);
-                        dS[q] = ptx::sdesc_sw128(s + L::dS + q * L::kState, 2048, 1024);
+                        E[q] = ptx::sdesc_sw128(s + L::E + q * L::kPl, 1024, 1024);
+                        U[q] = ptx::sdesc_sw128(s + L::U + q * L::kPl, 1024, 1024);
+                        S[q] = ptx::sdesc_sw128(s + L::S + q * L::kPl, 2048, 1024);
+                        dS[q] = ptx::sdesc_sw128(s + L::dS + q * L::kPl, 2048, 1024);
                     }
 #pragma unroll
                     for (int i = 0; i < NS; ++i) {
                         ptx::umma_ss(tmem, dO, S[i], id_o, more | (i > 0));
-                        ptx::umma_ss(tmem + kOu, dO, U[i], id_ou, more | (i > 0));
 #pragma unroll
                         for (int j = 0; i + j < NS; ++j) {
                             const uint32_t acc = more | (i + j > 0);
                             ptx::umma_ss(tmem + kXk, E[i], S[j], id_e, acc);
-                            ptx::umma_ss(tmem + kXu, U[i], dS[j], id_e, acc);
-                            ptx::umma_ss(tmem + kEu, E[i], U[j], id_eu, acc);
+                            ptx::umma_ss(tmem + kXu, U[i], dS[j], id_u, acc);
                         }
                     }
                     ptx::umma_commit(used(b));
@@ -342,6 +408,36 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
 #pragma unroll
         for (int i = 0; i < 4; ++i) dq[n][i] = dk[n][i] = 0.f;
 
+    // dQ += B K, dK += B^T Q - (beta F + its transpose) K
+    auto add_pairs = [&]() {
+#pragma unroll
+        for (int kx = 0; kx < 4; ++kx) {
+            uint32_t ab[NI][4], at[NI][4], af[NI][4];
+#pragma unroll
+            for (int q = 0; q < NI; ++q) {
+                frag_a<128>(base + L::B + q * L::kTile, wr * 16, kx * 16, ab[q]);
+                frag_a_t<128>(base + L::B + q * L::kTile, kx * 16, wr * 16, at[q]);
+                frag_a<128>(base + L::F + q * L::kTile, wr * 16, kx * 16, af[q]);
+                uint32_t ft[4];
+                frag_a_t<128>(base + L::F + q * L::kTile, kx * 16, wr * 16, ft);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) af[q][i] |= ft[i];  // of the two at least one is +0
+            }
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+                uint32_t b[NI][4];
+#pragma unroll
+                for (int q = 0; q < NI; ++q) key_b_t(base + L::K + q * L::kPlane, kx * 16, wc * KC + n * 16, b[q]);
+                if (kx <= wr) product<NI, NI, NI>(&dq[2 * n], ab, b);
+                product<NI, NI, NI>(&dk[2 * n], af, b);
+                if (kx < wr) continue;  // B is lower triangular
+#pragma unroll
+                for (int q = 0; q < NI; ++q) key_b_t(base + L::Q + q * L::kPlane, kx * 16, wc * KC + n * 16, b[q]);
+                product<NI, NI, NI>(&dk[2 * n], at, b);
+            }
+        }
+    };
+
     for (int hh = 0; hh < group; ++hh) {
         const int head = kh * group + hh;
         constexpr int XT = TC ? 4 : 2 * NH;  // tiles of 8 key channels in registers at a time
@@ -353,10 +449,9 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
             zero<2 * NP>(ou);
             zero<2 * NP>(eu);
         }
-        float ev[2] = {0.f, 0.f}, ss[2][4];
-        zero<2>(ss);
+        float ev[2] = {0.f, 0.f}, ss = 0.f;
         if constexpr (TC) {
-            gate = reinterpret_cast<float *>(smem + L::Gate) + (hh % 3) * kGateFloats;
+            gate = reinterpret_cast<float *>(smem + L::Gate) + (hh % L::kGates) * kGateFloats;
         } else {
             for (int i = tid; i < kGateFloats; i += kLocalThreads)
                 gate[i] = reinterpret_cast<const float *>(ws + (slot * p.n_heads + head) * terms_bytes(NS) + 2 * NS * kTri)[i];
@@ -368,25 +463,22 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
             ok &= wait_bar(bar(step % L::kStages), (step / L::kStages) & 1);
             if (!TC && sl == 0) __syncthreads();  // the gates
             const uint32_t s = base + (step % L::kStages) * L::kSlice;
-            // <S0, dS1>: the diagonals of S0^T dS1 of 16 x 16 blocks, shared out over the warps
+            // <S0, dS1>: both lie in the same order
 #pragma unroll
-            for (int b = warp; b < L::kSl / 16 * (DKP / 16); b += kLocalThreads / 32) {
-                const int c = b / (L::kSl / 16) * 16;
-                const uint32_t at = s + b % (L::kSl / 16) * L::kBlock + state_half(c);
-                uint32_t x[NS][4], y[NS][4];
+            for (int i = tid * 16; i < L::kSl / 16 * L::kState; i += kLocalThreads * 16) {
+                const char *at = smem + (s - base) + i / L::kState * L::kBlock + i % L::kState;
+                float x[8], y[8];
+                sum_planes<NS>(at + L::S, L::kPl, x);
+                sum_planes<NS>(at + L::dS, L::kPl, y);
 #pragma unroll
-                for (int q = 0; q < NS; ++q) {
-                    frag_a<128>(at + L::S + q * L::kState, 0, c & 63, x[q]);
-                    frag_b<128>(at + L::dS + q * L::kState, 0, c & 63, y[q]);
-                }
-                product<NS, NS, NS>(ss, x, y);
+                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], y[e], ss);
             }
 #pragma unroll
             for (int kx = 0; kx < L::kSl / 16; ++kx) {  // 16 value channels
                 const int vx = TC ? sl & 1 : kx;         // of the 32 that dO and V are copied by
                 uint32_t ae[NS][4];
 #pragma unroll
-                for (int q = 0; q < NS; ++q) frag_a_t<128>(s + kx * L::kBlock + L::E + q * L::kVal, 0, wr * 16, ae[q]);
+                for (int q = 0; q < NS; ++q) frag_a_t<128>(s + kx * L::kBlock + L::E + q * L::kPl, 0, wr * 16, ae[q]);
                 if (wc == 0) {  // E_r.V_r
                     uint32_t av[4];
                     if constexpr (NI == 1) frag_a<64>((TC ? base + L::Vals + ((step >> 1) % 3) * L::kVals : s) + L::V, wr * 16, vx * 16, av);
@@ -425,7 +517,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
 #pragma unroll
                     for (int q = 0; q < NI; ++q) frag_a<64>(s + L::dO + q * L::kIn, wr * 16, kx * 16, ao[q]);
 #pragma unroll
-                    for (int q = 0; q < NS; ++q) frag_a_t<128>(s + kx * L::kBlock + L::U + q * L::kVal, 0, wr * 16, au[q]);
+                    for (int q = 0; q < NS; ++q) frag_a_t<128>(s + kx * L::kBlock + L::U + q * L::kPl, 0, wr * 16, au[q]);
                     // dO S0^T, E S0^T, U dS1^T
 #pragma unroll
                     for (int n = 0; n < NH; ++n) {
@@ -433,11 +525,11 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                         const uint32_t at = s + kx * L::kBlock + state_half(c);
                         uint32_t b[NS][4];
 #pragma unroll
-                        for (int q = 0; q < NS; ++q) frag_b_t<128>(at + L::S + q * L::kState, 0, c & 63, b[q]);
+                        for (int q = 0; q < NS; ++q) frag_b_t<128>(at + L::S + q * L::kPl, 0, c & 63, b[q]);
                         product<NI, NS, NS>(&xq[2 * n], ao, b);
                         product<NS, NS, NS>(&xk[2 * n], ae, b);
 #pragma unroll
-                        for (int q = 0; q < NS; ++q) frag_b_t<128>(at + L::dS + q * L::kState, 0, c & 63, b[q]);
+                        for (int q = 0; q < NS; ++q) frag_b_t<128>(at + L::dS + q * L::kPl, 0, c & 63, b[q]);
                         product<NS, NS, NS>(&xu[2 * n], au, b);
                     }
                     // dO U^T, E U^T
@@ -446,7 +538,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                         if (NP * wc + n <= wr) {
                             uint32_t b[NS][4];
 #pragma unroll
-                            for (int q = 0; q < NS; ++q) frag_b_t<128>(s + kx * L::kBlock + L::U + q * L::kVal, 0, wc * PC + n * 16, b[q]);
+                            for (int q = 0; q < NS; ++q) frag_b_t<128>(s + kx * L::kBlock + L::U + q * L::kPl, 0, wc * PC + n * 16, b[q]);
                             product<NI, NS, NS>(&ou[2 * n], ao, b);
                             product<NS, NS, NS>(&eu[2 * n], ae, b);
                         }
@@ -456,9 +548,10 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
             else __syncthreads();
         }
         if constexpr (TC) {
+            if (hh > 0) add_pairs();  // the last head's
             ok &= wait_bar(sums_done, (hh + 1) & 1);
             ptx::tc_fence_after();
-            if (hh > 0) meet();  // B, F and the sums of the head before are done with
+            if (hh > 0) meet(1);  // B, F and the sums of the head before are done with
         }
 
         // row dots with q and k, and the products scaled into the head sums
@@ -511,7 +604,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                 }
             }
         }
-        // B (lower) and beta F + its transpose as operands; row and column sums
+        // B (lower) and -beta F (below the diagonal) as operands; row and column sums
         if constexpr (TC) {
             ptx::tmem_ld_frag4(lanes + kOu + wc * PC, reinterpret_cast<uint32_t *>(ou[0]));
             ptx::tmem_ld_frag4(lanes + kEu + wc * PC, reinterpret_cast<uint32_t *>(eu[0]));
@@ -537,7 +630,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                         const float e = j + i <= r ? ex2(d) : 0.f;
                         bv[i] = j + i <= r ? scale * e * ou[n][2 * h + i] : 0.f;
                         const float f = j + i < r ? e * eu[n][2 * h + i] : 0.f;
-                        fv[i] = -bet[r] * f;
+                        fv[i] = j + i < r ? -bet[r] * f : 0.f;
                         fk[h] = fmaf(f, kk, fk[h]);
                         const float m = j + i < r ? fmaf(bv[i], qk, fv[i] * kk) : 0.f;
                         mr[h] += m;
@@ -549,16 +642,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
 #pragma unroll
                     for (int q = 0; q < NI; ++q) {
                         *reinterpret_cast<uint32_t *>(smem + L::B + q * L::kTile + tile_off<128>(r, j)) = wb[q];
-                        char *ft = smem + L::F + q * L::kTile;
-                        if (j < r) {  // (r, j) and, below the diagonal, (r, j + 1) with their mirror images
-                            *reinterpret_cast<uint16_t *>(ft + tile_off<128>(r, j)) = (uint16_t)wf[q];
-                            *reinterpret_cast<uint16_t *>(ft + tile_off<128>(j, r)) = (uint16_t)wf[q];
-                        }
-                        if (j + 1 < r) {
-                            *reinterpret_cast<uint16_t *>(ft + tile_off<128>(r, j + 1)) = (uint16_t)(wf[q] >> 16);
-                            *reinterpret_cast<uint16_t *>(ft + tile_off<128>(j + 1, r)) = (uint16_t)(wf[q] >> 16);
-                        }
-                        if (j == r || j + 1 == r) *reinterpret_cast<uint16_t *>(ft + tile_off<128>(r, r)) = 0;
+                        *reinterpret_cast<uint32_t *>(smem + L::F + q * L::kTile + tile_off<128>(r, j)) = wf[q];
                     }
                 }
 #pragma unroll
@@ -576,77 +660,15 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                     r_m[wc * C + wr * 16 + gr + 8 * h] = b;
                 }
             }
-            // rows gr of the first tile's columns 0..7, rows gr + 8 of the second's 8..15
-            float d = gr == 2 * tq ? ss[0][0] + ss[1][2] : gr == 2 * tq + 1 ? ss[0][1] + ss[1][3] : 0.f;
+            float d = ss;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
             if (lane == 0) r_ss[warp] = d;
         }
-        meet();
-        if (warp == 0) {  // dbeta, dg: two tokens a lane, running sums over the chunk
-            float whole = 0.f;
-#pragma unroll
-            for (int i = 0; i < kLocalThreads / 32; ++i) whole += r_ss[i];
-            whole *= gate[3 * C];
-            Two a[2], b[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 2 * lane + i;
-                const float kx = parts(r_kx, r);
-                if (r < ch.len)
-                    p.dbeta[(ch.t0 + r) * p.n_heads + head] = r_ev[r] - gam[r] * kx - parts(r_fk, r);
-                const float cols = (c_m[r] + c_m[C + r]) + (c_m[2 * C + r] + c_m[3 * C + r]);
-                a[i] = add({gam[r] * (scale * parts(r_qx, r) - bet[r] * kx), 0.f}, add({parts(r_m, r), 0.f}, {-cols, 0.f}));
-                b[i] = {del[r] * parts(r_ku, r), 0.f};
-            }
-            // inclusive sums over the tokens of a and b; a0, b0 before token 2 lane
-            Two ra = add(a[0], a[1]), rb = add(b[0], b[1]);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const Two x = {__shfl_up_sync(0xffffffffu, ra.hi, o), __shfl_up_sync(0xffffffffu, ra.lo, o)};
-                const Two y = {__shfl_up_sync(0xffffffffu, rb.hi, o), __shfl_up_sync(0xffffffffu, rb.lo, o)};
-                if (lane >= o) {
-                    ra = add(x, ra);
-                    rb = add(y, rb);
-                }
-            }
-            const Two total = {__shfl_sync(0xffffffffu, ra.hi, 31), __shfl_sync(0xffffffffu, ra.lo, 31)};
-            Two a0 = {__shfl_up_sync(0xffffffffu, ra.hi, 1), __shfl_up_sync(0xffffffffu, ra.lo, 1)};
-            Two b0 = {__shfl_up_sync(0xffffffffu, rb.hi, 1), __shfl_up_sync(0xffffffffu, rb.lo, 1)};
-            if (lane == 0) a0 = b0 = {0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 2 * lane + i;
-                const Two before = i ? add(a0, a[0]) : a0, sb = i ? add(b0, b[0]) : b0;
-                const Two sum = add(add(total, {-before.hi, -before.lo}), add({whole, 0.f}, sb));
-                if (r < ch.len) {  // nothing passes a decay of 0: what the sums leave there is rounding
-                    const int64_t t = (ch.t0 + r) * p.n_heads + head;
-                    p.dg[t] = p.g[t] < kGFloor ? 0.f : sum.hi + sum.lo;
-                }
-            }
-        }
-        // dQ += B K, dK += B^T Q - (beta F + its transpose) K
-#pragma unroll
-        for (int kx = 0; kx < 4; ++kx) {
-            uint32_t ab[NI][4], at[NI][4], af[NI][4];
-#pragma unroll
-            for (int q = 0; q < NI; ++q) {
-                frag_a<128>(base + L::B + q * L::kTile, wr * 16, kx * 16, ab[q]);
-                frag_a_t<128>(base + L::B + q * L::kTile, kx * 16, wr * 16, at[q]);
-                frag_a<128>(base + L::F + q * L::kTile, wr * 16, kx * 16, af[q]);
-            }
-#pragma unroll
-            for (int n = 0; n < NH; ++n) {
-                uint32_t b[NI][4];
-#pragma unroll
-                for (int q = 0; q < NI; ++q) key_b_t(base + L::K + q * L::kPlane, kx * 16, wc * KC + n * 16, b[q]);
-                product<NI, NI, NI>(&dq[2 * n], ab, b);
-                product<NI, NI, NI>(&dk[2 * n], af, b);
-#pragma unroll
-                for (int q = 0; q < NI; ++q) key_b_t(base + L::Q + q * L::kPlane, kx * 16, wc * KC + n * 16, b[q]);
-                product<NI, NI, NI>(&dk[2 * n], at, b);
-            }
-        }
+        meet(2);
+        if (!TC && warp == 0) decay_gradients(head, gate);
+        // With tcgen05 the next head's slices come first: their buffers are waited for.
+        if (!TC || hh + 1 == group) add_pairs();
         if constexpr (!TC) {
             ptx::fence_proxy_async();  // B and F were written by plain stores; the next copies overwrite them
             __syncthreads();           // B, F, the gates and the sums are done with

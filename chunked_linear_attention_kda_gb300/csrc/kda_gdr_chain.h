@@ -111,7 +111,7 @@ struct ChainSmem {
     static constexpr int kSx = NS * (DKP / 16) * 512, kUx = NS * 4 * 512, kZx = NS * 2 * 512;
     static constexpr int kUo = kOut ? C * 64 : 0;
     static constexpr int kHandG = DKP * 64, kHand = kRev && kHelp ? kHandG + C * 64 : 0;
-    static constexpr int kKeepS = NS * 16 * DKP * 2;
+    static constexpr int kKeepP = 16 * (DKP + C) * 2, kKeepV = 16 * DKP * 2;  // a plane; U or E in it
     static constexpr int kKeep = kOut || NI == 3 ? 0 : scan_part(NS, DKP);
     static constexpr int Sx = 0, Uo = Sx + NH * kSx, Ux = Uo + NH * kUo, Zx = Ux + kUx, Hand = Zx + kZx, Keep = Hand + kHand;
     static constexpr int kPair = Keep + kKeep;
@@ -637,7 +637,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                 for (int q = 0; q < NS; ++q)
 #pragma unroll
                     for (int x = 0; x < KX / 2; ++x)
-                        store_block(ptx::smem_u32(keep) + q * 16 * DKP * 2 +
+                        store_block(ptx::smem_u32(keep) + q * L::kKeepP +
                                         state_half(c0 + x * 16) +
                                         tile_off<128>(lane & 15, ((c0 + x * 16) & 63) + (lane >> 4) * 8), sp[q][x]);
             }
@@ -680,14 +680,14 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                     } else if constexpr (L::kKeep > 0) {
 #pragma unroll
                         for (int q = 0; q < NS; ++q)
-                            store_block(ptx::smem_u32(keep) + L::kKeepS + q * 16 * C * 2 +
+                            store_block(ptx::smem_u32(keep) + q * L::kKeepP + L::kKeepV +
                                             tile_off<128>(lane & 15, (t0 + b) * 16 + (lane >> 4) * 8), a[q]);
                     } else {  // straight to the record
 #pragma unroll
                         for (int q = 0; q < NS; ++q)
 #pragma unroll
                             for (int y = 0; y < 4; ++y)
-                                *reinterpret_cast<uint32_t *>(rec + L::kKeepS + q * 16 * C * 2 +
+                                *reinterpret_cast<uint32_t *>(rec + q * L::kKeepP + L::kKeepV +
                                                               tile_off<128>(gr + (y & 1) * 8, (t0 + b) * 16 + (y >> 1) * 8 + tq * 2)) = a[q][y];
                     }
 #pragma unroll
@@ -759,7 +759,7 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
                     for (int x = 0; x < KX / 2; ++x)
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
-                            *reinterpret_cast<uint32_t *>(rec + q * 16 * DKP * 2 + state_half(c0 + x * 16) +
+                            *reinterpret_cast<uint32_t *>(rec + q * L::kKeepP + state_half(c0 + x * 16) +
                                                           tile_off<128>(gr + (y & 1) * 8, ((c0 + x * 16) & 63) + (y >> 1) * 8 + tq * 2)) = sp[q][x][y];
             }
             if constexpr (L::kKeep > 0) ptx::fence_proxy_async();
