@@ -77,7 +77,7 @@ struct LocalSmem {
     static constexpr int Gate = Pair + 2 * C * C * 4 + (TC ? 2 * NI * kTile : 0), Red = Gate + kGates * kGateFloats * 4;
     // Red: [kCols][64] row sums of q.x, k.x, k.x, F k.k, M over the column parts; [64] E.V;
     // [4][64] column sums of M over the row blocks; the warps' parts of <S0, dS1>
-    static constexpr int kRed = 5 * kCols * C + C + 4 * C + kLocalThreads / 32;
+    static constexpr int kRed = 5 * kCols * C + C + 4 * C + 4;
     static constexpr int Bars = (Red + kRed * 4 + 7) / 8 * 8;
     // a slice buffer full [kStages], K and Q full; with tcgen05 also a slice buffer read
     // [kStages], a head's sums complete, read, and one to drain by; then the tensor memory's address
@@ -151,11 +151,12 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
         else __syncthreads();
     };
     // dbeta and dg of a head, by a warp: two tokens a lane, running sums over the chunk
-    auto decay_gradients = [&](int head, const float *gate) {
+    auto decay_gradients = [&](int hh, const float *gate) {
+        const int head = kh * group + hh;
         const float *gam = gate, *del = gate + C, *bet = gate + 2 * C;
         float whole = 0.f;
 #pragma unroll
-        for (int i = 0; i < kLocalThreads / 32; ++i) whole += r_ss[i];
+        for (int i = 0; i < 4; ++i) whole += r_ss[i];
         whole *= gate[3 * C];
         Two a[2], b[2];
 #pragma unroll
@@ -204,21 +205,23 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
     const char *img = ws + im.offset + (im.all ? slot : (int64_t)ch.seq) * img_rec;
     bool ok = true;
     int issued = 0;
-    auto load = [&](int step) {  // slice `step % n_sl` of value head `step / n_sl`
+    // the records of a key head's value heads lie one after the other
+    const char *rec = ws + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
+                      (slot * p.n_heads + kh * group) * scan_bytes(NS, DKP, p.d_v);
+    const char *gates_of = ws + (slot * p.n_heads + kh * group) * terms_bytes(NS) + 2 * NS * kTri;
+    auto load = [&](int step, int hh, int sl) {  // slice sl of value head hh; step = hh n_sl + sl
         if (!ok) return;
         ++issued;
-        const int head = kh * group + step / n_sl, sl = step % n_sl;
         const uint32_t s = base + (step % L::kStages) * L::kSlice, m = bar(step % L::kStages);
-        const char *rec = ws + scan_offset(p.n_tok, p.n_seq, p.n_heads, NS) +
-                          (slot * p.n_heads + head) * scan_bytes(NS, DKP, p.d_v);
         const bool values = !TC || (sl & 1) == 0, gates = TC && sl == 0;  // n_sl is even with tcgen05
         ptx::mbar_arrive_tx(m, L::kSlice + (values ? L::kVals : 0) + (gates ? kGateFloats * 4 : 0));
+        bulk_load(s, rec + (size_t)step * L::kBlocks, L::kBlocks, m);
         if (gates)
-            bulk_load(base + L::Gate + (step / n_sl % L::kGates) * kGateFloats * 4,
-                      ws + (slot * p.n_heads + head) * terms_bytes(NS) + 2 * NS * kTri, kGateFloats * 4, m);
+            bulk_load(base + L::Gate + (hh % L::kGates) * kGateFloats * 4, gates_of + hh * terms_bytes(NS),
+                      kGateFloats * 4, m);
         if (values) {
             const uint32_t to = TC ? base + L::Vals + ((step >> 1) % 3) * L::kVals : s;
-            const int part = TC ? sl >> 1 : sl;
+            const int part = TC ? sl >> 1 : sl, head = kh * group + hh;
             if (image) {
                 const char *v = img + 2 * p.n_k_heads * kb + (size_t)part * NI * L::kIn;
                 bulk_load(to + L::dO, v + (p.n_heads + head) * vb, NI * L::kIn, m);
@@ -228,7 +231,6 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                 if (NI == 1) ptx::tma_load_3d(to + L::V, &tm_v, part * 32, head, (int)ch.t0, m);
             }
         }
-        bulk_load(s, rec + (size_t)sl * L::kBlocks, L::kBlocks, m);
     };
     const int loader = TC ? kLocalThreads + 32 : 0;
     if (tid == loader) {
@@ -257,7 +259,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                 ptx::tma_load_3d(base + L::K + h * kHalf, &tm_k, h * 64, kh, (int)ch.t0, m);
             }
         }
-        load(0);
+        load(0, 0, 0);
     }
     if constexpr (TC) ptx::tc_fence_before();
     __syncthreads();
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
         if (warp == kLocalThreads / 32 + 2) {  // dbeta and dg
             for (int hh = 0; hh < group; ++hh) {
                 meet(2);
-                decay_gradients(kh * group + hh, reinterpret_cast<float *>(smem + L::Gate) + (hh % L::kGates) * kGateFloats);
+                decay_gradients(hh, reinterpret_cast<float *>(smem + L::Gate) + (hh % L::kGates) * kGateFloats);
                 if (hh + 1 < group) ptx::named_arrive(1, kLocalThreads + 32);
             }
             __syncthreads();  // the end of the others
@@ -278,10 +280,14 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
         } else if (warp == kLocalThreads / 32 + 1) {  // a thread loads the slices, as buffers become free
             if (tid == loader) {
                 const int steps = group * n_sl;
-                for (int step = 1; step < steps; ++step) {
+                for (int step = 1, hh = 0, sl = 1; step < steps; ++step, ++sl) {
+                    if (sl == n_sl) {
+                        sl = 0;
+                        ++hh;
+                    }
                     if (step >= L::kStages) ok = wait_bar(used(step % L::kStages), (step / L::kStages - 1) & 1);
                     if (!ok) break;
-                    load(step);
+                    load(step, hh, sl);
                 }
                 if (!ok) {  // nothing may land in shared memory after the block has gone
                     drain_bar(bar(L::kStages), 0);
@@ -459,20 +465,21 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
 
         for (int sl = 0; sl < n_sl; ++sl) {
             const int step = hh * n_sl + sl;
-            if (!TC && tid == 0 && step > 0) load(step);
+            if (!TC && tid == 0 && step > 0) load(step, hh, sl);
             ok &= wait_bar(bar(step % L::kStages), (step / L::kStages) & 1);
             if (!TC && sl == 0) __syncthreads();  // the gates
             const uint32_t s = base + (step % L::kStages) * L::kSlice;
-            // <S0, dS1>: both lie in the same order
+            // <S0, dS1> by the warps without dV to write: both lie in the same order
+            if (wc == 0)
 #pragma unroll
-            for (int i = tid * 16; i < L::kSl / 16 * L::kState; i += kLocalThreads * 16) {
-                const char *at = smem + (s - base) + i / L::kState * L::kBlock + i % L::kState;
-                float x[8], y[8];
-                sum_planes<NS>(at + L::S, L::kPl, x);
-                sum_planes<NS>(at + L::dS, L::kPl, y);
+                for (int i = 0; i < L::kSl / 16 * L::kState; i += 128 * 16) {
+                    const char *at = smem + (s - base) + i / L::kState * L::kBlock + i % L::kState + tid * 16;
+                    float x[8], y[8];
+                    sum_planes<NS>(at + L::S, L::kPl, x);
+                    sum_planes<NS>(at + L::dS, L::kPl, y);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], y[e], ss);
-            }
+                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], y[e], ss);
+                }
 #pragma unroll
             for (int kx = 0; kx < L::kSl / 16; ++kx) {  // 16 value channels
                 const int vx = TC ? sl & 1 : kx;         // of the 32 that dO and V are copied by
@@ -660,13 +667,12 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                     r_m[wc * C + wr * 16 + gr + 8 * h] = b;
                 }
             }
-            float d = ss;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-            if (lane == 0) r_ss[warp] = d;
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (wc == 0 && lane == 0) r_ss[wr] = ss;
         }
         meet(2);
-        if (!TC && warp == 0) decay_gradients(head, gate);
+        if (!TC && warp == 0) decay_gradients(hh, gate);
         // With tcgen05 the next head's slices come first: their buffers are waited for.
         if (!TC || hh + 1 == group) add_pairs();
         if constexpr (!TC) {
