@@ -75,9 +75,9 @@ struct LocalSmem {
     // while the head three before is still being finished
     static constexpr int kGates = TC ? 4 : 1;
     static constexpr int Gate = Pair + 2 * C * C * 4 + (TC ? 2 * NI * kTile : 0), Red = Gate + kGates * kGateFloats * 4;
-    // Red: [kCols][64] row sums of q.x, k.x, k.x, F k.k, M over the column parts; [64] E.V;
+    // Red: [kCols][64] row sums of q.x, k.x, k.x, F k.k, M and E.V over the column parts;
     // [4][64] column sums of M over the row blocks; the warps' parts of <S0, dS1>
-    static constexpr int kRed = 5 * kCols * C + C + 4 * C + 4;
+    static constexpr int kRed = 6 * kCols * C + 4 * C + kLocalThreads / 32;
     static constexpr int Bars = (Red + kRed * 4 + 7) / 8 * 8;
     // a slice buffer full [kStages], K and Q full; with tcgen05 also a slice buffer read
     // [kStages], a head's sums complete, read, and one to drain by; then the tensor memory's address
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
     float *gate = reinterpret_cast<float *>(smem + L::Gate);  // TC: head hh's at hh % kGates
     float *red = reinterpret_cast<float *>(smem + L::Red);
     float *r_qx = red, *r_kx = r_qx + kCols * C, *r_ku = r_kx + kCols * C, *r_fk = r_ku + kCols * C;
-    float *r_m = r_fk + kCols * C, *r_ev = r_m + kCols * C, *c_m = r_ev + C, *r_ss = c_m + 4 * C;
+    float *r_m = r_fk + kCols * C, *r_ev = r_m + kCols * C, *c_m = r_ev + kCols * C, *r_ss = c_m + 4 * C;
 
     auto meet = [&](int id) {  // of the warps that compute and the one that sums dg
         if constexpr (TC) ptx::named_sync(id, kLocalThreads + 32);
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
         const float *gam = gate, *del = gate + C, *bet = gate + 2 * C;
         float whole = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) whole += r_ss[i];
+        for (int i = 0; i < kLocalThreads / 32; ++i) whole += r_ss[i];
         whole *= gate[3 * C];
         Two a[2], b[2];
 #pragma unroll
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
             const int r = 2 * lane + i;
             const float kx = parts(r_kx, r);
             if (r < ch.len)
-                p.dbeta[(ch.t0 + r) * p.n_heads + head] = r_ev[r] - gam[r] * kx - parts(r_fk, r);
+                p.dbeta[(ch.t0 + r) * p.n_heads + head] = parts(r_ev, r) - gam[r] * kx - parts(r_fk, r);
             const float cols = (c_m[r] + c_m[C + r]) + (c_m[2 * C + r] + c_m[3 * C + r]);
             a[i] = add({gam[r] * (scale * parts(r_qx, r) - bet[r] * kx), 0.f}, add({parts(r_m, r), 0.f}, {-cols, 0.f}));
             b[i] = {del[r] * parts(r_ku, r), 0.f};
@@ -469,11 +469,12 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
             ok &= wait_bar(bar(step % L::kStages), (step / L::kStages) & 1);
             if (!TC && sl == 0) __syncthreads();  // the gates
             const uint32_t s = base + (step % L::kStages) * L::kSlice;
-            // <S0, dS1> by the warps without dV to write: both lie in the same order
-            if (wc == 0)
+            // with tcgen05 the column parts take turns, a slice each; else the first sums, the second writes dV
+            const bool sums = wc == (TC ? sl & 1 : 0), writes = wc == (TC ? sl & 1 : 1);
+            if (sums)  // <S0, dS1>: both lie in the same order
 #pragma unroll
                 for (int i = 0; i < L::kSl / 16 * L::kState; i += 128 * 16) {
-                    const char *at = smem + (s - base) + i / L::kState * L::kBlock + i % L::kState + tid * 16;
+                    const char *at = smem + (s - base) + i / L::kState * L::kBlock + i % L::kState + (tid & 127) * 16;
                     float x[8], y[8];
                     sum_planes<NS>(at + L::S, L::kPl, x);
                     sum_planes<NS>(at + L::dS, L::kPl, y);
@@ -483,10 +484,11 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
 #pragma unroll
             for (int kx = 0; kx < L::kSl / 16; ++kx) {  // 16 value channels
                 const int vx = TC ? sl & 1 : kx;         // of the 32 that dO and V are copied by
+                if (TC && !sums) break;
                 uint32_t ae[NS][4];
 #pragma unroll
                 for (int q = 0; q < NS; ++q) frag_a_t<128>(s + kx * L::kBlock + L::E + q * L::kPl, 0, wr * 16, ae[q]);
-                if (wc == 0) {  // E_r.V_r
+                if (sums) {  // E_r.V_r
                     uint32_t av[4];
                     if constexpr (NI == 1) frag_a<64>((TC ? base + L::Vals + ((step >> 1) % 3) * L::kVals : s) + L::V, wr * 16, vx * 16, av);
 #pragma unroll
@@ -505,7 +507,8 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                         }
                         ev[i & 1] = fmaf(x0, z0, fmaf(x1, z1, ev[i & 1]));
                     }
-                } else if (wc == 1) {  // dV = beta E
+                }
+                if (writes) {  // dV = beta E
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float x0 = 0.f, x1 = 0.f;
@@ -607,7 +610,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                     r_qx[wc * C + r] = a;
                     r_kx[wc * C + r] = b;
                     r_ku[wc * C + r] = d;
-                    if (wc == 0) r_ev[r] = e;
+                    r_ev[wc * C + r] = e;
                 }
             }
         }
@@ -669,7 +672,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (wc == 0 && lane == 0) r_ss[wr] = ss;
+            if (lane == 0) r_ss[warp] = ss;
         }
         meet(2);
         if (!TC && warp == 0) decay_gradients(hh, gate);
