@@ -49,19 +49,22 @@ __device__ __forceinline__ float exp2_of(float hi, float lo) {
 // ---- the inverse of I + A, a head at a time by two warps, in place over A (fp32, rows kARow
 // apart; strictly lower entries valid). 16 x 16 diagonal blocks by forward substitution, a
 // column per thread; then [[X0, 0], [-X1 A10 X0, X1]] for pairs of 16-blocks and for the pair
-// of 32-blocks, products of three bf16 planes (2^-24). M^T = X0^T A10^T is formed first: its
+// of 32-blocks, products of as many bf16 planes as X is kept in. M^T = X0^T A10^T is formed first: its
 // accumulators are the B operand of X1 M, so M stays in registers.
-__device__ __forceinline__ void split_pair(float x, float y, uint32_t (*w)[4], int i) {
-    uint32_t s[3];
-    split2<3>(x, y, s);
-    w[0][i] = s[0]; w[1][i] = s[1]; w[2][i] = s[2];
+template <int NS, int R>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t (*w)[R], int i) {
+    uint32_t s[NS];
+    split2<NS>(x, y, s);
+#pragma unroll
+    for (int q = 0; q < NS; ++q) w[q][i] = s[q];
 }
-// D (16 x 8) += A B over planes i + j < 3
-__device__ __forceinline__ void mma3(float *d, const uint32_t (*a)[4], const uint32_t (*b)[2]) {
+// D (16 x 8) += A B over planes i + j < NS
+template <int NS>
+__device__ __forceinline__ void mma_planes(float *d, const uint32_t (*a)[4], const uint32_t (*b)[2]) {
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < NS; ++i)
 #pragma unroll
-        for (int j = 0; i + j < 3; ++j) ptx::mma16816(d, a[i], b[j][0], b[j][1]);
+        for (int j = 0; i + j < NS; ++j) ptx::mma16816(d, a[i], b[j][0], b[j][1]);
 }
 __device__ __forceinline__ void diagonal_column(float *A, int b, int c, bool on) {
     const float *D = A + (16 * b) * kARow + 16 * b;
@@ -84,7 +87,7 @@ __device__ __forceinline__ void diagonal_column(float *A, int b, int c, bool on)
 }
 // X block of size N at rows r0, columns c0 (its diagonal blocks at c0 and r0 done), columns
 // n0 .. n0 + 15 of it; reads A10 first, writes after the barrier
-template <int N>
+template <int N, int NS>
 __device__ __forceinline__ void join_blocks(float *A, int r0, int c0, int n0, bool on) {
     const int lane = threadIdx.x & 31, gr = lane >> 2, tq = lane & 3;
     float x[N / 16][2][4];
@@ -96,23 +99,21 @@ __device__ __forceinline__ void join_blocks(float *A, int r0, int c0, int n0, bo
             for (int j = 0; j < 4; ++j) m[i][j] = 0.f;
 #pragma unroll
         for (int k = 0; k < N; k += 16) {
-            uint32_t a[3][4];
+            uint32_t a[NS][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // X0^T[n][k] = X0[k][n]
                 const int n = n0 + gr + (i & 1) * 8, kk = k + tq * 2 + (i >> 1) * 8;
-                split_pair(A[(c0 + kk) * kARow + c0 + n], A[(c0 + kk + 1) * kARow + c0 + n], a, i);
+                split_pair<NS>(A[(c0 + kk) * kARow + c0 + n], A[(c0 + kk + 1) * kARow + c0 + n], a, i);
             }
 #pragma unroll
             for (int t = 0; t < N / 8; ++t) {
-                uint32_t b[3][2];
+                uint32_t b[NS][2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {  // A10[row][k]
                     const float2 v = *reinterpret_cast<const float2 *>(A + (r0 + t * 8 + gr) * kARow + c0 + k + tq * 2 + i * 8);
-                    uint32_t s[3];
-                    split2<3>(v.x, v.y, s);
-                    b[0][i] = s[0]; b[1][i] = s[1]; b[2][i] = s[2];
+                    split_pair<NS>(v.x, v.y, b, i);
                 }
-                mma3(m[t], a, b);
+                mma_planes<NS>(m[t], a, b);
             }
         }
 #pragma unroll
@@ -121,26 +122,24 @@ __device__ __forceinline__ void join_blocks(float *A, int r0, int c0, int n0, bo
             for (int j = 0; j < 4; ++j) x[i][0][j] = x[i][1][j] = 0.f;
 #pragma unroll
         for (int k = 0; k < N; k += 16) {
-            uint32_t b0[3][2], b1[3][2], s[3];
+            uint32_t b0[NS][2], b1[NS][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float *t = m[k / 8 + i];
-                split2<3>(t[0], t[1], s);
-                b0[0][i] = s[0]; b0[1][i] = s[1]; b0[2][i] = s[2];
-                split2<3>(t[2], t[3], s);
-                b1[0][i] = s[0]; b1[1][i] = s[1]; b1[2][i] = s[2];
+                split_pair<NS>(t[0], t[1], b0, i);
+                split_pair<NS>(t[2], t[3], b1, i);
             }
 #pragma unroll
             for (int mt = k / 16; mt < N / 16; ++mt) {  // X1 is lower triangular
-                uint32_t a[3][4];
+                uint32_t a[NS][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 v = *reinterpret_cast<const float2 *>(A + (r0 + mt * 16 + gr + (i & 1) * 8) * kARow +
                                                                        r0 + k + tq * 2 + (i >> 1) * 8);
-                    split_pair(v.x, v.y, a, i);
+                    split_pair<NS>(v.x, v.y, a, i);
                 }
-                mma3(x[mt][0], a, b0);
-                mma3(x[mt][1], a, b1);
+                mma_planes<NS>(x[mt][0], a, b0);
+                mma_planes<NS>(x[mt][1], a, b1);
             }
         }
     }
@@ -362,8 +361,8 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 3 : 1)
             float *X = A + (on ? hh : 0) * C * kARow;
             diagonal_column(X, t >> 4, t & 15, on);
             __syncthreads();
-            join_blocks<16>(X, 32 * w + 16, 32 * w, 0, on);
-            join_blocks<32>(X, 32, 0, 16 * w, on);
+            join_blocks<16, NS>(X, 32 * w + 16, 32 * w, 0, on);
+            join_blocks<32, NS>(X, 32, 0, 16 * w, on);
         }
         for (int i = tid; i < nh * 320; i += kTermThreads) {  // X out, split into planes on the way
             const int hh = i / 320, k = i % 320, b = k >> 5, r = (k >> 1) & 15, c = (k & 1) * 8;
