@@ -73,7 +73,7 @@ def _done(lib, status):
 
 
 def _bytes(need, like):
-    """A workspace; None where none is needed."""
+    """A workspace of ``need`` bytes on the device of ``like``."""
     return torch.empty(need, dtype=torch.uint8, device=like.device)
 
 

@@ -739,8 +739,8 @@ cudaError_t backward(const GdrArgs &p, cudaStream_t stream) {
 // where few independent sums make up the norm it was seen at 2e-5. Problems below 1024 (chunk,
 // head) pairs, whose time is latency and not products, take three planes (3e-7); 16K tokens
 // of 32 heads take 2.3 ms with two planes.
-int planes(int64_t n_tok, int32_t n_seq, int32_t n_heads, bool bf16) {
-    return bf16 && n_slots(n_tok, n_seq) * n_heads >= 1024 ? 2 : 3;
+int planes(int64_t n_tok, int32_t n_heads, bool bf16) {
+    return bf16 && n_tok * n_heads >= 65536 ? 2 : 3;
 }
 
 }  // namespace
@@ -748,7 +748,7 @@ int planes(int64_t n_tok, int32_t n_seq, int32_t n_heads, bool bf16) {
 
 size_t gdr_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k,
                                int32_t d_v, bool bf16) {
-    const int ns = gdr::planes(n_tok, n_seq, n_heads, bf16), dkp = d_k <= 64 ? 64 : 128;
+    const int ns = gdr::planes(n_tok, n_heads, bf16), dkp = d_k <= 64 ? 64 : 128;
     return gdr::scan_offset(n_tok, n_seq, n_heads, ns) +
            (size_t)gdr::n_slots(n_tok, n_seq) * (n_heads * gdr::scan_bytes(ns, dkp, d_v) +
                                                  gdr::Images::record(bf16 ? 1 : 3, dkp, d_v, n_k_heads, n_heads, 2));
@@ -757,7 +757,7 @@ size_t gdr_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, in
 cudaError_t launch_gdr_bwd(const GdrArgs &p, cudaStream_t stream) {
     using bf16 = __nv_bfloat16;
     if (!p.bf16) return p.d_k <= 64 ? gdr::backward<float, 64, 3>(p, stream) : gdr::backward<float, 128, 3>(p, stream);
-    if (gdr::planes(p.n_tok, p.n_seq, p.n_heads, true) == 3)
+    if (gdr::planes(p.n_tok, p.n_heads, true) == 3)
         return p.d_k <= 64 ? gdr::backward<bf16, 64, 3>(p, stream) : gdr::backward<bf16, 128, 3>(p, stream);
     return p.d_k <= 64 ? gdr::backward<bf16, 64, 2>(p, stream) : gdr::backward<bf16, 128, 2>(p, stream);
 }

@@ -110,8 +110,51 @@ def test_without_states(dtype):
 
 
 def test_many_chunks_take_the_two_plane_backward():
-    """At 1024 (chunk, head) pairs and more the bf16 backward carries two planes."""
+    """At 65536 (token, head) pairs and more the bf16 backward carries two planes."""
     check_backward(Inputs([700, 333], 16, 64, 32, 32, BF, seed=5))
+
+
+def wide(hv):
+    """Sequences of 65536 (token, head) pairs and a few: from there the bf16 backward carries two
+    planes. Too many for the host's recurrence: the same one runs on the device, in fp64."""
+    n = 65536 // hv + 5
+    return [n - 131, 0, 1, 130]
+
+
+def check_wide(x):
+    got = kda.gdr_chunk_bwd(*x.args, x.dout, x.dhf)
+    torch.cuda.synchronize()
+    assert kda.read_device_flags() == 0
+    assert_finite(*got)
+    f64 = [t.double() for t in (x.q, x.k, x.v, x.g, x.beta, x.h0)]
+    want = block.gdr_grads(*f64, x.cu_host, x.dout.double(), x.dhf.double())
+    for name, a, ref in zip(("dq", "dk", "dv", "dg", "dbeta", "dh0"), got, want):
+        e = float((a.double() - ref).norm() / ref.norm())
+        assert e <= bar(a, x.dtype), f"{name}: {e:.2e}"
+
+
+@pytest.mark.parametrize("hk,hv,dk,dv", [(64, 128, 128, 128), (128, 128, 128, 72), (16, 96, 100, 40), (64, 192, 72, 8),
+                                         (64, 128, 64, 128), (8, 128, 16, 24), (48, 96, 33, 31), (16, 288, 128, 16)])
+def test_two_plane_backward(hk, hv, dk, dv):
+    """One to eighteen value heads a key head, one to eight slices of value channels, padded
+    channels, rows that a tensor copy cannot fetch."""
+    check_wide(Inputs(wide(hv), hk, hv, dk, dv, BF, seed=dk + dv))
+
+
+def test_two_plane_backward_with_resets_and_slices():
+    x = Inputs(wide(128), 32, 128, 128, 64, BF, seed=6)
+    x.g[:, 0] = 0.0
+    for t in (0, 63, 64, 100, 383, 385, 387, 450):
+        x.g[t, 2] = -float("inf")
+    x.beta[10:20] = 0.0
+    check_wide(x)
+    ref = kda.gdr_chunk_bwd(*x.args, x.dout, x.dhf)
+    assert float(ref[3][x.g == -float("inf")].abs().max()) == 0.0
+    for _ in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(kda.gdr_chunk_bwd(*x.args, x.dout, x.dhf), ref))
+    for q, k, v in slices(x):
+        grads = kda.gdr_chunk_bwd(q, k, v, x.g, x.beta, x.h0, x.cu, x.dout, x.dhf)
+        assert all(torch.equal(a, b) for a, b in zip(grads, ref))
 
 
 @pytest.mark.parametrize("dtype", [FP, BF])
