@@ -16,8 +16,12 @@
 // Q, handed to the state warps ahead of their use. With four pairs (the backward pass, when
 // there are more chains than SMs) the state warps do that themselves: a step is longer but
 // covers twice the channels, and each scheduler has two state warps to choose from.
-// Per chunk a state warp issues about 170 mma.sync m16n8k16 (bf16, d_k = 128) of 8 cycles each:
-// 0.7 us bound a step from below; the rest is the latency of the hand-offs.
+// Per chunk a state warp issues 158 mma.sync m16n8k16 (bf16, d_k = 128, forward) of 8 cycles each
+// on its scheduler's tensor pipe, and the helper beside it another 72: 1850 cycles bound a step
+// from below. It takes 3400 (64K tokens, 32 heads: 1024 steps in 1.83 ms); the rest is the
+// latency of dependent products (20 cycles each) and of four hand-overs. Measured and dropped:
+// loops over the state's tiles that are not unrolled (3.0 ms), Y begun with the pair's own half
+// before the barrier (1.92 ms).
 #pragma once
 
 #include <cuda.h>
@@ -165,13 +169,16 @@ struct ChainMaps {
 inline unsigned chain_blocks(const GdrArgs &p, int pairs) {
     return (unsigned)((p.d_v + 16 * pairs - 1) / (16 * pairs)) * p.n_heads * p.n_seq;
 }
-// Pairs of the backward pass's chains. At 512 CTAs of two pairs (two sequences of 8K tokens, 32
-// heads, forward and reverse) a step takes 3500 (forward) and 4600 cycles (reverse), 1.12 ms in
-// all; as 256 CTAs of four pairs 4450 and 7800 cycles, 0.87 ms. The forward pass itself gains
-// nothing from four (the output would lengthen its step to over 6500 cycles).
+// Pairs of the backward pass's chains (d_k = d_v = 128). Two pairs end a step sooner (3500 cycles
+// forward, 4600 in reverse, against 4450 and 7800), four cover twice the channels: worth it
+// once the CTAs of two pairs are more than one and a half waves. With 128 CTAs of two pairs
+// (4K tokens, 16 heads) the backward pass takes 256 us with two and 372 with four, with 192
+// (24 heads) 402 and 412, with 256 (2K tokens, 32 heads) 248 and 243, with 512 (two sequences of
+// 8K tokens, 32 heads) 1696 and 1489. The forward pass gains nothing from four: the output would
+// lengthen its step to over 6500 cycles.
 inline int scan_pairs(const GdrArgs &p) {
     constexpr unsigned kSMs = 152;
-    return p.d_v > 32 && 2 * chain_blocks(p, 2) > kSMs ? 4 : 2;
+    return p.d_v > 32 && 2 * chain_blocks(p, 2) > kSMs + kSMs / 2 ? 4 : 2;
 }
 
 // The sequence of the given rank, longest first (ties by index): the longest chains start

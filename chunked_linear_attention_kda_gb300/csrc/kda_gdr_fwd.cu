@@ -10,14 +10,18 @@
 // Unlike the per-channel decay, the scalar one leaves K and Q as they are and only scales
 // rows, columns and pairs: no exponent above zero is formed, the decay is unbounded below.
 //
-// Two kernels. gdr_terms: X, P and the gates of every chunk, all chunks side by side.
-// gdr_chain: the chunks of a sequence in order. A warp owns 16 value channels and keeps
-// their state transposed (16 x d_k, fp32) in registers for the whole sequence. An fp32
-// accumulator tile of mma.sync lies in registers as the A operand (and as the B operand of
-// the transposed product) of the next one, so S^T -> Y^T -> Z^T -> U^T -> S^T never leaves
-// the warp: no barrier and no shared-memory round trip sits on the serial path, which is
-// what bounds this kernel (a tcgen05 form pays commit, tensor-memory read, convert, store
-// and fence at each of these hand-offs).
+// Two kernels. gdr_terms: X, P and the gates of every chunk, all chunks side by side. gdr_chain:
+// the chunks of a sequence in order. A pair of warps owns 16 value channels and keeps their
+// state transposed (16 x d_k) in registers for the whole sequence, each warp one half of d_k in
+// fp32 and both all of it as bf16 planes. An fp32 accumulator tile of mma.sync lies in registers
+// as the A operand (and as the B operand of the transposed product) of the next one, so
+// S^T -> Y^T -> Z^T -> U^T -> S^T passes through shared memory only where the two warps trade
+// halves. That serial path is what bounds the pass: a tcgen05 form pays commit, tensor-memory
+// read, convert, store and fence at each of its hand-offs, and a chunk has four.
+//
+// bf16, d_k = d_v = 128: 64K tokens of 16 key and 32 value heads in one sequence take 2.26 ms, 0.4
+// of it the terms and 1.83 the chains (1024 steps of 64 tokens); 20K tokens of 16 value heads in
+// 12 sequences 0.38 ms. Both are far from the bytes they move (0.24 and 0.05 ms).
 #include <cmath>
 
 #include "kda_gdr_chain.h"

@@ -110,13 +110,13 @@ def test_without_states(dtype):
 
 
 def test_many_chunks_take_the_two_plane_backward():
-    """At 65536 (token, head) pairs and more the bf16 backward carries two planes."""
+    """A bf16 backward of many (token, head) pairs carries two planes."""
     check_backward(Inputs([700, 333], 16, 64, 32, 32, BF, seed=5))
 
 
 def wide(hv):
-    """Sequences of 65536 (token, head) pairs and a few: from there the bf16 backward carries two
-    planes. Too many for the host's recurrence: the same one runs on the device, in fp64."""
+    """Sequences of 65536 (token, head) pairs and a few, where the bf16 backward carries two planes.
+    Too many for the host's recurrence: the same one runs on the device, in fp64."""
     n = 65536 // hv + 5
     return [n - 131, 0, 1, 130]
 
