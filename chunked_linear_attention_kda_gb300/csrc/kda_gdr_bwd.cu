@@ -53,9 +53,9 @@ struct LocalSmem {
     static constexpr bool TC = kTensor<T, NS>;
     static constexpr int NI = InputPlanes<T>::N;
     static constexpr int kThreads = kLocalThreads + (TC ? 96 : 0);  // a warp issues products, one loads, one sums dg
-    // Slices of the value channels: 16 and four buffers with tcgen05 (with 32 and two the copies
-    // waited for each other: 767 us against 16K tokens of 32 heads' KEEP), else 32 and one or two.
-    static constexpr int kSl = TC ? 16 : 32, kStages = TC ? 4 : 1;
+    // Slices of the value channels. With tcgen05 16 channels and six buffers: a copy takes 2500
+    // cycles to arrive and its buffer is read for 2000, the products of a slice take 750.
+    static constexpr int kSl = TC ? 16 : 32, kStages = TC ? 6 : 1;
     static constexpr int kPlane = C * DKP * 2;
     static constexpr int kIn = C * 32 * 2;  // a plane of 32 channels of dO or V
     // a block of 16 value channels as the chains left it: planes of S and U, planes of dS and E
@@ -68,16 +68,17 @@ struct LocalSmem {
     static constexpr int Vals = kStages * kSlice, kVals = TC ? 2 * kIn : 0;
     static constexpr int kTile = C * C * 2;  // bytes of a plane of B and F
     static constexpr int K = Vals + 3 * kVals, Q = K + NI * kPlane, Pair = Q + NI * kPlane;
-    // B and F: without tcgen05 over the first slice buffer, once the slices are done
-    static constexpr int B = TC ? Pair + 2 * C * C * 4 : 0, F = B + NI * kTile;
+    // q.k and k.k: with tcgen05 in tensor memory. B and F: without it over the first slice buffer,
+    // once the slices are done.
+    static constexpr int B = TC ? Pair : 0, F = B + NI * kTile;
     static_assert(TC || 2 * NI * kTile <= kSlice, "B and F fit a slice buffer");
     // a head's gates are loaded with its first slice, four slices ahead: with two slices a head
-    // while the head three before is still being finished
+    // the sums of the head three before may still be read
     static constexpr int kGates = TC ? 4 : 1;
-    static constexpr int Gate = Pair + 2 * C * C * 4 + (TC ? 2 * NI * kTile : 0), Red = Gate + kGates * kGateFloats * 4;
-    // Red: [kCols][64] row sums of q.x, k.x, k.x, F k.k, M and E.V over the column parts;
+    static constexpr int Gate = Pair + (TC ? 2 * NI * kTile : 2 * C * C * 4), Red = Gate + kGates * kGateFloats * 4;
+    // Red: [kCols][64] row sums of q.x, k.x, k.x, E.V - F k.k and M over the column parts;
     // [4][64] column sums of M over the row blocks; the warps' parts of <S0, dS1>
-    static constexpr int kRed = 6 * kCols * C + 4 * C + kLocalThreads / 32;
+    static constexpr int kRed = 5 * kCols * C + 4 * C + kLocalThreads / 32;
     static constexpr int Bars = (Red + kRed * 4 + 7) / 8 * 8;
     // a slice buffer full [kStages], K and Q full; with tcgen05 also a slice buffer read
     // [kStages], a head's sums complete, read, and one to drain by; then the tensor memory's address
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
     // columns of tensor memory: dO [S0 U]^T from 0, E [S0 U]^T, U dS1^T (64 tokens use 16 lanes of
     // each warp's 32)
     [[maybe_unused]] constexpr int kOu = DKP, kXk = DKP + C, kEu = kXk + DKP, kXu = 2 * kXk;
+    [[maybe_unused]] constexpr uint32_t kPairs = 16u << 16;  // k.k, then q.k, in the other 16 lanes
     constexpr int KC = DKP / kCols, NH = KC / 16;  // a warp's key channels, in steps of 16
     constexpr int PC = C / kCols, NP = PC / 16;              // its columns of the 64 x 64 products
     extern __shared__ __align__(1024) char smem_raw[];
@@ -140,11 +142,11 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
     const int kh = blockIdx.y, group = p.n_heads / p.n_k_heads;
     const int n_sl = pad_v(p.d_v) / L::kSl;
     const char *ws = static_cast<const char *>(p.workspace);
-    float *pair = reinterpret_cast<float *>(smem + L::Pair);
+    [[maybe_unused]] float *pair = reinterpret_cast<float *>(smem + L::Pair);
     float *gate = reinterpret_cast<float *>(smem + L::Gate);  // TC: head hh's at hh % kGates
     float *red = reinterpret_cast<float *>(smem + L::Red);
-    float *r_qx = red, *r_kx = r_qx + kCols * C, *r_ku = r_kx + kCols * C, *r_fk = r_ku + kCols * C;
-    float *r_m = r_fk + kCols * C, *r_ev = r_m + kCols * C, *c_m = r_ev + kCols * C, *r_ss = c_m + 4 * C;
+    float *r_qx = red, *r_kx = r_qx + kCols * C, *r_ku = r_kx + kCols * C, *r_ef = r_ku + kCols * C;
+    float *r_m = r_ef + kCols * C, *c_m = r_m + kCols * C, *r_ss = c_m + 4 * C;
 
     auto meet = [&](int id) {  // of the warps that compute and the one that sums dg
         if constexpr (TC) ptx::named_sync(id, kLocalThreads + 32);
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
             const int r = 2 * lane + i;
             const float kx = parts(r_kx, r);
             if (r < ch.len)
-                p.dbeta[(ch.t0 + r) * p.n_heads + head] = parts(r_ev, r) - gam[r] * kx - parts(r_fk, r);
+                p.dbeta[(ch.t0 + r) * p.n_heads + head] = parts(r_ef, r) - gam[r] * kx;
             const float cols = (c_m[r] + c_m[C + r]) + (c_m[2 * C + r] + c_m[3 * C + r]);
             a[i] = add({gam[r] * (scale * parts(r_qx, r) - bet[r] * kx), 0.f}, add({parts(r_m, r), 0.f}, {-cols, 0.f}));
             b[i] = {del[r] * parts(r_ku, r), 0.f};
@@ -285,7 +287,10 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                         sl = 0;
                         ++hh;
                     }
-                    if (step >= L::kStages) ok = wait_bar(used(step % L::kStages), (step / L::kStages - 1) & 1);
+                    // dO and V need the slice five before to be read, the gates the one four before
+                    const int last = step - (sl == 0 ? 4 : sl & 1 ? 6 : 5);
+                    if (step == 2) ok = wait_bar(bar(L::kStages), 0);  // K and Q first: they are waited for
+                    if (step >= L::kStages) ok = wait_bar(used(last % L::kStages), (last / L::kStages) & 1);
                     if (!ok) break;
                     load(step, hh, sl);
                 }
@@ -399,13 +404,19 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                     }
             }
         }
+        if constexpr (TC) {
+            ptx::tmem_st_frag4(lanes + kPairs + wc * PC, reinterpret_cast<const uint32_t *>(kk[0]));
+            ptx::tmem_st_frag4(lanes + kPairs + C + wc * PC, reinterpret_cast<const uint32_t *>(qk[0]));
+            ptx::tmem_st_wait();
+        } else {
 #pragma unroll
-        for (int n = 0; n < 2 * NP; ++n)
+            for (int n = 0; n < 2 * NP; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                pair[(n * 4 + i) * kLocalThreads + tid] = kk[n][i];
-                pair[(8 * NP + n * 4 + i) * kLocalThreads + tid] = qk[n][i];
-            }
+                for (int i = 0; i < 4; ++i) {
+                    pair[(n * 4 + i) * kLocalThreads + tid] = kk[n][i];
+                    pair[(8 * NP + n * 4 + i) * kLocalThreads + tid] = qk[n][i];
+                }
+        }
     }
 
     float dq[2 * NH][4], dk[2 * NH][4];  // this warp's rows and key channels
@@ -605,15 +616,15 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = wr * 16 + gr + 8 * h;
-                const float a = quad_sum(qx[h]), b = quad_sum(kx_[h]), d = quad_sum(ku[h]), e = quad_sum(ev[h]);
+                const float a = quad_sum(qx[h]), b = quad_sum(kx_[h]), d = quad_sum(ku[h]);
                 if (tq == 0) {
                     r_qx[wc * C + r] = a;
                     r_kx[wc * C + r] = b;
                     r_ku[wc * C + r] = d;
-                    r_ev[wc * C + r] = e;
                 }
             }
         }
+        float kp[2 * NP][4], qp[2 * NP][4];  // k.k and q.k
         // B (lower) and -beta F (below the diagonal) as operands; row and column sums
         if constexpr (TC) {
             ptx::tmem_ld_frag4(lanes + kOu + wc * PC, reinterpret_cast<uint32_t *>(ou[0]));
@@ -621,6 +632,9 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
             ptx::tmem_ld_wait();
             ptx::tc_fence_before();
             warp_arrive(sums_read);
+            ptx::tmem_ld_frag4(lanes + kPairs + wc * PC, reinterpret_cast<uint32_t *>(kp[0]));
+            ptx::tmem_ld_frag4(lanes + kPairs + C + wc * PC, reinterpret_cast<uint32_t *>(qp[0]));
+            ptx::tmem_ld_wait();
         }
         {
             float fk[2] = {0.f, 0.f}, mr[2] = {0.f, 0.f};
@@ -634,8 +648,8 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                     float bv[2], fv[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float kk = pair[(n * 4 + 2 * h + i) * kLocalThreads + tid];
-                        const float qk = pair[(8 * NP + n * 4 + 2 * h + i) * kLocalThreads + tid];
+                        const float kk = TC ? kp[n][2 * h + i] : pair[(n * 4 + 2 * h + i) * kLocalThreads + tid];
+                        const float qk = TC ? qp[n][2 * h + i] : pair[(8 * NP + n * 4 + 2 * h + i) * kLocalThreads + tid];
                         const float d = (G2[r].x - G2[j + i].x) + (G2[r].y - G2[j + i].y);
                         const float e = j + i <= r ? ex2(d) : 0.f;
                         bv[i] = j + i <= r ? scale * e * ou[n][2 * h + i] : 0.f;
@@ -664,9 +678,9 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float a = quad_sum(fk[h]), b = quad_sum(mr[h]);
+                const float a = quad_sum(ev[h] - fk[h]), b = quad_sum(mr[h]);
                 if (tq == 0) {
-                    r_fk[wc * C + wr * 16 + gr + 8 * h] = a;
+                    r_ef[wc * C + wr * 16 + gr + 8 * h] = a;
                     r_m[wc * C + wr * 16 + gr + 8 * h] = b;
                 }
             }

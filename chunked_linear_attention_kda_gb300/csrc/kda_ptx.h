@@ -250,6 +250,12 @@ __device__ __forceinline__ void tmem_ld_frag4(uint32_t ta, uint32_t *r) {
         "%14,%15}, [%16];"
         : KDA_R8(0), KDA_R8(8) : "r"(ta));
 }
+// the same fragments to tensor memory
+__device__ __forceinline__ void tmem_st_frag4(uint32_t ta, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+        "%13,%14,%15,%16};" ::"r"(ta), KDA_W8(0), KDA_W8(8));
+}
 #undef KDA_R8
 #undef KDA_W8
 __device__ __forceinline__ void tmem_ld_wait() {
