@@ -321,33 +321,33 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                     }
                     ptx::umma_commit(sums_done);
                 }
-                for (int step = 0, hh = 0, sl = 0; ok && step < steps; ++step) {
-                    const int b = step % L::kStages;
-                    ok = wait_bar(bar(b), (step / L::kStages) & 1);
+                // operands of the first buffers; the others' are as many 16-byte units further on
+                const uint64_t dO0 = ptx::sdesc_sw64(base + L::Vals, 512);
+                const uint64_t one0 = ptx::sdesc_sw128(base, 1024, 1024), all0 = ptx::sdesc_sw128(base, 2048, 1024);
+                for (int step = 0, hh = 0, sl = 0, b = 0, vb = 0, phase = 0; ok && step < steps; ++step) {
+                    ok = wait_bar(bar(b), phase);
                     if (ok && sl == 0) ok = wait_bar(sums_read, hh & 1);
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    const uint32_t s = base + b * L::kSlice, more = sl > 0;
-                    const uint64_t dO = ptx::sdesc_sw64(base + L::Vals + ((step >> 1) % 3) * L::kVals + (sl & 1) * 32, 512);
-                    uint64_t E[NS], U[NS], S[NS], dS[NS];
-#pragma unroll
-                    for (int q = 0; q < NS; ++q) {
-                        E[q] = ptx::sdesc_sw128(s + L::E + q * L::kPl, 1024, 1024);
-                        U[q] = ptx::sdesc_sw128(s + L::U + q * L::kPl, 1024, 1024);
-                        S[q] = ptx::sdesc_sw128(s + L::S + q * L::kPl, 2048, 1024);
-                        dS[q] = ptx::sdesc_sw128(s + L::dS + q * L::kPl, 2048, 1024);
-                    }
+                    const uint32_t more = sl > 0;
+                    const uint64_t dO = dO0 + (uint32_t)(vb * L::kVals + (sl & 1) * 32) / 16;
+                    const uint64_t one = one0 + (uint32_t)(b * L::kSlice) / 16, all = all0 + (uint32_t)(b * L::kSlice) / 16;
 #pragma unroll
                     for (int i = 0; i < NS; ++i) {
-                        ptx::umma_ss(tmem, dO, S[i], id_o, more | (i > 0));
+                        ptx::umma_ss(tmem, dO, all + (L::S + i * L::kPl) / 16, id_o, more | (i > 0));
 #pragma unroll
                         for (int j = 0; i + j < NS; ++j) {
                             const uint32_t acc = more | (i + j > 0);
-                            ptx::umma_ss(tmem + kXk, E[i], S[j], id_e, acc);
-                            ptx::umma_ss(tmem + kXu, U[i], dS[j], id_u, acc);
+                            ptx::umma_ss(tmem + kXk, one + (L::E + i * L::kPl) / 16, all + (L::S + j * L::kPl) / 16, id_e, acc);
+                            ptx::umma_ss(tmem + kXu, one + (L::U + i * L::kPl) / 16, all + (L::dS + j * L::kPl) / 16, id_u, acc);
                         }
                     }
                     ptx::umma_commit(used(b));
+                    if (++b == L::kStages) {
+                        b = 0;
+                        phase ^= 1;
+                    }
+                    if (sl & 1) vb = vb == 2 ? 0 : vb + 1;
                     if (++sl == n_sl) {
                         ptx::umma_commit(sums_done);
                         sl = 0;
