@@ -2,12 +2,15 @@
 // kda_gdr_bwd.cu): sizes, workspace layout, operand tiles and warp-level products.
 // Internal; not part of the C ABI.
 //
-// Precision. Every product runs on bf16 mma.sync with fp32 accumulation; an operand that is
-// not a bf16 input is carried as a sum of bf16 planes (hi + lo, or hi + mid + lo), so that
-// the fp32 results (states, gate and beta gradients) keep about 2^-17 of relative error per
-// operand for bf16 inputs and 2^-24 for fp32 inputs. NI = planes of an input tile (1: bf16,
-// 3: fp32), NS = planes of an intermediate (2 or 3); a product of plane i with plane j is
-// formed only where i + j < NS (the rest is below the accumulator's rounding of the sum).
+// Precision. Every product runs on bf16 tensor-core operations with fp32 accumulation (mma.sync;
+// tcgen05 where a chain of dependent products does not wait for it). An operand that is not a
+// bf16 input is carried as a sum of bf16 planes (hi + lo, or hi + mid + lo), so that the fp32
+// results (states, gate and beta gradients) keep about 2^-17 of relative error per operand for
+// bf16 inputs and 2^-24 for fp32 inputs. NI = planes of an input tile (1: bf16, 3: fp32), NS =
+// planes of an intermediate (2 or 3); a product of plane i with plane j is formed only where
+// i + j < NS (the rest is below the accumulator's rounding of the sum). Operands that reach only a
+// result of the inputs' type (S0 and P in O, B and F in dQ and dK) are carried in NI planes: for
+// bf16 one more rounding of the size of the result's own.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -20,6 +20,11 @@
 // other; and the local gradients, all chunks side by side, one CTA per (chunk, key head)
 // that walks over the value heads sharing the key head and adds their dQ and dK in
 // registers (no atomics: the same call gives the same bits).
+//
+// bf16, two sequences of 8K tokens, 16 key and 32 value heads, d_k = d_v = 128: 1.47 ms, of it the
+// terms 0.11, the chains 0.83 (a step is a chain of dependent products, as in the forward; the
+// tensor pipe is active for 52 % of it) and the local gradients 0.52 (2.3 GB at 0.66 of a plain
+// copy's bandwidth).
 #include <cmath>
 
 #include "kda_gdr_chain.h"
@@ -41,6 +46,15 @@ __global__ void __launch_bounds__(kChainThreads)
 }
 
 // ---------------------------------------------------------------- local gradients
+// With tcgen05 a CTA is eight warps that compute, each 16 tokens x one half of the key channels
+// (or of the 64 columns of a pair product), and three that serve them: one thread copies 16 value
+// channels of S0, U, dS1 and E at a time (24 KB, as the chains left them), one thread issues their
+// products into tensor memory, one warp sums dbeta and dg. A 64-row accumulator takes 16 lanes of
+// each warp's 32 and is read as the fragments of mma.sync, so that the pair products B K, B^T Q and
+// F K stay on mma.sync with their operands' scaling in registers; q.k and k.k wait in the other
+// 16 lanes. A head's pair products are added while the next head's slices are multiplied.
+// 16K tokens of 32 heads: 0.52 ms; all on mma.sync 0.95 ms (25 % of issue slots: two warps a
+// scheduler waited for fragments and for each other).
 constexpr int kLocalThreads = 256;          // that compute
 constexpr int kCols = kLocalThreads / 128;  // column parts: a warp has 16 tokens x 1 / kCols of the columns
 // The products with S0, dS1 and U run on tcgen05 where operands have one and two planes; three

@@ -11,6 +11,11 @@
 // registers across the row's reduction, every output written once. The sums over rows go to
 // one partial row per CTA (group), added up in a fixed order by a second kernel: the same
 // call gives the same bits.
+// bf16, of a plain copy's bandwidth: residual norm forward, 32K rows of 4096 or 8192 channels, 1.0
+// and 0.93 (155 and 339 us); its backward pass 0.79 (32K x 4096, 300 us); gated norm forward 0.85
+// (64K tokens x 32 heads x 128, 281 us), backward 0.75 (8191 tokens x 32 x 128, 66 us). The
+// backward passes wait for their rows' two sums and keep half the SMs' threads busy meanwhile:
+// registers for two rows' loads in flight take the rest.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -311,7 +316,8 @@ __global__ void __launch_bounds__(1024)
 
 constexpr int kSMs = 152;
 
-// warps to a row (a power of two) and 8-channel runs to a thread: one run up to 8192 channels
+// Warps to a row (a power of two) and 8-channel runs to a thread: one run up to 8192 channels, so
+// that a row's loads are all in flight at once; beyond, a CTA has no more threads.
 struct RowPlan { int wpr, nv; };
 RowPlan row_plan(int d) {
     int wpr = 1;
