@@ -12,10 +12,9 @@
 // one partial row per CTA (group), added up in a fixed order by a second kernel: the same
 // call gives the same bits.
 // bf16, of a plain copy's bandwidth: residual norm forward, 32K rows of 4096 or 8192 channels, 1.0
-// and 0.93 (155 and 339 us); its backward pass 0.79 (32K x 4096, 300 us); gated norm forward 0.85
-// (64K tokens x 32 heads x 128, 281 us), backward 0.75 (8191 tokens x 32 x 128, 66 us). The
-// backward passes wait for their rows' two sums and keep half the SMs' threads busy meanwhile:
-// registers for two rows' loads in flight take the rest.
+// and 0.93 (155 and 339 us); its backward pass 0.90 (32K x 4096, 262 us); gated norm forward 0.96
+// (64K tokens x 32 heads x 128, 248 us), backward 0.83 (8191 tokens x 32 x 128, 59 us, of them 5 the
+// sum over partial rows; 64K tokens 0.97).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -108,6 +107,12 @@ struct Held {
 #pragma unroll
         for (int i = 0; i < 8 * NV; ++i) x[i] = 0.f;
     }
+    __device__ __forceinline__ void put_run(int run, uint4 a) {
+        x[4 * run] = __uint_as_float(a.x);
+        x[4 * run + 1] = __uint_as_float(a.y);
+        x[4 * run + 2] = __uint_as_float(a.z);
+        x[4 * run + 3] = __uint_as_float(a.w);
+    }
     __device__ __forceinline__ float get(int i) const { return x[i]; }
 };
 template <int NV>
@@ -126,8 +131,36 @@ struct Held<bf16, NV, true> {
 #pragma unroll
         for (int i = 0; i < 4 * NV; ++i) w[i] = 0;
     }
+    __device__ __forceinline__ void put_run(int, uint4 a) { w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w; }
     __device__ __forceinline__ float get(int i) const {
         return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+};
+
+// Rows ahead of their use. A thread copies its 8 channels of N tensors' rows to slots of its own in
+// shared memory and reads them back itself: the next row is in flight, without registers for it
+// and without a barrier, while this one's sums are formed and its results written.
+template <typename T, int N, int THREADS>
+struct Ahead {
+    static constexpr int kRuns = sizeof(T) / 2, kBytes = N * kRuns * THREADS * 16;  // 16-byte runs
+    char *slots;
+    __device__ __forceinline__ explicit Ahead(char *smem) : slots(smem + threadIdx.x * 16) {}
+    __device__ __forceinline__ char *at(int n, int run) const { return slots + (n * kRuns + run) * (THREADS * 16); }
+    // channels 8 t .. of the row at p, zeros from d on
+    __device__ __forceinline__ void fetch(int n, const T *p, int d, int t) const {
+        const bool in = 8 * t < d;
+#pragma unroll
+        for (int run = 0; run < kRuns; ++run)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(at(n, run))),
+                         "l"(in ? p + 8 * t + run * (16 / sizeof(T)) : p), "r"(in ? 16 : 0) : "memory");
+    }
+    __device__ __forceinline__ static void wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+    __device__ __forceinline__ void read(int n, Held<T, 1, true> &h) const {
+#pragma unroll
+        for (int run = 0; run < kRuns; ++run) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(at(n, run));
+            h.put_run(run, a);
+        }
     }
 };
 
@@ -219,19 +252,32 @@ __global__ void __launch_bounds__(Rows<WPR>::kThreads)
 }
 
 // Each group walks over rows first, first + step, ...; its sums of dw (and dscale) go to
-// row `blockIdx.x * kGroups + group` of the partials. All of a row's loads are issued before
-// its reduction: 64 bytes a thread in flight at 2048 threads an SM.
+// row `blockIdx.x * kGroups + group` of the partials. The next row is copied ahead from the moment
+// that this one is in registers (32768 x 4096, bf16: 264 us; without it 302; two rows ahead 285).
 template <typename T, int WPR, int NV, bool VEC, bool SCALE>
 __global__ void __launch_bounds__(Rows<WPR>::kThreads, NV == 1 ? 1024 / Rows<WPR>::kThreads : 1)
     residual_norm_bwd_kernel(const ResidualNormArgs p, int64_t rounds) {
     using L = Rows<WPR>;
     __shared__ float2 buf[2][L::kWarps];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int group = threadIdx.x / L::G, t = threadIdx.x % L::G;
     const int64_t part = (int64_t)blockIdx.x * L::kGroups + group, step = (int64_t)gridDim.x * L::kGroups;
     const float inv_d = 1.f / p.d;
     // weight and scale wait in shared memory (up to 8192 channels, else they are reloaded
     // through the cache): 16 registers fewer, which two CTAs of 512 threads need
     extern __shared__ __align__(16) float params[];
+    constexpr bool AHEAD = VEC && NV == 1;
+    const Ahead<T, SCALE ? 4 : 3, L::kThreads> ahead(reinterpret_cast<char *>(params + (SCALE ? 2 : 1) * p.d));
+    auto fetch = [&](int64_t i) {
+        const int64_t row = part + i * step;
+        if (row < p.n_rows) {
+            ahead.fetch(0, static_cast<const T *>(p.r) + row * p.r_stride, p.d, t);
+            ahead.fetch(1, static_cast<const T *>(p.dy) + row * p.dy_stride, p.d, t);
+            if (p.dr) ahead.fetch(2, static_cast<const T *>(p.dr) + row * p.dr_stride, p.d, t);
+            if constexpr (SCALE) ahead.fetch(3, static_cast<const T *>(p.x) + row * p.x_stride, p.d, t);
+        }
+    };
+    if constexpr (AHEAD) fetch(0);
     const float *weight = p.weight, *scale = p.scale;
     if constexpr (NV == 1) {
         for (int i = threadIdx.x; i < p.d; i += L::kThreads) {
@@ -256,7 +302,15 @@ __global__ void __launch_bounds__(Rows<WPR>::kThreads, NV == 1 ? 1024 / Rows<WPR
         r.clear();
         dy.clear();
         dr.clear();
-        if (live) {
+        if constexpr (AHEAD) {
+            ahead.wait();
+            if (live) {
+                ahead.read(0, r);
+                ahead.read(1, dy);
+                if (p.dr) ahead.read(2, dr);
+                if constexpr (SCALE) ahead.read(3, x);
+            }
+        } else if (live) {
             r.load(static_cast<const T *>(p.r) + row * p.r_stride, p.d, t, L::G);
             dy.load(static_cast<const T *>(p.dy) + row * p.dy_stride, p.d, t, L::G);
             if (p.dr) dr.load(static_cast<const T *>(p.dr) + row * p.dr_stride, p.d, t, L::G);
@@ -271,6 +325,7 @@ __global__ void __launch_bounds__(Rows<WPR>::kThreads, NV == 1 ? 1024 / Rows<WPR
             sum.y = fmaf(w[i] * dy.get(i), r.get(i), sum.y);
         }
         sum = group_sum2<WPR>(sum, buf[i0 & 1], group);
+        if constexpr (AHEAD) fetch(i0 + 1);  // this row is in registers
         if (!live) continue;
         const float c = 1.f / sqrtf(fmaf(sum.x, inv_d, p.eps)), m = sum.y * c * c * inv_d;
         float g[8 * NV];
@@ -300,6 +355,7 @@ __global__ void __launch_bounds__(1024)
     sum_parts_kernel(const float *__restrict__ partial, int parts, int d, float *__restrict__ out0,
                      float *__restrict__ out1) {
     __shared__ float s[32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), l = threadIdx.x >> 5;
     const float *src = partial + (int64_t)blockIdx.y * parts * d;
     float x = 0.f;
@@ -315,6 +371,20 @@ __global__ void __launch_bounds__(1024)
 }
 
 constexpr int kSMs = 152;
+
+// launched while the kernel before it drains: the launch's latency, 2 us of 60, passes meanwhile
+cudaError_t sum_parts(const float *partial, int parts, int d, float *out0, float *out1, cudaStream_t stream) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((d + 31) / 32, out1 ? 2 : 1);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sum_parts_kernel, partial, parts, d, out0, out1);
+}
 
 // Warps to a row (a power of two) and 8-channel runs to a thread: one run up to 8192 channels, so
 // that a row's loads are all in flight at once; beyond, a CTA has no more threads.
@@ -342,14 +412,17 @@ cudaError_t residual_run(const ResidualNormArgs &p, bool bwd, cudaStream_t strea
     }
     const int64_t grid = residual_bwd_grid(p.n_rows, p.d), parts = grid * L::kGroups;
     const int64_t rounds = (p.n_rows + parts - 1) / parts;
-    const int smem = NV == 1 ? p.d * 4 * (p.scale ? 2 : 1) : 0;
+    const int ahead = VEC && NV == 1 ? p.scale ? Ahead<T, 4, L::kThreads>::kBytes
+                                              : Ahead<T, 3, L::kThreads>::kBytes : 0;
+    const int smem = (NV == 1 ? p.d * 4 * (p.scale ? 2 : 1) : 0) + ahead;
     auto kernel = p.scale ? residual_norm_bwd_kernel<T, WPR, NV, VEC, true> : residual_norm_bwd_kernel<T, WPR, NV, VEC, false>;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
     kernel<<<(unsigned)grid, L::kThreads, smem, stream>>>(p, rounds);
-    sum_parts_kernel<<<dim3((p.d + 31) / 32, p.scale ? 2 : 1), 1024, 0, stream>>>(p.partial, (int)parts, p.d, p.dw, p.dscale);
+    const cudaError_t e = sum_parts(p.partial, (int)parts, p.d, p.dw, p.scale ? p.dscale : nullptr, stream);
+    if (e != cudaSuccess) return e;
     count_launches(2);
     return cudaGetLastError();
 }
@@ -398,35 +471,72 @@ __device__ __forceinline__ uint32_t divide(uint32_t row, HeadDiv h) { return (__
 constexpr int kGatedThreads = 256;
 
 // G threads (a power of two up to a warp) hold a row of d <= 8 G channels.
+// A CTA walks over rows with the next one copied ahead; the grid is the CTAs that the SMs hold.
+// 65536 x 32 x 128, bf16: 248 us with five an SM, 262 with four, 276 with six (more requests in
+// flight than HBM orders well), 304 with six of which five are resident; a row a group and no
+// loop 283.
+constexpr int kGatedFwdCtas = 5;
 template <typename T, int G, bool VEC, bool SILU>
-__global__ void __launch_bounds__(kGatedThreads)
+__global__ void __launch_bounds__(kGatedThreads, kGatedFwdCtas)
     gated_norm_fwd_kernel(const GatedNormArgs p, const HeadDiv by) {
     const int t = threadIdx.x % G;
-    const int64_t row = ((int64_t)blockIdx.x * kGatedThreads + threadIdx.x) / G;
-    const bool live = row < p.n_tok * p.n_heads;
-    const uint32_t n = divide((uint32_t)row, by), h = (uint32_t)row - n * p.n_heads;
-    float x[8], z[8], w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    constexpr int kGroups = kGatedThreads / G;
+    const int64_t rows = p.n_tok * p.n_heads, step = (int64_t)gridDim.x * kGroups;
+    extern __shared__ __align__(16) char slots[];
+    const Ahead<T, 2, kGatedThreads> ahead(slots);
+    Held<T, 1, VEC> hx, hz;
+    // channel 0 of the row's head in x and gate
+    auto heads = [&](int64_t row, auto use) {
+        const uint32_t n = divide((uint32_t)row, by);
+        const int64_t h = (int64_t)((uint32_t)row - n * p.n_heads) * p.d;
+        use(static_cast<const T *>(p.x) + n * p.x_stride + h, static_cast<const T *>(p.gate) + n * p.gate_stride + h);
+    };
+    auto fetch = [&](int64_t row) {
+        if (row < rows)
+            heads(row, [&](const T *px, const T *pz) {
+                ahead.fetch(0, px, p.d, t);
+                ahead.fetch(1, pz, p.d, t);
+            });
+    };
+    float w[8];
     load_row<1, VEC>(p.weight, p.d, t, G, w);
-    if (live) {
-        load_row<1, VEC>(static_cast<const T *>(p.x) + n * p.x_stride + (int64_t)h * p.d, p.d, t, G, x);
-        load_row<1, VEC>(static_cast<const T *>(p.gate) + n * p.gate_stride + (int64_t)h * p.d, p.d, t, G, z);
+    int64_t row = (int64_t)blockIdx.x * kGroups + threadIdx.x / G;
+    if constexpr (VEC) fetch(row);
+    for (int64_t first = (int64_t)blockIdx.x * kGroups; first < rows; first += step, row += step) {
+        const bool live = row < rows;
+        hx.clear();
+        hz.clear();
+        if constexpr (VEC) {
+            ahead.wait();
+            if (live) {
+                ahead.read(0, hx);
+                ahead.read(1, hz);
+            }
+        } else if (live) {
+            heads(row, [&](const T *px, const T *pz) {
+                hx.load(px, p.d, t, G);
+                hz.load(pz, p.d, t, G);
+            });
+        }
+        float s = 0.f, x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = hx.get(i);
+            s = fmaf(x[i], x[i], s);
+        }
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if constexpr (VEC) fetch(row + step);  // this row is in registers
+        if (!live) continue;
+        const float c = 1.f / sqrtf(s / p.d + p.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float a, da;
+            act<SILU, sizeof(T) == 2>(hz.get(i), a, da);
+            x[i] = x[i] * c * w[i] * a;
+        }
+        store_row<1, VEC>(static_cast<T *>(p.y) + row * p.d, p.d, t, G, x);
     }
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
-#pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (!live) return;
-    const float c = 1.f / sqrtf(s / p.d + p.eps);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float a, da;
-        act<SILU, sizeof(T) == 2>(z[i], a, da);
-        x[i] = x[i] * c * w[i] * a;
-    }
-    store_row<1, VEC>(static_cast<T *>(p.y) + row * p.d, p.d, t, G, x);
 }
 
 template <typename T, int G, bool VEC, bool SILU>
@@ -434,6 +544,7 @@ __global__ void __launch_bounds__(kGatedThreads, 4)
     gated_norm_bwd_kernel(const GatedNormArgs p, const HeadDiv by, int64_t rounds) {
     constexpr int kGroups = kGatedThreads / G;
     __shared__ float sums[kGatedThreads / 32][8 * G];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int t = threadIdx.x % G;
     const int64_t rows = p.n_tok * p.n_heads, step = (int64_t)gridDim.x * kGroups;
     const float inv_d = 1.f / p.d;
@@ -441,43 +552,71 @@ __global__ void __launch_bounds__(kGatedThreads, 4)
     load_row<1, VEC>(p.weight, p.d, t, G, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[i] = 0.f;
+    extern __shared__ __align__(16) char slots[];
+    const Ahead<T, 3, kGatedThreads> ahead(slots);
+    const int64_t first = (int64_t)blockIdx.x * kGroups + threadIdx.x / G;
+    Held<T, 1, VEC> x, z, dy;
+    // channel 0 of the row's head in x, gate and dy
+    auto heads = [&](int64_t row, auto use) {
+        const uint32_t n = divide((uint32_t)row, by);
+        const int64_t h = (int64_t)((uint32_t)row - n * p.n_heads) * p.d;
+        use(static_cast<const T *>(p.x) + n * p.x_stride + h, static_cast<const T *>(p.gate) + n * p.gate_stride + h,
+            static_cast<const T *>(p.dy) + n * p.dy_stride + h);
+    };
+    auto fetch = [&](int64_t i) {
+        if (i * step + first < rows)
+            heads(i * step + first, [&](const T *px, const T *pz, const T *py) {
+                ahead.fetch(0, px, p.d, t);
+                ahead.fetch(1, pz, p.d, t);
+                ahead.fetch(2, py, p.d, t);
+            });
+    };
+    if constexpr (VEC) fetch(0);
     for (int64_t i0 = 0; i0 < rounds; ++i0) {
-        const int64_t row = i0 * step + (int64_t)blockIdx.x * kGroups + threadIdx.x / G;
+        const int64_t row = i0 * step + first;
         const bool live = row < rows;
-        float x[8], z[8], dy[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = z[i] = dy[i] = 0.f;
-        if (live) {
-            const uint32_t n = divide((uint32_t)row, by);
-            const int64_t h = (int64_t)((uint32_t)row - n * p.n_heads) * p.d;
-            load_row<1, VEC>(static_cast<const T *>(p.x) + n * p.x_stride + h, p.d, t, G, x);
-            load_row<1, VEC>(static_cast<const T *>(p.gate) + n * p.gate_stride + h, p.d, t, G, z);
-            load_row<1, VEC>(static_cast<const T *>(p.dy) + n * p.dy_stride + h, p.d, t, G, dy);
+        x.clear();
+        z.clear();
+        dy.clear();
+        if constexpr (VEC) {
+            ahead.wait();
+            if (live) {
+                ahead.read(0, x);
+                ahead.read(1, z);
+                ahead.read(2, dy);
+            }
+        } else if (live) {
+            heads(row, [&](const T *px, const T *pz, const T *py) {
+                x.load(px, p.d, t, G);
+                z.load(pz, p.d, t, G);
+                dy.load(py, p.d, t, G);
+            });
         }
         float xx = 0.f, tx = 0.f, a[8], da[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            act<SILU, sizeof(T) == 2>(z[i], a[i], da[i]);
-            xx = fmaf(x[i], x[i], xx);
-            tx = fmaf(w[i] * a[i] * dy[i], x[i], tx);
+            act<SILU, sizeof(T) == 2>(z.get(i), a[i], da[i]);
+            xx = fmaf(x.get(i), x.get(i), xx);
+            tx = fmaf(w[i] * a[i] * dy.get(i), x.get(i), tx);
         }
 #pragma unroll
         for (int o = G / 2; o > 0; o >>= 1) {
             xx += __shfl_xor_sync(0xffffffffu, xx, o);
             tx += __shfl_xor_sync(0xffffffffu, tx, o);
         }
+        if constexpr (VEC) fetch(i0 + 1);  // this row is in registers
         if (!live) continue;
         const float c = 1.f / sqrtf(fmaf(xx, inv_d, p.eps)), m = tx * c * c * inv_d;
-        float dx[8];
+        float dx[8], dz[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float n = x[i] * c, wd = w[i] * dy[i];
-            dx[i] = c * (wd * a[i] - x[i] * m);
-            z[i] = wd * n * da[i];
-            dw[i] = fmaf(dy[i] * a[i], n, dw[i]);
+            const float n = x.get(i) * c, wd = w[i] * dy.get(i);
+            dx[i] = c * (wd * a[i] - x.get(i) * m);
+            dz[i] = wd * n * da[i];
+            dw[i] = fmaf(dy.get(i) * a[i], n, dw[i]);
         }
         store_row<1, VEC>(static_cast<T *>(p.dx) + row * p.d, p.d, t, G, dx);
-        store_row<1, VEC>(static_cast<T *>(p.dgate) + row * p.d, p.d, t, G, z);
+        store_row<1, VEC>(static_cast<T *>(p.dgate) + row * p.d, p.d, t, G, dz);
     }
     // the warp's groups, then the CTA's warps, in a fixed order
 #pragma unroll
@@ -511,13 +650,18 @@ cudaError_t gated_run(const GatedNormArgs &p, bool bwd, cudaStream_t stream) {
     constexpr int kGroups = kGatedThreads / G;
     const int64_t rows = p.n_tok * p.n_heads;
     if (!bwd) {
-        gated_norm_fwd_kernel<T, G, VEC, SILU><<<(unsigned)((rows + kGroups - 1) / kGroups), kGatedThreads, 0, stream>>>(p, head_div(p.n_heads));
+        constexpr int smem = VEC ? Ahead<T, 2, kGatedThreads>::kBytes : 0;
+        const int64_t grid = std::min<int64_t>((rows + kGroups - 1) / kGroups, kSMs * kGatedFwdCtas);
+        gated_norm_fwd_kernel<T, G, VEC, SILU><<<(unsigned)grid, kGatedThreads, smem, stream>>>(p, head_div(p.n_heads));
         count_launches(1);
         return cudaGetLastError();
     }
     const int64_t grid = gated_bwd_grid(p.n_tok, p.n_heads, p.d), step = grid * kGroups;
-    gated_norm_bwd_kernel<T, G, VEC, SILU><<<(unsigned)grid, kGatedThreads, 0, stream>>>(p, head_div(p.n_heads), (rows + step - 1) / step);
-    sum_parts_kernel<<<dim3((p.d + 31) / 32, 1), 1024, 0, stream>>>(p.partial, (int)grid, p.d, p.dw, nullptr);
+    constexpr int smem = VEC ? Ahead<T, 3, kGatedThreads>::kBytes : 0;
+    static_assert(smem + kGatedThreads * 16 <= 48 * 1024, "needs no attribute");
+    gated_norm_bwd_kernel<T, G, VEC, SILU><<<(unsigned)grid, kGatedThreads, smem, stream>>>(p, head_div(p.n_heads), (rows + step - 1) / step);
+    const cudaError_t e = sum_parts(p.partial, (int)grid, p.d, p.dw, nullptr, stream);
+    if (e != cudaSuccess) return e;
     count_launches(2);
     return cudaGetLastError();
 }
