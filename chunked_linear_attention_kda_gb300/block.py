@@ -10,6 +10,8 @@ contiguous. There is no CPU path.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 import chunked_linear_attention_kda_gb300 as _kda
@@ -100,6 +102,12 @@ def _bytes(need, dev):
     return _empty((need,), torch.uint8, dev)
 
 
+@functools.lru_cache(maxsize=1024)
+def _need(what, *sizes):
+    """What a workspace size function says of these sizes."""
+    return getattr(_kda._lib or _kda.load_library(), what)(*sizes)
+
+
 def _gdr_inputs(q, k, v, g, beta, dev):
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q and k must be [N, H_k, d_k], v [N, H, d_v] (packed, token-major)")
@@ -109,6 +117,13 @@ def _gdr_inputs(q, k, v, g, beta, dev):
     if hk == 0 or h % hk != 0:
         raise ValueError(f"v's {h} heads must be a multiple of q's {hk}")
     dtype = q.dtype
+    # the usual call: everything as it should be, without a function call for each tensor
+    if (k.shape == shape and k.dtype is dtype and v.dtype is dtype and g.dtype is _F32 and
+            beta.dtype is _F32 and g.shape == (n, h) and beta.shape == (n, h) and
+            k.get_device() == dev and v.get_device() == dev and g.get_device() == dev and
+            beta.get_device() == dev and q.is_contiguous() and k.is_contiguous() and
+            v.is_contiguous() and g.is_contiguous() and beta.is_contiguous()):
+        return n, hk, h, dk, dv, (hk * dk, hk * dk, h * dv)
     strides = (_rows("q", q, shape, dtype, dev), _rows("k", k, shape, dtype, dev),
                _rows("v", v, (n, h, dv), dtype, dev))
     _flat("g", g, (n, h), _F32, dev)
@@ -148,7 +163,7 @@ def gdr_chunk_fwd(q, k, v, g, beta, h0=None, cu_seqlens=None, *, out=None, h_fin
         h_final = _empty((n_seq, h, dk, dv), torch.float32, dev)
     code = _CODE[q.dtype]
     if workspace is None:
-        need = lib.kda_gdr_chunk_fwd_workspace_bytes(n, n_seq, hk, h, dk, dv, code)
+        need = _need("kda_gdr_chunk_fwd_workspace_bytes", n, n_seq, hk, h, dk, dv, code)
         workspace = _bytes(need, dev)
     _done(lib, lib.kda_gdr_chunk_fwd(
         _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(h0), _p(cu_seqlens), _p(out),
@@ -177,7 +192,7 @@ def gdr_chunk_bwd(q, k, v, g, beta, h0, cu_seqlens, dout, dh_final=None, *, want
              if want_dh0 else None)
     code = _CODE[q.dtype]
     if workspace is None:
-        need = lib.kda_gdr_chunk_bwd_workspace_bytes(n, n_seq, hk, h, dk, dv, code)
+        need = _need("kda_gdr_chunk_bwd_workspace_bytes", n, n_seq, hk, h, dk, dv, code)
         workspace = _bytes(need, dev)
     _done(lib, lib.kda_gdr_chunk_bwd(
         _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(h0), _p(cu_seqlens), _p(dout),
@@ -265,7 +280,7 @@ def residual_norm_bwd(dy, r, weight, dr=None, x=None, scale=None, *, eps=1e-6, w
     dx = None if scale is None else _empty((n, d), r.dtype, dev)
     ds = None if scale is None else _empty((d,), _F32, dev)
     if workspace is None:
-        need = lib.kda_residual_norm_bwd_workspace_bytes(n, d, scale is not None)
+        need = _need("kda_residual_norm_bwd_workspace_bytes", n, d, scale is not None)
         workspace = _bytes(need, dev)
     _done(lib, lib.kda_residual_norm_bwd(
         _p(dy), ss[0], _p(dr), ss[1], _p(r), ss[2], None if scale is None else _p(x), ss[3],
@@ -309,7 +324,7 @@ def gated_norm_bwd(dy, x, gate, weight, *, eps=1e-6, activation="sigmoid", works
     dgate = _empty((n, h, d), x.dtype, dev)
     dw = _empty((d,), _F32, dev)
     if workspace is None:
-        need = lib.kda_gated_norm_bwd_workspace_bytes(n, h, d)
+        need = _need("kda_gated_norm_bwd_workspace_bytes", n, h, d)
         workspace = _bytes(need, dev)
     _done(lib, lib.kda_gated_norm_bwd(
         _p(dy), ys, _p(x), xs, _p(gate), gs, _p(weight), _p(dx), _p(dgate), _p(dw),
