@@ -105,7 +105,9 @@ struct ChainSmem {
     // ring 1
     static constexpr int K = 0, V = K + kKey, X = V + (kRev ? 0 : kVal), Gate1 = X + kX;
     static constexpr int kStage1 = (Gate1 + kGate + 1023) / 1024 * 1024;
-    static constexpr int N1 = NS == 2 ? (kRev ? 2 : 3) : 1;
+    // As many stages as fit (three planes, 512 tokens of 4 heads, backward: 76 us with two, 84 with
+    // one); for fp32 with d_k above 64 that is one, and a step waits for its chunk's copy.
+    static constexpr int N1 = NS == 2 ? (kRev ? 2 : 3) : NI == 1 || DKP == 64 ? 2 : 1;
     // ring 2
     static constexpr int Q = 0, dO = Q + kKey, P = dO + (kRev ? kVal : 0), Gate2 = P + kP;
     static constexpr int kStage2 = (Gate2 + kGate + 1023) / 1024 * 1024;
