@@ -416,7 +416,7 @@ cudaError_t residual_run(const ResidualNormArgs &p, bool bwd, cudaStream_t strea
                                               : Ahead<T, 3, L::kThreads>::kBytes : 0;
     const int smem = (NV == 1 ? p.d * 4 * (p.scale ? 2 : 1) : 0) + ahead;
     auto kernel = p.scale ? residual_norm_bwd_kernel<T, WPR, NV, VEC, true> : residual_norm_bwd_kernel<T, WPR, NV, VEC, false>;
-    if (smem > 48 * 1024) {
+    if (smem + (int)sizeof(float2) * 2 * L::kWarps > 48 * 1024) {  // with the static buffers
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }

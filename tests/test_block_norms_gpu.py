@@ -185,3 +185,37 @@ def test_binding_refuses():
         kda.residual_norm_fwd(x, w, eps=0.0)
     with pytest.raises(kda.KDAError):
         kda.residual_norm_fwd(x, w, x, out=x)
+
+
+# ---------------------------------------------------------------- more rows than a launch holds at once
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("n,d", [(1901, 2048), (701, 4096), (333, 8192), (5003, 264), (9001, 96), (1301, 1003)])
+@pytest.mark.parametrize("with_dr,with_scale", [(True, True), (False, False)])
+def test_residual_norm_backward_walks_over_rows(n, d, with_dr, with_scale, dtype):
+    r, dy, x = rand(1, n, d, dtype=dtype), rand(2, n, d, dtype=dtype), rand(3, n, d, dtype=dtype)
+    dr = rand(4, n, d, dtype=dtype) if with_dr else None
+    w, sc = 1 + 0.2 * rand(5, d), 0.5 + 0.2 * rand(6, d) if with_scale else None
+    got = kda.residual_norm_bwd(dy, r, w, dr, x if with_scale else None, sc, eps=EPS)
+    check(got, block.residual_norm_grads(block.f64(dy), block.f64(r), block.f64(w), block.f64(dr), block.f64(x),
+                                         block.f64(sc), EPS))
+    # a row does not depend on the ones a thread has handled before it
+    part = slice(n - 7, n)
+    last = kda.residual_norm_bwd(dy[part], r[part], w, None if dr is None else dr[part],
+                                 x[part] if with_scale else None, sc, eps=EPS)
+    assert torch.equal(last[1], got[1][part])
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("n,h,d", [(1301, 32, 128), (2003, 16, 64), (1001, 31, 100), (4001, 5, 256), (9001, 7, 24)])
+def test_gated_norm_walks_over_rows(n, h, d, dtype):
+    x, z, dy = (rand(i, n, h, d, dtype=dtype) for i in range(3))
+    w = 1 + 0.2 * rand(4, d)
+    y = kda.gated_norm_fwd(x, z, w, eps=EPS, activation="silu")
+    check((y,), (block.gated_norm(block.f64(x), block.f64(z), block.f64(w), EPS, "silu"),))
+    got = kda.gated_norm_bwd(dy, x, z, w, eps=EPS, activation="silu")
+    check(got, block.gated_norm_grads(block.f64(dy), block.f64(x), block.f64(z), block.f64(w), EPS, "silu"))
+    part = slice(n - 3, n)
+    assert torch.equal(kda.gated_norm_fwd(x[part], z[part], w, eps=EPS, activation="silu"), y[part])
+    last = kda.gated_norm_bwd(dy[part], x[part], z[part], w, eps=EPS, activation="silu")
+    assert torch.equal(last[0], got[0][part]) and torch.equal(last[1], got[1][part])
