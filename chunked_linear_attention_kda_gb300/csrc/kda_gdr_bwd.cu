@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
             }
         }
     };
-    // one thread loads: K and Q, then the 32-channel slices of the value heads, head after head
+    // one thread loads: K and Q, then the slices of the value heads, head after head
     auto bar = [&](int i) { return base + L::Bars + 8 * i; };  // a slice buffer's; kStages: K and Q
     auto used = [&](int i) { return bar(L::kStages + 1 + i); };
     [[maybe_unused]] const uint32_t sums_done = bar(2 * L::kStages + 1), sums_read = sums_done + 8, drain = sums_done + 16;
