@@ -118,8 +118,8 @@ def _gdr_inputs(q, k, v, g, beta, dev):
         raise ValueError(f"v's {h} heads must be a multiple of q's {hk}")
     dtype = q.dtype
     # the usual call: everything as it should be, without a function call for each tensor
-    if (k.shape == shape and k.dtype is dtype and v.dtype is dtype and g.dtype is _F32 and
-            beta.dtype is _F32 and g.shape == (n, h) and beta.shape == (n, h) and
+    if (k.shape == shape and v.shape[0] == n and k.dtype is dtype and v.dtype is dtype and
+            g.dtype is _F32 and beta.dtype is _F32 and g.shape == (n, h) and beta.shape == (n, h) and
             k.get_device() == dev and v.get_device() == dev and g.get_device() == dev and
             beta.get_device() == dev and q.is_contiguous() and k.is_contiguous() and
             v.is_contiguous() and g.is_contiguous() and beta.is_contiguous()):
@@ -212,9 +212,9 @@ def gdr_step(q, k, v, g, beta, state, slots=None, *, out=None):
     if slots is not None:
         _flat("slots", slots, (n,), _I32, dev)
     if out is None:
-        out = _empty(v.shape, q.dtype, dev)
+        out = _empty((n, h, dv), q.dtype, dev)
     else:
-        _flat("out", out, v.shape, q.dtype, dev)
+        _flat("out", out, (n, h, dv), q.dtype, dev)
     status = lib.kda_gdr_step(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, g.data_ptr(), beta.data_ptr(),
         state.data_ptr(), None if slots is None else slots.data_ptr(), out.data_ptr(), n,
