@@ -97,15 +97,20 @@ def _empty(shape, dtype, dev):
     return _strided((a, b, c, d), (b * c * d, c * d, d, 1), dtype)
 
 
-def _bytes(need, dev):
-    """A workspace of ``need`` bytes."""
-    return _empty((need,), torch.uint8, dev)
-
-
 @functools.lru_cache(maxsize=1024)
 def _need(what, *sizes):
     """What a workspace size function says of these sizes."""
     return getattr(_kda._lib or _kda.load_library(), what)(*sizes)
+
+
+def _workspace(given, dev, what, *sizes):
+    """The caller's workspace, or a new one of the bytes that the size function ``what`` says of
+    ``sizes``. Whether the caller's is large enough and aligned the library checks."""
+    if given is None:
+        return _empty((_need(what, *sizes),), torch.uint8, dev)
+    if given.get_device() != dev or not given.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return given
 
 
 def _gdr_inputs(q, k, v, g, beta, dev):
@@ -162,9 +167,7 @@ def gdr_chunk_fwd(q, k, v, g, beta, h0=None, cu_seqlens=None, *, out=None, h_fin
     elif output_final_state:
         h_final = _empty((n_seq, h, dk, dv), torch.float32, dev)
     code = _CODE[q.dtype]
-    if workspace is None:
-        need = _need("kda_gdr_chunk_fwd_workspace_bytes", n, n_seq, hk, h, dk, dv, code)
-        workspace = _bytes(need, dev)
+    workspace = _workspace(workspace, dev, "kda_gdr_chunk_fwd_workspace_bytes", n, n_seq, hk, h, dk, dv, code)
     _done(lib, lib.kda_gdr_chunk_fwd(
         _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(h0), _p(cu_seqlens), _p(out),
         _p(h_final), _p(workspace), workspace.numel() * workspace.element_size(), n, n_seq, hk,
@@ -191,9 +194,7 @@ def gdr_chunk_bwd(q, k, v, g, beta, h0, cu_seqlens, dout, dh_final=None, *, want
              _empty((n_seq, h, dk, dv), torch.float32, dev)
              if want_dh0 else None)
     code = _CODE[q.dtype]
-    if workspace is None:
-        need = _need("kda_gdr_chunk_bwd_workspace_bytes", n, n_seq, hk, h, dk, dv, code)
-        workspace = _bytes(need, dev)
+    workspace = _workspace(workspace, dev, "kda_gdr_chunk_bwd_workspace_bytes", n, n_seq, hk, h, dk, dv, code)
     _done(lib, lib.kda_gdr_chunk_bwd(
         _p(q), _p(k), _p(v), *strides, _p(g), _p(beta), _p(h0), _p(cu_seqlens), _p(dout),
         _p(dh_final), *[_p(t) for t in grads], _p(workspace),
@@ -279,9 +280,7 @@ def residual_norm_bwd(dy, r, weight, dr=None, x=None, scale=None, *, eps=1e-6, w
     dw = _empty((d,), _F32, dev)
     dx = None if scale is None else _empty((n, d), r.dtype, dev)
     ds = None if scale is None else _empty((d,), _F32, dev)
-    if workspace is None:
-        need = _need("kda_residual_norm_bwd_workspace_bytes", n, d, scale is not None)
-        workspace = _bytes(need, dev)
+    workspace = _workspace(workspace, dev, "kda_residual_norm_bwd_workspace_bytes", n, d, scale is not None)
     _done(lib, lib.kda_residual_norm_bwd(
         _p(dy), ss[0], _p(dr), ss[1], _p(r), ss[2], None if scale is None else _p(x), ss[3],
         _p(scale), _p(weight), _p(dx), _p(dres), _p(ds), _p(dw), _p(workspace),
@@ -323,9 +322,7 @@ def gated_norm_bwd(dy, x, gate, weight, *, eps=1e-6, activation="sigmoid", works
     dx = _empty((n, h, d), x.dtype, dev)
     dgate = _empty((n, h, d), x.dtype, dev)
     dw = _empty((d,), _F32, dev)
-    if workspace is None:
-        need = _need("kda_gated_norm_bwd_workspace_bytes", n, h, d)
-        workspace = _bytes(need, dev)
+    workspace = _workspace(workspace, dev, "kda_gated_norm_bwd_workspace_bytes", n, h, d)
     _done(lib, lib.kda_gated_norm_bwd(
         _p(dy), ys, _p(x), xs, _p(gate), gs, _p(weight), _p(dx), _p(dgate), _p(dw),
         _p(workspace), workspace.numel() * workspace.element_size(), n, h, d, eps,

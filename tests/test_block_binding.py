@@ -10,6 +10,7 @@ from chunked_linear_attention_kda_gb300 import block
 @pytest.fixture
 def on_host(monkeypatch):
     monkeypatch.setattr(block, "_start", lambda t, what: (None, 0, -1))
+    monkeypatch.setattr(block, "_empty", lambda shape, dtype, dev: torch.empty(shape, dtype=dtype))
 
 
 def inputs(n, m, hk=1, hv=2, d=8):
@@ -32,3 +33,31 @@ def test_values_of_another_length_are_refused(on_host, m, strided):
                  lambda: kda.gdr_step(q, k, v, g, beta, state, out=torch.zeros_like(v))):
         with pytest.raises(ValueError, match="v must be"):
             call()
+
+
+def calls_with_a_workspace(workspace, dev="cpu"):
+    q, k, v, g, beta = (t.to(dev) for t in inputs(8, 8))
+    cu = torch.tensor([0, 8], dtype=torch.int32, device=dev)
+    x, w = torch.ones(4, 16, device=dev), torch.ones(16, device=dev)
+    z = torch.ones(4, 2, 16, device=dev)
+    return (lambda: kda.gdr_chunk_fwd(q, k, v, g, beta, None, cu, workspace=workspace),
+            lambda: kda.gdr_chunk_bwd(q, k, v, g, beta, None, cu, torch.zeros_like(v), workspace=workspace),
+            lambda: kda.residual_norm_bwd(x, x, w, workspace=workspace),
+            lambda: kda.gated_norm_bwd(z, z, z, w, workspace=workspace))
+
+
+def test_a_workspace_with_gaps_is_refused(on_host):
+    # expanded, it spans a byte of the 16 MB that it counts; cut out, more than it counts
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(1 << 24), torch.zeros(1 << 20)[::2]):
+        for call in calls_with_a_workspace(bad):
+            with pytest.raises(ValueError, match="workspace"):
+                call()
+
+
+@pytest.mark.gpu
+def test_a_workspace_on_another_device_is_refused():
+    for call in calls_with_a_workspace(torch.zeros(1 << 24, dtype=torch.uint8), "cuda"):
+        with pytest.raises(ValueError, match="workspace"):
+            call()
+    for call in calls_with_a_workspace(torch.zeros(1 << 24, dtype=torch.uint8, device="cuda"), "cuda"):
+        call()
