@@ -6,7 +6,7 @@ Like the rest of the package a thin binding of the C ABI in ``include/kda.h``: m
 checks, output and workspace allocation through torch, raw pointers and the current
 stream. Inputs are torch CUDA tensors; q, k, v and the norms' activations may be slices of
 a wider tensor (any stride between tokens, a token's row contiguous), everything else is
-contiguous. There is no CPU path.
+contiguous. The tensors' device has to be the current one. There is no CPU path.
 """
 from __future__ import annotations
 
@@ -23,6 +23,7 @@ ACTIVATIONS = {"sigmoid": 0, "silu": 1}
 # The checks below run on every call, in front of kernels of a few microseconds: they read a
 # tensor's attributes once, compare device indexes, and take the raw stream handle.
 _stream = torch._C._cuda_getCurrentRawStream
+_current = torch._C._cuda_getDevice
 
 
 def _start(t, what):
@@ -32,6 +33,9 @@ def _start(t, what):
     if t.dtype not in _CODE:
         raise ValueError(f"{what}: activations must be bfloat16 or float32, got {t.dtype}")
     dev = t.get_device()
+    if _current() != dev:  # kernels go to the current device, whatever stream they are given
+        raise ValueError(f"{what}: the tensors are on cuda:{dev}, the current device is cuda:{_current()} "
+                         f"(call it under torch.cuda.device)")
     return _kda._lib or _kda.load_library(), _stream(dev), dev
 
 
@@ -81,8 +85,8 @@ _strided = getattr(getattr(torch._C._dynamo, "guards", None), "_empty_strided_cu
 
 
 def _empty(shape, dtype, dev):
-    """A contiguous tensor of one to four dimensions on the device of index ``dev``."""
-    if _strided is None or torch._C._cuda_getDevice() != dev:
+    """A contiguous tensor of one to four dimensions on ``dev``, the current device's index."""
+    if _strided is None:
         return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
     n = len(shape)  # a plain tuple is asked for, torch.Size is none
     if n == 3:

@@ -513,7 +513,8 @@ int32_t kda_chunk_fwd_pipeline_plan(const int32_t *host_cu_seqlens, int32_t n_se
  * beta are fp32; with KDA_BF16 the products run on the tensor cores with every operand
  * that is not itself a bf16 input carried in two bf16 parts (about 2^-17 of relative
  * rounding), with KDA_F32 in three (about 2^-24). Results are deterministic. cu_seqlens
- * is read on the device only, as above.
+ * is read on the device only, as above. Every call of this part launches on the current
+ * device, which has to hold its memory and own its stream.
  */
 
 /*

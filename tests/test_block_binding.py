@@ -61,3 +61,24 @@ def test_a_workspace_on_another_device_is_refused():
             call()
     for call in calls_with_a_workspace(torch.zeros(1 << 24, dtype=torch.uint8, device="cuda"), "cuda"):
         call()
+
+
+class OnDevice:
+    """What _start reads of a CUDA tensor."""
+    is_cuda, dtype = True, torch.float32
+
+    def __init__(self, index):
+        self.index = index
+
+    def get_device(self):
+        return self.index
+
+
+def test_a_device_that_is_not_current_is_refused(monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(block, "_current", lambda: 0, raising=False)
+    monkeypatch.setattr(block, "_stream", lambda dev: 7)
+    monkeypatch.setattr(kda, "_lib", object())
+    assert block._start(OnDevice(0), "gdr_step")[1:] == (7, 0)
+    with pytest.raises(ValueError, match="current device"):
+        block._start(OnDevice(1), "gdr_step")
