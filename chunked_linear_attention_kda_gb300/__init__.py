@@ -16,6 +16,7 @@ the states are fp32.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -717,5 +718,21 @@ def segmented_fwd(q, k, v, gate_logits, beta, h0=None, cu_seqlens=None, *, segme
     return out, h_final
 
 
-from .block import (gated_norm_bwd, gated_norm_fwd, gdr_chunk_bwd, gdr_chunk_fwd,  # noqa: E402
-                    gdr_step, residual_norm_bwd, residual_norm_fwd)
+# block.py imports torch, which this package leaves to the calls: it is loaded at the first use of
+# one of its names.
+_BLOCK = ("gdr_chunk_fwd", "gdr_chunk_bwd", "gdr_step", "residual_norm_fwd", "residual_norm_bwd",
+          "gated_norm_fwd", "gated_norm_bwd")
+
+
+def __getattr__(name):
+    if name != "block" and name not in _BLOCK:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    module = importlib.import_module(__name__ + ".block")
+    if name == "block":
+        return module
+    globals()[name] = value = getattr(module, name)
+    return value
+
+
+def __dir__():
+    return sorted({*globals(), *_BLOCK, "block"})

@@ -1,5 +1,9 @@
 """Checks of the block operators' Python binding on the host: the calls run up to their checks
 with CPU tensors (device index -1) and no library, so whatever passes them fails the test."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -82,3 +86,19 @@ def test_a_device_that_is_not_current_is_refused(monkeypatch):
     assert block._start(OnDevice(0), "gdr_step")[1:] == (7, 0)
     with pytest.raises(ValueError, match="current device"):
         block._start(OnDevice(1), "gdr_step")
+
+
+def test_the_package_imports_without_torch():
+    """Its calls need torch; building the library and reading its symbols do not."""
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import chunked_linear_attention_kda_gb300 as kda\n"
+            "from chunked_linear_attention_kda_gb300 import build\n"
+            "assert kda.library_path() and 'gdr_step' in dir(kda) and not hasattr(kda, 'nothing')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
+
+
+def test_every_public_name_is_there():
+    for name in kda.__all__:
+        assert getattr(kda, name) is not None
+    assert kda.block is block and kda.gdr_step is block.gdr_step
