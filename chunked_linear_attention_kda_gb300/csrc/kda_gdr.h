@@ -17,8 +17,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <vector>
-
 #include "kda_internal.h"
 #include "kda_ptx.h"
 
@@ -46,20 +44,6 @@ __device__ __forceinline__ int64_t slot_base(const int32_t *cu, int n) {
 // waits here for that one's results.
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-// Lets a kernel have `smem` bytes of dynamic shared memory on the current device; asked of the
-// runtime once per kernel and device (a call of 1 us in front of kernels of 10).
-inline cudaError_t allow_smem(const void *kernel, int smem) {
-    struct Seen { const void *kernel; int device; };
-    thread_local std::vector<Seen> seen;
-    int device = 0;
-    cudaError_t e = cudaGetDevice(&device);
-    if (e != cudaSuccess) return e;
-    for (const Seen &s : seen)
-        if (s.kernel == kernel && s.device == device) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) seen.push_back({kernel, device});
-    return e;
-}
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, const A &...args) {
     cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), smem);

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <vector>
+
 namespace kda {
 
 // Tile length in tokens and the lower bound of the log-decay. Both are fixed by
@@ -188,5 +190,21 @@ cudaError_t read_device_flags(unsigned int *flags, bool reset, cudaStream_t stre
 
 // Adds n to the process-wide kernel launch counter (kda_kernel_launch_count).
 void count_launches(uint64_t n);
+// Lets a kernel have `smem` bytes of dynamic shared memory on the current device; asked of the
+// runtime once per kernel and device (a call of 1 us in front of kernels of 10). The limit belongs
+// to the process: a kernel always asks for the same, the most that any of its launches takes, so
+// that no thread lowers it between another one's request and launch.
+inline cudaError_t allow_smem(const void *kernel, int smem) {
+    struct Seen { const void *kernel; int device; };
+    thread_local std::vector<Seen> seen;
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    for (const Seen &s : seen)
+        if (s.kernel == kernel && s.device == device) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) seen.push_back({kernel, device});
+    return e;
+}
 
 }  // namespace kda

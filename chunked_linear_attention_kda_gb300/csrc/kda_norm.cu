@@ -412,16 +412,18 @@ cudaError_t residual_run(const ResidualNormArgs &p, bool bwd, cudaStream_t strea
     }
     const int64_t grid = residual_bwd_grid(p.n_rows, p.d), parts = grid * L::kGroups;
     const int64_t rounds = (p.n_rows + parts - 1) / parts;
+    constexpr int most_d = 256 * WPR;  // channels of this instance where it keeps the parameters in shared memory
     const int ahead = VEC && NV == 1 ? p.scale ? Ahead<T, 4, L::kThreads>::kBytes
                                               : Ahead<T, 3, L::kThreads>::kBytes : 0;
-    const int smem = (NV == 1 ? p.d * 4 * (p.scale ? 2 : 1) : 0) + ahead;
+    const int per_d = NV == 1 ? p.scale ? 8 : 4 : 0, smem = p.d * per_d + ahead, most = most_d * per_d + ahead;
     auto kernel = p.scale ? residual_norm_bwd_kernel<T, WPR, NV, VEC, true> : residual_norm_bwd_kernel<T, WPR, NV, VEC, false>;
-    if (smem + (int)sizeof(float2) * 2 * L::kWarps > 48 * 1024) {  // with the static buffers
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (most + (int)sizeof(float2) * 2 * L::kWarps > 48 * 1024) {  // with the static buffers
+        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(kernel), most);
         if (e != cudaSuccess) return e;
     }
     kernel<<<(unsigned)grid, L::kThreads, smem, stream>>>(p, rounds);
-    const cudaError_t e = sum_parts(p.partial, (int)parts, p.d, p.dw, p.scale ? p.dscale : nullptr, stream);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = sum_parts(p.partial, (int)parts, p.d, p.dw, p.scale ? p.dscale : nullptr, stream);
     if (e != cudaSuccess) return e;
     count_launches(2);
     return cudaGetLastError();
@@ -660,7 +662,8 @@ cudaError_t gated_run(const GatedNormArgs &p, bool bwd, cudaStream_t stream) {
     constexpr int smem = VEC ? Ahead<T, 3, kGatedThreads>::kBytes : 0;
     static_assert(smem + kGatedThreads * 16 <= 48 * 1024, "needs no attribute");
     gated_norm_bwd_kernel<T, G, VEC, SILU><<<(unsigned)grid, kGatedThreads, smem, stream>>>(p, head_div(p.n_heads), (rows + step - 1) / step);
-    const cudaError_t e = sum_parts(p.partial, (int)grid, p.d, p.dw, nullptr, stream);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = sum_parts(p.partial, (int)grid, p.d, p.dw, nullptr, stream);
     if (e != cudaSuccess) return e;
     count_launches(2);
     return cudaGetLastError();

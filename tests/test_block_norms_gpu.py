@@ -4,6 +4,8 @@ definitions on the same inputs.
 Bars on the rel-L2 error: bf16 results are held to the definition's value rounded to bf16, from
 which an fp32 value can only differ next to a rounding boundary: 2.1e-3; fp32 results come from fp32 sums of up to 8192 terms (added pairwise or by a few
 threads: below 30 roundings of 2^-24) and a handful of roundings: 2e-6."""
+import threading
+
 import pytest
 import torch
 
@@ -219,3 +221,34 @@ def test_gated_norm_walks_over_rows(n, h, d, dtype):
     assert torch.equal(kda.gated_norm_fwd(x[part], z[part], w, eps=EPS, activation="silu"), y[part])
     last = kda.gated_norm_bwd(dy[part], x[part], z[part], w, eps=EPS, activation="silu")
     assert torch.equal(last[0], got[0][part]) and torch.equal(last[1], got[1][part])
+
+
+def test_threads_of_different_widths_keep_their_shared_memory():
+    """Threads run one kernel at two widths, whose launches take 192 and 164 KB of shared memory,
+    straight through the C entry: none takes another's away, so no launch is refused."""
+    lib = kda.load_library()
+    calls, keep = [], []
+    for i in range(4):
+        d = (8192, 4608)[i % 2]
+        x, dy, w, s = rand(i, 2, d), rand(i + 4, 2, d), rand(i + 8, d), rand(i + 12, d)
+        dx, dres, dw, ds = (torch.empty_like(t) for t in (x, x, w, w))
+        need = lib.kda_residual_norm_bwd_workspace_bytes(2, d, 1)
+        ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+        stream = torch.cuda.Stream()
+        keep.append((x, dy, w, s, dx, dres, dw, ds, ws, stream))
+        p = [t.data_ptr() for t in keep[-1][:9]]
+        calls.append((p[1], d, None, 0, p[0], d, p[0], d, p[3], p[2], p[4], p[5], p[7], p[6], p[8], need, 2, d,
+                      1e-5, 0, stream.cuda_stream))
+    torch.cuda.synchronize()
+    failures = []
+
+    def run(args):
+        failures.extend(status for status in (lib.kda_residual_norm_bwd(*args) for _ in range(10000)) if status)
+
+    threads = [threading.Thread(target=run, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failures, (len(failures), failures[0])
