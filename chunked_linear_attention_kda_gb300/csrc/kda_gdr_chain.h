@@ -99,8 +99,7 @@ struct ChainSmem {
     static constexpr bool kHelp = PAIRS == 2;
     static constexpr bool kOut = M == Mode::kForward, kRev = M == Mode::kReverse;
     static constexpr int kKey = NI * C * DKP * 2, kSlice = NI * C * 64, kVal = PAIRS / 2 * kSlice;
-    static constexpr int kX = NS * kTri;
-    static constexpr int kP = (kOut ? NI : NS) * kTri;       // the output takes P in bf16 for bf16
+    static constexpr int kX = NS * kTri, kP = NS * kTri;
     static constexpr int kGate = kChainGates * 4;
     // ring 1
     static constexpr int K = 0, V = K + kKey, X = V + (kRev ? 0 : kVal), Gate1 = X + kX;
@@ -273,7 +272,9 @@ __device__ __forceinline__ void get_block(const char *p, int plane, uint32_t (*a
         a[q][0] = x.x; a[q][1] = x.y; a[q][2] = x.z; a[q][3] = x.w;
     }
 }
-// ---- the output, 32 tokens x 16 value channels: o[m][n], token blocks m0 + m
+// ---- the output, 32 tokens x 16 value channels: o[m][n], token blocks h and 3 - h, whose products
+// with the lower triangle P are five blocks for either h
+__device__ __forceinline__ int out_block(int h, int m) { return m ? 3 - h : h; }
 
 // the A-operand planes of a 16 x 16 block as the B operand of the transposed product
 template <int NP>
@@ -284,23 +285,23 @@ __device__ __forceinline__ void as_b(const uint32_t (*a)[4], uint32_t (*b)[4]) {
     }
 }
 // o += Q S0, key channels of block kx; a the planes of S^T
-template <int NI, int DKP>
-__device__ __forceinline__ void add_queries(const uint32_t (*a)[4], uint32_t q, int m0, int kx, float (*o)[2][4]) {
-    uint32_t b[NI][4];
-    as_b<NI>(a, b);
+template <int NI, int NS, int DKP>
+__device__ __forceinline__ void add_queries(const uint32_t (*a)[4], uint32_t q, int h, int kx, float (*o)[2][4]) {
+    uint32_t b[NS][4];
+    as_b<NS>(a, b);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
         uint32_t f[NI][4];
 #pragma unroll
-        for (int x = 0; x < NI; ++x) key_a(q + x * C * DKP * 2, (m0 + m) * 16, kx * 16, f[x]);
-        product<NI, NI, NI>(o[m], f, b);
+        for (int x = 0; x < NI; ++x) key_a(q + x * C * DKP * 2, out_block(h, m) * 16, kx * 16, f[x]);
+        product<NI, NS, NS>(o[m], f, b);
     }
 }
-__device__ __forceinline__ void scale_output(float (*o)[2][4], const float *gate, float scale, int m0) {
+__device__ __forceinline__ void scale_output(float (*o)[2][4], const float *gate, float scale, int h) {
     const int gr = (threadIdx.x & 31) >> 2;
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-        const int r = (m0 + m) * 16 + gr;
+        const int r = out_block(h, m) * 16 + gr;
         const float g0 = scale * gate[r], g1 = scale * gate[r + 8];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -308,12 +309,12 @@ __device__ __forceinline__ void scale_output(float (*o)[2][4], const float *gate
         }
     }
 }
-// o += P U for the tokens of half h; uo the pair's U^T (fp32 accumulators)
-template <int NI, int NS>
+// o += P U; uo the pair's U^T (fp32 accumulators)
+template <int NS>
 __device__ __forceinline__ void add_p_values(const char *uo, uint32_t pt, int h, float (*o)[2][4]) {
 #pragma unroll
     for (int kx = 0; kx < 4; ++kx) {
-        if (kx > 2 * h + 1) break;
+        if (kx > 3 - h) break;
         uint32_t a[NS][4];
         float u[2][4];
 #pragma unroll
@@ -326,23 +327,23 @@ __device__ __forceinline__ void add_p_values(const char *uo, uint32_t pt, int h,
         as_b<NS>(a, b);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            if (kx > 2 * h + m) continue;
-            uint32_t f[NI][4];
+            if (kx > out_block(h, m)) continue;
+            uint32_t f[NS][4];
 #pragma unroll
-            for (int q = 0; q < NI; ++q) frag_a<32>(pt + q * kTri + tri_block(2 * h + m, kx), 0, 0, f[q]);
-            product<NI, NS, NS>(o[m], f, b);
+            for (int q = 0; q < NS; ++q) frag_a<32>(pt + q * kTri + tri_block(out_block(h, m), kx), 0, 0, f[q]);
+            product<NS, NS, NS>(o[m], f, b);
         }
     }
 }
 template <typename T>
-__device__ __forceinline__ void store_output(T *out, const float (*o)[2][4], int row0, int m0, int v0, int64_t tok0,
+__device__ __forceinline__ void store_output(T *out, const float (*o)[2][4], int row0, int h, int v0, int64_t tok0,
                                              int len, int head, const GdrArgs &p, bool wide) {
     const int gr = (threadIdx.x & 31) >> 2, tq = threadIdx.x & 3;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int r = row0 + (m0 + m) * 16 + gr + x * 8;
+            const int r = row0 + out_block(h, m) * 16 + gr + x * 8;
             if (r >= len) continue;
             T *row = out + ((tok0 + r) * p.n_heads + head) * p.d_v;
 #pragma unroll
@@ -799,15 +800,15 @@ __device__ __forceinline__ void chain(const CUtensorMap &tm_q, const CUtensorMap
             zero<4>(&o[0][0]);
 #pragma unroll
             for (int kx = 0; kx < KX; ++kx) {
-                uint32_t a[NI][4];
-                get_block<NI>(pair + L::Sx + hb * L::kSx + kx * 512, KX * 512, a);
-                add_queries<NI, DKP>(a, s + L::Q, 2 * h, kx, o);
+                uint32_t a[NS][4];
+                get_block<NS>(pair + L::Sx + hb * L::kSx + kx * 512, KX * 512, a);
+                add_queries<NI, NS, DKP>(a, s + L::Q, h, kx, o);
             }
-            scale_output(o, gate, scale, 2 * h);
-            add_p_values<NI, NS>(pair + L::Uo + hb * L::kUo, s + L::P, h, o);
+            scale_output(o, gate, scale, h);
+            add_p_values<NS>(pair + L::Uo + hb * L::kUo, s + L::P, h, o);
             warp_arrive(hempty(hb));
             warp_arrive(empty2(s2));
-            store_output(static_cast<T *>(p.out), o, i * C, 2 * h, v0, tok0, len, head, p, wide_out);
+            store_output(static_cast<T *>(p.out), o, i * C, h, v0, tok0, len, head, p, wide_out);
         }
     } else if constexpr (kRev && kHelp) {
         // ------------------------------------------------ G^T = (s gamma dO)^T Q, key channels of half

@@ -350,8 +350,7 @@ __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 3 : 1)
                             split2<NS>(x[2 * h], x[2 * h + 1], w);
                             char *at = P + tri_block(I[s], J[s]) + tile_off<32>(gr + 8 * h, n * 8 + tq * 2);
 #pragma unroll
-                            for (int pl = 0; pl < NS; ++pl)  // the forward pass alone reads NI planes of P
-                                if (pl < NI || values == 2) *reinterpret_cast<uint32_t *>(at + pl * kTri) = w[pl];
+                            for (int pl = 0; pl < NS; ++pl) *reinterpret_cast<uint32_t *>(at + pl * kTri) = w[pl];
                         }
                     }
                 }

@@ -384,3 +384,25 @@ def test_binding_refuses():
     y = Inputs([4], 1, 1, 160, 16, BF, seed=1)
     with pytest.raises(kda.KDAError):
         kda.gdr_chunk_fwd(*y.args)
+
+
+# ---------------------------------------------------------------- one rounding in a bf16 result
+
+def rounded_once(got, ref):
+    """A bf16 result against the definition's value rounded to bf16: apart only where the value
+    before its rounding, off by d, falls on the other side of a boundary. That happens to d / ulp
+    of the values, each then an ulp off, an ulp up to 2^-7 of the value: the mean square of the
+    difference is up to d ulp = 2e-5 2^-7 (d as for the fp32 results), its root 4e-4."""
+    e = rel_l2(got.double().cpu().numpy(), ref.to(BF).double().numpy())
+    assert e <= 4e-4, f"{e:.2e}"
+
+
+ROUNDED = [([1], 1, 1, 128, 128), ([200], 2, 4, 128, 128), ([0, 1, 130, 0, 64, 17], 2, 2, 128, 128),
+           ([5, 0, 66], 1, 4, 33, 31), ([100], 3, 3, 96, 112), ([90], 1, 2, 65, 33), ([140], 2, 2, 8, 128),
+           ([700, 333], 4, 8, 64, 64)]
+
+
+@pytest.mark.parametrize("lengths,hk,hv,dk,dv", ROUNDED)
+def test_forward_output_is_rounded_once(lengths, hk, hv, dk, dv):
+    x = Inputs(lengths, hk, hv, dk, dv, BF, seed=len(lengths) + dk)
+    rounded_once(forward(x)[0], block.gdr(*x.f64(), x.cu_host)[0])
