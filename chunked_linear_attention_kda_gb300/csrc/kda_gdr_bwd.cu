@@ -67,9 +67,9 @@ struct LocalSmem {
     static constexpr bool TC = kTensor<T, NS>;
     static constexpr int NI = InputPlanes<T>::N;
     static constexpr int kThreads = kLocalThreads + (TC ? 96 : 0);  // a warp issues products, one loads, one sums dg
-    // Slices of the value channels. With tcgen05 16 channels and six buffers: a copy takes 2500
-    // cycles to arrive and its buffer is read for 2000, the products of a slice take 750.
-    static constexpr int kSl = TC ? 16 : 32, kStages = TC ? 6 : 1;
+    // Slices of the value channels. With tcgen05 16 channels and five buffers, as many as fit: a copy
+    // takes 2500 cycles to arrive and its buffer is read for 2000, the products of a slice take 750.
+    static constexpr int kSl = TC ? 16 : 32, kStages = TC ? 5 : 1;
     static constexpr int kPlane = C * DKP * 2;
     static constexpr int kIn = C * 32 * 2;  // a plane of 32 channels of dO or V
     // a block of 16 value channels as the chains left it: planes of S and U, planes of dS and E
@@ -84,12 +84,12 @@ struct LocalSmem {
     static constexpr int K = Vals + 3 * kVals, Q = K + NI * kPlane, Pair = Q + NI * kPlane;
     // q.k and k.k: with tcgen05 in tensor memory. B and F: without it over the first slice buffer,
     // once the slices are done.
-    static constexpr int B = TC ? Pair : 0, F = B + NI * kTile;
-    static_assert(TC || 2 * NI * kTile <= kSlice, "B and F fit a slice buffer");
+    static constexpr int B = TC ? Pair : 0, F = B + NS * kTile;
+    static_assert(TC || 2 * NS * kTile <= kSlice, "B and F fit a slice buffer");
     // a head's gates are loaded with its first slice, four slices ahead: with two slices a head
     // the sums of the head three before may still be read
     static constexpr int kGates = TC ? 4 : 1;
-    static constexpr int Gate = Pair + (TC ? 2 * NI * kTile : 2 * C * C * 4), Red = Gate + kGates * kGateFloats * 4;
+    static constexpr int Gate = Pair + (TC ? 2 * NS * kTile : 2 * C * C * 4), Red = Gate + kGates * kGateFloats * 4;
     // Red: [kCols][64] row sums of q.x, k.x, k.x, E.V - F k.k and M over the column parts;
     // [4][64] column sums of M over the row blocks; the warps' parts of <S0, dS1>
     static constexpr int kRed = 5 * kCols * C + 4 * C + kLocalThreads / 32;
@@ -301,8 +301,10 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                         sl = 0;
                         ++hh;
                     }
-                    // dO and V need the slice five before to be read, the gates the one four before
-                    const int last = step - (sl == 0 ? 4 : sl & 1 ? 6 : 5);
+                    // its buffer, and those of dO and V, need the slice five before to be read, the
+                    // gates the one four before
+                    static_assert(L::kStages == 5 || !TC, "none of them an earlier one alone");
+                    const int last = step - (sl == 0 ? 4 : 5);
                     if (step == 2) ok = wait_bar(bar(L::kStages), 0);  // K and Q first: they are waited for
                     if (step >= L::kStages) ok = wait_bar(used(last % L::kStages), (last / L::kStages) & 1);
                     if (!ok) break;
@@ -443,9 +445,9 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
     auto add_pairs = [&]() {
 #pragma unroll
         for (int kx = 0; kx < 4; ++kx) {
-            uint32_t ab[NI][4], at[NI][4], af[NI][4];
+            uint32_t ab[NS][4], at[NS][4], af[NS][4];
 #pragma unroll
-            for (int q = 0; q < NI; ++q) {
+            for (int q = 0; q < NS; ++q) {
                 frag_a<128>(base + L::B + q * L::kTile, wr * 16, kx * 16, ab[q]);
                 frag_a_t<128>(base + L::B + q * L::kTile, kx * 16, wr * 16, at[q]);
                 frag_a<128>(base + L::F + q * L::kTile, wr * 16, kx * 16, af[q]);
@@ -459,12 +461,12 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                 uint32_t b[NI][4];
 #pragma unroll
                 for (int q = 0; q < NI; ++q) key_b_t(base + L::K + q * L::kPlane, kx * 16, wc * KC + n * 16, b[q]);
-                if (kx <= wr) product<NI, NI, NI>(&dq[2 * n], ab, b);
-                product<NI, NI, NI>(&dk[2 * n], af, b);
+                if (kx <= wr) product<NS, NI, NS>(&dq[2 * n], ab, b);
+                product<NS, NI, NS>(&dk[2 * n], af, b);
                 if (kx < wr) continue;  // B is lower triangular
 #pragma unroll
                 for (int q = 0; q < NI; ++q) key_b_t(base + L::Q + q * L::kPlane, kx * 16, wc * KC + n * 16, b[q]);
-                product<NI, NI, NI>(&dk[2 * n], at, b);
+                product<NS, NI, NS>(&dk[2 * n], at, b);
             }
         }
     };
@@ -674,11 +676,11 @@ __global__ void __launch_bounds__(LocalSmem<T, DKP, NS>::kThreads)
                         mr[h] += m;
                         mc[i] += m;
                     }
-                    uint32_t wb[NI], wf[NI];
-                    split2<NI>(bv[0], bv[1], wb);
-                    split2<NI>(fv[0], fv[1], wf);
+                    uint32_t wb[NS], wf[NS];
+                    split2<NS>(bv[0], bv[1], wb);
+                    split2<NS>(fv[0], fv[1], wf);
 #pragma unroll
-                    for (int q = 0; q < NI; ++q) {
+                    for (int q = 0; q < NS; ++q) {
                         *reinterpret_cast<uint32_t *>(smem + L::B + q * L::kTile + tile_off<128>(r, j)) = wb[q];
                         *reinterpret_cast<uint32_t *>(smem + L::F + q * L::kTile + tile_off<128>(r, j)) = wf[q];
                     }

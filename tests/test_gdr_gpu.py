@@ -406,3 +406,31 @@ ROUNDED = [([1], 1, 1, 128, 128), ([200], 2, 4, 128, 128), ([0, 1, 130, 0, 64, 1
 def test_forward_output_is_rounded_once(lengths, hk, hv, dk, dv):
     x = Inputs(lengths, hk, hv, dk, dv, BF, seed=len(lengths) + dk)
     rounded_once(forward(x)[0], block.gdr(*x.f64(), x.cu_host)[0])
+
+
+@pytest.mark.parametrize("lengths,hk,hv,dk,dv", ROUNDED)
+def test_gradients_are_rounded_once(lengths, hk, hv, dk, dv):
+    x = Inputs(lengths, hk, hv, dk, dv, BF, seed=len(lengths) + dk)
+    got = kda.gdr_chunk_bwd(*x.args, x.dout, x.dhf)
+    want = block.gdr_grads(*x.f64(), x.cu_host, block.f64(x.dout), block.f64(x.dhf))
+    for a, ref in zip(got[:3], want):
+        rounded_once(a, ref)
+
+
+@pytest.mark.parametrize("hk,hv,dk,dv", [(64, 128, 128, 128), (16, 96, 100, 40), (8, 128, 16, 24)])
+def test_gradients_of_many_pairs_are_rounded_once(hk, hv, dk, dv):
+    x = Inputs(wide(hv), hk, hv, dk, dv, BF, seed=dk + dv)
+    got = kda.gdr_chunk_bwd(*x.args, x.dout, x.dhf)
+    f64 = [t.double() for t in (x.q, x.k, x.v, x.g, x.beta, x.h0)]
+    want = block.gdr_grads(*f64, x.cu_host, x.dout.double(), x.dhf.double())
+    for a, ref in zip(got[:3], want):
+        rounded_once(a, ref.cpu())
+
+
+@pytest.mark.parametrize("lengths,hk,hv", [([9000], 1, 1), ([5000, 4100], 1, 2)])
+def test_long_sequences_of_few_heads(lengths, hk, hv):
+    """Two planes over a hundred chunks of one sequence and more, few heads: the norm of a gradient
+    is made up by its tokens alone."""
+    x = Inputs(lengths, hk, hv, 64, 64, BF, seed=hv)
+    check_forward(x)
+    check_wide(x)
