@@ -450,15 +450,29 @@ bool vec_ok(const void *p, int64_t stride, int es) {
 
 // ---------------------------------------------------------------- gated norm
 
-// act(z) and act'(z); silu when SILU, else the sigmoid. FAST (bf16 tensors): the hardware's
-// exponential and quotient, within a few units in 2^-22 of the sigmoid, far below the
-// result's rounding to bf16; with the accurate forms the bf16 kernels are bound by
-// instruction issue instead of HBM.
+// act(z): silu when SILU, else the sigmoid. FAST (bf16 tensors): the hardware's exponential and
+// quotient, within a few units in 2^-22 of the sigmoid, far below the result's rounding to bf16;
+// with the accurate forms the bf16 kernels are bound by instruction issue instead of HBM.
 template <bool SILU, bool FAST>
-__device__ __forceinline__ void act(float z, float &a, float &da) {
+__device__ __forceinline__ float act(float z) {
     const float s = FAST ? __fdividef(1.f, 1.f + __expf(-z)) : 1.f / (1.f + expf(-z));
-    a = SILU ? z * s : s;
-    da = SILU ? s * fmaf(z, 1.f - s, 1.f) : s * (1.f - s);
+    return SILU ? z * s : s;
+}
+// The sigmoid s and rest = 1 - s, of which act' is formed: s rest, or s (1 + z rest) for silu. rest is
+// exp(-z) s: as a difference it has lost 1e-3 at z = 10 and everything at 17, where s rounds to 1.
+template <bool FAST>
+__device__ __forceinline__ void act_parts(float z, float &s, float &rest) {
+    if constexpr (FAST) {  // the bound keeps exp(-z) finite, where the quotient is 0 already; NaN passes
+        float y;
+        asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(-z), "f"(88.f));
+        const float e = __expf(y);
+        s = __fdividef(1.f, 1.f + e);
+        rest = e * s;
+    } else {
+        const float e = expf(-z);
+        s = 1.f / (1.f + e);
+        rest = z > 0.f ? e * s : 1.f - s;
+    }
 }
 
 // row / n_heads for row < 2^31 as a multiplication: (umulhi(row, m) + row) >> s
@@ -533,9 +547,7 @@ __global__ void __launch_bounds__(kGatedThreads, kGatedFwdCtas)
         const float c = 1.f / sqrtf(s / p.d + p.eps);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float a, da;
-            act<SILU, sizeof(T) == 2>(hz.get(i), a, da);
-            x[i] = x[i] * c * w[i] * a;
+            x[i] = x[i] * c * w[i] * act<SILU, sizeof(T) == 2>(hz.get(i));
         }
         store_row<1, VEC>(static_cast<T *>(p.y) + row * p.d, p.d, t, G, x);
     }
@@ -594,12 +606,16 @@ __global__ void __launch_bounds__(kGatedThreads, 4)
                 dy.load(py, p.d, t, G);
             });
         }
-        float xx = 0.f, tx = 0.f, a[8], da[8];
+        float xx = 0.f, tx = 0.f, a[8], b[8];  // act; 1 - s, for silu act'
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            act<SILU, sizeof(T) == 2>(z.get(i), a[i], da[i]);
+            act_parts<sizeof(T) == 2>(z.get(i), a[i], b[i]);
+            if constexpr (SILU) {
+                b[i] = a[i] * fmaf(z.get(i), b[i], 1.f);
+                a[i] *= z.get(i);
+            }
             xx = fmaf(x.get(i), x.get(i), xx);
-            tx = fmaf(w[i] * a[i] * dy.get(i), x.get(i), tx);
+            tx = fmaf(a[i] * dy.get(i) * w[i], x.get(i), tx);
         }
 #pragma unroll
         for (int o = G / 2; o > 0; o >>= 1) {
@@ -612,10 +628,10 @@ __global__ void __launch_bounds__(kGatedThreads, 4)
         float dx[8], dz[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float n = x.get(i) * c, wd = w[i] * dy.get(i);
-            dx[i] = c * (wd * a[i] - x.get(i) * m);
-            dz[i] = wd * n * da[i];
-            dw[i] = fmaf(dy.get(i) * a[i], n, dw[i]);
+            const float n = x.get(i) * c, da = dy.get(i) * a[i], wa = da * w[i];
+            dx[i] = c * fmaf(-m, x.get(i), wa);
+            dz[i] = (SILU ? w[i] * dy.get(i) : wa) * n * b[i];
+            dw[i] = fmaf(da, n, dw[i]);
         }
         store_row<1, VEC>(static_cast<T *>(p.dx) + row * p.d, p.d, t, G, dx);
         store_row<1, VEC>(static_cast<T *>(p.dgate) + row * p.d, p.d, t, G, dz);

@@ -252,3 +252,37 @@ def test_threads_of_different_widths_keep_their_shared_memory():
         t.join()
     torch.cuda.synchronize()
     assert not failures, (len(failures), failures[0])
+
+
+@pytest.mark.parametrize("dtype,bar", [(FP, 4e-6), (BF, 2 ** -7)])
+@pytest.mark.parametrize("activation", ["sigmoid", "silu"])
+def test_gradient_of_a_closing_gate(activation, dtype, bar):
+    """The sigmoid's derivative falls to 1e-7 at z = +-16: every value of dgate keeps its own relative
+    accuracy. fp32: the exponential's and the quotient's roundings, those of the row's sum of 64
+    squares and a dozen products, 2^-24 each: 4e-6. bf16: an ulp, against the rounded definition."""
+    n, d = 66, 64
+    x, dy = rand(1, n, 2, d, dtype=dtype), rand(2, n, 2, d, dtype=dtype)
+    z = torch.linspace(-16, 16, n * 2 * d, device=DEV).view(n, 2, d).to(dtype)
+    w = 1 + 0.2 * rand(3, d)
+    if activation == "silu":
+        z = z[z[:, 0, 0] > -1]  # further down its derivative crosses zero
+        x, dy = x[:len(z)], dy[:len(z)]
+    got = kda.gated_norm_bwd(dy, x, z, w, eps=EPS, activation=activation)[1]
+    want = block.gated_norm_grads(block.f64(dy), block.f64(x), block.f64(z), block.f64(w), EPS, activation)[1]
+    if dtype == BF:
+        want = want.to(BF).double()
+    off = (got.double().cpu() - want).abs() / want.abs().clamp_min(1e-30)
+    assert float(off.max()) <= bar, f"{float(off.max()):.2e}"
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_a_nan_gate_stays_in_its_row(dtype):
+    x, z, dy = (rand(i, 5, 2, 64, dtype=dtype) for i in range(3))
+    w = 1 + 0.2 * rand(5, 64)
+    clean = kda.gated_norm_bwd(dy, x, z, w, eps=EPS)
+    z[2, 1, 7] = float("nan")
+    dx, dz, dw = kda.gated_norm_bwd(dy, x, z, w, eps=EPS)
+    assert bool(torch.isnan(dx[2, 1]).all()) and bool(torch.isnan(dz[2, 1, 7])) and bool(torch.isnan(dw[7]))
+    keep = torch.ones(5, 2, dtype=torch.bool, device=DEV)
+    keep[2, 1] = False
+    assert torch.equal(dx[keep], clean[0][keep]) and torch.equal(dz[keep], clean[1][keep])
