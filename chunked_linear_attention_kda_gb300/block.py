@@ -142,7 +142,8 @@ def _gdr_inputs(q, k, v, g, beta, dev):
 
 def _sequences(q, dev, n, h, dk, dv, h0, cu_seqlens):
     if cu_seqlens is None:
-        cu_seqlens = torch.tensor([0, n], dtype=torch.int32, device=q.device)
+        # formed on the device: a list would be copied from pageable memory, which a graph cannot capture
+        cu_seqlens = torch.arange(2, dtype=torch.int32, device=q.device).mul_(n)
     n_seq = cu_seqlens.numel() - 1
     if n_seq < 0:
         raise ValueError("cu_seqlens needs at least one entry")

@@ -434,3 +434,27 @@ def test_long_sequences_of_few_heads(lengths, hk, hv):
     x = Inputs(lengths, hk, hv, 64, 64, BF, seed=hv)
     check_forward(x)
     check_wide(x)
+
+
+def test_one_sequence_in_a_graph():
+    """Without offsets a call can be captured; the replay computes on what its inputs hold then."""
+    x = Inputs([150], 1, 2, 64, 64, BF, seed=47)
+    args = (x.q, x.k, x.v, x.g, x.beta, x.h0)
+
+    def both():
+        return (*kda.gdr_chunk_fwd(*args), *kda.gdr_chunk_bwd(*args, None, x.dout, x.dhf))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = both()
+    torch.cuda.synchronize()
+    x.v.copy_(x.v.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, both()))
+    assert kda.read_device_flags() == 0
