@@ -184,7 +184,9 @@ def gdr_chunk_bwd(q, k, v, g, beta, h0, cu_seqlens, dout, dh_final=None, *, want
                   workspace=None):
     """Backward of ``gdr_chunk_fwd`` through ``kda_gdr_chunk_bwd``: the gradients of ``<dout,
     out> + <dh_final, h_final>``. Returns ``(dq, dk, dv, dg, dbeta, dh0)`` (``dh0`` None unless
-    ``want_dh0``); ``dq`` and ``dk`` are summed over the value heads of a key head."""
+    ``want_dh0``); ``dq`` and ``dk`` are summed over the value heads of a key head. What a sequence
+    is packed with changes its gradients within their accuracy: bf16 calls below 8192 (token, head)
+    pairs carry more bits than larger ones, and the order of some sums follows the call's sizes."""
     lib, stream, dev = _start(q, "gdr_chunk_bwd")
     n, hk, h, dk, dv, strides = _gdr_inputs(q, k, v, g, beta, dev)
     n_seq, cu_seqlens = _sequences(q, dev, n, h, dk, dv, h0, cu_seqlens)

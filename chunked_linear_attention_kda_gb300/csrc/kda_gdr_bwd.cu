@@ -766,10 +766,13 @@ cudaError_t backward(const GdrArgs &p, cudaStream_t stream) {
 
 // Planes of the intermediates. dg sums inner products of states with state gradients, which
 // cancel. Over 110 bf16 problems of 1 to 32 heads and 4 to 2900 tokens its error with two planes
-// is up to 1.2e-5 of its norm below 2000 (token, head) pairs and up to 7.3e-6 above; with three
-// it stays at 4e-7. Three planes take twice the time and more: 84 against 44 us at 2048 pairs,
-// 303 against 131 us at 32768, 4.1 against 1.5 ms at 524288. So small problems, whose norm few
-// sums make up, take three.
+// is up to 1.2e-5 of its norm below 2000 (token, head) pairs, up to 7.2e-6 from there to 8192 and
+// beyond; with three it stays at 4.2e-7. Three planes take up to twice the time at small sizes, 77
+// against 47 us at 2048 pairs, and more at large ones, 303 against 141 us at 32768, 4.1 against
+// 1.5 ms at 524288. Calls whose norm few sums make up take three, up to four times the size
+// where the error is largest; there the call is short, and both times are mostly latency. The rule sees
+// the call alone (a sequence's length is on the device): so a sequence's gradients have the
+// accuracy of the call that it is packed into.
 int planes(int64_t n_tok, int32_t n_heads, bool bf16) {
     return bf16 && n_tok * n_heads >= 8192 ? 2 : 3;
 }

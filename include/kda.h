@@ -544,7 +544,11 @@ kda_status kda_gdr_chunk_fwd(const void *q, const void *k, const void *v, int64_
  * h_final or NULL (zero). dq, dk [n_tok, n_k_heads, d_k] (summed over the value heads that
  * share a key head) and dv [n_tok, n_heads, d_v] in dtype, dg, dbeta [n_tok, n_heads]
  * float32, dh0 like h0 or NULL, all contiguous and fully overwritten. Where g is -inf (or
- * below -200) dg is 0. workspace as above, kda_gdr_chunk_bwd_workspace_bytes() bytes: it
+ * below -200) dg is 0. With KDA_BF16 a call of less than 8192 (token, head) pairs carries its
+ * intermediates in three parts, a larger one in two (float32 gradients to about 4e-7 and 7e-6
+ * of their norm), and the number of sequences, heads and channel blocks decides the order of
+ * some sums: a sequence's gradients are the same in every bit for the same call, but not in
+ * calls that pack it with others. workspace as above, kda_gdr_chunk_bwd_workspace_bytes() bytes: it
  * receives the state and the state gradient of every chunk. Errors as kda_gdr_chunk_fwd.
  */
 size_t kda_gdr_chunk_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_k_heads,

@@ -458,3 +458,31 @@ def test_one_sequence_in_a_graph():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, both()))
     assert kda.read_device_flags() == 0
+
+
+# ---------------------------------------------------------------- many sequences
+
+def many(n):
+    """Empty and short sequences, every fiftieth of more than a chunk."""
+    return [70 if i % 50 == 7 else (1, 0, 3, 2, 5)[i % 5] for i in range(n)]
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("n", [300, 1024, 1100])
+def test_many_sequences(n, dtype):
+    """More sequences than threads of a chain (288), as many as it ranks by length (1024), and more."""
+    x = Inputs(many(n), 1, 2, 16, 16, dtype, seed=n)
+    check_forward(x)
+    check_backward(x)
+
+
+def test_packed_gradients_are_as_accurate_as_the_call():
+    """A sequence alone (three planes) and packed beyond 8192 (token, head) pairs (two): each within
+    its bar, so apart by two bars at most."""
+    x = Inputs([90, 2100], 2, 4, 64, 64, BF, seed=53)
+    packed = kda.gdr_chunk_bwd(*x.args, x.dout, x.dhf)
+    alone = kda.gdr_chunk_bwd(x.q[:90], x.k[:90], x.v[:90], x.g[:90], x.beta[:90], x.h0[:1], None, x.dout[:90],
+                              x.dhf[:1])
+    for a, b in zip(packed, alone):
+        a = a[:len(b)]
+        assert rel_l2(a.double().cpu().numpy(), b.double().cpu().numpy()) <= 2 * bar(a, BF)
