@@ -6,7 +6,9 @@ Like the rest of the package a thin binding of the C ABI in ``include/kda.h``: m
 checks, output and workspace allocation through torch, raw pointers and the current
 stream. Inputs are torch CUDA tensors; q, k, v and the norms' activations may be slices of
 a wider tensor (any stride between tokens, a token's row contiguous), everything else is
-contiguous. The tensors' device has to be the current one. There is no CPU path.
+contiguous. The tensors' device has to be the current one. There is no CPU path. The calls
+record nothing for autograd, whatever their inputs require: a gradient is a call of its own, and
+``examples/gated_delta_block.py`` has the autograd functions that join the two.
 """
 from __future__ import annotations
 

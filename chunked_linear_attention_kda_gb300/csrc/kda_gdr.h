@@ -79,8 +79,8 @@ __device__ __forceinline__ Chunk find_chunk(const int32_t *cu, int n_seq, int64_
     return {lo, left <= 0 ? 0 : left < C ? (int)left : C, t0};
 }
 
-// Per (slot, value head): X and P (NS triangular planes each) and the gate vectors gamma, delta, beta, Gamma (repeated) and the running sum of
-// g log2(e) as pairs of floats. The chains read the first four.
+// Per (slot, value head): X and P (NS triangular planes each) and the gate vectors gamma, delta, beta,
+// Gamma (repeated) and the running sum of g log2(e) as pairs of floats. The chains read the first four.
 constexpr int kGateFloats = 6 * C, kChainGates = 4 * C;
 __host__ __device__ constexpr size_t terms_bytes(int ns) {
     return (size_t)2 * ns * kTri + kGateFloats * 4;
@@ -174,7 +174,8 @@ __device__ __forceinline__ void key_b_t(uint32_t base, int k0, int n0, uint32_t 
 // last. The rest of the offset is tile_off<128>(value channel, c % 64).
 __device__ __forceinline__ int state_half(int c) { return (c >> 6) * 2048; }
 
-// A sum carried as two floats (the fp64 pipe of this part is narrow).
+// A sum carried as two floats (the fp64 pipe of this part is narrow), each addition's error by
+// Knuth's two-sum.
 struct Two { float hi, lo; };
 __device__ __forceinline__ Two add(Two x, Two y) {
     const float s = x.hi + y.hi, t = s - x.hi;

@@ -475,7 +475,8 @@ __device__ __forceinline__ void act_parts(float z, float &s, float &rest) {
     }
 }
 
-// row / n_heads for row < 2^31 as a multiplication: (umulhi(row, m) + row) >> s
+// row / n_heads for row < 2^31 as a multiplication, (umulhi(row, m) + row) >> s: division by an
+// invariant (Granlund and Montgomery, 1994)
 struct HeadDiv { uint32_t m, s; };
 HeadDiv head_div(uint32_t d) {
     uint32_t s = 0;

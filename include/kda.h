@@ -513,7 +513,9 @@ int32_t kda_chunk_fwd_pipeline_plan(const int32_t *host_cu_seqlens, int32_t n_se
  * beta are fp32; with KDA_BF16 the products run on the tensor cores with every operand
  * that is not itself a bf16 input carried in two bf16 parts (about 2^-17 of relative
  * rounding), with KDA_F32 in three (about 2^-24). Results are deterministic. cu_seqlens
- * is read on the device only, as above. Every call of this part launches on the current
+ * is read on the device only, as above. A NaN or an infinity stays in its sequence, but in the
+ * chunked calls it reaches every token of its own chunk of 64, the earlier ones too (0 times NaN in
+ * the triangular products), and all later ones. Every call of this part launches on the current
  * device, which has to hold its memory and own its stream.
  */
 
