@@ -21,9 +21,9 @@
 // that walks over the value heads sharing the key head and adds their dQ and dK in
 // registers (no atomics: the same call gives the same bits).
 //
-// bf16, two sequences of 8K tokens, 16 key and 32 value heads, d_k = d_v = 128: 1.47 ms, of it the
-// terms 0.11, the chains 0.83 (a step is a chain of dependent products, as in the forward; the
-// tensor pipe is active for 52 % of it) and the local gradients 0.52 (2.3 GB at 0.66 of a plain
+// bf16, two sequences of 8K tokens, 16 key and 32 value heads, d_k = d_v = 128: 1.51 ms, of it the
+// terms 0.11, the chains 0.85 (a step is a chain of dependent products, as in the forward; the
+// tensor pipe is active for 50 % of it) and the local gradients 0.56 (2.3 GB at 0.61 of a plain
 // copy's bandwidth).
 #include <cmath>
 
@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(kChainThreads)
 // each warp's 32 and is read as the fragments of mma.sync, so that the pair products B K, B^T Q and
 // F K stay on mma.sync with their operands' scaling in registers; q.k and k.k wait in the other
 // 16 lanes. A head's pair products are added while the next head's slices are multiplied.
-// 16K tokens of 32 heads: 0.52 ms; all on mma.sync 0.95 ms (25 % of issue slots: two warps a
-// scheduler waited for fragments and for each other).
+// 16K tokens of 32 heads: 0.56 ms. With B and F in one plane 0.52; all on mma.sync that took 0.95 (25 %
+// of issue slots: two warps a scheduler waited for fragments and for each other).
 constexpr int kLocalThreads = 256;          // that compute
 constexpr int kCols = kLocalThreads / 128;  // column parts: a warp has 16 tokens x 1 / kCols of the columns
 // The products with S0, dS1 and U run on tcgen05 where operands have one and two planes; three
@@ -767,12 +767,11 @@ cudaError_t backward(const GdrArgs &p, cudaStream_t stream) {
 // Planes of the intermediates. dg sums inner products of states with state gradients, which
 // cancel. Over 110 bf16 problems of 1 to 32 heads and 4 to 2900 tokens its error with two planes
 // is up to 1.2e-5 of its norm below 2000 (token, head) pairs, up to 7.2e-6 from there to 8192 and
-// beyond; with three it stays at 4.2e-7. Three planes take up to twice the time at small sizes, 77
-// against 47 us at 2048 pairs, and more at large ones, 303 against 141 us at 32768, 4.1 against
-// 1.5 ms at 524288. Calls whose norm few sums make up take three, up to four times the size
-// where the error is largest; there the call is short, and both times are mostly latency. The rule sees
-// the call alone (a sequence's length is on the device): so a sequence's gradients have the
-// accuracy of the call that it is packed into.
+// beyond; with three it stays at 4.2e-7. Three planes take about twice the time: 78 against 43 us
+// at 2048 pairs, 281 against 142 us at 32768, 3.53 against 1.51 ms at 524288. Calls whose norm few
+// sums make up take three, up to four times the size below which the error is largest: those are short
+// calls. The rule sees the call alone (a sequence's length is on the device), so a sequence's
+// gradients have the accuracy of the call that it is packed into.
 int planes(int64_t n_tok, int32_t n_heads, bool bf16) {
     return bf16 && n_tok * n_heads >= 8192 ? 2 : 3;
 }

@@ -16,12 +16,12 @@
 // Q, handed to the state warps ahead of their use. With four pairs (the backward pass, when
 // there are more chains than SMs) the state warps do that themselves: a step is longer but
 // covers twice the channels, and each scheduler has two state warps to choose from.
-// Per chunk a state warp issues 158 mma.sync m16n8k16 (bf16, d_k = 128, forward) of 8 cycles each
-// on its scheduler's tensor pipe, and the helper beside it another 72: 1850 cycles bound a step
-// from below. It takes 3400 (64K tokens, 32 heads: 1024 steps in 1.83 ms); the rest is the
-// latency of dependent products (20 cycles each) and of four hand-overs. Measured and dropped:
-// loops over the state's tiles that are not unrolled (3.0 ms), Y begun with the pair's own half
-// before the barrier (1.92 ms).
+// Per chunk the state warps of a pair issue 146 and 170 mma.sync m16n8k16 (bf16, d_k = 128, forward)
+// of 8 cycles each on their schedulers' tensor pipes, and the helper beside each another 94: 2100
+// cycles bound a step from below. It takes 3650 (64K tokens, 32 heads: 1024 steps in 1.97 ms); the rest
+// is the latency of dependent products (20 cycles each) and of four hand-overs. Measured and dropped,
+// against 1.83 ms with S0 and P in one plane in the output: loops over the state's tiles that are not
+// unrolled (3.0 ms), Y begun with the pair's own half before the barrier (1.92 ms).
 #pragma once
 
 #include <cuda.h>
@@ -104,7 +104,7 @@ struct ChainSmem {
     // ring 1
     static constexpr int K = 0, V = K + kKey, X = V + (kRev ? 0 : kVal), Gate1 = X + kX;
     static constexpr int kStage1 = (Gate1 + kGate + 1023) / 1024 * 1024;
-    // As many stages as fit (three planes, 512 tokens of 4 heads, backward: 76 us with two, 84 with
+    // As many stages as fit (three planes, 512 tokens of 4 heads, backward: 77 us with two, 85 with
     // one); for fp32 with d_k above 64 that is one, and a step waits for its chunk's copy.
     static constexpr int N1 = NS == 2 ? (kRev ? 2 : 3) : NI == 1 || DKP == 64 ? 2 : 1;
     // ring 2
@@ -173,9 +173,9 @@ inline unsigned chain_blocks(const GdrArgs &p, int pairs) {
 // Pairs of the backward pass's chains (d_k = d_v = 128). Two pairs end a step sooner (3500 cycles
 // forward, 4600 in reverse, against 4450 and 7800), four cover twice the channels: worth it
 // once the CTAs of two pairs are more than one and a half waves. With 128 CTAs of two pairs
-// (4K tokens, 16 heads) the backward pass takes 256 us with two and 372 with four, with 192
-// (24 heads) 402 and 412, with 256 (2K tokens, 32 heads) 248 and 243, with 512 (two sequences of
-// 8K tokens, 32 heads) 1696 and 1489. The forward pass gains nothing from four: the output would
+// (4K tokens, 16 heads) the backward pass takes 271 us with two and 376 with four, with 192
+// (24 heads) 400 and 424, with 256 (2K tokens, 32 heads) 249 and 250, with 512 (two sequences of
+// 8K tokens, 32 heads) 1697 and 1525. The forward pass gains nothing from four: the output would
 // lengthen its step to over 6500 cycles.
 inline int scan_pairs(const GdrArgs &p) {
     constexpr unsigned kSMs = 152;

@@ -19,9 +19,9 @@
 // halves. That serial path is what bounds the pass: a tcgen05 form pays commit, tensor-memory
 // read, convert, store and fence at each of its hand-offs, and a chunk has four.
 //
-// bf16, d_k = d_v = 128: 64K tokens of 16 key and 32 value heads in one sequence take 2.26 ms, 0.4
-// of it the terms and 1.83 the chains (1024 steps of 64 tokens); 20K tokens of 16 value heads in
-// 12 sequences 0.38 ms. Both are far from the bytes they move (0.24 and 0.05 ms).
+// bf16, d_k = d_v = 128: 64K tokens of 16 key and 32 value heads in one sequence take 2.42 ms, 0.42
+// of it the terms and 1.97 the chains (1024 steps of 64 tokens); 20K tokens of 16 value heads in
+// 12 sequences 0.39 ms. Both are far from the bytes they move (0.24 and 0.05 ms).
 #include <cmath>
 
 #include "kda_gdr_chain.h"
@@ -171,7 +171,7 @@ __device__ __forceinline__ void block_of(int w, int s, int &I, int &J) {
 // One CTA per (chunk, key head): the products K K^T and Q K^T once, then the value heads that share
 // them, two at a time. The inverse is the one serial part; three CTAs an SM cover it and the
 // kernel is bound by instruction issue (0.6 of the slots at 64K tokens of 16 key and 32 value
-// heads, 0.41 ms; two CTAs an SM with the products in registers 0.49 ms).
+// heads, 0.42 ms; two CTAs an SM with the products in registers, P out in one plane: 0.49 ms, three then 0.41).
 template <typename T, int DKP, int NS>
 __global__ void __launch_bounds__(kTermThreads, InputPlanes<T>::N == 1 ? 3 : 1)
     gdr_terms_kernel(const GdrArgs p, const Images im, int values, float scale, bool vec) {
