@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "kda_internal.h"
 #include "kda_ptx.h"
@@ -460,19 +461,12 @@ __device__ __forceinline__ float act(float z) {
 }
 // The sigmoid s and rest = 1 - s, of which act' is formed: s rest, or s (1 + z rest) for silu. rest is
 // exp(-z) s: as a difference it has lost 1e-3 at z = 10 and everything at 17, where s rounds to 1.
+// The bound takes an infinite exp(-z), where s is 0, out of that product.
 template <bool FAST>
 __device__ __forceinline__ void act_parts(float z, float &s, float &rest) {
-    if constexpr (FAST) {  // the bound keeps exp(-z) finite, where the quotient is 0 already; NaN passes
-        float y;
-        asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(-z), "f"(88.f));
-        const float e = __expf(y);
-        s = __fdividef(1.f, 1.f + e);
-        rest = e * s;
-    } else {
-        const float e = expf(-z);
-        s = 1.f / (1.f + e);
-        rest = z > 0.f ? e * s : 1.f - s;
-    }
+    const float e = FAST ? __expf(-z) : expf(-z);
+    s = FAST ? __fdividef(1.f, 1.f + e) : 1.f / (1.f + e);
+    rest = fminf(e, FLT_MAX) * s;
 }
 
 // row / n_heads for row < 2^31 as a multiplication, (umulhi(row, m) + row) >> s: division by an
