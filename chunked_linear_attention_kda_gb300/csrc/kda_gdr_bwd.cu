@@ -22,8 +22,8 @@
 // registers (no atomics: the same call gives the same bits).
 //
 // bf16, two sequences of 8K tokens, 16 key and 32 value heads, d_k = d_v = 128: 1.51 ms, of it the
-// terms 0.11, the chains 0.85 (a step is a chain of dependent products, as in the forward; the
-// tensor pipe is active for 50 % of it) and the local gradients 0.56 (2.3 GB at 0.61 of a plain
+// terms 0.11, the chains 0.83 (a step is a chain of dependent products, as in the forward; the
+// tensor pipe is active for 52 % of it) and the local gradients 0.56 (2.3 GB at 0.61 of a plain
 // copy's bandwidth).
 #include <cmath>
 

@@ -18,7 +18,7 @@
 // covers twice the channels, and each scheduler has two state warps to choose from.
 // Per chunk the state warps of a pair issue 146 and 170 mma.sync m16n8k16 (bf16, d_k = 128, forward)
 // of 8 cycles each on their schedulers' tensor pipes, and the helper beside each another 94: 2100
-// cycles bound a step from below. It takes 3650 (64K tokens, 32 heads: 1024 steps in 1.97 ms); the rest
+// cycles bound a step from below. It takes 3700 (64K tokens, 32 heads: 1024 steps in 1.98 ms); the rest
 // is the latency of dependent products (20 cycles each) and of four hand-overs. Measured and dropped,
 // against 1.83 ms with S0 and P in one plane in the output: loops over the state's tiles that are not
 // unrolled (3.0 ms), Y begun with the pair's own half before the barrier (1.92 ms).
@@ -173,9 +173,9 @@ inline unsigned chain_blocks(const GdrArgs &p, int pairs) {
 // Pairs of the backward pass's chains (d_k = d_v = 128). Two pairs end a step sooner (3500 cycles
 // forward, 4600 in reverse, against 4450 and 7800), four cover twice the channels: worth it
 // once the CTAs of two pairs are more than one and a half waves. With 128 CTAs of two pairs
-// (4K tokens, 16 heads) the backward pass takes 271 us with two and 376 with four, with 192
-// (24 heads) 400 and 424, with 256 (2K tokens, 32 heads) 249 and 250, with 512 (two sequences of
-// 8K tokens, 32 heads) 1697 and 1525. The forward pass gains nothing from four: the output would
+// (4K tokens, 16 heads) the backward pass takes 272 us with two and 371 with four, with 192
+// (24 heads) 403 and 415, with 256 (2K tokens, 32 heads) 249 and 248, with 512 (two sequences of
+// 8K tokens, 32 heads) 1710 and 1501. The forward pass gains nothing from four: the output would
 // lengthen its step to over 6500 cycles.
 inline int scan_pairs(const GdrArgs &p) {
     constexpr unsigned kSMs = 152;

@@ -19,8 +19,8 @@
 // halves. That serial path is what bounds the pass: a tcgen05 form pays commit, tensor-memory
 // read, convert, store and fence at each of its hand-offs, and a chunk has four.
 //
-// bf16, d_k = d_v = 128: 64K tokens of 16 key and 32 value heads in one sequence take 2.42 ms, 0.42
-// of it the terms and 1.97 the chains (1024 steps of 64 tokens); 20K tokens of 16 value heads in
+// bf16, d_k = d_v = 128: 64K tokens of 16 key and 32 value heads in one sequence take 2.43 ms, 0.42
+// of it the terms and 1.98 the chains (1024 steps of 64 tokens); 20K tokens of 16 value heads in
 // 12 sequences 0.39 ms. Both are far from the bytes they move (0.24 and 0.05 ms).
 #include <cmath>
 
