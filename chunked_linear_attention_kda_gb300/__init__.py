@@ -30,6 +30,8 @@ __all__ = ["validate_cu_seqlens", "count_nonfinite", "chunk_fwd", "chunk_fwd_sim
            "chunk_fwd_gated",
            "gdr_chunk_fwd", "gdr_chunk_bwd", "gdr_step", "residual_norm_fwd",
            "residual_norm_bwd", "gated_norm_fwd", "gated_norm_bwd",
+           "dla_chunk_fwd", "dla_chunk_bwd", "dla_step", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
+           "rotary_frequencies",
            "load_library",
            "kernel_launch_count", "read_device_flags", "selftest_bounded_wait",
            "library_path", "KDAError", "EXPORTED_SYMBOLS", "STATUS"]
@@ -53,7 +55,11 @@ EXPORTED_SYMBOLS = ("kda_version", "kda_status_string", "kda_last_error",
                     "kda_gdr_chunk_bwd_workspace_bytes", "kda_gdr_chunk_bwd", "kda_gdr_step",
                     "kda_residual_norm_fwd", "kda_residual_norm_bwd_workspace_bytes",
                     "kda_residual_norm_bwd", "kda_gated_norm_fwd",
-                    "kda_gated_norm_bwd_workspace_bytes", "kda_gated_norm_bwd")
+                    "kda_gated_norm_bwd_workspace_bytes", "kda_gated_norm_bwd",
+                    "kda_dla_chunk_fwd_workspace_bytes", "kda_dla_chunk_fwd",
+                    "kda_dla_chunk_bwd_workspace_bytes", "kda_dla_chunk_bwd", "kda_dla_step",
+                    "kda_qk_norm_rope_fwd", "kda_qk_norm_rope_bwd_workspace_bytes",
+                    "kda_qk_norm_rope_bwd")
 
 _lock = threading.Lock()
 _lib = None
@@ -160,7 +166,16 @@ def load_library(build_if_missing: bool = False) -> ctypes.CDLL:
                 ("kda_residual_norm_bwd", E, [P, I64] * 4 + [P] * 7 + [SZ, I64, I32, F, E, P]),
                 ("kda_gated_norm_fwd", E, [P, I64] * 2 + [P, P, I64, I32, I32, F, I32, E, P]),
                 ("kda_gated_norm_bwd_workspace_bytes", SZ, [I64, I32, I32]),
-                ("kda_gated_norm_bwd", E, [P, I64] * 3 + [P] * 5 + [SZ, I64, I32, I32, F, I32, E, P])):
+                ("kda_gated_norm_bwd", E, [P, I64] * 3 + [P] * 5 + [SZ, I64, I32, I32, F, I32, E, P]),
+                ("kda_dla_chunk_fwd_workspace_bytes", SZ, [I64] + [I32] * 5 + [E]),
+                ("kda_dla_chunk_fwd", E, [P] * 3 + [I64] * 3 + [P, I64, P, P, F] + [P] * 3 + [SZ, I64] + [I32] * 5 + [E, P]),
+                ("kda_dla_chunk_bwd_workspace_bytes", SZ, [I64] + [I32] * 5 + [E]),
+                ("kda_dla_chunk_bwd", E, [P] * 3 + [I64] * 3 + [P, I64, P, P, F] + [P] * 8 + [SZ, I64] + [I32] * 5 + [E, P]),
+                ("kda_dla_step", E, [P] * 3 + [I64] * 3 + [P, I64, P, P, F, P] + [I32] * 6 + [E, P]),
+                ("kda_qk_norm_rope_fwd", E, [P, I64] * 2 + [P] * 3 + [I32, P, I32, P, P, I64] + [I32] * 3 + [F, I32, E, P]),
+                ("kda_qk_norm_rope_bwd_workspace_bytes", SZ, [I64, I32]),
+                ("kda_qk_norm_rope_bwd", E, [P, I64] * 4 + [P] * 3 + [I32, P, I32] + [P] * 5 + [SZ, I64] + [I32] * 3 +
+                 [F, I32, E, P])):
             fn = getattr(lib, name)
             fn.restype, fn.argtypes = res, args
         _lib = lib
@@ -721,7 +736,8 @@ def segmented_fwd(q, k, v, gate_logits, beta, h0=None, cu_seqlens=None, *, segme
 # block.py imports torch, which this package leaves to the calls: it is loaded at the first use of
 # one of its names.
 _BLOCK = ("gdr_chunk_fwd", "gdr_chunk_bwd", "gdr_step", "residual_norm_fwd", "residual_norm_bwd",
-          "gated_norm_fwd", "gated_norm_bwd")
+          "gated_norm_fwd", "gated_norm_bwd", "dla_chunk_fwd", "dla_chunk_bwd", "dla_step",
+          "qk_norm_rope_fwd", "qk_norm_rope_bwd", "rotary_frequencies")
 
 
 def __getattr__(name):

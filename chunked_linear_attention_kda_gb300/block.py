@@ -1,6 +1,7 @@
-"""The operators of a block around the gated delta rule with one decay per head: the
-recurrence itself (chunked forward, one-token step over a pool of states), the residual
-norm before a block and the gated norm after the recurrence, with their backward passes.
+"""The operators of a block around the recurrences with one decay per head, the gated delta rule
+and linear attention: the recurrence itself (chunked forward, one-token step over a pool of
+states), the residual norm before a block, the norm of queries and keys with the position
+rotation, and the gated norm after the recurrence, with their backward passes.
 
 Like the rest of the package a thin binding of the C ABI in ``include/kda.h``: metadata
 checks, output and workspace allocation through torch, raw pointers and the current
@@ -337,3 +338,178 @@ def gated_norm_bwd(dy, x, gate, weight, *, eps=1e-6, activation="sigmoid", works
         _p(workspace), workspace.numel() * workspace.element_size(), n, h, d, eps,
         ACTIVATIONS[activation], _CODE[x.dtype], stream))
     return dx, dgate, dw
+
+
+def _scale(scale, dk):
+    return dk ** -0.5 if scale is None else float(scale)
+
+
+def _dla_inputs(q, k, v, g, dev):
+    """Sizes and strides; g's stride is 0 for one decay per head."""
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q and k must be [N, H_k, d_k], v [N, H, d_v] (packed, token-major)")
+    shape = q.shape
+    n, hk, dk = shape
+    _, h, dv = v.shape
+    if hk == 0 or h % hk != 0:
+        raise ValueError(f"v's {h} heads must be a multiple of q's {hk}")
+    dtype, gs = q.dtype, h if g.dim() == 2 else 0
+    # the usual call: everything as it should be, without a function call for each tensor
+    if (k.shape == shape and v.shape[0] == n and k.dtype is dtype and v.dtype is dtype and
+            g.dtype is _F32 and g.shape == ((n, h) if gs else (h,)) and k.get_device() == dev and
+            v.get_device() == dev and g.get_device() == dev and q.is_contiguous() and
+            k.is_contiguous() and v.is_contiguous() and g.is_contiguous()):
+        return n, hk, h, dk, dv, (hk * dk, hk * dk, h * dv), gs
+    strides = (_rows("q", q, shape, dtype, dev), _rows("k", k, shape, dtype, dev),
+               _rows("v", v, (n, h, dv), dtype, dev))
+    _flat("g", g, (n, h) if gs else (h,), _F32, dev)
+    return n, hk, h, dk, dv, strides, gs
+
+
+def dla_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, *, scale=None, out=None, h_final=None,
+                  output_final_state=True, workspace=None):
+    """Chunked forward of linear attention with one log-decay ``g`` per head, ``S = exp(g) S + k
+    v^T``, ``o = scale S^T q``, through ``kda_dla_chunk_fwd``. ``q, k`` [N, H_k, d_k], ``v`` [N, H,
+    d_v] (H a multiple of H_k; bf16 or fp32), ``g`` fp32 [N, H] (per token) or [H] (the same for
+    every token), ``h0`` [n_seq, H, d_k, d_v] fp32 or None, ``cu_seqlens`` int32 [n_seq + 1] (None:
+    one sequence), ``scale`` a number (None: d_k ** -0.5). Returns ``(out, h_final)``, the latter
+    None when ``output_final_state`` is False."""
+    lib, stream, dev = _start(q, "dla_chunk_fwd")
+    n, hk, h, dk, dv, strides, gs = _dla_inputs(q, k, v, g, dev)
+    n_seq, cu_seqlens = _sequences(q, dev, n, h, dk, dv, h0, cu_seqlens)
+    if out is None:
+        out = _empty((n, h, dv), q.dtype, dev)
+    else:
+        _flat("out", out, (n, h, dv), q.dtype, dev)
+    if h_final is not None:
+        _flat("h_final", h_final, (n_seq, h, dk, dv), _F32, dev)
+    elif output_final_state:
+        h_final = _empty((n_seq, h, dk, dv), torch.float32, dev)
+    code = _CODE[q.dtype]
+    workspace = _workspace(workspace, dev, "kda_dla_chunk_fwd_workspace_bytes", n, n_seq, hk, h, dk, dv, code)
+    _done(lib, lib.kda_dla_chunk_fwd(
+        _p(q), _p(k), _p(v), *strides, _p(g), gs, _p(h0), _p(cu_seqlens), _scale(scale, dk), _p(out),
+        _p(h_final), _p(workspace), workspace.numel() * workspace.element_size(), n, n_seq, hk,
+        h, dk, dv, code, stream))
+    return out, h_final
+
+
+def dla_chunk_bwd(q, k, v, g, h0, cu_seqlens, dout, dh_final=None, *, scale=None, want_dg=True,
+                  want_dh0=True, workspace=None):
+    """Backward of ``dla_chunk_fwd`` through ``kda_dla_chunk_bwd``: the gradients of ``<dout, out> +
+    <dh_final, h_final>``. Returns ``(dq, dk, dv, dg, dh0)``: ``dq`` and ``dk`` are summed over the
+    value heads of a key head, ``dg`` has g's shape (None unless ``want_dg``: decays that are not
+    trained), ``dh0`` is None unless ``want_dh0``."""
+    lib, stream, dev = _start(q, "dla_chunk_bwd")
+    n, hk, h, dk, dv, strides, gs = _dla_inputs(q, k, v, g, dev)
+    n_seq, cu_seqlens = _sequences(q, dev, n, h, dk, dv, h0, cu_seqlens)
+    _flat("dout", dout, (n, h, dv), q.dtype, dev)
+    if dh_final is not None:
+        _flat("dh_final", dh_final, (n_seq, h, dk, dv), _F32, dev)
+    grads = (_empty((n, hk, dk), q.dtype, dev),
+             _empty((n, hk, dk), q.dtype, dev),
+             _empty((n, h, dv), q.dtype, dev),
+             _empty((n, h) if gs else (h,), torch.float32, dev) if want_dg else None,
+             _empty((n_seq, h, dk, dv), torch.float32, dev) if want_dh0 else None)
+    code = _CODE[q.dtype]
+    workspace = _workspace(workspace, dev, "kda_dla_chunk_bwd_workspace_bytes", n, n_seq, hk, h, dk, dv, code)
+    _done(lib, lib.kda_dla_chunk_bwd(
+        _p(q), _p(k), _p(v), *strides, _p(g), gs, _p(h0), _p(cu_seqlens), _scale(scale, dk), _p(dout),
+        _p(dh_final), *[_p(t) for t in grads], _p(workspace),
+        workspace.numel() * workspace.element_size(), n, n_seq, hk, h, dk, dv, code, stream))
+    return grads
+
+
+def dla_step(q, k, v, g, state, slots=None, *, scale=None, out=None):
+    """One token per row through ``kda_dla_step``: row b updates ``state[slots[b]]`` in place
+    (``state`` [n_slots, H, d_k, d_v] fp32; ``slots`` int32 [B], None: row b has state b). A
+    slot outside the pool marks a padded row: its output is 0. The other tensors as for
+    ``dla_chunk_fwd`` with B tokens. Returns ``out`` [B, H, d_v]."""
+    lib, stream, dev = _start(q, "dla_step")
+    n, hk, h, dk, dv, strides, gs = _dla_inputs(q, k, v, g, dev)
+    _flat("state", state, (state.shape[0], h, dk, dv), _F32, dev)
+    if slots is not None:
+        _flat("slots", slots, (n,), _I32, dev)
+    if out is None:
+        out = _empty((n, h, dv), q.dtype, dev)
+    else:
+        _flat("out", out, (n, h, dv), q.dtype, dev)
+    status = lib.kda_dla_step(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides, g.data_ptr(), gs, state.data_ptr(),
+        None if slots is None else slots.data_ptr(), _scale(scale, dk), out.data_ptr(), n,
+        state.shape[0], hk, h, dk, dv, _CODE[q.dtype], stream)
+    if status:
+        _kda._check(lib, status)
+    return out
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, device="cuda"):
+    """The angles per position of ``rotary_dim`` rotated channels, ``base ** (-2 i / rotary_dim)``,
+    as ``qk_norm_rope_fwd`` takes them: fp64 [rotary_dim / 2]."""
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even")
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+    return base ** (-2 * i / max(rotary_dim, 1))
+
+
+def _qk_inputs(q, k, q_weight, k_weight, positions, freqs, dev):
+    """Sizes, the strides of q and k, the size of a position and the number of frequencies."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [N, H_q, d], k [N, H_k, d]")
+    n, hq, d = q.shape
+    hk, dtype = k.shape[1], q.dtype
+    strides = (_rows("q", q, q.shape, dtype, dev), _rows("k", k, (n, hk, d), dtype, dev))
+    _flat("q_weight", q_weight, (d,), _F32, dev)
+    _flat("k_weight", k_weight, (d,), _F32, dev)
+    if (positions is None) != (freqs is None):
+        raise ValueError("positions and freqs go together")
+    if freqs is None:
+        return n, hq, hk, d, strides, 4, 0
+    if freqs.dim() != 1 or 2 * freqs.shape[0] > d:
+        raise ValueError("freqs must be [R] with 2 R <= d")
+    _flat("freqs", freqs, freqs.shape, torch.float64, dev)
+    size = 8 if positions.dtype is torch.int64 else 4
+    _flat("positions", positions, (n,), torch.int64 if size == 8 else _I32, dev)
+    return n, hq, hk, d, strides, size, freqs.shape[0]
+
+
+def qk_norm_rope_fwd(q, k, q_weight, k_weight, positions=None, freqs=None, *, eps=1e-6,
+                     interleaved=False, q_out=None, k_out=None):
+    """Norm per head and rotation of queries and keys through ``kda_qk_norm_rope_fwd``: ``weight *
+    x / sqrt(mean(x^2) + eps)`` over the channels of each token and head, then pair i of the first 2 R
+    channels turned by ``positions[t] * freqs[i]``. ``q`` [N, H_q, d], ``k`` [N, H_k, d] bf16 or
+    fp32 (slices of one projection), weights [d] fp32, ``positions`` int32 or int64 [N], ``freqs``
+    fp64 [R] (``rotary_frequencies``; both None: no rotation). Pairs are channels i and R + i, or 2
+    i and 2 i + 1 when ``interleaved``. Returns ``(q_out, k_out)``, contiguous."""
+    lib, stream, dev = _start(q, "qk_norm_rope_fwd")
+    n, hq, hk, d, strides, size, n_freqs = _qk_inputs(q, k, q_weight, k_weight, positions, freqs, dev)
+    if q_out is None:
+        q_out = _empty((n, hq, d), q.dtype, dev)
+    else:
+        _flat("q_out", q_out, (n, hq, d), q.dtype, dev)
+    if k_out is None:
+        k_out = _empty((n, hk, d), q.dtype, dev)
+    else:
+        _flat("k_out", k_out, (n, hk, d), q.dtype, dev)
+    _done(lib, lib.kda_qk_norm_rope_fwd(
+        _p(q), strides[0], _p(k), strides[1], _p(q_weight), _p(k_weight), _p(positions), size, _p(freqs),
+        n_freqs, _p(q_out), _p(k_out), n, hq, hk, d, eps, interleaved, _CODE[q.dtype], stream))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions=None, freqs=None, *,
+                     eps=1e-6, interleaved=False, workspace=None):
+    """Gradients of ``qk_norm_rope_fwd`` through ``kda_qk_norm_rope_bwd`` from its inputs: ``(dq, dk,
+    dq_weight, dk_weight)``."""
+    lib, stream, dev = _start(q, "qk_norm_rope_bwd")
+    n, hq, hk, d, strides, size, n_freqs = _qk_inputs(q, k, q_weight, k_weight, positions, freqs, dev)
+    dys = (_rows("dq_out", dq_out, q.shape, q.dtype, dev), _rows("dk_out", dk_out, k.shape, q.dtype, dev))
+    dq, dk = _empty((n, hq, d), q.dtype, dev), _empty((n, hk, d), q.dtype, dev)
+    dwq, dwk = _empty((d,), _F32, dev), _empty((d,), _F32, dev)
+    workspace = _workspace(workspace, dev, "kda_qk_norm_rope_bwd_workspace_bytes", n, d)
+    _done(lib, lib.kda_qk_norm_rope_bwd(
+        _p(dq_out), dys[0], _p(dk_out), dys[1], _p(q), strides[0], _p(k), strides[1], _p(q_weight),
+        _p(k_weight), _p(positions), size, _p(freqs), n_freqs, _p(dq), _p(dk), _p(dwq), _p(dwk),
+        _p(workspace), workspace.numel() * workspace.element_size(), n, hq, hk, d, eps, interleaved,
+        _CODE[q.dtype], stream))
+    return dq, dk, dwq, dwk

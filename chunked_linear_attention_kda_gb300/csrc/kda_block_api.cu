@@ -1,7 +1,10 @@
 // kda_block_api.cu -- the C ABI of the operators around and beside the bounded recurrence:
-// the gated delta rule with one decay per head and the norms before and after a block.
+// the gated delta rule and linear attention with one decay per head, the norms before and after a
+// block and the norm of queries and keys with the position rotation.
 // Argument validation and launch; no arithmetic.
 #include <cuda_runtime.h>
+
+#include <cfloat>
 
 #include "kda_api.h"
 #include "kda_internal.h"
@@ -202,6 +205,255 @@ kda_status kda_gdr_step(const void *q, const void *k, const void *v, int64_t q_s
     kda::GdrStepArgs p{q, k, v, q_stride, k_stride, v_stride, g, beta, state, slots, out, n_rows, n_slots,
                        n_k_heads, n_heads, d_k, d_v, dtype == KDA_BF16};
     return launched(kda::launch_gdr_step(p, (cudaStream_t)stream), "gated delta rule step launch");
+}
+
+// ---------------------------------------------------------------- linear attention, one decay per head
+
+static kda_status check_dla(const kda::DlaArgs &p, int dtype) {
+    kda_status s = check_heads(p.n_k_heads, p.n_heads, p.d_k, p.d_v, dtype);
+    if (s != KDA_OK) return s;
+    if (p.n_heads > 65535) return api_fail(KDA_ERR_UNSUPPORTED, "n_heads above 65535");
+    if (p.n_tok < 0 || p.n_seq < 0) return api_fail(KDA_ERR_INVALID_ARG, "n_tok and n_seq must be >= 0");
+    if (p.n_tok > 0x7fffffffLL) return api_fail(KDA_ERR_UNSUPPORTED, "n_tok above 2^31 - 1");
+    if (p.n_tok > 0 && p.n_seq == 0) return api_fail(KDA_ERR_INVALID_ARG, "n_tok > 0 needs at least one sequence");
+    if ((int64_t)p.n_seq * p.n_heads > 0x7fffffffLL / 8)
+        return api_fail(KDA_ERR_INVALID_ARG, "n_seq * n_heads exceeds 2^28");
+    // a grid of a CTA for every chunk or segment and head
+    if ((p.n_tok / 64 + p.n_seq) * (int64_t)p.n_heads > 0x7fffffffLL)
+        return api_fail(KDA_ERR_UNSUPPORTED, "(n_tok / 64 + n_seq) * n_heads above 2^31 - 1");
+    if (p.n_seq > 0 && !p.cu_seqlens) return api_fail(KDA_ERR_INVALID_ARG, "cu_seqlens is NULL");
+    if (p.n_tok > 0 && (!p.q || !p.k || !p.v || !p.g))
+        return api_fail(KDA_ERR_INVALID_ARG, "q, k, v and g are required");
+    if (p.g_stride != 0 && p.g_stride != p.n_heads)
+        return api_fail(KDA_ERR_INVALID_ARG, "g_stride must be n_heads (a decay per token) or 0 (one per head)");
+    if (!(p.scale == p.scale) || p.scale > FLT_MAX || p.scale < -FLT_MAX)
+        return api_fail(KDA_ERR_INVALID_ARG, "scale must be finite");
+    const int64_t wk = (int64_t)p.n_k_heads * p.d_k, wv = (int64_t)p.n_heads * p.d_v;
+    if (p.q_stride < wk || p.k_stride < wk || p.v_stride < wv)
+        return api_fail(KDA_ERR_INVALID_ARG, "a token stride is smaller than a token's row");
+    const size_t es = dtype == KDA_BF16 ? 2 : 4;
+    const void *elems[] = {p.q, p.k, p.v, p.out, p.dout, p.dq, p.dk, p.dv};
+    for (const void *x : elems)
+        if (misaligned(x, es)) return api_fail(KDA_ERR_INVALID_ARG, "q, k, v, out and their gradients must be aligned to their element size");
+    const void *f32[] = {p.g, p.h0, p.cu_seqlens, p.h_final, p.dh_final, p.dg, p.dh0};
+    for (const void *x : f32)
+        if (misaligned(x, 4)) return api_fail(KDA_ERR_INVALID_ARG, "g, cu_seqlens, the states and their gradients must be 4-byte aligned");
+    return KDA_OK;
+}
+
+static kda::DlaArgs dla_args(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, const float *g, int64_t g_stride, const float *h0, const int32_t *cu,
+                             float scale, void *workspace, int64_t n_tok, int32_t n_seq, int32_t n_k_heads,
+                             int32_t n_heads, int32_t d_k, int32_t d_v, kda_dtype dtype) {
+    kda::DlaArgs p{};
+    p.q = q; p.k = k; p.v = v;
+    p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
+    p.g = g; p.g_stride = g_stride; p.h0 = h0; p.cu_seqlens = cu; p.scale = scale; p.workspace = workspace;
+    p.n_tok = n_tok; p.n_seq = n_seq; p.n_k_heads = n_k_heads; p.n_heads = n_heads;
+    p.d_k = d_k; p.d_v = d_v; p.bf16 = dtype == KDA_BF16;
+    return p;
+}
+static Range dla_decays(const float *g, const kda::DlaArgs &p) {
+    return {g, (size_t)(p.g_stride ? p.n_tok : 1) * p.n_heads * 4};
+}
+
+size_t kda_dla_chunk_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_k_heads, int32_t n_heads,
+                                         int32_t d_k, int32_t d_v, kda_dtype dtype) {
+    if (!gdr_sizes(n_tok, n_seq, n_k_heads, n_heads, d_k, d_v)) return 0;
+    return kda::dla_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v, dtype == KDA_BF16, false);
+}
+
+kda_status kda_dla_chunk_fwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, const float *g, int64_t g_stride, const float *h0,
+                             const int32_t *cu_seqlens, float scale, void *out, float *h_final, void *workspace,
+                             size_t workspace_bytes, int64_t n_tok, int32_t n_seq, int32_t n_k_heads,
+                             int32_t n_heads, int32_t d_k, int32_t d_v, kda_dtype dtype, void *stream) {
+    kda::DlaArgs p = dla_args(q, k, v, q_stride, k_stride, v_stride, g, g_stride, h0, cu_seqlens, scale, workspace,
+                              n_tok, n_seq, n_k_heads, n_heads, d_k, d_v, dtype);
+    p.out = out;
+    p.h_final = h_final;
+    kda_status s = check_dla(p, dtype);
+    if (s != KDA_OK) return s;
+    if (n_tok > 0 && !out) return api_fail(KDA_ERR_INVALID_ARG, "out is required");
+    if (n_seq == 0) return api_ok();
+    const size_t need = n_tok ? kda::dla_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v, p.bf16, false) : 0;
+    s = check_workspace(workspace, workspace_bytes, need);
+    if (s != KDA_OK) return s;
+    const size_t es = p.bf16 ? 2 : 4, st = (size_t)n_seq * n_heads * d_k * d_v * 4;
+    const int64_t wk = (int64_t)n_k_heads * d_k, wv = (int64_t)n_heads * d_v;
+    const Range ins[] = {rows(q, n_tok, q_stride, wk, es), rows(k, n_tok, k_stride, wk, es),
+                         rows(v, n_tok, v_stride, wv, es), dla_decays(g, p), {h0, st},
+                         {cu_seqlens, (size_t)(n_seq + 1) * 4}};
+    const Range outs[] = {rows(out, n_tok, wv, wv, es), {h_final, st}, {workspace, need}};
+    if (clash(ins, outs)) return api_fail(KDA_ERR_INVALID_ARG, kOverlap);
+    return launched(kda::launch_dla_fwd(p, (cudaStream_t)stream), "linear attention forward launch");
+}
+
+size_t kda_dla_chunk_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_k_heads, int32_t n_heads,
+                                         int32_t d_k, int32_t d_v, kda_dtype dtype) {
+    if (!gdr_sizes(n_tok, n_seq, n_k_heads, n_heads, d_k, d_v)) return 0;
+    return kda::dla_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v, dtype == KDA_BF16, true);
+}
+
+kda_status kda_dla_chunk_bwd(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, const float *g, int64_t g_stride, const float *h0,
+                             const int32_t *cu_seqlens, float scale, const void *dout, const float *dh_final,
+                             void *dq, void *dk, void *dv, float *dg, float *dh0, void *workspace,
+                             size_t workspace_bytes, int64_t n_tok, int32_t n_seq, int32_t n_k_heads,
+                             int32_t n_heads, int32_t d_k, int32_t d_v, kda_dtype dtype, void *stream) {
+    kda::DlaArgs p = dla_args(q, k, v, q_stride, k_stride, v_stride, g, g_stride, h0, cu_seqlens, scale, workspace,
+                              n_tok, n_seq, n_k_heads, n_heads, d_k, d_v, dtype);
+    p.dout = dout; p.dh_final = dh_final;
+    p.dq = dq; p.dk = dk; p.dv = dv; p.dg = dg; p.dh0 = dh0;
+    kda_status s = check_dla(p, dtype);
+    if (s != KDA_OK) return s;
+    if (n_tok > 0 && (!dout || !dq || !dk || !dv))
+        return api_fail(KDA_ERR_INVALID_ARG, "dout, dq, dk and dv are required");
+    if (n_seq == 0 && !(dg && g_stride == 0)) return api_ok();  // one sum per head is 0 even so
+    const size_t need = n_tok ? kda::dla_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v, p.bf16, true) : 0;
+    s = check_workspace(workspace, workspace_bytes, need);
+    if (s != KDA_OK) return s;
+    const size_t es = p.bf16 ? 2 : 4, st = (size_t)n_seq * n_heads * d_k * d_v * 4;
+    const int64_t wk = (int64_t)n_k_heads * d_k, wv = (int64_t)n_heads * d_v;
+    const Range ins[] = {rows(q, n_tok, q_stride, wk, es), rows(k, n_tok, k_stride, wk, es),
+                         rows(v, n_tok, v_stride, wv, es), dla_decays(g, p), {h0, st},
+                         {cu_seqlens, (size_t)(n_seq + 1) * 4}, rows(dout, n_tok, wv, wv, es), {dh_final, st}};
+    const Range outs[] = {rows(dq, n_tok, wk, wk, es), rows(dk, n_tok, wk, wk, es), rows(dv, n_tok, wv, wv, es),
+                          dla_decays(dg, p), {dh0, st}, {workspace, need}};
+    if (clash(ins, outs)) return api_fail(KDA_ERR_INVALID_ARG, kOverlap);
+    return launched(kda::launch_dla_bwd(p, (cudaStream_t)stream), "linear attention backward launch");
+}
+
+kda_status kda_dla_step(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                        int64_t v_stride, const float *g, int64_t g_stride, float *state, const int32_t *slots,
+                        float scale, void *out, int32_t n_rows, int32_t n_slots, int32_t n_k_heads, int32_t n_heads,
+                        int32_t d_k, int32_t d_v, kda_dtype dtype, void *stream) {
+    kda_status s = check_heads(n_k_heads, n_heads, d_k, d_v, dtype);
+    if (s != KDA_OK) return s;
+    if (n_rows < 0 || n_slots < 0) return api_fail(KDA_ERR_INVALID_ARG, "n_rows and n_slots must be >= 0");
+    if (!slots && n_rows > n_slots) return api_fail(KDA_ERR_INVALID_ARG, "without slots every row needs its state");
+    if ((int64_t)n_rows * n_heads > 0x7fffffffLL / 4)
+        return api_fail(KDA_ERR_INVALID_ARG, "n_rows * n_heads exceeds 2^29");
+    if (g_stride != 0 && g_stride != n_heads)
+        return api_fail(KDA_ERR_INVALID_ARG, "g_stride must be n_heads (a decay per row) or 0 (one per head)");
+    if (!(scale == scale) || scale > FLT_MAX || scale < -FLT_MAX)
+        return api_fail(KDA_ERR_INVALID_ARG, "scale must be finite");
+    if (n_rows == 0) return api_ok();
+    if (!q || !k || !v || !g || !out || (!state && n_slots > 0))
+        return api_fail(KDA_ERR_INVALID_ARG, "every pointer but slots is required");
+    const int64_t wk = (int64_t)n_k_heads * d_k, wv = (int64_t)n_heads * d_v;
+    if (q_stride < wk || k_stride < wk || v_stride < wv)
+        return api_fail(KDA_ERR_INVALID_ARG, "a token stride is smaller than a token's row");
+    const size_t es = dtype == KDA_BF16 ? 2 : 4;
+    if (misaligned(q, es) || misaligned(k, es) || misaligned(v, es) || misaligned(out, es))
+        return api_fail(KDA_ERR_INVALID_ARG, "q, k, v and out must be aligned to their element size");
+    if (misaligned(g, 4) || misaligned(state, 4) || misaligned(slots, 4))
+        return api_fail(KDA_ERR_INVALID_ARG, "g, state and slots must be 4-byte aligned");
+    const Range ins[] = {rows(q, n_rows, q_stride, wk, es), rows(k, n_rows, k_stride, wk, es),
+                         rows(v, n_rows, v_stride, wv, es), {g, (size_t)(g_stride ? n_rows : 1) * n_heads * 4},
+                         {slots, (size_t)n_rows * 4}};
+    const Range outs[] = {rows(out, n_rows, wv, wv, es), {state, (size_t)n_slots * n_heads * d_k * d_v * 4}};
+    if (clash(ins, outs)) return api_fail(KDA_ERR_INVALID_ARG, kOverlap);
+    kda::DlaStepArgs p{q, k, v, q_stride, k_stride, v_stride, g, g_stride, state, slots, scale, out, n_rows, n_slots,
+                       n_k_heads, n_heads, d_k, d_v, dtype == KDA_BF16};
+    return launched(kda::launch_dla_step(p, (cudaStream_t)stream), "linear attention step launch");
+}
+
+// ---------------------------------------------------------------- queries and keys
+
+static kda_status check_qk_norm(const kda::QkNormArgs &p, int dtype) {
+    if (dtype != KDA_F32 && dtype != KDA_BF16)
+        return api_fail(KDA_ERR_UNSUPPORTED, "dtype must be KDA_F32 or KDA_BF16");
+    if (p.n_tok < 0 || p.heads[0] <= 0 || p.heads[1] <= 0 || p.d <= 0)
+        return api_fail(KDA_ERR_INVALID_ARG, "n_tok must be >= 0, the head counts and d positive");
+    if (p.d > 256) return api_fail(KDA_ERR_UNSUPPORTED, "d above 256 is not built");
+    if (p.heads[0] > 32768 || p.heads[1] > 32768) return api_fail(KDA_ERR_UNSUPPORTED, "more than 32768 heads");
+    if (p.n_tok > 0x7fffffffLL) return api_fail(KDA_ERR_UNSUPPORTED, "n_tok above 2^31 - 1");
+    if (p.n_freqs < 0 || 2 * (int64_t)p.n_freqs > p.d)
+        return api_fail(KDA_ERR_INVALID_ARG, "n_freqs must be from 0 to d / 2");
+    if (!(p.eps > 0.f)) return api_fail(KDA_ERR_INVALID_ARG, "eps must be positive");
+    if (!p.weight[0] || !p.weight[1]) return api_fail(KDA_ERR_INVALID_ARG, "the weights are required");
+    if (p.n_tok > 0 && (!p.x[0] || !p.x[1] || !p.y[0] || !p.y[1]))
+        return api_fail(KDA_ERR_INVALID_ARG, "q, k and their results are required");
+    if (p.n_tok > 0 && p.n_freqs > 0 && (!p.positions || !p.freqs))
+        return api_fail(KDA_ERR_INVALID_ARG, "positions and freqs are required with n_freqs > 0");
+    const size_t es = dtype == KDA_BF16 ? 2 : 4;
+    for (int i = 0; i < 2; ++i) {
+        if (p.stride[i] < (int64_t)p.heads[i] * p.d || p.dy_stride[i] < (int64_t)p.heads[i] * p.d)
+            return api_fail(KDA_ERR_INVALID_ARG, "a token stride is smaller than a token's row");
+        if (misaligned(p.x[i], es) || misaligned(p.dy[i], es) || misaligned(p.y[i], es) ||
+            misaligned(p.weight[i], 4) || misaligned(p.dw[i], 4))
+            return api_fail(KDA_ERR_INVALID_ARG, "every tensor must be aligned to its element size");
+    }
+    if (misaligned(p.positions, p.wide_positions ? 8 : 4) || misaligned(p.freqs, 8))
+        return api_fail(KDA_ERR_INVALID_ARG, "positions and freqs must be aligned to their element size");
+    return KDA_OK;
+}
+
+kda_status kda_qk_norm_rope_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                const float *q_weight, const float *k_weight, const void *positions,
+                                int32_t position_bytes, const double *freqs, int32_t n_freqs, void *q_out,
+                                void *k_out, int64_t n_tok, int32_t n_q_heads, int32_t n_k_heads, int32_t d,
+                                float eps, int32_t interleaved, kda_dtype dtype, void *stream) {
+    if (position_bytes != 4 && position_bytes != 8)
+        return api_fail(KDA_ERR_INVALID_ARG, "position_bytes must be 4 or 8");
+    kda::QkNormArgs p{};
+    p.x[0] = q; p.x[1] = k; p.stride[0] = p.dy_stride[0] = q_stride; p.stride[1] = p.dy_stride[1] = k_stride;
+    p.weight[0] = q_weight; p.weight[1] = k_weight; p.y[0] = q_out; p.y[1] = k_out;
+    p.positions = positions; p.freqs = freqs; p.n_freqs = n_freqs; p.wide_positions = position_bytes == 8;
+    p.n_tok = n_tok; p.heads[0] = n_q_heads; p.heads[1] = n_k_heads; p.d = d; p.eps = eps;
+    p.interleaved = interleaved != 0; p.bf16 = dtype == KDA_BF16;
+    kda_status s = check_qk_norm(p, dtype);
+    if (s != KDA_OK) return s;
+    if (n_tok == 0) return api_ok();
+    const size_t es = p.bf16 ? 2 : 4;
+    const int64_t wq = (int64_t)n_q_heads * d, wk = (int64_t)n_k_heads * d;
+    const Range ins[] = {rows(q, n_tok, q_stride, wq, es), rows(k, n_tok, k_stride, wk, es), {q_weight, (size_t)d * 4},
+                         {k_weight, (size_t)d * 4}, {positions, (size_t)n_tok * position_bytes}, {freqs, (size_t)n_freqs * 8}};
+    const Range outs[] = {rows(q_out, n_tok, wq, wq, es), rows(k_out, n_tok, wk, wk, es)};
+    if (clash(ins, outs)) return api_fail(KDA_ERR_INVALID_ARG, kOverlap);
+    return launched(kda::launch_qk_norm(p, false, (cudaStream_t)stream), "query and key norm launch");
+}
+
+size_t kda_qk_norm_rope_bwd_workspace_bytes(int64_t n_tok, int32_t d) {
+    if (n_tok < 0 || d <= 0 || d > 256) return 0;
+    return kda::qk_norm_workspace_bytes(n_tok, d);
+}
+
+kda_status kda_qk_norm_rope_bwd(const void *dq_out, int64_t dq_out_stride, const void *dk_out, int64_t dk_out_stride,
+                                const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                const float *q_weight, const float *k_weight, const void *positions,
+                                int32_t position_bytes, const double *freqs, int32_t n_freqs, void *dq, void *dk,
+                                float *dq_weight, float *dk_weight, void *workspace, size_t workspace_bytes,
+                                int64_t n_tok, int32_t n_q_heads, int32_t n_k_heads, int32_t d, float eps,
+                                int32_t interleaved, kda_dtype dtype, void *stream) {
+    if (position_bytes != 4 && position_bytes != 8)
+        return api_fail(KDA_ERR_INVALID_ARG, "position_bytes must be 4 or 8");
+    kda::QkNormArgs p{};
+    p.x[0] = q; p.x[1] = k; p.stride[0] = q_stride; p.stride[1] = k_stride;
+    p.dy[0] = dq_out; p.dy[1] = dk_out; p.dy_stride[0] = dq_out_stride; p.dy_stride[1] = dk_out_stride;
+    p.weight[0] = q_weight; p.weight[1] = k_weight; p.y[0] = dq; p.y[1] = dk; p.dw[0] = dq_weight; p.dw[1] = dk_weight;
+    p.partial = static_cast<float *>(workspace);
+    p.positions = positions; p.freqs = freqs; p.n_freqs = n_freqs; p.wide_positions = position_bytes == 8;
+    p.n_tok = n_tok; p.heads[0] = n_q_heads; p.heads[1] = n_k_heads; p.d = d; p.eps = eps;
+    p.interleaved = interleaved != 0; p.bf16 = dtype == KDA_BF16;
+    kda_status s = check_qk_norm(p, dtype);
+    if (s != KDA_OK) return s;
+    if (!dq_weight || !dk_weight) return api_fail(KDA_ERR_INVALID_ARG, "the weights' gradients are required");
+    if (n_tok > 0 && (!dq_out || !dk_out)) return api_fail(KDA_ERR_INVALID_ARG, "dq_out and dk_out are required");
+    const size_t need = kda::qk_norm_workspace_bytes(n_tok, d);
+    s = check_workspace(workspace, workspace_bytes, need);
+    if (s != KDA_OK) return s;
+    const size_t es = p.bf16 ? 2 : 4;
+    const int64_t wq = (int64_t)n_q_heads * d, wk = (int64_t)n_k_heads * d;
+    const Range ins[] = {rows(q, n_tok, q_stride, wq, es), rows(k, n_tok, k_stride, wk, es),
+                         rows(dq_out, n_tok, dq_out_stride, wq, es), rows(dk_out, n_tok, dk_out_stride, wk, es),
+                         {q_weight, (size_t)d * 4}, {k_weight, (size_t)d * 4},
+                         {positions, (size_t)n_tok * position_bytes}, {freqs, (size_t)n_freqs * 8}};
+    const Range outs[] = {rows(dq, n_tok, wq, wq, es), rows(dk, n_tok, wk, wk, es), {dq_weight, (size_t)d * 4},
+                          {dk_weight, (size_t)d * 4}, {workspace, need}};
+    if (clash(ins, outs)) return api_fail(KDA_ERR_INVALID_ARG, kOverlap);
+    return launched(kda::launch_qk_norm(p, true, (cudaStream_t)stream), "query and key norm backward launch");
 }
 
 // ---------------------------------------------------------------- norms

@@ -130,6 +130,68 @@ struct GdrStepArgs {
 };
 cudaError_t launch_gdr_step(const GdrStepArgs &args, cudaStream_t stream);
 
+// Linear attention with one decay per head: as GdrArgs without beta, with the output's scale; g
+// [n_tok, n_heads] (g_stride = n_heads) or one decay per head [n_heads] (g_stride = 0), dg like g
+// (or NULL).
+struct DlaArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const float *g;
+    int64_t g_stride;
+    const float *h0;
+    const int32_t *cu_seqlens;
+    float scale;
+    void *out;
+    float *h_final;
+    const void *dout;
+    const float *dh_final;
+    void *dq, *dk, *dv;
+    float *dg, *dh0;
+    void *workspace;
+    int64_t n_tok;
+    int32_t n_seq, n_k_heads, n_heads, d_k, d_v;
+    bool bf16;
+};
+size_t dla_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k, int32_t d_v,
+                           bool bf16, bool bwd);
+cudaError_t launch_dla_fwd(const DlaArgs &args, cudaStream_t stream);
+cudaError_t launch_dla_bwd(const DlaArgs &args, cudaStream_t stream);
+
+// One token per row, as GdrStepArgs.
+struct DlaStepArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const float *g;
+    int64_t g_stride;
+    float *state;
+    const int32_t *slots;
+    float scale;
+    void *out;
+    int32_t n_rows, n_slots, n_k_heads, n_heads, d_k, d_v;
+    bool bf16;
+};
+cudaError_t launch_dla_step(const DlaStepArgs &args, cudaStream_t stream);
+
+// The norm of queries and keys per head with the position rotation (kda_qk_norm.cu): x[0] = q,
+// x[1] = k [n_tok, heads[i], d], tokens stride[i] elements apart; y (the forward's outputs, the
+// backward's gradients dx) contiguous; positions int32 or int64 (wide) [n_tok]; freqs [n_freqs]
+// radians per position.
+struct QkNormArgs {
+    const void *x[2], *dy[2];
+    int64_t stride[2], dy_stride[2];
+    const float *weight[2];
+    void *y[2];
+    float *dw[2], *partial;
+    const void *positions;
+    const double *freqs;
+    int64_t n_tok;
+    int32_t heads[2], d, n_freqs;
+    float eps;
+    bool wide_positions, interleaved, bf16;
+};
+size_t qk_norm_workspace_bytes(int64_t n_tok, int32_t d);
+cudaError_t launch_qk_norm(const QkNormArgs &args, bool bwd, cudaStream_t stream);
+
 // The norms around a block (kda_norm.cu). Strides in elements between rows (tokens);
 // outputs contiguous. Forward: x, residual, scale, weight -> y, r. Backward: r, x, dy, dr,
 // scale, weight -> dx, dresidual, dw, dscale, with the partial sums in `partial`.

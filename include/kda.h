@@ -632,6 +632,111 @@ kda_status kda_gated_norm_bwd(const void *dy, int64_t dy_stride, const void *x,
                               int32_t n_heads, int32_t d, float eps, int32_t activation,
                               kda_dtype dtype, void *stream);
 
+/*
+ * ---- linear attention with one decay per head ----
+ *
+ * The recurrence without the delta rule's correction, the layer of retention, lightning attention
+ * and scalar state spaces, on the same boundary as the gated delta rule above:
+ *
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ *
+ * q, k, v, h0, h_final, cu_seqlens, out as there (value head h reads key head h / (n_heads /
+ * n_k_heads)). g float32: with g_stride = n_heads a log-decay per token and head [n_tok,
+ * n_heads], contiguous; with g_stride = 0 one per head [n_heads], the same for every token. Any
+ * value up to 0; -inf forgets everything, values below -200 act as -inf in the chunked calls.
+ * scale: finite (d_k^-1/2 is usual). 1 <= d_k, d_v <= 128, n_heads a multiple of n_k_heads and at
+ * most 65535. Inputs are aligned to their element size; 16-byte aligned rows are read faster.
+ * State, sums and the gradient of g are fp32; with KDA_BF16 the products of the chunked calls run on
+ * the tensor cores with every operand that is not itself a bf16 input carried in two bf16 parts
+ * (about 2^-17 of relative rounding), with KDA_F32 they are fp32 FMAs. Results are
+ * deterministic: the same call gives the same bits; long sequences are cut into segments by the
+ * call's sizes, so that packing a sequence with others may change its results' last bits. A NaN or an
+ * infinity stays in its sequence, but in the chunked calls it reaches every token of its own
+ * chunk, the earlier ones too, and all later ones. Asynchronous on `stream`; nothing is allocated.
+ *
+ * kda_dla_chunk_fwd -- the forward pass over packed sequences. workspace: device memory, 16-byte
+ * aligned, kda_dla_chunk_fwd_workspace_bytes() bytes (0 for invalid sizes), caller-owned, contents
+ * ignored on entry. out and h_final (may be NULL) may not overlap an input, the workspace or each other.
+ * No sequence or no token is valid (h_final = h0). Errors as kda_gdr_chunk_fwd, and
+ * KDA_ERR_INVALID_ARG for another g_stride or a scale that is not finite.
+ *
+ * kda_dla_chunk_bwd -- gradients of <dout, out> + <dh_final, h_final> with respect to q, k, v, g and
+ * h0. dout [n_tok, n_heads, d_v] dtype, dh_final like h_final or NULL (zero). dq, dk [n_tok,
+ * n_k_heads, d_k] (summed over the value heads that share a key head), dv [n_tok, n_heads, d_v] in
+ * dtype, dg like g (with g_stride = 0 the sum over all tokens) or NULL, dh0 like h0 or NULL, all
+ * contiguous and fully overwritten. Where g is -inf (or below -200) dg is 0. workspace as above,
+ * kda_dla_chunk_bwd_workspace_bytes() bytes: it receives the state and the state gradient of every chunk.
+ *
+ * kda_dla_step -- one token for each of n_rows sequences, in place on a pool of states, as
+ * kda_gdr_step: row b reads and rewrites state[slots[b]] (slots NULL: state b); a slot outside
+ * [0, n_slots) marks a padded row: its out is 0 and no state is touched. Two rows of a call may
+ * not share a slot. g [n_rows, n_heads] (g_stride = n_heads) or [n_heads] (g_stride = 0).
+ */
+size_t kda_dla_chunk_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_k_heads,
+                                         int32_t n_heads, int32_t d_k, int32_t d_v,
+                                         kda_dtype dtype);
+kda_status kda_dla_chunk_fwd(const void *q, const void *k, const void *v, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const float *g,
+                             int64_t g_stride, const float *h0, const int32_t *cu_seqlens,
+                             float scale, void *out, float *h_final, void *workspace,
+                             size_t workspace_bytes, int64_t n_tok, int32_t n_seq,
+                             int32_t n_k_heads, int32_t n_heads, int32_t d_k, int32_t d_v,
+                             kda_dtype dtype, void *stream);
+size_t kda_dla_chunk_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_k_heads,
+                                         int32_t n_heads, int32_t d_k, int32_t d_v,
+                                         kda_dtype dtype);
+kda_status kda_dla_chunk_bwd(const void *q, const void *k, const void *v, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, const float *g,
+                             int64_t g_stride, const float *h0, const int32_t *cu_seqlens,
+                             float scale, const void *dout, const float *dh_final, void *dq,
+                             void *dk, void *dv, float *dg, float *dh0, void *workspace,
+                             size_t workspace_bytes, int64_t n_tok, int32_t n_seq,
+                             int32_t n_k_heads, int32_t n_heads, int32_t d_k, int32_t d_v,
+                             kda_dtype dtype, void *stream);
+kda_status kda_dla_step(const void *q, const void *k, const void *v, int64_t q_stride,
+                        int64_t k_stride, int64_t v_stride, const float *g, int64_t g_stride,
+                        float *state, const int32_t *slots, float scale, void *out,
+                        int32_t n_rows, int32_t n_slots, int32_t n_k_heads, int32_t n_heads,
+                        int32_t d_k, int32_t d_v, kda_dtype dtype, void *stream);
+
+/*
+ * kda_qk_norm_rope_fwd -- the norm of queries and keys per head and their rotation by position, in
+ * one pass over both:
+ *   n = x / sqrt(mean(x^2) + eps),   y = rot(weight n)               per token and head of d channels
+ * q [n_tok, n_q_heads, d], k [n_tok, n_k_heads, d] dtype, tokens q_stride / k_stride elements
+ * apart (slices of one projection); q_weight, k_weight [d] float32; q_out, k_out contiguous. rot turns
+ * pair i of the first 2 n_freqs channels by the angle positions[t] freqs[i]: channels i and n_freqs +
+ * i, or with interleaved != 0 channels 2 i and 2 i + 1:
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * positions [n_tok] int32 (position_bytes = 4) or int64 (8), any sign and size; freqs [n_freqs]
+ * float64, finite, radians per position. An angle is formed in 64-bit fixed point, modulo whole
+ * turns, to about 2^-52 of its size: positions far into a context lose nothing. n_freqs = 0: no
+ * rotation, positions and freqs may be NULL. 1 <= d <= 256, 0 <= 2 n_freqs <= d, eps > 0.
+ *
+ * kda_qk_norm_rope_bwd -- the gradients dq, dk (contiguous) and dq_weight, dk_weight [d] from dq_out
+ * and dk_out (tokens dq_out_stride / dk_out_stride elements apart). workspace: 16-byte aligned,
+ * kda_qk_norm_rope_bwd_workspace_bytes() bytes. Sums over rows run in a fixed order.
+ * Both: asynchronous on `stream`, nothing allocated, no output over an input; KDA_ERR_INVALID_ARG,
+ * KDA_ERR_UNSUPPORTED (dtype, d, more than 32768 heads) or KDA_ERR_CUDA as above.
+ */
+kda_status kda_qk_norm_rope_fwd(const void *q, int64_t q_stride, const void *k,
+                                int64_t k_stride, const float *q_weight,
+                                const float *k_weight, const void *positions,
+                                int32_t position_bytes, const double *freqs, int32_t n_freqs,
+                                void *q_out, void *k_out, int64_t n_tok, int32_t n_q_heads,
+                                int32_t n_k_heads, int32_t d, float eps, int32_t interleaved,
+                                kda_dtype dtype, void *stream);
+size_t kda_qk_norm_rope_bwd_workspace_bytes(int64_t n_tok, int32_t d);
+kda_status kda_qk_norm_rope_bwd(const void *dq_out, int64_t dq_out_stride, const void *dk_out,
+                                int64_t dk_out_stride, const void *q, int64_t q_stride,
+                                const void *k, int64_t k_stride, const float *q_weight,
+                                const float *k_weight, const void *positions,
+                                int32_t position_bytes, const double *freqs, int32_t n_freqs,
+                                void *dq, void *dk, float *dq_weight, float *dk_weight,
+                                void *workspace, size_t workspace_bytes, int64_t n_tok,
+                                int32_t n_q_heads, int32_t n_k_heads, int32_t d, float eps,
+                                int32_t interleaved, kda_dtype dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

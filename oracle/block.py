@@ -1,4 +1,4 @@
-"""fp64 definitions of the operators around the gated delta rule with one decay per head.
+"""fp64 definitions of the operators around the recurrences with one decay per head.
 
 TEST INFRASTRUCTURE ONLY (see the package docstring).
 
@@ -74,3 +74,51 @@ def gated_norm(x, gate, weight, eps, activation):
 def gated_norm_grads(dy, x, gate, weight, eps, activation):
     xs = [t.clone().requires_grad_(True) for t in (x, gate, weight)]
     return torch.autograd.grad((gated_norm(*xs, eps, activation) * dy).sum(), xs)
+
+
+def dla(q, k, v, g, h0, cu, scale=None):
+    """Linear attention with one decay per head: as ``gdr`` without beta; ``g`` [N, H] or [H]."""
+    group = v.shape[1] // q.shape[1]
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    g = g.expand(v.shape[:2])
+    outs, ends = [], []
+    for n, (a, b) in enumerate(zip(cu[:-1], cu[1:])):
+        S = q.new_zeros(v.shape[1], q.shape[2], v.shape[2]) if h0 is None else h0[n]
+        for t in range(a, b):
+            kt, qt = (x[t].repeat_interleave(group, 0) for x in (k, q))
+            S = g[t].exp()[:, None, None] * S + kt[:, :, None] * v[t][:, None, :]
+            outs.append(scale * torch.einsum("hkv,hk->hv", S, qt))
+        ends.append(S)
+    out = torch.stack(outs) if outs else v.new_zeros(0, *v.shape[1:])
+    return out, torch.stack(ends) if ends else v.new_zeros(0, v.shape[1], q.shape[2], v.shape[2])
+
+
+def dla_grads(q, k, v, g, h0, cu, dout, dh_final, scale=None):
+    """Gradients of ``<dout, out> + <dh_final, h_final>``: ``(dq, dk, dv, dg, dh0)``."""
+    if h0 is None:
+        h0 = q.new_zeros(len(cu) - 1, v.shape[1], q.shape[2], v.shape[2])
+    xs = [x.clone().requires_grad_(True) for x in (q, k, v, g, h0)]
+    out, end = dla(*xs, cu, scale)
+    loss = (out * dout).sum()
+    if dh_final is not None:
+        loss = loss + (end * dh_final).sum()
+    return torch.autograd.grad(loss, xs, allow_unused=True, materialize_grads=True)
+
+
+def head_norm_rope(x, weight, positions, freqs, eps, interleaved):
+    """``x`` [N, H, d] normed over its channels, the first 2 R of them turned pair by pair."""
+    y = weight * x / torch.sqrt((x * x).mean(-1, keepdim=True) + eps)
+    if freqs is None or freqs.numel() == 0:
+        return y
+    r = freqs.numel()
+    angle = (positions.double()[:, None] * freqs)[:, None]
+    cos, sin = angle.cos(), angle.sin()
+    a, b = (y[..., 0:2 * r:2], y[..., 1:2 * r:2]) if interleaved else (y[..., :r], y[..., r:2 * r])
+    a, b = a * cos - b * sin, b * cos + a * sin
+    head = torch.stack((a, b), -1).flatten(-2) if interleaved else torch.cat((a, b), -1)
+    return torch.cat((head, y[..., 2 * r:]), -1)
+
+
+def head_norm_rope_grads(dy, x, weight, positions, freqs, eps, interleaved):
+    xs = [t.clone().requires_grad_(True) for t in (x, weight)]
+    return torch.autograd.grad((head_norm_rope(*xs, positions, freqs, eps, interleaved) * dy).sum(), xs)
