@@ -558,11 +558,4 @@ cudaError_t launch_dla_simt(const DlaArgs &p, bool bwd, cudaStream_t stream) {
     return p.bf16 ? dla::run<__nv_bfloat16>(p, bwd, stream) : dla::run<float>(p, bwd, stream);
 }
 
-size_t dla_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t, int32_t d_k, int32_t d_v, bool,
-                           bool bwd) {
-    return dla_simt_workspace_bytes(n_tok, n_seq, n_heads, d_k, d_v, bwd);
-}
-cudaError_t launch_dla_fwd(const DlaArgs &p, cudaStream_t stream) { return launch_dla_simt(p, false, stream); }
-cudaError_t launch_dla_bwd(const DlaArgs &p, cudaStream_t stream) { return launch_dla_simt(p, true, stream); }
-
 }  // namespace kda

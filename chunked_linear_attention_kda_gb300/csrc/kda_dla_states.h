@@ -1,0 +1,336 @@
+// The walk over a segment that carries the state alone, forward over K and V or in reverse over Q
+// and dO (the gradient of the state), on tcgen05. Internal; included by the forward pass (what each
+// segment adds to the state) and the backward pass (the state at every block of 128 tokens).
+#pragma once
+
+#include <algorithm>
+#include <cmath>
+
+#include "kda_dla_tc.h"
+
+namespace kda {
+namespace dla {
+
+// one 16 x 16 block of fragments to a swizzled tile, `a` the address of the lane's row
+__device__ __forceinline__ void store_matrices(uint32_t a, const uint32_t *f) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(f[0]), "r"(f[1]),
+                 "r"(f[2]), "r"(f[3]) : "memory");
+}
+__device__ __forceinline__ void store_matrices_t(uint32_t a, const uint32_t *f) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(f[0]), "r"(f[1]),
+                 "r"(f[2]), "r"(f[3]) : "memory");
+}
+
+// How a call is cut into segments
+struct Plan {
+    int seg;             // tokens of a segment
+    int64_t slots;       // of segments
+    bool cut;            // some sequence may have more than one
+    bool vec_q, vec_k, vec_v, vec_o;  // 16-byte rows
+    float *states;       // [slots][heads] states at the segments' starts (reverse: gradients at their ends)
+    float *decays;       // [slots][heads] decays over the segments
+};
+// Tiles of a segment. A segment costs its tiles and about `start` tiles more to begin; the last one
+// runs alone for as long as it is. Over all heads the sum of both is least at the square root.
+inline int segment_tiles(int64_t n_tok, int32_t n_heads) {
+    constexpr double start = 3.0, sms = 152.0;
+    const double tiles = (double)((n_tok + C - 1) / C);
+    return std::max(8, (int)std::ceil(std::sqrt(start * tiles * n_heads / sms)));
+}
+inline size_t plan_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k, bool bwd) {
+    const int64_t seg = (int64_t)segment_tiles(n_tok, n_heads) * C;
+    if (n_tok <= seg) return 256;
+    const size_t units = (size_t)(n_tok / seg + n_seq) * n_heads;
+    return (units * state_floats(d_k <= 64 ? 64 : 128) * 4 + units * 4 + 255) / 256 * 256 * (bwd ? 2 : 1);
+}
+inline Plan make_plan(const DlaArgs &p, bool bwd) {
+    Plan plan{};
+    plan.seg = segment_tiles(p.n_tok, p.n_heads) * C;
+    plan.cut = p.n_tok > plan.seg;
+    plan.slots = p.n_tok / plan.seg + p.n_seq;
+    plan.vec_q = gdr::rows_vec<__nv_bfloat16>(p.q, p.q_stride, p.d_k);
+    plan.vec_k = gdr::rows_vec<__nv_bfloat16>(p.k, p.k_stride, p.d_k);
+    plan.vec_v = gdr::rows_vec<__nv_bfloat16>(p.v, p.v_stride, p.d_v);
+    plan.vec_o = bwd && gdr::rows_vec<__nv_bfloat16>(p.dout, (int64_t)p.n_heads * p.d_v, p.d_v);
+    plan.states = static_cast<float *>(p.workspace);
+    plan.decays = plan.states + (size_t)plan.slots * p.n_heads * state_floats(p.d_k <= 64 ? 64 : 128);
+    return plan;
+}
+
+// NC key channels from c0 on of one value channel: a state of the workspace
+template <int NC>
+__device__ __forceinline__ void load_state(float *st, const float *from, int dv, int c0) {
+#pragma unroll
+    for (int i = 0; i < NC; i += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(from + (c0 + i) / 4 * 512 + dv * 4);
+        st[i] = x.x; st[i + 1] = x.y; st[i + 2] = x.z; st[i + 3] = x.w;
+    }
+}
+template <int NC>
+__device__ __forceinline__ void store_state(const float *st, float *to, int dv, int c0) {
+#pragma unroll
+    for (int i = 0; i < NC; i += 4)
+        *reinterpret_cast<float4 *>(to + (c0 + i) / 4 * 512 + dv * 4) = make_float4(st[i], st[i + 1], st[i + 2], st[i + 3]);
+}
+// the caller's [d_k][d_v] (NULL: zeros)
+template <int NC>
+__device__ __forceinline__ void load_given(float *st, const float *from, int d_k, int d_v, int dv, int c0) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i) st[i] = from && dv < d_v && c0 + i < d_k ? from[(int64_t)(c0 + i) * d_v + dv] : 0.f;
+}
+template <int NC>
+__device__ __forceinline__ void store_given(const float *st, float *to, int d_k, int d_v, int dv, int c0) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+        if (dv < d_v && c0 + i < d_k) to[(int64_t)(c0 + i) * d_v + dv] = st[i];
+}
+
+// warps: 0 issues products, 1 forms gates, 2 and 3 load, 4..7 scale the keys, 8..15 hold the state
+constexpr int kStateThreads = 512;
+
+template <int DK>
+struct StateSmem {
+    static constexpr int kKey = DK / 64 * kHalf, kVal = 2 * kHalf;
+    static constexpr int K = 0, V = kKey, kStage = V + kVal;
+    static constexpr int kStages = 4;
+    static constexpr int Kp = kStages * kStage, Gate = Kp + 2 * kKey;
+    static constexpr int kGates = 4;
+    static constexpr int Bars = Gate + kGates * (int)sizeof(TileGates);
+    static constexpr int Full = 0, Empty = kStages, GFull = 2 * kStages, GEmpty = GFull + kGates, KpFull = GEmpty + kGates,
+                         KpEmpty = KpFull + 1, DsFull = KpEmpty + 1, DsEmpty = DsFull + 2, Drain = DsEmpty + 2, kBars = Drain + 1;
+    static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;
+    static_assert(kBytes <= 227 * 1024, "fits an SM");
+};
+
+// What a segment adds to the state, from a state of zero, and its decay. The last segment of the
+// walk hands on to none and is left out.
+template <int DK, bool REV>
+__device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CUtensorMap &tm_val, const DlaArgs &p,
+                                             const Plan &plan, bool copies, unsigned unit) {
+    using L = StateSmem<DK>;
+    constexpr int S = L::kStages;
+    extern __shared__ __align__(1024) char smem_raw[];
+    char *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t base = ptx::smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int head = unit % p.n_heads, kh = head / (p.n_heads / p.n_k_heads);
+    const int64_t slot = unit / p.n_heads;
+    const Segment sg = find_segment(p.cu_seqlens, p.n_seq, slot, plan.seg);
+    if (sg.len == 0 || (REV ? sg.index == 0 : sg.last)) return;
+    const int nc = (int)((sg.len + C - 1) / C);
+    auto bar = [&](int i) { return base + L::Bars + 8 * i; };
+    auto gate = [&](int n) { return reinterpret_cast<TileGates *>(smem + L::Gate) + n % L::kGates; };
+    auto tile = [&](int n) { return REV ? nc - 1 - n : n; };  // the n-th of the walk
+    auto rows_of = [&](int c) { return (int)min((int64_t)C, sg.len - (int64_t)c * C); };
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            ptx::mbar_init(bar(L::Full + i), 1);
+            ptx::mbar_init(bar(L::Empty + i), 1 + 4);
+        }
+        for (int i = 0; i < L::kGates; ++i) {
+            ptx::mbar_init(bar(L::GFull + i), 1);
+            ptx::mbar_init(bar(L::GEmpty + i), 4 + 8);
+        }
+        ptx::mbar_init(bar(L::KpFull), 4);
+        ptx::mbar_init(bar(L::KpEmpty), 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(L::DsFull + i), 1);
+            ptx::mbar_init(bar(L::DsEmpty + i), 8);
+        }
+        ptx::mbar_init(bar(L::Drain), 1);
+        ptx::mbar_init_fence();
+    }
+    if (warp == 0) ptx::tmem_alloc(bar(L::kBars), 256);
+    if (p.d_v <= 64)  // channels that no value head has
+        for (int i = tid; i < S * kHalf / 16; i += kStateThreads)
+            *reinterpret_cast<uint4 *>(smem + (i / (kHalf / 16)) * L::kStage + L::V + kHalf + (i % (kHalf / 16)) * 16) = make_uint4(0, 0, 0, 0);
+    ptx::fence_proxy_async();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<const uint32_t *>(smem + L::Bars + 8 * L::kBars);
+    bool ok = true;
+    auto wait = [&](int b, int parity) { ok = wait_bar(bar(b), parity & 1) && ok; };
+    if (warp == 0) {
+        if (lane == 0) {
+            constexpr uint32_t id = ptx::idesc_bf16(128, DK, 1, 1);
+            for (int n = 0; n < nc; ++n) {
+                const int s = n % S;
+                wait(L::KpFull, n);
+                if (n >= 2) wait(L::DsEmpty + (n & 1), (n >> 1) - 1);
+                ptx::tc_fence_after();
+                const uint64_t v = ptx::sdesc_sw128(base + s * L::kStage + L::V, kHalf, 1024);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k)
+                        ptx::umma_ss(tmem + (n & 1) * 128, v + 128 * k, ptx::sdesc_sw128(base + L::Kp + i * L::kKey, kHalf, 1024) + 128 * k,
+                                     id, i + k > 0);
+                ptx::umma_commit(bar(L::DsFull + (n & 1)));
+                ptx::umma_commit(bar(L::KpEmpty));
+                ptx::umma_commit(bar(L::Empty + s));
+            }
+            ptx::umma_commit(bar(L::Drain));
+            drain_bar(bar(L::Drain), 0);
+        }
+    } else if (warp == 1) {
+        float g[2];
+        fetch_gates(p, sg.t0 + (int64_t)tile(0) * C, rows_of(tile(0)), head, g);
+        for (int n = 0; n < nc; ++n) {
+            float next[2] = {0.f, 0.f};
+            if (n + 1 < nc) fetch_gates(p, sg.t0 + (int64_t)tile(n + 1) * C, rows_of(tile(n + 1)), head, next);
+            if (n >= L::kGates) wait(L::GEmpty + n % L::kGates, n / L::kGates - 1);
+            form_gates<REV>(g, p.scale, gate(n));
+            warp_arrive(bar(L::GFull + n % L::kGates));
+            g[0] = next[0];
+            g[1] = next[1];
+        }
+    } else if (warp < 4) {
+        const Source k{&tm_key, static_cast<const __nv_bfloat16 *>(REV ? p.q : p.k), REV ? p.q_stride : p.k_stride, kh, p.d_k,
+                       DK / 64, REV ? plan.vec_q : plan.vec_k};
+        const Source v{&tm_val, static_cast<const __nv_bfloat16 *>(REV ? p.dout : p.v), REV ? (int64_t)p.n_heads * p.d_v : p.v_stride,
+                       head, p.d_v, p.d_v > 64 ? 2 : 1, REV ? plan.vec_o : plan.vec_v};
+        int copied = 0;
+        for (int n = 0; n < nc; ++n) {
+            const int s = n % S, rows = rows_of(tile(n));
+            if (n >= S) wait(L::Empty + s, n / S - 1);
+            ok = __all_sync(0xffffffffu, ok);
+            const uint32_t at = base + s * L::kStage;
+            const int64_t t0 = sg.t0 + (int64_t)tile(n) * C;
+            if (copies && rows == C) {
+                if (ok && warp == 2 && lane == 0) {
+                    const uint32_t m = bar(L::Full + s);
+                    ptx::mbar_arrive_tx(m, L::kKey + v.halves * kHalf);
+                    tile_by_copy(k, at + L::K, t0, m);
+                    tile_by_copy(v, at + L::V, t0, m);
+                    copied = n + 1;
+                }
+            } else {
+                if (ok) {
+                    tile_by_threads(k, at + L::K, t0, rows, tid - 64, 64);
+                    tile_by_threads(v, at + L::V, t0, rows, tid - 64, 64);
+                }
+                tile_loaded(bar(L::Full + s));
+            }
+        }
+        if (!ok)
+            for (int n = max(0, copied - S); n < copied; ++n) drain_bar(bar(L::Full + n % S), (n / S) & 1);
+    } else if (warp < 8) {
+        for (int n = 0; n < nc; ++n) {
+            const int s = n % S;
+            wait(L::GFull + n % L::kGates, n / L::kGates);
+            wait(L::Full + s, n / S);
+            if (n > 0) wait(L::KpEmpty, n - 1);
+            scale_rows(smem + s * L::kStage + L::K, smem + L::Kp, L::kKey, *gate(n), L::kKey, tid - 128, 128);
+            ptx::fence_proxy_async();
+            warp_arrive(bar(L::KpFull));
+            warp_arrive(bar(L::Empty + s));
+            warp_arrive(bar(L::GEmpty + n % L::kGates));
+        }
+    } else {
+        constexpr int NC = DK / 2;
+        const int dv = (warp & 3) * 32 + lane, part = (warp - 8) >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        float st[NC], decay = 1.f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) st[i] = 0.f;
+        for (int n = 0; n < nc; ++n) {
+            wait(L::GFull + n % L::kGates, n / L::kGates);
+            const float whole = gate(n)->whole;
+            warp_arrive(bar(L::GEmpty + n % L::kGates));
+            decay *= whole;
+            wait(L::DsFull + (n & 1), n >> 1);
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < NC; i += 16) {
+                float d[16];
+                ptx::tmem_ld16(lanes + (n & 1) * 128 + part * NC + i, reinterpret_cast<uint32_t *>(d));
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) st[i + j] = fmaf(whole, st[i + j], d[j]);
+            }
+            ptx::tc_fence_before();
+            warp_arrive(bar(L::DsEmpty + (n & 1)));
+        }
+        const size_t at = (size_t)slot * p.n_heads + head;
+        store_state<NC>(st, plan.states + at * state_floats(DK), dv, part * NC);
+        if (tid == 256) plan.decays[at] = decay;
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 0) ptx::tmem_dealloc(tmem, 256);
+}
+
+template <int DK>
+__global__ void __launch_bounds__(kStateThreads, 1)
+    dla_segments_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const DlaArgs p,
+                        const Plan plan, bool copies, bool rev) {
+    gdr::let_next_kernel_start();
+    if (rev) segment_walk<DK, true>(tm_q, tm_o, p, plan, copies, blockIdx.x);
+    else segment_walk<DK, false>(tm_k, tm_v, p, plan, copies, blockIdx.x);
+}
+
+// The states at the segments' starts (reverse: the gradients at their ends), in place of what the
+// segments add: 16 bytes of a sequence's and head's state a thread, segment after segment.
+template <int DK>
+__global__ void __launch_bounds__(256) dla_join_kernel(const DlaArgs p, const Plan plan, bool rev) {
+    gdr::let_next_kernel_start();
+    constexpr int kBlocks = state_floats(DK) / 4 / 256;
+    const int i = (blockIdx.x % kBlocks) * 256 + threadIdx.x;
+    const int head = blockIdx.x / kBlocks % p.n_heads, seq = blockIdx.x / kBlocks / p.n_heads;
+    const int64_t len = p.cu_seqlens[seq + 1] - p.cu_seqlens[seq], m = (len + plan.seg - 1) / plan.seg;
+    if (m < 2) {
+        gdr::wait_for_previous_kernel();  // whoever waits for this kernel waits for that one
+        return;
+    }
+    const int dv = i & 127, c = i >> 7 << 2;
+    const float *given = rev ? p.dh_final : p.h0;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (given && dv < p.d_v) {
+        const float *from = given + ((int64_t)seq * p.n_heads + head) * p.d_k * p.d_v + dv;
+        if (c < p.d_k) x.x = from[(int64_t)c * p.d_v];
+        if (c + 1 < p.d_k) x.y = from[(int64_t)(c + 1) * p.d_v];
+        if (c + 2 < p.d_k) x.z = from[(int64_t)(c + 2) * p.d_v];
+        if (c + 3 < p.d_k) x.w = from[(int64_t)(c + 3) * p.d_v];
+    }
+    const int64_t slot0 = segment_base(p.cu_seqlens, seq, plan.seg);
+    gdr::wait_for_previous_kernel();
+    auto unit = [&](int64_t n) { return (size_t)(slot0 + (rev ? m - 1 - n : n)) * p.n_heads + head; };
+    auto at = [&](int64_t n) { return reinterpret_cast<float4 *>(plan.states + unit(n) * state_floats(DK)) + i; };
+    for (int64_t n0 = 0; n0 < m; n0 += 4) {
+        float4 add[4];
+        float decay[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n0 + j + 1 < m) {  // the last one hands on to none
+                add[j] = *at(n0 + j);
+                decay[j] = plan.decays[unit(n0 + j)];
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (n0 + j >= m) break;
+            *at(n0 + j) = x;
+            if (n0 + j + 1 == m) break;
+            x.x = fmaf(decay[j], x.x, add[j].x);
+            x.y = fmaf(decay[j], x.y, add[j].y);
+            x.z = fmaf(decay[j], x.z, add[j].z);
+            x.w = fmaf(decay[j], x.w, add[j].w);
+        }
+    }
+}
+
+template <int DK>
+cudaError_t launch_segments(const DlaArgs &p, const Plan &plan, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                            const CUtensorMap &o, bool copies, bool rev, cudaStream_t stream) {
+    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dla_segments_kernel<DK>), StateSmem<DK>::kBytes);
+    if (e != cudaSuccess) return e;
+    dla_segments_kernel<DK><<<(unsigned)(plan.slots * p.n_heads), kStateThreads, StateSmem<DK>::kBytes, stream>>>(
+        q, k, v, o, p, plan, copies, rev);
+    count_launches(1);
+    return gdr::launch_dependent(dla_join_kernel<DK>, dim3((unsigned)(state_floats(DK) / 1024 * p.n_heads * p.n_seq)), 256, 0, stream,
+                                 p, plan, rev);
+}
+
+}  // namespace dla
+}  // namespace kda

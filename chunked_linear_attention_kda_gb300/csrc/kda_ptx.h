@@ -236,6 +236,9 @@ __device__ __forceinline__ void tmem_st16(uint32_t ta, const uint32_t *r) {
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
         "%13,%14,%15,%16};" ::"r"(ta), KDA_W8(0), KDA_W8(8));
 }
+__device__ __forceinline__ void tmem_st8(uint32_t ta, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(ta), KDA_W8(0));
+}
 __device__ __forceinline__ void tmem_st32(uint32_t ta, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"

@@ -92,7 +92,8 @@ uint64_t kda_kernel_launch_count(void);
  * two seconds); that kernel then stopped early and its outputs are unspecified:
  * bit 0 the 16-token-step tensor-core forward (and the self-test below), bit 1 the
  * gate-projection GEMM, bit 2 the backward's serial passes, bit 3 the 64-token-step
- * tensor-core forward, bit 4 the chains of the gated delta rule. A healthy run leaves the word 0. Returns KDA_ERR_INVALID_ARG
+ * tensor-core forward, bit 4 the chains of the gated delta rule, bit 5 linear
+ * attention with one decay per head. A healthy run leaves the word 0. Returns KDA_ERR_INVALID_ARG
  * for a NULL `flags`, KDA_ERR_CUDA if the copy or the synchronisation fails.
  */
 kda_status kda_read_device_flags(uint32_t *flags, int reset, void *stream);
