@@ -32,12 +32,13 @@ struct FwdSmem {
     static constexpr int kStages = 3;
     static constexpr int Kp = kStages * kStage, P = Kp + 2 * kKey, O = P + 2 * kHalf, Gate = O + 2 * kHalf;
     static constexpr int kGates = 4;
-    static constexpr int Bars = Gate + kGates * (int)sizeof(TileGates);
+    static constexpr int Ring = Gate + kGates * (int)sizeof(TileGates), Bars = Ring + kAhead * C * 4;
     // full, empty [stages], gates full, empty [4], QK full, empty [2], then one each
     static constexpr int Full = 0, Empty = kStages, GFull = 2 * kStages, GEmpty = GFull + kGates, QkFull = GEmpty + kGates,
                          QkEmpty = QkFull + 2, PFull = QkEmpty + 2, PEmpty = PFull + 1, KpFull = PEmpty + 1,
                          KpEmpty = KpFull + 1, DsFull = KpEmpty + 1, DsEmpty = DsFull + 1, SFull = DsEmpty + 1,
-                         SEmpty = SFull + 1, OFull = SEmpty + 1, OEmpty = OFull + 1, Drain = OEmpty + 1, kBars = Drain + 1;
+                         SEmpty = SFull + 1, O1Empty = SEmpty + 1, O2Full = O1Empty + 1, O2Empty = O2Full + 1, Drain = O2Empty + 1,
+                         kBars = Drain + 1;
     static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;  // the base is rounded up to 1024
     static_assert(kBytes <= 227 * 1024, "fits an SM");
 };
@@ -91,8 +92,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ptx::mbar_init(bar(L::DsEmpty), 8);
         ptx::mbar_init(bar(L::SFull), 8);
         ptx::mbar_init(bar(L::SEmpty), 1);
-        ptx::mbar_init(bar(L::OFull), 1);
-        ptx::mbar_init(bar(L::OEmpty), 4);
+        ptx::mbar_init(bar(L::O1Empty), 4);
+        ptx::mbar_init(bar(L::O2Full), 1);
+        ptx::mbar_init(bar(L::O2Empty), 4);
         ptx::mbar_init(bar(L::Drain), 1);
         ptx::mbar_init_fence();
     }
@@ -113,77 +115,78 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     auto wait = [&](int b, int parity) { ok = wait_bar(bar(b), parity & 1) && ok; };
 
     if (warp == 0) {
-        if (lane == 0) {
-            constexpr uint32_t id_qk = ptx::idesc_bf16(64, C, 0, 0), id_o1 = ptx::idesc_bf16(128, C, 0, 0);
-            constexpr uint32_t id_o2 = ptx::idesc_bf16(128, C, 1, 0), id_ds = ptx::idesc_bf16(128, DK, 1, 1);
-            auto pairs = [&](int c) {
-                const int s = c % S;
-                wait(L::Full + s, c / S);
-                if (c >= 2) wait(L::QkEmpty + (c & 1), (c >> 1) - 1);
-                ptx::tc_fence_after();
+        // The whole warp walks, one lane issues: operands by offsets in uniform registers.
+        constexpr uint32_t id_qk = ptx::idesc_bf16(64, C, 0, 0), id_o1 = ptx::idesc_bf16(128, C, 0, 0);
+        constexpr uint32_t id_o2 = ptx::idesc_bf16(128, C, 1, 0), id_ds = ptx::idesc_bf16(128, DK, 1, 1);
+        const uint32_t leader = ptx::elect_one();
+        const uint64_t q0 = ptx::sdesc_sw128(base + L::Q, 16, 1024), k0 = ptx::sdesc_sw128(base + L::K, 16, 1024);
+        const uint64_t v0 = ptx::sdesc_sw128(base + L::V, kHalf, 1024), kp = ptx::sdesc_sw128(base + L::Kp, kHalf, 1024);
+        const uint64_t pp = ptx::sdesc_sw128(base + L::P, 16, 1024);
+        auto step = [](int k) { return (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) / 16; };  // 16 channels, K-major
+        int next = 0, next_phase = 0;  // the stage of the next Q K^T
+        auto pairs = [&](int c) {
+            wait(L::Full + next, next_phase);
+            if (c >= 2) wait(L::QkEmpty + (c & 1), (c >> 1) - 1);
+            ptx::tc_fence_after();
+            const uint32_t at = (uint32_t)next * (L::kStage / 16);
 #pragma unroll
-                for (int k = 0; k < DK / 16; ++k) {
-                    const uint32_t at = base + s * L::kStage + (k >> 2) * kHalf + (k & 3) * 32;
-                    ptx::umma_ss(tmem + kTmQk + (c & 1) * C, ptx::sdesc_sw128(at + L::Q, 16, 1024),
-                                 ptx::sdesc_sw128(at + L::K, 16, 1024), id_qk, k > 0);
-                }
-                ptx::umma_commit(bar(L::QkFull + (c & 1)));
-            };
-            pairs(0);
-            for (int c = 0; c < nc; ++c) {
-                const int s = c % S;
-                if (c + 1 < nc) pairs(c + 1);
-                wait(L::SFull, c);
-                if (c > 0) wait(L::OEmpty, c - 1);
-                ptx::tc_fence_after();
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)
-                        ptx::umma_ts(tmem + kTmO1, tmem + kTmS + i * (DK / 2) + 8 * k,
-                                     ptx::sdesc_sw128(base + s * L::kStage + L::Q + (k >> 2) * kHalf + (k & 3) * 32, 16, 1024),
-                                     id_o1, i + k > 0);
-                ptx::umma_commit(bar(L::SEmpty));
-                const uint64_t v = ptx::sdesc_sw128(base + s * L::kStage + L::V, kHalf, 1024);
-                if (c + 1 < nc || keep_end) {
-                    wait(L::KpFull, c);
-                    if (c > 0) wait(L::DsEmpty, c - 1);
-                    ptx::tc_fence_after();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int k = 0; k < C / 16; ++k)
-                            ptx::umma_ss(tmem + kTmDs, v + 128 * k, ptx::sdesc_sw128(base + L::Kp + i * L::kKey, kHalf, 1024) + 128 * k,
-                                         id_ds, i + k > 0);
-                    ptx::umma_commit(bar(L::DsFull));
-                    ptx::umma_commit(bar(L::KpEmpty));
-                }
-                wait(L::PFull, c);
+            for (int k = 0; k < DK / 16; ++k)
+                ptx::umma_ss_by(leader, tmem + kTmQk + (c & 1) * C, q0 + (at + step(k)), k0 + (at + step(k)), id_qk, k > 0);
+            ptx::umma_commit_by(leader, bar(L::QkFull + (c & 1)));
+            if (++next == S) {
+                next = 0;
+                next_phase ^= 1;
+            }
+        };
+        pairs(0);
+        int s = 0;
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+            // in the order in which their operands come: dS^T is waited for by the state's warps while
+            // O1 is formed, and O1 by the next tile's planes of S
+            if (c + 1 < nc) pairs(c + 1);
+            const uint32_t at = (uint32_t)s * (L::kStage / 16);
+            if (c + 1 < nc || keep_end) {
+                wait(L::KpFull, c);
+                if (c > 0) wait(L::DsEmpty, c - 1);
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
-                        ptx::umma_ss(tmem + kTmO2, v + 128 * k, ptx::sdesc_sw128(base + L::P + i * kHalf + k * 32, 16, 1024), id_o2, i + k > 0);
-                ptx::umma_commit(bar(L::OFull));
-                ptx::umma_commit(bar(L::PEmpty));
-                ptx::umma_commit(bar(L::Empty + s));
+                        ptx::umma_ss_by(leader, tmem + kTmDs, v0 + (at + 128 * k), kp + (i * L::kKey / 16 + 128 * k), id_ds, i + k > 0);
+                ptx::umma_commit_by(leader, bar(L::DsFull));
+                ptx::umma_commit_by(leader, bar(L::KpEmpty));
             }
-            ptx::umma_commit(bar(L::Drain));
-            drain_bar(bar(L::Drain), 0);
+            wait(L::SFull, c);
+            if (c > 0) wait(L::O1Empty, c - 1);
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < DK / 16; ++k)
+                    ptx::umma_ts_by(leader, tmem + kTmO1, tmem + kTmS + i * (DK / 2) + 8 * k, q0 + (at + step(k)), id_o1, i + k > 0);
+            ptx::umma_commit_by(leader, bar(L::SEmpty));
+            wait(L::PFull, c);
+            if (c > 0) wait(L::O2Empty, c - 1);
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < C / 16; ++k)
+                    ptx::umma_ss_by(leader, tmem + kTmO2, v0 + (at + 128 * k), pp + (i * kHalf + k * 32) / 16, id_o2, i + k > 0);
+            ptx::umma_commit_by(leader, bar(L::O2Full));
+            ptx::umma_commit_by(leader, bar(L::PEmpty));
+            ptx::umma_commit_by(leader, bar(L::Empty + s));
+            if (++s == S) s = 0;
         }
+        ptx::umma_commit_by(leader, bar(L::Drain));
+        drain_bar(bar(L::Drain), 0);
     } else if (warp == 1) {
-        float g[2];
-        fetch_gates(p, sg.t0, rows_of(0), head, g);
-        for (int c = 0; c < nc; ++c) {
-            float next[2] = {0.f, 0.f};
-            if (c + 1 < nc) fetch_gates(p, sg.t0 + (int64_t)(c + 1) * C, rows_of(c + 1), head, next);
-            if (c >= L::kGates) wait(L::GEmpty + c % L::kGates, c / L::kGates - 1);
-            form_gates<false>(g, 0.f, gate(c));
-            warp_arrive(bar(L::GFull + c % L::kGates));
-            g[0] = next[0];
-            g[1] = next[1];
-        }
+        walk_gates<false>(
+            p, reinterpret_cast<float *>(smem + L::Ring), sg.t0, head, nc, [](int n) { return n; }, rows_of, gate,
+            [&](int n) { if (n >= L::kGates) wait(L::GEmpty + n % L::kGates, n / L::kGates - 1); },
+            [&](int n) { warp_arrive(bar(L::GFull + n % L::kGates)); });
     } else if (warp < 4) {
         const Source q{&tm_q, static_cast<const __nv_bfloat16 *>(p.q), p.q_stride, kh, p.d_k, DK / 64, plan.vec_q};
         const Source k{&tm_k, static_cast<const __nv_bfloat16 *>(p.k), p.k_stride, kh, p.d_k, DK / 64, plan.vec_k};
@@ -220,47 +223,40 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int w = warp - 4, gr = lane >> 2, tq = lane & 3;
         const uint32_t lanes = tmem + ((uint32_t)(w * 32) << 16);
         const uint32_t put_at = base + L::P, row = 16 * w + ((lane >> 3) & 1) * 8 + (lane & 7), col8 = (lane >> 4) * 8;
-        for (int c = 0; c < nc; ++c) {
+        auto keys = [&](int c) {  // K' of tile c
             const int s = c % S;
-            const TileGates &g = *gate(c);
             wait(L::GFull + c % L::kGates, c / L::kGates);
             wait(L::Full + s, c / S);
             if (c > 0) wait(L::KpEmpty, c - 1);
-            scale_rows(smem + s * L::kStage + L::K, smem + L::Kp, L::kKey, g, L::kKey, tid - 128, 128);
+            scale_rows(smem + s * L::kStage + L::K, smem + L::Kp, L::kKey, *gate(c), L::kKey, tid - 128, 128);
             ptx::fence_proxy_async();
             warp_arrive(bar(L::KpFull));
             warp_arrive(bar(L::Empty + s));
+        };
+        keys(0);
+        for (int c = 0; c < nc; ++c) {
+            const TileGates &g = *gate(c);
             wait(L::QkFull + (c & 1), c >> 1);
             ptx::tc_fence_after();
-            float x[8][4];
-            ptx::tmem_ld_frag4(lanes + kTmQk + (c & 1) * C, reinterpret_cast<uint32_t *>(x[0]));
-            if (w >= 2) ptx::tmem_ld_frag4(lanes + kTmQk + (c & 1) * C + 32, reinterpret_cast<uint32_t *>(x[4]));
-            ptx::tmem_ld_wait();
-            ptx::tc_fence_before();
-            warp_arrive(bar(L::QkEmpty + (c & 1)));
             const int r0 = 16 * w + gr;
             const float2 G0 = g.G[r0], G1 = g.G[r0 + 8];
             if (c > 0) wait(L::PEmpty, c - 1);
-#pragma unroll
-            for (int J = 0; J < 4; ++J) {
-                if (J > w) break;
+#pragma unroll 1
+            for (int J = 0; J <= w; ++J) {  // 16 columns; a loop that is not unrolled, see wait_longer
+                float x[2][4];
+                ptx::tmem_ld_frag2(lanes + kTmQk + (c & 1) * C + 16 * J, reinterpret_cast<uint32_t *>(x[0]));
+                ptx::tmem_ld_wait();
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    float *d = x[2 * J + n];
+                    float *d = x[n];
                     const int col = 16 * J + 8 * n + 2 * tq;
                     const float4 Gc = *reinterpret_cast<const float4 *>(&g.G[col]);
                     const float2 a = make_float2(Gc.x, Gc.y), b = make_float2(Gc.z, Gc.w);
-                    d[0] *= exp2_between(G0, a);
-                    d[1] *= exp2_between(G0, b);
-                    d[2] *= exp2_between(G1, a);
-                    d[3] *= exp2_between(G1, b);
-                    if (J == w) {
-                        if (r0 < col) d[0] = 0.f;
-                        if (r0 < col + 1) d[1] = 0.f;
-                        if (r0 + 8 < col) d[2] = 0.f;
-                        if (r0 + 8 < col + 1) d[3] = 0.f;
-                    }
+                    d[0] = r0 >= col ? d[0] * exp2_between(G0, a) : 0.f;
+                    d[1] = r0 > col ? d[1] * exp2_between(G0, b) : 0.f;
+                    d[2] = r0 + 8 >= col ? d[2] * exp2_between(G1, a) : 0.f;
+                    d[3] = r0 + 8 > col ? d[3] * exp2_between(G1, b) : 0.f;
                     split(d[0], d[1], hi[2 * n], lo[2 * n]);
                     split(d[2], d[3], hi[2 * n + 1], lo[2 * n + 1]);
                 }
@@ -268,9 +264,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 store_matrices(at, hi);
                 store_matrices(at + kHalf, lo);
             }
+            ptx::tc_fence_before();
+            warp_arrive(bar(L::QkEmpty + (c & 1)));
             ptx::fence_proxy_async();
             warp_arrive(bar(L::PFull));
             warp_arrive(bar(L::GEmpty + c % L::kGates));
+            if (c + 1 < nc) keys(c + 1);
         }
     } else if (warp < 16) {
         constexpr int NC = DK / 2;  // key channels of a thread
@@ -326,55 +325,76 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const bool live = 32 * w < p.d_v;
         const int64_t row_stride = (int64_t)p.n_heads * p.d_v;
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + sg.t0 * row_stride + (int64_t)head * p.d_v;
-        const int groups = (p.d_v + 7) / 8;
+        const int ch = (ot & 15) * 8;  // copied out: eight channels of every eighth token
         for (int c = 0; c < nc; ++c) {
             const TileGates &g = *gate(c);
             wait(L::GFull + c % L::kGates, c / L::kGates);
-            wait(L::OFull, c);
+            // 16 value channels x 32 tokens a time; O1 leaves tensor memory first
+            float o[4][4][4];
+            wait(L::SEmpty, c);  // O1 is formed
+            ptx::tc_fence_after();
+            if (live) {
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    ptx::tmem_ld_frag4(tmem + ((uint32_t)(32 * w + 16 * (h & 1)) << 16) + kTmO1 + 32 * (h >> 1),
+                                       reinterpret_cast<uint32_t *>(o[h][0]));
+                ptx::tmem_ld_wait();
+            }
+            ptx::tc_fence_before();
+            warp_arrive(bar(L::O1Empty));
+            if (live)
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const float2 gam = *reinterpret_cast<const float2 *>(&g.gam[32 * (h >> 1) + 8 * n + 2 * tq]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[h][n][e] *= e & 1 ? gam.y : gam.x;
+                    }
+            warp_arrive(bar(L::GEmpty + c % L::kGates));
+            wait(L::O2Full, c);
             ptx::tc_fence_after();
             if (live)
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {  // 16 value channels x 32 tokens
+                for (int h = 0; h < 4; ++h) {
                     const int dv0 = 32 * w + 16 * (h & 1), tok0 = 32 * (h >> 1);
-                    const uint32_t at = tmem + ((uint32_t)dv0 << 16) + tok0;
-                    float a[4][4], b[4][4];
-                    ptx::tmem_ld_frag4(at + kTmO1, reinterpret_cast<uint32_t *>(a[0]));
-                    ptx::tmem_ld_frag4(at + kTmO2, reinterpret_cast<uint32_t *>(b[0]));
+                    float b[4][4];
+                    ptx::tmem_ld_frag4(tmem + ((uint32_t)dv0 << 16) + kTmO2 + tok0, reinterpret_cast<uint32_t *>(b[0]));
                     ptx::tmem_ld_wait();
                     uint32_t f[8];
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
-                        const float2 gam = *reinterpret_cast<const float2 *>(&g.gam[tok0 + 8 * n + 2 * tq]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) b[n][e] = p.scale * fmaf(e & 1 ? gam.y : gam.x, a[n][e], b[n][e]);
+                        for (int e = 0; e < 4; ++e) b[n][e] = p.scale * (o[h][n][e] + b[n][e]);
                         f[2 * n] = ptx::pack_bf16(b[n][0], b[n][1]);
                         f[2 * n + 1] = ptx::pack_bf16(b[n][2], b[n][3]);
                     }
 #pragma unroll
                     for (int n = 0; n < 4; n += 2) {
-                        const int tok = tok0 + 8 * n + (lane >> 4) * 8 + (lane & 7), ch = dv0 + ((lane >> 3) & 1) * 8;
-                        store_matrices_t(base + L::O + gdr::key_off(tok, ch), f + 2 * n);
+                        const int tok = tok0 + 8 * n + (lane >> 4) * 8 + (lane & 7), at = dv0 + ((lane >> 3) & 1) * 8;
+                        store_matrices_t(base + L::O + gdr::key_off(tok, at), f + 2 * n);
                     }
                 }
             ptx::tc_fence_before();
-            warp_arrive(bar(L::OEmpty));
-            warp_arrive(bar(L::GEmpty + c % L::kGates));
+            warp_arrive(bar(L::O2Empty));
             ptx::named_sync(2, 128);
             const int rows = rows_of(c);
-            __nv_bfloat16 *o = out + (int64_t)c * C * row_stride;
-            for (int i = ot; i < rows * groups; i += 128) {
-                const int r = i / groups, ch = (i - r * groups) * 8;
-                const uint4 x = *reinterpret_cast<const uint4 *>(smem + L::O + gdr::key_off(r, ch));
-                __nv_bfloat16 *to = o + r * row_stride + ch;
-                if (wide_out) {
-                    *reinterpret_cast<uint4 *>(to) = x;
-                } else {
-                    const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+            __nv_bfloat16 *to = out + ((int64_t)c * C + (ot >> 4)) * row_stride + ch;
+            if (ch < p.d_v)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (ch + j < p.d_v) reinterpret_cast<uint16_t *>(to)[j] = (uint16_t)(e[j >> 1] >> (16 * (j & 1)));
+                for (int i = 0; i < 8; ++i, to += 8 * row_stride) {
+                    const int r = (ot >> 4) + 8 * i;
+                    if (r >= rows) break;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(smem + L::O + gdr::key_off(r, ch));
+                    if (wide_out) {
+                        *reinterpret_cast<uint4 *>(to) = x;
+                    } else {
+                        const uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (ch + j < p.d_v) reinterpret_cast<uint16_t *>(to)[j] = (uint16_t)(e[j >> 1] >> (16 * (j & 1)));
+                    }
                 }
-            }
             ptx::named_sync(2, 128);
         }
     }

@@ -75,14 +75,18 @@ __device__ __forceinline__ void store_state(const float *st, float *to, int dv, 
 // the caller's [d_k][d_v] (NULL: zeros)
 template <int NC>
 __device__ __forceinline__ void load_given(float *st, const float *from, int d_k, int d_v, int dv, int c0) {
+    const int n = from && dv < d_v ? d_k - c0 : 0;
+    const float *x = from + (int64_t)c0 * d_v + dv;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) st[i] = from && dv < d_v && c0 + i < d_k ? from[(int64_t)(c0 + i) * d_v + dv] : 0.f;
+    for (int i = 0; i < NC; ++i, x += d_v) st[i] = i < n ? *x : 0.f;
 }
 template <int NC>
 __device__ __forceinline__ void store_given(const float *st, float *to, int d_k, int d_v, int dv, int c0) {
+    const int n = dv < d_v ? d_k - c0 : 0;
+    float *x = to + (int64_t)c0 * d_v + dv;
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-        if (dv < d_v && c0 + i < d_k) to[(int64_t)(c0 + i) * d_v + dv] = st[i];
+    for (int i = 0; i < NC; ++i, x += d_v)
+        if (i < n) *x = st[i];
 }
 
 // warps: 0 issues products, 1 forms gates, 2 and 3 load, 4..7 scale the keys, 8..15 hold the state
@@ -93,11 +97,11 @@ struct StateSmem {
     static constexpr int kKey = DK / 64 * kHalf, kVal = 2 * kHalf;
     static constexpr int K = 0, V = kKey, kStage = V + kVal;
     static constexpr int kStages = 4;
-    static constexpr int Kp = kStages * kStage, Gate = Kp + 2 * kKey;
+    static constexpr int Kp = kStages * kStage, Gate = Kp + 2 * 2 * kKey;  // two buffers of two planes
     static constexpr int kGates = 4;
-    static constexpr int Bars = Gate + kGates * (int)sizeof(TileGates);
+    static constexpr int Ring = Gate + kGates * (int)sizeof(TileGates), Bars = Ring + kAhead * C * 4;
     static constexpr int Full = 0, Empty = kStages, GFull = 2 * kStages, GEmpty = GFull + kGates, KpFull = GEmpty + kGates,
-                         KpEmpty = KpFull + 1, DsFull = KpEmpty + 1, DsEmpty = DsFull + 2, Drain = DsEmpty + 2, kBars = Drain + 1;
+                         KpEmpty = KpFull + 2, DsFull = KpEmpty + 2, DsEmpty = DsFull + 2, Drain = DsEmpty + 2, kBars = Drain + 1;
     static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;
     static_assert(kBytes <= 227 * 1024, "fits an SM");
 };
@@ -131,9 +135,9 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
             ptx::mbar_init(bar(L::GFull + i), 1);
             ptx::mbar_init(bar(L::GEmpty + i), 4 + 8);
         }
-        ptx::mbar_init(bar(L::KpFull), 4);
-        ptx::mbar_init(bar(L::KpEmpty), 1);
         for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(L::KpFull + i), 4);
+            ptx::mbar_init(bar(L::KpEmpty + i), 1);
             ptx::mbar_init(bar(L::DsFull + i), 1);
             ptx::mbar_init(bar(L::DsEmpty + i), 8);
         }
@@ -152,39 +156,34 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
     bool ok = true;
     auto wait = [&](int b, int parity) { ok = wait_bar(bar(b), parity & 1) && ok; };
     if (warp == 0) {
-        if (lane == 0) {
-            constexpr uint32_t id = ptx::idesc_bf16(128, DK, 1, 1);
-            for (int n = 0; n < nc; ++n) {
-                const int s = n % S;
-                wait(L::KpFull, n);
-                if (n >= 2) wait(L::DsEmpty + (n & 1), (n >> 1) - 1);
-                ptx::tc_fence_after();
-                const uint64_t v = ptx::sdesc_sw128(base + s * L::kStage + L::V, kHalf, 1024);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int k = 0; k < C / 16; ++k)
-                        ptx::umma_ss(tmem + (n & 1) * 128, v + 128 * k, ptx::sdesc_sw128(base + L::Kp + i * L::kKey, kHalf, 1024) + 128 * k,
-                                     id, i + k > 0);
-                ptx::umma_commit(bar(L::DsFull + (n & 1)));
-                ptx::umma_commit(bar(L::KpEmpty));
-                ptx::umma_commit(bar(L::Empty + s));
-            }
-            ptx::umma_commit(bar(L::Drain));
-            drain_bar(bar(L::Drain), 0);
-        }
-    } else if (warp == 1) {
-        float g[2];
-        fetch_gates(p, sg.t0 + (int64_t)tile(0) * C, rows_of(tile(0)), head, g);
+        constexpr uint32_t id = ptx::idesc_bf16(128, DK, 1, 1);
+        const uint32_t leader = ptx::elect_one();
+        const uint64_t v0 = ptx::sdesc_sw128(base + L::V, kHalf, 1024), kp = ptx::sdesc_sw128(base + L::Kp, kHalf, 1024);
+        int s = 0;
+#pragma unroll 1
         for (int n = 0; n < nc; ++n) {
-            float next[2] = {0.f, 0.f};
-            if (n + 1 < nc) fetch_gates(p, sg.t0 + (int64_t)tile(n + 1) * C, rows_of(tile(n + 1)), head, next);
-            if (n >= L::kGates) wait(L::GEmpty + n % L::kGates, n / L::kGates - 1);
-            form_gates<REV>(g, p.scale, gate(n));
-            warp_arrive(bar(L::GFull + n % L::kGates));
-            g[0] = next[0];
-            g[1] = next[1];
+            wait(L::KpFull + (n & 1), n >> 1);
+            if (n >= 2) wait(L::DsEmpty + (n & 1), (n >> 1) - 1);
+            ptx::tc_fence_after();
+            const uint32_t at = (uint32_t)s * (L::kStage / 16), key = (uint32_t)(n & 1) * (2 * L::kKey / 16);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < C / 16; ++k)
+                    ptx::umma_ss_by(leader, tmem + (n & 1) * 128, v0 + (at + 128 * k), kp + (key + i * L::kKey / 16 + 128 * k), id,
+                                    i + k > 0);
+            ptx::umma_commit_by(leader, bar(L::DsFull + (n & 1)));
+            ptx::umma_commit_by(leader, bar(L::KpEmpty + (n & 1)));
+            ptx::umma_commit_by(leader, bar(L::Empty + s));
+            if (++s == S) s = 0;
         }
+        ptx::umma_commit_by(leader, bar(L::Drain));
+        drain_bar(bar(L::Drain), 0);
+    } else if (warp == 1) {
+        walk_gates<REV>(
+            p, reinterpret_cast<float *>(smem + L::Ring), sg.t0, head, nc, tile, rows_of, gate,
+            [&](int n) { if (n >= L::kGates) wait(L::GEmpty + n % L::kGates, n / L::kGates - 1); },
+            [&](int n) { warp_arrive(bar(L::GFull + n % L::kGates)); });
     } else if (warp < 4) {
         const Source k{&tm_key, static_cast<const __nv_bfloat16 *>(REV ? p.q : p.k), REV ? p.q_stride : p.k_stride, kh, p.d_k,
                        DK / 64, REV ? plan.vec_q : plan.vec_k};
@@ -220,10 +219,10 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
             const int s = n % S;
             wait(L::GFull + n % L::kGates, n / L::kGates);
             wait(L::Full + s, n / S);
-            if (n > 0) wait(L::KpEmpty, n - 1);
-            scale_rows(smem + s * L::kStage + L::K, smem + L::Kp, L::kKey, *gate(n), L::kKey, tid - 128, 128);
+            if (n >= 2) wait(L::KpEmpty + (n & 1), (n >> 1) - 1);
+            scale_rows(smem + s * L::kStage + L::K, smem + L::Kp + (n & 1) * 2 * L::kKey, L::kKey, *gate(n), L::kKey, tid - 128, 128);
             ptx::fence_proxy_async();
-            warp_arrive(bar(L::KpFull));
+            warp_arrive(bar(L::KpFull + (n & 1)));
             warp_arrive(bar(L::Empty + s));
             warp_arrive(bar(L::GEmpty + n % L::kGates));
         }

@@ -20,9 +20,9 @@ constexpr long long kWaitLimit = 4000000000LL;  // SM cycles, about two seconds
 
 static __device__ unsigned int g_dla_flags;  // bit 5: a pipeline wait exceeded its limit
 
-// Bounded wait. False when this or any other wait of the grid gave up.
-__device__ __forceinline__ bool wait_bar(uint32_t a, uint32_t parity) {
-    if (ptx::mbar_try(a, parity)) return true;
+// Bounded wait. False when this or any other wait of the grid gave up. Its loop is a call: the
+// kernels' dozens of waits inlined made them 100 KB long, and their warps wait for instructions as it is.
+static __device__ __noinline__ bool wait_longer(uint32_t a, uint32_t parity) {
     const long long t0 = clock64();
     for (uint32_t it = 1;; ++it) {
         if (ptx::mbar_try(a, parity)) return true;
@@ -34,6 +34,9 @@ __device__ __forceinline__ bool wait_bar(uint32_t a, uint32_t parity) {
             }
         }
     }
+}
+__device__ __forceinline__ bool wait_bar(uint32_t a, uint32_t parity) {
+    return ptx::mbar_try(a, parity) || wait_longer(a, parity);
 }
 // for copies and products in flight after a failed wait: waits for them whatever the flag says
 static __device__ __noinline__ void drain_bar(uint32_t a, uint32_t parity) {
@@ -120,7 +123,7 @@ __device__ __forceinline__ void tile_by_copy(const Source &s, uint32_t dst, int6
     for (int h = 0; h < s.halves; ++h) ptx::tma_load_3d(dst + h * kHalf, s.map, h * 64, s.head, (int)t0, mbar);
 }
 // the same by threads, rows past the end as zeros
-__device__ __forceinline__ void tile_by_threads(const Source &s, uint32_t dst, int64_t t0, int rows, int tid, int n) {
+static __device__ __noinline__ void tile_by_threads(const Source s, uint32_t dst, int64_t t0, int rows, int tid, int n) {
     const __nv_bfloat16 *p = s.base + t0 * s.stride + (int64_t)s.head * s.d;
     for (int h = 0; h < s.halves; ++h)
         gdr::load_tile<__nv_bfloat16, 128>(dst + h * kHalf, 0, p + h * 64, s.stride, rows, s.d - h * 64, s.vec, tid, n);
@@ -150,36 +153,72 @@ __device__ __forceinline__ uint2 planes_of(float x) {
     const uint32_t hi = ptx::pack_bf16(x, x), lo = ptx::pack_bf16(x - gdr::lo_f(hi), x - gdr::lo_f(hi));
     return make_uint2(hi, lo);
 }
-// a tile's gates' inputs, two tokens a lane, ahead of their use
-__device__ __forceinline__ void fetch_gates(const DlaArgs &p, int64_t t0, int len, int head, float *g) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r = 2 * (threadIdx.x & 31) + i;
-        g[i] = r < len ? p.g[(t0 + r) * p.g_stride + head] : 0.f;
-    }
+// Sums of g log2(e) in fixed point, 40 bits behind the point: exact, so that differences of
+// neighbours stay exact after a long run of strong decays, and a scan's step is one addition (in two
+// floats the six dependent additions of a two-sum made it the longest chain of a tile).
+__device__ __forceinline__ int64_t fixed_exponent(float g) {
+    const Two x = decay_exponent(g);
+    return __float2ll_rn(x.hi * 1099511627776.f) + __float2ll_rn(x.lo * 1099511627776.f);
 }
-// del: REV: factor gam (the reverse walk's keys are scale gamma q), else delta past the tile, and
-// past `after` as well
+__device__ __forceinline__ float from_fixed(int64_t x) { return __ll2float_rn(x) * 9.094947017729282e-13f; }
+// REV: del is the factor scale gam (the reverse walk's keys are scale gam q), else the decay past a token
 template <bool REV>
-__device__ __forceinline__ void form_gates(const float *g, float scale, TileGates *out) {
+__device__ __forceinline__ void form_gates(float2 g, float scale, TileGates *out) {
     const int lane = threadIdx.x & 31;
-    Two s[2];
+    const int64_t first = fixed_exponent(g.x), both = first + fixed_exponent(g.y);
+    int64_t run = both;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) s[i] = decay_exponent(g[i]);
-    s[1] = add(s[0], s[1]);
-    const Two run = warp_scan(s[1]), total = last_lane(run);
-    Two before = up(run, 1);
-    if (lane == 0) before = {0.f, 0.f};
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, run, 31);
+    const int64_t G[2] = {run - both + first, run};
+    float2 at[2];
+    float gam[2];
+    uint2 del[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = 2 * lane + i;
-        const Two G = i ? run : add(before, s[0]);
-        const float gam = exp2_of(G);
-        out->G[r] = make_float2(G.hi, G.lo);
-        out->gam[r] = gam;
-        out->del[r] = planes_of(REV ? scale * gam : ex2((total.hi - G.hi) + (total.lo - G.lo)));
+        const float hi = from_fixed(G[i]);
+        at[i] = make_float2(hi, from_fixed(G[i] - __float2ll_rn(hi * 1099511627776.f)));
+        gam[i] = ex2(hi);
+        del[i] = planes_of(REV ? scale * gam[i] : ex2(from_fixed(total - G[i])));
     }
-    if (lane == 0) out->whole = exp2_of(total);
+    *reinterpret_cast<float4 *>(&out->G[2 * lane]) = make_float4(at[0].x, at[0].y, at[1].x, at[1].y);
+    *reinterpret_cast<float2 *>(&out->gam[2 * lane]) = make_float2(gam[0], gam[1]);
+    *reinterpret_cast<uint4 *>(&out->del[2 * lane]) = make_uint4(del[0].x, del[0].y, del[1].x, del[1].y);
+    if (lane == 0) out->whole = ex2(from_fixed(total));
+}
+// Every tile's gates, by one warp. Their inputs go to `ring` (kAhead tiles of 64 floats) kAhead tiles
+// ahead by asynchronous copies: a fetch takes longer than a tile's products. tile(n): the n-th tile of
+// the walk; rows(c): its tokens; slot(n), ready(n) and done(n): where its gates go, the wait for that
+// slot and the hand-over.
+constexpr int kAhead = 8;
+template <bool REV, typename Tile, typename Rows, typename Slot, typename Ready, typename Done>
+__device__ __forceinline__ void walk_gates(const DlaArgs &p, float *ring, int64_t t0, int head, int nc, Tile tile, Rows rows,
+                                           Slot slot, Ready ready, Done done) {
+    const int r = 2 * (threadIdx.x & 31);
+    auto fetch = [&](int n) {
+        if (n < nc) {
+            const int c = tile(n), len = rows(c);
+            const float *g = p.g + (t0 + (int64_t)c * C + r) * p.g_stride + head;
+            const uint32_t to = ptx::smem_u32(ring + n % kAhead * C + r);
+            ptx::cp_async_4(to, r < len ? g : p.g, r < len ? 4 : 0);
+            ptx::cp_async_4(to + 4, r + 1 < len ? g + p.g_stride : p.g, r + 1 < len ? 4 : 0);
+        }
+        ptx::cp_async_commit();
+    };
+#pragma unroll 1
+    for (int n = 0; n < kAhead - 1; ++n) fetch(n);
+#pragma unroll 1
+    for (int n = 0; n < nc; ++n) {
+        fetch(n + kAhead - 1);
+        gdr::cp_async_wait<kAhead - 1>();
+        const float2 g = *reinterpret_cast<const float2 *>(ring + n % kAhead * C + r);  // this lane's own copies
+        ready(n);
+        form_gates<REV>(g, p.scale, slot(n));
+        done(n);
+    }
 }
 
 // The planes of a tile's rows times their factors: hi = k d, lo the rest of the product and k times
