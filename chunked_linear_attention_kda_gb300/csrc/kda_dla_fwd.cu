@@ -6,10 +6,12 @@
 // every product has 128 rows:
 //   Q K^T                        64 x 64, both tiles as they were copied
 //   O1 = S^T Q^T                 S^T as two bf16 planes in tensor memory (the A operand)
-//   O2 = V^T P^T                 P = e Q K^T as two planes in shared memory
-//   dS^T = V^T K'                K' = delta K as two planes in shared memory
-//   o = scale (gamma O1 + O2),  S^T <- Gamma S^T + dS^T
-// The state is converted once a tile, off the products' path: what waits for it is O1 alone.
+//   O2 = V^T P^T                 P = scale e Q K^T as two planes in shared memory
+//   dS^T = V'^T K                V' = delta V as two planes in tensor memory
+//   o = scale gamma O1 + O2,  S^T <- Gamma S^T + dS^T
+// The state is converted once a tile, off the products' path: what waits for it is O1 alone. Shared
+// memory's 128 bytes a cycle bound a tile (the operands of the products, V' and P formed, the output
+// turned): what can be is an A operand in tensor memory.
 //
 // A long sequence is cut into segments, so that few heads fill the GPU: a first launch forms what
 // each segment adds to the state (kda_dla_states.h: K and V are read once more), a second one the
@@ -22,28 +24,29 @@ namespace kda {
 namespace dla {
 namespace {
 
-// warps: 0 issues products, 1 forms gates, 2 and 3 load, 4..7 K' and P, 8..15 the state, 16..19 the output
-constexpr int kFwdThreads = 640;
+// warps: 0 and 1 issue products, 2 and 3 load, 4..7 scale values, 8..15 form P, 16..23 hold the state, 24..31 the output
+constexpr int kFwdThreads = 1024;
+// Registers a thread has at launch, and each warpgroup's after it gave away or took some: together what
+// the block was launched with.
+constexpr int kRegsLaunch = 64, kRegsServe = 40, kRegsPairs = 56, kRegsState = 96, kRegsOut = 64;
+static_assert(2 * (kRegsServe + kRegsPairs + kRegsState + kRegsOut) == 8 * kRegsLaunch, "the launch's registers");
 
 template <int DK>
 struct FwdSmem {
     static constexpr int kKey = DK / 64 * kHalf, kVal = 2 * kHalf;
-    static constexpr int Q = 0, K = kKey, V = 2 * kKey, kStage = V + kVal;
+    static constexpr int Q = 0, K = kKey, V = 2 * kKey, Gate = V + kVal, kStage = Gate + 2048;
     static constexpr int kStages = 3;
-    static constexpr int Kp = kStages * kStage, P = Kp + 2 * kKey, O = P + 2 * kHalf, Gate = O + 2 * kHalf;
-    static constexpr int kGates = 4;
-    static constexpr int Ring = Gate + kGates * (int)sizeof(TileGates), Bars = Ring + kAhead * C * 4;
-    // full, empty [stages], gates full, empty [4], QK full, empty [2], then one each
-    static constexpr int Full = 0, Empty = kStages, GFull = 2 * kStages, GEmpty = GFull + kGates, QkFull = GEmpty + kGates,
-                         QkEmpty = QkFull + 2, PFull = QkEmpty + 2, PEmpty = PFull + 1, KpFull = PEmpty + 1,
-                         KpEmpty = KpFull + 1, DsFull = KpEmpty + 1, DsEmpty = DsFull + 1, SFull = DsEmpty + 1,
-                         SEmpty = SFull + 1, O1Empty = SEmpty + 1, O2Full = O1Empty + 1, O2Empty = O2Full + 1, Drain = O2Empty + 1,
-                         kBars = Drain + 1;
+    static constexpr int P = kStages * kStage, O = P + 2 * kHalf, Bars = O + 2 * kHalf;
+    // full, empty [stages], then one each, but QK and O2 full, which alternate: either may be formed a tile
+    // before the last one was seen, and a phase's parity tells neighbours apart only
+    static constexpr int Full = 0, Empty = kStages, QkFull = 2 * kStages, PFull = QkFull + 2, PEmpty = PFull + 1,
+                         VpFull = PEmpty + 1, VpEmpty = VpFull + 1, DsFull = VpEmpty + 1, DsEmpty = DsFull + 1, SFull = DsEmpty + 1, O1Full = SFull + 1, O1Empty = O1Full + 1,
+                         O2Full = O1Empty + 1, O2Empty = O2Full + 2, Drain = O2Empty + 1, kBars = Drain + 2;
     static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;  // the base is rounded up to 1024
-    static_assert(kBytes <= 227 * 1024, "fits an SM");
+    static_assert(sizeof(TileGates) <= 2048 && kBytes <= 227 * 1024, "fits an SM");
 };
 // columns of tensor memory
-constexpr int kTmDs = 0, kTmS = 128, kTmO1 = 256, kTmO2 = 320, kTmQk = 384;
+constexpr int kTmDs = 0, kTmS = 128, kTmO1 = 256, kTmV = 320, kTmQk = 384;  // kTmQk: Q K^T, then O2, of two tiles
 
 template <int DK>
 __global__ void __launch_bounds__(kFwdThreads, 1)
@@ -55,7 +58,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     extern __shared__ __align__(1024) char smem_raw[];
     char *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_u32(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // equal over a warp, and told to the compiler so: branches and loops on them keep operands in
+    // uniform registers
+    auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int head = blockIdx.x % p.n_heads, kh = head / (p.n_heads / p.n_k_heads);
     const int64_t slot = blockIdx.x / p.n_heads;
     const Segment sg = find_segment(p.cu_seqlens, p.n_seq, slot, plan.seg);
@@ -65,37 +71,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             for (int i = tid; i < p.d_k * p.d_v; i += kFwdThreads) p.h_final[state_at + i] = p.h0 ? p.h0[state_at + i] : 0.f;
         return;
     }
-    const int nc = (int)((sg.len + C - 1) / C);
-    const bool keep_end = sg.last && p.h_final;  // else the last tile adds to no state
+    const int nc = uniform((int)((sg.len + C - 1) / C));
+    const bool keep_end = uniform(sg.last) && p.h_final;  // else the last tile adds to no state
     auto bar = [&](int i) { return base + L::Bars + 8 * i; };
-    auto gate = [&](int c) { return reinterpret_cast<TileGates *>(smem + L::Gate) + c % L::kGates; };
+    auto gate = [&](int c) -> const TileGates & {  // in the tile's stage
+        return *reinterpret_cast<const TileGates *>(smem + c % S * L::kStage + L::Gate);
+    };
     auto rows_of = [&](int c) { return (int)min((int64_t)C, sg.len - (int64_t)c * C); };
 
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             ptx::mbar_init(bar(L::Full + i), 1);
-            ptx::mbar_init(bar(L::Empty + i), 1 + 4);
+            ptx::mbar_init(bar(L::Empty + i), 2 + 4 + 8 + 8 + 8);  // products, keys, P, state, output
         }
-        for (int i = 0; i < L::kGates; ++i) {
-            ptx::mbar_init(bar(L::GFull + i), 1);
-            ptx::mbar_init(bar(L::GEmpty + i), 4 + 8 + 4);
-        }
-        for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(bar(L::QkFull + i), 1);
-            ptx::mbar_init(bar(L::QkEmpty + i), 4);
-        }
-        ptx::mbar_init(bar(L::PFull), 4);
+        ptx::mbar_init(bar(L::QkFull), 1);
+        ptx::mbar_init(bar(L::QkFull + 1), 1);
+        ptx::mbar_init(bar(L::PFull), 8);
         ptx::mbar_init(bar(L::PEmpty), 1);
-        ptx::mbar_init(bar(L::KpFull), 4);
-        ptx::mbar_init(bar(L::KpEmpty), 1);
+        ptx::mbar_init(bar(L::VpFull), 4);
+        ptx::mbar_init(bar(L::VpEmpty), 1);
         ptx::mbar_init(bar(L::DsFull), 1);
         ptx::mbar_init(bar(L::DsEmpty), 8);
         ptx::mbar_init(bar(L::SFull), 8);
-        ptx::mbar_init(bar(L::SEmpty), 1);
-        ptx::mbar_init(bar(L::O1Empty), 4);
+        ptx::mbar_init(bar(L::O1Full), 1);
+        ptx::mbar_init(bar(L::O1Empty), 8);
         ptx::mbar_init(bar(L::O2Full), 1);
-        ptx::mbar_init(bar(L::O2Empty), 4);
+        ptx::mbar_init(bar(L::O2Full + 1), 1);
+        ptx::mbar_init(bar(L::O2Empty), 8);
         ptx::mbar_init(bar(L::Drain), 1);
+        ptx::mbar_init(bar(L::Drain + 1), 1);
         ptx::mbar_init_fence();
     }
     if (warp == 0) ptx::tmem_alloc(bar(L::kBars), 512);
@@ -115,134 +119,166 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     auto wait = [&](int b, int parity) { ok = wait_bar(bar(b), parity & 1) && ok; };
 
     if (warp == 0) {
-        // The whole warp walks, one lane issues: operands by offsets in uniform registers.
+        ptx::regs_decrease<kRegsServe>();
+        // Q K^T a tile ahead, and O1. Two warps issue, because a product takes its warp 40 to 70 cycles to issue
+        // and a tile has 40 of them. The whole warp walks, an elected lane issues: operands are formed in
+        // uniform registers.
         constexpr uint32_t id_qk = ptx::idesc_bf16(64, C, 0, 0), id_o1 = ptx::idesc_bf16(128, C, 0, 0);
-        constexpr uint32_t id_o2 = ptx::idesc_bf16(128, C, 1, 0), id_ds = ptx::idesc_bf16(128, DK, 1, 1);
         const uint32_t leader = ptx::elect_one();
         const uint64_t q0 = ptx::sdesc_sw128(base + L::Q, 16, 1024), k0 = ptx::sdesc_sw128(base + L::K, 16, 1024);
-        const uint64_t v0 = ptx::sdesc_sw128(base + L::V, kHalf, 1024), kp = ptx::sdesc_sw128(base + L::Kp, kHalf, 1024);
-        const uint64_t pp = ptx::sdesc_sw128(base + L::P, 16, 1024);
         auto step = [](int k) { return (uint32_t)((k >> 2) * kHalf + (k & 3) * 32) / 16; };  // 16 channels, K-major
         int next = 0, next_phase = 0;  // the stage of the next Q K^T
-        auto pairs = [&](int c) {
-            wait(L::Full + next, next_phase);
-            if (c >= 2) wait(L::QkEmpty + (c & 1), (c >> 1) - 1);
-            ptx::tc_fence_after();
-            const uint32_t at = (uint32_t)next * (L::kStage / 16);
+        int s = 0;
+#pragma unroll 1
+        for (int c = -1; c < nc; ++c) {
+            if (c + 1 < nc) {
+                wait(L::Full + next, next_phase);
+                if (c >= 1) wait(L::O2Empty, c - 1);  // the columns
+                ptx::tc_fence_after();
+                const uint32_t at = (uint32_t)next * (L::kStage / 16);
+                if (leader) {
 #pragma unroll
-            for (int k = 0; k < DK / 16; ++k)
-                ptx::umma_ss_by(leader, tmem + kTmQk + (c & 1) * C, q0 + (at + step(k)), k0 + (at + step(k)), id_qk, k > 0);
-            ptx::umma_commit_by(leader, bar(L::QkFull + (c & 1)));
-            if (++next == S) {
-                next = 0;
-                next_phase ^= 1;
+                    for (int k = 0; k < DK / 16; ++k)
+                        ptx::umma_ss(tmem + kTmQk + ((c + 1) & 1) * C, q0 + (at + step(k)), k0 + (at + step(k)), id_qk, k > 0);
+                    ptx::umma_commit(bar(L::QkFull + ((c + 1) & 1)));
+                }
+                __syncwarp();
+                if (++next == S) {
+                    next = 0;
+                    next_phase ^= 1;
+                }
             }
-        };
-        pairs(0);
+            if (c < 0) continue;
+            wait(L::SFull, c);
+            if (c > 0) wait(L::O1Empty, c - 1);
+            ptx::tc_fence_after();
+            const uint32_t at = (uint32_t)s * (L::kStage / 16);
+            if (leader) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int k = 0; k < DK / 16; ++k)
+                        ptx::umma_ts(tmem + kTmO1, tmem + kTmS + i * (DK / 2) + 8 * k, q0 + (at + step(k)), id_o1, i + k > 0);
+                ptx::umma_commit(bar(L::O1Full));
+                ptx::umma_commit(bar(L::Empty + s));
+            }
+            __syncwarp();
+            if (++s == S) s = 0;
+        }
+        if (leader) ptx::umma_commit(bar(L::Drain));
+        __syncwarp();
+        drain_bar(bar(L::Drain), 0);
+    } else if (warp == 1) {
+        ptx::regs_decrease<kRegsServe>();
+        // dS^T and O2
+        constexpr uint32_t id_o2 = ptx::idesc_bf16(128, C, 1, 0), id_ds = ptx::idesc_bf16(128, DK, 0, 1);
+        const uint32_t leader = ptx::elect_one();
+        const uint64_t v0 = ptx::sdesc_sw128(base + L::V, kHalf, 1024), k0 = ptx::sdesc_sw128(base + L::K, kHalf, 1024);
+        const uint64_t pp = ptx::sdesc_sw128(base + L::P, 16, 1024);
         int s = 0;
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
-            // in the order in which their operands come: dS^T is waited for by the state's warps while
-            // O1 is formed, and O1 by the next tile's planes of S
-            if (c + 1 < nc) pairs(c + 1);
             const uint32_t at = (uint32_t)s * (L::kStage / 16);
+            wait(L::Full + s, c / S);
             if (c + 1 < nc || keep_end) {
-                wait(L::KpFull, c);
+                wait(L::VpFull, c);
                 if (c > 0) wait(L::DsEmpty, c - 1);
                 ptx::tc_fence_after();
+                if (leader) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int k = 0; k < C / 16; ++k)
+                            ptx::umma_ts(tmem + kTmDs, tmem + kTmV + i * 32 + 8 * k, k0 + (at + 128 * k), id_ds, i + k > 0);
+                    ptx::umma_commit(bar(L::DsFull));
+                    ptx::umma_commit(bar(L::VpEmpty));
+                }
+                __syncwarp();
+            }
+            wait(L::PFull, c);
+            ptx::tc_fence_after();
+            if (leader) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
-                        ptx::umma_ss_by(leader, tmem + kTmDs, v0 + (at + 128 * k), kp + (i * L::kKey / 16 + 128 * k), id_ds, i + k > 0);
-                ptx::umma_commit_by(leader, bar(L::DsFull));
-                ptx::umma_commit_by(leader, bar(L::KpEmpty));
+                        ptx::umma_ss(tmem + kTmQk + (c & 1) * C, v0 + (at + 128 * k), pp + (i * kHalf + k * 32) / 16, id_o2, i + k > 0);
+                ptx::umma_commit(bar(L::O2Full + (c & 1)));
+                ptx::umma_commit(bar(L::PEmpty));
+                ptx::umma_commit(bar(L::Empty + s));
             }
-            wait(L::SFull, c);
-            if (c > 0) wait(L::O1Empty, c - 1);
-            ptx::tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int k = 0; k < DK / 16; ++k)
-                    ptx::umma_ts_by(leader, tmem + kTmO1, tmem + kTmS + i * (DK / 2) + 8 * k, q0 + (at + step(k)), id_o1, i + k > 0);
-            ptx::umma_commit_by(leader, bar(L::SEmpty));
-            wait(L::PFull, c);
-            if (c > 0) wait(L::O2Empty, c - 1);
-            ptx::tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int k = 0; k < C / 16; ++k)
-                    ptx::umma_ss_by(leader, tmem + kTmO2, v0 + (at + 128 * k), pp + (i * kHalf + k * 32) / 16, id_o2, i + k > 0);
-            ptx::umma_commit_by(leader, bar(L::O2Full));
-            ptx::umma_commit_by(leader, bar(L::PEmpty));
-            ptx::umma_commit_by(leader, bar(L::Empty + s));
+            __syncwarp();
             if (++s == S) s = 0;
         }
-        ptx::umma_commit_by(leader, bar(L::Drain));
-        drain_bar(bar(L::Drain), 0);
-    } else if (warp == 1) {
-        walk_gates<false>(
-            p, reinterpret_cast<float *>(smem + L::Ring), sg.t0, head, nc, [](int n) { return n; }, rows_of, gate,
-            [&](int n) { if (n >= L::kGates) wait(L::GEmpty + n % L::kGates, n / L::kGates - 1); },
-            [&](int n) { warp_arrive(bar(L::GFull + n % L::kGates)); });
+        if (leader) ptx::umma_commit(bar(L::Drain + 1));
+        __syncwarp();
+        drain_bar(bar(L::Drain + 1), 0);
     } else if (warp < 4) {
-        const Source q{&tm_q, static_cast<const __nv_bfloat16 *>(p.q), p.q_stride, kh, p.d_k, DK / 64, plan.vec_q};
-        const Source k{&tm_k, static_cast<const __nv_bfloat16 *>(p.k), p.k_stride, kh, p.d_k, DK / 64, plan.vec_k};
-        const Source v{&tm_v, static_cast<const __nv_bfloat16 *>(p.v), p.v_stride, head, p.d_v, p.d_v > 64 ? 2 : 1, plan.vec_v};
-        int copied = 0;  // tiles whose copies were begun
+        ptx::regs_decrease<kRegsServe>();
+        const Source in[3] = {{&tm_k, static_cast<const __nv_bfloat16 *>(p.k), p.k_stride, kh, p.d_k, DK / 64, plan.vec_k},
+                              {&tm_q, static_cast<const __nv_bfloat16 *>(p.q), p.q_stride, kh, p.d_k, DK / 64, plan.vec_q},
+                              {&tm_v, static_cast<const __nv_bfloat16 *>(p.v), p.v_stride, head, p.d_v, p.d_v > 64 ? 2 : 1, plan.vec_v}};
+        const TileGates *gates = gates_of(plan.gates, p, sg.seq, (int64_t)sg.index * (plan.seg / C), head);
+        int begun = 0;  // tiles whose copies were begun
+#pragma unroll 1
         for (int c = 0; c < nc; ++c) {
             const int s = c % S, rows = rows_of(c);
             if (c >= S) wait(L::Empty + s, c / S - 1);
             ok = __all_sync(0xffffffffu, ok);
-            const uint32_t at = base + s * L::kStage;
+            const uint32_t at = base + s * L::kStage, m = bar(L::Full + s);
             const int64_t t0 = sg.t0 + (int64_t)c * C;
-            if (copies && rows == C) {
-                if (ok && warp == 2 && lane == 0) {
-                    const uint32_t m = bar(L::Full + s);
-                    ptx::mbar_arrive_tx(m, 2 * L::kKey + v.halves * kHalf);
-                    tile_by_copy(k, at + L::K, t0, m);
-                    tile_by_copy(q, at + L::Q, t0, m);
-                    tile_by_copy(v, at + L::V, t0, m);
-                    copied = c + 1;
+            const bool copy = copies && rows == C;
+            if (!copy) {
+                const uint32_t to[3] = {at + L::K, at + L::Q, at + L::V};
+                if (ok) tiles_by_threads(in, to, 3, t0, rows, tid - 64, 64);
+                rows_loaded(64);
+            }
+            if (ok && tid == 64) {
+                ptx::mbar_arrive_tx(m, (uint32_t)sizeof(TileGates) + (copy ? 2 * L::kKey + in[2].halves * kHalf : 0));
+                if (copy) {
+                    tile_by_copy(in[0], at + L::K, t0, m);
+                    tile_by_copy(in[1], at + L::Q, t0, m);
+                    tile_by_copy(in[2], at + L::V, t0, m);
                 }
-            } else {
-                if (ok) {
-                    tile_by_threads(k, at + L::K, t0, rows, tid - 64, 64);
-                    tile_by_threads(q, at + L::Q, t0, rows, tid - 64, 64);
-                    tile_by_threads(v, at + L::V, t0, rows, tid - 64, 64);
-                }
-                tile_loaded(bar(L::Full + s));
+                if (c == 0) gdr::wait_for_previous_kernel();  // the gates
+                bulk_load(at + L::Gate, gates + (int64_t)c * p.n_heads, sizeof(TileGates), m);
+                begun = c + 1;
             }
         }
         // nothing may land in shared memory after the block has gone
         if (!ok)
-            for (int c = max(0, copied - S); c < copied; ++c) drain_bar(bar(L::Full + c % S), (c / S) & 1);
+            for (int c = max(0, begun - S); c < begun; ++c) drain_bar(bar(L::Full + c % S), (c / S) & 1);
     } else if (warp < 8) {
-        const int w = warp - 4, gr = lane >> 2, tq = lane & 3;
+        ptx::regs_decrease<kRegsServe>();
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+            const int s = c % S;
+            wait(L::Full + s, c / S);
+            if (c > 0) wait(L::VpEmpty, c - 1);
+            ptx::tc_fence_after();
+            scale_values(base + s * L::kStage + L::V, tmem, kTmV, gate(c).del, 1.f);
+            ptx::tc_fence_before();
+            warp_arrive(bar(L::VpFull));
+            warp_arrive(bar(L::Empty + s));
+        }
+    } else if (warp < 16) {
+        ptx::regs_decrease<kRegsPairs>();
+        // 16 rows by two warps, which take turns at its blocks of 16 columns
+        const int w = warp & 3, J0 = (warp - 8) >> 2, gr = lane >> 2, tq = lane & 3;
         const uint32_t lanes = tmem + ((uint32_t)(w * 32) << 16);
         const uint32_t put_at = base + L::P, row = 16 * w + ((lane >> 3) & 1) * 8 + (lane & 7), col8 = (lane >> 4) * 8;
-        auto keys = [&](int c) {  // K' of tile c
-            const int s = c % S;
-            wait(L::GFull + c % L::kGates, c / L::kGates);
-            wait(L::Full + s, c / S);
-            if (c > 0) wait(L::KpEmpty, c - 1);
-            scale_rows(smem + s * L::kStage + L::K, smem + L::Kp, L::kKey, *gate(c), L::kKey, tid - 128, 128);
-            ptx::fence_proxy_async();
-            warp_arrive(bar(L::KpFull));
-            warp_arrive(bar(L::Empty + s));
-        };
-        keys(0);
-        for (int c = 0; c < nc; ++c) {
-            const TileGates &g = *gate(c);
-            wait(L::QkFull + (c & 1), c >> 1);
-            ptx::tc_fence_after();
-            const int r0 = 16 * w + gr;
-            const float2 G0 = g.G[r0], G1 = g.G[r0 + 8];
-            if (c > 0) wait(L::PEmpty, c - 1);
+        const int r0 = 16 * w + gr;
 #pragma unroll 1
-            for (int J = 0; J <= w; ++J) {  // 16 columns; a loop that is not unrolled, see wait_longer
+        for (int c = 0; c < nc; ++c) {
+            const int s = c % S;
+            wait(L::Full + s, c / S);  // the gates
+            const TileGates &g = gate(c);
+            const float2 G0 = g.G[r0], G1 = g.G[r0 + 8];
+            wait(L::QkFull + (c & 1), c >> 1);
+            if (c > 0) wait(L::PEmpty, c - 1);
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int J = J0; J <= w; J += 2) {  // a loop that is not unrolled: warps wait for instructions
                 float x[2][4];
                 ptx::tmem_ld_frag2(lanes + kTmQk + (c & 1) * C + 16 * J, reinterpret_cast<uint32_t *>(x[0]));
                 ptx::tmem_ld_wait();
@@ -253,10 +289,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     const int col = 16 * J + 8 * n + 2 * tq;
                     const float4 Gc = *reinterpret_cast<const float4 *>(&g.G[col]);
                     const float2 a = make_float2(Gc.x, Gc.y), b = make_float2(Gc.z, Gc.w);
-                    d[0] = r0 >= col ? d[0] * exp2_between(G0, a) : 0.f;
-                    d[1] = r0 > col ? d[1] * exp2_between(G0, b) : 0.f;
-                    d[2] = r0 + 8 >= col ? d[2] * exp2_between(G1, a) : 0.f;
-                    d[3] = r0 + 8 > col ? d[3] * exp2_between(G1, b) : 0.f;
+                    d[0] = r0 >= col ? p.scale * d[0] * exp2_between(G0, a) : 0.f;
+                    d[1] = r0 > col ? p.scale * d[1] * exp2_between(G0, b) : 0.f;
+                    d[2] = r0 + 8 >= col ? p.scale * d[2] * exp2_between(G1, a) : 0.f;
+                    d[3] = r0 + 8 > col ? p.scale * d[3] * exp2_between(G1, b) : 0.f;
                     split(d[0], d[1], hi[2 * n], lo[2 * n]);
                     split(d[2], d[3], hi[2 * n + 1], lo[2 * n + 1]);
                 }
@@ -265,25 +301,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 store_matrices(at + kHalf, lo);
             }
             ptx::tc_fence_before();
-            warp_arrive(bar(L::QkEmpty + (c & 1)));
             ptx::fence_proxy_async();
             warp_arrive(bar(L::PFull));
-            warp_arrive(bar(L::GEmpty + c % L::kGates));
-            if (c + 1 < nc) keys(c + 1);
+            warp_arrive(bar(L::Empty + s));
         }
-    } else if (warp < 16) {
+    } else if (warp < 24) {
+        ptx::regs_increase<kRegsState>();
         constexpr int NC = DK / 2;  // key channels of a thread
-        const int dv = (warp & 3) * 32 + lane, part = (warp - 8) >> 2;
+        const int dv = (warp & 3) * 32 + lane, part = (warp - 16) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         float st[NC];
         const bool cut = sg.index > 0 || !sg.last;
         gdr::wait_for_previous_kernel();
-        if (cut) {
-            load_state<NC>(st, plan.states + ((size_t)slot * p.n_heads + head) * state_floats(DK), dv, part * NC);
-        } else {
-            load_given<NC>(st, p.h0 ? p.h0 + state_at : nullptr, p.d_k, p.d_v, dv, part * NC);
-        }
-        auto write_planes = [&] {
+        if (cut) load_state<NC>(st, plan.states + ((size_t)slot * p.n_heads + head) * state_floats(DK), dv, part * NC);
+        else load_given<NC>(st, p.h0 ? p.h0 + state_at : nullptr, p.d_k, p.d_v, dv, part * NC);
+#pragma unroll 1
+        for (int c = 0;; ++c) {
+            if (c > 0) {
+                wait(L::O1Full, c - 1);  // the last planes are read
+                ptx::tc_fence_after();
+            }
 #pragma unroll
             for (int i = 0; i < NC; i += 16) {
                 uint32_t hi[8], lo[8];
@@ -295,13 +332,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             warp_arrive(bar(L::SFull));
-        };
-        write_planes();
-        for (int c = 0; c < nc; ++c) {
             if (c + 1 == nc && !keep_end) break;
-            wait(L::GFull + c % L::kGates, c / L::kGates);
-            const float whole = gate(c)->whole;
-            warp_arrive(bar(L::GEmpty + c % L::kGates));
+            wait(L::Full + c % S, c / S);
+            const float whole = gate(c).whole;
+            warp_arrive(bar(L::Empty + c % S));
             wait(L::DsFull, c);
             ptx::tc_fence_after();
 #pragma unroll
@@ -315,75 +349,65 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             ptx::tc_fence_before();
             warp_arrive(bar(L::DsEmpty));
             if (c + 1 == nc) break;
-            wait(L::SEmpty, c);
-            ptx::tc_fence_after();
-            write_planes();
         }
         if (keep_end) store_given<NC>(st, p.h_final + state_at, p.d_k, p.d_v, dv, part * NC);
     } else {
-        const int w = warp - 16, tq = lane & 3, ot = tid - 512;
+        // 32 value channels x 32 tokens a warp
+        const int w = warp & 3, tok0 = 32 * ((warp - 24) >> 2), tq = lane & 3, ot = tid - 768;
         const bool live = 32 * w < p.d_v;
         const int64_t row_stride = (int64_t)p.n_heads * p.d_v;
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + sg.t0 * row_stride + (int64_t)head * p.d_v;
-        const int ch = (ot & 15) * 8;  // copied out: eight channels of every eighth token
+        const int ch = (ot & 15) * 8;  // copied out: eight channels of every sixteenth token
+        const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16) + tok0;
+#pragma unroll 1
         for (int c = 0; c < nc; ++c) {
-            const TileGates &g = *gate(c);
-            wait(L::GFull + c % L::kGates, c / L::kGates);
-            // 16 value channels x 32 tokens a time; O1 leaves tensor memory first
-            float o[4][4][4];
-            wait(L::SEmpty, c);  // O1 is formed
+            const int s = c % S;
+            wait(L::Full + s, c / S);
+            const TileGates &g = gate(c);
+            // O1 leaves tensor memory first
+            float o[2][4][4];
+            wait(L::O1Full, c);
             ptx::tc_fence_after();
             if (live) {
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    ptx::tmem_ld_frag4(tmem + ((uint32_t)(32 * w + 16 * (h & 1)) << 16) + kTmO1 + 32 * (h >> 1),
-                                       reinterpret_cast<uint32_t *>(o[h][0]));
+                ptx::tmem_ld_frag4(lanes + kTmO1, reinterpret_cast<uint32_t *>(o[0][0]));
+                ptx::tmem_ld_frag4(lanes + (16u << 16) + kTmO1, reinterpret_cast<uint32_t *>(o[1][0]));
                 ptx::tmem_ld_wait();
             }
             ptx::tc_fence_before();
             warp_arrive(bar(L::O1Empty));
-            if (live)
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        const float2 gam = *reinterpret_cast<const float2 *>(&g.gam[32 * (h >> 1) + 8 * n + 2 * tq]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[h][n][e] *= e & 1 ? gam.y : gam.x;
-                    }
-            warp_arrive(bar(L::GEmpty + c % L::kGates));
-            wait(L::O2Full, c);
+            wait(L::O2Full + (c & 1), c >> 1);
             ptx::tc_fence_after();
             if (live)
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    const int dv0 = 32 * w + 16 * (h & 1), tok0 = 32 * (h >> 1);
+                for (int h = 0; h < 2; ++h) {
                     float b[4][4];
-                    ptx::tmem_ld_frag4(tmem + ((uint32_t)dv0 << 16) + kTmO2 + tok0, reinterpret_cast<uint32_t *>(b[0]));
+                    ptx::tmem_ld_frag4(lanes + ((uint32_t)(16 * h) << 16) + kTmQk + (c & 1) * C, reinterpret_cast<uint32_t *>(b[0]));
                     ptx::tmem_ld_wait();
                     uint32_t f[8];
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
+                        const float2 gam = *reinterpret_cast<const float2 *>(&g.gam[tok0 + 8 * n + 2 * tq]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) b[n][e] = p.scale * (o[h][n][e] + b[n][e]);
+                        for (int e = 0; e < 4; ++e) b[n][e] = fmaf(e & 1 ? gam.y : gam.x, o[h][n][e], b[n][e]);
                         f[2 * n] = ptx::pack_bf16(b[n][0], b[n][1]);
                         f[2 * n + 1] = ptx::pack_bf16(b[n][2], b[n][3]);
                     }
 #pragma unroll
                     for (int n = 0; n < 4; n += 2) {
-                        const int tok = tok0 + 8 * n + (lane >> 4) * 8 + (lane & 7), at = dv0 + ((lane >> 3) & 1) * 8;
+                        const int tok = tok0 + 8 * n + (lane >> 4) * 8 + (lane & 7), at = 32 * w + 16 * h + ((lane >> 3) & 1) * 8;
                         store_matrices_t(base + L::O + gdr::key_off(tok, at), f + 2 * n);
                     }
                 }
             ptx::tc_fence_before();
             warp_arrive(bar(L::O2Empty));
-            ptx::named_sync(2, 128);
+            warp_arrive(bar(L::Empty + s));
+            ptx::named_sync(2, 256);
             const int rows = rows_of(c);
             __nv_bfloat16 *to = out + ((int64_t)c * C + (ot >> 4)) * row_stride + ch;
             if (ch < p.d_v)
 #pragma unroll
-                for (int i = 0; i < 8; ++i, to += 8 * row_stride) {
-                    const int r = (ot >> 4) + 8 * i;
+                for (int i = 0; i < 4; ++i, to += 16 * row_stride) {
+                    const int r = (ot >> 4) + 16 * i;
                     if (r >= rows) break;
                     const uint4 x = *reinterpret_cast<const uint4 *>(smem + L::O + gdr::key_off(r, ch));
                     if (wide_out) {
@@ -395,7 +419,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             if (ch + j < p.d_v) reinterpret_cast<uint16_t *>(to)[j] = (uint16_t)(e[j >> 1] >> (16 * (j & 1)));
                     }
                 }
-            ptx::named_sync(2, 128);
+            ptx::named_sync(2, 256);
         }
     }
     __syncwarp();
@@ -410,19 +434,12 @@ cudaError_t forward(const DlaArgs &p, cudaStream_t stream) {
                         TileMap::encode(&k, p.k, p.n_tok, p.k_stride, p.n_k_heads, p.d_k) &&
                         TileMap::encode(&v, p.v, p.n_tok, p.v_stride, p.n_heads, p.d_v);
     const bool wide = p.d_v % 8 == 0 && (uintptr_t)p.out % 16 == 0;
-    Plan plan = make_plan(p, false);
-    const unsigned blocks = (unsigned)(plan.slots * p.n_heads);
-    if (plan.cut) {
-        const cudaError_t e = launch_segments<DK>(p, plan, q, k, v, v, copies, false, stream);
-        if (e != cudaSuccess) return e;
-        return gdr::launch_dependent(dla_forward_kernel<DK>, dim3(blocks), kFwdThreads, FwdSmem<DK>::kBytes, stream, q, k, v, p,
-                                     plan, copies, wide);
-    }
-    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dla_forward_kernel<DK>), FwdSmem<DK>::kBytes);
+    const Plan plan = make_plan(p, false);
+    cudaError_t e = launch_gates(p, plan, stream);
+    if (e == cudaSuccess && plan.cut) e = launch_segments<DK>(p, plan, q, k, v, v, copies, false, stream);
     if (e != cudaSuccess) return e;
-    dla_forward_kernel<DK><<<blocks, kFwdThreads, FwdSmem<DK>::kBytes, stream>>>(q, k, v, p, plan, copies, wide);
-    count_launches(1);
-    return cudaGetLastError();
+    return gdr::launch_dependent(dla_forward_kernel<DK>, dim3((unsigned)(plan.slots * p.n_heads)), kFwdThreads, FwdSmem<DK>::kBytes,
+                                 stream, q, k, v, p, plan, copies, wide);
 }
 
 }  // namespace
@@ -439,7 +456,7 @@ cudaError_t launch_dla_fwd(const DlaArgs &p, cudaStream_t stream) {
 cudaError_t launch_dla_bwd(const DlaArgs &p, cudaStream_t stream) { return launch_dla_simt(p, true, stream); }
 
 size_t dla_tc_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k) {
-    return dla::plan_bytes(n_tok, n_seq, n_heads, d_k, false);
+    return dla::plan_bytes(n_tok, n_seq, n_heads, d_k);
 }
 
 cudaError_t launch_dla_tc_fwd(const DlaArgs &p, cudaStream_t stream) {

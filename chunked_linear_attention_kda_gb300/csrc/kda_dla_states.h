@@ -27,6 +27,7 @@ struct Plan {
     int64_t slots;       // of segments
     bool cut;            // some sequence may have more than one
     bool vec_q, vec_k, vec_v, vec_o;  // 16-byte rows
+    TileGates *gates;    // [tiles][heads]
     float *states;       // [slots][heads] states at the segments' starts (reverse: gradients at their ends)
     float *decays;       // [slots][heads] decays over the segments
 };
@@ -37,11 +38,14 @@ inline int segment_tiles(int64_t n_tok, int32_t n_heads) {
     const double tiles = (double)((n_tok + C - 1) / C);
     return std::max(8, (int)std::ceil(std::sqrt(start * tiles * n_heads / sms)));
 }
-inline size_t plan_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k, bool bwd) {
+// The workspace: the tiles' gates, then, when sequences are cut, the segments' states and decays.
+inline size_t gate_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads) {
+    return (size_t)n_slots(n_tok, n_seq) * n_heads * sizeof(TileGates);
+}
+inline size_t plan_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k) {
     const int64_t seg = (int64_t)segment_tiles(n_tok, n_heads) * C;
-    if (n_tok <= seg) return 256;
-    const size_t units = (size_t)(n_tok / seg + n_seq) * n_heads;
-    return (units * state_floats(d_k <= 64 ? 64 : 128) * 4 + units * 4 + 255) / 256 * 256 * (bwd ? 2 : 1);
+    const size_t units = n_tok > seg ? (size_t)(n_tok / seg + n_seq) * n_heads : 0;
+    return (gate_bytes(n_tok, n_seq, n_heads) + units * (state_floats(d_k <= 64 ? 64 : 128) + 1) * 4 + 255) / 256 * 256;
 }
 inline Plan make_plan(const DlaArgs &p, bool bwd) {
     Plan plan{};
@@ -52,9 +56,30 @@ inline Plan make_plan(const DlaArgs &p, bool bwd) {
     plan.vec_k = gdr::rows_vec<__nv_bfloat16>(p.k, p.k_stride, p.d_k);
     plan.vec_v = gdr::rows_vec<__nv_bfloat16>(p.v, p.v_stride, p.d_v);
     plan.vec_o = bwd && gdr::rows_vec<__nv_bfloat16>(p.dout, (int64_t)p.n_heads * p.d_v, p.d_v);
-    plan.states = static_cast<float *>(p.workspace);
+    plan.gates = static_cast<TileGates *>(p.workspace);
+    plan.states = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + gate_bytes(p.n_tok, p.n_seq, p.n_heads));
     plan.decays = plan.states + (size_t)plan.slots * p.n_heads * state_floats(p.d_k <= 64 ? 64 : 128);
     return plan;
+}
+
+// The gates of every tile and head: a warp each, eight heads of a tile side by side, whose decays are
+// neighbours in memory.
+static __global__ void __launch_bounds__(256) dla_gates_kernel(const DlaArgs p, TileGates *out) {
+    gdr::let_next_kernel_start();
+    const int64_t slot = blockIdx.x;
+    const Chunk ch = find_chunk(p.cu_seqlens, p.n_seq, slot);
+    if (ch.len == 0) return;
+    const int r = 2 * (threadIdx.x & 31);
+    for (int head = blockIdx.y * 8 + (threadIdx.x >> 5); head < p.n_heads; head += gridDim.y * 8) {
+        const float *g = p.g + (ch.t0 + r) * p.g_stride + head;
+        const float2 x = make_float2(r < ch.len ? g[0] : 0.f, r + 1 < ch.len ? g[p.g_stride] : 0.f);
+        form_gates(x, p.scale, out + slot * p.n_heads + head);
+    }
+}
+inline cudaError_t launch_gates(const DlaArgs &p, const Plan &plan, cudaStream_t stream) {
+    dla_gates_kernel<<<dim3((unsigned)n_slots(p.n_tok, p.n_seq), std::min(8192, (p.n_heads + 7) / 8)), 256, 0, stream>>>(p, plan.gates);
+    count_launches(1);
+    return cudaGetLastError();
 }
 
 // NC key channels from c0 on of one value channel: a state of the workspace
@@ -89,64 +114,64 @@ __device__ __forceinline__ void store_given(const float *st, float *to, int d_k,
         if (i < n) *x = st[i];
 }
 
-// warps: 0 issues products, 1 forms gates, 2 and 3 load, 4..7 scale the keys, 8..15 hold the state
-constexpr int kStateThreads = 512;
+// warps: 0 issues products, 1..3 load, 4..11 scale the values (every other tile each four), 12..19 read the sums
+constexpr int kSegmentThreads = 640;
+constexpr int kSum = 8;  // tiles that are summed in tensor memory
 
 template <int DK>
-struct StateSmem {
+struct SegmentSmem {
     static constexpr int kKey = DK / 64 * kHalf, kVal = 2 * kHalf;
-    static constexpr int K = 0, V = kKey, kStage = V + kVal;
-    static constexpr int kStages = 4;
-    static constexpr int Kp = kStages * kStage, Gate = Kp + 2 * 2 * kKey;  // two buffers of two planes
-    static constexpr int kGates = 4;
-    static constexpr int Ring = Gate + kGates * (int)sizeof(TileGates), Bars = Ring + kAhead * C * 4;
-    static constexpr int Full = 0, Empty = kStages, GFull = 2 * kStages, GEmpty = GFull + kGates, KpFull = GEmpty + kGates,
-                         KpEmpty = KpFull + 2, DsFull = KpEmpty + 2, DsEmpty = DsFull + 2, Drain = DsEmpty + 2, kBars = Drain + 1;
-    static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;
-    static_assert(kBytes <= 227 * 1024, "fits an SM");
+    static constexpr int K = 0, V = kKey, Gate = V + kVal, kStage = Gate + 2048;
+    static constexpr int kStages = 6, Bars = kStages * kStage;
+    static constexpr int Full = 0, Empty = kStages, VpFull = 2 * kStages, VpEmpty = VpFull + 2, DsFull = VpEmpty + 2,
+                         DsEmpty = DsFull + 2, Drain = DsEmpty + 2, kBars = Drain + 1;
+    static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;  // the base is rounded up to 1024
+    static_assert(sizeof(TileGates) <= 2048 && kBytes <= 227 * 1024, "fits an SM");
 };
 
-// What a segment adds to the state, from a state of zero, and its decay. The last segment of the
-// walk hands on to none and is left out.
+// What a segment adds to the state, from a state of zero, and its decay. The values' factors reach to the
+// segment's end, so that the sum over tiles stays in tensor memory, from the last tile to the first (REV,
+// the gradient: from the first to the last); every eighth tile it is added to registers, because the
+// tensor cores drop bits below a running sum's last place. The last segment of the walk hands on to
+// none and is left out.
 template <int DK, bool REV>
 __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CUtensorMap &tm_val, const DlaArgs &p,
                                              const Plan &plan, bool copies, unsigned unit) {
-    using L = StateSmem<DK>;
+    using L = SegmentSmem<DK>;
     constexpr int S = L::kStages;
     extern __shared__ __align__(1024) char smem_raw[];
     char *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t base = ptx::smem_u32(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };  // equal over a warp, and told so
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int head = unit % p.n_heads, kh = head / (p.n_heads / p.n_k_heads);
     const int64_t slot = unit / p.n_heads;
     const Segment sg = find_segment(p.cu_seqlens, p.n_seq, slot, plan.seg);
-    if (sg.len == 0 || (REV ? sg.index == 0 : sg.last)) return;
-    const int nc = (int)((sg.len + C - 1) / C);
+    if (sg.len == 0 || (REV ? sg.index == 0 : sg.last)) {
+        gdr::wait_for_previous_kernel();  // whoever waits for this kernel waits for that one
+        return;
+    }
+    const int nc = uniform((int)((sg.len + C - 1) / C));
     auto bar = [&](int i) { return base + L::Bars + 8 * i; };
-    auto gate = [&](int n) { return reinterpret_cast<TileGates *>(smem + L::Gate) + n % L::kGates; };
-    auto tile = [&](int n) { return REV ? nc - 1 - n : n; };  // the n-th of the walk
+    auto tile = [&](int n) { return REV ? n : nc - 1 - n; };  // the n-th of the walk
     auto rows_of = [&](int c) { return (int)min((int64_t)C, sg.len - (int64_t)c * C); };
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             ptx::mbar_init(bar(L::Full + i), 1);
-            ptx::mbar_init(bar(L::Empty + i), 1 + 4);
-        }
-        for (int i = 0; i < L::kGates; ++i) {
-            ptx::mbar_init(bar(L::GFull + i), 1);
-            ptx::mbar_init(bar(L::GEmpty + i), 4 + 8);
+            ptx::mbar_init(bar(L::Empty + i), 1 + 8);  // all eight scaling warps read the decay
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(bar(L::KpFull + i), 4);
-            ptx::mbar_init(bar(L::KpEmpty + i), 1);
+            ptx::mbar_init(bar(L::VpFull + i), 4);
+            ptx::mbar_init(bar(L::VpEmpty + i), 1);
             ptx::mbar_init(bar(L::DsFull + i), 1);
             ptx::mbar_init(bar(L::DsEmpty + i), 8);
         }
         ptx::mbar_init(bar(L::Drain), 1);
         ptx::mbar_init_fence();
     }
-    if (warp == 0) ptx::tmem_alloc(bar(L::kBars), 256);
+    if (warp == 0) ptx::tmem_alloc(bar(L::kBars), 512);
     if (p.d_v <= 64)  // channels that no value head has
-        for (int i = tid; i < S * kHalf / 16; i += kStateThreads)
+        for (int i = tid; i < S * kHalf / 16; i += kSegmentThreads)
             *reinterpret_cast<uint4 *>(smem + (i / (kHalf / 16)) * L::kStage + L::V + kHalf + (i % (kHalf / 16)) * 16) = make_uint4(0, 0, 0, 0);
     ptx::fence_proxy_async();
     ptx::tc_fence_before();
@@ -156,88 +181,94 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
     bool ok = true;
     auto wait = [&](int b, int parity) { ok = wait_bar(bar(b), parity & 1) && ok; };
     if (warp == 0) {
-        constexpr uint32_t id = ptx::idesc_bf16(128, DK, 1, 1);
+        constexpr uint32_t id = ptx::idesc_bf16(128, DK, 0, 1);
         const uint32_t leader = ptx::elect_one();
-        const uint64_t v0 = ptx::sdesc_sw128(base + L::V, kHalf, 1024), kp = ptx::sdesc_sw128(base + L::Kp, kHalf, 1024);
+        const uint64_t k0 = ptx::sdesc_sw128(base + L::K, kHalf, 1024);
         int s = 0;
 #pragma unroll 1
         for (int n = 0; n < nc; ++n) {
-            wait(L::KpFull + (n & 1), n >> 1);
-            if (n >= 2) wait(L::DsEmpty + (n & 1), (n >> 1) - 1);
+            const int b = (n / kSum) & 1;  // the buffer of this sum
+            wait(L::VpFull + (n & 1), n >> 1);
+            if (n % kSum == 0 && n >= 2 * kSum) wait(L::DsEmpty + b, n / (2 * kSum) - 1);
             ptx::tc_fence_after();
-            const uint32_t at = (uint32_t)s * (L::kStage / 16), key = (uint32_t)(n & 1) * (2 * L::kKey / 16);
+            const uint32_t at = (uint32_t)s * (L::kStage / 16), more = n % kSum != 0;
+            if (leader) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int k = 0; k < C / 16; ++k)
-                    ptx::umma_ss_by(leader, tmem + (n & 1) * 128, v0 + (at + 128 * k), kp + (key + i * L::kKey / 16 + 128 * k), id,
-                                    i + k > 0);
-            ptx::umma_commit_by(leader, bar(L::DsFull + (n & 1)));
-            ptx::umma_commit_by(leader, bar(L::KpEmpty + (n & 1)));
-            ptx::umma_commit_by(leader, bar(L::Empty + s));
+                    for (int k = 0; k < C / 16; ++k)
+                        ptx::umma_ts(tmem + b * 128, tmem + 256 + (n & 1) * 64 + i * 32 + 8 * k, k0 + (at + 128 * k), id,
+                                     i + k > 0 ? 1 : more);
+                if ((n + 1) % kSum == 0 || n + 1 == nc) ptx::umma_commit(bar(L::DsFull + b));
+                ptx::umma_commit(bar(L::VpEmpty + (n & 1)));
+                ptx::umma_commit(bar(L::Empty + s));
+            }
+            __syncwarp();
             if (++s == S) s = 0;
         }
-        ptx::umma_commit_by(leader, bar(L::Drain));
+        if (leader) ptx::umma_commit(bar(L::Drain));
+        __syncwarp();
         drain_bar(bar(L::Drain), 0);
-    } else if (warp == 1) {
-        walk_gates<REV>(
-            p, reinterpret_cast<float *>(smem + L::Ring), sg.t0, head, nc, tile, rows_of, gate,
-            [&](int n) { if (n >= L::kGates) wait(L::GEmpty + n % L::kGates, n / L::kGates - 1); },
-            [&](int n) { warp_arrive(bar(L::GFull + n % L::kGates)); });
     } else if (warp < 4) {
-        const Source k{&tm_key, static_cast<const __nv_bfloat16 *>(REV ? p.q : p.k), REV ? p.q_stride : p.k_stride, kh, p.d_k,
-                       DK / 64, REV ? plan.vec_q : plan.vec_k};
-        const Source v{&tm_val, static_cast<const __nv_bfloat16 *>(REV ? p.dout : p.v), REV ? (int64_t)p.n_heads * p.d_v : p.v_stride,
-                       head, p.d_v, p.d_v > 64 ? 2 : 1, REV ? plan.vec_o : plan.vec_v};
-        int copied = 0;
+        const Source in[2] = {
+            {&tm_key, static_cast<const __nv_bfloat16 *>(REV ? p.q : p.k), REV ? p.q_stride : p.k_stride, kh, p.d_k, DK / 64,
+             REV ? plan.vec_q : plan.vec_k},
+            {&tm_val, static_cast<const __nv_bfloat16 *>(REV ? p.dout : p.v), REV ? (int64_t)p.n_heads * p.d_v : p.v_stride, head,
+             p.d_v, p.d_v > 64 ? 2 : 1, REV ? plan.vec_o : plan.vec_v}};
+        const TileGates *gates = gates_of(plan.gates, p, sg.seq, (int64_t)sg.index * (plan.seg / C), head);
+        int begun = 0;  // tiles whose copies were begun
         for (int n = 0; n < nc; ++n) {
-            const int s = n % S, rows = rows_of(tile(n));
+            const int s = n % S, c = tile(n), rows = rows_of(c);
             if (n >= S) wait(L::Empty + s, n / S - 1);
             ok = __all_sync(0xffffffffu, ok);
-            const uint32_t at = base + s * L::kStage;
-            const int64_t t0 = sg.t0 + (int64_t)tile(n) * C;
-            if (copies && rows == C) {
-                if (ok && warp == 2 && lane == 0) {
-                    const uint32_t m = bar(L::Full + s);
-                    ptx::mbar_arrive_tx(m, L::kKey + v.halves * kHalf);
-                    tile_by_copy(k, at + L::K, t0, m);
-                    tile_by_copy(v, at + L::V, t0, m);
-                    copied = n + 1;
+            const uint32_t at = base + s * L::kStage, m = bar(L::Full + s);
+            const int64_t t0 = sg.t0 + (int64_t)c * C;
+            const bool copy = copies && rows == C;
+            if (!copy) {
+                const uint32_t to[2] = {at + L::K, at + L::V};
+                if (ok) tiles_by_threads(in, to, 2, t0, rows, tid - 32, 96);
+                rows_loaded(96);
+            }
+            if (ok && tid == 32) {
+                ptx::mbar_arrive_tx(m, (uint32_t)sizeof(TileGates) + (copy ? L::kKey + in[1].halves * kHalf : 0));
+                if (copy) {
+                    tile_by_copy(in[0], at + L::K, t0, m);
+                    tile_by_copy(in[1], at + L::V, t0, m);
                 }
-            } else {
-                if (ok) {
-                    tile_by_threads(k, at + L::K, t0, rows, tid - 64, 64);
-                    tile_by_threads(v, at + L::V, t0, rows, tid - 64, 64);
-                }
-                tile_loaded(bar(L::Full + s));
+                if (n == 0) gdr::wait_for_previous_kernel();  // the gates
+                bulk_load(at + L::Gate, gates + (int64_t)c * p.n_heads, sizeof(TileGates), m);
+                begun = n + 1;
             }
         }
+        // nothing may land in shared memory after the block has gone
         if (!ok)
-            for (int n = max(0, copied - S); n < copied; ++n) drain_bar(bar(L::Full + n % S), (n / S) & 1);
-    } else if (warp < 8) {
+            for (int n = max(0, begun - S); n < begun; ++n) drain_bar(bar(L::Full + n % S), (n / S) & 1);
+    } else if (warp < 12) {
+        float beyond = 1.f;  // the decay from the tile's end to the walk's
+        const int turn = (warp - 4) >> 2;
         for (int n = 0; n < nc; ++n) {
             const int s = n % S;
-            wait(L::GFull + n % L::kGates, n / L::kGates);
             wait(L::Full + s, n / S);
-            if (n >= 2) wait(L::KpEmpty + (n & 1), (n >> 1) - 1);
-            scale_rows(smem + s * L::kStage + L::K, smem + L::Kp + (n & 1) * 2 * L::kKey, L::kKey, *gate(n), L::kKey, tid - 128, 128);
-            ptx::fence_proxy_async();
-            warp_arrive(bar(L::KpFull + (n & 1)));
+            const TileGates *g = reinterpret_cast<const TileGates *>(smem + s * L::kStage + L::Gate);
+            if ((n & 1) == turn) {
+                if (n >= 2) wait(L::VpEmpty + turn, (n >> 1) - 1);
+                ptx::tc_fence_after();
+                scale_values(base + s * L::kStage + L::V, tmem, 256 + turn * 64, REV ? g->gam : g->del, beyond);
+                ptx::tc_fence_before();
+                warp_arrive(bar(L::VpFull + turn));
+            }
+            beyond *= g->whole;
             warp_arrive(bar(L::Empty + s));
-            warp_arrive(bar(L::GEmpty + n % L::kGates));
         }
+        if (tid == 128) plan.decays[(size_t)slot * p.n_heads + head] = beyond;
     } else {
-        constexpr int NC = DK / 2;
-        const int dv = (warp & 3) * 32 + lane, part = (warp - 8) >> 2;
+        constexpr int NC = DK / 2;  // key channels of a thread
+        const int dv = (warp & 3) * 32 + lane, part = (warp - 12) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        float st[NC], decay = 1.f;
+        float st[NC];
 #pragma unroll
         for (int i = 0; i < NC; ++i) st[i] = 0.f;
-        for (int n = 0; n < nc; ++n) {
-            wait(L::GFull + n % L::kGates, n / L::kGates);
-            const float whole = gate(n)->whole;
-            warp_arrive(bar(L::GEmpty + n % L::kGates));
-            decay *= whole;
+        for (int n = 0; n * kSum < nc; ++n) {
             wait(L::DsFull + (n & 1), n >> 1);
             ptx::tc_fence_after();
 #pragma unroll
@@ -246,22 +277,20 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
                 ptx::tmem_ld16(lanes + (n & 1) * 128 + part * NC + i, reinterpret_cast<uint32_t *>(d));
                 ptx::tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) st[i + j] = fmaf(whole, st[i + j], d[j]);
+                for (int j = 0; j < 16; ++j) st[i + j] += d[j];
             }
             ptx::tc_fence_before();
             warp_arrive(bar(L::DsEmpty + (n & 1)));
         }
-        const size_t at = (size_t)slot * p.n_heads + head;
-        store_state<NC>(st, plan.states + at * state_floats(DK), dv, part * NC);
-        if (tid == 256) plan.decays[at] = decay;
+        store_state<NC>(st, plan.states + ((size_t)slot * p.n_heads + head) * state_floats(DK), dv, part * NC);
     }
     __syncwarp();
     __syncthreads();
-    if (warp == 0) ptx::tmem_dealloc(tmem, 256);
+    if (warp == 0) ptx::tmem_dealloc(tmem, 512);
 }
 
 template <int DK>
-__global__ void __launch_bounds__(kStateThreads, 1)
+__global__ void __launch_bounds__(kSegmentThreads, 1)
     dla_segments_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const DlaArgs p,
                         const Plan plan, bool copies, bool rev) {
@@ -322,11 +351,9 @@ __global__ void __launch_bounds__(256) dla_join_kernel(const DlaArgs p, const Pl
 template <int DK>
 cudaError_t launch_segments(const DlaArgs &p, const Plan &plan, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                             const CUtensorMap &o, bool copies, bool rev, cudaStream_t stream) {
-    const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dla_segments_kernel<DK>), StateSmem<DK>::kBytes);
+    const cudaError_t e = gdr::launch_dependent(dla_segments_kernel<DK>, dim3((unsigned)(plan.slots * p.n_heads)), kSegmentThreads,
+                                                SegmentSmem<DK>::kBytes, stream, q, k, v, o, p, plan, copies, rev);
     if (e != cudaSuccess) return e;
-    dla_segments_kernel<DK><<<(unsigned)(plan.slots * p.n_heads), kStateThreads, StateSmem<DK>::kBytes, stream>>>(
-        q, k, v, o, p, plan, copies, rev);
-    count_launches(1);
     return gdr::launch_dependent(dla_join_kernel<DK>, dim3((unsigned)(state_floats(DK) / 1024 * p.n_heads * p.n_seq)), 256, 0, stream,
                                  p, plan, rev);
 }

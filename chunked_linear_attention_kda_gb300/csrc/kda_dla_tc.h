@@ -16,32 +16,30 @@ namespace dla {
 
 constexpr int C = 64;            // tokens of a tile
 constexpr int kHalf = C * 128;   // bytes of a tile's 64 channels
-constexpr long long kWaitLimit = 4000000000LL;  // SM cycles, about two seconds
+constexpr uint32_t kWaitLimit = 3000000000u;  // SM cycles, about one and a half seconds
 
 static __device__ unsigned int g_dla_flags;  // bit 5: a pipeline wait exceeded its limit
 
-// Bounded wait. False when this or any other wait of the grid gave up. Its loop is a call: the
-// kernels' dozens of waits inlined made them 100 KB long, and their warps wait for instructions as it is.
-static __device__ __noinline__ bool wait_longer(uint32_t a, uint32_t parity) {
-    const long long t0 = clock64();
+// Bounded wait. False when this or any other wait of the grid gave up.
+__device__ __forceinline__ bool wait_bar(uint32_t a, uint32_t parity) {
+    if (ptx::mbar_try(a, parity)) return true;
+    const uint32_t t0 = clock();
+#pragma unroll 1
     for (uint32_t it = 1;; ++it) {
         if (ptx::mbar_try(a, parity)) return true;
         if ((it & 63u) == 0) {
             if (*(volatile unsigned int *)&g_dla_flags != 0u) return false;
-            if (clock64() - t0 > kWaitLimit) {
+            if ((uint32_t)clock() - t0 > kWaitLimit) {
                 atomicOr(&g_dla_flags, 32u);
                 return false;
             }
         }
     }
 }
-__device__ __forceinline__ bool wait_bar(uint32_t a, uint32_t parity) {
-    return ptx::mbar_try(a, parity) || wait_longer(a, parity);
-}
 // for copies and products in flight after a failed wait: waits for them whatever the flag says
-static __device__ __noinline__ void drain_bar(uint32_t a, uint32_t parity) {
-    const long long t0 = clock64();
-    while (!ptx::mbar_try(a, parity) && clock64() - t0 < kWaitLimit) {}
+__device__ __forceinline__ void drain_bar(uint32_t a, uint32_t parity) {
+    const uint32_t t0 = clock();
+    while (!ptx::mbar_try(a, parity) && (uint32_t)clock() - t0 < kWaitLimit) {}
 }
 __device__ __forceinline__ void warp_arrive(uint32_t a) {
     __syncwarp();
@@ -122,47 +120,59 @@ struct Source {
 __device__ __forceinline__ void tile_by_copy(const Source &s, uint32_t dst, int64_t t0, uint32_t mbar) {
     for (int h = 0; h < s.halves; ++h) ptx::tma_load_3d(dst + h * kHalf, s.map, h * 64, s.head, (int)t0, mbar);
 }
-// the same by threads, rows past the end as zeros
-static __device__ __noinline__ void tile_by_threads(const Source s, uint32_t dst, int64_t t0, int rows, int tid, int n) {
-    const __nv_bfloat16 *p = s.base + t0 * s.stride + (int64_t)s.head * s.d;
-    for (int h = 0; h < s.halves; ++h)
-        gdr::load_tile<__nv_bfloat16, 128>(dst + h * kHalf, 0, p + h * 64, s.stride, rows, s.d - h * 64, s.vec, tid, n);
+// the same of `n` inputs by threads, rows past the end as zeros
+__device__ __forceinline__ void tiles_by_threads(const Source *inputs, const uint32_t *dst, int n, int64_t t0, int rows,
+                                                 int tid, int threads) {
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const Source &s = inputs[i];
+        const __nv_bfloat16 *p = s.base + t0 * s.stride + (int64_t)s.head * s.d;
+#pragma unroll 1
+        for (int h = 0; h < s.halves; ++h)
+            gdr::load_tile<__nv_bfloat16, 128>(dst[i] + h * kHalf, 0, p + h * 64, s.stride, rows, s.d - h * 64, s.vec, tid, threads);
+    }
 }
-
-// The two loading warps' rows are in shared memory, for tensor-core operand reads too. Both warps come
-// here for every such tile, whatever their waits said: the barrier counts on it.
-__device__ __forceinline__ void tile_loaded(uint32_t mbar) {
+// The loading warps' rows are in shared memory, for tensor-core operand reads too. All of them come here
+// for every such tile, whatever their waits said: the barrier counts on it.
+__device__ __forceinline__ void rows_loaded(int threads) {
     ptx::cp_async_commit();
     ptx::cp_async_wait0();
     ptx::fence_proxy_async();
-    ptx::named_sync(1, 64);
-    if ((threadIdx.x & 63) == 0) ptx::mbar_arrive(mbar);
+    ptx::named_sync(1, threads);
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t mbar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(mbar) : "memory");
 }
 
 // ---------------------------------------------------------------- gates
-// Of one tile: running sums of g log2(e), the decays up to and with each token (gam), those past it
-// times a factor as two bf16 planes, each twice in a word (del), the decay of all (whole)
+// Of one tile and head, formed for all tiles by a launch of their own (kda_dla_fwd.cu) and copied in with the
+// tile: running sums of g log2(e), scale times the decays up to and with each token (gam), the decays
+// past each (del), the decay of all (whole) and its exponent. Formed beside the products by one warp they
+// were the longest chain of a tile (1700 cycles of scans and conversions).
 struct TileGates {
     float2 G[C];
-    float gam[C];
-    uint2 del[C];
-    float whole;
-    float pad[3];
+    float gam[C], del[C];
+    float whole, pad;
+    float2 sum;
 };
-__device__ __forceinline__ uint2 planes_of(float x) {
-    const uint32_t hi = ptx::pack_bf16(x, x), lo = ptx::pack_bf16(x - gdr::lo_f(hi), x - gdr::lo_f(hi));
-    return make_uint2(hi, lo);
+static_assert(sizeof(TileGates) % 16 == 0, "copied in bulk");
+// The gates of tile c of a sequence lie at slot_base(cu, sequence) + c, as in kda_gdr.h
+__device__ __forceinline__ const TileGates *gates_of(const TileGates *all, const DlaArgs &p, int seq, int64_t c, int head) {
+    return all + ((slot_base(p.cu_seqlens, seq) + c) * p.n_heads + head);
 }
 // Sums of g log2(e) in fixed point, 40 bits behind the point: exact, so that differences of
-// neighbours stay exact after a long run of strong decays, and a scan's step is one addition (in two
-// floats the six dependent additions of a two-sum made it the longest chain of a tile).
+// neighbours stay exact after a long run of strong decays.
 __device__ __forceinline__ int64_t fixed_exponent(float g) {
     const Two x = decay_exponent(g);
     return __float2ll_rn(x.hi * 1099511627776.f) + __float2ll_rn(x.lo * 1099511627776.f);
 }
 __device__ __forceinline__ float from_fixed(int64_t x) { return __ll2float_rn(x) * 9.094947017729282e-13f; }
-// REV: del is the factor scale gam (the reverse walk's keys are scale gam q), else the decay past a token
-template <bool REV>
+__device__ __forceinline__ float2 two_from_fixed(int64_t x) {
+    const float hi = from_fixed(x);
+    return make_float2(hi, from_fixed(x - __float2ll_rn(hi * 1099511627776.f)));
+}
+// a tile's gates by one warp, two tokens a lane; tokens past the end have g = 0
 __device__ __forceinline__ void form_gates(float2 g, float scale, TileGates *out) {
     const int lane = threadIdx.x & 31;
     const int64_t first = fixed_exponent(g.x), both = first + fixed_exponent(g.y);
@@ -173,57 +183,17 @@ __device__ __forceinline__ void form_gates(float2 g, float scale, TileGates *out
         if (lane >= o) run += y;
     }
     const int64_t total = __shfl_sync(0xffffffffu, run, 31);
-    const int64_t G[2] = {run - both + first, run};
-    float2 at[2];
-    float gam[2];
-    uint2 del[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float hi = from_fixed(G[i]);
-        at[i] = make_float2(hi, from_fixed(G[i] - __float2ll_rn(hi * 1099511627776.f)));
-        gam[i] = ex2(hi);
-        del[i] = planes_of(REV ? scale * gam[i] : ex2(from_fixed(total - G[i])));
-    }
-    *reinterpret_cast<float4 *>(&out->G[2 * lane]) = make_float4(at[0].x, at[0].y, at[1].x, at[1].y);
-    *reinterpret_cast<float2 *>(&out->gam[2 * lane]) = make_float2(gam[0], gam[1]);
-    *reinterpret_cast<uint4 *>(&out->del[2 * lane]) = make_uint4(del[0].x, del[0].y, del[1].x, del[1].y);
-    if (lane == 0) out->whole = ex2(from_fixed(total));
-}
-// Every tile's gates, by one warp. Their inputs go to `ring` (kAhead tiles of 64 floats) kAhead tiles
-// ahead by asynchronous copies: a fetch takes longer than a tile's products. tile(n): the n-th tile of
-// the walk; rows(c): its tokens; slot(n), ready(n) and done(n): where its gates go, the wait for that
-// slot and the hand-over.
-constexpr int kAhead = 8;
-template <bool REV, typename Tile, typename Rows, typename Slot, typename Ready, typename Done>
-__device__ __forceinline__ void walk_gates(const DlaArgs &p, float *ring, int64_t t0, int head, int nc, Tile tile, Rows rows,
-                                           Slot slot, Ready ready, Done done) {
-    const int r = 2 * (threadIdx.x & 31);
-    auto fetch = [&](int n) {
-        if (n < nc) {
-            const int c = tile(n), len = rows(c);
-            const float *g = p.g + (t0 + (int64_t)c * C + r) * p.g_stride + head;
-            const uint32_t to = ptx::smem_u32(ring + n % kAhead * C + r);
-            ptx::cp_async_4(to, r < len ? g : p.g, r < len ? 4 : 0);
-            ptx::cp_async_4(to + 4, r + 1 < len ? g + p.g_stride : p.g, r + 1 < len ? 4 : 0);
-        }
-        ptx::cp_async_commit();
-    };
-#pragma unroll 1
-    for (int n = 0; n < kAhead - 1; ++n) fetch(n);
-#pragma unroll 1
-    for (int n = 0; n < nc; ++n) {
-        fetch(n + kAhead - 1);
-        gdr::cp_async_wait<kAhead - 1>();
-        const float2 g = *reinterpret_cast<const float2 *>(ring + n % kAhead * C + r);  // this lane's own copies
-        ready(n);
-        form_gates<REV>(g, p.scale, slot(n));
-        done(n);
+    const int64_t before = run - both + first;
+    const float2 a = two_from_fixed(before), b = two_from_fixed(run);
+    reinterpret_cast<float4 *>(out->G)[lane] = make_float4(a.x, a.y, b.x, b.y);
+    reinterpret_cast<float2 *>(out->gam)[lane] = make_float2(scale * ex2(a.x), scale * ex2(b.x));
+    reinterpret_cast<float2 *>(out->del)[lane] = make_float2(ex2(from_fixed(total - before)), ex2(from_fixed(total - run)));
+    if (lane == 0) {
+        out->whole = ex2(from_fixed(total));
+        out->sum = two_from_fixed(total);
     }
 }
 
-// The planes of a tile's rows times their factors: hi = k d, lo the rest of the product and k times
-// the factor's second plane. k d has 16 bits, so that its rest beside hi is exact. Eight channels a
-// time, `dst` and `dst + plane`.
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -234,22 +204,45 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-__device__ __forceinline__ void scale_rows(const char *src, char *dst, int plane, const TileGates &gate, int bytes,
-                                           int tid, int n) {
-#pragma unroll 4
-    for (int i = tid; i < bytes / 16; i += n) {
-        const uint4 k = reinterpret_cast<const uint4 *>(src)[i];
-        const uint2 d = gate.del[(i >> 3) & (C - 1)];
-        const uint32_t x[4] = {k.x, k.y, k.z, k.w};
-        uint32_t hi[4], lo[4];
+// A tile's values times their tokens' factors, V'^T, as two planes in tensor memory (columns `to` .. + 31
+// and + 32 .. + 63, two tokens a column): hi = v f, lo the rest of the product and v times the factor's
+// second plane; v f has 16 bits, so that its rest beside hi is exact. By one warp of each quarter of the
+// lanes, 32 value channels. As an A operand there it costs shared memory, which bounds these kernels, one
+// read of the tile; as planes in shared memory for either operand a read, two writes and two more reads.
+__device__ __forceinline__ void scale_values(uint32_t tile, uint32_t tmem, uint32_t to, const float *factor, float more) {
+    const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
+    const uint32_t col = (lane >> 3 & 1) * 8;  // matrices 0, 1: channels 0..7 and 8..15 of eight tokens; 2, 3: of the next eight
+#pragma unroll 1
+    for (int t0 = 0; t0 < C; t0 += 32) {
+        uint32_t fh[4], fl[4];  // of the tokens t0 + 8 n + 2 (lane % 4) and the next
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            hi[e] = mul_bf16x2(x[e], d.x);
-            lo[e] = fma_bf16x2(x[e], d.y, fma_bf16x2(x[e], d.x, hi[e] ^ 0x80008000u));
+        for (int n = 0; n < 4; ++n) {
+            const float2 f = *reinterpret_cast<const float2 *>(factor + t0 + 8 * n + 2 * (lane & 3));
+            const float x = more * f.x, y = more * f.y;
+            fh[n] = ptx::pack_bf16(x, y);
+            fl[n] = ptx::pack_bf16(x - gdr::lo_f(fh[n]), y - gdr::hi_f(fh[n]));
         }
-        reinterpret_cast<uint4 *>(dst)[i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        reinterpret_cast<uint4 *>(dst + plane)[i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int dv = 32 * q + 16 * h + col;
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int tok = t0 + 16 * n + (lane >> 4) * 8 + (lane & 7);
+                ptx::ldsm_x4_t(tile + gdr::key_off(tok, dv), hi[4 * n], hi[4 * n + 1], hi[4 * n + 2], hi[4 * n + 3]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t v = hi[i];
+                hi[i] = mul_bf16x2(v, fh[i >> 1]);
+                lo[i] = fma_bf16x2(v, fl[i >> 1], fma_bf16x2(v, fh[i >> 1], hi[i] ^ 0x80008000u));
+            }
+            const uint32_t at = tmem + ((uint32_t)(32 * q + 16 * h) << 16) + to + t0 / 2;
+            ptx::tmem_st_half4(at, hi);
+            ptx::tmem_st_half4(at + 32, lo);
+        }
     }
+    ptx::tmem_st_wait();
 }
 
 // two fp32 values as two packed planes

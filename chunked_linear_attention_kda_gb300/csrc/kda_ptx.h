@@ -192,25 +192,6 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
         "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, "
         "%3, p; }" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc));
 }
-// The same for a converged warp, of which the lane with `leader` issues: descriptors that the whole warp
-// computes stay in uniform registers, where a branch of one lane moves them there for every product.
-__device__ __forceinline__ void umma_ss_by(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t id,
-                                           uint32_t acc) {
-    asm volatile(
-        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc), "r"(leader));
-}
-__device__ __forceinline__ void umma_ts_by(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t id,
-                                           uint32_t acc) {
-    asm volatile(
-        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d), "r"(a), "l"(b), "r"(id), "r"(acc), "r"(leader));
-}
-__device__ __forceinline__ void umma_commit_by(uint32_t leader, uint32_t mbar) {
-    asm volatile(
-        "{ .reg .pred q; setp.ne.b32 q, %1, 0; "
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(mbar), "r"(leader) : "memory");
-}
 // one lane of a converged warp
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t r;
@@ -287,6 +268,11 @@ __device__ __forceinline__ void tmem_st_frag4(uint32_t ta, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
         "%13,%14,%15,%16};" ::"r"(ta), KDA_W8(0), KDA_W8(8));
+}
+// 16 lanes x 16 columns (warp-collective): r[2 n], r[2 n + 1] are columns 4 n + lane % 4 of the lanes
+// lane / 4 and lane / 4 + 8: 8 x 8 matrices of 16-bit elements as ldmatrix gives them, two elements a column
+__device__ __forceinline__ void tmem_st_half4(uint32_t ta, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(ta), KDA_W8(0));
 }
 #undef KDA_R8
 #undef KDA_W8
