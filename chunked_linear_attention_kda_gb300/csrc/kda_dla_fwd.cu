@@ -31,19 +31,24 @@ constexpr int kFwdThreads = 1024;
 constexpr int kRegsLaunch = 64, kRegsServe = 40, kRegsPairs = 56, kRegsState = 96, kRegsOut = 64;
 static_assert(2 * (kRegsServe + kRegsPairs + kRegsState + kRegsOut) == 8 * kRegsLaunch, "the launch's registers");
 
+// Queries and keys of a tile are free once their products are done, its values when the output that was
+// turned in their place is copied out, its gates after all of it: rings of their own. A tile takes 4000
+// cycles to arrive, and with one ring of three stages that was waited for.
 template <int DK>
 struct FwdSmem {
     static constexpr int kKey = DK / 64 * kHalf, kVal = 2 * kHalf;
-    static constexpr int Q = 0, K = kKey, V = 2 * kKey, Gate = V + kVal, kStage = Gate + 2048;
-    static constexpr int kStages = 3;
-    static constexpr int P = kStages * kStage, O = P + 2 * kHalf, Bars = O + 2 * kHalf;
-    // full, empty [stages], then one each, but QK and O2 full, which alternate: either may be formed a tile
-    // before the last one was seen, and a phase's parity tells neighbours apart only
-    static constexpr int Full = 0, Empty = kStages, QkFull = 2 * kStages, PFull = QkFull + 2, PEmpty = PFull + 1,
-                         VpFull = PEmpty + 1, VpEmpty = VpFull + 1, DsFull = VpEmpty + 1, DsEmpty = DsFull + 1, SFull = DsEmpty + 1, O1Full = SFull + 1, O1Empty = O1Full + 1,
-                         O2Full = O1Empty + 1, O2Empty = O2Full + 2, Drain = O2Empty + 1, kBars = Drain + 2;
+    static constexpr int kStages = 4, kGates = 6;
+    static constexpr int Q = 0, K = kKey, kPair = 2 * kKey;  // a stage of queries and keys
+    static constexpr int V = kStages * kPair, P = V + kStages * kVal, Gate = P + 2 * kHalf, Bars = Gate + kGates * (int)sizeof(TileGates);
+    // rings' full and empty, then one each, but those of QK and O2, which alternate: either may be formed a
+    // tile before the last one was seen, and a phase's parity tells neighbours apart only
+    static constexpr int KFull = 0, KEmpty = KFull + kStages, VFull = KEmpty + kStages, VEmpty = VFull + kStages,
+                         GFull = VEmpty + kStages, GEmpty = GFull + kGates, QkFull = GEmpty + kGates, PFull = QkFull + 2,
+                         PEmpty = PFull + 1, VpFull = PEmpty + 1, VpEmpty = VpFull + 1, DsFull = VpEmpty + 1,
+                         DsEmpty = DsFull + 1, SFull = DsEmpty + 1, O1Full = SFull + 1, O1Empty = O1Full + 1,
+                         O2Full = O1Empty + 1, O2Empty = O2Full + 2, Drain = O2Empty + 2, kBars = Drain + 2;
     static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;  // the base is rounded up to 1024
-    static_assert(sizeof(TileGates) <= 2048 && kBytes <= 227 * 1024, "fits an SM");
+    static_assert(kBytes <= 227 * 1024, "fits an SM");
 };
 // columns of tensor memory
 constexpr int kTmDs = 0, kTmS = 128, kTmO1 = 256, kTmV = 320, kTmQk = 384;  // kTmQk: Q K^T, then O2, of two tiles
@@ -74,15 +79,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int nc = uniform((int)((sg.len + C - 1) / C));
     const bool keep_end = uniform(sg.last) && p.h_final;  // else the last tile adds to no state
     auto bar = [&](int i) { return base + L::Bars + 8 * i; };
-    auto gate = [&](int c) -> const TileGates & {  // in the tile's stage
-        return *reinterpret_cast<const TileGates *>(smem + c % S * L::kStage + L::Gate);
+    auto gate = [&](int c) -> const TileGates & {
+        return reinterpret_cast<const TileGates *>(smem + L::Gate)[c % L::kGates];
     };
     auto rows_of = [&](int c) { return (int)min((int64_t)C, sg.len - (int64_t)c * C); };
 
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
-            ptx::mbar_init(bar(L::Full + i), 1);
-            ptx::mbar_init(bar(L::Empty + i), 2 + 4 + 8 + 8 + 8);  // products, keys, P, state, output
+            ptx::mbar_init(bar(L::KFull + i), 1);
+            ptx::mbar_init(bar(L::KEmpty + i), 2);
+            ptx::mbar_init(bar(L::VFull + i), 1);
+            ptx::mbar_init(bar(L::VEmpty + i), 8);
+        }
+        for (int i = 0; i < L::kGates; ++i) {
+            ptx::mbar_init(bar(L::GFull + i), 1);
+            ptx::mbar_init(bar(L::GEmpty + i), 4 + 8 + 8 + 8);  // values, P, state, output
         }
         ptx::mbar_init(bar(L::QkFull), 1);
         ptx::mbar_init(bar(L::QkFull + 1), 1);
@@ -98,6 +109,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ptx::mbar_init(bar(L::O2Full), 1);
         ptx::mbar_init(bar(L::O2Full + 1), 1);
         ptx::mbar_init(bar(L::O2Empty), 8);
+        ptx::mbar_init(bar(L::O2Empty + 1), 8);
         ptx::mbar_init(bar(L::Drain), 1);
         ptx::mbar_init(bar(L::Drain + 1), 1);
         ptx::mbar_init_fence();
@@ -107,7 +119,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     for (int i = tid; i < 2 * kHalf / 16; i += kFwdThreads) reinterpret_cast<uint4 *>(smem + L::P)[i] = make_uint4(0, 0, 0, 0);
     if (p.d_v <= 64)
         for (int i = tid; i < S * kHalf / 16; i += kFwdThreads)
-            *reinterpret_cast<uint4 *>(smem + (i / (kHalf / 16)) * L::kStage + L::V + kHalf + (i % (kHalf / 16)) * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(smem + L::V + (i / (kHalf / 16)) * L::kVal + kHalf + (i % (kHalf / 16)) * 16) = make_uint4(0, 0, 0, 0);
     ptx::fence_proxy_async();
     ptx::tc_fence_before();
     __syncthreads();
@@ -120,7 +132,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
     if (warp == 0) {
         ptx::regs_decrease<kRegsServe>();
-        // Q K^T a tile ahead, and O1. Two warps issue, because a product takes its warp 40 to 70 cycles to issue
+        // Q K^T a tile ahead, and O1 (in the other order the next tile's P waits for this one's state: 445 -> 463 us
+        // at 64K tokens of 32 heads). Two warps issue, because a product takes its warp 40 to 70 cycles to issue
         // and a tile has 40 of them. The whole warp walks, an elected lane issues: operands are formed in
         // uniform registers.
         constexpr uint32_t id_qk = ptx::idesc_bf16(64, C, 0, 0), id_o1 = ptx::idesc_bf16(128, C, 0, 0);
@@ -132,10 +145,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll 1
         for (int c = -1; c < nc; ++c) {
             if (c + 1 < nc) {
-                wait(L::Full + next, next_phase);
-                if (c >= 1) wait(L::O2Empty, c - 1);  // the columns
+                wait(L::KFull + next, next_phase);
+                if (c >= 1) wait(L::O2Empty + ((c + 1) & 1), (c - 1) >> 1);  // the columns
                 ptx::tc_fence_after();
-                const uint32_t at = (uint32_t)next * (L::kStage / 16);
+                const uint32_t at = (uint32_t)next * (L::kPair / 16);
                 if (leader) {
 #pragma unroll
                     for (int k = 0; k < DK / 16; ++k)
@@ -148,22 +161,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     next_phase ^= 1;
                 }
             }
-            if (c < 0) continue;
-            wait(L::SFull, c);
-            if (c > 0) wait(L::O1Empty, c - 1);
-            ptx::tc_fence_after();
-            const uint32_t at = (uint32_t)s * (L::kStage / 16);
-            if (leader) {
+            if (c >= 0) {
+                wait(L::SFull, c);
+                if (c > 0) wait(L::O1Empty, c - 1);
+                ptx::tc_fence_after();
+                const uint32_t at = (uint32_t)s * (L::kPair / 16);
+                if (leader) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int k = 0; k < DK / 16; ++k)
-                        ptx::umma_ts(tmem + kTmO1, tmem + kTmS + i * (DK / 2) + 8 * k, q0 + (at + step(k)), id_o1, i + k > 0);
-                ptx::umma_commit(bar(L::O1Full));
-                ptx::umma_commit(bar(L::Empty + s));
+                        for (int k = 0; k < DK / 16; ++k)
+                            ptx::umma_ts(tmem + kTmO1, tmem + kTmS + i * (DK / 2) + 8 * k, q0 + (at + step(k)), id_o1, i + k > 0);
+                    ptx::umma_commit(bar(L::O1Full));
+                    ptx::umma_commit(bar(L::KEmpty + s));
+                }
+                __syncwarp();
+                if (++s == S) s = 0;
             }
-            __syncwarp();
-            if (++s == S) s = 0;
         }
         if (leader) ptx::umma_commit(bar(L::Drain));
         __syncwarp();
@@ -178,8 +192,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         int s = 0;
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
-            const uint32_t at = (uint32_t)s * (L::kStage / 16);
-            wait(L::Full + s, c / S);
+            const uint32_t at = (uint32_t)s * (L::kVal / 16), key = (uint32_t)s * (L::kPair / 16);
+            wait(L::KFull + s, c / S);
+            wait(L::VFull + s, c / S);
             if (c + 1 < nc || keep_end) {
                 wait(L::VpFull, c);
                 if (c > 0) wait(L::DsEmpty, c - 1);
@@ -189,9 +204,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int k = 0; k < C / 16; ++k)
-                            ptx::umma_ts(tmem + kTmDs, tmem + kTmV + i * 32 + 8 * k, k0 + (at + 128 * k), id_ds, i + k > 0);
+                            ptx::umma_ts(tmem + kTmDs, tmem + kTmV + i * 32 + 8 * k, k0 + (key + 128 * k), id_ds, i + k > 0);
                     ptx::umma_commit(bar(L::DsFull));
                     ptx::umma_commit(bar(L::VpEmpty));
+                    ptx::umma_commit(bar(L::KEmpty + s));
                 }
                 __syncwarp();
             }
@@ -205,7 +221,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         ptx::umma_ss(tmem + kTmQk + (c & 1) * C, v0 + (at + 128 * k), pp + (i * kHalf + k * 32) / 16, id_o2, i + k > 0);
                 ptx::umma_commit(bar(L::O2Full + (c & 1)));
                 ptx::umma_commit(bar(L::PEmpty));
-                ptx::umma_commit(bar(L::Empty + s));
             }
             __syncwarp();
             if (++s == S) s = 0;
@@ -215,51 +230,64 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         drain_bar(bar(L::Drain + 1), 0);
     } else if (warp < 4) {
         ptx::regs_decrease<kRegsServe>();
-        const Source in[3] = {{&tm_k, static_cast<const __nv_bfloat16 *>(p.k), p.k_stride, kh, p.d_k, DK / 64, plan.vec_k},
-                              {&tm_q, static_cast<const __nv_bfloat16 *>(p.q), p.q_stride, kh, p.d_k, DK / 64, plan.vec_q},
-                              {&tm_v, static_cast<const __nv_bfloat16 *>(p.v), p.v_stride, head, p.d_v, p.d_v > 64 ? 2 : 1, plan.vec_v}};
+        // one loads keys, queries and gates, the other values
+        const bool pair = warp == 2;
+        const Source in[2] = {
+            {pair ? &tm_k : &tm_v, static_cast<const __nv_bfloat16 *>(pair ? p.k : p.v), pair ? p.k_stride : p.v_stride, pair ? kh : head,
+             pair ? p.d_k : p.d_v, pair ? DK / 64 : p.d_v > 64 ? 2 : 1, pair ? plan.vec_k : plan.vec_v},
+            {&tm_q, static_cast<const __nv_bfloat16 *>(p.q), p.q_stride, kh, p.d_k, DK / 64, plan.vec_q}};
         const TileGates *gates = gates_of(plan.gates, p, sg.seq, (int64_t)sg.index * (plan.seg / C), head);
+        const int full = pair ? L::KFull : L::VFull, empty = pair ? L::KEmpty : L::VEmpty;
         int begun = 0;  // tiles whose copies were begun
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
             const int s = c % S, rows = rows_of(c);
-            if (c >= S) wait(L::Empty + s, c / S - 1);
+            if (c >= S) wait(empty + s, c / S - 1);
+            if (pair && c >= L::kGates) wait(L::GEmpty + c % L::kGates, c / L::kGates - 1);
             ok = __all_sync(0xffffffffu, ok);
-            const uint32_t at = base + s * L::kStage, m = bar(L::Full + s);
+            if (!ok) break;
+            const uint32_t to[2] = {base + (pair ? s * L::kPair + L::K : L::V + s * L::kVal), base + s * L::kPair + L::Q};
             const int64_t t0 = sg.t0 + (int64_t)c * C;
-            const bool copy = copies && rows == C;
-            if (!copy) {
-                const uint32_t to[3] = {at + L::K, at + L::Q, at + L::V};
-                if (ok) tiles_by_threads(in, to, 3, t0, rows, tid - 64, 64);
-                rows_loaded(64);
-            }
-            if (ok && tid == 64) {
-                ptx::mbar_arrive_tx(m, (uint32_t)sizeof(TileGates) + (copy ? 2 * L::kKey + in[2].halves * kHalf : 0));
-                if (copy) {
-                    tile_by_copy(in[0], at + L::K, t0, m);
-                    tile_by_copy(in[1], at + L::Q, t0, m);
-                    tile_by_copy(in[2], at + L::V, t0, m);
+            const uint32_t m = bar(full + s);
+            if (copies && rows == C) {
+                if (lane == 0) {
+                    ptx::mbar_arrive_tx(m, pair ? 2 * L::kKey : in[0].halves * kHalf);
+                    tile_by_copy(in[0], to[0], t0, m);
+                    if (pair) tile_by_copy(in[1], to[1], t0, m);
                 }
-                if (c == 0) gdr::wait_for_previous_kernel();  // the gates
-                bulk_load(at + L::Gate, gates + (int64_t)c * p.n_heads, sizeof(TileGates), m);
-                begun = c + 1;
+            } else {
+                tiles_by_threads(in, to, pair ? 2 : 1, t0, rows, lane, 32);
+                rows_loaded();
+                if (lane == 0) ptx::mbar_arrive(m);
             }
+            if (pair && lane == 0) {
+                if (c == 0) gdr::wait_for_previous_kernel();  // the gates
+                const uint32_t gm = bar(L::GFull + c % L::kGates);
+                ptx::mbar_arrive_tx(gm, sizeof(TileGates));
+                bulk_load(base + L::Gate + c % L::kGates * (uint32_t)sizeof(TileGates), gates + (int64_t)c * p.n_heads, sizeof(TileGates), gm);
+            }
+            begun = c + 1;
         }
         // nothing may land in shared memory after the block has gone
-        if (!ok)
-            for (int c = max(0, begun - S); c < begun; ++c) drain_bar(bar(L::Full + c % S), (c / S) & 1);
+        if (!ok) {
+            for (int c = max(0, begun - S); c < begun; ++c) drain_bar(bar(full + c % S), (c / S) & 1);
+            if (pair)
+                for (int c = max(0, begun - L::kGates); c < begun; ++c) drain_bar(bar(L::GFull + c % L::kGates), (c / L::kGates) & 1);
+        }
     } else if (warp < 8) {
         ptx::regs_decrease<kRegsServe>();
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
+            if (c + 1 == nc && !keep_end) break;  // adds to no state
             const int s = c % S;
-            wait(L::Full + s, c / S);
+            wait(L::GFull + c % L::kGates, c / L::kGates);
+            wait(L::VFull + s, c / S);
             if (c > 0) wait(L::VpEmpty, c - 1);
             ptx::tc_fence_after();
-            scale_values(base + s * L::kStage + L::V, tmem, kTmV, gate(c).del, 1.f);
+            scale_values(base + L::V + s * L::kVal, tmem, kTmV, gate(c).del, 1.f);
             ptx::tc_fence_before();
             warp_arrive(bar(L::VpFull));
-            warp_arrive(bar(L::Empty + s));
+            warp_arrive(bar(L::GEmpty + c % L::kGates));
         }
     } else if (warp < 16) {
         ptx::regs_decrease<kRegsPairs>();
@@ -270,8 +298,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const int r0 = 16 * w + gr;
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
-            const int s = c % S;
-            wait(L::Full + s, c / S);  // the gates
+            wait(L::GFull + c % L::kGates, c / L::kGates);
             const TileGates &g = gate(c);
             const float2 G0 = g.G[r0], G1 = g.G[r0 + 8];
             wait(L::QkFull + (c & 1), c >> 1);
@@ -303,7 +330,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             ptx::tc_fence_before();
             ptx::fence_proxy_async();
             warp_arrive(bar(L::PFull));
-            warp_arrive(bar(L::Empty + s));
+            warp_arrive(bar(L::GEmpty + c % L::kGates));
         }
     } else if (warp < 24) {
         ptx::regs_increase<kRegsState>();
@@ -333,9 +360,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             ptx::tc_fence_before();
             warp_arrive(bar(L::SFull));
             if (c + 1 == nc && !keep_end) break;
-            wait(L::Full + c % S, c / S);
+            wait(L::GFull + c % L::kGates, c / L::kGates);
             const float whole = gate(c).whole;
-            warp_arrive(bar(L::Empty + c % S));
+            warp_arrive(bar(L::GEmpty + c % L::kGates));
             wait(L::DsFull, c);
             ptx::tc_fence_after();
 #pragma unroll
@@ -361,8 +388,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16) + tok0;
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
-            const int s = c % S;
-            wait(L::Full + s, c / S);
+            const uint32_t stage = L::V + c % S * L::kVal;  // in the place of the tile's values
+            wait(L::GFull + c % L::kGates, c / L::kGates);
             const TileGates &g = gate(c);
             // O1 leaves tensor memory first
             float o[2][4][4];
@@ -395,12 +422,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                     for (int n = 0; n < 4; n += 2) {
                         const int tok = tok0 + 8 * n + (lane >> 4) * 8 + (lane & 7), at = 32 * w + 16 * h + ((lane >> 3) & 1) * 8;
-                        store_matrices_t(base + L::O + gdr::key_off(tok, at), f + 2 * n);
+                        store_matrices_t(base + stage + gdr::key_off(tok, at), f + 2 * n);
                     }
                 }
             ptx::tc_fence_before();
-            warp_arrive(bar(L::O2Empty));
-            warp_arrive(bar(L::Empty + s));
+            warp_arrive(bar(L::O2Empty + (c & 1)));
+            warp_arrive(bar(L::GEmpty + c % L::kGates));
             ptx::named_sync(2, 256);
             const int rows = rows_of(c);
             __nv_bfloat16 *to = out + ((int64_t)c * C + (ot >> 4)) * row_stride + ch;
@@ -409,7 +436,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 for (int i = 0; i < 4; ++i, to += 16 * row_stride) {
                     const int r = (ot >> 4) + 16 * i;
                     if (r >= rows) break;
-                    const uint4 x = *reinterpret_cast<const uint4 *>(smem + L::O + gdr::key_off(r, ch));
+                    const uint4 x = *reinterpret_cast<const uint4 *>(smem + stage + gdr::key_off(r, ch));
                     if (wide_out) {
                         *reinterpret_cast<uint4 *>(to) = x;
                     } else {
@@ -419,7 +446,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             if (ch + j < p.d_v) reinterpret_cast<uint16_t *>(to)[j] = (uint16_t)(e[j >> 1] >> (16 * (j & 1)));
                     }
                 }
-            ptx::named_sync(2, 256);
+            ptx::fence_proxy_async();  // the next tile is copied there
+            warp_arrive(bar(L::VEmpty + c % S));
         }
     }
     __syncwarp();

@@ -31,25 +31,45 @@ struct Plan {
     float *states;       // [slots][heads] states at the segments' starts (reverse: gradients at their ends)
     float *decays;       // [slots][heads] decays over the segments
 };
-// Tiles of a segment. A segment costs its tiles and about `start` tiles more to begin; the last one
-// runs alone for as long as it is. Over all heads the sum of both is least at the square root.
-inline int segment_tiles(int64_t n_tok, int32_t n_heads) {
-    constexpr double start = 3.0, sms = 152.0;
-    const double tiles = (double)((n_tok + C - 1) / C);
-    return std::max(8, (int)std::ceil(std::sqrt(start * tiles * n_heads / sms)));
+// Tiles of a segment, from the call's sizes alone (the sequences' lengths are on the device). Cutting costs
+// K and V read once more, what a CTA takes to begin (the time of four tiles) and the join; not cutting
+// leaves SMs idle. One sequence: the count of segments whose waves of CTAs take least, in times of a
+// tile (64K tokens of 32 heads: 9 segments 602 us, 40 segments 680). Several, of whatever lengths: longer segments cost
+// balance, shorter ones beginnings; the sum is least at the square root.
+inline int segment_tiles(int64_t n_tok, int32_t n_seq, int32_t n_heads) {
+    constexpr int kSMs = 152;
+    const int64_t tiles = (n_tok + C - 1) / C;
+    if (tiles <= 8) return 8;
+    if (n_seq > 1) return std::max(8, (int)std::ceil(std::sqrt(8.0 * (double)tiles * n_heads / kSMs)));
+    struct Last { int64_t tiles; int32_t heads; int best; };
+    thread_local Last last{0, 0, 0};
+    if (last.tiles == tiles && last.heads == n_heads) return last.best;
+    double least = 0;
+    int best = 0;
+    for (int n = 1; n <= 256 && n * 8 <= tiles + 7; ++n) {
+        const int64_t m = (tiles + n - 1) / n, units = (tiles + m - 1) / m * n_heads;
+        double cost = (double)((units + kSMs - 1) / kSMs) * (m + 4);
+        if (n > 1) cost += (double)((units - n_heads + kSMs - 1) / kSMs) * (0.38 * m + 2.5) + 3;
+        if (best == 0 || cost < least) {
+            least = cost;
+            best = (int)m;
+        }
+    }
+    last = {tiles, n_heads, best};
+    return best;
 }
 // The workspace: the tiles' gates, then, when sequences are cut, the segments' states and decays.
 inline size_t gate_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads) {
     return (size_t)n_slots(n_tok, n_seq) * n_heads * sizeof(TileGates);
 }
 inline size_t plan_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k) {
-    const int64_t seg = (int64_t)segment_tiles(n_tok, n_heads) * C;
+    const int64_t seg = (int64_t)segment_tiles(n_tok, n_seq, n_heads) * C;
     const size_t units = n_tok > seg ? (size_t)(n_tok / seg + n_seq) * n_heads : 0;
     return (gate_bytes(n_tok, n_seq, n_heads) + units * (state_floats(d_k <= 64 ? 64 : 128) + 1) * 4 + 255) / 256 * 256;
 }
 inline Plan make_plan(const DlaArgs &p, bool bwd) {
     Plan plan{};
-    plan.seg = segment_tiles(p.n_tok, p.n_heads) * C;
+    plan.seg = segment_tiles(p.n_tok, p.n_seq, p.n_heads) * C;
     plan.cut = p.n_tok > plan.seg;
     plan.slots = p.n_tok / plan.seg + p.n_seq;
     plan.vec_q = gdr::rows_vec<__nv_bfloat16>(p.q, p.q_stride, p.d_k);
@@ -114,7 +134,7 @@ __device__ __forceinline__ void store_given(const float *st, float *to, int d_k,
         if (i < n) *x = st[i];
 }
 
-// warps: 0 issues products, 1..3 load, 4..11 scale the values (every other tile each four), 12..19 read the sums
+// warps: 0 issues products, 1 loads, 4..11 scale the values (every other tile each four), 12..19 read the sums
 constexpr int kSegmentThreads = 640;
 constexpr int kSum = 8;  // tiles that are summed in tensor memory
 
@@ -209,7 +229,7 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
         if (leader) ptx::umma_commit(bar(L::Drain));
         __syncwarp();
         drain_bar(bar(L::Drain), 0);
-    } else if (warp < 4) {
+    } else if (warp == 1) {
         const Source in[2] = {
             {&tm_key, static_cast<const __nv_bfloat16 *>(REV ? p.q : p.k), REV ? p.q_stride : p.k_stride, kh, p.d_k, DK / 64,
              REV ? plan.vec_q : plan.vec_k},
@@ -221,15 +241,16 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
             const int s = n % S, c = tile(n), rows = rows_of(c);
             if (n >= S) wait(L::Empty + s, n / S - 1);
             ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             const uint32_t at = base + s * L::kStage, m = bar(L::Full + s);
             const int64_t t0 = sg.t0 + (int64_t)c * C;
             const bool copy = copies && rows == C;
             if (!copy) {
                 const uint32_t to[2] = {at + L::K, at + L::V};
-                if (ok) tiles_by_threads(in, to, 2, t0, rows, tid - 32, 96);
-                rows_loaded(96);
+                tiles_by_threads(in, to, 2, t0, rows, lane, 32);
+                rows_loaded();
             }
-            if (ok && tid == 32) {
+            if (lane == 0) {
                 ptx::mbar_arrive_tx(m, (uint32_t)sizeof(TileGates) + (copy ? L::kKey + in[1].halves * kHalf : 0));
                 if (copy) {
                     tile_by_copy(in[0], at + L::K, t0, m);
@@ -237,13 +258,13 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
                 }
                 if (n == 0) gdr::wait_for_previous_kernel();  // the gates
                 bulk_load(at + L::Gate, gates + (int64_t)c * p.n_heads, sizeof(TileGates), m);
-                begun = n + 1;
             }
+            begun = n + 1;
         }
         // nothing may land in shared memory after the block has gone
         if (!ok)
             for (int n = max(0, begun - S); n < begun; ++n) drain_bar(bar(L::Full + n % S), (n / S) & 1);
-    } else if (warp < 12) {
+    } else if (warp >= 4 && warp < 12) {
         float beyond = 1.f;  // the decay from the tile's end to the walk's
         const int turn = (warp - 4) >> 2;
         for (int n = 0; n < nc; ++n) {
@@ -261,7 +282,7 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
             warp_arrive(bar(L::Empty + s));
         }
         if (tid == 128) plan.decays[(size_t)slot * p.n_heads + head] = beyond;
-    } else {
+    } else if (warp >= 12) {
         constexpr int NC = DK / 2;  // key channels of a thread
         const int dv = (warp & 3) * 32 + lane, part = (warp - 12) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);

@@ -132,13 +132,12 @@ __device__ __forceinline__ void tiles_by_threads(const Source *inputs, const uin
             gdr::load_tile<__nv_bfloat16, 128>(dst[i] + h * kHalf, 0, p + h * 64, s.stride, rows, s.d - h * 64, s.vec, tid, threads);
     }
 }
-// The loading warps' rows are in shared memory, for tensor-core operand reads too. All of them come here
-// for every such tile, whatever their waits said: the barrier counts on it.
-__device__ __forceinline__ void rows_loaded(int threads) {
+// a loading warp's rows are in shared memory, for tensor-core operand reads too
+__device__ __forceinline__ void rows_loaded() {
     ptx::cp_async_commit();
     ptx::cp_async_wait0();
     ptx::fence_proxy_async();
-    ptx::named_sync(1, threads);
+    __syncwarp();
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t mbar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
