@@ -280,12 +280,13 @@ kda_status kda_read_device_flags(uint32_t *flags, int reset, void *stream) {
     unsigned int f64 = 0;
     e = kda::read_fwd64_flags(&f64, reset != 0, (cudaStream_t)stream);
     if (e != cudaSuccess) return launched(e, "reading the device status word");
-    unsigned int gf = 0, gb = 0, df = 0;
+    unsigned int gf = 0, gb = 0, df = 0, db = 0;
     e = kda::read_gdr_fwd_flags(&gf, reset != 0, (cudaStream_t)stream);
     if (e == cudaSuccess) e = kda::read_gdr_bwd_flags(&gb, reset != 0, (cudaStream_t)stream);
     if (e == cudaSuccess) e = kda::read_dla_fwd_flags(&df, reset != 0, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = kda::read_dla_bwd_flags(&db, reset != 0, (cudaStream_t)stream);
     if (e != cudaSuccess) return launched(e, "reading the device status word");
-    *flags = v | g | bw | f64 | gf | gb | df;
+    *flags = v | g | bw | f64 | gf | gb | df | db;
     return ok();
 }
 

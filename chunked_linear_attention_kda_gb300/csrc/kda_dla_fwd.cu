@@ -464,7 +464,7 @@ cudaError_t forward(const DlaArgs &p, cudaStream_t stream) {
     const bool wide = p.d_v % 8 == 0 && (uintptr_t)p.out % 16 == 0;
     const Plan plan = make_plan(p, false);
     cudaError_t e = launch_gates(p, plan, stream);
-    if (e == cudaSuccess && plan.cut) e = launch_segments<DK>(p, plan, q, k, v, v, copies, false, stream);
+    if (e == cudaSuccess && plan.cut) e = launch_segments<DK>(p, plan, q, k, v, v, copies, 1, stream);
     if (e != cudaSuccess) return e;
     return gdr::launch_dependent(dla_forward_kernel<DK>, dim3((unsigned)(plan.slots * p.n_heads)), kFwdThreads, FwdSmem<DK>::kBytes,
                                  stream, q, k, v, p, plan, copies, wide);
@@ -473,15 +473,19 @@ cudaError_t forward(const DlaArgs &p, cudaStream_t stream) {
 }  // namespace
 }  // namespace dla
 
-size_t dla_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t, int32_t d_k, int32_t d_v, bool bf16,
-                           bool bwd) {
-    if (bf16 && !bwd) return dla_tc_fwd_workspace_bytes(n_tok, n_seq, n_heads, d_k);
-    return dla_simt_workspace_bytes(n_tok, n_seq, n_heads, d_k, d_v, bwd);
+size_t dla_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k, int32_t d_v,
+                           bool bf16, bool bwd) {
+    if (!bf16) return dla_simt_workspace_bytes(n_tok, n_seq, n_heads, d_k, d_v, bwd);
+    return bwd ? dla_tc_bwd_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v)
+               : dla_tc_fwd_workspace_bytes(n_tok, n_seq, n_heads, d_k);
 }
+// without a token the states pass through: nothing of bf16 is read
 cudaError_t launch_dla_fwd(const DlaArgs &p, cudaStream_t stream) {
     return p.bf16 && p.n_tok > 0 ? launch_dla_tc_fwd(p, stream) : launch_dla_simt(p, false, stream);
 }
-cudaError_t launch_dla_bwd(const DlaArgs &p, cudaStream_t stream) { return launch_dla_simt(p, true, stream); }
+cudaError_t launch_dla_bwd(const DlaArgs &p, cudaStream_t stream) {
+    return p.bf16 && p.n_tok > 0 ? launch_dla_tc_bwd(p, stream) : launch_dla_simt(p, true, stream);
+}
 
 size_t dla_tc_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k) {
     return dla::plan_bytes(n_tok, n_seq, n_heads, d_k);

@@ -310,21 +310,36 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
     if (warp == 0) ptx::tmem_dealloc(tmem, 512);
 }
 
+// The plan as one direction's walk sees it: the reverse one's states and decays lie behind the forward one's.
+template <int DK>
+__host__ __device__ __forceinline__ Plan of_walk(Plan plan, const DlaArgs &p, bool rev) {
+    const size_t units = (size_t)plan.slots * p.n_heads;
+    if (rev) {
+        plan.states += units * state_floats(DK);
+        plan.decays += units;
+    }
+    return plan;
+}
+
+// Forward, or with twice the blocks in reverse first and forward
 template <int DK>
 __global__ void __launch_bounds__(kSegmentThreads, 1)
     dla_segments_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const DlaArgs p,
-                        const Plan plan, bool copies, bool rev) {
+                        const Plan plan, bool copies) {
     gdr::let_next_kernel_start();
-    if (rev) segment_walk<DK, true>(tm_q, tm_o, p, plan, copies, blockIdx.x);
-    else segment_walk<DK, false>(tm_k, tm_v, p, plan, copies, blockIdx.x);
+    const unsigned n = (unsigned)plan.slots * p.n_heads, rest = gridDim.x - n;
+    if (blockIdx.x < rest) segment_walk<DK, true>(tm_q, tm_o, p, of_walk<DK>(plan, p, true), copies, blockIdx.x);
+    else segment_walk<DK, false>(tm_k, tm_v, p, plan, copies, blockIdx.x - rest);
 }
 
 // The states at the segments' starts (reverse: the gradients at their ends), in place of what the
 // segments add: 16 bytes of a sequence's and head's state a thread, segment after segment.
 template <int DK>
-__global__ void __launch_bounds__(256) dla_join_kernel(const DlaArgs p, const Plan plan, bool rev) {
+__global__ void __launch_bounds__(256) dla_join_kernel(const DlaArgs p, const Plan both) {
     gdr::let_next_kernel_start();
+    const bool rev = blockIdx.y == 1;
+    const Plan plan = of_walk<DK>(both, p, rev);
     constexpr int kBlocks = state_floats(DK) / 4 / 256;
     const int i = (blockIdx.x % kBlocks) * 256 + threadIdx.x;
     const int head = blockIdx.x / kBlocks % p.n_heads, seq = blockIdx.x / kBlocks / p.n_heads;
@@ -371,12 +386,12 @@ __global__ void __launch_bounds__(256) dla_join_kernel(const DlaArgs p, const Pl
 
 template <int DK>
 cudaError_t launch_segments(const DlaArgs &p, const Plan &plan, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                            const CUtensorMap &o, bool copies, bool rev, cudaStream_t stream) {
-    const cudaError_t e = gdr::launch_dependent(dla_segments_kernel<DK>, dim3((unsigned)(plan.slots * p.n_heads)), kSegmentThreads,
-                                                SegmentSmem<DK>::kBytes, stream, q, k, v, o, p, plan, copies, rev);
+                            const CUtensorMap &o, bool copies, int walks, cudaStream_t stream) {
+    const cudaError_t e = gdr::launch_dependent(dla_segments_kernel<DK>, dim3((unsigned)(walks * plan.slots * p.n_heads)), kSegmentThreads,
+                                                SegmentSmem<DK>::kBytes, stream, q, k, v, o, p, plan, copies);
     if (e != cudaSuccess) return e;
-    return gdr::launch_dependent(dla_join_kernel<DK>, dim3((unsigned)(state_floats(DK) / 1024 * p.n_heads * p.n_seq)), 256, 0, stream,
-                                 p, plan, rev);
+    return gdr::launch_dependent(dla_join_kernel<DK>, dim3((unsigned)(state_floats(DK) / 1024 * p.n_heads * p.n_seq), walks), 256, 0,
+                                 stream, p, plan);
 }
 
 }  // namespace dla

@@ -81,7 +81,7 @@ __device__ __forceinline__ Segment find_segment(const int32_t *cu, int n_seq, in
 __host__ __device__ constexpr int state_floats(int dkp) { return dkp * 128; }
 
 // ---------------------------------------------------------------- tiles
-// The tensor maps of inputs [tokens, heads, d]: boxes of 64 tokens x 64 channels of one head.
+// The tensor maps of inputs [tokens, heads, d]: boxes of `rows` tokens x 64 channels of one head.
 struct TileMap {
     static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
         static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -95,12 +95,12 @@ struct TileMap {
         return fn;
     }
     // false: rows that a tensor copy cannot fetch (the kernels then load them by threads)
-    static bool encode(CUtensorMap *m, const void *base, int64_t n_tok, int64_t stride, int heads, int d) {
+    static bool encode(CUtensorMap *m, const void *base, int64_t n_tok, int64_t stride, int heads, int d, int rows = C) {
         auto enc = encoder();
         if (!enc || n_tok == 0 || !gdr::rows_vec<__nv_bfloat16>(base, stride, d)) return false;
         const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)n_tok};
         const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
-        const cuuint32_t box[3] = {64, 1, C}, step[3] = {1, 1, 1};
+        const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, step[3] = {1, 1, 1};
         return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, step,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -156,8 +156,9 @@ size_t dla_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_
                            bool bf16, bool bwd);
 cudaError_t launch_dla_fwd(const DlaArgs &args, cudaStream_t stream);
 cudaError_t launch_dla_bwd(const DlaArgs &args, cudaStream_t stream);
-// The forward pass's status word (bit 5: a pipeline wait gave up).
+// The status words of the two passes (bit 5: a pipeline wait gave up).
 cudaError_t read_dla_fwd_flags(unsigned int *flags, bool reset, cudaStream_t stream);
+cudaError_t read_dla_bwd_flags(unsigned int *flags, bool reset, cudaStream_t stream);
 
 // One token per row, as GdrStepArgs.
 struct DlaStepArgs {
