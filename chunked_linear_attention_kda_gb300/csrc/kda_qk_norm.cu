@@ -9,11 +9,12 @@
 // Angles: a frequency is held as the fraction of a turn per position in 64-bit fixed point; times the
 // position, modulo 2^64, it is the angle's fraction of a turn to 2^-64 of a turn per position, whatever
 // the position's size or sign, by integer products alone (fp64 is narrow on this part).
-// Both passes are bound by HBM: every input is read once and kept in registers across its row's
-// sums. A CTA takes a few tokens at a time: its threads form the tokens' sines and cosines in shared
-// memory, a pair each, which all heads then share; groups of threads walk over the rows (token,
-// head). Sums over rows go to one partial row a CTA and are added up by a second kernel in a fixed
-// order: the same call gives the same bits.
+// Both passes are bound by HBM: every input is read once and kept in registers across its row's sums.
+// Groups of threads hold rows; a warp's groups take the heads of one token in turn, so that its angles are
+// formed once and stay in registers, and a thread holds both channels of each of its pairs, so that
+// none goes through shared memory (a first form, with a run of channels a thread and the angles in shared
+// memory, was bound by that: 511 us at 64K tokens). Sums over rows go to one partial row a CTA
+// and are added up by a second kernel in a fixed order: the same call gives the same bits.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -30,31 +31,6 @@ constexpr int kMaxD = 256;
 
 __device__ __forceinline__ float get(const float *p) { return *p; }
 __device__ __forceinline__ float get(const bf16 *p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void put(float *p, float x) { *p = x; }
-__device__ __forceinline__ void put(bf16 *p, float x) { *p = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void load8(const float *p, float *x) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const bf16 *p, float *x) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void store8(float *p, const float *x) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void store8(bf16 *p, const float *x) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(ptx::pack_bf16(x[0], x[1]), ptx::pack_bf16(x[2], x[3]),
-                                               ptx::pack_bf16(x[4], x[5]), ptx::pack_bf16(x[6], x[7]));
-}
-
 // The fraction of a turn that a position adds to a pair's angle
 __device__ __forceinline__ uint64_t turn_fraction(double freq) {
     const double t = freq * 0.15915494309189535;  // 1 / (2 pi)
@@ -68,33 +44,95 @@ __device__ __forceinline__ float2 cos_sin(uint64_t turn) {
     return cs;
 }
 
-// A group of G threads (a power of two up to 32) holds a row of d channels, eight a thread: with
-// VEC thread t the run 8 t .., otherwise the channels t + G i.
-template <bool VEC>
-__device__ __forceinline__ int channel(int t, int G, int i) { return VEC ? 8 * t + i : t + G * i; }
+// A group of G threads (a power of two up to 32) holds a row of d channels, eight a thread. With VEC
+// in two runs of four, which are the two channels of four pairs (in halves: from 4 t and R + 4 t on,
+// threads beyond the pairs two runs side by side; interleaved: two runs side by side), otherwise the
+// channels t + G i.
+enum Kind { kSingle, kHalves, kInterleaved };  // not VEC, VEC by the order of pairs
+struct Runs { int a, b; };
+__device__ __forceinline__ Runs runs(int t, int R, bool interleaved) {
+    if (!interleaved && 4 * t < R) return {4 * t, R + 4 * t};
+    const int c = interleaved ? 8 * t : 2 * R + 8 * (t - R / 4);
+    return {c, c + 4};
+}
 
-template <bool VEC, typename T>
-__device__ __forceinline__ void load_row(const T *p, int d, int t, int G, float *x) {
-    if constexpr (VEC) {
-        if (8 * t < d) {
-            load8(p + 8 * t, x);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    } else {
+// A thread's eight channels as they were loaded, so that several rows are in flight without their fp32 copies
+template <typename T, bool VEC>
+struct Row {
+    float x[8];
+    __device__ __forceinline__ void load(const T *p, int d, int t, int G, Runs) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = t + G * i < d ? get(p + t + G * i) : 0.f;
     }
-}
-template <bool VEC, typename T>
-__device__ __forceinline__ void store_row(T *p, int d, int t, int G, const float *x) {
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
+    __device__ __forceinline__ void unpack(float *y) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[i];
+    }
+};
+template <>
+struct Row<bf16, true> {
+    uint2 a, b;
+    __device__ __forceinline__ void clear() { a = b = make_uint2(0, 0); }
+    __device__ __forceinline__ void load(const bf16 *p, int d, int, int, Runs r) {
+        clear();
+        if (r.a < d) {
+            a = *reinterpret_cast<const uint2 *>(p + r.a);
+            b = *reinterpret_cast<const uint2 *>(p + r.b);
+        }
+    }
+    __device__ __forceinline__ void unpack(float *y) const {
+        const uint32_t w[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[2 * i] = __uint_as_float(w[i] << 16);
+            y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+template <>
+struct Row<float, true> {
+    float4 a, b;
+    __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void load(const float *p, int d, int, int, Runs r) {
+        clear();
+        if (r.a < d) {
+            a = *reinterpret_cast<const float4 *>(p + r.a);
+            b = *reinterpret_cast<const float4 *>(p + r.b);
+        }
+    }
+    __device__ __forceinline__ void unpack(float *y) const {
+        y[0] = a.x; y[1] = a.y; y[2] = a.z; y[3] = a.w;
+        y[4] = b.x; y[5] = b.y; y[6] = b.z; y[7] = b.w;
+    }
+};
+template <bool VEC>
+__device__ __forceinline__ void store_row(float *p, const float *x, int d, int t, int G, Runs r) {
     if constexpr (VEC) {
-        if (8 * t < d) store8(p + 8 * t, x);
+        if (r.a < d) {
+            *reinterpret_cast<float4 *>(p + r.a) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(p + r.b) = make_float4(x[4], x[5], x[6], x[7]);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (t + G * i < d) put(p + t + G * i, x[i]);
+            if (t + G * i < d) p[t + G * i] = x[i];
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store_row(bf16 *p, const float *x, int d, int t, int G, Runs r) {
+    if constexpr (VEC) {
+        if (r.a < d) {
+            *reinterpret_cast<uint2 *>(p + r.a) = make_uint2(ptx::pack_bf16(x[0], x[1]), ptx::pack_bf16(x[2], x[3]));
+            *reinterpret_cast<uint2 *>(p + r.b) = make_uint2(ptx::pack_bf16(x[4], x[5]), ptx::pack_bf16(x[6], x[7]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (t + G * i < d) p[t + G * i] = __float2bfloat16_rn(x[i]);
     }
 }
 __device__ __forceinline__ float group_sum(float x, int G) {
@@ -102,52 +140,32 @@ __device__ __forceinline__ float group_sum(float x, int G) {
     return x;
 }
 
-// The row x turned by the token's angles (sign = -1: back). cs: the token's (cos, sin) pairs;
-// stage: d floats of this group. Every thread of the warp calls it.
-template <bool VEC>
-__device__ __forceinline__ void turn(float *x, const float2 *cs, int R, bool interleaved, float sign, int t, int G,
-                                     float *stage) {
-    if (VEC && interleaved) {
+// The row x turned by its token's angles, cs the (cos, sin) of this thread's four pairs (VEC) or of each of its
+// eight channels' pairs; sign = -1: back. stage: 2 R floats of this group (not VEC). The whole warp calls it.
+template <Kind KIND>
+__device__ __forceinline__ void turn(float *x, const float2 *cs, int R, bool interleaved, float sign, int t, int G, float *stage) {
+    if constexpr (KIND != kSingle) {  // threads without pairs have the angle 0
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const int c = 8 * t + i;
-            if (c < 2 * R) {
-                const float2 a = cs[c >> 1];
-                const float s = sign * a.y, y = x[i] * a.x - x[i + 1] * s;
-                x[i + 1] = fmaf(x[i + 1], a.x, x[i] * s);
-                x[i] = y;
-            }
+        for (int i = 0; i < 4; ++i) {
+            float &a = KIND == kInterleaved ? x[2 * i] : x[i], &b = KIND == kInterleaved ? x[2 * i + 1] : x[4 + i];
+            const float s = sign * cs[i].y, y = a * cs[i].x - b * s;
+            b = fmaf(b, cs[i].x, a * s);
+            a = y;
         }
-        return;
-    }
-    if (VEC && (R & 7) == 0) {  // a run's partners are another thread's run
-        const int by = R >> 3, lane = threadIdx.x & 31;
-        const bool low = t < by, in = t < 2 * by;
-        const int from = in ? (low ? lane + by : lane - by) : lane;
+    } else {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (t + G * i < 2 * R) stage[t + G * i] = x[i];
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float other = __shfl_sync(0xffffffffu, x[i], from);
-            if (in) {
-                const float2 a = cs[8 * (low ? t : t - by) + i];
-                x[i] = fmaf(low ? -other : other, sign * a.y, x[i] * a.x);
+            const int c = t + G * i;
+            if (c < 2 * R) {
+                const bool low = interleaved ? (c & 1) == 0 : c < R;
+                const float other = stage[interleaved ? c ^ 1 : low ? c + R : c - R];
+                x[i] = fmaf(low ? -other : other, sign * cs[i].y, x[i] * cs[i].x);
             }
-        }
-        return;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (channel<VEC>(t, G, i) < 2 * R) stage[channel<VEC>(t, G, i)] = x[i];
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = channel<VEC>(t, G, i);
-        if (c < 2 * R) {
-            const bool low = interleaved ? (c & 1) == 0 : c < R;
-            const int pair = interleaved ? c >> 1 : low ? c : c - R;
-            const float other = stage[interleaved ? c ^ 1 : low ? c + R : c - R];
-            const float2 a = cs[pair];
-            x[i] = fmaf(low ? -other : other, sign * a.y, x[i] * a.x);
         }
     }
 }
@@ -156,30 +174,30 @@ __device__ __forceinline__ int64_t position(const QkNormArgs &p, int64_t t) {
     return p.wide_positions ? static_cast<const int64_t *>(p.positions)[t] : static_cast<const int32_t *>(p.positions)[t];
 }
 
-// A CTA takes `tokens` tokens at a time, every gridDim.x-th of such blocks. Dynamic shared memory:
-// the pairs' fractions of a turn, the tokens' (cos, sin) [tokens][R], the groups' stages.
-struct Layout {
-    int tokens, G;
-    __host__ __device__ size_t angles(int R) const { return 8 * (size_t)R; }
-    __host__ __device__ size_t stages(int R) const { return angles(R) + (size_t)tokens * R * 8; }
-    __host__ __device__ size_t bytes(int R, bool staged) const {
-        return stages(R) + (staged ? (size_t)kThreads / G * 2 * R * 4 : 0);
-    }
-};
+// Rows of a group that are in flight at once
+template <bool BWD>
+constexpr int kBatch = BWD ? 2 : 4;
 
-template <typename T, bool VEC, bool BWD>
-__global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkNormArgs p, const Layout l) {
-    extern __shared__ __align__(16) char smem[];
-    uint64_t *frac = reinterpret_cast<uint64_t *>(smem);
-    float2 *cs = reinterpret_cast<float2 *>(smem + l.angles(p.n_freqs));
-    const int R = p.n_freqs, G = l.G, groups = kThreads / G;
-    const int tid = threadIdx.x, group = tid / G, t = tid % G;
-    float *stage = reinterpret_cast<float *>(smem + l.stages(R)) + group * 2 * R;
-    const int heads = p.heads[0] + p.heads[1];
-    for (int i = tid; i < R; i += kThreads) frac[i] = turn_fraction(p.freqs[i]);
-    float w[2][8];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) load_row<VEC>(p.weight[n], p.d, t, G, w[n]);
+// A CTA's warps take kThreads / 32 / share tokens at a time, share of them the heads of one; every
+// gridDim.x-th of such blocks of tokens. Dynamic shared memory (not VEC): the groups' stages.
+template <typename T, Kind KIND, bool BWD>
+__global__ void __launch_bounds__(kThreads, BWD ? 3 : 4) qk_norm_kernel(const QkNormArgs p, int G, int share) {
+    extern __shared__ __align__(16) float stages[];
+    __shared__ __align__(16) float weight[2][kMaxD];
+    __shared__ uint64_t fraction[kMaxD / 2];
+    constexpr bool VEC = KIND != kSingle;
+    constexpr int NB = kBatch<BWD>, NA = VEC ? 4 : 8;
+    if constexpr (BWD) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int R = p.n_freqs, tid = threadIdx.x, warp = tid >> 5, t = tid & (G - 1);
+    const int per_warp = 32 / G, first = (warp % share) * per_warp + (tid & 31) / G, stride = share * per_warp;  // heads
+    const Runs run = runs(t, R, KIND == kInterleaved);
+    float *stage = stages + tid / G * 2 * R;
+    for (int i = tid; i < kMaxD; i += kThreads) {
+        weight[0][i] = i < p.d ? p.weight[0][i] : 0.f;
+        weight[1][i] = i < p.d ? p.weight[1][i] : 0.f;
+    }
+    for (int i = tid; i < R; i += kThreads) fraction[i] = turn_fraction(p.freqs[i]);
+    __syncthreads();
     float dw[2][8];
     if constexpr (BWD)
 #pragma unroll
@@ -187,55 +205,83 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkNormArgs p, c
 #pragma unroll
             for (int i = 0; i < 8; ++i) dw[n][i] = 0.f;
     const float inv_d = 1.f / p.d;
-    for (int64_t t0 = (int64_t)blockIdx.x * l.tokens; t0 < p.n_tok; t0 += (int64_t)gridDim.x * l.tokens) {
-        const int n_tok = (int)min((int64_t)l.tokens, p.n_tok - t0);
-        __syncthreads();
-        for (int i = tid; i < n_tok * R; i += kThreads) {
-            const int tok = i / R;
-            cs[i] = cos_sin(frac[i - tok * R] * (uint64_t)position(p, t0 + tok));
-        }
-        __syncthreads();
-        const int rows = n_tok * heads, rounds = (rows + groups - 1) / groups;
-        for (int n = 0; n < rounds; ++n) {
-            const int row = n * groups + group;
-            const bool live = row < rows;
-            const int tok = live ? row / heads : 0, h = live ? row - tok * heads : 0;
-            const int which = h >= p.heads[0], head = which ? h - p.heads[0] : h;
-            float x[8], u[8];
+    const int tokens = kThreads / 32 / share;
+    for (int64_t tok = (int64_t)blockIdx.x * tokens + warp / share; tok < p.n_tok; tok += (int64_t)gridDim.x * tokens) {
+        float2 cs[NA];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = u[i] = 0.f;
-            if (live) {
-                load_row<VEC>(static_cast<const T *>(p.x[which]) + (t0 + tok) * p.stride[which] + (int64_t)head * p.d, p.d, t, G, x);
-                if constexpr (BWD)
-                    load_row<VEC>(static_cast<const T *>(p.dy[which]) + (t0 + tok) * p.dy_stride[which] + (int64_t)head * p.d, p.d, t, G, u);
-            }
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-            ss = group_sum(ss, G);
-            const float c = 1.f / sqrtf(ss * inv_d + p.eps);
-            T *y = static_cast<T *>(p.y[which]) + ((t0 + tok) * p.heads[which] + head) * p.d;
-            if constexpr (!BWD) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= c * (which ? w[1][i] : w[0][i]);
-                turn<VEC>(x, cs + tok * R, R, p.interleaved, 1.f, t, G, stage);
-                if (live) store_row<VEC>(y, p.d, t, G, x);
-            } else {
-                turn<VEC>(u, cs + tok * R, R, p.interleaved, -1.f, t, G, stage);
-                float tn = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] *= c;
-                    const float un = u[i] * x[i];
-                    if (which) dw[1][i] += un;
-                    else dw[0][i] += un;
-                    u[i] *= which ? w[1][i] : w[0][i];
-                    tn = fmaf(u[i], x[i], tn);
+        for (int which = 0; which < 2; ++which) {
+            const int heads = p.heads[which];
+            const T *x_at = static_cast<const T *>(p.x[which]) + tok * p.stride[which];  // offsets of heads fit 32 bits
+            const T *u_at = BWD ? static_cast<const T *>(p.dy[which]) + tok * p.dy_stride[which] : nullptr;
+            T *y_at = static_cast<T *>(p.y[which]) + tok * heads * p.d;
+            Row<T, VEC> x_row[NB], u_row[BWD ? NB : 1];
+            auto fetch = [&](int n, int h) {
+                if (h < heads) {
+                    x_row[n].load(x_at + h * p.d, p.d, t, G, run);
+                    if constexpr (BWD) u_row[n].load(u_at + h * p.d, p.d, t, G, run);
+                } else {
+                    x_row[n].clear();
+                    if constexpr (BWD) u_row[n].clear();
                 }
-                tn = group_sum(tn, G) * inv_d;
+            };
 #pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = c * (u[i] - x[i] * tn);
-                if (live) store_row<VEC>(y, p.d, t, G, u);
+            for (int n = 0; n < NB; ++n) fetch(n, first + n * stride);
+            if (which == 0) {  // while the first rows are under way
+                const uint64_t at = R > 0 ? (uint64_t)position(p, tok) : 0;
+#pragma unroll
+                for (int i = 0; i < NA; ++i) {
+                    const int c = t + G * i;
+                    const int pair = VEC ? 4 * t + i : p.interleaved ? c >> 1 : c < R ? c : c - R;
+                    cs[i] = cos_sin((VEC ? pair < R : c < 2 * R) ? fraction[pair] * at : 0);
+                }
+            }
+            float w[8];
+            if constexpr (VEC) {
+                const float4 a = *reinterpret_cast<const float4 *>(&weight[which][min(run.a, kMaxD - 4)]);
+                const float4 b = *reinterpret_cast<const float4 *>(&weight[which][min(run.b, kMaxD - 4)]);
+                w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+                w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = weight[which][t + G * i];
+            }
+            // as many rounds for all groups of a warp: its threads meet in the sums
+#pragma unroll 1
+            for (int h0 = first; h0 - (tid & 31) / G < heads; h0 += NB * stride) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const int h = h0 + n * stride;
+                    const bool live = h < heads;
+                    float x[8], u[8];
+                    x_row[n].unpack(x);
+                    if constexpr (BWD) u_row[n].unpack(u);
+                    fetch(n, h + NB * stride);  // on its way as soon as its registers are free
+                    float ss = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+                    ss = group_sum(ss, G);
+                    const float c = rsqrtf(ss * inv_d + p.eps);  // 2^-22 at most
+                    if constexpr (!BWD) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] *= c * w[i];
+                        turn<KIND>(x, cs, R, p.interleaved, 1.f, t, G, stage);
+                        if (live) store_row<VEC>(y_at + h * p.d, x, p.d, t, G, run);
+                    } else {
+                        turn<KIND>(u, cs, R, p.interleaved, -1.f, t, G, stage);
+                        float tn = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            x[i] *= c;
+                            dw[which][i] = fmaf(u[i], x[i], dw[which][i]);
+                            u[i] *= w[i];
+                            tn = fmaf(u[i], x[i], tn);
+                        }
+                        tn = group_sum(tn, G) * inv_d;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) u[i] = c * (u[i] - x[i] * tn);
+                        if (live) store_row<VEC>(y_at + h * p.d, u, p.d, t, G, run);
+                    }
+                }
             }
         }
     }
@@ -249,7 +295,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkNormArgs p, c
             for (int i = 0; i < 8; ++i) {
                 float x = dw[n][i];
                 for (int o = G; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                const int c = channel<VEC>(t, G, i);
+                const int c = VEC ? (i < 4 ? run.a + i : run.b + i - 4) : t + G * i;
                 if ((tid & 31) < G && c < p.d) sum[tid >> 5][c] = x;
             }
             __syncthreads();
@@ -263,59 +309,76 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const QkNormArgs p, c
     }
 }
 
-// dw[n][c] = the sum of the partial rows: a warp per channel column, rows dealt out to its lanes
-__global__ void __launch_bounds__(kThreads) qk_norm_sum_kernel(const float *partial, int rows, int d, float *dq, float *dk) {
-    const int n = blockIdx.y, c0 = blockIdx.x * 32, c = c0 + (threadIdx.x & 31), part = threadIdx.x >> 5;
-    __shared__ float sum[kThreads / 32][32];
+// dw[n][c] = the sum of the partial rows, 32 channels a CTA, the rows dealt out to its warps
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads) qk_norm_sum_kernel(const float *partial, int rows, int d, float *dq, float *dk) {
+    const int n = blockIdx.y, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, part = threadIdx.x >> 5;
+    __shared__ float sum[kSumThreads / 32][32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float x = 0.f;
-    if (c < d)
-        for (int i = part; i < rows; i += kThreads / 32) x += partial[((int64_t)n * rows + i) * d + c];
-    sum[part][threadIdx.x & 31] = x;
+    if (c < d) {
+        const float *at = partial + (int64_t)n * rows * d + c;
+#pragma unroll 8
+        for (int i = part; i < rows; i += kSumThreads / 32) x += at[(int64_t)i * d];
+    }
+    sum[part][lane] = x;
     __syncthreads();
     if (part == 0 && c < d) {
         x = 0.f;
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) x += sum[i][threadIdx.x];
+        for (int i = 0; i < kSumThreads / 32; ++i) x += sum[i][lane];
         (n ? dk : dq)[c] = x;
     }
 }
 
-constexpr int kBwdBlocks = 152 * 4;
+constexpr int kBlocks = 152 * 4, kBwdBlocks = 152 * 3;
 
+// four channels of a row at once: rows of 16 (fp32) or 8 bytes, pairs in fours
 template <typename T>
 bool vector_rows(const QkNormArgs &p, bool bwd) {
-    if (p.d % 8 != 0) return false;
+    if (p.d % 8 != 0 || p.n_freqs % 4 != 0) return false;
+    constexpr size_t align = 4 * sizeof(T);
     for (int i = 0; i < 2; ++i) {
         const void *ptrs[] = {p.x[i], p.y[i], bwd ? p.dy[i] : nullptr};
         for (const void *x : ptrs)
-            if ((uintptr_t)x % 16 != 0) return false;
-        if ((uintptr_t)p.weight[i] % 16 != 0) return false;
-        if (p.stride[i] * sizeof(T) % 16 != 0 || (bwd && p.dy_stride[i] * sizeof(T) % 16 != 0)) return false;
+            if ((uintptr_t)x % align != 0) return false;
+        if (p.stride[i] % 4 != 0 || (bwd && p.dy_stride[i] % 4 != 0)) return false;
     }
     return true;
 }
 
 template <typename T, bool BWD>
 cudaError_t run(const QkNormArgs &p, cudaStream_t stream) {
-    const int heads = p.heads[0] + p.heads[1];
-    Layout l;
-    l.G = 1;
-    while (8 * l.G < p.d) l.G *= 2;
-    // as many tokens as give every group a few rows, and every thread a sine
-    const int groups = kThreads / l.G;
-    l.tokens = std::max(1, std::min(16, 8 * groups / heads));
-    const int64_t blocks = (p.n_tok + l.tokens - 1) / l.tokens;
-    const unsigned grid = (unsigned)(BWD ? std::min<int64_t>(blocks, kBwdBlocks) : std::min<int64_t>(blocks, 0x7fffffff));
+    int G = 1;
+    while (8 * G < p.d) G *= 2;
+    const int warps = kThreads / 32, heads = std::max(p.heads[0], p.heads[1]);
+    // A token to a warp, which forms its angles; with too few tokens for the warps of all SMs to several, as far
+    // as there are heads (backward, whose rows take longer, with less than four each)
+    int share = 1;
+    while (share < warps && p.n_tok * share < (BWD ? 4 * kBwdBlocks : kBlocks) * warps && share * (32 / G) < heads) share *= 2;
+    const int64_t blocks = (p.n_tok * share + warps - 1) / warps;
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, BWD ? kBwdBlocks : kBlocks);
     const bool vec = vector_rows<T>(p, BWD);
-    const bool staged = !(vec && (p.interleaved || p.n_freqs % 8 == 0));
-    const size_t smem = l.bytes(p.n_freqs, staged);
+    const size_t smem = vec ? 0 : (size_t)kThreads / G * 2 * p.n_freqs * 4;
     if (grid > 0) {
-        if (vec) qk_norm_kernel<T, true, BWD><<<grid, kThreads, smem, stream>>>(p, l);
-        else qk_norm_kernel<T, false, BWD><<<grid, kThreads, smem, stream>>>(p, l);
+        if (!vec) qk_norm_kernel<T, kSingle, BWD><<<grid, kThreads, smem, stream>>>(p, G, share);
+        else if (p.interleaved) qk_norm_kernel<T, kInterleaved, BWD><<<grid, kThreads, smem, stream>>>(p, G, share);
+        else qk_norm_kernel<T, kHalves, BWD><<<grid, kThreads, smem, stream>>>(p, G, share);
         count_launches(1);
     }
     if (BWD) {
-        qk_norm_sum_kernel<<<dim3((p.d + 31) / 32, 2), kThreads, 0, stream>>>(p.partial, (int)grid, p.d, p.dw[0], p.dw[1]);
+        // launched early: it waits for the partial rows on the device
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((p.d + 31) / 32, 2);
+        cfg.blockDim = dim3(kSumThreads);
+        cfg.stream = stream;
+        cfg.attrs = &attr;
+        cfg.numAttrs = grid > 0 ? 1 : 0;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, qk_norm_sum_kernel, (const float *)p.partial, (int)grid, (int)p.d, p.dw[0], p.dw[1]);
+        if (e != cudaSuccess) return e;
         count_launches(1);
     }
     return cudaGetLastError();
