@@ -475,7 +475,7 @@ cudaError_t forward(const DlaArgs &p, cudaStream_t stream) {
 
 size_t dla_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k, int32_t d_v,
                            bool bf16, bool bwd) {
-    if (!bf16) return dla_simt_workspace_bytes(n_tok, n_seq, n_heads, d_k, d_v, bwd);
+    if (!bf16) return dla_simt_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v, bwd);
     return bwd ? dla_tc_bwd_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v)
                : dla_tc_fwd_workspace_bytes(n_tok, n_seq, n_heads, d_k);
 }
