@@ -604,10 +604,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 if (r < C) G = {t->G[r].x, t->G[r].y};
                 else if (two) G = add({s0.x, s0.y}, {t[p.n_heads].G[r - C].x, t[p.n_heads].G[r - C].y});
                 g.G[r] = make_float2(G.hi, G.lo);
-                g.gam[r] = p.scale * exp2_of(G);
+                g.gam[r] = p.scale * ex2(G.hi) * ex2(G.lo);  // a whole part and a fraction, or a sum of such
                 g.del[r] = exp2_between(make_float2(total.hi, total.lo), make_float2(G.hi, G.lo));
             }
-            if (lane == 0) g.whole = exp2_of(total);
+            if (lane == 0) g.whole = ex2(total.hi) * ex2(total.lo);
             warp_arrive(bar(L::GFull + (n & 1)));
         };
         auto decays = [&](const Block &c, int n) {  // dg of a unit, four neighbouring tokens a lane

@@ -53,7 +53,9 @@ struct FwdSmem {
 // columns of tensor memory
 constexpr int kTmDs = 0, kTmS = 128, kTmO1 = 256, kTmV = 320, kTmQk = 384;  // kTmQk: Q K^T, then O2, of two tiles
 
-template <int DK>
+// OWN: the gates are formed here, by a loading warp (short calls; apart, because the rest takes 1.3 times as
+// long with that code beside it)
+template <int DK, bool OWN>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     dla_forward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const DlaArgs p, const Plan plan, bool copies,
@@ -260,7 +262,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 rows_loaded();
                 if (lane == 0) ptx::mbar_arrive(m);
             }
-            if (pair && lane == 0) {
+            if (OWN && pair) {
+                const int r = 2 * lane;
+                const float *g = p.g + (t0 + r) * p.g_stride + head;
+                form_gates(make_float2(r < rows ? g[0] : 0.f, r + 1 < rows ? g[p.g_stride] : 0.f), p.scale,
+                           reinterpret_cast<TileGates *>(smem + L::Gate) + c % L::kGates);
+                warp_arrive(bar(L::GFull + c % L::kGates));
+            } else if (pair && lane == 0) {
                 if (c == 0) gdr::wait_for_previous_kernel();  // the gates
                 const uint32_t gm = bar(L::GFull + c % L::kGates);
                 ptx::mbar_arrive_tx(gm, sizeof(TileGates));
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // nothing may land in shared memory after the block has gone
         if (!ok) {
             for (int c = max(0, begun - S); c < begun; ++c) drain_bar(bar(full + c % S), (c / S) & 1);
-            if (pair)
+            if (pair && !OWN)
                 for (int c = max(0, begun - L::kGates); c < begun; ++c) drain_bar(bar(L::GFull + c % L::kGates), (c / L::kGates) & 1);
         }
     } else if (warp < 8) {
@@ -463,11 +471,21 @@ cudaError_t forward(const DlaArgs &p, cudaStream_t stream) {
                         TileMap::encode(&v, p.v, p.n_tok, p.v_stride, p.n_heads, p.d_v);
     const bool wide = p.d_v % 8 == 0 && (uintptr_t)p.out % 16 == 0;
     const Plan plan = make_plan(p, false);
+    // A short call forms the gates beside the tiles' copies: a launch less (40 tokens of 32 heads in a graph:
+    // ... us, ... with the launch), but 2 us a tile that nothing hides.
+    const dim3 grid((unsigned)(plan.slots * p.n_heads));
+    if (p.n_tok <= 4 * C && !plan.cut) {
+        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dla_forward_kernel<DK, true>), FwdSmem<DK>::kBytes);
+        if (e != cudaSuccess) return e;
+        dla_forward_kernel<DK, true><<<grid, kFwdThreads, FwdSmem<DK>::kBytes, stream>>>(q, k, v, p, plan, copies, wide);
+        count_launches(1);
+        return cudaGetLastError();
+    }
     cudaError_t e = launch_gates(p, plan, stream);
     if (e == cudaSuccess && plan.cut) e = launch_segments<DK>(p, plan, q, k, v, v, copies, 1, stream);
     if (e != cudaSuccess) return e;
-    return gdr::launch_dependent(dla_forward_kernel<DK>, dim3((unsigned)(plan.slots * p.n_heads)), kFwdThreads, FwdSmem<DK>::kBytes,
-                                 stream, q, k, v, p, plan, copies, wide);
+    return gdr::launch_dependent(dla_forward_kernel<DK, false>, grid, kFwdThreads, FwdSmem<DK>::kBytes, stream, q, k, v, p, plan, copies,
+                                 wide);
 }
 
 }  // namespace

@@ -170,6 +170,7 @@ __device__ __forceinline__ int64_t chunk_at(const DlaArgs &p, int64_t slot, int 
 __global__ void __launch_bounds__(kThreads) dla_simt_add_kernel(const DlaArgs p, bool bwd) {
     __shared__ __align__(16) float ks[C][kDkBlock], vs[C][128];
     __shared__ Gates gate;
+    gdr::let_next_kernel_start();
     const int64_t slot = blockIdx.x;
     const Chunk ch = find_chunk(p.cu_seqlens, p.n_seq, slot);
     if (ch.len == 0) return;
@@ -227,6 +228,8 @@ __global__ void __launch_bounds__(kThreads) dla_simt_add_kernel(const DlaArgs p,
 // add, and the sequences' last: one element of a sequence's and head's state a thread
 __global__ void __launch_bounds__(kThreads) dla_simt_walk_kernel(const DlaArgs p, bool bwd) {
     constexpr int kAhead = 8;
+    gdr::let_next_kernel_start();
+    gdr::wait_for_previous_kernel();
     const bool rev = blockIdx.z == 1;
     const int seq = blockIdx.x / p.n_heads, head = blockIdx.x % p.n_heads;
     const Space s = space_of(p, bwd);
@@ -292,11 +295,15 @@ __global__ void __launch_bounds__(kThreads) dla_simt_out_kernel(const DlaArgs p)
     S &s = *reinterpret_cast<S *>(smem_raw);
     const int64_t slot = blockIdx.x;
     const Chunk ch = find_chunk(p.cu_seqlens, p.n_seq, slot);
-    if (ch.len == 0) return;
+    if (ch.len == 0) {
+        gdr::wait_for_previous_kernel();
+        return;
+    }
     const int head = blockIdx.y, kh = head / (p.n_heads / p.n_k_heads);
     load_tile<16 * NK>(s.q, static_cast<const float *>(p.q) + ch.t0 * p.q_stride + (int64_t)kh * p.d_k, p.q_stride, ch.len, p.d_k);
     load_tile<16 * NK>(s.k, static_cast<const float *>(p.k) + ch.t0 * p.k_stride + (int64_t)kh * p.d_k, p.k_stride, ch.len, p.d_k);
     load_tile<16 * NV>(s.v, static_cast<const float *>(p.v) + ch.t0 * p.v_stride + (int64_t)head * p.d_v, p.v_stride, ch.len, p.d_v);
+    gdr::wait_for_previous_kernel();
     load_state<NK, NV>(s.s, static_cast<const float *>(p.workspace) + chunk_at(p, slot, head, false) * p.d_k * p.d_v, p.d_k, p.d_v);
     if (threadIdx.x < 32) chunk_gates(p, ch, head, &s.gate);
     __syncthreads();
@@ -341,7 +348,9 @@ __global__ void __launch_bounds__(kThreads) dla_simt_grad_kernel(const DlaArgs p
     const Space at = space_of(p, true);
     float *ws = static_cast<float *>(p.workspace);
     float *sums = p.dg && p.g_stride == 0 ? ws + at.sums : nullptr;
+    gdr::let_next_kernel_start();
     if (ch.len == 0) {
+        gdr::wait_for_previous_kernel();
         if (sums && tid == 0) sums[slot * p.n_heads + head] = 0.f;
         return;
     }
@@ -351,6 +360,7 @@ __global__ void __launch_bounds__(kThreads) dla_simt_grad_kernel(const DlaArgs p
     load_tile<16 * NK>(s.k, static_cast<const float *>(p.k) + ch.t0 * p.k_stride + (int64_t)kh * p.d_k, p.k_stride, ch.len, p.d_k);
     load_tile<16 * NV>(s.v, static_cast<const float *>(p.v) + ch.t0 * p.v_stride + (int64_t)head * p.d_v, p.v_stride, ch.len, p.d_v);
     load_tile<16 * NV>(s.d, static_cast<const float *>(p.dout) + ch.t0 * row + (int64_t)head * p.d_v, row, ch.len, p.d_v);
+    gdr::wait_for_previous_kernel();
     load_state<NK, NV>(s.s, ws + chunk_at(p, slot, head, false) * at.state, p.d_k, p.d_v);
     if (warp == 0) chunk_gates(p, ch, head, &s.gate);
     __syncthreads();
@@ -493,6 +503,7 @@ __global__ void __launch_bounds__(kThreads) dla_simt_grad_kernel(const DlaArgs p
 
 // dq (blockIdx.y = 0) or dk of a key head: the sum of its value heads' parts
 __global__ void __launch_bounds__(kThreads) dla_simt_shared_heads_kernel(const DlaArgs p) {
+    gdr::wait_for_previous_kernel();
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, group = p.n_heads / p.n_k_heads;
     if (i >= p.n_tok * p.n_k_heads * p.d_k) return;
     const Space at = space_of(p, true);
@@ -522,17 +533,8 @@ __global__ void __launch_bounds__(kThreads) dla_sum_decay_kernel(const float *su
 template <int NK, int NV>
 cudaError_t results(const DlaArgs &p, bool bwd, cudaStream_t stream) {
     const dim3 grid((unsigned)n_slots(p.n_tok, p.n_seq), p.n_heads);
-    if (!bwd) {
-        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dla_simt_out_kernel<NK, NV>), sizeof(OutSmem<NK, NV>));
-        if (e != cudaSuccess) return e;
-        dla_simt_out_kernel<NK, NV><<<grid, kThreads, sizeof(OutSmem<NK, NV>), stream>>>(p);
-    } else {
-        const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dla_simt_grad_kernel<NK, NV>), sizeof(GradSmem<NK, NV>));
-        if (e != cudaSuccess) return e;
-        dla_simt_grad_kernel<NK, NV><<<grid, kThreads, sizeof(GradSmem<NK, NV>), stream>>>(p);
-    }
-    count_launches(1);
-    return cudaGetLastError();
+    return bwd ? gdr::launch_dependent(dla_simt_grad_kernel<NK, NV>, grid, kThreads, sizeof(GradSmem<NK, NV>), stream, p)
+               : gdr::launch_dependent(dla_simt_out_kernel<NK, NV>, grid, kThreads, sizeof(OutSmem<NK, NV>), stream, p);
 }
 
 }  // namespace
@@ -557,20 +559,17 @@ cudaError_t launch_dla_simt(const DlaArgs &p, bool bwd, cudaStream_t stream) {
         dla_simt_add_kernel<<<grid, kThreads, 0, stream>>>(p, bwd);
         count_launches(1);
     }
-    if (p.n_seq > 0) {
-        const dim3 grid((unsigned)p.n_seq * p.n_heads, (p.d_k * p.d_v + kThreads - 1) / kThreads, walks);
-        dla_simt_walk_kernel<<<grid, kThreads, 0, stream>>>(p, bwd);
-        count_launches(1);
-    }
     cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && p.n_seq > 0) {
+        const dim3 grid((unsigned)p.n_seq * p.n_heads, (p.d_k * p.d_v + kThreads - 1) / kThreads, walks);
+        e = gdr::launch_dependent(dla_simt_walk_kernel, grid, kThreads, 0, stream, p, bwd);
+    }
     if (e == cudaSuccess && p.n_tok > 0) {
         if (p.d_k <= 64) e = p.d_v <= 64 ? results<4, 4>(p, bwd, stream) : results<4, 8>(p, bwd, stream);
         else e = p.d_v <= 64 ? results<8, 4>(p, bwd, stream) : results<8, 8>(p, bwd, stream);
         if (e == cudaSuccess && bwd && p.n_heads > p.n_k_heads) {
             const int64_t n = p.n_tok * p.n_k_heads * p.d_k;
-            dla_simt_shared_heads_kernel<<<dim3((unsigned)((n + kThreads - 1) / kThreads), 2), kThreads, 0, stream>>>(p);
-            count_launches(1);
-            e = cudaGetLastError();
+            e = gdr::launch_dependent(dla_simt_shared_heads_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads), 2), kThreads, 0, stream, p);
         }
     }
     if (e == cudaSuccess && bwd && p.dg && p.g_stride == 0) {
