@@ -43,7 +43,7 @@ struct WalkSmem {
     static constexpr int kStages = 4;
     static constexpr int Out = kStages * kStage, Bars = Out + 2 * plane_bytes(DK, DV);
     static constexpr int Full = 0, Empty = kStages, VpFull = 2 * kStages, VpEmpty = VpFull + 1, DsFull = VpEmpty + 1,
-                         DsEmpty = DsFull + 2, OutFull = DsEmpty + 2, OutEmpty = OutFull + 1, Drain = OutEmpty + 1, kBars = Drain + 1;
+                         DsEmpty = DsFull + 2, OutFull = DsEmpty + 2, OutEmpty = OutFull + 1, Drain = OutEmpty + 1, Partial = Drain + 1, kBars = Partial + 1;
     static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;  // the base is rounded up to 1024
     static_assert(sizeof(TileGates) <= 2048 && kBytes <= 227 * 1024, "fits an SM");
 };
@@ -89,13 +89,10 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
         ptx::mbar_init(bar(L::OutFull), 8);
         ptx::mbar_init(bar(L::OutEmpty), 1);
         ptx::mbar_init(bar(L::Drain), 1);
+        ptx::mbar_init(bar(L::Partial), 1);
         ptx::mbar_init_fence();
     }
     if (warp == 0) ptx::tmem_alloc(bar(L::kBars), 512);
-    if (p.d_v <= 64)  // channels that no value head has
-        for (int i = tid; i < S * kHalf / 16; i += kWalkThreads)
-            *reinterpret_cast<uint4 *>(smem + (i / (kHalf / 16)) * L::kStage + L::V + kHalf + (i % (kHalf / 16)) * 16) = make_uint4(0, 0, 0, 0);
-    ptx::fence_proxy_async();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -146,15 +143,29 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
             if (!ok) break;
             const uint32_t at = base + s * L::kStage, m = bar(L::Full + s);
             const int64_t t0 = sg.t0 + (int64_t)c * C;
-            const bool copy = copies && rows == C;
-            if (!copy) {
+            const uint32_t bytes = copies ? L::kKey + in[1].halves * kHalf : 0;
+            if (!copies) {
                 const uint32_t to[2] = {at + L::K, at + L::V};
                 tiles_by_threads(in, to, 2, t0, rows, lane, 32);
                 rows_loaded();
+            } else if (rows < C) {
+                // copied whole; what is another sequence's goes before it is handed over
+                const uint32_t by = bar(L::Partial);
+                if (lane == 0) {
+                    ptx::mbar_arrive_tx(by, bytes);
+                    tile_by_copy(in[0], at + L::K, t0, by);
+                    tile_by_copy(in[1], at + L::V, t0, by);
+                }
+                if (!wait_bar(by, 0)) drain_bar(by, 0);
+                clear_rows(at + L::K, in[0].halves, kHalf, rows, C);
+                clear_rows(at + L::V, in[1].halves, kHalf, rows, C);
+                ptx::fence_proxy_async();
+                __syncwarp();
             }
             if (lane == 0) {
-                ptx::mbar_arrive_tx(m, (uint32_t)sizeof(TileGates) + (copy ? L::kKey + in[1].halves * kHalf : 0));
-                if (copy) {
+                const bool whole = copies && rows == C;
+                ptx::mbar_arrive_tx(m, (uint32_t)sizeof(TileGates) + (whole ? bytes : 0));
+                if (whole) {
                     tile_by_copy(in[0], at + L::K, t0, m);
                     tile_by_copy(in[1], at + L::V, t0, m);
                 }
@@ -190,7 +201,8 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
             if (n > 0) wait(L::VpEmpty, n - 1);
             ptx::tc_fence_after();
             const TileGates *g = reinterpret_cast<const TileGates *>(smem + s * L::kStage + L::Gate);
-            scale_values(base + s * L::kStage + L::V, tmem, 256, REV ? g->gam : g->del, 1.f);
+            if (32 * (warp & 3) < p.d_v)  // other lanes' rows are not read
+                scale_values(base + s * L::kStage + L::V, tmem, 256, REV ? g->gam : g->del, 1.f);
             ptx::tc_fence_before();
             warp_arrive(bar(L::VpFull));
             warp_arrive(bar(L::Empty + s));
@@ -199,6 +211,7 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
         constexpr int NC = DK / 2;  // key channels of a thread
         const int dv = (warp & 3) * 32 + lane, part = (warp - 8) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const bool live = 32 * (warp & 3) < DV;  // the channels that are kept
         float st[NC];
         const bool cut = sg.index > 0 || !sg.last;
         gdr::wait_for_previous_kernel();
@@ -212,7 +225,7 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
         for (int n = 0; n < nc; ++n) {
             if (enters(n)) {
                 if (kept > 0) wait(L::OutEmpty, kept - 1);
-                if (dv < DV) {
+                if (live) {
 #pragma unroll
                     for (int i = 0; i < NC; i += 8) {
                         uint32_t hi[4], lo[4];
@@ -235,6 +248,7 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
             warp_arrive(bar(L::Empty + s));
             wait(L::DsFull + (n & 1), n >> 1);
             ptx::tc_fence_after();
+            if (32 * (warp & 3) < p.d_v)
 #pragma unroll
             for (int i = 0; i < NC; i += 16) {
                 float d[16];
@@ -297,7 +311,7 @@ struct GradSmem {
     static constexpr int Sums = Gate + 2 * (int)sizeof(BlockGates), Bars = Sums + (int)sizeof(BlockSums);
     static constexpr int KqFull = 0, VoFull = 1, TilesEmpty = 2, X0Full = 3, X1Full = 4, X0Empty = 5, X1Empty = 6, F1 = 7, F2 = 8,
                          WFull = 9, F3 = 10, AEmpty = 11, F4 = 12, PFull = 13, Scaled = 14, F5 = 15, CEmpty = 16, GFull = 17,
-                         GEmpty = 19, SumsFull = 21, SumsEmpty = 22, Drain = 23, kBars = 24;
+                         GEmpty = 19, SumsFull = 21, SumsEmpty = 22, Drain = 23, Partial = 24, kBars = 26;
     static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;  // the base is rounded up to 1024
     static_assert(sizeof(BlockGates) % 16 == 0 && sizeof(BlockSums) % 16 == 0 && kBytes <= 227 * 1024, "fits an SM");
 };
@@ -393,7 +407,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     BlockSums &sums = *reinterpret_cast<BlockSums *>(smem + L::Sums);
     if (tid == 0) {
         const int ones[] = {L::KqFull, L::VoFull, L::X0Full, L::X1Full, L::X0Empty, L::F1, L::F2, L::F3, L::F4, L::F5, L::GFull,
-                            L::GFull + 1, L::SumsEmpty, L::Drain};
+                            L::GFull + 1, L::SumsEmpty, L::Drain, L::Partial, L::Partial + 1};
         for (int i : ones) ptx::mbar_init(bar(i), 1);
         const int eights[] = {L::WFull, L::AEmpty, L::PFull, L::Scaled, L::CEmpty};
         for (int i : eights) ptx::mbar_init(bar(i), 8);
@@ -521,6 +535,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         drain_bar(bar(L::Drain), 0);
     } else if (warp == 1) {
         ptx::regs_decrease<kGradServe>();
+        int partials = 0;
         for (int64_t u = blockIdx.x; next_unit(u, b); u += gridDim.x, ++i) {
             if (i > 0) wait(L::TilesEmpty, i - 1);
             ok = __all_sync(0xffffffffu, ok);
@@ -532,15 +547,29 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                                   {&tm_v, static_cast<const __nv_bfloat16 *>(p.v), p.v_stride, b.head, p.d_v, DV / 64, bp.walk.vec_v},
                                   {&tm_o, static_cast<const __nv_bfloat16 *>(p.dout), ov, b.head, p.d_v, DV / 64, bp.walk.vec_o}};
             const int to[4] = {L::K, L::Q, L::V, L::dO};
-            if (copies && b.len == kBlock) {
+            if (copies) {
+                // a partial block is copied whole; what is another sequence's goes before it is handed over
+                const bool whole = b.len == kBlock;
                 if (lane == 0) {
 #pragma unroll 1
                     for (int n = 0; n < 4; ++n) {
-                        const uint32_t m = bar(n < 2 ? L::KqFull : L::VoFull);
+                        const uint32_t m = bar(whole ? (n < 2 ? L::KqFull : L::VoFull) : n < 2 ? L::Partial : L::Partial + 1);
                         if ((n & 1) == 0) ptx::mbar_arrive_tx(m, n < 2 ? 2 * L::kKey : 2 * L::kVal);
                         for (int h = 0; h < in[n].halves; ++h)
                             ptx::tma_load_3d(base + to[n] + h * kWide, in[n].map, h * 64, in[n].head, (int)b.t0, m);
                     }
+                }
+                if (!whole) {
+#pragma unroll 1
+                    for (int n = 0; n < 4; n += 2) {
+                        const uint32_t by = bar(L::Partial + n / 2);
+                        if (!wait_bar(by, partials & 1)) drain_bar(by, partials & 1);
+                        clear_rows(base + to[n], in[n].halves, kWide, b.len, kBlock);
+                        clear_rows(base + to[n + 1], in[n + 1].halves, kWide, b.len, kBlock);
+                        ptx::fence_proxy_async();
+                        warp_arrive(bar(n < 2 ? L::KqFull : L::VoFull));
+                    }
+                    ++partials;
                 }
             } else {
 #pragma unroll 1

@@ -46,7 +46,7 @@ struct FwdSmem {
                          GFull = VEmpty + kStages, GEmpty = GFull + kGates, QkFull = GEmpty + kGates, PFull = QkFull + 2,
                          PEmpty = PFull + 1, VpFull = PEmpty + 1, VpEmpty = VpFull + 1, DsFull = VpEmpty + 1,
                          DsEmpty = DsFull + 1, SFull = DsEmpty + 1, O1Full = SFull + 1, O1Empty = O1Full + 1,
-                         O2Full = O1Empty + 1, O2Empty = O2Full + 2, Drain = O2Empty + 2, kBars = Drain + 2;
+                         O2Full = O1Empty + 1, O2Empty = O2Full + 2, Drain = O2Empty + 2, Partial = Drain + 2, kBars = Partial + 2;
     static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;  // the base is rounded up to 1024
     static_assert(kBytes <= 227 * 1024, "fits an SM");
 };
@@ -86,6 +86,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     };
     auto rows_of = [&](int c) { return (int)min((int64_t)C, sg.len - (int64_t)c * C); };
 
+    // the state's lines are asked for while the block sets itself up
+    if (p.h0 && sg.index == 0 && sg.last && tid * 32 < p.d_k * p.d_v)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.h0 + state_at + tid * 32));
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             ptx::mbar_init(bar(L::KFull + i), 1);
@@ -114,14 +117,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         ptx::mbar_init(bar(L::O2Empty + 1), 8);
         ptx::mbar_init(bar(L::Drain), 1);
         ptx::mbar_init(bar(L::Drain + 1), 1);
+        ptx::mbar_init(bar(L::Partial), 1);
+        ptx::mbar_init(bar(L::Partial + 1), 1);
         ptx::mbar_init_fence();
     }
     if (warp == 0) ptx::tmem_alloc(bar(L::kBars), 512);
-    // P is zero above its diagonal blocks, V in channels that no value head has
+    // P is zero above its diagonal blocks
     for (int i = tid; i < 2 * kHalf / 16; i += kFwdThreads) reinterpret_cast<uint4 *>(smem + L::P)[i] = make_uint4(0, 0, 0, 0);
-    if (p.d_v <= 64)
-        for (int i = tid; i < S * kHalf / 16; i += kFwdThreads)
-            *reinterpret_cast<uint4 *>(smem + L::V + (i / (kHalf / 16)) * L::kVal + kHalf + (i % (kHalf / 16)) * 16) = make_uint4(0, 0, 0, 0);
     ptx::fence_proxy_async();
     ptx::tc_fence_before();
     __syncthreads();
@@ -251,11 +253,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const uint32_t to[2] = {base + (pair ? s * L::kPair + L::K : L::V + s * L::kVal), base + s * L::kPair + L::Q};
             const int64_t t0 = sg.t0 + (int64_t)c * C;
             const uint32_t m = bar(full + s);
-            if (copies && rows == C) {
+            if (copies) {
+                // a partial tile is copied whole; what is another sequence's goes before it is handed over
+                const uint32_t by = rows == C ? m : bar(L::Partial + (pair ? 0 : 1));
                 if (lane == 0) {
-                    ptx::mbar_arrive_tx(m, pair ? 2 * L::kKey : in[0].halves * kHalf);
-                    tile_by_copy(in[0], to[0], t0, m);
-                    if (pair) tile_by_copy(in[1], to[1], t0, m);
+                    ptx::mbar_arrive_tx(by, pair ? 2 * L::kKey : in[0].halves * kHalf);
+                    tile_by_copy(in[0], to[0], t0, by);
+                    if (pair) tile_by_copy(in[1], to[1], t0, by);
+                }
+                if (rows < C) {  // the walk's last
+                    if (!wait_bar(by, 0)) drain_bar(by, 0);
+                    clear_rows(to[0], in[0].halves, kHalf, rows, C);
+                    if (pair) clear_rows(to[1], in[1].halves, kHalf, rows, C);
+                    ptx::fence_proxy_async();
+                    warp_arrive(m);
                 }
             } else {
                 tiles_by_threads(in, to, pair ? 2 : 1, t0, rows, lane, 32);
@@ -292,7 +303,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             wait(L::VFull + s, c / S);
             if (c > 0) wait(L::VpEmpty, c - 1);
             ptx::tc_fence_after();
-            scale_values(base + L::V + s * L::kVal, tmem, kTmV, gate(c).del, 1.f);
+            if (32 * (warp & 3) < p.d_v) scale_values(base + L::V + s * L::kVal, tmem, kTmV, gate(c).del, 1.f);
             ptx::tc_fence_before();
             warp_arrive(bar(L::VpFull));
             warp_arrive(bar(L::GEmpty + c % L::kGates));
@@ -345,6 +356,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         constexpr int NC = DK / 2;  // key channels of a thread
         const int dv = (warp & 3) * 32 + lane, part = (warp - 16) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        // Lanes of channels that no value has hold what they will: a product's row depends on its own lane
+        // alone, and theirs are not read.
+        const bool live = 32 * (warp & 3) < p.d_v;
         float st[NC];
         const bool cut = sg.index > 0 || !sg.last;
         gdr::wait_for_previous_kernel();
@@ -356,6 +370,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 wait(L::O1Full, c - 1);  // the last planes are read
                 ptx::tc_fence_after();
             }
+            if (live)
 #pragma unroll
             for (int i = 0; i < NC; i += 16) {
                 uint32_t hi[8], lo[8];
@@ -373,6 +388,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             warp_arrive(bar(L::GEmpty + c % L::kGates));
             wait(L::DsFull, c);
             ptx::tc_fence_after();
+            if (live)
 #pragma unroll
             for (int i = 0; i < NC; i += 16) {
                 float d[16];

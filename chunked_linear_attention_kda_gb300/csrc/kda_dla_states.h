@@ -152,7 +152,7 @@ struct SegmentSmem {
     static constexpr int K = 0, V = kKey, Gate = V + kVal, kStage = Gate + 2048;
     static constexpr int kStages = 6, Bars = kStages * kStage;
     static constexpr int Full = 0, Empty = kStages, VpFull = 2 * kStages, VpEmpty = VpFull + 2, DsFull = VpEmpty + 2,
-                         DsEmpty = DsFull + 2, Drain = DsEmpty + 2, kBars = Drain + 1;
+                         DsEmpty = DsFull + 2, Drain = DsEmpty + 2, Partial = Drain + 1, kBars = Partial + 1;
     static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;  // the base is rounded up to 1024
     static_assert(sizeof(TileGates) <= 2048 && kBytes <= 227 * 1024, "fits an SM");
 };
@@ -195,13 +195,10 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
             ptx::mbar_init(bar(L::DsEmpty + i), 8);
         }
         ptx::mbar_init(bar(L::Drain), 1);
+        ptx::mbar_init(bar(L::Partial), 1);
         ptx::mbar_init_fence();
     }
     if (warp == 0) ptx::tmem_alloc(bar(L::kBars), 512);
-    if (p.d_v <= 64)  // channels that no value head has
-        for (int i = tid; i < S * kHalf / 16; i += kSegmentThreads)
-            *reinterpret_cast<uint4 *>(smem + (i / (kHalf / 16)) * L::kStage + L::V + kHalf + (i % (kHalf / 16)) * 16) = make_uint4(0, 0, 0, 0);
-    ptx::fence_proxy_async();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -252,15 +249,29 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
             if (!ok) break;
             const uint32_t at = base + s * L::kStage, m = bar(L::Full + s);
             const int64_t t0 = sg.t0 + (int64_t)c * C;
-            const bool copy = copies && rows == C;
-            if (!copy) {
+            const uint32_t bytes = copies ? L::kKey + in[1].halves * kHalf : 0;
+            if (!copies) {
                 const uint32_t to[2] = {at + L::K, at + L::V};
                 tiles_by_threads(in, to, 2, t0, rows, lane, 32);
                 rows_loaded();
+            } else if (rows < C) {
+                // copied whole; what is another sequence's goes before it is handed over
+                const uint32_t by = bar(L::Partial);
+                if (lane == 0) {
+                    ptx::mbar_arrive_tx(by, bytes);
+                    tile_by_copy(in[0], at + L::K, t0, by);
+                    tile_by_copy(in[1], at + L::V, t0, by);
+                }
+                if (!wait_bar(by, 0)) drain_bar(by, 0);
+                clear_rows(at + L::K, in[0].halves, kHalf, rows, C);
+                clear_rows(at + L::V, in[1].halves, kHalf, rows, C);
+                ptx::fence_proxy_async();
+                __syncwarp();
             }
             if (lane == 0) {
-                ptx::mbar_arrive_tx(m, (uint32_t)sizeof(TileGates) + (copy ? L::kKey + in[1].halves * kHalf : 0));
-                if (copy) {
+                const bool whole = copies && rows == C;
+                ptx::mbar_arrive_tx(m, (uint32_t)sizeof(TileGates) + (whole ? bytes : 0));
+                if (whole) {
                     tile_by_copy(in[0], at + L::K, t0, m);
                     tile_by_copy(in[1], at + L::V, t0, m);
                 }
@@ -282,7 +293,8 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
             if ((n & 1) == turn) {
                 if (n >= 2) wait(L::VpEmpty + turn, (n >> 1) - 1);
                 ptx::tc_fence_after();
-                scale_values(base + s * L::kStage + L::V, tmem, 256 + turn * 64, REV ? g->gam : g->del, beyond);
+                if (32 * (warp & 3) < p.d_v)  // other lanes' rows are not read
+                    scale_values(base + s * L::kStage + L::V, tmem, 256 + turn * 64, REV ? g->gam : g->del, beyond);
                 ptx::tc_fence_before();
                 warp_arrive(bar(L::VpFull + turn));
             }
@@ -300,6 +312,7 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
         for (int n = 0; n * kSum < nc; ++n) {
             wait(L::DsFull + (n & 1), n >> 1);
             ptx::tc_fence_after();
+            if (32 * (warp & 3) < p.d_v)
 #pragma unroll
             for (int i = 0; i < NC; i += 16) {
                 float d[16];

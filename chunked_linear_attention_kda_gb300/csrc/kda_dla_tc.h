@@ -65,7 +65,9 @@ struct Segment {
     int64_t t0, len;   // len = 0 and index > 0: an unused slot
     bool last;         // the sequence ends in it
 };
-__device__ __forceinline__ int64_t segment_base(const int32_t *cu, int n, int seg) { return cu[n] / seg + n; }
+__device__ __forceinline__ int64_t segment_base(const int32_t *cu, int n, int seg) {
+    return (int64_t)((uint32_t)cu[n] / (uint32_t)seg) + n;
+}
 __device__ __forceinline__ Segment find_segment(const int32_t *cu, int n_seq, int64_t slot, int seg) {
     int lo = 0, hi = n_seq - 1;  // largest n with segment_base(n) <= slot
     while (lo < hi) {
@@ -115,10 +117,15 @@ struct Source {
     int head, d, halves;   // halves of 64 channels in the tile; those past d stay as they are
     bool vec;              // 16-byte rows
 };
-// The tile of tokens t0 .. t0 + rows by one thread's tensor copies; a full tile only, so that no
-// row of another sequence gets in
+// The tile of the tokens from t0 on by one thread's tensor copies
 __device__ __forceinline__ void tile_by_copy(const Source &s, uint32_t dst, int64_t t0, uint32_t mbar) {
     for (int h = 0; h < s.halves; ++h) ptx::tma_load_3d(dst + h * kHalf, s.map, h * 64, s.head, (int)t0, mbar);
+}
+// Its rows from `rows` on as zeros, by a warp: they are another sequence's. `pitch`: bytes of a half.
+__device__ __forceinline__ void clear_rows(uint32_t dst, int halves, int pitch, int rows, int total) {
+    const uint32_t zero[4] = {0, 0, 0, 0};
+    for (int h = 0; h < halves; ++h)
+        for (int i = rows * 8 + (threadIdx.x & 31); i < total * 8; i += 32) gdr::st_shared_16(dst + h * pitch + i * 16, zero);
 }
 // the same of `n` inputs by threads, rows past the end as zeros
 __device__ __forceinline__ void tiles_by_threads(const Source *inputs, const uint32_t *dst, int n, int64_t t0, int rows,
