@@ -34,13 +34,18 @@ struct Plan {
 // Tiles of a segment, from the call's sizes alone (the sequences' lengths are on the device). Cutting costs
 // K and V read once more, what a CTA takes to begin (the time of four tiles) and the join; not cutting
 // leaves SMs idle. One sequence: the count of segments whose waves of CTAs take least, in times of a
-// tile (64K tokens of 32 heads: 9 segments 602 us, 40 segments 680). Several, of whatever lengths: longer segments cost
-// balance, shorter ones beginnings; the sum is least at the square root.
+// tile (64K tokens of 32 heads: 19 segments 636 us, 40 segments 716). Several, of whatever lengths: longer segments cost
+// balance, shorter ones beginnings; the sum is least at the square root (20K tokens in two sequences, 8
+// heads: 71 us with 23 tiles, 82 with 16, 116 with 48). Where sequences and heads are two waves by
+// themselves, most sequences stay whole (20K tokens in 12 sequences, 32 heads: 217 us with 23 tiles, 194 with 64).
 inline int segment_tiles(int64_t n_tok, int32_t n_seq, int32_t n_heads) {
     constexpr int kSMs = 152;
     const int64_t tiles = (n_tok + C - 1) / C;
     if (tiles <= 8) return 8;
-    if (n_seq > 1) return std::max(8, (int)std::ceil(std::sqrt(8.0 * (double)tiles * n_heads / kSMs)));
+    if (n_seq > 1) {
+        const double m = std::sqrt(8.0 * (double)tiles * n_heads / kSMs), whole = 2.5 * (double)tiles / n_seq;
+        return std::max(8, (int)std::ceil((int64_t)n_seq * n_heads >= 2 * kSMs ? std::max(m, whole) : m));
+    }
     struct Last { int64_t tiles; int32_t heads; int best; };
     thread_local Last last{0, 0, 0};
     if (last.tiles == tiles && last.heads == n_heads) return last.best;
