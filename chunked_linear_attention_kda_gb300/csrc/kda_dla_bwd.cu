@@ -114,10 +114,10 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
             const uint32_t at = (uint32_t)s * (L::kStage / 16);
             if (leader) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 2; i >= 0; --i)  // the smallest first
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
-                        ptx::umma_ts(tmem + (n & 1) * 128, tmem + 256 + i * 32 + 8 * k, k0 + (at + 128 * k), id, i + k > 0);
+                        ptx::umma_ts(tmem + (n & 1) * 128, tmem + 256 + i * 32 + 8 * k, k0 + (at + 128 * k), id, i < 2 || k > 0);
                 ptx::umma_commit(bar(L::DsFull + (n & 1)));
                 ptx::umma_commit(bar(L::VpEmpty));
                 ptx::umma_commit(bar(L::Empty + s));
@@ -202,7 +202,7 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
             ptx::tc_fence_after();
             const TileGates *g = reinterpret_cast<const TileGates *>(smem + s * L::kStage + L::Gate);
             if (32 * (warp & 3) < p.d_v)  // other lanes' rows are not read
-                scale_values(base + s * L::kStage + L::V, tmem, 256, REV ? g->gam : g->del, 1.f);
+                scale_values<3>(base + s * L::kStage + L::V, tmem, 256, REV ? g->gam : g->del, 1.f);
             ptx::tc_fence_before();
             warp_arrive(bar(L::VpFull));
             warp_arrive(bar(L::Empty + s));
@@ -250,13 +250,13 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
             ptx::tc_fence_after();
             if (32 * (warp & 3) < p.d_v)
 #pragma unroll
-            for (int i = 0; i < NC; i += 16) {
-                float d[16];
-                ptx::tmem_ld16(lanes + (n & 1) * 128 + part * NC + i, reinterpret_cast<uint32_t *>(d));
-                ptx::tmem_ld_wait();
+                for (int i = 0; i < NC; i += 16) {
+                    float d[16];
+                    ptx::tmem_ld16(lanes + (n & 1) * 128 + part * NC + i, reinterpret_cast<uint32_t *>(d));
+                    ptx::tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) st[i + j] = fmaf(whole, st[i + j], d[j]);
-            }
+                    for (int j = 0; j < 16; ++j) st[i + j] = fmaf(whole, st[i + j], d[j]);
+                }
             ptx::tc_fence_before();
             warp_arrive(bar(L::DsEmpty + (n & 1)));
         }
@@ -474,10 +474,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             wait(L::X0Full, i);
             if (leader) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 1; h >= 0; --h)  // the small plane first
 #pragma unroll
                     for (int n = 0; n < DV / 16; ++n)
-                        ptx::umma_ss(tmem + T3, o + step(n), xc + (uint32_t)(h * L::kPlane / 16 + 128 * n), id_k, h + n > 0);
+                        ptx::umma_ss(tmem + T3, o + step(n), xc + (uint32_t)(h * L::kPlane / 16 + 128 * n), id_k, h == 0 || n > 0);
                 ptx::umma_commit(bar(L::F2));
                 ptx::umma_commit(bar(L::X0Empty));
             }
@@ -498,15 +498,15 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             ptx::tc_fence_after();
             if (leader) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 1; h >= 0; --h)  // the small plane first
 #pragma unroll
                     for (int n = 0; n < DK / 16; ++n)
-                        ptx::umma_ss(tmem + T2, k + step(n), x + (uint32_t)(h * L::kPlane / 16) + plane_step(n), id_vk, h + n > 0);
+                        ptx::umma_ss(tmem + T2, k + step(n), x + (uint32_t)(h * L::kPlane / 16) + plane_step(n), id_vk, h == 0 || n > 0);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int h = 1; h >= 0; --h)  // the small plane first
 #pragma unroll
                     for (int n = 0; n < DV / 16; ++n)
-                        ptx::umma_ss(tmem + T3, v + step(n), xc + (uint32_t)(h * L::kPlane / 16 + 128 * n), id_k, h + n > 0);
+                        ptx::umma_ss(tmem + T3, v + step(n), xc + (uint32_t)(h * L::kPlane / 16 + 128 * n), id_k, h == 0 || n > 0);
                 ptx::umma_commit(bar(L::F4));
                 ptx::umma_commit(bar(L::X1Empty));
             }

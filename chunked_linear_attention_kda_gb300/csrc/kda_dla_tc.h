@@ -3,7 +3,7 @@
 //
 // A tile is 64 tokens of one head in column halves of 64 channels, each 64 rows of 128 bytes in the
 // 128-byte swizzle of tensor copies, which tcgen05 reads K-major or MN-major as it stands. Operands
-// that are not bf16 inputs are sums of two bf16 planes (2^-18 of relative rounding).
+// that are not bf16 inputs are sums of two bf16 planes (within 2^-16 of the value).
 #pragma once
 
 #include <cuda.h>
@@ -216,42 +216,52 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-// A tile's values times their tokens' factors, V'^T, as two planes in tensor memory (columns `to` .. + 31
-// and + 32 .. + 63, two tokens a column): hi = v f, lo the rest of the product and v times the factor's
-// second plane; v f has 16 bits, so that its rest beside hi is exact. By one warp of each quarter of the
-// lanes, 32 value channels. As an A operand there it costs shared memory, which bounds these kernels, one
-// read of the tile; as planes in shared memory for either operand a read, two writes and two more reads.
+// A tile's values times their tokens' factors, V'^T, as NP planes in tensor memory (columns `to` + 32 i .. + 31,
+// two tokens a column): v times the factor's first plane has 16 bits, so that its rest beside hi is exact;
+// every further plane takes what is left and v times the factor's next plane. Two are within 2^-15 of
+// the product, three within 2^-23. By one warp of each quarter of the lanes, 32 value channels. As an A
+// operand there it costs shared memory, which bounds these kernels, one read of the tile; as planes in
+// shared memory for either operand a read, a write a plane and a read each.
+template <int NP>
 __device__ __forceinline__ void scale_values(uint32_t tile, uint32_t tmem, uint32_t to, const float *factor, float more) {
     const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
     const uint32_t col = (lane >> 3 & 1) * 8;  // matrices 0, 1: channels 0..7 and 8..15 of eight tokens; 2, 3: of the next eight
+    constexpr uint32_t minus = 0x80008000u;
 #pragma unroll 1
     for (int t0 = 0; t0 < C; t0 += 32) {
-        uint32_t fh[4], fl[4];  // of the tokens t0 + 8 n + 2 (lane % 4) and the next
+        uint32_t f[NP][4];  // of the tokens t0 + 8 n + 2 (lane % 4) and the next
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            const float2 f = *reinterpret_cast<const float2 *>(factor + t0 + 8 * n + 2 * (lane & 3));
-            const float x = more * f.x, y = more * f.y;
-            fh[n] = ptx::pack_bf16(x, y);
-            fl[n] = ptx::pack_bf16(x - gdr::lo_f(fh[n]), y - gdr::hi_f(fh[n]));
+            const float2 y = *reinterpret_cast<const float2 *>(factor + t0 + 8 * n + 2 * (lane & 3));
+            float a = more * y.x, b = more * y.y;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                f[i][n] = ptx::pack_bf16(a, b);
+                a -= gdr::lo_f(f[i][n]);
+                b -= gdr::hi_f(f[i][n]);
+            }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int dv = 32 * q + 16 * h + col;
-            uint32_t hi[8], lo[8];
+            uint32_t x[NP][8];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int tok = t0 + 16 * n + (lane >> 4) * 8 + (lane & 7);
-                ptx::ldsm_x4_t(tile + gdr::key_off(tok, dv), hi[4 * n], hi[4 * n + 1], hi[4 * n + 2], hi[4 * n + 3]);
+                ptx::ldsm_x4_t(tile + gdr::key_off(tok, dv), x[0][4 * n], x[0][4 * n + 1], x[0][4 * n + 2], x[0][4 * n + 3]);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t v = hi[i];
-                hi[i] = mul_bf16x2(v, fh[i >> 1]);
-                lo[i] = fma_bf16x2(v, fl[i >> 1], fma_bf16x2(v, fh[i >> 1], hi[i] ^ 0x80008000u));
+                const uint32_t v = x[0][i];
+                x[0][i] = mul_bf16x2(v, f[0][i >> 1]);
+                const uint32_t rest = fma_bf16x2(v, f[0][i >> 1], x[0][i] ^ minus);  // exact
+                x[1][i] = fma_bf16x2(v, f[1][i >> 1], rest);
+                if constexpr (NP == 3)  // rest - x[1], exact, + v f[1], + v f[2]
+                    x[2][i] = fma_bf16x2(v, f[2][i >> 1], fma_bf16x2(v, f[1][i >> 1], fma_bf16x2(0x3f803f80u, rest, x[1][i] ^ minus)));
             }
             const uint32_t at = tmem + ((uint32_t)(32 * q + 16 * h) << 16) + to + t0 / 2;
-            ptx::tmem_st_half4(at, hi);
-            ptx::tmem_st_half4(at + 32, lo);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) ptx::tmem_st_half4(at + 32 * i, x[i]);
         }
     }
     ptx::tmem_st_wait();

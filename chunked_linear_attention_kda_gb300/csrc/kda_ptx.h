@@ -43,15 +43,6 @@ __device__ __forceinline__ bool mbar_try(uint32_t a, uint32_t parity) {
         : "=r"(ok) : "r"(a), "r"(parity) : "memory");
     return ok != 0;
 }
-// the same, asleep for up to `ns` nanoseconds rather than the hardware's own time before it answers no
-__device__ __forceinline__ bool mbar_try_for(uint32_t a, uint32_t parity, uint32_t ns) {
-    uint32_t ok;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; "
-        "selp.u32 %0, 1, 0, p; }"
-        : "=r"(ok) : "r"(a), "r"(parity), "r"(ns) : "memory");
-    return ok != 0;
-}
 __device__ __forceinline__ bool mbar_try_cluster(uint32_t a, uint32_t parity) {
     uint32_t ok;
     asm volatile(
