@@ -886,6 +886,7 @@ __global__ void __launch_bounds__(256) dla_shared_heads_kernel(const float *dq, 
     const int64_t row = i / (DK / 8);  // token and key head
     const int c = (int)(i % (DK / 8)) * 8;
     if (row >= 2 * rows || c >= p.d_k) return;
+    if ((row >= rows ? row - rows : row) / p.n_k_heads >= p.cu_seqlens[p.n_seq]) return;  // behind the last sequence
     const bool second = row >= rows;
     const float *from = (second ? dk : dq) + (second ? row - rows : row) * group * DK + c;
     float x[8];

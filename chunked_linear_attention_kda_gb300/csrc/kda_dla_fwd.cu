@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const Segment sg = find_segment(p.cu_seqlens, p.n_seq, slot, plan.seg);
     const int64_t state_at = ((int64_t)sg.seq * p.n_heads + head) * p.d_k * p.d_v;
     if (sg.len == 0) {
+        gdr::wait_for_previous_kernel();  // whoever waits for this kernel waits for that one
         if (sg.last && p.h_final)  // an empty sequence
             for (int i = tid; i < p.d_k * p.d_v; i += kFwdThreads) p.h_final[state_at + i] = p.h0 ? p.h0[state_at + i] : 0.f;
         return;

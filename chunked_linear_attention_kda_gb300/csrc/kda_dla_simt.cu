@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads) dla_simt_grad_kernel(const DlaArgs p
 __global__ void __launch_bounds__(kThreads) dla_simt_shared_heads_kernel(const DlaArgs p) {
     gdr::wait_for_previous_kernel();
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, group = p.n_heads / p.n_k_heads;
-    if (i >= p.n_tok * p.n_k_heads * p.d_k) return;
+    if (i >= (int64_t)p.cu_seqlens[p.n_seq] * p.n_k_heads * p.d_k) return;
     const Space at = space_of(p, true);
     const float *from = static_cast<const float *>(p.workspace) + (blockIdx.y ? at.dk : at.dq) + i / p.d_k * group * p.d_k + i % p.d_k;
     float x = 0.f;

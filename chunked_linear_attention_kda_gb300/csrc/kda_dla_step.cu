@@ -58,6 +58,11 @@ __global__ void __launch_bounds__(kThreads) dla_step_kernel(const DlaStepArgs p,
             }
         }
     const float decay = expf(p.g[b * p.g_stride + head]);
+    if (decay == 0.f)  // what is forgotten may be anything: a NaN that the slot's last owner left
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int x = 0; x < VEC; ++x) s[i][x] = 0.f;
     float v[VEC], o[VEC];
 #pragma unroll
     for (int x = 0; x < VEC; ++x) {

@@ -184,7 +184,8 @@ __device__ __forceinline__ float exp2_fixed(int64_t x) {
     const float2 y = from_fixed(x);
     return ex2(y.x) * ex2(y.y);
 }
-// a tile's gates by one warp, two tokens a lane; tokens past the end have g = 0
+// A tile's gates by one warp, two tokens a lane; tokens past the end have g = 0. A g that is NaN, or past what
+// the sums hold (whose decay is infinite), makes all of them NaN: as a fixed point number it would pass for a 0.
 __device__ __forceinline__ void form_gates(float2 g, float scale, TileGates *out) {
     const int lane = threadIdx.x & 31;
     const int64_t first = fixed_exponent(g.x), both = first + fixed_exponent(g.y);
@@ -196,13 +197,17 @@ __device__ __forceinline__ void form_gates(float2 g, float scale, TileGates *out
     }
     const int64_t total = __shfl_sync(0xffffffffu, run, 31);
     const int64_t before = run - both + first;
-    const float2 a = from_fixed(before), b = from_fixed(run);
+    const float bad = __any_sync(0xffffffffu, !(g.x <= 1e6f && g.y <= 1e6f)) ? __int_as_float(0x7fffffff) : 0.f;
+    float2 a = from_fixed(before), b = from_fixed(run);
+    a.x += bad;
+    b.x += bad;
     reinterpret_cast<float4 *>(out->G)[lane] = make_float4(a.x, a.y, b.x, b.y);
     reinterpret_cast<float2 *>(out->gam)[lane] = make_float2(scale * ex2(a.x) * ex2(a.y), scale * ex2(b.x) * ex2(b.y));
-    reinterpret_cast<float2 *>(out->del)[lane] = make_float2(exp2_fixed(total - before), exp2_fixed(total - run));
+    reinterpret_cast<float2 *>(out->del)[lane] = make_float2(exp2_fixed(total - before) + bad, exp2_fixed(total - run) + bad);
     if (lane == 0) {
-        out->whole = exp2_fixed(total);
-        out->sum = from_fixed(total);
+        out->whole = exp2_fixed(total) + bad;
+        const float2 sum = from_fixed(total);
+        out->sum = make_float2(sum.x + bad, sum.y);
     }
 }
 

@@ -649,11 +649,14 @@ kda_status kda_gated_norm_bwd(const void *dy, int64_t dy_stride, const void *x,
  * most 65535. Inputs are aligned to their element size; 16-byte aligned rows are read faster.
  * State, sums and the gradient of g are fp32; with KDA_BF16 the products of the chunked calls run on
  * the tensor cores with every operand that is not itself a bf16 input carried in two bf16 parts
- * (about 2^-17 of relative rounding), with KDA_F32 they are fp32 FMAs. Results are
+ * (within 2^-16 of its value; h_final, dg and dh0 are within some 5e-6 of their norms), with KDA_F32
+ * they are fp32 FMAs. Results are
  * deterministic: the same call gives the same bits; long sequences are cut into segments by the
  * call's sizes, so that packing a sequence with others may change its results' last bits. A NaN or an
  * infinity stays in its sequence, but in the chunked calls it reaches every token of its own
- * chunk, the earlier ones too, and all later ones. Asynchronous on `stream`; nothing is allocated.
+ * chunk, the earlier ones too, and all later ones. A call may hold more tokens than cu_seqlens[n_seq]
+ * (a captured call of fewer tokens than its buffers have): those behind it change nothing, and
+ * their rows of the results are left as they were. Asynchronous on `stream`; nothing is allocated.
  *
  * kda_dla_chunk_fwd -- the forward pass over packed sequences. workspace: device memory, 16-byte
  * aligned, kda_dla_chunk_fwd_workspace_bytes() bytes (0 for invalid sizes), caller-owned, contents
@@ -671,7 +674,8 @@ kda_status kda_gated_norm_bwd(const void *dy, int64_t dy_stride, const void *x,
  * kda_dla_step -- one token for each of n_rows sequences, in place on a pool of states, as
  * kda_gdr_step: row b reads and rewrites state[slots[b]] (slots NULL: state b); a slot outside
  * [0, n_slots) marks a padded row: its out is 0 and no state is touched. Two rows of a call may
- * not share a slot. g [n_rows, n_heads] (g_stride = n_heads) or [n_heads] (g_stride = 0).
+ * not share a slot. g [n_rows, n_heads] (g_stride = n_heads) or [n_heads] (g_stride = 0); a decay of
+ * 0 forgets whatever the state held, a NaN too.
  */
 size_t kda_dla_chunk_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_k_heads,
                                          int32_t n_heads, int32_t d_k, int32_t d_v,

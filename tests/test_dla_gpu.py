@@ -281,6 +281,57 @@ def test_a_nan_stays_in_its_sequence(dtype):
 
 
 @pytest.mark.parametrize("dtype", [FP, BF])
+def test_a_decay_that_is_nan_shows(dtype):
+    """It reaches the tokens from its own on, of its head and sequence alone."""
+    x = Inputs([100, 230, 40], 2, 2, 128, 128, dtype, seed=25)
+    ref, grads = forward(x), backward(x)
+    x.g[150, 1] = float("nan")
+    out, end = forward(x)
+    got = backward(x)
+    assert bool(torch.isnan(out[150:330, 1]).all()) and bool(torch.isnan(end[1, 1]).all())
+    assert bool(torch.isnan(got[0][150:330, 1]).all()) and bool(torch.isnan(got[4][1, 1]).all())
+    for a, b in [(out, ref[0])] + list(zip(got[:4], grads[:4])):
+        assert torch.equal(a[:, 0], b[:, 0]) and torch.equal(a[:100], b[:100]) and torch.equal(a[330:], b[330:])
+    for a, b in ((end, ref[1]), (got[4], grads[4])):
+        assert torch.equal(a[[0, 2]], b[[0, 2]]) and torch.equal(a[1, 0], b[1, 0])
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("hk", [4, 1])
+def test_tokens_behind_the_last_sequence(hk, dtype, per_head):
+    """Buffers with more tokens than the sequences: those change nothing, their results are not written."""
+    lengths, n, more = [130, 0, 77], 207, 93
+    x = Inputs(lengths, hk, 4, 128, 64, dtype, seed=26, per_head=per_head)
+    y = Inputs([n + more], hk, 4, 128, 64, dtype, seed=27, per_head=per_head)
+    for name in ("q", "k", "v", "dout") + (() if per_head else ("g",)):
+        getattr(y, name)[:n] = getattr(x, name)
+        getattr(y, name)[n:] = float("nan")
+    g = x.g if per_head else y.g
+    lib, stream = kda.load_library(), torch.cuda.current_stream().cuda_stream
+    sizes = (n + more, 3, hk, 4, 128, 64, {FP: 0, BF: 1}[dtype])
+    ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device=DEV)
+    ins = (y.q.data_ptr(), y.k.data_ptr(), y.v.data_ptr(), hk * 128, hk * 128, 256, g.data_ptr(), 0 if per_head else 4,
+           x.h0.data_ptr(), x.cu.data_ptr(), 128 ** -0.5)
+    for t in (y.q, y.k, y.v):
+        assert t.is_contiguous()
+    out, end = torch.full_like(y.v, 7.0), torch.empty_like(x.h0)
+    assert lib.kda_dla_chunk_fwd(*ins, out.data_ptr(), end.data_ptr(), ws.data_ptr(), ws.numel(), *sizes, stream) == 0
+    ref = forward(x)  # the same chunks in the same order: the same bits
+    assert torch.equal(out[:n], ref[0]) and torch.equal(end, ref[1]) and bool((out[n:] == 7).all())
+    dq, dk, dv = torch.full_like(y.q, 7.0), torch.full_like(y.k, 7.0), torch.full_like(y.v, 7.0)
+    dg, dh0 = torch.full_like(g, 7.0), torch.empty_like(x.h0)
+    assert lib.kda_dla_chunk_bwd(*ins, y.dout.data_ptr(), x.dhf.data_ptr(), *[t.data_ptr() for t in (dq, dk, dv, dg, dh0)],
+                                 ws.data_ptr(), ws.numel(), *sizes, stream) == 0
+    grads = backward(x)
+    for a, b in zip((dq, dk, dv, dg, dh0), grads):
+        if a.shape[0] == n + more:
+            assert bool((a[n:] == 7).all())
+            a = a[:n]
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [FP, BF])
 def test_no_token(dtype):
     x = Inputs([0, 0], 2, 2, 64, 64, dtype, seed=14)
     out, end = forward(x)
@@ -424,6 +475,7 @@ def test_step_reset_forgets():
     x = Inputs([1] * 2, 1, 2, 64, 64, FP, seed=22)
     x.g[0] = -INF
     pool = torch.randn(2, 2, 64, 64, device=DEV)
+    pool[0, 0, 3] = float("nan")
     kda.dla_step(x.q, x.k, x.v, x.g, pool)
     for h in range(2):
         assert torch.equal(pool[0, h], x.k[0, 0][:, None] * x.v[0, h][None])
