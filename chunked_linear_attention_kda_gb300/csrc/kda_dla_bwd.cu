@@ -60,8 +60,9 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
     auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };  // equal over a warp, and told so
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int head = unit % p.n_heads, kh = head / (p.n_heads / p.n_k_heads);
-    const int64_t slot = unit / p.n_heads;
-    const Segment sg = find_segment(p.cu_seqlens, p.n_seq, slot, plan.seg);
+    const Ordered mine = jth_longest(p.cu_seqlens, p.n_seq, unit / p.n_heads, plan.slots, plan.seg, smem);
+    const int64_t slot = mine.slot;
+    const Segment sg = mine.sg;
     const int64_t state_at = ((int64_t)sg.seq * p.n_heads + head) * p.d_k * p.d_v;
     if (sg.len == 0) {
         if (REV && sg.last && p.dh0)  // an empty sequence
@@ -267,16 +268,16 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
     if (warp == 0) ptx::tmem_dealloc(tmem, 512);
 }
 
-// the first half of the blocks walks in reverse, the second forward
+// every segment in reverse and forward, side by side
 template <int DK, int DV>
 __global__ void __launch_bounds__(kWalkThreads, 1)
     dla_states_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const DlaArgs p,
                       const BwdPlan bp, bool copies) {
     gdr::let_next_kernel_start();
-    const unsigned n = gridDim.x / 2;
-    if (blockIdx.x < n) state_walk<DK, DV, true>(tm_q, tm_o, p, bp, copies, blockIdx.x);
-    else state_walk<DK, DV, false>(tm_k, tm_v, p, bp, copies, blockIdx.x - n);
+    const unsigned pair = blockIdx.x / (2 * p.n_heads), head = blockIdx.x % p.n_heads, unit = pair * p.n_heads + head;
+    if (blockIdx.x / p.n_heads % 2 == 0) state_walk<DK, DV, true>(tm_q, tm_o, p, bp, copies, unit);
+    else state_walk<DK, DV, false>(tm_k, tm_v, p, bp, copies, unit);
 }
 
 // ---------------------------------------------------------------- gradients

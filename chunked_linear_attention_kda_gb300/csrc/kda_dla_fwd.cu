@@ -73,8 +73,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     const int head = blockIdx.x % p.n_heads, kh = head / (p.n_heads / p.n_k_heads);
-    const int64_t slot = blockIdx.x / p.n_heads;
-    const Segment sg = find_segment(p.cu_seqlens, p.n_seq, slot, plan.seg);
+    const Ordered unit = jth_longest(p.cu_seqlens, p.n_seq, blockIdx.x / p.n_heads, plan.slots, plan.seg, smem);
+    const int64_t slot = unit.slot;
+    const Segment sg = unit.sg;
     const int64_t state_at = ((int64_t)sg.seq * p.n_heads + head) * p.d_k * p.d_v;
     if (sg.len == 0) {
         gdr::wait_for_previous_kernel();  // whoever waits for this kernel waits for that one
@@ -492,7 +493,7 @@ cudaError_t forward(const DlaArgs &p, cudaStream_t stream) {
     const bool wide = p.d_v % 8 == 0 && (uintptr_t)p.out % 16 == 0;
     const Plan plan = make_plan(p, false);
     // A short call forms the gates beside the tiles' copies: a launch less (40 tokens of 32 heads in a graph:
-    // ... us, ... with the launch), but 2 us a tile that nothing hides.
+    // 8.8 us, 10 with the launch), but 2 us a tile that nothing hides.
     const dim3 grid((unsigned)(plan.slots * p.n_heads));
     if (p.n_tok <= 4 * C && !plan.cut) {
         const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dla_forward_kernel<DK, true>), FwdSmem<DK>::kBytes);
