@@ -493,7 +493,7 @@ cudaError_t forward(const DlaArgs &p, cudaStream_t stream) {
     const bool wide = p.d_v % 8 == 0 && (uintptr_t)p.out % 16 == 0;
     const Plan plan = make_plan(p, false);
     // A short call forms the gates beside the tiles' copies: a launch less (40 tokens of 32 heads in a graph:
-    // 8.8 us, 10 with the launch), but 2 us a tile that nothing hides.
+    // 8.7 us, 9.6 with the launch), but 2 us a tile that nothing hides.
     const dim3 grid((unsigned)(plan.slots * p.n_heads));
     if (p.n_tok <= 4 * C && !plan.cut) {
         const cudaError_t e = allow_smem(reinterpret_cast<const void *>(dla_forward_kernel<DK, true>), FwdSmem<DK>::kBytes);

@@ -35,15 +35,16 @@ struct Plan {
 // K and V read once more, what a CTA takes to begin (the time of four tiles) and the join; not cutting
 // leaves SMs idle. One sequence: the count of segments whose waves of CTAs take least, in times of a
 // tile (64K tokens of 32 heads: 19 segments 636 us, 40 segments 716). Several, of whatever lengths: longer segments cost
-// balance, shorter ones beginnings; the sum is least at the square root (20K tokens in two sequences, 8
-// heads: 71 us with 23 tiles, 82 with 16, 116 with 48). Where sequences and heads are two waves by
-// themselves, most sequences stay whole (20K tokens in 12 sequences, 32 heads: 217 us with 23 tiles, 194 with 64).
+// balance, shorter ones beginnings; the sum is least near a square root (20K tokens in two sequences, 8
+// heads: 90 us with 12 tiles, 69 with 17, 90 with 30; 60K in four, 32 heads: 569 us with 57 tiles, 524 with
+// 69, 606 with 85). Where sequences and heads are two waves by themselves, most sequences stay whole (20K
+// tokens in 12 sequences, 32 heads: 198 us with 53 tiles, 166 with 66).
 inline int segment_tiles(int64_t n_tok, int32_t n_seq, int32_t n_heads) {
     constexpr int kSMs = 152;
     const int64_t tiles = (n_tok + C - 1) / C;
     if (tiles <= 8) return 8;
     if (n_seq > 1) {
-        const double m = std::sqrt(8.0 * (double)tiles * n_heads / kSMs), whole = 2.5 * (double)tiles / n_seq;
+        const double m = std::sqrt(16.0 * (double)tiles * n_heads / kSMs), whole = 2.5 * (double)tiles / n_seq;
         return std::max(8, (int)std::ceil((int64_t)n_seq * n_heads >= 2 * kSMs ? std::max(m, whole) : m));
     }
     struct Last { int64_t tiles; int32_t heads; int best; };
