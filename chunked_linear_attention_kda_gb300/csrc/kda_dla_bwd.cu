@@ -310,9 +310,9 @@ struct GradSmem {
     static constexpr int kKey = DK / 64 * kWide, kVal = DV / 64 * kWide, kPlane = plane_bytes(DK, DV);
     static constexpr int Q = 0, K = kKey, V = 2 * kKey, dO = V + kVal, X = dO + kVal, Gate = X + 2 * kPlane;
     static constexpr int Sums = Gate + 2 * (int)sizeof(BlockGates), Bars = Sums + (int)sizeof(BlockSums);
-    static constexpr int KqFull = 0, VoFull = 1, TilesEmpty = 2, X0Full = 3, X1Full = 4, X0Empty = 5, X1Empty = 6, F1 = 7, F2 = 8,
+    static constexpr int KqFull = 0, VoFull = 1, KvEmpty = 2, X0Full = 3, X1Full = 4, X0Empty = 5, X1Empty = 6, F1 = 7, F2 = 8,
                          WFull = 9, F3 = 10, AEmpty = 11, F4 = 12, PFull = 13, Scaled = 14, F5 = 15, CEmpty = 16, GFull = 17,
-                         GEmpty = 19, SumsFull = 21, SumsEmpty = 22, Drain = 23, Partial = 24, kBars = 26;
+                         GEmpty = 19, SumsFull = 21, SumsEmpty = 22, Drain = 23, Partial = 24, QoEmpty = 26, kBars = 28;
     static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;  // the base is rounded up to 1024
     static_assert(sizeof(BlockGates) % 16 == 0 && sizeof(BlockSums) % 16 == 0 && kBytes <= 227 * 1024, "fits an SM");
 };
@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         for (int i : ones) ptx::mbar_init(bar(i), 1);
         const int eights[] = {L::WFull, L::AEmpty, L::PFull, L::Scaled, L::CEmpty};
         for (int i : eights) ptx::mbar_init(bar(i), 8);
-        ptx::mbar_init(bar(L::TilesEmpty), 1 + 16);  // the products, the rows' warps
+        ptx::mbar_init(bar(L::KvEmpty), 1 + 8);  // the products, the rows' warps that read it
+        ptx::mbar_init(bar(L::QoEmpty), 1 + 8);
         ptx::mbar_init(bar(L::X1Empty), 1 + 4);
         ptx::mbar_init(bar(L::GEmpty), 16 + (p.dg ? 1 : 0));
         ptx::mbar_init(bar(L::GEmpty + 1), 16 + (p.dg ? 1 : 0));
@@ -494,8 +495,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 ptx::umma_commit(bar(L::F3));
             }
             __syncwarp();
-            wait(L::AEmpty, i);
             wait(L::X1Full, i);
+            wait(L::F3, i);  // W is read; dQ leaves tensor memory beside the next product
             ptx::tc_fence_after();
             if (leader) {
 #pragma unroll
@@ -503,6 +504,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 #pragma unroll
                     for (int n = 0; n < DK / 16; ++n)
                         ptx::umma_ss(tmem + T2, k + step(n), x + (uint32_t)(h * L::kPlane / 16) + plane_step(n), id_vk, h == 0 || n > 0);
+            }
+            __syncwarp();
+            wait(L::AEmpty, i);
+            ptx::tc_fence_after();
+            if (leader) {
 #pragma unroll
                 for (int h = 1; h >= 0; --h)  // the small plane first
 #pragma unroll
@@ -510,6 +516,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                         ptx::umma_ss(tmem + T3, v + step(n), xc + (uint32_t)(h * L::kPlane / 16 + 128 * n), id_k, h == 0 || n > 0);
                 ptx::umma_commit(bar(L::F4));
                 ptx::umma_commit(bar(L::X1Empty));
+                ptx::umma_commit(bar(L::KvEmpty));
             }
             __syncwarp();
             wait(L::PFull, i);
@@ -527,7 +534,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                     for (int n = 0; n < kBlock / 16; ++n)
                         ptx::umma_ts(tmem + T3, tmem + T1 + 16 * n + 8 * h, qc + (uint32_t)(128 * n), id_k, 1);
                 ptx::umma_commit(bar(L::F5));
-                ptx::umma_commit(bar(L::TilesEmpty));
+                ptx::umma_commit(bar(L::QoEmpty));
             }
             __syncwarp();
         }
@@ -538,48 +545,58 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         ptx::regs_decrease<kGradServe>();
         int partials = 0;
         for (int64_t u = blockIdx.x; next_unit(u, b); u += gridDim.x, ++i) {
-            if (i > 0) wait(L::TilesEmpty, i - 1);
+            if (i > 0) wait(L::KvEmpty, i - 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
+            // Keys and values are free two products before queries and dO: half of the next unit's copies begin
+            // then (two sequences of 8K tokens, 32 heads: 573 us with all of them at the end, 545 so). The copies are
+            // written out: from an array of their sources, walked by a loop, they began 2 us a unit later.
             const int kh = b.head / group;
-            const int64_t ov = (int64_t)p.n_heads * p.d_v;
-            const Source in[4] = {{&tm_k, static_cast<const __nv_bfloat16 *>(p.k), p.k_stride, kh, p.d_k, DK / 64, bp.walk.vec_k},
-                                  {&tm_q, static_cast<const __nv_bfloat16 *>(p.q), p.q_stride, kh, p.d_k, DK / 64, bp.walk.vec_q},
-                                  {&tm_v, static_cast<const __nv_bfloat16 *>(p.v), p.v_stride, b.head, p.d_v, DV / 64, bp.walk.vec_v},
-                                  {&tm_o, static_cast<const __nv_bfloat16 *>(p.dout), ov, b.head, p.d_v, DV / 64, bp.walk.vec_o}};
-            const int to[4] = {L::K, L::Q, L::V, L::dO};
+            const bool whole = b.len == kBlock;
+            auto copy = [&](const CUtensorMap &map, int to, int halves, int head, uint32_t m) {
+                for (int h = 0; h < halves; ++h) ptx::tma_load_3d(base + to + h * kWide, &map, h * 64, head, (int)b.t0, m);
+            };
             if (copies) {
                 // a partial block is copied whole; what is another sequence's goes before it is handed over
-                const bool whole = b.len == kBlock;
+                const uint32_t kq = bar(whole ? L::KqFull : L::Partial), vo = bar(whole ? L::VoFull : L::Partial + 1);
                 if (lane == 0) {
-#pragma unroll 1
-                    for (int n = 0; n < 4; ++n) {
-                        const uint32_t m = bar(whole ? (n < 2 ? L::KqFull : L::VoFull) : n < 2 ? L::Partial : L::Partial + 1);
-                        if ((n & 1) == 0) ptx::mbar_arrive_tx(m, n < 2 ? 2 * L::kKey : 2 * L::kVal);
-                        for (int h = 0; h < in[n].halves; ++h)
-                            ptx::tma_load_3d(base + to[n] + h * kWide, in[n].map, h * 64, in[n].head, (int)b.t0, m);
-                    }
+                    ptx::mbar_arrive_tx(kq, 2 * L::kKey);
+                    copy(tm_k, L::K, DK / 64, kh, kq);
+                    ptx::mbar_arrive_tx(vo, 2 * L::kVal);
+                    copy(tm_v, L::V, DV / 64, b.head, vo);
+                }
+                if (i > 0) wait(L::QoEmpty, i - 1);  // given up: the copies come all the same, to be waited for
+                if (lane == 0) {
+                    copy(tm_q, L::Q, DK / 64, kh, kq);
+                    copy(tm_o, L::dO, DV / 64, b.head, vo);
                 }
                 if (!whole) {
-#pragma unroll 1
-                    for (int n = 0; n < 4; n += 2) {
-                        const uint32_t by = bar(L::Partial + n / 2);
-                        if (!wait_bar(by, partials & 1)) drain_bar(by, partials & 1);
-                        clear_rows(base + to[n], in[n].halves, kWide, b.len, kBlock);
-                        clear_rows(base + to[n + 1], in[n + 1].halves, kWide, b.len, kBlock);
-                        ptx::fence_proxy_async();
-                        warp_arrive(bar(n < 2 ? L::KqFull : L::VoFull));
-                    }
+                    if (!wait_bar(kq, partials & 1)) drain_bar(kq, partials & 1);
+                    clear_rows(base + L::K, DK / 64, kWide, b.len, kBlock);
+                    clear_rows(base + L::Q, DK / 64, kWide, b.len, kBlock);
+                    ptx::fence_proxy_async();
+                    warp_arrive(bar(L::KqFull));
+                    if (!wait_bar(vo, partials & 1)) drain_bar(vo, partials & 1);
+                    clear_rows(base + L::V, DV / 64, kWide, b.len, kBlock);
+                    clear_rows(base + L::dO, DV / 64, kWide, b.len, kBlock);
+                    ptx::fence_proxy_async();
+                    warp_arrive(bar(L::VoFull));
                     ++partials;
                 }
             } else {
+                const int64_t ov = (int64_t)p.n_heads * p.d_v;
+                const Source in[4] = {{&tm_k, static_cast<const __nv_bfloat16 *>(p.k), p.k_stride, kh, p.d_k, DK / 64, bp.walk.vec_k},
+                                      {&tm_v, static_cast<const __nv_bfloat16 *>(p.v), p.v_stride, b.head, p.d_v, DV / 64, bp.walk.vec_v},
+                                      {&tm_q, static_cast<const __nv_bfloat16 *>(p.q), p.q_stride, kh, p.d_k, DK / 64, bp.walk.vec_q},
+                                      {&tm_o, static_cast<const __nv_bfloat16 *>(p.dout), ov, b.head, p.d_v, DV / 64, bp.walk.vec_o}};
+                const int to[4] = {L::K, L::V, L::Q, L::dO};
+                if (i > 0) wait(L::QoEmpty, i - 1);
 #pragma unroll 1
-                for (int n = 0; n < 4; ++n) {
-                    wide_tile(in[n], base + to[n], b.t0, b.len, lane);
-                    if (n & 1) {
-                        rows_loaded();
-                        if (lane == 0) ptx::mbar_arrive(bar(n < 2 ? L::KqFull : L::VoFull));
-                    }
+                for (int n = 0; n < 4; ++n) wide_tile(in[n], base + to[n], b.t0, b.len, lane);
+                rows_loaded();
+                if (lane == 0) {
+                    ptx::mbar_arrive(bar(L::KqFull));
+                    ptx::mbar_arrive(bar(L::VoFull));
                 }
             }
         }
@@ -788,13 +805,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
+            // the part of the state: times gamma or delta, and its dot product with the row's q or k
+            const float f = keys ? g.del[x] : g.gam[x];
             if (keys) {
                 warp_arrive(bar(L::PFull));
                 wait(L::F4, i);
                 ptx::tc_fence_after();
             }
-            // the part of the state: times gamma or delta, and its dot product with the row's q or k
-            const float f = keys ? g.del[x] : g.gam[x];
             float dot = 0.f;
 #pragma unroll 1
             for (int c = part * NK; c < (part + 1) * NK; c += 16) {
@@ -832,7 +849,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             ptx::tc_fence_before();
             warp_arrive(bar(keys ? L::Scaled : L::WFull));
             warp_arrive(bar(L::GEmpty + (i & 1)));
-            warp_arrive(bar(L::TilesEmpty));
+            warp_arrive(bar(keys ? L::KvEmpty : L::QoEmpty));
             if (p.dg) {
                 if (keys) {
                     sums.b[part][x] = f * dot;

@@ -101,6 +101,7 @@ __device__ __forceinline__ Ordered jth_longest(const int32_t *cu, int n_seq, int
     }
     __syncthreads();
     const Ordered got = *out;
+    ptx::fence_proxy_async();  // tensor copies come next
     __syncthreads();
     return got;
 }
