@@ -312,7 +312,7 @@ struct GradSmem {
     static constexpr int Sums = Gate + 2 * (int)sizeof(BlockGates), Bars = Sums + (int)sizeof(BlockSums);
     static constexpr int KqFull = 0, VoFull = 1, KvEmpty = 2, X0Full = 3, X1Full = 4, X0Empty = 5, X1Empty = 6, F1 = 7, F2 = 8,
                          WFull = 9, F3 = 10, AEmpty = 11, F4 = 12, PFull = 13, Scaled = 14, F5 = 15, CEmpty = 16, GFull = 17,
-                         GEmpty = 19, SumsFull = 21, SumsEmpty = 22, Drain = 23, Partial = 24, QoEmpty = 26, kBars = 28;
+                         GEmpty = 19, SumsFull = 21, SumsEmpty = 22, Drain = 23, Partial = 24, QoEmpty = 26, F2w = 27, CvEmpty = 28, kBars = 30;
     static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;  // the base is rounded up to 1024
     static_assert(sizeof(BlockGates) % 16 == 0 && sizeof(BlockSums) % 16 == 0 && kBytes <= 227 * 1024, "fits an SM");
 };
@@ -407,10 +407,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     BlockGates *gates = reinterpret_cast<BlockGates *>(smem + L::Gate);
     BlockSums &sums = *reinterpret_cast<BlockSums *>(smem + L::Sums);
     if (tid == 0) {
-        const int ones[] = {L::KqFull, L::VoFull, L::X0Full, L::X1Full, L::X0Empty, L::F1, L::F2, L::F3, L::F4, L::F5, L::GFull,
+        const int ones[] = {L::KqFull, L::VoFull, L::X0Full, L::X1Full, L::X0Empty, L::F1, L::F2w, L::F2, L::F3, L::F4, L::F5, L::GFull,
                             L::GFull + 1, L::SumsEmpty, L::Drain, L::Partial, L::Partial + 1};
         for (int i : ones) ptx::mbar_init(bar(i), 1);
-        const int eights[] = {L::WFull, L::AEmpty, L::PFull, L::Scaled, L::CEmpty};
+        const int eights[] = {L::WFull, L::AEmpty, L::PFull, L::Scaled, L::CvEmpty, L::CEmpty};
         for (int i : eights) ptx::mbar_init(bar(i), 8);
         ptx::mbar_init(bar(L::KvEmpty), 1 + 8);  // the products, the rows' warps that read it
         ptx::mbar_init(bar(L::QoEmpty), 1 + 8);
@@ -466,14 +466,17 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 ptx::umma_commit(bar(L::F1));
             }
             __syncwarp();
-            if (i > 0) wait(L::CEmpty, i - 1);
+            if (i > 0) wait(L::CvEmpty, i - 1);
             ptx::tc_fence_after();
             if (leader) {
 #pragma unroll
                 for (int n = 0; n < DV / 16; ++n) ptx::umma_ss(tmem + T2, o + step(n), v + step(n), id_pair, n > 0);
+                ptx::umma_commit(bar(L::F2w));
             }
             __syncwarp();
             wait(L::X0Full, i);
+            if (i > 0) wait(L::CEmpty, i - 1);
+            ptx::tc_fence_after();
             if (leader) {
 #pragma unroll
                 for (int h = 1; h >= 0; --h)  // the small plane first
@@ -749,7 +752,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             wait(L::GFull + (i & 1), i >> 1);
             const BlockGates &g = gates[i & 1];
             const float2 G = g.G[x];
-            wait(keys ? L::F1 : L::F2, i);
+            wait(keys ? L::F1 : L::F2w, i);
             ptx::tc_fence_after();
             if (p.dg && i > 0) wait(L::SumsEmpty, i - 1);
             float col = 0.f;
@@ -807,11 +810,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             ptx::tc_fence_before();
             // the part of the state: times gamma or delta, and its dot product with the row's q or k
             const float f = keys ? g.del[x] : g.gam[x];
-            if (keys) {
-                warp_arrive(bar(L::PFull));
-                wait(L::F4, i);
-                ptx::tc_fence_after();
-            }
+            if (keys) warp_arrive(bar(L::PFull));
+            wait(keys ? L::F4 : L::F2, i);
+            ptx::tc_fence_after();
             float dot = 0.f;
 #pragma unroll 1
             for (int c = part * NK; c < (part + 1) * NK; c += 16) {
@@ -864,6 +865,19 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             ptx::tc_fence_after();
             const int64_t t = b.t0 + x;
             const bool in = x < b.len;
+            if (keys) {
+                __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(p.dv) + (t * p.n_heads + b.head) * p.d_v;
+#pragma unroll 1
+                for (int c = part * NV; c < (part + 1) * NV; c += 32) {
+                    float y[32];
+                    ptx::tmem_ld32(lanes + T2 + c, reinterpret_cast<uint32_t *>(y));
+                    ptx::tmem_ld_wait();
+                    if (in) store_row<32>(dv, y, c, p.d_v, wide_v);
+                }
+                // the next block's pair product goes there
+                ptx::tc_fence_before();
+                warp_arrive(bar(L::CvEmpty));
+            }
             __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(keys ? p.dk : p.dq) + (t * p.n_k_heads + b.head) * p.d_k;
             float *partial = group > 1 ? (keys ? bp.dk : bp.dq) + (t * p.n_heads + b.head) * DK : nullptr;
 #pragma unroll 1
@@ -874,16 +888,6 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 if (in) {
                     if (partial) store_part<32>(partial + c, y);
                     else store_row<32>(to, y, c, p.d_k, wide_k);
-                }
-            }
-            if (keys) {
-                __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(p.dv) + (t * p.n_heads + b.head) * p.d_v;
-#pragma unroll 1
-                for (int c = part * NV; c < (part + 1) * NV; c += 32) {
-                    float y[32];
-                    ptx::tmem_ld32(lanes + T2 + c, reinterpret_cast<uint32_t *>(y));
-                    ptx::tmem_ld_wait();
-                    if (in) store_row<32>(dv, y, c, p.d_v, wide_v);
                 }
             }
             ptx::tc_fence_before();
