@@ -44,20 +44,31 @@ __device__ __forceinline__ float2 cos_sin(uint64_t turn) {
     return cs;
 }
 
-// A group of G threads (a power of two up to 32) holds a row of d channels, eight a thread. With VEC
-// in two runs of four, which are the two channels of four pairs (in halves: from 4 t and R + 4 t on,
-// threads beyond the pairs two runs side by side; interleaved: two runs side by side), otherwise the
-// channels t + G i.
-enum Kind { kSingle, kHalves, kInterleaved };  // not VEC, VEC by the order of pairs
-struct Runs { int a, b; };
-__device__ __forceinline__ Runs runs(int t, int R, bool interleaved) {
-    if (!interleaved && 4 * t < R) return {4 * t, R + 4 * t};
-    const int c = interleaved ? 8 * t : 2 * R + 8 * (t - R / 4);
-    return {c, c + 4};
+// A group of G threads (a power of two up to 32) holds a row of d channels, eight a thread: both channels
+// of four pairs, by loads of four channels or, where the row's length, its halves or its address allow no more, of
+// two; otherwise (odd lengths) the channels t + G i, and the pairs meet in shared memory. 20000
+// tokens of 32 + 32 heads of 100 channels, backward: 1160 us by single channels, 238 by two.
+enum Kind { kSingle, kHalves, kInterleaved, kHalves2, kInterleaved2 };
+__host__ __device__ constexpr int width(Kind k) { return k == kSingle ? 1 : k == kHalves || k == kInterleaved ? 4 : 2; }
+__host__ __device__ constexpr bool interleaves(Kind k) { return k == kInterleaved || k == kInterleaved2; }
+// Where the thread's channels 0 and 1, 2 and 3, 4 and 5, 6 and 7 lie. Loads of four: pairs from 4 t on (halves: beyond
+// the pairs two runs side by side). Loads of two: the slots t and t + G of two pairs each, or of four
+// channels side by side beyond the pairs.
+struct Runs { int a, a2, b, b2; };
+template <Kind KIND>
+__device__ __forceinline__ Runs runs(int t, int R, int G) {
+    if constexpr (width(KIND) == 2) {
+        auto slot = [&](int s) { return interleaves(KIND) || 2 * s >= R ? make_int2(4 * s, 4 * s + 2) : make_int2(2 * s, R + 2 * s); };
+        const int2 x = slot(t), y = slot(t + G);
+        return {x.x, y.x, x.y, y.y};
+    } else {
+        if (KIND == kHalves && 4 * t < R) return {4 * t, 4 * t + 2, R + 4 * t, R + 4 * t + 2};
+        return {8 * t, 8 * t + 2, 8 * t + 4, 8 * t + 6};
+    }
 }
 
 // A thread's eight channels as they were loaded, so that several rows are in flight without their fp32 copies
-template <typename T, bool VEC>
+template <typename T, int W>
 struct Row {
     float x[8];
     __device__ __forceinline__ void load(const T *p, int d, int t, int G, Runs) {
@@ -74,7 +85,7 @@ struct Row {
     }
 };
 template <>
-struct Row<bf16, true> {
+struct Row<bf16, 4> {
     uint2 a, b;
     __device__ __forceinline__ void clear() { a = b = make_uint2(0, 0); }
     __device__ __forceinline__ void load(const bf16 *p, int d, int, int, Runs r) {
@@ -94,7 +105,7 @@ struct Row<bf16, true> {
     }
 };
 template <>
-struct Row<float, true> {
+struct Row<float, 4> {
     float4 a, b;
     __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void load(const float *p, int d, int, int, Runs r) {
@@ -109,12 +120,51 @@ struct Row<float, true> {
         y[4] = b.x; y[5] = b.y; y[6] = b.z; y[7] = b.w;
     }
 };
-template <bool VEC>
+template <>
+struct Row<bf16, 2> : Row<bf16, 4> {
+    __device__ __forceinline__ void load(const bf16 *p, int d, int, int, Runs r) {
+        clear();
+        if (r.a < d) {
+            a.x = *reinterpret_cast<const uint32_t *>(p + r.a);
+            b.x = *reinterpret_cast<const uint32_t *>(p + r.b);
+        }
+        if (r.a2 < d) {
+            a.y = *reinterpret_cast<const uint32_t *>(p + r.a2);
+            b.y = *reinterpret_cast<const uint32_t *>(p + r.b2);
+        }
+    }
+};
+template <>
+struct Row<float, 2> : Row<float, 4> {
+    __device__ __forceinline__ void load(const float *p, int d, int, int, Runs r) {
+        clear();
+        auto at = [&](int c) { return *reinterpret_cast<const float2 *>(p + c); };
+        if (r.a < d) {
+            const float2 x = at(r.a), y = at(r.b);
+            a.x = x.x; a.y = x.y; b.x = y.x; b.y = y.y;
+        }
+        if (r.a2 < d) {
+            const float2 x = at(r.a2), y = at(r.b2);
+            a.z = x.x; a.w = x.y; b.z = y.x; b.w = y.y;
+        }
+    }
+};
+template <int W>
 __device__ __forceinline__ void store_row(float *p, const float *x, int d, int t, int G, Runs r) {
-    if constexpr (VEC) {
+    if constexpr (W == 4) {
         if (r.a < d) {
             *reinterpret_cast<float4 *>(p + r.a) = make_float4(x[0], x[1], x[2], x[3]);
             *reinterpret_cast<float4 *>(p + r.b) = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    } else if constexpr (W == 2) {
+        auto put = [&](int c, float lo, float hi) { *reinterpret_cast<float2 *>(p + c) = make_float2(lo, hi); };
+        if (r.a < d) {
+            put(r.a, x[0], x[1]);
+            put(r.b, x[4], x[5]);
+        }
+        if (r.a2 < d) {
+            put(r.a2, x[2], x[3]);
+            put(r.b2, x[6], x[7]);
         }
     } else {
 #pragma unroll
@@ -122,12 +172,22 @@ __device__ __forceinline__ void store_row(float *p, const float *x, int d, int t
             if (t + G * i < d) p[t + G * i] = x[i];
     }
 }
-template <bool VEC>
+template <int W>
 __device__ __forceinline__ void store_row(bf16 *p, const float *x, int d, int t, int G, Runs r) {
-    if constexpr (VEC) {
+    if constexpr (W == 4) {
         if (r.a < d) {
             *reinterpret_cast<uint2 *>(p + r.a) = make_uint2(ptx::pack_bf16(x[0], x[1]), ptx::pack_bf16(x[2], x[3]));
             *reinterpret_cast<uint2 *>(p + r.b) = make_uint2(ptx::pack_bf16(x[4], x[5]), ptx::pack_bf16(x[6], x[7]));
+        }
+    } else if constexpr (W == 2) {
+        auto put = [&](int c, float lo, float hi) { *reinterpret_cast<uint32_t *>(p + c) = ptx::pack_bf16(lo, hi); };
+        if (r.a < d) {
+            put(r.a, x[0], x[1]);
+            put(r.b, x[4], x[5]);
+        }
+        if (r.a2 < d) {
+            put(r.a2, x[2], x[3]);
+            put(r.b2, x[6], x[7]);
         }
     } else {
 #pragma unroll
@@ -140,14 +200,14 @@ __device__ __forceinline__ float group_sum(float x, int G) {
     return x;
 }
 
-// The row x turned by its token's angles, cs the (cos, sin) of this thread's four pairs (VEC) or of each of its
-// eight channels' pairs; sign = -1: back. stage: 2 R floats of this group (not VEC). The whole warp calls it.
+// The row x turned by its token's angles, cs the (cos, sin) of this thread's four pairs or, by single channels, of each of its
+// eight channels' pairs; sign = -1: back. stage: 2 R floats of this group (single channels). The whole warp calls it.
 template <Kind KIND>
 __device__ __forceinline__ void turn(float *x, const float2 *cs, int R, bool interleaved, float sign, int t, int G, float *stage) {
     if constexpr (KIND != kSingle) {  // threads without pairs have the angle 0
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float &a = KIND == kInterleaved ? x[2 * i] : x[i], &b = KIND == kInterleaved ? x[2 * i + 1] : x[4 + i];
+            float &a = interleaves(KIND) ? x[2 * i] : x[i], &b = interleaves(KIND) ? x[2 * i + 1] : x[4 + i];
             const float s = sign * cs[i].y, y = a * cs[i].x - b * s;
             b = fmaf(b, cs[i].x, a * s);
             a = y;
@@ -179,18 +239,17 @@ template <bool BWD>
 constexpr int kBatch = BWD ? 2 : 4;
 
 // A CTA's warps take kThreads / 32 / share tokens at a time, share of them the heads of one; every
-// gridDim.x-th of such blocks of tokens. Dynamic shared memory (not VEC): the groups' stages.
+// gridDim.x-th of such blocks of tokens. Dynamic shared memory (single channels): the groups' stages.
 template <typename T, Kind KIND, bool BWD>
 __global__ void __launch_bounds__(kThreads, BWD ? 3 : 4) qk_norm_kernel(const QkNormArgs p, int G, int share) {
     extern __shared__ __align__(16) float stages[];
     __shared__ __align__(16) float weight[2][kMaxD];
     __shared__ uint64_t fraction[kMaxD / 2];
-    constexpr bool VEC = KIND != kSingle;
-    constexpr int NB = kBatch<BWD>, NA = VEC ? 4 : 8;
+    constexpr int W = width(KIND), NB = kBatch<BWD>, NA = W > 1 ? 4 : 8;
     if constexpr (BWD) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int R = p.n_freqs, tid = threadIdx.x, warp = tid >> 5, t = tid & (G - 1);
     const int per_warp = 32 / G, first = (warp % share) * per_warp + (tid & 31) / G, stride = share * per_warp;  // heads
-    const Runs run = runs(t, R, KIND == kInterleaved);
+    const Runs run = runs<KIND>(t, R, G);
     float *stage = stages + tid / G * 2 * R;
     for (int i = tid; i < kMaxD; i += kThreads) {
         weight[0][i] = i < p.d ? p.weight[0][i] : 0.f;
@@ -214,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? 3 : 4) qk_norm_kernel(const Qk
             const T *x_at = static_cast<const T *>(p.x[which]) + tok * p.stride[which];  // offsets of heads fit 32 bits
             const T *u_at = BWD ? static_cast<const T *>(p.dy[which]) + tok * p.dy_stride[which] : nullptr;
             T *y_at = static_cast<T *>(p.y[which]) + tok * heads * p.d;
-            Row<T, VEC> x_row[NB], u_row[BWD ? NB : 1];
+            Row<T, W> x_row[NB], u_row[BWD ? NB : 1];
             auto fetch = [&](int n, int h) {
                 if (h < heads) {
                     x_row[n].load(x_at + h * p.d, p.d, t, G, run);
@@ -231,12 +290,25 @@ __global__ void __launch_bounds__(kThreads, BWD ? 3 : 4) qk_norm_kernel(const Qk
 #pragma unroll
                 for (int i = 0; i < NA; ++i) {
                     const int c = t + G * i;
-                    const int pair = VEC ? 4 * t + i : p.interleaved ? c >> 1 : c < R ? c : c - R;
-                    cs[i] = cos_sin((VEC ? pair < R : c < 2 * R) ? fraction[pair] * at : 0);
+                    const int pair = KIND == kHalves2        ? 2 * (t + (i >> 1) * G) + (i & 1)
+                                     : KIND == kInterleaved2 ? 2 * (t + (i & 1) * G) + (i >> 1)
+                                     : W == 4                ? 4 * t + i
+                                     : p.interleaved         ? c >> 1
+                                     : c < R                 ? c
+                                                             : c - R;
+                    cs[i] = cos_sin((W > 1 ? pair < R : c < 2 * R) ? fraction[pair] * at : 0);
                 }
             }
             float w[8];
-            if constexpr (VEC) {
+            if constexpr (W == 2) {
+                const int at[4] = {run.a, run.a2, run.b, run.b2};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 x = *reinterpret_cast<const float2 *>(&weight[which][min(at[i], kMaxD - 2)]);
+                    w[2 * i] = x.x;
+                    w[2 * i + 1] = x.y;
+                }
+            } else if constexpr (W == 4) {
                 const float4 a = *reinterpret_cast<const float4 *>(&weight[which][min(run.a, kMaxD - 4)]);
                 const float4 b = *reinterpret_cast<const float4 *>(&weight[which][min(run.b, kMaxD - 4)]);
                 w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
@@ -265,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? 3 : 4) qk_norm_kernel(const Qk
 #pragma unroll
                         for (int i = 0; i < 8; ++i) x[i] *= c * w[i];
                         turn<KIND>(x, cs, R, p.interleaved, 1.f, t, G, stage);
-                        if (live) store_row<VEC>(y_at + h * p.d, x, p.d, t, G, run);
+                        if (live) store_row<W>(y_at + h * p.d, x, p.d, t, G, run);
                     } else {
                         turn<KIND>(u, cs, R, p.interleaved, -1.f, t, G, stage);
                         float tn = 0.f;
@@ -279,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? 3 : 4) qk_norm_kernel(const Qk
                         tn = group_sum(tn, G) * inv_d;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) u[i] = c * (u[i] - x[i] * tn);
-                        if (live) store_row<VEC>(y_at + h * p.d, u, p.d, t, G, run);
+                        if (live) store_row<W>(y_at + h * p.d, u, p.d, t, G, run);
                     }
                 }
             }
@@ -295,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, BWD ? 3 : 4) qk_norm_kernel(const Qk
             for (int i = 0; i < 8; ++i) {
                 float x = dw[n][i];
                 for (int o = G; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                const int c = VEC ? (i < 4 ? run.a + i : run.b + i - 4) : t + G * i;
+                const int c = W > 1 ? (i < 2 ? run.a : i < 4 ? run.a2 : i < 6 ? run.b : run.b2) + (i & 1) : t + G * i;
                 if ((tid & 31) < G && c < p.d) sum[tid >> 5][c] = x;
             }
             __syncthreads();
@@ -333,18 +405,15 @@ __global__ void __launch_bounds__(kSumThreads) qk_norm_sum_kernel(const float *p
 
 constexpr int kBlocks = 152 * 4, kBwdBlocks = 152 * 3;
 
-// four channels of a row at once: rows of 16 (fp32) or 8 bytes, pairs in fours
+// The most channels of a row at once that lengths, halves and addresses allow
 template <typename T>
-bool vector_rows(const QkNormArgs &p, bool bwd) {
-    if (p.d % 8 != 0 || p.n_freqs % 4 != 0) return false;
-    constexpr size_t align = 4 * sizeof(T);
-    for (int i = 0; i < 2; ++i) {
-        const void *ptrs[] = {p.x[i], p.y[i], bwd ? p.dy[i] : nullptr};
-        for (const void *x : ptrs)
-            if ((uintptr_t)x % align != 0) return false;
-        if (p.stride[i] % 4 != 0 || (bwd && p.dy_stride[i] % 4 != 0)) return false;
-    }
-    return true;
+int load_width(const QkNormArgs &p, bool bwd) {
+    uintptr_t all = 0;
+    for (int i = 0; i < 2; ++i)
+        all |= (uintptr_t)p.x[i] | (uintptr_t)p.y[i] | (bwd ? (uintptr_t)p.dy[i] | (uintptr_t)p.dy_stride[i] * sizeof(T) : 0) |
+               (uintptr_t)p.stride[i] * sizeof(T);
+    if (p.d % 8 == 0 && p.n_freqs % 4 == 0 && all % (4 * sizeof(T)) == 0) return 4;
+    return p.d % 4 == 0 && (p.interleaved || p.n_freqs % 2 == 0) && all % (2 * sizeof(T)) == 0 ? 2 : 1;
 }
 
 template <typename T, bool BWD>
@@ -358,12 +427,14 @@ cudaError_t run(const QkNormArgs &p, cudaStream_t stream) {
     while (share < warps && p.n_tok * share < (BWD ? 4 * kBwdBlocks : kBlocks) * warps && share * (32 / G) < heads) share *= 2;
     const int64_t blocks = (p.n_tok * share + warps - 1) / warps;
     const unsigned grid = (unsigned)std::min<int64_t>(blocks, BWD ? kBwdBlocks : kBlocks);
-    const bool vec = vector_rows<T>(p, BWD);
-    const size_t smem = vec ? 0 : (size_t)kThreads / G * 2 * p.n_freqs * 4;
+    const int w = load_width<T>(p, BWD);
+    const size_t smem = w > 1 ? 0 : (size_t)kThreads / G * 2 * p.n_freqs * 4;
     if (grid > 0) {
-        if (!vec) qk_norm_kernel<T, kSingle, BWD><<<grid, kThreads, smem, stream>>>(p, G, share);
-        else if (p.interleaved) qk_norm_kernel<T, kInterleaved, BWD><<<grid, kThreads, smem, stream>>>(p, G, share);
-        else qk_norm_kernel<T, kHalves, BWD><<<grid, kThreads, smem, stream>>>(p, G, share);
+        auto kernel = w == 1          ? qk_norm_kernel<T, kSingle, BWD>
+                      : p.interleaved ? w == 4 ? qk_norm_kernel<T, kInterleaved, BWD> : qk_norm_kernel<T, kInterleaved2, BWD>
+                      : w == 4        ? qk_norm_kernel<T, kHalves, BWD>
+                                      : qk_norm_kernel<T, kHalves2, BWD>;
+        kernel<<<grid, kThreads, smem, stream>>>(p, G, share);
         count_launches(1);
     }
     if (BWD) {

@@ -70,7 +70,8 @@ def check(x, interleaved=False, eps=1e-6):
 
 SHAPES = [(1, 1, 1, 128, 128), (1, 32, 8, 128, 64), (5, 2, 2, 64, 64), (33, 3, 1, 100, 50), (7, 4, 4, 80, 20),
           (130, 7, 1, 256, 128), (17, 1, 5, 256, 256), (9, 2, 2, 8, 8), (3, 1, 1, 1, 0), (12, 2, 3, 33, 32),
-          (40, 32, 32, 128, 0), (20, 5, 2, 128, 48), (600, 16, 4, 72, 72), (11, 2, 1, 2, 2), (5, 300, 300, 16, 8)]
+          (40, 32, 32, 128, 0), (20, 5, 2, 128, 48), (600, 16, 4, 72, 72), (11, 2, 1, 2, 2), (5, 300, 300, 16, 8),
+          (50, 4, 2, 100, 100), (21, 3, 3, 100, 0), (70, 2, 4, 36, 20), (9, 5, 1, 252, 124), (6, 1, 1, 4, 4), (19, 2, 2, 20, 6)]
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
