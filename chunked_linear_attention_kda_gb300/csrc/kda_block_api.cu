@@ -250,7 +250,7 @@ static kda::DlaArgs dla_args(const void *q, const void *k, const void *v, int64_
     p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
     p.g = g; p.g_stride = g_stride; p.h0 = h0; p.cu_seqlens = cu; p.scale = scale; p.workspace = workspace;
     p.n_tok = n_tok; p.n_seq = n_seq; p.n_k_heads = n_k_heads; p.n_heads = n_heads;
-    p.d_k = d_k; p.d_v = d_v; p.bf16 = dtype == KDA_BF16;
+    p.d_k = p.in_k = d_k; p.d_v = p.in_v = d_v; p.bf16 = dtype == KDA_BF16;
     return p;
 }
 static Range dla_decays(const float *g, const kda::DlaArgs &p) {

@@ -74,7 +74,7 @@ cudaError_t launch_dla_sum_decay(const float *sums, int64_t rows, int heads, flo
 size_t dla_simt_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k, int32_t d_v, bool bwd);
 cudaError_t launch_dla_simt(const DlaArgs &args, bool bwd, cudaStream_t stream);
 // bf16 inputs: tcgen05 (kda_dla_fwd.cu, kda_dla_bwd.cu).
-size_t dla_tc_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k);
+size_t dla_tc_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k, int32_t d_v);
 cudaError_t launch_dla_tc_fwd(const DlaArgs &args, cudaStream_t stream);
 size_t dla_tc_bwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k, int32_t d_v);
 cudaError_t launch_dla_tc_bwd(const DlaArgs &args, cudaStream_t stream);

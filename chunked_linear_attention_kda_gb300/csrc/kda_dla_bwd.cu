@@ -131,10 +131,10 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
         drain_bar(bar(L::Drain), 0);
     } else if (warp == 1) {
         const Source in[2] = {
-            {&tm_key, static_cast<const __nv_bfloat16 *>(REV ? p.q : p.k), REV ? p.q_stride : p.k_stride, kh, p.d_k, DK / 64,
+            {&tm_key, static_cast<const __nv_bfloat16 *>(REV ? p.q : p.k), REV ? p.q_stride : p.k_stride, kh, p.in_k, DK / 64,
              REV ? plan.vec_q : plan.vec_k},
-            {&tm_val, static_cast<const __nv_bfloat16 *>(REV ? p.dout : p.v), REV ? (int64_t)p.n_heads * p.d_v : p.v_stride, head,
-             p.d_v, p.d_v > 64 ? 2 : 1, REV ? plan.vec_o : plan.vec_v}};
+            {&tm_val, static_cast<const __nv_bfloat16 *>(REV ? p.dout : p.v), REV ? (int64_t)p.n_heads * p.in_v : p.v_stride, head,
+             p.in_v, p.d_v > 64 ? 2 : 1, REV ? plan.vec_o : plan.vec_v}};
         const TileGates *gates = gates_of(plan.gates, p, sg.seq, (int64_t)sg.index * (plan.seg / C), head);
         int begun = 0;  // tiles whose copies were begun
         for (int n = 0; n < steps; ++n) {
@@ -587,11 +587,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                     ++partials;
                 }
             } else {
-                const int64_t ov = (int64_t)p.n_heads * p.d_v;
-                const Source in[4] = {{&tm_k, static_cast<const __nv_bfloat16 *>(p.k), p.k_stride, kh, p.d_k, DK / 64, bp.walk.vec_k},
-                                      {&tm_v, static_cast<const __nv_bfloat16 *>(p.v), p.v_stride, b.head, p.d_v, DV / 64, bp.walk.vec_v},
-                                      {&tm_q, static_cast<const __nv_bfloat16 *>(p.q), p.q_stride, kh, p.d_k, DK / 64, bp.walk.vec_q},
-                                      {&tm_o, static_cast<const __nv_bfloat16 *>(p.dout), ov, b.head, p.d_v, DV / 64, bp.walk.vec_o}};
+                const int64_t ov = (int64_t)p.n_heads * p.in_v;
+                const Source in[4] = {{&tm_k, static_cast<const __nv_bfloat16 *>(p.k), p.k_stride, kh, p.in_k, DK / 64, bp.walk.vec_k},
+                                      {&tm_v, static_cast<const __nv_bfloat16 *>(p.v), p.v_stride, b.head, p.in_v, DV / 64, bp.walk.vec_v},
+                                      {&tm_q, static_cast<const __nv_bfloat16 *>(p.q), p.q_stride, kh, p.in_k, DK / 64, bp.walk.vec_q},
+                                      {&tm_o, static_cast<const __nv_bfloat16 *>(p.dout), ov, b.head, p.in_v, DV / 64, bp.walk.vec_o}};
                 const int to[4] = {L::K, L::V, L::Q, L::dO};
                 if (i > 0) wait(L::QoEmpty, i - 1);
 #pragma unroll 1
@@ -940,7 +940,7 @@ int walk_segment(int64_t n_tok, int32_t n_seq, int32_t n_heads) {
     return (m + (m & 1)) * C;
 }
 struct Layout {
-    size_t gates, decays, joins, states, sums, parts, bytes;
+    size_t gates, joins, states, sums, parts, copies, bytes;
     int seg;
     int64_t slots;
 };
@@ -956,14 +956,18 @@ Layout layout(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, 
     l.states = l.joins + up(2 * units * (state_floats(dkp) + 1) * 4);
     l.sums = l.states + blocks * pair_bytes(dkp, dvp);
     l.parts = up(l.sums + blocks * 4);
-    l.bytes = l.parts + (n_heads > n_k_heads ? 2 * (size_t)n_tok * n_heads * dkp * 4 : 0);
+    l.copies = up(l.parts + (n_heads > n_k_heads ? 2 * (size_t)n_tok * n_heads * dkp * 4 : 0));
+    l.bytes = l.copies + copies_bytes(n_tok, n_heads, n_k_heads, d_k, d_v, true);
     return l;
 }
 
 template <int DK, int DV>
-cudaError_t backward(const DlaArgs &p, cudaStream_t stream) {
+cudaError_t backward(const DlaArgs &args, cudaStream_t stream) {
+    DlaArgs p = args;
     const Layout l = layout(p.n_tok, p.n_seq, p.n_heads, p.n_k_heads, p.d_k, p.d_v);
     char *ws = static_cast<char *>(p.workspace);
+    cudaError_t e = align_inputs(p, ws + l.copies, true, stream);
+    if (e != cudaSuccess) return e;
     BwdPlan bp{};
     Plan &plan = bp.walk;
     plan = make_plan(p, true);
@@ -977,17 +981,17 @@ cudaError_t backward(const DlaArgs &p, cudaStream_t stream) {
     bp.sums = reinterpret_cast<float *>(ws + l.sums);
     bp.dq = reinterpret_cast<float *>(ws + l.parts);
     bp.dk = bp.dq + (size_t)p.n_tok * p.n_heads * DK;
-    const int64_t os = (int64_t)p.n_heads * p.d_v;
+    const int64_t os = (int64_t)p.n_heads * p.in_v;
     CUtensorMap m[4], wm[4];  // q, k, v, dout; tiles of 64 and of 128 tokens
     bool copies = true;
     for (int rows : {C, kBlock}) {
         CUtensorMap *to = rows == C ? m : wm;
-        copies = copies && TileMap::encode(&to[0], p.q, p.n_tok, p.q_stride, p.n_k_heads, p.d_k, rows) &&
-                 TileMap::encode(&to[1], p.k, p.n_tok, p.k_stride, p.n_k_heads, p.d_k, rows) &&
-                 TileMap::encode(&to[2], p.v, p.n_tok, p.v_stride, p.n_heads, p.d_v, rows) &&
-                 TileMap::encode(&to[3], p.dout, p.n_tok, os, p.n_heads, p.d_v, rows);
+        copies = copies && TileMap::encode(&to[0], p.q, p.n_tok, p.q_stride, p.n_k_heads, p.in_k, rows) &&
+                 TileMap::encode(&to[1], p.k, p.n_tok, p.k_stride, p.n_k_heads, p.in_k, rows) &&
+                 TileMap::encode(&to[2], p.v, p.n_tok, p.v_stride, p.n_heads, p.in_v, rows) &&
+                 TileMap::encode(&to[3], p.dout, p.n_tok, os, p.n_heads, p.in_v, rows);
     }
-    cudaError_t e = launch_gates(p, plan, stream);
+    e = launch_gates(p, plan, stream);
     if (e != cudaSuccess) return e;
     if (plan.cut) {
         e = launch_segments<DK>(p, plan, m[0], m[1], m[2], m[3], copies, 2, stream);

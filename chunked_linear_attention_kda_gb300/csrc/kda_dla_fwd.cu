@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const bool pair = warp == 2;
         const Source in[2] = {
             {pair ? &tm_k : &tm_v, static_cast<const __nv_bfloat16 *>(pair ? p.k : p.v), pair ? p.k_stride : p.v_stride, pair ? kh : head,
-             pair ? p.d_k : p.d_v, pair ? DK / 64 : p.d_v > 64 ? 2 : 1, pair ? plan.vec_k : plan.vec_v},
-            {&tm_q, static_cast<const __nv_bfloat16 *>(p.q), p.q_stride, kh, p.d_k, DK / 64, plan.vec_q}};
+             pair ? p.in_k : p.in_v, pair ? DK / 64 : p.d_v > 64 ? 2 : 1, pair ? plan.vec_k : plan.vec_v},
+            {&tm_q, static_cast<const __nv_bfloat16 *>(p.q), p.q_stride, kh, p.in_k, DK / 64, plan.vec_q}};
         const TileGates *gates = gates_of(plan.gates, p, sg.seq, (int64_t)sg.index * (plan.seg / C), head);
         const int full = pair ? L::KFull : L::VFull, empty = pair ? L::KEmpty : L::VEmpty;
         int begun = 0;  // tiles whose copies were begun
@@ -487,9 +487,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 template <int DK>
 cudaError_t forward(const DlaArgs &p, cudaStream_t stream) {
     CUtensorMap q, k, v;
-    const bool copies = TileMap::encode(&q, p.q, p.n_tok, p.q_stride, p.n_k_heads, p.d_k) &&
-                        TileMap::encode(&k, p.k, p.n_tok, p.k_stride, p.n_k_heads, p.d_k) &&
-                        TileMap::encode(&v, p.v, p.n_tok, p.v_stride, p.n_heads, p.d_v);
+    const bool copies = TileMap::encode(&q, p.q, p.n_tok, p.q_stride, p.n_k_heads, p.in_k) &&
+                        TileMap::encode(&k, p.k, p.n_tok, p.k_stride, p.n_k_heads, p.in_k) &&
+                        TileMap::encode(&v, p.v, p.n_tok, p.v_stride, p.n_heads, p.in_v);
     const bool wide = p.d_v % 8 == 0 && (uintptr_t)p.out % 16 == 0;
     const Plan plan = make_plan(p, false);
     // A short call forms the gates beside the tiles' copies: a launch less (40 tokens of 32 heads in a graph:
@@ -516,7 +516,7 @@ size_t dla_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_
                            bool bf16, bool bwd) {
     if (!bf16) return dla_simt_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v, bwd);
     return bwd ? dla_tc_bwd_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v)
-               : dla_tc_fwd_workspace_bytes(n_tok, n_seq, n_heads, d_k);
+               : dla_tc_fwd_workspace_bytes(n_tok, n_seq, n_heads, n_k_heads, d_k, d_v);
 }
 // without a token the states pass through: nothing of bf16 is read
 cudaError_t launch_dla_fwd(const DlaArgs &p, cudaStream_t stream) {
@@ -526,11 +526,14 @@ cudaError_t launch_dla_bwd(const DlaArgs &p, cudaStream_t stream) {
     return p.bf16 && p.n_tok > 0 ? launch_dla_tc_bwd(p, stream) : launch_dla_simt(p, true, stream);
 }
 
-size_t dla_tc_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k) {
-    return dla::plan_bytes(n_tok, n_seq, n_heads, d_k);
+size_t dla_tc_fwd_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k, int32_t d_v) {
+    return dla::plan_bytes(n_tok, n_seq, n_heads, d_k) + dla::copies_bytes(n_tok, n_heads, n_k_heads, d_k, d_v, false);
 }
 
-cudaError_t launch_dla_tc_fwd(const DlaArgs &p, cudaStream_t stream) {
+cudaError_t launch_dla_tc_fwd(const DlaArgs &args, cudaStream_t stream) {
+    DlaArgs p = args;
+    const cudaError_t e = dla::align_inputs(p, static_cast<char *>(p.workspace) + dla::plan_bytes(p.n_tok, p.n_seq, p.n_heads, p.d_k), false, stream);
+    if (e != cudaSuccess) return e;
     return p.d_k <= 64 ? dla::forward<64>(p, stream) : dla::forward<128>(p, stream);
 }
 

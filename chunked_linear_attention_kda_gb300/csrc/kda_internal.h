@@ -151,6 +151,7 @@ struct DlaArgs {
     int64_t n_tok;
     int32_t n_seq, n_k_heads, n_heads, d_k, d_v;
     bool bf16;
+    int32_t in_k, in_v;  // channels from head to head of q and k, of v and dout: d_k, d_v, or an aligned copy's
 };
 size_t dla_workspace_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, int32_t d_k, int32_t d_v,
                            bool bf16, bool bwd);
