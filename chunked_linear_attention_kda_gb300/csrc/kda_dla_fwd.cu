@@ -18,7 +18,9 @@
 //
 // A long sequence is cut into segments, so that few heads fill the GPU: a first launch forms what
 // each segment adds to the state (kda_dla_states.h: K and V are read once more), a second one the
-// states at the segments' starts, a third the output, all segments side by side.
+// states at the segments' starts, a third the output, all segments side by side. 64K tokens of 32 heads, 128 x
+// 128: gates 14 us, segments 164 us (1.07 GB, the copy rate), join 12 us, output 400 us (2.15 GB, 0.8 of it; 3500
+// cycles a tile, with no unit above half: the roles of a tile wait for one another).
 #include <cmath>
 
 #include "kda_dla_states.h"

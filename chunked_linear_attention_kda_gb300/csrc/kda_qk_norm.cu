@@ -13,7 +13,8 @@
 // Groups of threads hold rows; a warp's groups take the heads of one token in turn, so that its angles are
 // formed once and stay in registers, and a thread holds both channels of each of its pairs, so that
 // none goes through shared memory (a first form, with a run of channels a thread and the angles in shared
-// memory, was bound by that: 511 us at 64K tokens). Sums over rows go to one partial row a CTA
+// memory, was bound by that: 511 us at 64K tokens of 32 + 8 heads of 128 channels, 224 so, 0.90 of the copy
+// rate; backward of 8191 tokens of 32 + 32 heads 95 us, 0.64, with the conversions and sums in 0.57 of the issue slots). Sums over rows go to one partial row a CTA
 // and are added up by a second kernel in a fixed order: the same call gives the same bits.
 #include <cuda_bf16.h>
 
