@@ -646,7 +646,8 @@ kda_status kda_gated_norm_bwd(const void *dy, int64_t dy_stride, const void *x,
  * n_heads], contiguous; with g_stride = 0 one per head [n_heads], the same for every token. Any
  * value up to 0; -inf forgets everything, values below -200 act as -inf in the chunked calls.
  * scale: finite (d_k^-1/2 is usual). 1 <= d_k, d_v <= 128, n_heads a multiple of n_k_heads and at
- * most 65535. Inputs are aligned to their element size; 16-byte aligned rows are read faster.
+ * most 65535. Inputs are aligned to their element size; 16-byte aligned rows are read faster (bf16
+ * heads that are no multiple of 8 channels wide are copied to such rows in the workspace first).
  * State, sums and the gradient of g are fp32; with KDA_BF16 the products of the chunked calls run on
  * the tensor cores with every operand that is not itself a bf16 input carried in two bf16 parts
  * (within 2^-16 of its value; h_final, dg and dh0 are within some 5e-6 of their norms), with KDA_F32

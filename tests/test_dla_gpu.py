@@ -3,9 +3,10 @@
 
 Bars on the rel-L2 error, from the number formats:
   bf16 results   the definition's rounded once: half a step is 2^-8 of a value at most; the operands in
-                 two bf16 parts add 2^-17 each: 2^-8 + 2^-14
-  fp32 results of bf16 inputs   operands in two parts keep 2^-18 each, through a product of two and
-                 sums of 256 terms in fp32, dg through sums over a chunk's rows and columns: 2e-5
+                 two bf16 parts add half a step of half a step each, 2^-16: 2^-8 + 2^-14
+  fp32 results of bf16 inputs   operands in two parts are off by 2^-16 at most and 2^-18 in the root mean
+                 square, through products of up to four of them and sums of 256 terms in fp32, dg
+                 through sums over a chunk's rows and columns: 2e-5
   fp32 results of fp32 inputs   sums of up to 256 terms, each addition 2^-24, random in sign, and the
                  exponentials' 2^-22: 6e-6
   one token      fp32 arithmetic throughout, sums of 128 terms: 1e-6
@@ -236,9 +237,10 @@ def slices(x):
         yield views
 
 
+@pytest.mark.parametrize("lengths,dk,dv", [([130, 70], 128, 64), ([130, 70], 33, 31), ([40], 64, 31), ([1100], 33, 128)])
 @pytest.mark.parametrize("dtype", [FP, BF])
-def test_slices_of_a_projection_give_the_same_bits(dtype):
-    x = Inputs([130, 70], 2, 4, 128, 64, dtype, seed=11)
+def test_slices_of_a_projection_give_the_same_bits(dtype, lengths, dk, dv):
+    x = Inputs(lengths, 2, 4, dk, dv, dtype, seed=11)
     ref, grads = forward(x), backward(x)
     for q, k, v in slices(x):
         got = kda.dla_chunk_fwd(q, k, v, x.g, x.h0, x.cu)
@@ -386,6 +388,25 @@ def test_another_stream_and_a_callers_workspace():
     s.synchronize()
     assert got[0] is out and all(torch.equal(a, b) for a, b in zip(got, ref))
     assert all(torch.equal(a, b) for a, b in zip(back, grads))
+
+
+@pytest.mark.parametrize("dk", [128, 33])
+def test_two_calls_at_once(dk):
+    """Calls on two streams share nothing, whichever of them a kernel of the other's follows."""
+    xs = [Inputs([600, 90], 4, 4, dk, 128, BF, seed=28), Inputs([20, 700], 4, 4, dk, 128, BF, seed=29)]
+    ref = [(*forward(x), *backward(x)) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, (x, s) in enumerate(zip(xs, streams)):
+            with torch.cuda.stream(s):
+                got[i].append((*kda.dla_chunk_fwd(*x.args), *kda.dla_chunk_bwd(*x.args, x.dout, x.dhf)))
+    torch.cuda.synchronize()
+    assert kda.read_device_flags() == 0
+    for want, calls in zip(ref, got):
+        for call in calls:
+            assert all(torch.equal(a, b) for a, b in zip(call, want))
 
 
 def test_in_a_graph():
