@@ -181,7 +181,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 // ---------------------------------------------------------------- gates
 // Of one tile and head, formed for all tiles by a launch of their own (kda_dla_fwd.cu) and copied in with the
-// tile: running sums of g log2(e), whole part and fraction, scale times the decays up to and with each token (gam), the decays
+// tile: running sums of g log2(e), whole number and rest, scale times the decays up to and with each token (gam), the decays
 // past each (del), the decay of all (whole) and its exponent. Formed beside the products by one warp they
 // were the longest chain of a tile (1700 cycles of scans and conversions).
 struct TileGates {
@@ -195,18 +195,24 @@ static_assert(sizeof(TileGates) % 16 == 0, "copied in bulk");
 __device__ __forceinline__ const TileGates *gates_of(const TileGates *all, const DlaArgs &p, int seq, int64_t c, int head) {
     return all + ((slot_base(p.cu_seqlens, seq) + c) * p.n_heads + head);
 }
-// Sums of g log2(e) in fixed point, 32 bits behind the point: exact, so that differences of neighbours
-// stay exact after a long run of strong decays, and a scan's step is one addition. By conversions of 32
-// bits alone: those of 64 are as slow as fp64 on this part (gates of 64K tokens of 32 heads: 31 us with them).
+// Sums of g log2(e) in fixed point, 44 bits behind the point: exact, so that differences of neighbours
+// stay exact after a long run of strong decays, and a scan's step is one addition. An exponent is cut off
+// after 20 bits, towards zero: what is left is exact and of its sign, however small the exponent is, and
+// gives the other 24. (Rounded down, the rest of a small negative one is near 1 and loses its last places, the
+// same at every token of a constant rate: a state of 64K tokens at -3.7e-5 was off by 9e-5 of its norm.) By
+// conversions of 32 bits alone: those of 64 are as slow as fp64 on this part (gates of 64K tokens of 32
+// heads: 31 us with them).
+constexpr int kPoint = 44;
 __device__ __forceinline__ int64_t fixed_exponent(float g) {
     const Two x = decay_exponent(g);
-    const float n = floorf(x.hi);
-    const uint32_t f = __float2uint_rn((x.hi - n) * 4294967296.f);  // x.hi has 24 bits, its fraction too
-    return (((int64_t)(int)n << 32) | f) + __float2int_rn(x.lo * 4294967296.f);
+    const float y = x.hi * 0x1p20f, n = truncf(y);
+    return ((int64_t)(int)n << 24) + __float2int_rn(fmaf(x.lo, 0x1p20f, y - n) * 0x1p24f);
 }
-// whole and fraction, to 2^-25
+// the nearest whole number and the rest, to 2^-26 and to 2^-37 near 0
 __device__ __forceinline__ float2 from_fixed(int64_t x) {
-    return make_float2((float)(int)(x >> 32), (float)(uint32_t)x * 2.3283064365386963e-10f);
+    const int n = (int)((x + ((int64_t)1 << (kPoint - 1))) >> kPoint);
+    const int64_t f = x - ((int64_t)n << kPoint);
+    return make_float2((float)n, fmaf((float)(int)(f >> 32), 0x1p-12f, (float)(uint32_t)f * 0x1p-44f));
 }
 __device__ __forceinline__ float exp2_fixed(int64_t x) {
     const float2 y = from_fixed(x);
@@ -225,7 +231,7 @@ __device__ __forceinline__ void form_gates(float2 g, float scale, TileGates *out
     }
     const int64_t total = __shfl_sync(0xffffffffu, run, 31);
     const int64_t before = run - both + first;
-    const float bad = __any_sync(0xffffffffu, !(g.x <= 1e6f && g.y <= 1e6f)) ? __int_as_float(0x7fffffff) : 0.f;
+    const float bad = __any_sync(0xffffffffu, !(g.x <= 1e3f && g.y <= 1e3f)) ? __int_as_float(0x7fffffff) : 0.f;
     float2 a = from_fixed(before), b = from_fixed(run);
     a.x += bad;
     b.x += bad;

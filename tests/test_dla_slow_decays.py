@@ -1,0 +1,128 @@
+"""Linear attention with decays near none, g from log(1 - 2^-11) to -1e-6 at every token and slopes
+down to 1e-8: rates of retention and lightning layers, whose memories are as long as the sequence.
+An error of the rate, however small beside 1, is the same at every token and adds up over the memory.
+
+The reference is a chunked fp64 form, held to the recurrence of ``oracle.block`` on the CPU. Bars: those of
+``tests/test_dla_gpu.py``, per head. What a long memory adds to them is each tile's rounding of the state,
+2^-24 at most and random in sign: sqrt(256) 2^-24 = 1e-6 over 16K tokens at most, of which its root mean
+square is a third.
+"""
+import math
+
+import pytest
+import torch
+
+import chunked_linear_attention_kda_gb300 as kda
+from oracle import block
+from tests.test_dla_gpu import BF, DEV, FP, Inputs, backward, bar, forward, rel
+
+RATES = [math.log1p(-2.0 ** -11), -1e-4, -3.7e-5, -1e-6]
+SLOPES = [-1e-5 * 2.0 ** (-h / 4) for h in range(32)]
+F64 = torch.float64
+
+
+def chunked(q, k, v, g, h0, scale):
+    """One sequence in fp64, chunk by chunk of 64 tokens (zeros past its end), g [N, H]."""
+    n, hv, c = v.shape[0], v.shape[1], 64
+    more = -n % c
+    group = hv // q.shape[1]
+
+    def split(x):
+        x = torch.cat((x, x.new_zeros(more, *x.shape[1:])))
+        return x.unflatten(0, (-1, c)).movedim(2, 1)  # [chunks, H, 64, ...]
+
+    q, k = (split(x.repeat_interleave(group, 1)) for x in (q, k))
+    v, g = split(v), split(g).cumsum(-1)
+    low = torch.ones(c, c, dtype=torch.bool, device=q.device).tril()
+    pair = torch.where(low, (g[..., :, None] - g[..., None, :]), -math.inf).exp()
+    add = ((g[..., -1:] - g).exp()[..., None] * k).mT @ v
+    whole = g[..., -1].exp()[..., None, None]
+    S, starts = h0[0], []
+    for i in range(q.shape[0]):
+        starts.append(S)
+        S = whole[i] * S + add[i]
+    out = (g.exp()[..., None] * q) @ torch.stack(starts) + (pair * (q @ k.mT)) @ v
+    return scale * out.movedim(1, 2).flatten(0, 1)[:n], S[None]
+
+
+def gradients(xs, scale, dout, dhf):
+    xs = [x.clone().requires_grad_(True) for x in xs]
+    out, end = chunked(*xs, scale)
+    return torch.autograd.grad((out * dout).sum() + (end * dhf).sum(), xs)
+
+
+def test_the_chunked_form_is_the_recurrence():
+    gen = torch.Generator().manual_seed(0)
+    r = lambda *s: torch.randn(s, generator=gen, dtype=F64)  # noqa: E731
+    q, k, v, g, h0 = r(150, 2, 5), r(150, 2, 5), r(150, 4, 3), -0.1 * r(150, 4).abs(), r(1, 4, 5, 3)
+    dout, dhf = r(150, 4, 3), r(1, 4, 5, 3)
+    got = chunked(q, k, v, g, h0, 0.3) + gradients((q, k, v, g, h0), 0.3, dout, dhf)
+    want = block.dla(q, k, v, g, h0, [0, 150], 0.3) + block.dla_grads(q, k, v, g, h0, [0, 150], dout, dhf, 0.3)
+    assert all(torch.allclose(a, b, atol=1e-10) for a, b in zip(got, want))
+
+
+def inputs(n, hk, dk, dv, dtype, rates, per_head, seed):
+    x = Inputs([n], hk, len(rates), dk, dv, dtype, seed=seed)
+    rates = torch.tensor(rates, device=DEV)
+    x.g = rates if per_head else rates.expand(n, len(rates)).contiguous()
+    return x
+
+
+def each_head(name, got, want, heads, dtype, head_axis):
+    for h in range(heads):
+        a, b = got.select(head_axis, h), want.select(head_axis, h)
+        assert rel(a, b) <= bar(got, dtype), f"{name}, head {h}: {rel(a, b):.2e}"
+
+
+def check(x):
+    xs = x.f64(DEV)
+    scale, hv = x.q.shape[2] ** -0.5, x.v.shape[1]
+    out, end = forward(x)
+    want = chunked(*xs[:3], xs[3].expand(x.v.shape[:2]), xs[4], scale)
+    each_head("out", out, want[0], hv, x.dtype, 1)
+    each_head("h_final", end, want[1], hv, x.dtype, 1)
+    got = backward(x)
+    want = gradients((*xs[:3], xs[3].expand(x.v.shape[:2]), xs[4]), scale, x.dout.double(), x.dhf.double())
+    for i, (name, a, b) in enumerate(zip(("dq", "dk", "dv", "dg", "dh0"), got, want)):
+        if name == "dg" and x.g.dim() == 1:  # the terms cancel: of the sum of their sizes
+            err = (a.double() - b.sum(0)).abs() / b.abs().sum(0)
+            assert float(err.max()) <= bar(a, x.dtype), f"dg: {err}"
+        else:
+            each_head(name, a, b, a.shape[1], x.dtype, 1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("n,hk,dk,dv", [(8192, 2, 64, 64), (8192, 4, 128, 128), (8191, 1, 33, 72)])
+def test_constant_rates(n, hk, dk, dv, dtype, per_head):
+    check(inputs(n, hk, dk, dv, dtype, RATES, per_head, seed=n + dk))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_slopes_of_many_heads(dtype):
+    """Memories far longer than the sequence."""
+    check(inputs(16384, 8, 64, 64, dtype, SLOPES, True, seed=2))
+
+
+@pytest.mark.gpu
+def test_ragged_slow_decays():
+    """Rates that differ from token to token, a fifth of the tokens without any, several sequences."""
+    lengths = [3000, 0, 1, 8192, 515]
+    x = Inputs(lengths, 2, 4, 64, 128, BF, seed=3)
+    gen = torch.Generator().manual_seed(4)
+    g = -(10.0 ** (-7 + 4 * torch.rand(sum(lengths), 4, generator=gen)))
+    g[torch.rand(g.shape, generator=gen) < 0.2] = 0.0
+    x.g = g.to(DEV)
+    out, end = forward(x)
+    grads = backward(x)
+    for i, (a, b) in enumerate(zip(x.cu_host[:-1], x.cu_host[1:])):
+        if a == b:
+            continue
+        xs = [t[a:b].double() for t in (x.q, x.k, x.v, x.g)] + [x.h0[i:i + 1].double()]
+        want = chunked(*xs, 8.0 ** -1) + gradients(xs, 8.0 ** -1, x.dout[a:b].double(), x.dhf[i:i + 1].double())
+        got = (out[a:b], end[i:i + 1], *[t[a:b] for t in grads[:4]], grads[4][i:i + 1])
+        for name, y, ref in zip(("out", "h_final", "dq", "dk", "dv", "dg", "dh0"), got, want):
+            if name != "dg" or b - a > 1:  # of one token dg is a single sum that may cancel
+                assert rel(y, ref) <= bar(y, BF), f"{name} of sequence {i}: {rel(y, ref):.2e}"
