@@ -62,6 +62,25 @@ __device__ __forceinline__ float exp2_of(Two x) {
     const float e = ex2(x.hi);
     return fmaf(e * 0.693147181f, x.lo, e);
 }
+// 2^(n + f), n whole, f up to 1/2 of either sign, in two floats: near 1 what the decay takes away has 23 bits
+// of its own.
+__device__ __forceinline__ Two exp2_parts(float n, float f) {
+    const float e = ex2(n), m = expm1f(f * 0.693147181f), w = 1.f + m;
+    return {e * w, e * (m - (w - 1.f))};
+}
+// The decays that multiply a state one after the other. Near 1 a float is off by up to 2^-25, and with a
+// constant rate by the same amount every time, which adds up over the memory (64K tokens in tiles of 64 at
+// rates of 1e-6: the state off by 4e-5 of its norm). So what a factor's rounding left out, relative to it, goes
+// to the next factor: a product over any run is off by one rounding at its start and one at its end. Below
+// 1/4 nothing is handed on: what is left of a state does not add up.
+struct Factors {
+    float owed = 0.f;
+    __device__ __forceinline__ float next(Two decay) {
+        const float more = fmaf(decay.hi, owed, decay.lo), w = decay.hi + more;
+        owed = w > 0.25f ? __fdividef((decay.hi - w) + more, w) : 0.f;
+        return w;
+    }
+};
 // 2^(a - b) for neighbouring sums
 __device__ __forceinline__ float exp2_between(float2 a, float2 b) { return ex2((a.x - b.x) + (a.y - b.y)); }
 

@@ -226,6 +226,7 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
             load_given<NC>(st, from ? from + state_at : nullptr, p.d_k, p.d_v, dv, part * NC);
         }
         int kept = 0;
+        Factors decays;
 #pragma unroll 1
         for (int n = 0; n < nc; ++n) {
             if (enters(n)) {
@@ -249,7 +250,7 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
             if (n >= steps) break;
             const int s = n % S;
             wait(L::Full + s, n / S);
-            const float whole = reinterpret_cast<const TileGates *>(smem + s * L::kStage + L::Gate)->whole;
+            const float whole = decays.next(reinterpret_cast<const TileGates *>(smem + s * L::kStage + L::Gate)->whole);
             warp_arrive(bar(L::Empty + s));
             wait(L::DsFull + (n & 1), n >> 1);
             ptx::tc_fence_after();
@@ -649,7 +650,12 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             if (n >= 2) wait(L::GEmpty + (n & 1), (n >> 1) - 1);
             const TileGates *t = gates_of(bp.walk.gates, p, c.seq, 2 * c.index, c.head);
             const bool two = c.len > C;
-            const float2 s0 = t->sum, s1 = two ? t[p.n_heads].sum : make_float2(0.f, 0.f);
+            float2 s0 = from_fixed(t->sum), s1 = make_float2(0.f, 0.f);
+            s0.x += nan_of(*t);
+            if (two) {
+                s1 = from_fixed(t[p.n_heads].sum);
+                s1.x += nan_of(t[p.n_heads]);
+            }
             const Two total = add({s0.x, s0.y}, {s1.x, s1.y});
 #pragma unroll 1
             for (int e = 0; e < 4; ++e) {
@@ -957,7 +963,7 @@ Layout layout(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t n_k_heads, 
     const size_t units = n_tok > l.seg ? (size_t)l.slots * n_heads : 0, blocks = (size_t)block_slots(n_tok, n_seq) * n_heads;
     l.gates = 0;
     l.joins = up(gate_bytes(n_tok, n_seq, n_heads));
-    l.states = l.joins + up(2 * units * (state_floats(dkp) + 1) * 4);
+    l.states = l.joins + up(2 * units * (state_floats(dkp) * 4 + sizeof(Two)));
     l.sums = l.states + blocks * pair_bytes(dkp, dvp);
     l.parts = up(l.sums + blocks * 4);
     l.copies = up(l.parts + (n_heads > n_k_heads ? 2 * (size_t)n_tok * n_heads * dkp * 4 : 0));
@@ -980,7 +986,7 @@ cudaError_t backward(const DlaArgs &args, cudaStream_t stream) {
     plan.cut = p.n_tok > l.seg;
     plan.states = reinterpret_cast<float *>(ws + l.joins);
     const size_t units = plan.cut ? (size_t)l.slots * p.n_heads : 0;
-    plan.decays = plan.states + 2 * units * state_floats(DK);
+    plan.decays = reinterpret_cast<Two *>(plan.states + 2 * units * state_floats(DK));
     bp.states = ws + l.states;
     bp.sums = reinterpret_cast<float *>(ws + l.sums);
     bp.dq = reinterpret_cast<float *>(ws + l.parts);

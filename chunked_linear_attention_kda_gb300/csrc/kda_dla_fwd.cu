@@ -368,6 +368,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const bool live = 32 * (warp & 3) < p.d_v;
         float st[NC];
         const bool cut = sg.index > 0 || !sg.last;
+        Factors decays;
         gdr::wait_for_previous_kernel();
         if (cut) load_state<NC>(st, plan.states + ((size_t)slot * p.n_heads + head) * state_floats(DK), dv, part * NC);
         else load_given<NC>(st, p.h0 ? p.h0 + state_at : nullptr, p.d_k, p.d_v, dv, part * NC);
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             warp_arrive(bar(L::SFull));
             if (c + 1 == nc && !keep_end) break;
             wait(L::GFull + c % L::kGates, c / L::kGates);
-            const float whole = gate(c).whole;
+            const float whole = decays.next(gate(c).whole);
             warp_arrive(bar(L::GEmpty + c % L::kGates));
             wait(L::DsFull, c);
             ptx::tc_fence_after();

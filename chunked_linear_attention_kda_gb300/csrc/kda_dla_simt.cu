@@ -23,7 +23,8 @@ constexpr int kDkBlock = 32;
 
 struct Gates {
     float2 G[C];     // sums of g log2(e) up to and with each token
-    float gam[C], del[C], whole;
+    float gam[C], del[C];
+    Two whole;  // in two parts
 };
 // by one warp; tokens past the chunk's end have g = 0
 __device__ void chunk_gates(const DlaArgs &p, const Chunk &ch, int head, Gates *out) {
@@ -46,7 +47,10 @@ __device__ void chunk_gates(const DlaArgs &p, const Chunk &ch, int head, Gates *
         out->gam[r] = exp2_of(G);
         out->del[r] = exp2_between(make_float2(total.hi, total.lo), make_float2(G.hi, G.lo));
     }
-    if (lane == 0) out->whole = exp2_of(total);
+    if (lane == 0) {
+        const float n = rintf(total.hi);
+        out->whole = exp2_parts(n, (total.hi - n) + total.lo);
+    }
 }
 
 // rows x cols of src into a tile of 64 x W, zeros beyond
@@ -143,7 +147,7 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
-// The workspace: [directions][slots][heads] states, as many decays, then (backward) sums of dg and the
+// The workspace: [directions][slots][heads] states, as many decays in two parts, then (backward) sums of dg and the
 // parts of dq and dk of shared heads.
 struct Space {
     size_t state, decays, sums, dq, dk, floats;
@@ -153,7 +157,7 @@ __host__ __device__ inline Space space(int64_t n_tok, int32_t n_seq, int32_t n_h
     Space s;
     s.state = (size_t)d_k * d_v;
     s.decays = walks * chunks * s.state;
-    s.sums = s.decays + walks * chunks;
+    s.sums = s.decays + 2 * walks * chunks;
     s.dq = s.sums + (bwd ? chunks : 0);
     s.dk = s.dq + (bwd && n_heads > n_k_heads ? (size_t)n_tok * n_heads * d_k : 0);
     s.floats = s.dk + (s.dk - s.dq);
@@ -222,7 +226,10 @@ __global__ void __launch_bounds__(kThreads) dla_simt_add_kernel(const DlaArgs p,
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (i0 + ti + i < p.d_k && tj + j < p.d_v) ws[at * s.state + (int64_t)(i0 + ti + i) * p.d_v + tj + j] = add[i][j];
-    if (i0 == 0 && tid == 0) ws[s.decays + at] = gate.whole;
+    if (i0 == 0 && tid == 0) {
+        ws[s.decays + 2 * at] = gate.whole.hi;
+        ws[s.decays + 2 * at + 1] = gate.whole.lo;
+    }
 }
 
 // The states at the chunks' starts (reverse: the gradients of their ends) in place of what the chunks
@@ -242,20 +249,22 @@ __global__ void __launch_bounds__(kThreads) dla_simt_walk_kernel(const DlaArgs p
     const int64_t len = p.cu_seqlens[seq + 1] - p.cu_seqlens[seq];
     const int64_t nc = (len + C - 1) / C, slot0 = slot_base(p.cu_seqlens, seq);
     float x = from ? from[given] : 0.f;
+    Factors decays;
     for (int64_t n0 = 0; n0 < nc; n0 += kAhead) {
-        float add[kAhead], decay[kAhead];
+        float add[kAhead];
+        Two decay[kAhead];
 #pragma unroll
         for (int e = 0; e < kAhead; ++e)
             if (n0 + e < nc) {
                 const int64_t at = chunk_at(p, slot0 + (rev ? nc - 1 - n0 - e : n0 + e), head, rev);
                 add[e] = ws[at * s.state + i];
-                decay[e] = ws[s.decays + at];
+                decay[e] = {ws[s.decays + 2 * at], ws[s.decays + 2 * at + 1]};
             }
 #pragma unroll
         for (int e = 0; e < kAhead; ++e)
             if (n0 + e < nc) {
                 ws[chunk_at(p, slot0 + (rev ? nc - 1 - n0 - e : n0 + e), head, rev) * s.state + i] = x;
-                x = fmaf(decay[e], x, add[e]);
+                x = fmaf(decays.next(decay[e]), x, add[e]);
             }
     }
     if (to) to[given] = x;
@@ -466,7 +475,7 @@ __global__ void __launch_bounds__(kThreads) dla_simt_grad_kernel(const DlaArgs p
         float whole = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) whole += s.ss[i];
-        whole *= s.gate.whole;
+        whole *= s.gate.whole.hi;
         Two a[2], b[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

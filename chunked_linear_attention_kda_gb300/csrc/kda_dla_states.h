@@ -29,7 +29,7 @@ struct Plan {
     bool vec_q, vec_k, vec_v, vec_o;  // 16-byte rows
     TileGates *gates;    // [tiles][heads]
     float *states;       // [slots][heads] states at the segments' starts (reverse: gradients at their ends)
-    float *decays;       // [slots][heads] decays over the segments
+    Two *decays;         // [slots][heads] decays over the segments, in two parts
 };
 // Tiles of a segment, from the call's sizes alone (the sequences' lengths are on the device). Cutting costs
 // K and V read once more, what a CTA takes to begin (the time of four tiles) and the join; not cutting
@@ -71,7 +71,7 @@ inline size_t gate_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads) {
 inline size_t plan_bytes(int64_t n_tok, int32_t n_seq, int32_t n_heads, int32_t d_k) {
     const int64_t seg = (int64_t)segment_tiles(n_tok, n_seq, n_heads) * C;
     const size_t units = n_tok > seg ? (size_t)(n_tok / seg + n_seq) * n_heads : 0;
-    return (gate_bytes(n_tok, n_seq, n_heads) + units * (state_floats(d_k <= 64 ? 64 : 128) + 1) * 4 + 255) / 256 * 256;
+    return (gate_bytes(n_tok, n_seq, n_heads) + units * (state_floats(d_k <= 64 ? 64 : 128) * 4 + sizeof(Two)) + 255) / 256 * 256;
 }
 inline Plan make_plan(const DlaArgs &p, bool bwd) {
     Plan plan{};
@@ -84,7 +84,7 @@ inline Plan make_plan(const DlaArgs &p, bool bwd) {
     plan.vec_o = bwd && gdr::rows_vec<__nv_bfloat16>(p.dout, (int64_t)p.n_heads * p.in_v, p.in_v);
     plan.gates = static_cast<TileGates *>(p.workspace);
     plan.states = reinterpret_cast<float *>(static_cast<char *>(p.workspace) + gate_bytes(p.n_tok, p.n_seq, p.n_heads));
-    plan.decays = plan.states + (size_t)plan.slots * p.n_heads * state_floats(p.d_k <= 64 ? 64 : 128);
+    plan.decays = reinterpret_cast<Two *>(plan.states + (size_t)plan.slots * p.n_heads * state_floats(p.d_k <= 64 ? 64 : 128));
     return plan;
 }
 
@@ -346,7 +346,9 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
         if (!ok)
             for (int n = max(0, begun - S); n < begun; ++n) drain_bar(bar(L::Full + n % S), (n / S) & 1);
     } else if (warp >= 4 && warp < 12) {
-        float beyond = 1.f;  // the decay from the tile's end to the walk's
+        // the exponent of the decay from the tile's end to the walk's, in fixed point; past -2048 it may be any
+        int64_t past = 0;
+        float bad = 0.f;
         const int turn = (warp - 4) >> 2;
         for (int n = 0; n < nc; ++n) {
             const int s = n % S;
@@ -356,14 +358,18 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
                 if (n >= 2) wait(L::VpEmpty + turn, (n >> 1) - 1);
                 ptx::tc_fence_after();
                 if (32 * (warp & 3) < p.d_v)  // other lanes' rows are not read
-                    scale_values<3>(base + s * L::kStage + L::V, tmem, 256 + turn * 96, REV ? g->gam : g->del, beyond);
+                    scale_values<3>(base + s * L::kStage + L::V, tmem, 256 + turn * 96, REV ? g->gam : g->del, exp2_fixed(past) + bad);
                 ptx::tc_fence_before();
                 warp_arrive(bar(L::VpFull + turn));
             }
-            beyond *= g->whole;
+            past = max(past + g->sum, -((int64_t)2048 << kPoint));
+            bad += nan_of(*g);
             warp_arrive(bar(L::Empty + s));
         }
-        if (tid == 128) plan.decays[(size_t)slot * p.n_heads + head] = beyond;
+        if (tid == 128) {
+            const Two beyond = exp2_fixed_parts(past);
+            plan.decays[(size_t)slot * p.n_heads + head] = {beyond.hi + bad, beyond.lo};
+        }
     } else if (warp >= 12) {
         constexpr int NC = DK / 2;  // key channels of a thread
         const int dv = (warp & 3) * 32 + lane, part = (warp - 12) >> 2;
@@ -445,9 +451,10 @@ __global__ void __launch_bounds__(256) dla_join_kernel(const DlaArgs p, const Pl
     gdr::wait_for_previous_kernel();
     auto unit = [&](int64_t n) { return (size_t)(slot0 + (rev ? m - 1 - n : n)) * p.n_heads + head; };
     auto at = [&](int64_t n) { return reinterpret_cast<float4 *>(plan.states + unit(n) * state_floats(DK)) + i; };
+    Factors decays;
     for (int64_t n0 = 0; n0 < m; n0 += 4) {
         float4 add[4];
-        float decay[4];
+        Two decay[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (n0 + j + 1 < m) {  // the last one hands on to none
@@ -459,10 +466,11 @@ __global__ void __launch_bounds__(256) dla_join_kernel(const DlaArgs p, const Pl
             if (n0 + j >= m) break;
             *at(n0 + j) = x;
             if (n0 + j + 1 == m) break;
-            x.x = fmaf(decay[j], x.x, add[j].x);
-            x.y = fmaf(decay[j], x.y, add[j].y);
-            x.z = fmaf(decay[j], x.z, add[j].z);
-            x.w = fmaf(decay[j], x.w, add[j].w);
+            const float w = decays.next(decay[j]);
+            x.x = fmaf(w, x.x, add[j].x);
+            x.y = fmaf(w, x.y, add[j].y);
+            x.z = fmaf(w, x.z, add[j].z);
+            x.w = fmaf(w, x.w, add[j].w);
         }
     }
 }

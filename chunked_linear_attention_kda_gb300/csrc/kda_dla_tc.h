@@ -182,13 +182,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 // ---------------------------------------------------------------- gates
 // Of one tile and head, formed for all tiles by a launch of their own (kda_dla_fwd.cu) and copied in with the
 // tile: running sums of g log2(e), whole number and rest, scale times the decays up to and with each token (gam), the decays
-// past each (del), the decay of all (whole) and its exponent. Formed beside the products by one warp they
+// past each (del), the decay of all in two parts (whole) and its exponent in fixed point (sum). Formed beside the products by one warp they
 // were the longest chain of a tile (1700 cycles of scans and conversions).
 struct TileGates {
     float2 G[C];
     float gam[C], del[C];
-    float whole, pad;
-    float2 sum;
+    Two whole;
+    int64_t sum;
 };
 static_assert(sizeof(TileGates) % 16 == 0, "copied in bulk");
 // The gates of tile c of a sequence lie at slot_base(cu, sequence) + c, as in kda_gdr.h
@@ -218,6 +218,12 @@ __device__ __forceinline__ float exp2_fixed(int64_t x) {
     const float2 y = from_fixed(x);
     return ex2(y.x) * ex2(y.y);
 }
+__device__ __forceinline__ Two exp2_fixed_parts(int64_t x) {
+    const float2 y = from_fixed(x);
+    return exp2_parts(y.x, y.y);
+}
+// NaN where a tile's gates are, which its sum cannot show
+__device__ __forceinline__ float nan_of(const TileGates &g) { return g.whole.hi - g.whole.hi; }
 // A tile's gates by one warp, two tokens a lane; tokens past the end have g = 0. A g that is NaN, or past what
 // the sums hold (whose decay is infinite), makes all of them NaN: as a fixed point number it would pass for a 0.
 __device__ __forceinline__ void form_gates(float2 g, float scale, TileGates *out) {
@@ -239,9 +245,9 @@ __device__ __forceinline__ void form_gates(float2 g, float scale, TileGates *out
     reinterpret_cast<float2 *>(out->gam)[lane] = make_float2(scale * ex2(a.x) * ex2(a.y), scale * ex2(b.x) * ex2(b.y));
     reinterpret_cast<float2 *>(out->del)[lane] = make_float2(exp2_fixed(total - before) + bad, exp2_fixed(total - run) + bad);
     if (lane == 0) {
-        out->whole = exp2_fixed(total) + bad;
-        const float2 sum = from_fixed(total);
-        out->sum = make_float2(sum.x + bad, sum.y);
+        const Two whole = exp2_fixed_parts(total);
+        out->whole = {whole.hi + bad, whole.lo};
+        out->sum = total;
     }
 }
 
