@@ -129,3 +129,30 @@ def test_ragged_slow_decays():
         for name, y, ref in zip(("out", "h_final", "dq", "dk", "dv", "dg", "dh0"), got, want):
             if name != "dg" or b - a > 1:  # of one token dg is a single sum that may cancel
                 assert rel(y, ref) <= bar(y, BF), f"{name} of sequence {i}: {rel(y, ref):.2e}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_many_steps(dtype):
+    """4096 tokens one by one. A step rounds the state twice, 2^-24 at most and random in sign: sqrt(2 4096) 2^-24 =
+    5.4e-6 at most, whatever the rate; a rate rounded beside 1, by up to 2^-25 a step and always the same
+    way, is off by ten times as much."""
+    n = 4096
+    x = inputs(n, 2, 64, 64, dtype, RATES, True, seed=5)
+    xs = x.f64(DEV)
+    want, end = chunked(*xs[:3], xs[3].expand(x.v.shape[:2]), xs[4], 0.125)
+    pool = x.h0.clone()
+    out = torch.cat([kda.dla_step(x.q[t:t + 1], x.k[t:t + 1], x.v[t:t + 1], x.g, pool) for t in range(n)])
+    for h in range(4):
+        assert rel(pool[:, h], end[:, h]) <= 5.4e-6, f"state, head {h}: {rel(pool[:, h], end[:, h]):.2e}"
+        assert rel(out[:, h], want[:, h]) <= (5.4e-6 if dtype == FP else 2.0 ** -8 + 5.4e-6)
+
+
+@pytest.mark.gpu
+def test_a_step_keeps_an_infinity():
+    x = inputs(1, 1, 64, 64, FP, [0.0, -1e-6, -1e-3, -3.0], True, seed=6)
+    pool = x.h0.clone()
+    pool[0, :, 5, 7], pool[0, :, 9, 11] = math.inf, -math.inf
+    kda.dla_step(x.q, x.k, x.v, x.g, pool)
+    assert bool((pool[0, :, 5, 7] == math.inf).all()) and bool((pool[0, :, 9, 11] == -math.inf).all())
+    assert int(torch.isfinite(pool).sum()) == pool.numel() - 8
