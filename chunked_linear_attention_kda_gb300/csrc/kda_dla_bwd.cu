@@ -46,7 +46,7 @@ struct WalkSmem {
     static constexpr int K = 0, V = kKey, Gate = V + kVal, kStage = Gate + 2048;
     static constexpr int kStages = 4;
     static constexpr int Out = kStages * kStage, Bars = Out + 2 * plane_bytes(DK, DV);
-    static constexpr int Full = 0, Empty = kStages, VpFull = 2 * kStages, VpEmpty = VpFull + 1, DsFull = VpEmpty + 1,
+    static constexpr int Full = 0, Empty = kStages, VpFull = 2 * kStages, VpEmpty = VpFull + 2, DsFull = VpEmpty + 2,
                          DsEmpty = DsFull + 2, OutFull = DsEmpty + 2, OutEmpty = OutFull + 1, Drain = OutEmpty + 1, Partial = Drain + 1, kBars = Partial + 1;
     static constexpr int kBytes = Bars + 8 * kBars + 16 + 1024;  // the base is rounded up to 1024
     static_assert(sizeof(TileGates) <= 2048 && kBytes <= 227 * 1024, "fits an SM");
@@ -85,9 +85,9 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
             ptx::mbar_init(bar(L::Full + i), 1);
             ptx::mbar_init(bar(L::Empty + i), 1 + 4 + 8);
         }
-        ptx::mbar_init(bar(L::VpFull), 4);
-        ptx::mbar_init(bar(L::VpEmpty), 1);
         for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(bar(L::VpFull + i), 4);
+            ptx::mbar_init(bar(L::VpEmpty + i), 1);
             ptx::mbar_init(bar(L::DsFull + i), 1);
             ptx::mbar_init(bar(L::DsEmpty + i), 8);
         }
@@ -113,7 +113,7 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
         int s = 0;
 #pragma unroll 1
         for (int n = 0; n < steps; ++n) {
-            wait(L::VpFull, n);
+            wait(L::VpFull + (n & 1), n >> 1);
             if (n >= 2) wait(L::DsEmpty + (n & 1), (n >> 1) - 1);
             ptx::tc_fence_after();
             const uint32_t at = (uint32_t)s * (L::kStage / 16);
@@ -122,9 +122,9 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
                 for (int i = 2; i >= 0; --i)  // the smallest first
 #pragma unroll
                     for (int k = 0; k < C / 16; ++k)
-                        ptx::umma_ts(tmem + (n & 1) * 128, tmem + 256 + i * 32 + 8 * k, k0 + (at + 128 * k), id, i < 2 || k > 0);
+                        ptx::umma_ts(tmem + (n & 1) * 128, tmem + 256 + (n & 1) * 96 + i * 32 + 8 * k, k0 + (at + 128 * k), id, i < 2 || k > 0);
                 ptx::umma_commit(bar(L::DsFull + (n & 1)));
-                ptx::umma_commit(bar(L::VpEmpty));
+                ptx::umma_commit(bar(L::VpEmpty + (n & 1)));
                 ptx::umma_commit(bar(L::Empty + s));
             }
             __syncwarp();
@@ -203,13 +203,16 @@ __device__ __forceinline__ void state_walk(const CUtensorMap &tm_key, const CUte
         for (int n = 0; n < steps; ++n) {
             const int s = n % S;
             wait(L::Full + s, n / S);
-            if (n > 0) wait(L::VpEmpty, n - 1);
-            ptx::tc_fence_after();
+            auto ready = [&] {
+                if (n >= 2) wait(L::VpEmpty + (n & 1), (n >> 1) - 1);
+                ptx::tc_fence_after();
+            };
             const TileGates *g = reinterpret_cast<const TileGates *>(smem + s * L::kStage + L::Gate);
             if (32 * (warp & 3) < p.d_v)  // other lanes' rows are not read
-                scale_values<3>(base + s * L::kStage + L::V, tmem, 256, REV ? g->gam : g->del, 1.f);
+                scale_values<3>(base + s * L::kStage + L::V, tmem, 256 + (n & 1) * 96, REV ? g->gam : g->del, 1.f, ready);
+            else ready();
             ptx::tc_fence_before();
-            warp_arrive(bar(L::VpFull));
+            warp_arrive(bar(L::VpFull + (n & 1)));
             warp_arrive(bar(L::Empty + s));
         }
     } else if (warp >= 8) {

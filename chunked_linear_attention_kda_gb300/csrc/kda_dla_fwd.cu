@@ -308,9 +308,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const int s = c % S;
             wait(L::GFull + c % L::kGates, c / L::kGates);
             wait(L::VFull + s, c / S);
-            if (c > 0) wait(L::VpEmpty, c - 1);
-            ptx::tc_fence_after();
-            if (32 * (warp & 3) < p.d_v) scale_values<2>(base + L::V + s * L::kVal, tmem, kTmV, gate(c).del, 1.f);
+            auto ready = [&] {
+                if (c > 0) wait(L::VpEmpty, c - 1);
+                ptx::tc_fence_after();
+            };
+            if (32 * (warp & 3) < p.d_v) scale_values<2>(base + L::V + s * L::kVal, tmem, kTmV, gate(c).del, 1.f, ready);
+            else ready();
             ptx::tc_fence_before();
             warp_arrive(bar(L::VpFull));
             warp_arrive(bar(L::GEmpty + c % L::kGates));

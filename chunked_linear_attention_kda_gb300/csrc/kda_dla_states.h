@@ -221,7 +221,7 @@ struct SegmentSmem {
 // tensor cores drop bits below a running sum's last place, and the smallest planes' products come first for
 // the same reason. Three planes of the values times their factors, where the forward pass's last walk has room
 // for two: a state is read by every later token and dg is summed from it (8192 tokens: dg off by
-// 5.5e-6 of its norm with two, 4.0e-6 with three, dh0 by 4.7e-6 and 2.0e-6; the walk takes 164 us and
+// 5.5e-6 of its norm with two, 3.1e-6 with three, dh0 by 4.7e-6 and 0.3e-6; the walk takes 164 us and
 // 172 us). The last segment of the walk hands on to
 // none and is left out.
 template <int DK, bool REV>
@@ -355,10 +355,13 @@ __device__ __forceinline__ void segment_walk(const CUtensorMap &tm_key, const CU
             wait(L::Full + s, n / S);
             const TileGates *g = reinterpret_cast<const TileGates *>(smem + s * L::kStage + L::Gate);
             if ((n & 1) == turn) {
-                if (n >= 2) wait(L::VpEmpty + turn, (n >> 1) - 1);
-                ptx::tc_fence_after();
+                auto ready = [&] {
+                    if (n >= 2) wait(L::VpEmpty + turn, (n >> 1) - 1);
+                    ptx::tc_fence_after();
+                };
                 if (32 * (warp & 3) < p.d_v)  // other lanes' rows are not read
-                    scale_values<3>(base + s * L::kStage + L::V, tmem, 256 + turn * 96, REV ? g->gam : g->del, exp2_fixed(past) + bad);
+                    scale_values<3>(base + s * L::kStage + L::V, tmem, 256 + turn * 96, REV ? g->gam : g->del, exp2_fixed(past) + bad, ready);
+                else ready();
                 ptx::tc_fence_before();
                 warp_arrive(bar(L::VpFull + turn));
             }

@@ -3,7 +3,8 @@
 //
 // A tile is 64 tokens of one head in column halves of 64 channels, each 64 rows of 128 bytes in the
 // 128-byte swizzle of tensor copies, which tcgen05 reads K-major or MN-major as it stands. Operands
-// that are not bf16 inputs are sums of two bf16 planes (within 2^-16 of the value).
+// that are not bf16 inputs are sums of bf16 planes: states and pair weights of two (within 2^-17 of the value),
+// values times their decays as scale_values says.
 #pragma once
 
 #include <cuda.h>
@@ -262,28 +263,32 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
     return d;
 }
 // A tile's values times their tokens' factors, V'^T, as NP planes in tensor memory (columns `to` + 32 i .. + 31,
-// two tokens a column): v times the factor's first plane has 16 bits, so that its rest beside hi is exact;
-// every further plane takes what is left and v times the factor's next plane. Two are within 2^-15 of
-// the product, three within 2^-23. By one warp of each quarter of the lanes, 32 value channels. As an A
-// operand there it costs shared memory, which bounds these kernels, one read of the tile; as planes in
-// shared memory for either operand a read, a write a plane and a read each.
-template <int NP>
-__device__ __forceinline__ void scale_values(uint32_t tile, uint32_t tmem, uint32_t to, const float *factor, float more) {
+// two tokens a column). Two, by bf16 arithmetic: v times the factor's first plane has 16 bits, so that its rest
+// beside the first plane is exact, and the second takes that and v times the factor's second plane: within
+// 2^-14.8 of the product (4 instructions a pair of values; by fp32 arithmetic, 10, they are within 2^-17, and 64K
+// tokens of 32 heads take 702 us instead of 632). Three, by fp32 arithmetic: every plane is what is left of
+// the product, which one FMA forms exactly, rounded to bf16: within 2^-25. (In bf16 arithmetic what is left after two is
+// not always exact, and three were within 2^-16.) By one warp of each quarter of the lanes, 32 value channels. As an
+// A operand there it costs shared memory, which bounds these kernels, one read of the tile; as planes in
+// shared memory for either operand a read, a write a plane and a read each. `ready` waits until the planes may be
+// written; the first are formed before it.
+template <int NP, typename Ready>
+__device__ __forceinline__ void scale_values(uint32_t tile, uint32_t tmem, uint32_t to, const float *factor, float more, Ready ready) {
     const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3;
     const uint32_t col = (lane >> 3 & 1) * 8;  // matrices 0, 1: channels 0..7 and 8..15 of eight tokens; 2, 3: of the next eight
     constexpr uint32_t minus = 0x80008000u;
 #pragma unroll 1
     for (int t0 = 0; t0 < C; t0 += 32) {
-        uint32_t f[NP][4];  // of the tokens t0 + 8 n + 2 (lane % 4) and the next
+        float2 f[4];  // of the tokens t0 + 8 n + 2 (lane % 4) and the next
+        uint32_t f0[4], f1[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            const float2 y = *reinterpret_cast<const float2 *>(factor + t0 + 8 * n + 2 * (lane & 3));
-            float a = more * y.x, b = more * y.y;
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                f[i][n] = ptx::pack_bf16(a, b);
-                a -= gdr::lo_f(f[i][n]);
-                b -= gdr::hi_f(f[i][n]);
+            f[n] = *reinterpret_cast<const float2 *>(factor + t0 + 8 * n + 2 * (lane & 3));
+            f[n].x *= more;
+            f[n].y *= more;
+            if constexpr (NP == 2) {
+                f0[n] = ptx::pack_bf16(f[n].x, f[n].y);
+                f1[n] = ptx::pack_bf16(f[n].x - gdr::lo_f(f0[n]), f[n].y - gdr::hi_f(f0[n]));
             }
         }
 #pragma unroll
@@ -298,12 +303,19 @@ __device__ __forceinline__ void scale_values(uint32_t tile, uint32_t tmem, uint3
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const uint32_t v = x[0][i];
-                x[0][i] = mul_bf16x2(v, f[0][i >> 1]);
-                const uint32_t rest = fma_bf16x2(v, f[0][i >> 1], x[0][i] ^ minus);  // exact
-                x[1][i] = fma_bf16x2(v, f[1][i >> 1], rest);
-                if constexpr (NP == 3)  // rest - x[1], exact, + v f[1], + v f[2]
-                    x[2][i] = fma_bf16x2(v, f[2][i >> 1], fma_bf16x2(v, f[1][i >> 1], fma_bf16x2(0x3f803f80u, rest, x[1][i] ^ minus)));
+                if constexpr (NP == 2) {
+                    x[0][i] = mul_bf16x2(v, f0[i >> 1]);
+                    x[1][i] = fma_bf16x2(v, f1[i >> 1], fma_bf16x2(v, f0[i >> 1], x[0][i] ^ minus));
+                } else {
+                    const float a = gdr::lo_f(v), b = gdr::hi_f(v);
+                    const float2 y = f[i >> 1];
+                    x[0][i] = ptx::pack_bf16(a * y.x, b * y.y);
+                    const float ra = fmaf(a, y.x, -gdr::lo_f(x[0][i])), rb = fmaf(b, y.y, -gdr::hi_f(x[0][i]));
+                    x[1][i] = ptx::pack_bf16(ra, rb);
+                    x[2][i] = ptx::pack_bf16(ra - gdr::lo_f(x[1][i]), rb - gdr::hi_f(x[1][i]));
+                }
             }
+            if (t0 == 0 && h == 0) ready();
             const uint32_t at = tmem + ((uint32_t)(32 * q + 16 * h) << 16) + to + t0 / 2;
 #pragma unroll
             for (int i = 0; i < NP; ++i) ptx::tmem_st_half4(at + 32 * i, x[i]);
