@@ -61,9 +61,13 @@ __global__ void __launch_bounds__(kThreads) dla_step_kernel(const DlaStepArgs p,
         }
     // The decay in two parts: a float beside 1 is off by up to 2^-25, with a constant rate by the same amount at
     // every token, which adds up (4096 tokens at g = -1e-4: the state by 8e-5 of its norm).
-    const float g = p.g[b * p.g_stride + head], less = expm1f(g);
-    const bool slow = g > -0.5f;
-    const float decay = slow ? 1.f + less : expf(g), rest = slow ? less - (decay - 1.f) : 0.f;
+    const float g = p.g[b * p.g_stride + head];
+    float decay = expf(g), rest = 0.f;
+    if (g > -0.5f) {  // a branch: selected from both, 253 rows take 156 us
+        const float less = expm1f(g);
+        decay = 1.f + less;
+        rest = less - (decay - 1.f);
+    }
     if (decay == 0.f)  // what is forgotten may be anything: a NaN that the slot's last owner left
 #pragma unroll
         for (int i = 0; i < R; ++i)
