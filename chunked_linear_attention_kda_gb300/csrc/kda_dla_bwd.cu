@@ -6,8 +6,8 @@
 // segment's tiles in both directions that leaves the state at each block of 128 tokens' start and the
 // gradient at its end in the workspace, as two bf16 planes that tensor copies of a block's gradients read;
 // the gradients, every block and value head by itself; with shared heads the sums over value heads.
-// Two sequences of 8K tokens, 32 heads, 128 x 128: gates 7 us, states 171 us (1.07 GB, 0.94 of the copy rate),
-// gradients 350 us (1.45 GB, 0.62; a block is a chain of five products, 13 us). Blocks of 128 tokens, because
+// Two sequences of 8K tokens, 32 heads, 128 x 128: gates 8 us, states 174 us (1.07 GB, 0.92 of the copy rate),
+// gradients 338 us (1.45 GB, 0.64; a block is a chain of five products, 12 us). Blocks of 128 tokens, because
 // their four products fill tensor memory and their tiles shared memory; blocks of 64 would keep twice
 // the states, 1.07 GB more traffic.
 #include <cmath>
@@ -944,7 +944,13 @@ __global__ void __launch_bounds__(256) dla_shared_heads_kernel(const float *dq, 
 }
 
 // ---------------------------------------------------------------- host
-// Both walks of every sequence and head; with fewer than an SM's worth of them sequences are cut.
+// Both walks of every sequence and head are a CTA each. Where there are fewer than 96, sequences of more than 16 tiles
+// are cut, which costs K, V, Q and dO read once more and the join; the lengths, which would tell more, are on the
+// device. Measured both ways, us, heads of 128 channels, cut / whole. Ragged batches of few heads gain: 8K tokens
+// with 15 x 512, 8 heads (256 walks, whole) 207 / 254; 64K with 100, 24 heads (96 walks, whole) 1759 / 1973; 16K
+// with 100 tokens 496 / 536. Equal lengths of many heads lose: 2 x 8K tokens, 32 heads (128 walks, whole) 649 / 541; one
+// of 16K, 48 heads (96, whole) 894 / 796, 47 heads (94, cut) 877 / 782, 32 heads (64, cut) 624 / 611; 4 x 4K,
+// 8 heads (64, cut) 199 / 184. The limit of 96 lies between what few long and what many equal ones ask for.
 int walk_segment(int64_t n_tok, int32_t n_seq, int32_t n_heads) {
     const int64_t tiles = (n_tok + C - 1) / C;
     if ((int64_t)n_seq * n_heads * 2 >= 96 || tiles <= 16) return (int)std::min<int64_t>((tiles + 1) / 2 * 2, (int64_t)1 << 24) * C;

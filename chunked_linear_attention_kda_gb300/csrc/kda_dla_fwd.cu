@@ -7,10 +7,10 @@
 //   Q K^T                        64 x 64, both tiles as they were copied
 //   O1 = S^T Q^T                 S^T as two bf16 planes in tensor memory (the A operand)
 //   O2 = V^T P^T                 P = scale e Q K^T as two planes in shared memory
-//   dS^T = V'^T K                V' = delta V as two planes in tensor memory: a state's sums are off by 4e-6
-//                                of its norm, a thousandth of what a bf16 input is rounded by; three planes leave
-//                                1.5e-6, but then Q K^T has room for one tile and 64K tokens of 32 heads
-//                                take 517 us instead of 400
+//   dS^T = V'^T K                V' = delta V as two planes in tensor memory: a tile's sums are off by 4e-6
+//                                of their norm, a thousandth of what a bf16 input is rounded by; with a third
+//                                plane Q K^T has room for one tile, and this launch takes 517 us instead
+//                                of 400 at 64K tokens of 32 heads
 //   o = scale gamma O1 + O2,  S^T <- Gamma S^T + dS^T
 // The state is converted once a tile, off the products' path: what waits for it is O1 alone. Shared
 // memory's 128 bytes a cycle bound a tile (the operands of the products, V' and P formed, the output
@@ -19,8 +19,8 @@
 // A long sequence is cut into segments, so that few heads fill the GPU: a first launch forms what
 // each segment adds to the state (kda_dla_states.h: K and V are read once more), a second one the
 // states at the segments' starts, a third the output, all segments side by side. 64K tokens of 32 heads, 128 x
-// 128: gates 14 us, segments 164 us (1.07 GB, the copy rate), join 12 us, output 400 us (2.15 GB, 0.8 of it; 3500
-// cycles a tile, with no unit above half: the roles of a tile wait for one another).
+// 128, 630 us: under the profiler gates 17 us, segments 172 us (1.07 GB, 0.93 of the copy rate), join 12 us, output
+// 390 us (2.15 GB, 0.83 of it; 3500 cycles a tile, with no unit above half: the roles of a tile wait for one another).
 #include <cmath>
 
 #include "kda_dla_states.h"

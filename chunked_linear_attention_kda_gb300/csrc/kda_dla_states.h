@@ -141,7 +141,8 @@ inline cudaError_t align_inputs(DlaArgs &p, char *at, bool bwd, cudaStream_t str
 }
 
 // The gates of every tile and head: a warp four heads of a tile, whose decays are neighbours in memory and
-// whose scans run beside each other (64K tokens of 32 heads: 31 us with a head a warp, 14 with four).
+// whose scans run beside each other (64K tokens of 32 heads: 31 us with a head a warp, 14 with four; 17 since a
+// tile's decay is formed in two parts).
 static __global__ void __launch_bounds__(256) dla_gates_kernel(const DlaArgs p, TileGates *out) {
     gdr::let_next_kernel_start();
     const int quads = (p.n_heads + 3) / 4;

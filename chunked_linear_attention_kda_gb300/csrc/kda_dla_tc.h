@@ -266,7 +266,7 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 // two tokens a column). Two, by bf16 arithmetic: v times the factor's first plane has 16 bits, so that its rest
 // beside the first plane is exact, and the second takes that and v times the factor's second plane: within
 // 2^-14.8 of the product (4 instructions a pair of values; by fp32 arithmetic, 10, they are within 2^-17, and 64K
-// tokens of 32 heads take 702 us instead of 632). Three, by fp32 arithmetic: every plane is what is left of
+// tokens of 32 heads take 665 us instead of 625). Three, by fp32 arithmetic: every plane is what is left of
 // the product, which one FMA forms exactly, rounded to bf16: within 2^-25. (In bf16 arithmetic what is left after two is
 // not always exact, and three were within 2^-16.) By one warp of each quarter of the lanes, 32 value channels. As an
 // A operand there it costs shared memory, which bounds these kernels, one read of the tile; as planes in

@@ -650,7 +650,7 @@ kda_status kda_gated_norm_bwd(const void *dy, int64_t dy_stride, const void *x,
  * heads that are no multiple of 8 channels wide are copied to such rows in the workspace first).
  * State, sums and the gradient of g are fp32; with KDA_BF16 the products of the chunked calls run on
  * the tensor cores with every operand that is not itself a bf16 input carried in two or three bf16 parts
- * (within 2^-14.8 of its value at most; h_final is within some 4e-6 of its norm, dg within 8e-6, dh0 within 1e-6,
+ * (within 2^-14.8 of its value at most; h_final is within some 5e-6 of its norm, dg within 8e-6, dh0 within 1e-6,
  * however slow the decays and long the memories), with KDA_F32 they are fp32 FMAs. Results are
  * deterministic: the same call gives the same bits; long sequences are cut into segments by the
  * call's sizes, so that packing a sequence with others may change its results' last bits. A NaN or an
