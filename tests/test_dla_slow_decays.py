@@ -156,3 +156,41 @@ def test_a_step_keeps_an_infinity():
     kda.dla_step(x.q, x.k, x.v, x.g, pool)
     assert bool((pool[0, :, 5, 7] == math.inf).all()) and bool((pool[0, :, 9, 11] == -math.inf).all())
     assert int(torch.isfinite(pool).sum()) == pool.numel() - 8
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [FP, BF])
+@pytest.mark.parametrize("at", [1000, 4097, 8191])
+def test_a_decay_that_is_nan_shows_through_segments(dtype, at):
+    """Few heads, so that the sequence is cut: every token from the NaN's on, of its head alone, and the
+    gradient of the starting state."""
+    x = inputs(8192, 2, 64, 64, dtype, RATES[:2], False, seed=7)
+    ref, grads = forward(x), backward(x)
+    x.g[at, 1] = float("nan")
+    got, back = forward(x), backward(x)
+    chunk = at // 128 * 128
+    assert bool(torch.isnan(got[0][at:, 1]).all()) and bool(torch.isnan(got[1][0, 1]).all())
+    assert bool(torch.isnan(back[0][at:, 1]).all()) and bool(torch.isnan(back[4][0, 1]).all())
+    assert torch.equal(got[0][:chunk, 1], ref[0][:chunk, 1])
+    for a, b in zip((got[0], back[0], back[1], back[2], back[3]), (ref[0], *grads[:4])):
+        assert torch.equal(a[:, 0], b[:, 0])
+    assert torch.equal(got[1][0, 0], ref[1][0, 0]) and torch.equal(back[4][0, 0], grads[4][0, 0])
+
+
+@pytest.mark.gpu
+def test_strong_decays_after_slow_ones_through_segments():
+    """A segment whose sum of exponents passes any that fp32 holds, and resets, beside heads that keep all."""
+    x = inputs(8192, 2, 64, 64, BF, RATES, False, seed=8)
+    x.g[1000:3000, 0] = -60.0
+    x.g[4000, 1] = -math.inf
+    x.g[5000:, 2] = -200.0
+    xs = x.f64(DEV)
+    xs[3] = xs[3].clamp(min=-300.0)
+    out, end = forward(x)
+    want = chunked(*xs[:3], xs[3], xs[4], 0.125)
+    each_head("out", out, want[0], 4, BF, 1)
+    each_head("h_final", end, want[1], 4, BF, 1)
+    got = backward(x)
+    ref = gradients((*xs[:3], xs[3], xs[4]), 0.125, x.dout.double(), x.dhf.double())
+    for name, a, b in zip(("dq", "dk", "dv", "dg", "dh0"), got, ref):
+        assert rel(a, b) <= bar(a, BF), f"{name}: {rel(a, b):.2e}"
